@@ -6,6 +6,7 @@ inputs of the workloads the library is measured on.
 """
 from .ckv import (  # noqa: F401
     CkvError,
+    ckv_build_step_maps,
     ckv_c128_online_decode,
     ckv_c128_online_decode_fp8,
     ckv_c128_online_prefill,
@@ -16,6 +17,10 @@ from .ckv import (  # noqa: F401
     ckv_check_distinct,
     ckv_check_distinct_noalloc,
     ckv_expand_pools_and_append_tail,
+    ckv_fp4_attention,
+    ckv_fp4_attention_workspace,
+    ckv_fp4_load,
+    ckv_fp4_store,
     ckv_kpool_compress,
     ckv_kpool_compress_set_variant,
     ckv_kpool_decode_update,
@@ -23,6 +28,7 @@ from .ckv import (  # noqa: F401
     ckv_latency_probe,
     ckv_plan_online_prefill,
     ckv_plan_online_prefill_device,
+    ckv_qk_norm_rope,
     ckv_wait_timeout_selftest,
     load,
 )

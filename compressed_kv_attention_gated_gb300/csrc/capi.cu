@@ -5,6 +5,7 @@
 // Nothing is allocated and nothing synchronises.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "ckv.h"
@@ -37,6 +38,57 @@ int32_t pow2_shift(int64_t n) {
 }
 bool pool_size_ok(int32_t P) { return P == 1 || P == 2 || P == 4 || P == 8 || P == 16; }
 bool head_dim_ok(int32_t D) { return D == 128 || D == 256 || D == 512; }
+bool dtype_ok(ckv_dtype t) { return t == CKV_F32 || t == CKV_BF16; }
+
+// A power of two in [2^-64, 2^64], the range in which every product of the
+// 4-bit format is an exact fp32 and bf16 number.
+bool cache_scale_ok(float g) {
+  int e = 0;
+  return g > 0.f && std::frexp(g, &e) == 0.5f && e >= -63 && e <= 65;
+}
+
+// One row set of ckv_qk_norm_rope.
+ckv_status check_norm_rows(const ckv_norm_rows& r) {
+  if (r.tokens < 0 || r.heads < 0 || r.reserved != 0) return CKV_ERR_SHAPE;
+  if (!dtype_ok(r.dtype) || !dtype_ok(r.out_dtype)) return CKV_ERR_DTYPE;
+  if (r.tokens == 0 || r.heads == 0) return CKV_OK;
+  if (r.tokens > INT32_MAX) return CKV_ERR_SHAPE;
+  if (!r.x || !r.out || !r.positions) return CKV_ERR_NULL;
+  if (r.stride_t < 0 || r.stride_h < 0 || r.out_stride_t < 0 || r.out_stride_h < 0) return CKV_ERR_SHAPE;
+  const int64_t in = r.dtype == CKV_F32 ? 4 : 8, out = r.out_dtype == CKV_F32 ? 4 : 8;
+  if (!aligned(r.x, 16) || !aligned(r.out, 16) || !aligned(r.weight, 16) || !aligned(r.positions, 4) || r.stride_t % in ||
+      r.stride_h % in || r.out_stride_t % out || r.out_stride_h % out)
+    return CKV_ERR_ALIGN;
+  // rows read and rows written at the same place have to be the same rows
+  if (r.x == r.out && (r.dtype != r.out_dtype || r.stride_t != r.out_stride_t || r.stride_h != r.out_stride_h))
+    return CKV_ERR_SHAPE;
+  return CKV_OK;
+}
+
+// What ckv_fp4_store and ckv_fp4_load check alike; fills `a` when there is work.
+ckv_status check_fp4_rows(ckv::Fp4RowsArgs& a, const void* rows, ckv_dtype dtype, int64_t stride, int64_t n, int32_t D,
+                          const uint8_t* kv_cache, int64_t num_pages, int32_t page_size, const int64_t* loc, float g,
+                          int32_t* err_word) {
+  if (n < 0 || !head_dim_ok(D) || page_size <= 0 || num_pages < 0 || stride < 0 || !cache_scale_ok(g)) return CKV_ERR_SHAPE;
+  if (!dtype_ok(dtype)) return CKV_ERR_DTYPE;
+  a.n = 0;
+  if (n == 0) return CKV_OK;
+  if (n > INT32_MAX) return CKV_ERR_SHAPE;
+  if (!rows || !kv_cache || !loc) return CKV_ERR_NULL;
+  if (!aligned(rows, 16) || !aligned(kv_cache, 16) || !aligned(loc, 8) || !aligned(err_word, 4) ||
+      stride % (dtype == CKV_F32 ? 4 : 8) || static_cast<int64_t>(page_size) * (D / 2 + D / 16) % 16)
+    return CKV_ERR_ALIGN;
+  a.n = n;
+  a.stride = stride;
+  a.cache = const_cast<uint8_t*>(kv_cache);
+  a.loc = loc;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.page_shift = pow2_shift(page_size);
+  a.g = g;
+  a.err = err_word;
+  return CKV_OK;
+}
 
 }  // namespace
 
@@ -499,6 +551,157 @@ ckv_status ckv_latency_probe(int32_t hops, const int32_t* idx, const void* rows,
   if (!aligned(idx, 4) || !aligned(rows, 8) || !aligned(out, 8)) return CKV_ERR_ALIGN;
   return cuda_status(ckv::launch_latency_probe(hops, idx, rows, num_rows, out, n_warps, warps_per_cta,
                                                use_pdl != 0, static_cast<cudaStream_t>(stream)));
+}
+
+ckv_status ckv_build_step_maps(const int32_t* seq_lens, const int32_t* query_lens, int32_t B,
+                               int32_t P, int32_t page_size, int32_t* block_table,
+                               int64_t table_stride, int32_t max_pages, const int32_t* free_pages,
+                               int64_t num_free, int32_t* cursor, int32_t* cursor_out,
+                               const int32_t* tail_blocks, int32_t num_tokens, int32_t* row_start,
+                               int32_t* positions, int32_t* batch_ids, int32_t* slot_mapping,
+                               int64_t* cache_loc, int32_t* tail_slots, int32_t* row_positions,
+                               int32_t* ctx_rows, int32_t use_pdl, int32_t* err_word, void* stream) {
+  if (B < 0 || B > 8192 || P < 1 || P > 1024 || page_size < 1 || max_pages < 0 || table_stride < max_pages ||
+      num_free < 0 || num_free > INT32_MAX || num_tokens < 0)
+    return CKV_ERR_SHAPE;
+  if (!cursor || !cursor_out || (B > 0 && (!seq_lens || !query_lens || (max_pages > 0 && !block_table))) ||
+      (num_free > 0 && !free_pages) || (tail_slots && B > 0 && !tail_blocks))
+    return CKV_ERR_NULL;
+  if (!aligned(seq_lens, 4) || !aligned(query_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+      !aligned(cursor, 4) || !aligned(cursor_out, 4) || !aligned(tail_blocks, 4) || !aligned(row_start, 4) ||
+      !aligned(positions, 4) || !aligned(batch_ids, 4) || !aligned(slot_mapping, 4) || !aligned(cache_loc, 8) ||
+      !aligned(tail_slots, 4) || !aligned(row_positions, 4) || !aligned(ctx_rows, 4) || !aligned(err_word, 4))
+    return CKV_ERR_ALIGN;
+  ckv::StepMapsArgs a{};
+  a.seq_lens = seq_lens;
+  a.query_lens = query_lens;
+  a.block_table = block_table;
+  a.table_stride = table_stride;
+  a.free_pages = free_pages;
+  a.num_free = num_free;
+  a.cursor = cursor;
+  a.cursor_out = cursor_out;
+  a.tail_blocks = tail_blocks;
+  a.row_start = row_start;
+  a.positions = positions;
+  a.batch_ids = batch_ids;
+  a.slot_mapping = slot_mapping;
+  a.cache_loc = cache_loc;
+  a.tail_slots = tail_slots;
+  a.row_positions = row_positions;
+  a.ctx_rows = ctx_rows;
+  a.err = err_word;
+  a.B = B;
+  a.P = P;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.num_tokens = num_tokens;
+  return cuda_status(ckv::launch_step_maps(a, use_pdl != 0, static_cast<cudaStream_t>(stream)));
+}
+
+ckv_status ckv_qk_norm_rope(const ckv_norm_rows* q, const ckv_norm_rows* k, const float* cos_sin,
+                            int64_t num_positions, int32_t D, int32_t rope_dim, int32_t rope_offset,
+                            int32_t interleaved, float eps, int32_t use_pdl, int32_t* err_word,
+                            void* stream) {
+  if (!q) return CKV_ERR_NULL;
+  if (!head_dim_ok(D) || rope_dim < 0 || rope_dim % 2 || rope_offset < 0 || rope_offset % 2 || rope_dim > D ||
+      rope_offset > D - rope_dim || num_positions < 0 || !(eps >= 0.f))
+    return CKV_ERR_SHAPE;
+  ckv::NormRopeArgs a{};
+  const ckv_norm_rows* sets[2] = {q, k};
+  for (int i = 0; i < 2; ++i) {
+    if (!sets[i]) continue;
+    const ckv_status st = check_norm_rows(*sets[i]);
+    if (st != CKV_OK) return st;
+    if (sets[i]->tokens > 0 && sets[i]->heads > 0) a.set[i] = *sets[i];
+  }
+  if (rope_dim > 0 && !cos_sin) return CKV_ERR_NULL;
+  if (!aligned(cos_sin, 4) || !aligned(err_word, 4)) return CKV_ERR_ALIGN;
+  if (a.set[0].tokens == 0 && a.set[1].tokens == 0) return CKV_OK;
+  a.cos_sin = cos_sin;
+  a.num_positions = num_positions;
+  a.err = err_word;
+  a.eps = eps;
+  a.rope_dim = rope_dim;
+  a.rope_offset = rope_offset;
+  a.interleaved = interleaved != 0;
+  return cuda_status(ckv::launch_norm_rope(a, D, use_pdl != 0, static_cast<cudaStream_t>(stream)));
+}
+
+ckv_status ckv_fp4_store(const void* rows, ckv_dtype dtype, int64_t stride, int64_t n, int32_t D,
+                         uint8_t* kv_cache, int64_t num_pages, int32_t page_size,
+                         const int64_t* loc, float cache_scale, int32_t use_pdl, int32_t* err_word,
+                         void* stream) {
+  ckv::Fp4RowsArgs a{};
+  const ckv_status st = check_fp4_rows(a, rows, dtype, stride, n, D, kv_cache, num_pages, page_size, loc, cache_scale, err_word);
+  if (st != CKV_OK || a.n == 0) return st;
+  a.rows = rows;
+  return cuda_status(ckv::launch_fp4_store(a, D, dtype, use_pdl != 0, static_cast<cudaStream_t>(stream)));
+}
+
+ckv_status ckv_fp4_load(const uint8_t* kv_cache, int64_t num_pages, int32_t page_size,
+                        const int64_t* loc, int64_t n, int32_t D, void* out, ckv_dtype dtype,
+                        int64_t stride, float cache_scale, int32_t use_pdl, int32_t* err_word,
+                        void* stream) {
+  ckv::Fp4RowsArgs a{};
+  const ckv_status st = check_fp4_rows(a, out, dtype, stride, n, D, kv_cache, num_pages, page_size, loc, cache_scale, err_word);
+  if (st != CKV_OK || a.n == 0) return st;
+  if (stride < D && n > 1) return CKV_ERR_SHAPE;  // rows written over one another
+  a.out = out;
+  return cuda_status(ckv::launch_fp4_load(a, D, dtype, use_pdl != 0, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t ckv_fp4_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
+  if (T <= 0 || B <= 0 || H < 1 || H > 1024 || T > INT32_MAX / H || !head_dim_ok(D) || max_rows < 1) return 0;
+  return ckv::fp4_attention_workspace(T, B, H, D, max_rows);
+}
+
+ckv_status ckv_fp4_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T,
+                             int32_t H, int32_t D, const uint8_t* kv_cache, int64_t num_pages,
+                             int32_t page_size, float cache_scale, const int32_t* block_table,
+                             int64_t table_stride, int32_t max_pages, const int32_t* row_start,
+                             int32_t B, const int32_t* ctx_rows, int64_t max_rows,
+                             float softmax_scale, const float* sink, uint16_t* out, float* lse,
+                             void* workspace, int64_t workspace_bytes, int32_t use_pdl,
+                             int32_t* err_word, void* stream) {
+  if (T < 0 || B < 0 || B > 65536 || H < 1 || H > 1024 || !head_dim_ok(D) || num_pages < 0 || page_size < 1 ||
+      max_pages < 0 || table_stride < max_pages || !cache_scale_ok(cache_scale) || !std::isfinite(softmax_scale))
+    return CKV_ERR_SHAPE;
+  if (T == 0 || B == 0) return CKV_OK;
+  if (max_rows < 1 || max_rows > INT32_MAX - 1024 || max_rows > static_cast<int64_t>(max_pages) * page_size ||
+      T > INT32_MAX / H || q_stride_t < 0 || q_stride_h < 0)
+    return CKV_ERR_SHAPE;
+  if (!q || !kv_cache || !block_table || !row_start || !ctx_rows || !out) return CKV_ERR_NULL;
+  if (!aligned(q, 16) || q_stride_t % 8 || q_stride_h % 8 || !aligned(kv_cache, 16) || !aligned(block_table, 4) ||
+      !aligned(row_start, 4) || !aligned(ctx_rows, 4) || !aligned(sink, 4) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(workspace, 16) || !aligned(err_word, 4) || static_cast<int64_t>(page_size) * (D / 2 + D / 16) % 16)
+    return CKV_ERR_ALIGN;
+  const int64_t need = ckv::fp4_attention_workspace(T, B, H, D, max_rows);
+  if (need > 0 && !workspace) return CKV_ERR_NULL;
+  if (workspace_bytes < need) return CKV_ERR_SHAPE;
+  ckv::Fp4AttentionArgs a{};
+  a.q = q;
+  a.q_st = q_stride_t;
+  a.q_sh = q_stride_h;
+  a.cache = kv_cache;
+  a.num_pages = num_pages;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.row_start = row_start;
+  a.ctx_rows = ctx_rows;
+  a.sink = sink;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.err = err_word;
+  a.T = T;
+  a.H = H;
+  a.B = B;
+  a.page_size = page_size;
+  a.max_rows = static_cast<int32_t>(max_rows);
+  a.g = cache_scale;
+  a.softmax_scale = softmax_scale;
+  return cuda_status(ckv::launch_fp4_attention(a, D, use_pdl != 0, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

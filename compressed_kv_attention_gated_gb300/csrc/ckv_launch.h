@@ -125,6 +125,78 @@ struct C128PrefillArgs {
   int32_t write_early;
 };
 
+// ---- a serving step around the compressed cache
+struct StepMapsArgs {
+  const int32_t* seq_lens;
+  const int32_t* query_lens;
+  int32_t* block_table;
+  int64_t table_stride;
+  const int32_t* free_pages;
+  int64_t num_free;
+  int32_t* cursor;
+  int32_t* cursor_out;
+  const int32_t* tail_blocks;
+  int32_t* row_start;
+  int32_t* positions;
+  int32_t* batch_ids;
+  int32_t* slot_mapping;
+  int64_t* cache_loc;
+  int32_t* tail_slots;
+  int32_t* row_positions;
+  int32_t* ctx_rows;
+  int32_t* err;
+  int32_t B, P, page_size, max_pages, num_tokens;
+};
+
+struct NormRopeArgs {
+  ckv_norm_rows set[2];  // queries, keys (tokens == 0: none)
+  const float* cos_sin;
+  int64_t num_positions;
+  int32_t* err;
+  float eps;
+  int32_t rope_dim, rope_offset, interleaved;
+};
+
+struct Fp4RowsArgs {
+  const void* rows;  // store: the values
+  void* out;         // load: where they go
+  int64_t stride;    // elements between rows
+  int64_t n;
+  uint8_t* cache;
+  const int64_t* loc;
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t page_shift;  // log2(page_size) when page_size is a power of two, else -1
+  float g;             // cache_scale
+  int32_t* err;
+};
+
+struct Fp4AttentionArgs {
+  const uint16_t* q;
+  int64_t q_st, q_sh;
+  const uint8_t* cache;
+  int64_t num_pages;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* row_start;
+  const int32_t* ctx_rows;
+  const float* sink;
+  uint16_t* out;
+  float* lse;
+  void* workspace;
+  int32_t* err;
+  int64_t T;
+  int32_t H, B, page_size, max_rows;
+  float g, softmax_scale;
+};
+
+cudaError_t launch_step_maps(const StepMapsArgs& a, bool use_pdl, cudaStream_t s);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int D, bool use_pdl, cudaStream_t s);
+cudaError_t launch_fp4_store(const Fp4RowsArgs& a, int D, int dtype, bool use_pdl, cudaStream_t s);
+cudaError_t launch_fp4_load(const Fp4RowsArgs& a, int D, int dtype, bool use_pdl, cudaStream_t s);
+int64_t fp4_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows);
+cudaError_t launch_fp4_attention(const Fp4AttentionArgs& a, int D, bool use_pdl, cudaStream_t s);
+
 cudaError_t launch_kpool_compress(const KpoolCompressArgs& a, int P, bool round_scale,
                                   bool use_pdl, cudaStream_t s);
 cudaError_t launch_kpool_decode_update(const KpoolDecodeArgs& a, int P, bool round_scale,

@@ -61,6 +61,7 @@ typedef int32_t ckv_status;
 #define CKV_DEVERR_SEQ_LEN 0x10u   /* decode seq_len < 1 */
 #define CKV_DEVERR_TIMEOUT 0x20u   /* a pipeline wait gave up after 2 s (never expected) */
 #define CKV_DEVERR_DISTINCT 0x40u  /* ckv_check_distinct: an id repeats or is >= range */
+#define CKV_DEVERR_PAGES 0x80u     /* step maps: free list or block table exhausted, or a page that the table lacks */
 
 typedef int32_t ckv_dtype;
 #define CKV_F32 0
@@ -491,6 +492,164 @@ ckv_status ckv_c128_online_prefill_counted_fp8(float* state, int64_t num_slots, 
  */
 ckv_status ckv_latency_probe(int32_t hops, const int32_t* idx, const void* rows, int64_t num_rows, void* out,
                              int32_t n_warps, int32_t warps_per_cta, int32_t use_pdl, void* stream);
+
+/* ======================================================================
+ * A serving step around the compressed cache (no counterpart in the sources):
+ * where a step's rows go, the norm and rotation that queries and compressed
+ * rows get, a 4-bit paged cache of the compressed rows, and the attention
+ * that reads it.
+ * ====================================================================== */
+
+/*
+ * Block tables and slot maps of one step, built on the device from request
+ * lengths (no host round trip, graph-capturable).  Request i brings n =
+ * query_lens[i] >= 0 tokens and has s = seq_lens[i] >= n tokens with them: its
+ * tokens are the positions s - n .. s - 1 and follow the ragged rows of
+ * requests 0..i-1.  A chunk of P tokens gives one cache row; the request holds
+ * floor(s / P) rows, kept in ceil(floor(s / P) / page_size) pages.
+ *   - Pages that the request needs after the step and not before it are taken
+ *     from free_pages, in request order from index cursor[0] on, and written
+ *     to its row of block_table; other entries stay as they are.
+ *   - cursor_out[0] = cursor[0] + the pages taken (at most num_free).
+ *     cursor_out may equal cursor (the list is consumed in place); then
+ *     cursor has a second word, which must be 0 and is 0 again afterwards.
+ *   - Per ragged token (every array nullable; entries from the last token to
+ *     num_tokens are -1, so that the other calls skip them):
+ *       positions      its position
+ *       batch_ids      its request
+ *       slot_mapping   int32 and
+ *       cache_loc      int64: the cache location page * page_size + row of the
+ *                      chunk row that the token closes ((position + 1) % P ==
+ *                      0), else -1
+ *       tail_slots     tail_blocks[i] * P + position % P (needs tail_blocks; -1
+ *                      where tail_blocks[i] < 0)
+ *       row_positions  first position of the chunk that the token closes, else -1
+ *       ctx_rows       rows that the token may attend to: (position + 1) / P
+ *   - row_start [B + 1] (nullable): first ragged row of each request, and the
+ *     number of tokens.
+ * seq_lens, query_lens  device int32 [B], B <= 8192.    tail_blocks  device int32 [B].
+ * block_table  device int32, request i's row at i * table_stride (>= max_pages).
+ * free_pages   device int32 [num_free]: page ids.       cursor  device int32.
+ * P            1..1024.
+ * Errors (err_word): a length < 0 or n > s sets CKV_DEVERR_SEQ_LEN and the
+ * request counts as having no tokens; more than num_tokens tokens set
+ * CKV_DEVERR_PLAN and those past it are dropped (row_start is clamped too); a
+ * page past max_pages, past the free list, or < 0 in the table sets
+ * CKV_DEVERR_PAGES, and locations in it are -1; a location or tail slot that
+ * does not fit 32 bits sets CKV_DEVERR_CACHE_LOC / CKV_DEVERR_TAIL_BLOCK and
+ * is -1 in the 32-bit map.
+ */
+ckv_status ckv_build_step_maps(const int32_t* seq_lens, const int32_t* query_lens, int32_t B,
+                               int32_t P, int32_t page_size, int32_t* block_table,
+                               int64_t table_stride, int32_t max_pages, const int32_t* free_pages,
+                               int64_t num_free, int32_t* cursor, int32_t* cursor_out,
+                               const int32_t* tail_blocks, int32_t num_tokens, int32_t* row_start,
+                               int32_t* positions, int32_t* batch_ids, int32_t* slot_mapping,
+                               int64_t* cache_loc, int32_t* tail_slots, int32_t* row_positions,
+                               int32_t* ctx_rows, int32_t use_pdl, int32_t* err_word, void* stream);
+
+/* One set of rows of ckv_qk_norm_rope: tokens x heads vectors of D channels. */
+typedef struct ckv_norm_rows {
+  const void* x;             /* device; row (t, h) at t*stride_t + h*stride_h elements */
+  void* out;                 /* device; as x with its own strides; may be x itself */
+  const float* weight;       /* device fp32 [D], nullable (= 1) */
+  const int32_t* positions;  /* device int32 [tokens]; < 0: the token's rows are skipped */
+  int64_t stride_t, stride_h;
+  int64_t out_stride_t, out_stride_h;
+  int64_t tokens;
+  int32_t heads;
+  ckv_dtype dtype;           /* of x: CKV_F32 or CKV_BF16 */
+  ckv_dtype out_dtype;       /* of out */
+  int32_t reserved;          /* 0 */
+} ckv_norm_rows;
+
+/*
+ * Root-mean-square norm of every head's vector and the rotation of its
+ * position, in one pass over two sets of rows (queries, and keys or compressed
+ * rows): y = x / sqrt(mean(x^2) + eps) * weight, then the channels
+ * [rope_offset, rope_offset + rope_dim) of y are rotated: with R = rope_dim
+ * and c, s = cos_sin[position][i], cos_sin[position][R/2 + i], i < R/2, the pair
+ * (a, b) becomes (a c - b s, b c + a s), where the pair is channels (i, i + R/2)
+ * of the span, or (2 i, 2 i + 1) when interleaved != 0.  Computed in fp32 and
+ * rounded once, to out_dtype.  Rows of tokens with a negative position are
+ * neither read nor written.
+ * q, k      host structs; k may be NULL.  Rows 16-byte aligned.
+ * cos_sin   device fp32 [num_positions][rope_dim] (NULL with rope_dim == 0); a
+ *           position >= num_positions sets CKV_DEVERR_SEQ_LEN and its rows are
+ *           skipped.
+ * D         128, 256 or 512.   rope_dim even, 0..D.   rope_offset even, with
+ *           rope_offset + rope_dim <= D.   eps >= 0.
+ * out may be x with the same strides and type; any other overlap is a race.
+ */
+ckv_status ckv_qk_norm_rope(const ckv_norm_rows* q, const ckv_norm_rows* k, const float* cos_sin,
+                            int64_t num_positions, int32_t D, int32_t rope_dim, int32_t rope_offset,
+                            int32_t interleaved, float eps, int32_t use_pdl, int32_t* err_word,
+                            void* stream);
+
+/*
+ * 4-bit rows.  A row of D channels (128, 256 or 512) is D/16 blocks of 16; a
+ * block is stored as 16 FP4-e2m1 codes and one FP8-e4m3 scale, and stands for
+ *     value = code * scale * cache_scale.
+ * cache_scale (g) is one power of two, 2^-64 .. 2^64, for the whole cache; a
+ * block's scale covers block maxima from about g * 2^-7 (below, codes lose
+ * precision) to g * 2688 (above, they saturate).
+ *   scale = e4m3(min(absmax / (6 g), 448)), code = e2m1(x / (scale g)),
+ * each rounded to nearest, ties to even, saturating; a block whose scale rounds
+ * to 0 stores zeros.  With g a power of two every other step is exact.
+ * kv_cache  device uint8 [num_pages][page_size][D/2 + D/16]: per page, page_size
+ *           rows of D/2 code bytes (channel 2i in the low half of byte i), then
+ *           page_size rows of D/16 scale bytes.  A page's bytes must be a
+ *           multiple of 16 (with D = 128: an even page_size).
+ * rows, out device, row i at i * stride elements, 16-byte aligned rows.
+ * loc       device int64 [n]: cache location page * page_size + row; negative: row i is
+ *           skipped (not read, not written); >= num_pages * page_size: also
+ *           skipped, and sets CKV_DEVERR_CACHE_LOC.  Locations of one store are distinct.
+ * A NaN is stored as some finite value, an infinity saturates.
+ */
+ckv_status ckv_fp4_store(const void* rows, ckv_dtype dtype, int64_t stride, int64_t n, int32_t D,
+                         uint8_t* kv_cache, int64_t num_pages, int32_t page_size,
+                         const int64_t* loc, float cache_scale, int32_t use_pdl, int32_t* err_word,
+                         void* stream);
+/* The stored rows' values, fp32 or bf16 (both hold them exactly). */
+ckv_status ckv_fp4_load(const uint8_t* kv_cache, int64_t num_pages, int32_t page_size,
+                        const int64_t* loc, int64_t n, int32_t D, void* out, ckv_dtype dtype,
+                        int64_t stride, float cache_scale, int32_t use_pdl, int32_t* err_word,
+                        void* stream);
+
+/*
+ * Attention over a 4-bit cache whose rows serve all heads, as key and as value
+ * (compressed rows are shared by the heads).  Token t of request b (ragged rows
+ * row_start[b] .. row_start[b+1] - 1) sees the first ctx_rows[t] cache rows of its
+ * request, row j being row j % page_size of page block_table[b][j / page_size]:
+ *     z_j = softmax_scale * <q[t][h], k_j>,   lse[t][h] = log(sum_j e^z_j [+ e^sink[h]]),
+ *     out[t][h] = sum_j e^(z_j - lse) k_j.
+ * A token with ctx_rows[t] == 0 gets zeros and lse = sink[h], or -infinity without
+ * sink.  Rows with ctx_rows[t] < 0, and rows from row_start[B] on, are left as they were.
+ * One token per request is the decode form, several the verify and prompt forms.
+ * q          device bf16, row (t, h) at t*q_stride_t + h*q_stride_h elements, 16-byte aligned.
+ * kv_cache, page_size, num_pages, cache_scale  as for ckv_fp4_store.
+ * block_table  device int32, request b's row at b * table_stride (>= max_pages).  A page
+ *            id outside [0, num_pages) sets CKV_DEVERR_CACHE_LOC; its rows count as unseen.
+ * row_start  device int32 [B + 1], non-decreasing from 0 on.   ctx_rows device int32 [T].
+ * max_rows   host bound of ctx_rows (1 <= max_rows <= max_pages * page_size): larger entries
+ *            set CKV_DEVERR_SEQ_LEN and are clamped.  It chooses how far the rows are
+ *            split over CTAs, so a tight bound is faster.
+ * sink       device fp32 [H], nullable.
+ * out        device bf16 [T][H][D] contiguous.    lse  device fp32 [T][H], nullable.
+ * H          1..1024.    D  128, 256 or 512.    B <= 65536.
+ * workspace  device, 16-byte aligned, ckv_fp4_attention_workspace() bytes (may be NULL when
+ *            that is 0); its contents need no initial value and do not outlive the call.
+ *            Calls that overlap on the GPU need one each.
+ */
+int64_t ckv_fp4_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows);
+ckv_status ckv_fp4_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T,
+                             int32_t H, int32_t D, const uint8_t* kv_cache, int64_t num_pages,
+                             int32_t page_size, float cache_scale, const int32_t* block_table,
+                             int64_t table_stride, int32_t max_pages, const int32_t* row_start,
+                             int32_t B, const int32_t* ctx_rows, int64_t max_rows,
+                             float softmax_scale, const float* sink, uint16_t* out, float* lse,
+                             void* workspace, int64_t workspace_bytes, int32_t use_pdl,
+                             int32_t* err_word, void* stream);
 
 #ifdef __cplusplus
 }
