@@ -47,8 +47,12 @@ namespace {
 constexpr int kKeys = 128;       // cache rows per tile
 constexpr int kRing = 4;         // units of 128 keys x 128 channels
 constexpr int kUnitBytes = 32768;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarps = 8;
-constexpr int kThreads = (kSoftWarps + 1 + kLoadWarps) * 32;
+// Warpgroups (4 warps) 0 and 1: softmax; 2: its first warp issues the MMAs; 3 and 4: load and decode.
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 12, kLoadWarps = 8;
+constexpr int kThreads = (kLoadWarp + kLoadWarps) * 32;
+// Registers per thread: 96 at launch (640 x 96 = 61,440), then 256 x 128 + 128 x 40 + 256 x 88 = 60,416.
+constexpr int kSoftRegs = 128, kMmaRegs = 40, kLoadRegs = 88;
+static_assert(256 * kSoftRegs + 128 * kMmaRegs + 256 * kLoadRegs <= kThreads * 96, "registers of the launch");
 constexpr float kJump = 8.f;     // log2 of the largest weight before the reference moves
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -116,6 +120,8 @@ struct Layout {
   static constexpr int kQ = kRing * kUnitBytes;             // Q: D/64 blocks of R rows x 128 bytes
   static constexpr int kP = kQ + (D / 64) * R * 128;        // P: 128 keys x 128 bytes
   static constexpr int kSmall = kP + kBufs * kKeys * 128;
+  static constexpr int kOutPitch = D * 2 + 64;              // output rows on their way out: two rows of 64 bytes hit all banks
+  static_assert(R * kOutPitch <= kRing * kUnitBytes, "output staging");
   static constexpr int kTmemO = 0, kTmemS = kUnits * R;
   static constexpr int kTmemUsed = kTmemS + kBufs * R;
   static constexpr int kTmem = kTmemUsed <= 32 ? 32 : kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
@@ -129,11 +135,12 @@ struct Small {
   int32_t abort;
   Tile tile;
   int32_t ctx_max, ctx_min;
-  float c[R];      // score factor: softmax_scale * log2(e) * cache_scale / the row's power of two
-  float ref[R];    // reference of the weights, log2 units
-  int32_t ctx[R];  // cache rows that the row sees (0: a row without a token)
+  alignas(16) float c[R];  // score factor: softmax_scale * log2(e) * cache_scale / the row's power of two
+  alignas(16) float ref[R];  // reference of the weights, log2 units
+  alignas(16) int32_t ctx[R];  // cache rows that the row sees (0: a row without a token)
+  int64_t q[R];    // where the row's query begins, elements
   int32_t out[R];  // flat (token, head) index, -1: none
-  float keep[R];   // what a move of the references leaves of sums and outputs
+  alignas(16) float keep[R];  // what a move of the references leaves of sums and outputs
   float part[4][R];
   uint8_t bad[4][kKeys];  // keys of a tile that are not there (ring over tiles)
 };
@@ -170,6 +177,17 @@ __device__ __forceinline__ float reduce_columns(float (&v)[n], int lane) {
   return v[0];
 }
 
+// Columns of a per-row array, 16 bytes at a time.  They are read in one go before
+// anything is stored: the compiler may not move a load over a store that could alias.
+template <int n>
+__device__ __forceinline__ void load_cols(const float* p, float (&v)[n]) {
+#pragma unroll
+  for (int i = 0; i < n; i += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(p + i);
+    v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+  }
+}
+
 __device__ __forceinline__ void soft_barrier() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool p) {
   uint32_t r;
@@ -183,21 +201,54 @@ __device__ __forceinline__ bool soft_any(bool p) {
 }
 static_assert(kSoftWarps * 32 == 256, "the softmax warps' named barrier");
 
-// 8 codes (one 32-bit word) times their block's scale -> 8 fp16 values.
-__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s) {
+// Decoding on the integer and fp16 pipes (a hardware conversion of two codes
+// runs at an eighth of their rate).  A code's exponent and mantissa bits at bits
+// 11..9 of an fp16 are its value * 2^-14 (a subnormal code lands on a subnormal),
+// an e4m3's bits shifted up by 7 its value * 2^-8; the scale is brought to
+// scale * 2^7 (at most 57344), so that the product is value * 2^-7: at least
+// 2^-17 with 6 significant bits, exact in fp16.  Every byte decodes to a finite
+// number.  The left shifts are multiplications by kernel parameters, which the
+// multiplier pipe does beside the logic pipe.  Codes come out in pairs (i, i + 4) of the word's eight.
+constexpr float kUnscale = 128.f;
+
+struct Shifts {
+  uint32_t by[6];  // 2^9, 2^12, 2^5, 2^8, 2^1, 2^4
+};
+
+__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s, const Shifts& k) {
+  const uint32_t m[4] = {((w * k.by[0]) & 0x0E000E00u) | ((w * k.by[1]) & 0x80008000u),
+                         ((w * k.by[2]) & 0x0E000E00u) | ((w * k.by[3]) & 0x80008000u),
+                         ((w * k.by[4]) & 0x0E000E00u) | ((w * k.by[5]) & 0x80008000u), ((w >> 3) & 0x0E000E00u) | (w & 0x80008000u)};
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>((w >> (8 * i)) & 0xFFu), __NV_E2M1);
-    const __half2 p = __hmul2(__half2(h), s);
+    const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&m[i]), s);
     r[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// Four e4m3 bytes, each twice in a register, times 2^7.
+__device__ __forceinline__ void decode_scales(uint32_t b, __half2 (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = b >> (8 * i);  // bytes i and i + 2 in the low byte of each half
+    const uint32_t m = ((x & 0x007F007Fu) << 7) | ((x & 0x00800080u) << 8);
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&m), __float2half2_rn(32768.f));
+    s[i] = __low2half2(v);
+    s[i + 2] = __high2half2(v);
+  }
+}
+
+// Where channel c of a row is kept in the decoded tile (and so in Q and O): the
+// eight channels of a word in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ constexpr int channel_of(int place) {
+  return (place & ~7) | ((place & 1) << 2) | ((place >> 1) & 3);
+}
+
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk,
-                                                                    int page_shift) {
+                                                                    int page_shift, const __grid_constant__ Shifts shifts) {
   using L = Layout<D, R>;
   extern __shared__ uint8_t s_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -247,7 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
         flag_error(a.err, CKV_DEVERR_SEQ_LEN);
         ctx = a.max_rows;
       }
-      if (ctx >= 0) flat = tile.tok0 * a.H + tile.base + r;
+      if (ctx >= 0) {
+        flat = tile.tok0 * a.H + tile.base + r;
+        sm.q[r] = t * a.q_st + (flat - t * a.H) * a.q_sh;
+      }
     }
     sm.ctx[r] = max(ctx, 0);
     sm.out[r] = flat;
@@ -269,58 +323,65 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
   // nothing to add: only the first range answers for rows that see nothing
   const bool idle = n == 0 && (blockIdx.y > 0 || ctx_max < 0);
 
-  if (!idle && warp < kSoftWarps) {
+  if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    if (!idle) {
     // ------------------------------------------------------------- softmax
     const int quad = warp & 3, half = warp >> 2;
     const int col0 = half * L::kCols;
-    // queries: a warp takes every eighth row, scales it and stores it as fp16
+    // queries: a warp takes R/8 rows, a lane eight channels of a row (16 at D = 512); all
+    // loads are issued before the first is used
+    if (n > 0) {
+      constexpr int kC = D == 512 ? 16 : 8;     // channels of a lane
+      constexpr int kSpan = D / kC;             // lanes of a row
+      constexpr int kLoads = R / kSoftWarps * kSpan / 32;
+      constexpr int kBatch = kLoads < 4 ? kLoads : 4;  // rows in flight (registers)
+      const int sub = lane / kSpan, ch = lane % kSpan * kC;
+      static_assert(kLoads >= 1 && kLoads % kBatch == 0, "");
 #pragma unroll 1
-    for (int r = warp; r < R && n > 0; r += kSoftWarps) {
-      constexpr int kC = D / 32;  // channels of a lane, 4, 8 or 16 neighbours
-      float v[kC];
-      const int32_t flat = sm.out[r];
-      if (flat >= 0) {
-        const int32_t t = flat / a.H, h = flat - t * a.H;
-        const uint16_t* q = a.q + t * a.q_st + h * a.q_sh + lane * kC;
-        if constexpr (kC == 4) {
-          const uint2 w = *reinterpret_cast<const uint2*>(q);
-          v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
-        } else {
+      for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
+      uint4 raw[kBatch][kC / 8];
 #pragma unroll
-          for (int i = 0; i < kC; i += 8) {
-            const uint4 w = *reinterpret_cast<const uint4*>(q + i);
-            v[i] = bf16_lo(w.x), v[i + 1] = bf16_hi(w.x), v[i + 2] = bf16_lo(w.y), v[i + 3] = bf16_hi(w.y);
-            v[i + 4] = bf16_lo(w.z), v[i + 5] = bf16_hi(w.z), v[i + 6] = bf16_lo(w.w), v[i + 7] = bf16_hi(w.w);
-          }
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = warp * (R / kSoftWarps) + (i0 + i) * (32 / kSpan) + sub;
+        const bool on = sm.out[r] >= 0;
+        const uint4* q = reinterpret_cast<const uint4*>(a.q + sm.q[r] + ch);
+#pragma unroll
+        for (int x = 0; x < kC / 8; ++x) raw[i][x] = on ? q[x] : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = warp * (R / kSoftWarps) + (i0 + i) * (32 / kSpan) + sub;
+        uint32_t am = 0;  // the largest magnitude: bf16 bits order like the values
+#pragma unroll
+        for (int x = 0; x < kC / 8; ++x) {
+          const uint32_t w[4] = {raw[i][x].x, raw[i][x].y, raw[i][x].z, raw[i][x].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) am = __vmaxu2(am, w[y] & 0x7FFF7FFFu);
         }
-      } else {
+        am = max(am >> 16, am & 0xFFFFu);
 #pragma unroll
-        for (int i = 0; i < kC; ++i) v[i] = 0.f;
+        for (int o = 1; o < kSpan; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+        // power of two that brings the largest channel to [2^14, 2^15); 1 for a row of zeros or with an infinity or NaN
+        const int e = static_cast<int>(am >> 7);
+        const int se = am == 0u || e == 255 ? 127 : min(127 + 14 + 127 - e, 253);
+        const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
+        if (lane % kSpan == 0)
+          sm.c[r] = a.softmax_scale * kLog2e * kUnscale * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
+        uint8_t* row = smem + L::kQ + (ch / 64) * (R * 128) + r * 128;
+#pragma unroll
+        for (int x = 0; x < kC / 8; ++x) {
+          const uint32_t w[4] = {raw[i][x].x, raw[i][x].y, raw[i][x].z, raw[i][x].w};
+          uint32_t v[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {  // channels y and y + 4 of the eight
+            const float lo = y & 1 ? bf16_hi(w[y / 2]) : bf16_lo(w[y / 2]), hi = y & 1 ? bf16_hi(w[2 + y / 2]) : bf16_lo(w[2 + y / 2]);
+            const __half2 p = __floats2half2_rn(lo * up, hi * up);
+            v[y] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          *reinterpret_cast<uint4*>(row + ((((ch % 64) / 8 + x) ^ (r & 7)) * 16)) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
       }
-      float am = 0.f;
-#pragma unroll
-      for (int i = 0; i < kC; ++i) am = fmaxf(am, fabsf(v[i]));
-      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(am));
-      // power of two that brings the largest channel to [2^14, 2^15); 1 for a row of zeros or with an infinity
-      const int e = static_cast<int>(top >> 23);
-      const int se = top == 0u || e == 255 ? 127 : min(127 + 14 + 127 - e, 253);
-      const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
-      if (lane == 0) sm.c[r] = a.softmax_scale * kLog2e * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
-      uint32_t w[kC / 2];
-#pragma unroll
-      for (int i = 0; i < kC; i += 2) {
-        const __half2 p = __floats2half2_rn(v[i] * up, v[i + 1] * up);
-        w[i / 2] = *reinterpret_cast<const uint32_t*>(&p);
-      }
-      const int ch = lane * kC;
-      uint8_t* row = smem + L::kQ + (ch / 64) * (R * 128) + r * 128;
-      if constexpr (kC == 4) {
-        *reinterpret_cast<uint2*>(row + ((((ch % 64) / 8) ^ (r & 7)) * 16) + (ch % 8) * 2) = make_uint2(w[0], w[1]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kC; i += 8)
-          *reinterpret_cast<uint4*>(row + ((((ch + i) % 64) / 8) ^ (r & 7)) * 16) =
-              make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
       }
     }
     fence_proxy_async_smem();
@@ -346,27 +407,44 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       const bool gone = sm.bad[j & 3][quad * 32 + lane] != 0;
       const bool masks = gone || key - lane + 32 > ctx_min;
       const uint32_t at_s = tmem + lanes + L::kTmemS + buf * R + col0;
-      // scores in log2 units over the rows' references, -infinity for keys that a row does not see
-      float z[L::kCols];
-      tmem_ld<L::kCols>(at_s, z);
-      float over = -INFINITY;
+      // scores in log2 units, -infinity for keys that a row does not see
+      auto read_scores = [&](float (&z)[L::kCols]) {
+        tmem_ld<L::kCols>(at_s, z);
 #pragma unroll
-      for (int i = 0; i < L::kCols; ++i) {
-        z[i] = fmaf(z[i], sm.c[col0 + i], -sm.ref[col0 + i]);
-        if (masks) z[i] = !gone && key < sm.ctx[col0 + i] ? z[i] : -INFINITY;
-        over = fmaxf(over, z[i]);
-      }
+        for (int i = 0; i < L::kCols; i += 4) {
+          const float4 c = *reinterpret_cast<const float4*>(&sm.c[col0 + i]);
+          z[i] *= c.x, z[i + 1] *= c.y, z[i + 2] *= c.z, z[i + 3] *= c.w;
+        }
+        if (masks) {
+#pragma unroll
+          for (int i = 0; i < L::kCols; i += 4) {
+            const int4 x = *reinterpret_cast<const int4*>(&sm.ctx[col0 + i]);
+            z[i] = !gone && key < x.x ? z[i] : -INFINITY;
+            z[i + 1] = !gone && key < x.y ? z[i + 1] : -INFINITY;
+            z[i + 2] = !gone && key < x.z ? z[i + 2] : -INFINITY;
+            z[i + 3] = !gone && key < x.w ? z[i + 3] : -INFINITY;
+          }
+        }
+      };
+      auto over_refs = [&](float (&z)[L::kCols]) {
+        float over = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < L::kCols; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sm.ref[col0 + i]);
+          z[i] -= f.x, z[i + 1] -= f.y, z[i + 2] -= f.z, z[i + 3] -= f.w;
+          over = fmaxf(over, fmaxf(fmaxf(z[i], z[i + 1]), fmaxf(z[i + 2], z[i + 3])));
+        }
+        return over;
+      };
+      float z[L::kCols];
+      read_scores(z);
+      const float over = over_refs(z);
       ok = ok && *reinterpret_cast<volatile int32_t*>(&sm.abort) == 0;
       if (soft_any(over > kJump || !ok)) {
         ok = !soft_any(!ok);
         if (!ok) break;
         // new references: the largest score so far of each row
-        tmem_ld<L::kCols>(at_s, z);
-#pragma unroll
-        for (int i = 0; i < L::kCols; ++i) {
-          z[i] *= sm.c[col0 + i];
-          if (masks) z[i] = !gone && key < sm.ctx[col0 + i] ? z[i] : -INFINITY;
-        }
+        read_scores(z);
         const float top = reduce_columns<L::kCols, true>(z, lane);
         constexpr int kShare = 32 / L::kCols;  // lanes that hold the same row's result
         if (lane % kShare == 0) sm.part[quad][col0 + lane / kShare] = top;
@@ -379,9 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
           sm.ref[r] = now;
         }
         soft_barrier();
-#pragma unroll
-        for (int i = 0; i < L::kCols; ++i) l[i] *= sm.keep[col0 + i];
         if (j > 0) {
+          load_cols<L::kCols>(&sm.keep[col0], z);
+#pragma unroll
+          for (int i = 0; i < L::kCols; ++i) l[i] *= z[i];
           ok = mbar_wait(&sm.o_done, (j - 1) & 1);
           if (!ok) atomicExch(&sm.abort, 1);
           __syncwarp();
@@ -394,18 +473,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
               const uint32_t at = tmem + lanes + L::kTmemO + u * R + col0 + i;
               tmem_ld<8>(at, o);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] *= sm.keep[col0 + i + x];
+              for (int x = 0; x < 8; ++x) o[x] *= z[i + x];
               tmem_st8(at, o);
             }
           }
           tc_wait_st();
         }
-        tmem_ld<L::kCols>(at_s, z);
-#pragma unroll
-        for (int i = 0; i < L::kCols; ++i) {
-          z[i] = fmaf(z[i], sm.c[col0 + i], -sm.ref[col0 + i]);
-          if (masks) z[i] = !gone && key < sm.ctx[col0 + i] ? z[i] : -INFINITY;
-        }
+        read_scores(z);
+        over_refs(z);
       }
       // weights, rounded to fp16, as row `key` of P
       uint8_t* row = smem + L::kP + buf * (kKeys * 128) + (quad * 32 + lane) * 128;
@@ -456,15 +531,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
           const float top = fmaxf(m, s);
           const float keep = fast_exp2(m - top);  // 0 where no key was seen
           all = (total == 0.f ? 0.f : total * keep) + (s == top ? 1.f : fast_exp2(s - top));
-          sm.c[r] = all == 0.f ? 0.f : keep * a.g / all;
+          sm.c[r] = all == 0.f ? 0.f : keep * kUnscale * a.g / all;
           m = top;
         } else {
-          sm.c[r] = all == 0.f ? 0.f : a.g / all;
+          sm.c[r] = all == 0.f ? 0.f : kUnscale * a.g / all;
         }
         if (a.lse && flat >= 0) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
       }
     }
     soft_barrier();
+    load_cols<L::kCols>(&sm.c[col0], l);
 #pragma unroll 1
     for (int u = 0; u < L::kUnits; ++u) {
       float o[L::kCols];
@@ -474,24 +550,40 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < L::kCols; ++i) o[i] = 0.f;
       }
-      const int ch = u * 128 + quad * 32 + lane;
+      const int ch = u * 128 + channel_of(quad * 32 + lane);
       if (split) {
 #pragma unroll
         for (int i = 0; i < L::kCols; ++i) ws[(slot * R + col0 + i) * D + ch] = o[i];
       } else {
+        // through shared memory (the ring is free) so that rows leave in 16-byte pieces; lanes
+        // with channels 2c and 2c + 1 (two apart) trade halves: one has both channels of row i, the other of row i + 1
+        const bool odd = lane & 2;
+        uint8_t* to = smem + (col0 + (odd ? 1 : 0)) * L::kOutPitch + (ch & ~1) * 2;
 #pragma unroll
         for (int i = 0; i < L::kCols; i += 2) {
-          // neighbouring lanes (channels) trade halves: the even one writes both channels of row i, the odd one of row i + 1
-          const float v0 = n > 0 ? o[i] * sm.c[col0 + i] : 0.f, v1 = n > 0 ? o[i + 1] * sm.c[col0 + i + 1] : 0.f;
-          const float got = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? v0 : v1, 1);
-          const int32_t flat = sm.out[col0 + i + (lane & 1)];
-          const uint32_t w = lane & 1 ? pack_bf16x2_rn(got, v1) : pack_bf16x2_rn(v0, got);
-          if (flat >= 0) *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(flat) * D + (ch & ~1)) = w;
+          const float v0 = o[i] * l[i], v1 = o[i + 1] * l[i + 1];
+          const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 2);
+          *reinterpret_cast<uint32_t*>(to + i * L::kOutPitch) = odd ? pack_bf16x2_rn(got, v1) : pack_bf16x2_rn(v0, got);
         }
       }
     }
+    if (!split) {
+      soft_barrier();
+      constexpr int kRowLanes = D / 8;  // 16-byte pieces of a row
+#pragma unroll 4
+      for (int i = threadIdx.x; i < R * kRowLanes; i += kSoftWarps * 32) {
+        const int r = i / kRowLanes, x = i % kRowLanes;
+        const int32_t flat = sm.out[r];
+        if (flat >= 0)
+          *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(flat) * D + x * 8) =
+              *reinterpret_cast<const uint4*>(smem + r * L::kOutPitch + x * 16);
+      }
+    }
     tc_fence_before();
-  } else if (!idle && warp == kMmaWarp && n > 0) {
+    }
+  } else if (warp < kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (warp == kMmaWarp && n > 0) {
     // ------------------------------------------------------------ tensor cores
     if (elect_one()) {
       constexpr uint32_t kIdescS = idesc_f16(R, false, false), kIdescO = idesc_f16(R, true, true);
@@ -539,10 +631,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       if (!mbar_wait(&sm.drain, 0) || !ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
     }
     __syncwarp();
-  } else if (!idle && warp > kMmaWarp && n > 0) {
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    if (n > 0) {
     // ------------------------------------------------------- load and decode
-    const int tid = threadIdx.x - (kMmaWarp + 1) * 32;
-    const int key = tid >> 1, part = tid & 1;  // 64 channels of a unit: 32 code bytes, 4 scale bytes
+    const int tid = threadIdx.x - kLoadWarp * 32;
+    // 64 channels of a unit: 32 code bytes, 4 scale bytes; neighbouring lanes have neighbouring
+    // keys, whose 16-byte chunks the swizzle spreads over all banks
+    const int key = tid & (kKeys - 1), part = tid / kKeys;
     const int32_t* table = a.table + static_cast<int64_t>(tile.b) * a.table_stride;
     const int64_t page_bytes = fp4_page_bytes<D>(a.page_size);
     struct Unit {
@@ -602,11 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
             uint8_t* unit = smem + i * kUnitBytes + part * 16384 + key * 128;
             const uint32_t word[8] = {reg[i].c[0].x, reg[i].c[0].y, reg[i].c[0].z, reg[i].c[0].w,
                                       reg[i].c[1].x, reg[i].c[1].y, reg[i].c[1].z, reg[i].c[1].w};
+            __half2 sc[4];
+            decode_scales(reg[i].s, sc);
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-              const __half_raw sr = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>((reg[i].s >> (8 * (w / 2))) & 0xFFu), __NV_E4M3);
-              *reinterpret_cast<uint4*>(unit + ((w ^ (key & 7)) * 16)) = decode8(word[w], __half2half2(__half(sr)));
-            }
+            for (int w = 0; w < 8; ++w) *reinterpret_cast<uint4*>(unit + ((w ^ (key & 7)) * 16)) = decode8(word[w], sc[w / 2], shifts);
             if (c % L::kUnits == 0 && part == 0) sm.bad[(c / L::kUnits) & 3][key] = was_bad[i] ? 1 : 0;
             fence_proxy_async_smem();
             __syncwarp();
@@ -624,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     if (!ok) {
       atomicExch(&sm.abort, 1);
       if (lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+    }
     }
   }
   pdl_trigger();
@@ -680,7 +777,7 @@ __global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ F
       acc[4 * i + 3] = fmaf(v.w, w, acc[4 * i + 3]);
     }
   }
-  const float inv = all == 0.f ? 0.f : a.g / all;
+  const float inv = all == 0.f ? 0.f : kUnscale * a.g / all;
 #pragma unroll
   for (int i = 0; i < D / 128; ++i)
     *reinterpret_cast<uint2*>(a.out + flat * D + i * 128 + lane * 4) =
@@ -696,7 +793,7 @@ cudaError_t launch(const Fp4AttentionArgs& a, const SplitPlan& p, bool use_pdl, 
   if ((a.page_size & (a.page_size - 1)) == 0)
     for (shift = 0; (1 << shift) != a.page_size;) ++shift;
   e = launch_ex(fp4_attention_kernel<D, R>, dim3(p.tiles, p.splits), dim3(kThreads), smem_bytes<D, R>(), use_pdl, s, a, p.chunk,
-                shift);
+                shift, Shifts{{1u << 9, 1u << 12, 1u << 5, 1u << 8, 1u << 1, 1u << 4}});
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_ex(fp4_join_kernel<D, R>, dim3(p.tiles, R / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
 }
