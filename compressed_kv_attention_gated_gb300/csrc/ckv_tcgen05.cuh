@@ -62,6 +62,15 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, u
       : "memory");
 }
 
+// The same with A in tensor memory (a lane per row, two K elements per column).
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
 // kN consecutive columns of the warp's 32 lanes (one lane per thread).
 template <int kN>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[kN]) {
@@ -93,6 +102,11 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[kN]) {
 }
 
 // Store 8 consecutive columns of the warp's 32 lanes (finish with tc_wait_st).
+__device__ __forceinline__ void tmem_st8(uint32_t addr, uint4 lo, uint4 hi) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(lo.x), "r"(lo.y),
+               "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const float* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
                "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),

@@ -50,8 +50,8 @@ constexpr int kUnitBytes = 32768;
 // Warpgroups (4 warps) 0 and 1: softmax; 2: its first warp issues the MMAs; 3 and 4: load and decode.
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 12, kLoadWarps = 8;
 constexpr int kThreads = (kLoadWarp + kLoadWarps) * 32;
-// Registers per thread: 96 at launch (640 x 96 = 61,440), then 256 x 128 + 128 x 40 + 256 x 88 = 60,416.
-constexpr int kSoftRegs = 128, kMmaRegs = 40, kLoadRegs = 88;
+// Registers per thread: 96 at launch (640 x 96 = 61,440), then 256 x 120 + 128 x 64 + 256 x 88 = 61,440.
+constexpr int kSoftRegs = 120, kMmaRegs = 64, kLoadRegs = 88;
 static_assert(256 * kSoftRegs + 128 * kMmaRegs + 256 * kLoadRegs <= kThreads * 96, "registers of the launch");
 constexpr float kJump = 8.f;     // log2 of the largest weight before the reference moves
 constexpr float kLn2 = 0.69314718055994531f;
@@ -123,14 +123,16 @@ struct Layout {
   static constexpr int kOutPitch = D * 2 + 64;              // output rows on their way out: two rows of 64 bytes hit all banks
   static_assert(R * kOutPitch <= kRing * kUnitBytes, "output staging");
   static constexpr int kTmemO = 0, kTmemS = kUnits * R;
-  static constexpr int kTmemUsed = kTmemS + kBufs * R;
+  static constexpr int kTmemK = kTmemS + kBufs * R;         // decoded units as A of the first product, 64 columns each
+  static constexpr int kSlots = kTmemK + 4 * 64 <= 512 ? 4 : 3;
+  static constexpr int kTmemUsed = kTmemK + kSlots * 64;
   static constexpr int kTmem = kTmemUsed <= 32 ? 32 : kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
   static_assert(kTmemUsed <= 512, "tensor memory");
 };
 
 template <int R>
 struct Small {
-  uint64_t full[kRing], empty[kRing], s_full[2], p_full[2], q_full, o_done, drain;
+  uint64_t full[kRing], empty[kRing], a_free[4], s_full[2], p_full[2], q_full, o_done, drain;
   uint32_t tmem;
   int32_t abort;
   Tile tile;
@@ -140,6 +142,7 @@ struct Small {
   alignas(16) int32_t ctx[R];  // cache rows that the row sees (0: a row without a token)
   int64_t q[R];    // where the row's query begins, elements
   int32_t out[R];  // flat (token, head) index, -1: none
+  float sink[R];   // log2 units, -infinity without
   alignas(16) float keep[R];  // what a move of the references leaves of sums and outputs
   float part[4][R];
   uint8_t bad[4][kKeys];  // keys of a tile that are not there (ring over tiles)
@@ -261,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       for (int i = 0; i < kRing; ++i) {
         mbar_init(&sm.full[i], kLoadWarps);
         mbar_init(&sm.empty[i], 1);
+        mbar_init(&sm.a_free[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.s_full[i], 1);
@@ -306,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     sm.ctx[r] = max(ctx, 0);
     sm.out[r] = flat;
     sm.ref[r] = kNegBig;
+    sm.sink[r] = a.sink && flat >= 0 ? a.sink[flat % a.H] * kLog2e : -INFINITY;
     const uint32_t in_warp = R < 32 ? (1u << (R & 31)) - 1u : 0xFFFFFFFFu;
     const int top = __reduce_max_sync(in_warp, ctx);
     const int low = __reduce_min_sync(in_warp, ctx < 0 ? INT32_MAX : ctx);
@@ -335,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       constexpr int kC = D == 512 ? 16 : 8;     // channels of a lane
       constexpr int kSpan = D / kC;             // lanes of a row
       constexpr int kLoads = R / kSoftWarps * kSpan / 32;
-      constexpr int kBatch = kLoads < 4 ? kLoads : 4;  // rows in flight (registers)
+      constexpr int kBatch = kLoads < 8 ? kLoads : 8;  // rows in flight (registers)
       const int sub = lane / kSpan, ch = lane % kSpan * kC;
       static_assert(kLoads >= 1 && kLoads % kBatch == 0, "");
 #pragma unroll 1
@@ -526,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
         ml[R + r] = total;
       } else {
         float m = sm.ref[r], all = total;
-        if (a.sink && flat >= 0) {
-          const float s = a.sink[flat % a.H] * kLog2e;
+        if (a.sink) {
+          const float s = sm.sink[r];
           const float top = fmaxf(m, s);
           const float keep = fast_exp2(m - top);  // 0 where no key was seen
           all = (total == 0.f ? 0.f : total * keep) + (s == top ? 1.f : fast_exp2(s - top));
@@ -598,10 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
           if (!ok) break;
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
-            const uint64_t da = smem_desc_sw128(base + (c % kRing) * kUnitBytes + (s / 4) * 16384 + (s % 4) * 32, 16, 1024);
             const uint64_t db = smem_desc_sw128(base + L::kQ + (u * 2 + s / 4) * (R * 128) + (s % 4) * 32, 16, 1024);
-            mma_f16_ss(d, da, db, kIdescS, u > 0 || s > 0);
+            mma_f16_ts(d, tmem + L::kTmemK + (c % L::kSlots) * 64 + s * 8, db, kIdescS, u > 0 || s > 0);
           }
+          tc_commit(&sm.a_free[c % L::kSlots]);
         }
         tc_commit(&sm.s_full[j & 1]);
       };
@@ -636,15 +641,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (n > 0) {
     // ------------------------------------------------------- load and decode
-    const int tid = threadIdx.x - kLoadWarp * 32;
-    // 64 channels of a unit: 32 code bytes, 4 scale bytes; neighbouring lanes have neighbouring
-    // keys, whose 16-byte chunks the swizzle spreads over all banks
-    const int key = tid & (kKeys - 1), part = tid / kKeys;
+    // a thread has 64 channels of a unit's 128 for one key, that of its lane of tensor memory;
+    // neighbouring lanes have neighbouring keys, whose 16-byte chunks the swizzle spreads over all banks
+    const int quad = warp & 3, key = quad * 32 + lane, part = (warp - kLoadWarp) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const int32_t* table = a.table + static_cast<int64_t>(tile.b) * a.table_stride;
     const int64_t page_bytes = fp4_page_bytes<D>(a.page_size);
     struct Unit {
-      uint4 c[2];
-      uint32_t s;
+      uint4 c[2];  // 64 codes
+      uint32_t s;  // 4 scales
     };
     Unit reg[kRing];
     const uint8_t *codes = nullptr, *scales = nullptr;
@@ -670,12 +675,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       }
     };
     auto load = [&](Unit& x, int u) {
-      x.c[0] = x.c[1] = make_uint4(0, 0, 0, 0);
-      x.s = 0;
-      if (there) {
-        x.c[0] = *reinterpret_cast<const uint4*>(codes + u * 64);
-        x.c[1] = *reinterpret_cast<const uint4*>(codes + u * 64 + 16);
-        x.s = *reinterpret_cast<const uint32_t*>(scales + u * 8);
+      x.s = there ? *reinterpret_cast<const uint32_t*>(scales + u * 8) : 0u;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x.c[i] = make_uint4(0, 0, 0, 0);
+        if (there) x.c[i] = *reinterpret_cast<const uint4*>(codes + u * 64 + i * 16);
       }
     };
     const int total = n * L::kUnits;
@@ -693,17 +697,26 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       for (int i = 0; i < kRing; ++i) {
         const int c = c0 + i;
         if (c < total && ok) {
-          if (c >= kRing) ok = mbar_wait(&sm.empty[i], ((c / kRing) - 1) & 1);
+          if (c >= L::kSlots) ok = mbar_wait(&sm.a_free[c % L::kSlots], ((c / L::kSlots) - 1) & 1);
+          if (c >= kRing) ok = ok && mbar_wait(&sm.empty[i], ((c / kRing) - 1) & 1);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (ok) {
+            tc_fence_after();
             uint8_t* unit = smem + i * kUnitBytes + part * 16384 + key * 128;
-            const uint32_t word[8] = {reg[i].c[0].x, reg[i].c[0].y, reg[i].c[0].z, reg[i].c[0].w,
-                                      reg[i].c[1].x, reg[i].c[1].y, reg[i].c[1].z, reg[i].c[1].w};
+            const uint32_t a_tile = tmem + lanes + L::kTmemK + (c % L::kSlots) * 64 + part * 32;
             __half2 sc[4];
             decode_scales(reg[i].s, sc);
 #pragma unroll
-            for (int w = 0; w < 8; ++w) *reinterpret_cast<uint4*>(unit + ((w ^ (key & 7)) * 16)) = decode8(word[w], sc[w / 2], shifts);
+            for (int b = 0; b < 4; ++b) {  // blocks of 16 channels
+              const uint4 x = reg[i].c[b / 2];
+              const uint4 lo = decode8(b & 1 ? x.z : x.x, sc[b], shifts), hi = decode8(b & 1 ? x.w : x.y, sc[b], shifts);
+              *reinterpret_cast<uint4*>(unit + (((2 * b) ^ (key & 7)) * 16)) = lo;
+              *reinterpret_cast<uint4*>(unit + (((2 * b + 1) ^ (key & 7)) * 16)) = hi;
+              tmem_st8(a_tile + b * 8, lo, hi);
+            }
             if (c % L::kUnits == 0 && part == 0) sm.bad[(c / L::kUnits) & 3][key] = was_bad[i] ? 1 : 0;
+            tc_wait_st();
+            tc_fence_before();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.full[i]);
