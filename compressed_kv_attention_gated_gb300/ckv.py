@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -19,6 +21,7 @@ from . import build as _build
 
 _lock = threading.Lock()
 _lib = None
+_binding = None
 
 CKV_F32 = 0
 CKV_BF16 = 1
@@ -614,6 +617,26 @@ STEP_MAPS = ("row_start", "positions", "batch_ids", "slot_mapping", "cache_loc",
              "ctx_rows")
 
 
+def _native():
+    """The compiled checks and calls of the serving-step entry points (csrc/binding.cpp)."""
+    global _binding
+    if _binding is None:
+        load()
+        with _lock:
+            if _binding is None:
+                if not os.path.exists(_build.BINDING):
+                    raise RuntimeError(f"{_build.BINDING} is missing: build it first "
+                                       "(python -c 'import __graft_entry__ as g; g.build()')")
+                loader = importlib.machinery.ExtensionFileLoader("ckv_binding", _build.BINDING)
+                _binding = importlib.util.module_from_spec(
+                    importlib.util.spec_from_file_location("ckv_binding", _build.BINDING, loader=loader))
+    return _binding
+
+
+def _raw(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
+
+
 def ckv_build_step_maps(seq_lens, query_lens, block_table, free_pages, cursor, pool_size, page_size, num_tokens,
                         tail_blocks=None, cursor_out=None, out=None, use_pdl=False, err_word=None, stream=None):
     """Block tables and slot maps of one step; see ckv_build_step_maps in include/ckv.h.
@@ -627,60 +650,18 @@ def ckv_build_step_maps(seq_lens, query_lens, block_table, free_pages, cursor, p
     cache_loc int64 [num_tokens], the others int32 [num_tokens]; maps that it
     lacks are not built.
     """
-    L = load()
-    B = seq_lens.numel()
-    if out is None:
+    native = _binding or _native()
+    if stream is not None and out is None:
+        _cuda("ckv_build_step_maps", seq_lens)
         with _on(stream):
-            out = {k: torch.empty(B + 1 if k == "row_start" else num_tokens,
+            out = {k: torch.empty(seq_lens.numel() + 1 if k == "row_start" else num_tokens,
                                   dtype=torch.int64 if k == "cache_loc" else torch.int32, device=seq_lens.device)
                    for k in STEP_MAPS if k != "tail_slots" or tail_blocks is not None}
-    _need(set(out) <= set(STEP_MAPS), f"out may hold {STEP_MAPS}")
-    _cuda("ckv_build_step_maps", seq_lens, query_lens, block_table, free_pages, cursor, tail_blocks, cursor_out,
-          err_word, *out.values())
-    for t in (seq_lens, query_lens, tail_blocks):
-        _need(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() == B),
-              "seq_lens, query_lens and tail_blocks must be contiguous int32 [B]")
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B
-          and (block_table.stride(1) == 1 or block_table.shape[1] <= 1), "block_table must be int32 [B, max_pages], last dim contiguous")
-    _need(B <= 1 or block_table.stride(0) >= block_table.shape[1], "rows of block_table overlap")
-    _need(free_pages.dtype == torch.int32 and free_pages.is_contiguous(), "free_pages must be contiguous int32")
-    inplace = cursor_out is None or cursor_out.data_ptr() == cursor.data_ptr()
-    _need(cursor.dtype == torch.int32 and cursor.is_contiguous() and cursor.numel() >= (2 if inplace else 1),
-          "cursor must be int32 [1], or [2] when it is moved in place")
-    _need(cursor_out is None or (cursor_out.dtype == torch.int32 and cursor_out.numel() >= 1), "cursor_out must be int32 [1]")
-    for k, t in out.items():
-        _need(t.dtype == (torch.int64 if k == "cache_loc" else torch.int32) and t.is_contiguous()
-              and t.numel() == (B + 1 if k == "row_start" else num_tokens), f"out[{k!r}] has the wrong type or size")
-    stride = max(block_table.stride(0), block_table.shape[1])
-    _check("ckv_build_step_maps", L.ckv_build_step_maps(
-        _ptr(seq_lens), _ptr(query_lens), B, int(pool_size), int(page_size), _ptr(block_table), stride,
-        block_table.shape[1], _ptr(free_pages), free_pages.numel(), _ptr(cursor),
-        _ptr(cursor if inplace else cursor_out), _ptr(tail_blocks), int(num_tokens),
-        *(_ptr(out.get(k)) for k in STEP_MAPS), int(bool(use_pdl)), _ptr(err_word), _stream(stream, cursor)))
+    status, out = native.step_maps(seq_lens, query_lens, block_table, free_pages, cursor, pool_size, page_size,
+                                   num_tokens, tail_blocks, cursor_out, out, use_pdl, err_word, _raw(stream))
+    if status:
+        _check("ckv_build_step_maps", status)
     return out
-
-
-def _norm_rows(name, x, positions, weight, out, D):
-    _need(x.dim() == 3 and x.shape[2] == D and x.stride(2) == 1, f"{name} must be [tokens, heads, D], last dim contiguous")
-    if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    _need(out.shape == x.shape and out.stride(2) == 1, f"{name}_out must have the shape of {name}, last dim contiguous")
-    _need(positions.dtype == torch.int32 and positions.is_contiguous() and positions.numel() == x.shape[0],
-          f"{name}_positions must be contiguous int32 [tokens]")
-    _need(weight is None or (weight.dtype == torch.float32 and weight.is_contiguous() and weight.numel() == D),
-          f"{name}_weight must be contiguous float32 [D]")
-    T, H, _ = x.shape
-    # rows that share memory would be written over one another
-    st, sh = out.stride(0), out.stride(1)
-    _need(T * H <= 1 or (min(s for s, n in ((st, T), (sh, H)) if n > 1) >= D
-                         and (T == 1 or H == 1 or st >= H * sh or sh >= T * st)), f"rows of {name}_out overlap")
-
-    def steps(t):  # the stride of a dimension of one entry is never used: 0 passes every check
-        return (t.stride(0) if T > 1 else 0, t.stride(1) if H > 1 else 0)
-
-    s = NormRows(x.data_ptr(), out.data_ptr(), None if weight is None else weight.data_ptr(), positions.data_ptr(),
-                 *steps(x), *steps(out), T, H, _dtype(x), _dtype(out), 0)
-    return s, out
 
 
 def ckv_qk_norm_rope(q, q_positions, cos_sin=None, q_weight=None, q_out=None, k=None, k_positions=None, k_weight=None,
@@ -694,30 +675,18 @@ def ckv_qk_norm_rope(q, q_positions, cos_sin=None, q_weight=None, q_out=None, k=
     the last rope_dim channels.  Returns (q_out, k_out): new bf16 tensors, or
     the float32/bf16 ones given (q_out may be q).
     """
-    L = load()
-    _cuda("ckv_qk_norm_rope", q, q_positions, cos_sin, q_weight, q_out, k, k_positions, k_weight, k_out, err_word)
-    D = q.shape[-1]
-    _need(cos_sin is None or (cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()),
-          "cos_sin must be contiguous float32 [positions, rope_dim]")
-    n_pos, R = (0, 0) if cos_sin is None else cos_sin.shape
-    if rope_offset is None:
-        rope_offset = D - R
-    _need(k is None or k_positions is not None, "k needs k_positions")
-    with _on(stream):
-        a, q_out = _norm_rows("q", q, q_positions, q_weight, q_out, D)
-        b = None
-        if k is not None:
-            b, k_out = _norm_rows("k", k, k_positions, k_weight, k_out, D)
-    _check("ckv_qk_norm_rope", L.ckv_qk_norm_rope(
-        ctypes.byref(a), None if b is None else ctypes.byref(b), _ptr(cos_sin), n_pos, D, R, int(rope_offset),
-        int(bool(interleaved)), float(eps), int(bool(use_pdl)), _ptr(err_word), _stream(stream, q)))
-    return q_out, (k_out if b is not None else None)
-
-
-def _fp4_cache(kv_cache, D):
-    _need(kv_cache.dtype == torch.uint8 and kv_cache.is_contiguous() and kv_cache.dim() == 3
-          and kv_cache.shape[2] == D // 2 + D // 16, "kv_cache must be contiguous uint8 [pages, page_size, D/2 + D/16]")
-    return kv_cache.shape[0], kv_cache.shape[1]
+    native = _binding or _native()
+    if stream is not None:
+        _cuda("ckv_qk_norm_rope", q, k)
+        with _on(stream):
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
+            if k is not None and k_out is None:
+                k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+    status, q_out, k_out = native.qk_norm_rope(q, q_positions, cos_sin, q_weight, q_out, k, k_positions, k_weight,
+                                               k_out, rope_offset, interleaved, eps, use_pdl, err_word, _raw(stream))
+    if status:
+        _check("ckv_qk_norm_rope", status)
+    return q_out, k_out
 
 
 def ckv_fp4_store(rows, kv_cache, loc, cache_scale=1.0, use_pdl=False, err_word=None, stream=None):
@@ -727,15 +696,9 @@ def ckv_fp4_store(rows, kv_cache, loc, cache_scale=1.0, use_pdl=False, err_word=
     page_size, D/2 + D/16]; loc int64 [n], < 0 skips a row; cache_scale a power
     of two.
     """
-    L = load()
-    _cuda("ckv_fp4_store", rows, kv_cache, loc, err_word)
-    _need(rows.dim() == 2 and rows.stride(1) == 1, "rows must be [n, D], last dim contiguous")
-    n, D = rows.shape
-    pages, ps = _fp4_cache(kv_cache, D)
-    _need(loc.dtype == torch.int64 and loc.is_contiguous() and loc.numel() == n, "loc must be contiguous int64 [n]")
-    _check("ckv_fp4_store", L.ckv_fp4_store(
-        _ptr(rows), _dtype(rows), rows.stride(0) if n > 1 else 0, n, D, _ptr(kv_cache), pages, ps, _ptr(loc),
-        float(cache_scale), int(bool(use_pdl)), _ptr(err_word), _stream(stream, rows)))
+    status = (_binding or _native()).fp4_store(rows, kv_cache, loc, cache_scale, use_pdl, err_word, _raw(stream))
+    if status:
+        _check("ckv_fp4_store", status)
 
 
 def ckv_fp4_load(kv_cache, loc, out, cache_scale=1.0, use_pdl=False, err_word=None, stream=None):
@@ -744,15 +707,9 @@ def ckv_fp4_load(kv_cache, loc, out, cache_scale=1.0, use_pdl=False, err_word=No
     kv_cache, loc, cache_scale as for ckv_fp4_store; out float32/bf16 [n, D] (last
     dim contiguous); rows with loc < 0 are left as they are.
     """
-    L = load()
-    _cuda("ckv_fp4_load", kv_cache, loc, out, err_word)
-    _need(out.dim() == 2 and out.stride(1) == 1, "out must be [n, D], last dim contiguous")
-    n, D = out.shape
-    pages, ps = _fp4_cache(kv_cache, D)
-    _need(loc.dtype == torch.int64 and loc.is_contiguous() and loc.numel() == n, "loc must be contiguous int64 [n]")
-    _check("ckv_fp4_load", L.ckv_fp4_load(
-        _ptr(kv_cache), pages, ps, _ptr(loc), n, D, _ptr(out), _dtype(out), out.stride(0) if n > 1 else 0,
-        float(cache_scale), int(bool(use_pdl)), _ptr(err_word), _stream(stream, out)))
+    status = (_binding or _native()).fp4_load(out, kv_cache, loc, cache_scale, use_pdl, err_word, _raw(stream))
+    if status:
+        _check("ckv_fp4_load", status)
     return out
 
 
@@ -772,34 +729,20 @@ def ckv_fp4_attention(q, kv_cache, block_table, row_start, ctx_rows, max_rows, s
     workspace: a uint8 tensor of ckv_fp4_attention_workspace() bytes, by default
     taken from the caching allocator of torch for this call.
     """
-    L = load()
-    _cuda("ckv_fp4_attention", q, kv_cache, block_table, row_start, ctx_rows, sink, out, lse, workspace, err_word)
-    _need(q.dtype == torch.bfloat16 and q.dim() == 3 and q.stride(2) == 1, "q must be bf16 [T, H, D], last dim contiguous")
-    T, H, D = q.shape
-    pages, ps = _fp4_cache(kv_cache, D)
-    _need(row_start.dtype == torch.int32 and row_start.is_contiguous() and row_start.numel() >= 1, "row_start must be int32 [B + 1]")
-    B = row_start.numel() - 1
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B
-          and (block_table.stride(1) == 1 or block_table.shape[1] <= 1), "block_table must be int32 [B, max_pages], last dim contiguous")
-    _need(ctx_rows.dtype == torch.int32 and ctx_rows.is_contiguous() and ctx_rows.numel() == T, "ctx_rows must be int32 [T]")
-    _need(sink is None or (sink.dtype == torch.float32 and sink.is_contiguous() and sink.numel() == H), "sink must be float32 [H]")
-    need = L.ckv_fp4_attention_workspace(T, B, H, D, int(max_rows))
-    with _on(stream):
-        if out is None:
-            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _need(out.dtype == torch.bfloat16 and out.is_contiguous() and tuple(out.shape) == (T, H, D), "out must be contiguous bf16 [T, H, D]")
-    _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (T, H), "lse must be contiguous float32 [T, H]")
-    _need(workspace is None or workspace.is_contiguous(), "workspace must be contiguous")
-    _check("ckv_fp4_attention", L.ckv_fp4_attention(
-        _ptr(q), q.stride(0) if T > 1 else 0, q.stride(1) if H > 1 else 0, T, H, D, _ptr(kv_cache), pages, ps,
-        float(cache_scale), _ptr(block_table), max(block_table.stride(0), block_table.shape[1]), block_table.shape[1],
-        _ptr(row_start), B, _ptr(ctx_rows), int(max_rows), float(softmax_scale), _ptr(sink), _ptr(out), _ptr(lse),
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), int(bool(use_pdl)),
-        _ptr(err_word), _stream(stream, q)))
+    native = _binding or _native()
+    if stream is not None:
+        _cuda("ckv_fp4_attention", q)
+        T, H, D = q.shape
+        need = ckv_fp4_attention_workspace(T, row_start.numel() - 1, H, D, max_rows)
+        with _on(stream):
+            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+            lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if lse is None else lse
+            if workspace is None and need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    status, out, lse = native.fp4_attention(q, kv_cache, block_table, row_start, ctx_rows, max_rows, softmax_scale,
+                                            cache_scale, sink, out, lse, workspace, use_pdl, err_word, _raw(stream))
+    if status:
+        _check("ckv_fp4_attention", status)
     return out, lse
 
 
