@@ -52,7 +52,7 @@ ckv_status check_norm_rows(const ckv_norm_rows& r) {
   if (r.tokens < 0 || r.heads < 0 || r.reserved != 0) return CKV_ERR_SHAPE;
   if (!dtype_ok(r.dtype) || !dtype_ok(r.out_dtype)) return CKV_ERR_DTYPE;
   if (r.tokens == 0 || r.heads == 0) return CKV_OK;
-  if (r.tokens > INT32_MAX) return CKV_ERR_SHAPE;
+  if (r.tokens > (1 << 30) / r.heads) return CKV_ERR_SHAPE;  // rows are counted in 32 bits
   if (!r.x || !r.out || !r.positions) return CKV_ERR_NULL;
   if (r.stride_t < 0 || r.stride_h < 0 || r.out_stride_t < 0 || r.out_stride_h < 0) return CKV_ERR_SHAPE;
   const int64_t in = r.dtype == CKV_F32 ? 4 : 8, out = r.out_dtype == CKV_F32 ? 4 : 8;

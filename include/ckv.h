@@ -572,8 +572,8 @@ typedef struct ckv_norm_rows {
  * (a, b) becomes (a c - b s, b c + a s), where the pair is channels (i, i + R/2)
  * of the span, or (2 i, 2 i + 1) when interleaved != 0.  Computed in fp32 and
  * rounded once, to out_dtype.  Rows of tokens with a negative position are
- * neither read nor written.
- * q, k      host structs; k may be NULL.  Rows 16-byte aligned.
+ * not written, whatever they hold.
+ * q, k      host structs; k may be NULL.  Rows 16-byte aligned; tokens * heads <= 2^30.
  * cos_sin   device fp32 [num_positions][rope_dim] (NULL with rope_dim == 0); a
  *           position >= num_positions sets CKV_DEVERR_SEQ_LEN and its rows are
  *           skipped.
