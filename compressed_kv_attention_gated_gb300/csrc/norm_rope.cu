@@ -5,15 +5,21 @@
 //   become (a c - b s, b c + a s); fp32 throughout, one rounding to the output.
 //
 // Bound by HBM: D values in, D values out, a few FMAs each.  A lane owns eight
-// neighbouring channels (two such groups at D = 512), so every access is 16
-// bytes per lane; a row takes 32 lanes (16 at D = 128, two rows to a warp).
-// Warps stay resident and walk over the rows: the next row and its position
-// are on their way while a row is worked on, and weights stay in registers.
+// channels (two such groups at D = 512), a row takes 32 lanes (16 at D = 128, two
+// rows to a warp).  A warp takes a token and some of its heads: position, angles
+// and weights are loaded once for all of them, and the next rows are on their way
+// (2 KB per warp) while a batch of rows is worked on, whose sums are formed side by
+// side so that the shuffles' latencies overlap.
 //
-// The rotation's partner is in the same lane when pairs are neighbours, and in
-// another one when they are halves of the span: the normalised row then goes
-// through the warp's row in shared memory.  Spans and offsets that are not whole
-// groups of eight channels (16 for halves) take a channel-by-channel path.
+// Both channels of a rotated pair belong to one lane: eight neighbours when pairs
+// are neighbours (16-byte accesses), and when they are halves of the span, four
+// of the first half and their four partners (8-byte accesses at bf16, still 256
+// bytes in a row per warp).  Spans and offsets that are not whole groups of eight
+// channels take a channel-by-channel path through shared memory.
+//
+// Measured (GB300, L2 cold, 6.8 TB/s copy peak): 8192 tokens x 64 heads of 512,
+// bf16: 175-177 us (a copy of the same bytes 167), 65,536 x 24 of 128: 142-146 us
+// (copy 125).  Loading the angles per row instead of per token: 205-273 and 179-198.
 #include <cstdint>
 
 #include "ckv_device.cuh"
@@ -24,201 +30,287 @@ namespace ckv {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormBlocks = 4;  // per SM
-
+constexpr uint32_t kNormShare = 32;  // heads of a token that a warp takes at most
 enum Rotation { kNone, kPairs, kHalves, kAny };
 
-// A lane's channels of one row as they come from memory, and where they belong.
-template <int kGroups>
-struct Fetched {
-  uint4 raw[kGroups * 2];  // fp32: 8 words per group; bf16: the first 4
-  int64_t out;             // element offset of the row's output
-  int32_t pos;             // < 0: nothing to do
-  int32_t set;
-};
+// Blocks per SM: two, because 128 registers hold everything.  (With three and a few
+// spilled registers 8192 x 64 rows of 512 took 220-257 us instead of 173-177.)
+constexpr int kNormBlocks = 2;
 
-__device__ __forceinline__ float4 as_float4(uint4 w) {
-  return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+// Two fp32 values for the packed instructions (each half an ordinary IEEE operation).
+struct Two {
+  uint64_t v;
+  __device__ __forceinline__ Two() {}
+  __device__ __forceinline__ Two(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
-template <int D, Rotation kRot>
-__global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-  constexpr int kLanes = D >= 256 ? 32 : D / 8;   // of a row
-  constexpr int kRows = 32 / kLanes;              // rows of a warp
-  constexpr int kGroups = D / (kLanes * 8);
-  constexpr bool kStage = kRot == kHalves || kRot == kAny;
-  __shared__ __align__(16) float s_rows[kStage ? kNormThreads / 32 * kRows : 1][kStage ? D : 4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane / kLanes, sl = lane % kLanes;
-  float* s_row = s_rows[kStage ? warp * kRows + sub : 0];
-  pdl_wait();
-  const uint32_t rows_q = static_cast<uint32_t>(a.set[0].tokens * a.set[0].heads);
-  const uint32_t rows = rows_q + static_cast<uint32_t>(a.set[1].tokens * a.set[1].heads);
-  const uint32_t step = gridDim.x * (kNormThreads / 32) * kRows;
+__device__ __forceinline__ void widen(uint4 x, uint4 y, bool f32, Two (&v)[4]) {
+  if (f32) {
+    v[0] = Two(__uint_as_float(x.x), __uint_as_float(x.y)), v[1] = Two(__uint_as_float(x.z), __uint_as_float(x.w));
+    v[2] = Two(__uint_as_float(y.x), __uint_as_float(y.y)), v[3] = Two(__uint_as_float(y.z), __uint_as_float(y.w));
+  } else {
+    v[0] = Two(bf16_lo(x.x), bf16_hi(x.x)), v[1] = Two(bf16_lo(x.y), bf16_hi(x.y));
+    v[2] = Two(bf16_lo(x.z), bf16_hi(x.z)), v[3] = Two(bf16_lo(x.w), bf16_hi(x.w));
+  }
+}
 
-  auto fetch = [&](Fetched<kGroups>& f, uint32_t r) {
-    f.pos = -1;
-    if (r >= rows) return;
-    f.set = r >= rows_q;
-    const ckv_norm_rows& m = a.set[f.set];
-    const uint32_t i = f.set ? r - rows_q : r;
-    const uint32_t t = i / static_cast<uint32_t>(m.heads), h = i - t * static_cast<uint32_t>(m.heads);
-    f.out = t * m.out_stride_t + h * m.out_stride_h;
-    f.pos = m.positions[t];
-    const int64_t in = t * m.stride_t + h * m.stride_h + sl * 8;
+template <bool kSplit>
+__device__ __forceinline__ void store_row(const ckv_norm_rows& m, int64_t at, const int (&base)[2], const float (&v)[8]) {
+  if (m.out_dtype == CKV_F32) {
+    float* o = static_cast<float*>(m.out) + at;
+    *reinterpret_cast<float4*>(o + base[0]) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(o + base[1]) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(m.out) + at;
+    const uint4 x = make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
+    if constexpr (kSplit) {
+      *reinterpret_cast<uint2*>(o + base[0]) = make_uint2(x.x, x.y);
+      *reinterpret_cast<uint2*>(o + base[1]) = make_uint2(x.z, x.w);
+    } else {
+      *reinterpret_cast<uint4*>(o + base[0]) = x;
+    }
+  }
+}
+
+// Heads h0 .. h1 - 1 of token t of one set, by one warp.  The lane's channels are
+// base[g][0] + 0..3 and base[g][1] + 0..3.
+template <int D, Rotation kRot, bool kF32>
+__device__ __forceinline__ void norm_heads(const NormRopeArgs& a, const ckv_norm_rows& m, uint32_t t, uint32_t h0, uint32_t h1,
+                                           float* s_row) {
+  constexpr int kLanes = D >= 256 ? 32 : D / 8;  // of a row
+  constexpr int kRows = 32 / kLanes;             // rows of a warp
+  constexpr int kGroups = D / (kLanes * 8);
+  constexpr int kBatch = (D == 512 ? 2 : 4) / (kF32 ? 2 : 1);
+  const int sl = (threadIdx.x & 31) % kLanes, sub = (threadIdx.x & 31) / kLanes;
+  const int half = a.rope_dim >> 1;
+  int base[kGroups][2];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (m.dtype == CKV_F32) {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(m.x) + in + g * 256);
-        f.raw[2 * g] = p[0];
-        f.raw[2 * g + 1] = p[1];
+  for (int g = 0; g < kGroups; ++g) {
+    const int q = g * 32 + sl;  // of D/8
+    base[g][0] = q * 8;
+    base[g][1] = q * 8 + 4;
+    if constexpr (kRot == kHalves) {
+      if (q * 8 < a.rope_dim) {
+        base[g][0] = a.rope_offset + q * 4;
+        base[g][1] = a.rope_offset + half + q * 4;
       } else {
-        f.raw[2 * g] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.x) + in + g * 256);
+        const int c = q * 8 - a.rope_dim;
+        base[g][0] = c < a.rope_offset ? c : c + a.rope_dim;
+        base[g][1] = base[g][0] + 4;
+      }
+    }
+  }
+  struct Rows {
+    uint4 raw[kBatch][kGroups][kF32 ? 2 : 1];
+  };
+  const int64_t in0 = static_cast<int64_t>(t) * m.stride_t;
+  auto load = [&](Rows& x, uint32_t h) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const uint32_t hh = h + b * kRows + sub;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        x.raw[b][g][0] = x.raw[b][g][kF32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
+        if (hh < h1) {
+          const int64_t in = in0 + hh * m.stride_h;
+          if constexpr (kF32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              x.raw[b][g][i] = *reinterpret_cast<const uint4*>(static_cast<const float*>(m.x) + in + base[g][i]);
+          } else if constexpr (kRot == kHalves) {
+            const uint2 lo = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(m.x) + in + base[g][0]);
+            const uint2 hi = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(m.x) + in + base[g][1]);
+            x.raw[b][g][0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          } else {
+            x.raw[b][g][0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.x) + in + base[g][0]);
+          }
+        }
       }
     }
   };
-
-  float w[kGroups][8];
-  int w_set = -1;
-  uint32_t base = (blockIdx.x * (kNormThreads / 32) + warp) * kRows;
-  Fetched<kGroups> next;
-  fetch(next, base + sub);
-  for (; base < rows; base += step) {
-    const Fetched<kGroups> f = next;
-    if (base + step < rows) fetch(next, base + step + sub);
-    const ckv_norm_rows& m = a.set[f.pos >= 0 ? f.set : 0];
-    bool on = f.pos >= 0;
-    if (kRot != kNone && on && f.pos >= a.num_positions) {
-      if (sl == 0) flag_error(a.err, CKV_DEVERR_SEQ_LEN);
-      on = false;
-    }
-    float v[kGroups][8];
-    float sum = 0.f;
+  const int32_t pos = m.positions[t];
+  Rows cur, next;
+  load(cur, h0);
+  if (pos < 0) return;
+  if (kRot != kNone && pos >= a.num_positions) {
+    if (sl == 0) flag_error(a.err, CKV_DEVERR_SEQ_LEN);
+    return;
+  }
+  const float* cs = a.cos_sin + static_cast<int64_t>(pos) * a.rope_dim;
+  bool in_span[kGroups];
+  Two c2[kGroups][2], s2[kGroups][2], w[kGroups][4];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (m.dtype == CKV_F32) {
-        const float4 x = as_float4(f.raw[2 * g]), y = as_float4(f.raw[2 * g + 1]);
-        v[g][0] = x.x, v[g][1] = x.y, v[g][2] = x.z, v[g][3] = x.w;
-        v[g][4] = y.x, v[g][5] = y.y, v[g][6] = y.z, v[g][7] = y.w;
-      } else {
-        const uint4 x = f.raw[2 * g];
-        v[g][0] = bf16_lo(x.x), v[g][1] = bf16_hi(x.x), v[g][2] = bf16_lo(x.y), v[g][3] = bf16_hi(x.y);
-        v[g][4] = bf16_lo(x.z), v[g][5] = bf16_hi(x.z), v[g][6] = bf16_lo(x.w), v[g][7] = bf16_hi(x.w);
+  for (int g = 0; g < kGroups; ++g) {
+    in_span[g] = false;
+    if constexpr (kRot == kPairs || kRot == kHalves) {
+      in_span[g] = kRot == kPairs ? base[g][0] >= a.rope_offset && base[g][0] < a.rope_offset + a.rope_dim : (g * 32 + sl) * 8 < a.rope_dim;
+      float4 co = make_float4(1.f, 1.f, 1.f, 1.f), si = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (in_span[g]) {
+        const int p = kRot == kPairs ? (base[g][0] - a.rope_offset) >> 1 : base[g][0] - a.rope_offset;
+        co = __ldg(reinterpret_cast<const float4*>(cs + p));
+        si = __ldg(reinterpret_cast<const float4*>(cs + half + p));
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(v[g][j], v[g][j], sum);
+      c2[g][0] = Two(co.x, co.y), c2[g][1] = Two(co.z, co.w);
+      s2[g][0] = Two(si.x, si.y), s2[g][1] = Two(si.z, si.w);
     }
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    const float inv = 1.f / sqrtf(sum * (1.f / D) + a.eps);
-    if (on && w_set != f.set) {
-      w_set = f.set;
+    for (int i = 0; i < 2; ++i) {
+      const float4 f = m.weight ? __ldg(reinterpret_cast<const float4*>(m.weight + base[g][i])) : make_float4(1.f, 1.f, 1.f, 1.f);
+      w[g][2 * i] = Two(f.x, f.y);
+      w[g][2 * i + 1] = Two(f.z, f.w);
+    }
+  }
+  const int64_t out0 = static_cast<int64_t>(t) * m.out_stride_t;
+  for (uint32_t h = h0; h < h1; h += kBatch * kRows) {
+    if (h + kBatch * kRows < h1) load(next, h + kBatch * kRows);
+    float inv[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      Two sum(0.f, 0.f);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
+        Two v[4];
+        widen(cur.raw[b][g][0], cur.raw[b][g][kF32 ? 1 : 0], kF32, v);
 #pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-          const float4 x = m.weight ? *reinterpret_cast<const float4*>(m.weight + g * 256 + sl * 8 + j) : make_float4(1.f, 1.f, 1.f, 1.f);
-          w[g][j] = x.x, w[g][j + 1] = x.y, w[g][j + 2] = x.z, w[g][j + 3] = x.w;
-        }
+        for (int j = 0; j < 4; ++j) sum = fma(v[j], v[j], sum);
       }
+      float lo, hi;
+      sum.get(lo, hi);
+      inv[b] = lo + hi;
     }
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[g][j] *= inv * w[g][j];
-      if constexpr (kStage) {
-        float4* s = reinterpret_cast<float4*>(s_row + g * 256 + sl * 8);
-        s[0] = make_float4(v[g][0], v[g][1], v[g][2], v[g][3]);
-        s[1] = make_float4(v[g][4], v[g][5], v[g][6], v[g][7]);
-      }
+      for (int b = 0; b < kBatch; ++b) inv[b] += __shfl_xor_sync(0xFFFFFFFFu, inv[b], o);
     }
-    if constexpr (kStage) __syncwarp();
-    if (kRot != kNone && on) {
-      const float* cs = a.cos_sin + static_cast<int64_t>(f.pos) * a.rope_dim;
-      const int half = a.rope_dim >> 1;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) inv[b] = rsqrtf(inv[b] * (1.f / D) + a.eps);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const uint32_t hh = h + b * kRows + sub;
+      const int64_t out = out0 + hh * m.out_stride_h;
+      const Two scale(inv[b], inv[b]);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const int c0 = g * 256 + sl * 8, k0 = c0 - a.rope_offset;
-        if constexpr (kRot == kPairs) {
-          if (k0 >= 0 && k0 < a.rope_dim) {
-            const float4 co = __ldg(reinterpret_cast<const float4*>(cs + k0 / 2)), si = __ldg(reinterpret_cast<const float4*>(cs + half + k0 / 2));
-            const float c[4] = {co.x, co.y, co.z, co.w}, s[4] = {si.x, si.y, si.z, si.w};
+        Two z[4];
+        widen(cur.raw[b][g][0], cur.raw[b][g][kF32 ? 1 : 0], kF32, z);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = mul(mul(z[j], scale), w[g][j]);
+        if constexpr (kRot == kAny) {
+          // the normalised row, for the partners of other lanes
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[j].get(s_row[base[g][0] + 2 * j], s_row[base[g][0] + 2 * j + 1]);
+        } else {
+          if (kRot == kPairs && in_span[g]) {  // z[j] = (x, y): (x, y) c + (-y, x) s
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float x = v[g][2 * j], y = v[g][2 * j + 1];
-              v[g][2 * j] = x * c[j] - y * s[j];
-              v[g][2 * j + 1] = y * c[j] + x * s[j];
+              float x, y, c[2], si[2];
+              z[j].get(x, y);
+              c2[g][j >> 1].get(c[0], c[1]);
+              s2[g][j >> 1].get(si[0], si[1]);
+              z[j] = fma(z[j], Two(c[j & 1], c[j & 1]), mul(Two(-y, x), Two(si[j & 1], si[j & 1])));
+            }
+          } else if (kRot == kHalves && in_span[g]) {  // z[j], z[2 + j] = two x and their two y
+            const Two minus(-1.f, -1.f);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const Two x = z[j], y = z[2 + j];
+              z[j] = fma(x, c2[g][j], mul(mul(y, minus), s2[g][j]));
+              z[2 + j] = fma(y, c2[g][j], mul(x, s2[g][j]));
             }
           }
-        } else if constexpr (kRot == kHalves) {
-          if (k0 >= 0 && k0 < a.rope_dim) {
-            const bool second = k0 >= half;
-            const int p = second ? k0 - half : k0;
-            const float* mate = s_row + (second ? c0 - half : c0 + half);
+          float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              const float4 co = __ldg(reinterpret_cast<const float4*>(cs + p + j)), si = __ldg(reinterpret_cast<const float4*>(cs + half + p + j));
-              const float4 o = *reinterpret_cast<const float4*>(mate + j);
-              const float c[4] = {co.x, co.y, co.z, co.w}, s[4] = {si.x, si.y, si.z, si.w}, z[4] = {o.x, o.y, o.z, o.w};
+          for (int j = 0; j < 4; ++j) z[j].get(v[2 * j], v[2 * j + 1]);
+          if (hh < h1) store_row<kRot == kHalves>(m, out, base[g], v);
+        }
+      }
+      if constexpr (kRot == kAny) {
+        __syncwarp();
+        if (hh < h1) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x = v[g][j + i];
-                v[g][j + i] = second ? x * c[i] + z[i] * s[i] : x * c[i] - z[i] * s[i];
+          for (int g = 0; g < kGroups; ++g) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int c = base[g][0] + j, k = c - a.rope_offset;
+              v[j] = s_row[c];
+              if (k >= 0 && k < a.rope_dim) {
+                const bool second = a.interleaved ? (k & 1) : k >= half;
+                const int p = a.interleaved ? k >> 1 : (second ? k - half : k);
+                const int mate = a.interleaved ? (second ? c - 1 : c + 1) : (second ? c - half : c + half);
+                const float cc = __ldg(cs + p), ss = __ldg(cs + half + p);
+                v[j] = second ? v[j] * cc + s_row[mate] * ss : v[j] * cc - s_row[mate] * ss;
               }
             }
-          }
-        } else if constexpr (kRot == kAny) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int c = c0 + j, k = k0 + j;
-            if (k >= 0 && k < a.rope_dim) {
-              const bool second = a.interleaved ? (k & 1) : k >= half;
-              const int p = a.interleaved ? k >> 1 : (second ? k - half : k);
-              const int mate = a.interleaved ? (second ? c - 1 : c + 1) : (second ? c - half : c + half);
-              const float co = __ldg(cs + p), si = __ldg(cs + half + p);
-              v[g][j] = second ? v[g][j] * co + s_row[mate] * si : v[g][j] * co - s_row[mate] * si;
-            }
+            store_row<false>(m, out, base[g], v);
           }
         }
+        __syncwarp();
       }
     }
-    if (on) {
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const int64_t at = f.out + g * 256 + sl * 8;
-        if (m.out_dtype == CKV_F32) {
-          float4* p = reinterpret_cast<float4*>(static_cast<float*>(m.out) + at);
-          p[0] = make_float4(v[g][0], v[g][1], v[g][2], v[g][3]);
-          p[1] = make_float4(v[g][4], v[g][5], v[g][6], v[g][7]);
-        } else {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(m.out) + at) =
-              make_uint4(pack_bf16x2_rn(v[g][0], v[g][1]), pack_bf16x2_rn(v[g][2], v[g][3]),
-                         pack_bf16x2_rn(v[g][4], v[g][5]), pack_bf16x2_rn(v[g][6], v[g][7]));
-        }
-      }
-    }
-    if constexpr (kStage) __syncwarp();
+    cur = next;
+  }
+}
+
+template <int D, Rotation kRot>
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks)
+    norm_rope_kernel(const __grid_constant__ NormRopeArgs a, uint32_t share) {
+  constexpr int kRows = D >= 256 ? 1 : 256 / D;  // of a warp
+  __shared__ float s_rows[kRot == kAny ? kNormThreads / 32 * kRows : 1][kRot == kAny ? D : 1];
+  const int warp = threadIdx.x >> 5, sub = (threadIdx.x & 31) / (32 / kRows);
+  float* s_row = s_rows[kRot == kAny ? warp * kRows + sub : 0];
+  pdl_wait();
+  // a unit is `share` heads of a token
+  const uint32_t per_q = (a.set[0].heads + share - 1) / share, per_k = (a.set[1].heads + share - 1) / share;
+  const uint32_t units_q = static_cast<uint32_t>(a.set[0].tokens) * per_q;
+  const uint32_t units = units_q + static_cast<uint32_t>(a.set[1].tokens) * per_k;
+  const uint32_t step = gridDim.x * (kNormThreads / 32);
+  for (uint32_t u = blockIdx.x * (kNormThreads / 32) + warp; u < units; u += step) {
+    const ckv_norm_rows& m = a.set[u >= units_q];
+    const uint32_t i = u < units_q ? u : u - units_q, per = u < units_q ? per_q : per_k;
+    const uint32_t t = i / per, h0 = (i - t * per) * share, h1 = min(h0 + share, static_cast<uint32_t>(m.heads));
+    if (m.dtype == CKV_F32) norm_heads<D, kRot, true>(a, m, t, h0, h1, s_row);
+    else norm_heads<D, kRot, false>(a, m, t, h0, h1, s_row);
   }
 }
 
 template <int D, Rotation kRot>
 cudaError_t launch_rot(const NormRopeArgs& a, bool use_pdl, cudaStream_t s) {
-  constexpr int kPerBlock = kNormThreads / 32 * (D >= 256 ? 1 : 256 / D);
-  const int64_t rows = a.set[0].tokens * a.set[0].heads + a.set[1].tokens * a.set[1].heads;
   int dev = 0, sms = 0;
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  const int64_t want = (rows + kPerBlock - 1) / kPerBlock, most = static_cast<int64_t>(sms) * kNormBlocks;
-  return launch_ex(norm_rope_kernel<D, kRot>, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kNormThreads), 0, use_pdl,
-                   s, a);
+  const int64_t most = static_cast<int64_t>(sms) * kNormBlocks;
+  // as many heads of a token to a warp as leaves every resident warp two units
+  int64_t units = 0;
+  uint32_t share = kNormShare;
+  for (; share >= 1; share /= 2) {
+    units = 0;
+    for (const ckv_norm_rows& m : a.set) units += m.tokens * ((m.heads + share - 1) / share);
+    if (units >= 2 * most * (kNormThreads / 32) || share == 1) break;
+  }
+  const int64_t want = (units + kNormThreads / 32 - 1) / (kNormThreads / 32);
+  return launch_ex(norm_rope_kernel<D, kRot>, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kNormThreads), 0, use_pdl, s,
+                   a, share);
 }
 
 template <int D>
 cudaError_t launch_d(const NormRopeArgs& a, bool use_pdl, cudaStream_t s) {
   if (a.rope_dim == 0) return launch_rot<D, kNone>(a, use_pdl, s);
   // whole groups of eight channels, and cos | sin rows that 16-byte loads can start in
-  const bool whole = a.rope_offset % 8 == 0 && a.rope_dim % (a.interleaved ? 8 : 16) == 0 &&
+  const bool whole = a.rope_offset % 8 == 0 && a.rope_dim % 8 == 0 &&
                      reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0;
   if (!whole) return launch_rot<D, kAny>(a, use_pdl, s);
   return a.interleaved ? launch_rot<D, kPairs>(a, use_pdl, s) : launch_rot<D, kHalves>(a, use_pdl, s);
