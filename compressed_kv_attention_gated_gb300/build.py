@@ -25,7 +25,8 @@ BINDING = os.path.join(LIBDIR, "ckv_binding.so")
 
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 CUDA_SOURCES = ["kpool.cu", "c128.cu", "prefill_tma.cu", "planner_device.cu", "validate.cu", "probe.cu",
-                "step_maps.cu", "norm_rope.cu", "fp4_rows.cu", "fp4_attention.cu", "capi.cu"]
+                "step_maps.cu", "norm_rope.cu", "fp4_rows.cu", "fp4_attention.cu",
+                "fp4_attention_rows.cu", "capi.cu"]
 CXX_SOURCES = ["planner.cpp"]
 BINDING_SOURCE = "binding.cpp"  # CPython module over torch tensors, linked against the library
 

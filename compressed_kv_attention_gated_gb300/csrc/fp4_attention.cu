@@ -32,85 +32,17 @@
 //
 // Long rows of few tiles are split over CTAs (blockIdx.y), whose partial
 // outputs (fp32) and references a second kernel joins in a fixed order.
-#include <cmath>
-#include <cstdint>
-
-#include "ckv_device.cuh"
-#include "ckv_fp4.cuh"
-#include "ckv_launch.h"
-#include "ckv_launch_util.cuh"
-#include "ckv_tcgen05.cuh"
+#include "fp4_attention.cuh"
 
 namespace ckv {
 namespace {
 
-constexpr int kKeys = 128;       // cache rows per tile
-constexpr int kRing = 4;         // units of 128 keys x 128 channels
-constexpr int kUnitBytes = 32768;
 // Warpgroups (4 warps) 0 and 1: softmax; 2: its first warp issues the MMAs; 3 and 4: load and decode.
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 12, kLoadWarps = 8;
 constexpr int kThreads = (kLoadWarp + kLoadWarps) * 32;
 // Registers per thread: 96 at launch (640 x 96 = 61,440), then 256 x 120 + 128 x 64 + 256 x 88 = 61,440.
 constexpr int kSoftRegs = 120, kMmaRegs = 64, kLoadRegs = 88;
 static_assert(256 * kSoftRegs + 128 * kMmaRegs + 256 * kLoadRegs <= kThreads * 96, "registers of the launch");
-constexpr float kJump = 8.f;     // log2 of the largest weight before the reference moves
-constexpr float kLn2 = 0.69314718055994531f;
-
-struct SplitPlan {
-  int R;        // rows per tile
-  int tiles;    // bound of the number of tiles
-  int splits;   // ranges of cache rows per tile
-  int chunk;    // cache rows per range (multiple of kKeys)
-};
-
-SplitPlan plan_splits(int64_t T, int32_t B, int32_t H, int64_t max_rows) {
-  SplitPlan p;
-  const int64_t rows = (T + B - 1) / B * H;  // of an average request
-  p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  p.tiles = static_cast<int>(T * H / p.R + B);
-  const int64_t busy = (T * H + p.R - 1) / p.R;
-  const int64_t most = (max_rows + kKeys - 1) / kKeys;
-  int64_t s = 152 / (busy < 1 ? 1 : busy);
-  s = s < 1 ? 1 : s > most ? most : s;
-  p.chunk = static_cast<int>(((max_rows + s - 1) / s + kKeys - 1) / kKeys * kKeys);
-  p.splits = static_cast<int>((max_rows + p.chunk - 1) / p.chunk);
-  return p;
-}
-
-// Which request and rows a tile has.  Request b's tiles start at
-// floor(row_start[b] * H / R) + b: increasing, and never fewer than it needs.
-struct Tile {
-  int32_t tok0, ntok;  // the request's ragged rows
-  int32_t b;
-  int32_t base, rows;  // first (token, head) row of the tile in the request, and how many (<= 0: none)
-};
-
-__device__ __forceinline__ int32_t start_of(const Fp4AttentionArgs& a, int32_t b) {
-  return min(max(a.row_start[b], 0), static_cast<int32_t>(a.T));
-}
-
-// By one converged warp.
-__device__ __forceinline__ Tile find_tile(const Fp4AttentionArgs& a, int32_t tile, int R) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = a.B;  // the request is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int i = lo + lane * step;
-    const bool le = lane * step < n && start_of(a, i) * static_cast<int64_t>(a.H) / R + i <= tile;
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, le);
-    const int last = m ? 31 - __clz(m) : 0;
-    lo += last * step;
-    n = min(step, n - last * step);
-  }
-  Tile t;
-  t.b = lo;
-  t.tok0 = start_of(a, lo);
-  t.ntok = start_of(a, lo + 1) - t.tok0;
-  t.base = (tile - static_cast<int32_t>(t.tok0 * static_cast<int64_t>(a.H) / R + lo)) * R;
-  t.rows = t.base < 0 ? 0 : min(R, t.ntok * a.H - t.base);  // base < 0: row_start does not begin with 0
-  return t;
-}
-
 template <int D, int R>
 struct Layout {
   static constexpr int kUnits = D / 128;
@@ -145,7 +77,7 @@ struct Small {
   float sink[R];   // log2 units, -infinity without
   alignas(16) float keep[R];  // what a move of the references leaves of sums and outputs
   float part[4][R];
-  uint8_t bad[4][kKeys];  // keys of a tile that are not there (ring over tiles)
+  uint32_t bad[4][4];  // a bit per key of a tile whose page is not there (ring over tiles)
 };
 
 template <int D, int R>
@@ -180,17 +112,6 @@ __device__ __forceinline__ float reduce_columns(float (&v)[n], int lane) {
   return v[0];
 }
 
-// Columns of a per-row array, 16 bytes at a time.  They are read in one go before
-// anything is stored: the compiler may not move a load over a store that could alias.
-template <int n>
-__device__ __forceinline__ void load_cols(const float* p, float (&v)[n]) {
-#pragma unroll
-  for (int i = 0; i < n; i += 4) {
-    const float4 f = *reinterpret_cast<const float4*>(p + i);
-    v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
-  }
-}
-
 __device__ __forceinline__ void soft_barrier() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool p) {
   uint32_t r;
@@ -203,51 +124,6 @@ __device__ __forceinline__ bool soft_any(bool p) {
   return r != 0;
 }
 static_assert(kSoftWarps * 32 == 256, "the softmax warps' named barrier");
-
-// Decoding on the integer and fp16 pipes (a hardware conversion of two codes
-// runs at an eighth of their rate).  A code's exponent and mantissa bits at bits
-// 11..9 of an fp16 are its value * 2^-14 (a subnormal code lands on a subnormal),
-// an e4m3's bits shifted up by 7 its value * 2^-8; the scale is brought to
-// scale * 2^7 (at most 57344), so that the product is value * 2^-7: at least
-// 2^-17 with 6 significant bits, exact in fp16.  Every byte decodes to a finite
-// number.  The left shifts are multiplications by kernel parameters, which the
-// multiplier pipe does beside the logic pipe.  Codes come out in pairs (i, i + 4) of the word's eight.
-constexpr float kUnscale = 128.f;
-
-struct Shifts {
-  uint32_t by[6];  // 2^9, 2^12, 2^5, 2^8, 2^1, 2^4
-};
-
-__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s, const Shifts& k) {
-  const uint32_t m[4] = {((w * k.by[0]) & 0x0E000E00u) | ((w * k.by[1]) & 0x80008000u),
-                         ((w * k.by[2]) & 0x0E000E00u) | ((w * k.by[3]) & 0x80008000u),
-                         ((w * k.by[4]) & 0x0E000E00u) | ((w * k.by[5]) & 0x80008000u), ((w >> 3) & 0x0E000E00u) | (w & 0x80008000u)};
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&m[i]), s);
-    r[i] = *reinterpret_cast<const uint32_t*>(&p);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
-// Four e4m3 bytes, each twice in a register, times 2^7.
-__device__ __forceinline__ void decode_scales(uint32_t b, __half2 (&s)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t x = b >> (8 * i);  // bytes i and i + 2 in the low byte of each half
-    const uint32_t m = ((x & 0x007F007Fu) << 7) | ((x & 0x00800080u) << 8);
-    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&m), __float2half2_rn(32768.f));
-    s[i] = __low2half2(v);
-    s[i + 2] = __high2half2(v);
-  }
-}
-
-// Where channel c of a row is kept in the decoded tile (and so in Q and O): the
-// eight channels of a word in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ constexpr int channel_of(int place) {
-  return (place & ~7) | ((place & 1) << 2) | ((place >> 1) & 3);
-}
 
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk,
@@ -354,38 +230,33 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
 #pragma unroll
         for (int x = 0; x < kC / 8; ++x) raw[i][x] = on ? q[x] : make_uint4(0, 0, 0, 0);
       }
+uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int r = warp * (R / kSoftWarps) + (i0 + i) * (32 / kSpan) + sub;
-        uint32_t am = 0;  // the largest magnitude: bf16 bits order like the values
+        am[i] = 0;
 #pragma unroll
         for (int x = 0; x < kC / 8; ++x) {
           const uint32_t w[4] = {raw[i][x].x, raw[i][x].y, raw[i][x].z, raw[i][x].w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) am = __vmaxu2(am, w[y] & 0x7FFF7FFFu);
+          for (int y = 0; y < 4; ++y) am[i] = max(am[i], max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
         }
-        am = max(am >> 16, am & 0xFFFFu);
+      }
 #pragma unroll
-        for (int o = 1; o < kSpan; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-        // power of two that brings the largest channel to [2^14, 2^15); 1 for a row of zeros or with an infinity or NaN
-        const int e = static_cast<int>(am >> 7);
-        const int se = am == 0u || e == 255 ? 127 : min(127 + 14 + 127 - e, 253);
+      for (int o = 1; o < kSpan; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) am[i] = max(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = warp * (R / kSoftWarps) + (i0 + i) * (32 / kSpan) + sub;
+        const int se = query_exponent(am[i]);
         const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
         if (lane % kSpan == 0)
           sm.c[r] = a.softmax_scale * kLog2e * kUnscale * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
         uint8_t* row = smem + L::kQ + (ch / 64) * (R * 128) + r * 128;
 #pragma unroll
-        for (int x = 0; x < kC / 8; ++x) {
-          const uint32_t w[4] = {raw[i][x].x, raw[i][x].y, raw[i][x].z, raw[i][x].w};
-          uint32_t v[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {  // channels y and y + 4 of the eight
-            const float lo = y & 1 ? bf16_hi(w[y / 2]) : bf16_lo(w[y / 2]), hi = y & 1 ? bf16_hi(w[2 + y / 2]) : bf16_lo(w[2 + y / 2]);
-            const __half2 p = __floats2half2_rn(lo * up, hi * up);
-            v[y] = *reinterpret_cast<const uint32_t*>(&p);
-          }
-          *reinterpret_cast<uint4*>(row + ((((ch % 64) / 8 + x) ^ (r & 7)) * 16)) = make_uint4(v[0], v[1], v[2], v[3]);
-        }
+        for (int x = 0; x < kC / 8; ++x)
+          *reinterpret_cast<uint4*>(row + ((((ch % 64) / 8 + x) ^ (r & 7)) * 16)) = query8(raw[i][x], up);
       }
       }
     }
@@ -409,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       if (!ok) atomicExch(&sm.abort, 1);
       __syncwarp();
       tc_fence_after();
-      const bool gone = sm.bad[j & 3][quad * 32 + lane] != 0;
+      const bool gone = (sm.bad[j & 3][quad] >> lane) & 1;
       const bool masks = gone || key - lane + 32 > ctx_min;
       const uint32_t at_s = tmem + lanes + L::kTmemS + buf * R + col0;
       // scores in log2 units, -infinity for keys that a row does not see
@@ -509,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     }
     // --------------------------------------------------------------- output
     if (n > 0 && ok) {
-      ok = mbar_wait(&sm.o_done, (n - 1) & 1);
+      // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's
+      ok = mbar_wait(&sm.drain, 0);
       __syncwarp();
       tc_fence_after();
     }
@@ -631,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
         if (!L::kAhead && j + 1 < n) scores(j + 1);
       }
       if (!ok) atomicExch(&sm.abort, 1);
-      // tensor memory is given back only when no MMA writes it any more
+      // the end of every MMA: the output may be read, and tensor memory given back
       tc_commit(&sm.drain);
       if (!mbar_wait(&sm.drain, 0) || !ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
     }
@@ -641,95 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (n > 0) {
     // ------------------------------------------------------- load and decode
-    // a thread has 64 channels of a unit's 128 for one key, that of its lane of tensor memory;
-    // neighbouring lanes have neighbouring keys, whose 16-byte chunks the swizzle spreads over all banks
-    const int quad = warp & 3, key = quad * 32 + lane, part = (warp - kLoadWarp) >> 2;
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const int32_t* table = a.table + static_cast<int64_t>(tile.b) * a.table_stride;
-    const int64_t page_bytes = fp4_page_bytes<D>(a.page_size);
-    struct Unit {
-      uint4 c[2];  // 64 codes
-      uint32_t s;  // 4 scales
-    };
-    Unit reg[kRing];
-    const uint8_t *codes = nullptr, *scales = nullptr;
-    bool there = false, bad = false;
-    // where the key's row of tile j is
-    auto locate = [&](int j) {
-      const int k = k_first + j * kKeys + key;
-      there = false;
-      bad = false;
-      if (k < k_last) {
-        const int pg = page_shift >= 0 ? k >> page_shift : k / a.page_size;
-        const int row = k - pg * a.page_size;
-        const int32_t page = table[pg];
-        if (page >= 0 && page < a.num_pages) {
-          const uint8_t* p = a.cache + page * page_bytes;
-          codes = p + static_cast<int64_t>(row) * (D / 2) + part * 32;
-          scales = p + static_cast<int64_t>(a.page_size) * (D / 2) + static_cast<int64_t>(row) * (D / 16) + part * 4;
-          there = true;
-        } else {
-          bad = true;
-          if (part == 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
-        }
-      }
-    };
-    auto load = [&](Unit& x, int u) {
-      x.s = there ? *reinterpret_cast<const uint32_t*>(scales + u * 8) : 0u;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x.c[i] = make_uint4(0, 0, 0, 0);
-        if (there) x.c[i] = *reinterpret_cast<const uint4*>(codes + u * 64 + i * 16);
-      }
-    };
-    const int total = n * L::kUnits;
-    bool was_bad[kRing];
-#pragma unroll
-    for (int c = 0; c < kRing; ++c) {
-      if (c % L::kUnits == 0 && c < total) locate(c / L::kUnits);
-      if (c < total) load(reg[c], c % L::kUnits);
-      was_bad[c] = bad;
-    }
-    bool ok = true;
-#pragma unroll 1
-    for (int c0 = 0; c0 < total && ok; c0 += kRing) {
-#pragma unroll
-      for (int i = 0; i < kRing; ++i) {
-        const int c = c0 + i;
-        if (c < total && ok) {
-          if (c >= L::kSlots) ok = mbar_wait(&sm.a_free[c % L::kSlots], ((c / L::kSlots) - 1) & 1);
-          if (c >= kRing) ok = ok && mbar_wait(&sm.empty[i], ((c / kRing) - 1) & 1);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (ok) {
-            tc_fence_after();
-            uint8_t* unit = smem + i * kUnitBytes + part * 16384 + key * 128;
-            const uint32_t a_tile = tmem + lanes + L::kTmemK + (c % L::kSlots) * 64 + part * 32;
-            __half2 sc[4];
-            decode_scales(reg[i].s, sc);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {  // blocks of 16 channels
-              const uint4 x = reg[i].c[b / 2];
-              const uint4 lo = decode8(b & 1 ? x.z : x.x, sc[b], shifts), hi = decode8(b & 1 ? x.w : x.y, sc[b], shifts);
-              *reinterpret_cast<uint4*>(unit + (((2 * b) ^ (key & 7)) * 16)) = lo;
-              *reinterpret_cast<uint4*>(unit + (((2 * b + 1) ^ (key & 7)) * 16)) = hi;
-              tmem_st8(a_tile + b * 8, lo, hi);
-            }
-            if (c % L::kUnits == 0 && part == 0) sm.bad[(c / L::kUnits) & 3][key] = was_bad[i] ? 1 : 0;
-            tc_wait_st();
-            tc_fence_before();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.full[i]);
-            const int next = c + kRing;
-            if (next < total) {
-              if (next % L::kUnits == 0) locate(next / L::kUnits);
-              load(reg[i], next % L::kUnits);
-              was_bad[i] = bad;
-            }
-          }
-        }
-      }
-    }
+    const bool ok = load_units<D, true, L::kSlots>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, shifts, smem,
+                                                   tmem + L::kTmemK, sm.full, sm.empty, sm.a_free, sm.bad);
     if (!ok) {
       atomicExch(&sm.abort, 1);
       if (lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
@@ -744,87 +529,60 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
   }
 }
 
-// Joins the ranges of a tile: one warp per row, in the order of the ranges.
 template <int D, int R>
-__global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int splits) {
-  const int lane = threadIdx.x & 31;
-  pdl_wait();
-  const Tile t = find_tile(a, blockIdx.x, R);
-  if (t.rows <= 0) return;
-  int ctx_max = 0;
-  for (int i = lane; i < R; i += 32)
-    if (i < t.rows) ctx_max = max(ctx_max, min(a.ctx_rows[t.tok0 + (t.base + i) / a.H], a.max_rows));
-  ctx_max = __reduce_max_sync(0xFFFFFFFFu, ctx_max);
-  const int used = (ctx_max + chunk - 1) / chunk;
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (used <= 1 || r >= t.rows) return;
-  if (a.ctx_rows[t.tok0 + (t.base + r) / a.H] < 0) return;
-  const float* ws = static_cast<const float*>(a.workspace);
-  const int64_t slot0 = static_cast<int64_t>(blockIdx.x) * splits;
-  const float* ml = ws + static_cast<int64_t>(gridDim.x) * splits * R * D + slot0 * R * 2;
-  const int64_t flat = static_cast<int64_t>(t.tok0) * a.H + t.base + r;
-  float m = kNegBig;
-  for (int s = lane; s < used; s += 32) m = fmaxf(m, ml[s * 2 * R + r]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  float all = 0.f;
-  if (a.sink) {
-    const float s = a.sink[flat % a.H] * kLog2e;
-    m = fmaxf(m, s);
-    all = s == m ? 1.f : fast_exp2(s - m);
-  }
-  float acc[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-  for (int s = 0; s < used; ++s) {
-    const float l = ml[s * 2 * R + R + r];
-    const float w = fast_exp2(ml[s * 2 * R + r] - m);
-    all += l == 0.f ? 0.f : l * w;
-    const float4* o = reinterpret_cast<const float4*>(ws + ((slot0 + s) * R + r) * D);
-#pragma unroll
-    for (int i = 0; i < D / 128; ++i) {
-      const float4 v = o[i * 32 + lane];
-      acc[4 * i] = fmaf(v.x, w, acc[4 * i]);
-      acc[4 * i + 1] = fmaf(v.y, w, acc[4 * i + 1]);
-      acc[4 * i + 2] = fmaf(v.z, w, acc[4 * i + 2]);
-      acc[4 * i + 3] = fmaf(v.w, w, acc[4 * i + 3]);
-    }
-  }
-  const float inv = all == 0.f ? 0.f : kUnscale * a.g / all;
-#pragma unroll
-  for (int i = 0; i < D / 128; ++i)
-    *reinterpret_cast<uint2*>(a.out + flat * D + i * 128 + lane * 4) =
-        make_uint2(pack_bf16x2_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack_bf16x2_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
-  if (lane == 0 && a.lse) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
-}
-
-template <int D, int R>
-cudaError_t launch(const Fp4AttentionArgs& a, const SplitPlan& p, bool use_pdl, cudaStream_t s) {
+cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cudaStream_t s) {
   cudaError_t e = set_max_smem_once<fp4_attention_kernel<D, R>>(smem_bytes<D, R>());
   if (e != cudaSuccess) return e;
-  int shift = -1;
-  if ((a.page_size & (a.page_size - 1)) == 0)
-    for (shift = 0; (1 << shift) != a.page_size;) ++shift;
   e = launch_ex(fp4_attention_kernel<D, R>, dim3(p.tiles, p.splits), dim3(kThreads), smem_bytes<D, R>(), use_pdl, s, a, p.chunk,
-                shift, Shifts{{1u << 9, 1u << 12, 1u << 5, 1u << 8, 1u << 1, 1u << 4}});
+                page_shift_of(a.page_size), kShifts);
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_ex(fp4_join_kernel<D, R>, dim3(p.tiles, R / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
 }
 
 template <int D>
-cudaError_t launch_d(const Fp4AttentionArgs& a, const SplitPlan& p, bool use_pdl, cudaStream_t s) {
+cudaError_t launch_d(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cudaStream_t s) {
   return p.R == 16 ? launch<D, 16>(a, p, use_pdl, s) : p.R == 32 ? launch<D, 32>(a, p, use_pdl, s) : launch<D, 64>(a, p, use_pdl, s);
+}
+
+// Rows per tile, and into how many ranges of cache rows a tile is split: the count that a model of
+// the time finds best.  A CTA costs a few microseconds around its tiles, a tile of 128 rows what D
+// asks for; CTAs run in waves over the 152 SMs; split tiles write and read fp32 partials and need
+// a second launch.  Lengths are known on the host by their bound only, so ranges are of equal size.
+Fp4Plan plan_fp4(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
+  Fp4Plan p;
+  const int64_t rows = (T + B - 1) / B * H;  // of an average request
+  p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : D == 512 ? 64 : 128;
+  p.tiles = static_cast<int>(T * H / p.R + B);
+  int64_t busy = (T * H + p.R - 1) / p.R;
+  busy = busy < T && busy < B ? (T < B ? T : B) : busy;
+  const int64_t most = (max_rows + kKeys - 1) / kKeys;
+  const double around = 5.0, tile = D == 512 ? 3.5 : D == 256 ? 1.6 : 0.9, join = 4.0;
+  double best = 0;
+  int64_t best_s = 1;
+  for (int64_t s = 1; s <= most && s <= 64; ++s) {
+    const int64_t waves = (busy * s + 151) / 152;
+    double us = waves * (around + tile * static_cast<double>((most + s - 1) / s));
+    if (s > 1) us += join + 2.0 * static_cast<double>(busy * s) * p.R * D * 4 / 4e6;
+    if (s == 1 || us < best) {
+      best = us;
+      best_s = s;
+    }
+  }
+  p.chunk = static_cast<int>((most + best_s - 1) / best_s * kKeys);
+  p.splits = static_cast<int>((max_rows + p.chunk - 1) / p.chunk);
+  return p;
 }
 
 }  // namespace
 
 int64_t fp4_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
-  const SplitPlan p = plan_splits(T, B, H, max_rows);
+  const Fp4Plan p = plan_fp4(T, B, H, D, max_rows);
   return p.splits == 1 ? 0 : static_cast<int64_t>(p.tiles) * p.splits * p.R * (D + 2) * static_cast<int64_t>(sizeof(float));
 }
 
 cudaError_t launch_fp4_attention(const Fp4AttentionArgs& a, int D, bool use_pdl, cudaStream_t s) {
-  const SplitPlan p = plan_splits(a.T, a.B, a.H, a.max_rows);
+  const Fp4Plan p = plan_fp4(a.T, a.B, a.H, D, a.max_rows);
+  if (p.R == 128) return launch_fp4_attention_rows(a, p, D, use_pdl, s);
   return D == 128 ? launch_d<128>(a, p, use_pdl, s) : D == 256 ? launch_d<256>(a, p, use_pdl, s) : launch_d<512>(a, p, use_pdl, s);
 }
 

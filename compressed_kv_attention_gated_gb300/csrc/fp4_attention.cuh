@@ -1,0 +1,330 @@
+// fp4_attention.cuh -- what the two forms of the 4-bit attention share: tiles of
+// (token, head) rows, the decoding of cache rows into shared (and tensor) memory,
+// and the joining of split ranges.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+#include "ckv_device.cuh"
+#include "ckv_fp4.cuh"
+#include "ckv_launch.h"
+#include "ckv_launch_util.cuh"
+#include "ckv_tcgen05.cuh"
+
+namespace ckv {
+
+constexpr int kKeys = 128;       // cache rows per tile
+constexpr int kRing = 4;         // units of 128 keys x 128 channels
+constexpr int kUnitBytes = 32768;
+constexpr float kJump = 8.f;     // log2 of the largest weight before a row's reference moves
+constexpr float kLn2 = 0.69314718055994531f;
+
+// How a call is cut up (fp4_attention.cu).
+struct Fp4Plan {
+  int R;        // (token, head) rows per tile: 16, 32, 64 (keys on the M side) or 128 (rows on the M side)
+  int tiles;    // bound of the number of tiles
+  int splits;   // ranges of cache rows per tile
+  int chunk;    // cache rows per range (multiple of kKeys)
+};
+cudaError_t launch_fp4_attention_rows(const Fp4AttentionArgs& a, const Fp4Plan& p, int D, bool use_pdl, cudaStream_t s);
+
+namespace {
+
+// Which request and rows a tile has.  Request b's tiles start at
+// floor(row_start[b] * H / R) + b: increasing, and never fewer than it needs.
+struct Tile {
+  int32_t tok0, ntok;  // the request's ragged rows
+  int32_t b;
+  int32_t base, rows;  // first (token, head) row of the tile in the request, and how many (<= 0: none)
+};
+
+__device__ __forceinline__ int32_t start_of(const Fp4AttentionArgs& a, int32_t b) {
+  return min(max(a.row_start[b], 0), static_cast<int32_t>(a.T));
+}
+
+// By one converged warp.
+__device__ __forceinline__ Tile find_tile(const Fp4AttentionArgs& a, int32_t tile, int R) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = a.B;  // the request is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lo + lane * step;
+    const bool le = lane * step < n && start_of(a, i) * static_cast<int64_t>(a.H) / R + i <= tile;
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, le);
+    const int last = m ? 31 - __clz(m) : 0;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  Tile t;
+  t.b = lo;
+  t.tok0 = start_of(a, lo);
+  t.ntok = start_of(a, lo + 1) - t.tok0;
+  t.base = (tile - static_cast<int32_t>(t.tok0 * static_cast<int64_t>(a.H) / R + lo)) * R;
+  t.rows = t.base < 0 ? 0 : min(R, t.ntok * a.H - t.base);  // base < 0: row_start does not begin with 0
+  return t;
+}
+
+// Decoding on the integer and fp16 pipes (a hardware conversion of two codes
+// runs at an eighth of their rate).  A code's exponent and mantissa bits at bits
+// 11..9 of an fp16 are its value * 2^-14 (a subnormal code lands on a subnormal),
+// an e4m3's bits shifted up by 7 its value * 2^-8; the scale is brought to
+// scale * 2^7 (at most 57344), so that the product is value * 2^-7: at least
+// 2^-17 with 6 significant bits, exact in fp16.  Every byte decodes to a finite
+// number.  The left shifts are multiplications by kernel parameters, which the
+// multiplier pipe does beside the logic pipe.  Codes come out in pairs (i, i + 4) of the word's eight.
+constexpr float kUnscale = 128.f;
+
+struct Shifts {
+  uint32_t by[6];  // 2^9, 2^12, 2^5, 2^8, 2^1, 2^4
+};
+
+constexpr Shifts kShifts{{1u << 9, 1u << 12, 1u << 5, 1u << 8, 1u << 1, 1u << 4}};
+
+// log2 of a page size that is a power of two, else -1
+inline int page_shift_of(int32_t page_size) {
+  if (page_size & (page_size - 1)) return -1;
+  int s = 0;
+  while ((1 << s) != page_size) ++s;
+  return s;
+}
+
+__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s, const Shifts& k) {
+  const uint32_t m[4] = {((w * k.by[0]) & 0x0E000E00u) | ((w * k.by[1]) & 0x80008000u),
+                         ((w * k.by[2]) & 0x0E000E00u) | ((w * k.by[3]) & 0x80008000u),
+                         ((w * k.by[4]) & 0x0E000E00u) | ((w * k.by[5]) & 0x80008000u), ((w >> 3) & 0x0E000E00u) | (w & 0x80008000u)};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&m[i]), s);
+    r[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Four e4m3 bytes, each twice in a register, times 2^7.
+__device__ __forceinline__ void decode_scales(uint32_t b, __half2 (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = b >> (8 * i);  // bytes i and i + 2 in the low byte of each half
+    const uint32_t m = ((x & 0x007F007Fu) << 7) | ((x & 0x00800080u) << 8);
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&m), __float2half2_rn(32768.f));
+    s[i] = __low2half2(v);
+    s[i + 2] = __high2half2(v);
+  }
+}
+
+// Queries.  A row is scaled by a power of two that brings its largest magnitude (its
+// bf16 bits) to [2^14, 2^15); by 1 when it is zero, infinite or NaN.  Returns the
+// power's biased exponent.
+__device__ __forceinline__ int query_exponent(uint32_t am) {
+  const int e = static_cast<int>(am >> 7);
+  return am == 0u || e == 255 ? 127 : min(127 + 14 + 127 - e, 253);
+}
+
+// Eight bf16 channels times `up`, as fp16 in the order in which codes are decoded.
+__device__ __forceinline__ uint4 query8(uint4 raw, float up) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t v[4];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {  // channels y and y + 4
+    const float lo = y & 1 ? bf16_hi(w[y / 2]) : bf16_lo(w[y / 2]), hi = y & 1 ? bf16_hi(w[2 + y / 2]) : bf16_lo(w[2 + y / 2]);
+    const __half2 p = __floats2half2_rn(lo * up, hi * up);
+    v[y] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Where channel c of a row is kept in the decoded tile (and so in Q and O): the
+// eight channels of a word in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ constexpr int channel_of(int place) {
+  return (place & ~7) | ((place & 1) << 2) | ((place >> 1) & 3);
+}
+
+// Columns of a per-row array, 16 bytes at a time.  They are read in one go before
+// anything is stored: the compiler may not move a load over a store that could alias.
+template <int n>
+__device__ __forceinline__ void load_cols(const float* p, float (&v)[n]) {
+#pragma unroll
+  for (int i = 0; i < n; i += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(p + i);
+    v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+  }
+}
+
+// The work of 8 warps (tid 0..255): cache rows k_first .. k_last - 1 of the tile's
+// request, 128 at a time and 128 channels at a time, through the ring of units.
+// A unit is two blocks of 128 keys x 64 channels of fp16, 128 bytes per key, with
+// the 128-byte swizzle; with kCopy it also goes to tensor memory (a lane per
+// key, 64 columns, slot c % kSlots from column tmem_k on).
+//   full[c % kRing]    one arrival per warp when unit c is there
+//   empty[c % kRing]   completed when both products are done with it
+//   a_free[c % kSlots] completed when the first product is done with it (only waited for where
+//                      kSlots < kRing, and there a tile is kRing units: the other waits imply it)
+//   bad[tile & 3]      a bit per key whose page is not there
+// Rows that are not there are zeros.  False when a wait ran out.
+template <int D, bool kCopy, int kSlots>
+__device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile& tile, int tid, int k_first, int k_last, int page_shift,
+                                           const Shifts& shifts, uint8_t* ring, uint32_t tmem_k, uint64_t* full, uint64_t* empty,
+                                           uint64_t* a_free, uint32_t (*bad)[4]) {
+  constexpr int kUnits = D / 128;
+  static_assert(kSlots == kRing || kUnits == kRing, "waits");
+  // a thread has 64 channels of a unit's 128 for one key, that of its lane of tensor memory;
+  // neighbouring lanes have neighbouring keys, whose 16-byte chunks the swizzle spreads over all banks
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, key = quad * 32 + lane, part = tid >> 7;
+  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const int32_t* table = a.table + static_cast<int64_t>(tile.b) * a.table_stride;
+  const int64_t page_bytes = fp4_page_bytes<D>(a.page_size);
+  struct Unit {
+    uint4 c[2];  // 64 codes
+    uint32_t s;  // 4 scales
+  };
+  Unit reg[kRing];
+  const uint8_t *codes = nullptr, *scales = nullptr;
+  bool there = false;
+  uint32_t gone = 0;  // the warp's keys without a page
+  // where the key's row of tile j is
+  auto locate = [&](int j) {
+    const int k = k_first + j * kKeys + key;
+    there = false;
+    bool missing = false;
+    if (k < k_last) {
+      const int pg = page_shift >= 0 ? k >> page_shift : k / a.page_size;
+      const int row = k - pg * a.page_size;
+      const int32_t page = table[pg];
+      if (page >= 0 && page < a.num_pages) {
+        const uint8_t* p = a.cache + page * page_bytes;
+        codes = p + static_cast<int64_t>(row) * (D / 2) + part * 32;
+        scales = p + static_cast<int64_t>(a.page_size) * (D / 2) + static_cast<int64_t>(row) * (D / 16) + part * 4;
+        there = true;
+      } else {
+        missing = true;
+        if (part == 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
+      }
+    }
+    gone = __ballot_sync(0xFFFFFFFFu, missing);
+  };
+  auto load = [&](Unit& x, int u) {
+    x.s = there ? *reinterpret_cast<const uint32_t*>(scales + u * 8) : 0u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x.c[i] = make_uint4(0, 0, 0, 0);
+      if (there) x.c[i] = *reinterpret_cast<const uint4*>(codes + u * 64 + i * 16);
+    }
+  };
+  const int total = k_last > k_first ? (k_last - k_first + kKeys - 1) / kKeys * kUnits : 0;
+  uint32_t was_gone[kRing / kUnits > 0 ? kRing / kUnits : 1];
+#pragma unroll
+  for (int c = 0; c < kRing; ++c) {
+    if (c < total) {
+      if (c % kUnits == 0) {
+        locate(c / kUnits);
+        was_gone[c / kUnits] = gone;
+      }
+      load(reg[c], c % kUnits);
+    }
+  }
+  bool ok = true;
+#pragma unroll 1
+  for (int c0 = 0; c0 < total && ok; c0 += kRing) {
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) {
+      const int c = c0 + i;
+      if (c < total && ok) {
+        // the ring's last unit in this place has served both products
+        if (c >= kRing) ok = mbar_wait(&empty[i], ((c / kRing) - 1) & 1);
+        if (kCopy && kSlots < kRing && i >= kSlots) ok = ok && mbar_wait(&a_free[c % kSlots], ((c / kSlots) - 1) & 1);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok) {
+          if (kCopy) tc_fence_after();
+          uint8_t* unit = ring + i * kUnitBytes + part * 16384 + key * 128;
+          const uint32_t a_tile = tmem_k + lanes + (c % kSlots) * 64 + part * 32;
+          __half2 sc[4];
+          decode_scales(reg[i].s, sc);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {  // blocks of 16 channels
+            const uint4 x = reg[i].c[b / 2];
+            const uint4 lo = decode8(b & 1 ? x.z : x.x, sc[b], shifts), hi = decode8(b & 1 ? x.w : x.y, sc[b], shifts);
+            *reinterpret_cast<uint4*>(unit + (((2 * b) ^ (key & 7)) * 16)) = lo;
+            *reinterpret_cast<uint4*>(unit + (((2 * b + 1) ^ (key & 7)) * 16)) = hi;
+            if (kCopy) tmem_st8(a_tile + b * 8, lo, hi);
+          }
+          if (i % kUnits == 0 && part == 0 && lane == 0) bad[(c / kUnits) & 3][quad] = was_gone[i / kUnits];
+          if (kCopy) {
+            tc_wait_st();
+            tc_fence_before();
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[i]);
+          const int next = c + kRing;
+          if (next < total) {
+            if (i % kUnits == 0) {
+              locate(next / kUnits);
+              was_gone[i / kUnits] = gone;
+            }
+            load(reg[i], i % kUnits);
+          }
+        }
+      }
+    }
+  }
+  return ok;
+}
+
+// Joins the ranges of a tile: one warp per row, in the order of the ranges.
+template <int D, int R>
+__global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int splits) {
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  const Tile t = find_tile(a, blockIdx.x, R);
+  if (t.rows <= 0) return;
+  int ctx_max = 0;
+  for (int i = lane; i < R; i += 32)
+    if (i < t.rows) ctx_max = max(ctx_max, min(a.ctx_rows[t.tok0 + (t.base + i) / a.H], a.max_rows));
+  ctx_max = __reduce_max_sync(0xFFFFFFFFu, ctx_max);
+  const int used = (ctx_max + chunk - 1) / chunk;
+  const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  if (used <= 1 || r >= t.rows) return;
+  if (a.ctx_rows[t.tok0 + (t.base + r) / a.H] < 0) return;
+  const float* ws = static_cast<const float*>(a.workspace);
+  const int64_t slot0 = static_cast<int64_t>(blockIdx.x) * splits;
+  const float* ml = ws + static_cast<int64_t>(gridDim.x) * splits * R * D + slot0 * R * 2;
+  const int64_t flat = static_cast<int64_t>(t.tok0) * a.H + t.base + r;
+  float m = kNegBig;
+  for (int s = lane; s < used; s += 32) m = fmaxf(m, ml[s * 2 * R + r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  float all = 0.f;
+  if (a.sink) {
+    const float s = a.sink[flat % a.H] * kLog2e;
+    m = fmaxf(m, s);
+    all = s == m ? 1.f : fast_exp2(s - m);
+  }
+  float acc[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+  for (int s = 0; s < used; ++s) {
+    const float l = ml[s * 2 * R + R + r];
+    const float w = fast_exp2(ml[s * 2 * R + r] - m);
+    all += l == 0.f ? 0.f : l * w;
+    const float4* o = reinterpret_cast<const float4*>(ws + ((slot0 + s) * R + r) * D);
+#pragma unroll
+    for (int i = 0; i < D / 128; ++i) {
+      const float4 v = o[i * 32 + lane];
+      acc[4 * i] = fmaf(v.x, w, acc[4 * i]);
+      acc[4 * i + 1] = fmaf(v.y, w, acc[4 * i + 1]);
+      acc[4 * i + 2] = fmaf(v.z, w, acc[4 * i + 2]);
+      acc[4 * i + 3] = fmaf(v.w, w, acc[4 * i + 3]);
+    }
+  }
+  const float inv = all == 0.f ? 0.f : kUnscale * a.g / all;
+#pragma unroll
+  for (int i = 0; i < D / 128; ++i)
+    *reinterpret_cast<uint2*>(a.out + flat * D + i * 128 + lane * 4) =
+        make_uint2(pack_bf16x2_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack_bf16x2_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
+  if (lane == 0 && a.lse) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+}
+
+}  // namespace
+}  // namespace ckv

@@ -1,0 +1,433 @@
+// fp4_attention_rows.cu -- attention over the 4-bit paged cache with the (token,
+// head) rows on the M side of both products, for requests with more than 32 rows
+// at D = 128 and 256 (fp4_attention.cu holds the other form and the formulas):
+//   S [128 rows x 128 keys]   = Q [128 x D] K^T
+//   O [128 rows x D]         += P [128 x 128 keys] K
+// A thread owns a row of S: its maximum and sum need no other thread, and its
+// weights go back to tensor memory as A of the second product.  Per 128 keys the
+// softmax warps evaluate 128 x 128 exponentials, which bounds the loop (16 per
+// clock and SM: 1024 clocks); the products take 256 to 512 (D = 128).
+//
+// As in the other form a row's weights are taken against a reference that moves
+// only when a score exceeds it by 2^8; here that is one warp's own affair.
+//
+// At D = 512 the accumulator would fill tensor memory, and with few rows most of
+// M would be idle while one warp does the whole softmax: those take the other form.
+#include "fp4_attention.cuh"
+
+namespace ckv {
+namespace {
+
+// Warpgroup 0: softmax; 1: its first warp issues the MMAs; 2 and 3: load and decode.
+constexpr int kRowMmaWarp = 4, kRowLoadWarp = 8;
+constexpr int kRowThreads = 512;
+// Registers per thread: 128 at launch (65,536), then 128 x 224 + 128 x 56 + 256 x 104 = 62,464.
+constexpr int kRowSoftRegs = 224, kRowMmaRegs = 56, kRowLoadRegs = 104;
+static_assert(128 * kRowSoftRegs + 128 * kRowMmaRegs + 256 * kRowLoadRegs <= kRowThreads * 128, "registers of the launch");
+
+template <int D>
+struct RowLayout {
+  static constexpr int kUnits = D / 128;
+  static constexpr int kSBufs = D == 128 ? 2 : 1;
+  static constexpr int kQ = kRing * kUnitBytes;   // Q: D/64 blocks of 128 rows x 128 bytes
+  static constexpr int kSmall = kQ + (D / 64) * 128 * 128;
+  static constexpr int kTmemO = 0, kTmemS = D, kTmemP = D + kSBufs * 128;  // P: two buffers of 64 columns
+  static_assert(kTmemP + 2 * 64 <= 512, "tensor memory");
+  static constexpr int kOutPitch = D * 2 + 16;    // output rows on their way out
+  static_assert(128 * kOutPitch <= kRing * kUnitBytes, "output staging");
+};
+
+struct RowSmall {
+  uint64_t full[kRing], empty[kRing], s_full[2], s_read, p_full[2], q_full, o_done, drain;
+  uint32_t tmem;
+  int32_t abort;
+  Tile tile;
+  int32_t ctx_max;
+  alignas(16) uint32_t bad[4][4];
+  float c[128];     // score factors
+  int64_t q[128];   // where the rows' queries begin, elements
+  int32_t out[128]; // flat (token, head) index, -1: none
+};
+
+template <int D>
+constexpr int row_smem_bytes() {
+  return RowLayout<D>::kSmall + static_cast<int>(sizeof(RowSmall)) + 1024;
+}
+
+__device__ __forceinline__ void row_barrier() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// 16 packed columns of the warp's lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRowThreads, 1)
+    fp4_attention_rows_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int page_shift, const __grid_constant__ Shifts shifts) {
+  using L = RowLayout<D>;
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  RowSmall& sm = *reinterpret_cast<RowSmall*>(smem + L::kSmall);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == kRowMmaWarp) {
+    tmem_alloc<512>(&sm.tmem);
+    if (lane == 0) {
+      for (int i = 0; i < kRing; ++i) {
+        mbar_init(&sm.full[i], 8);
+        mbar_init(&sm.empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sm.s_full[i], 1);
+        mbar_init(&sm.p_full[i], 4);
+      }
+      mbar_init(&sm.s_read, 4);
+      mbar_init(&sm.q_full, 4);
+      mbar_init(&sm.o_done, 1);
+      mbar_init(&sm.drain, 1);
+      sm.abort = 0;
+      fence_mbar_init();
+    }
+  }
+  pdl_wait();
+  if (warp == 0) {
+    const Tile t = find_tile(a, blockIdx.x, 128);
+    if (lane == 0) {
+      sm.tile = t;
+      sm.ctx_max = -1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Tile tile = sm.tile;
+  const uint32_t tmem = sm.tmem;
+  int32_t my_ctx = -1, my_flat = -1;  // of thread r < 128: its row
+  if (threadIdx.x < 128) {
+    const int r = threadIdx.x;
+    if (r < tile.rows) {
+      const int t = tile.tok0 + (tile.base + r) / a.H;
+      my_ctx = a.ctx_rows[t];
+      if (my_ctx > a.max_rows) {
+        flag_error(a.err, CKV_DEVERR_SEQ_LEN);
+        my_ctx = a.max_rows;
+      }
+      if (my_ctx >= 0) {
+        my_flat = tile.tok0 * a.H + tile.base + r;
+        sm.q[r] = t * a.q_st + (my_flat - t * a.H) * a.q_sh;
+      }
+    }
+    sm.out[r] = my_flat;
+    const int top = __reduce_max_sync(0xFFFFFFFFu, my_ctx);
+    if (lane == 0) atomicMax(&sm.ctx_max, top);
+  }
+  __syncthreads();
+  const int ctx_max = sm.ctx_max;
+  const int k_first = blockIdx.y * chunk;
+  const int k_last = min(ctx_max, k_first + chunk);
+  const bool split = ctx_max > chunk;  // several CTAs share the tile
+  const int n = k_last > k_first ? (k_last - k_first + kKeys - 1) / kKeys : 0;
+  // nothing to add: only the first range answers for rows that see nothing
+  const bool idle = n == 0 && (blockIdx.y > 0 || ctx_max < 0);
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowSoftRegs));
+    if (!idle) {
+      // ----------------------------------------------------------- queries
+      // eight channels per lane, D/8 lanes per row; every load of a batch is issued before the first is used
+      if (n > 0) {
+        constexpr int kSpan = D / 8 < 32 ? D / 8 : 32;  // lanes of a row
+        constexpr int kPer = 32 / kSpan;                // rows of a warp at a time
+        constexpr int kBatch = 16;
+        const int sub = lane / kSpan, ch = lane % kSpan * 8;
+        static_assert(D <= 256 && 32 % (kBatch * kPer) == 0, "");
+#pragma unroll 1
+        for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += kBatch * kPer) {
+          uint4 raw[kBatch];
+          uint32_t am[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * kPer + sub;
+            raw[i] = sm.out[r] >= 0 ? *reinterpret_cast<const uint4*>(a.q + sm.q[r] + ch) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            am[i] = 0;  // the largest magnitude: bf16 bits order like the values
+#pragma unroll
+            for (int y = 0; y < 4; ++y) am[i] = max(am[i], max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
+          }
+#pragma unroll
+          for (int o = 1; o < kSpan; o <<= 1) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) am[i] = max(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * kPer + sub;
+            const int se = query_exponent(am[i]);
+            const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
+            if (lane % kSpan == 0)
+              sm.c[r] = a.softmax_scale * kLog2e * kUnscale * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
+            *reinterpret_cast<uint4*>(smem + L::kQ + (ch / 64) * (128 * 128) + r * 128 + (((ch % 64) / 8) ^ (r & 7)) * 16) =
+                query8(raw[i], up);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+
+      // ----------------------------------------------------------- softmax
+      const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+      const float c = n > 0 ? sm.c[threadIdx.x] : 0.f;  // the warp's own rows
+      float ref = kNegBig, l = 0.f;
+      bool ok = true;
+#pragma unroll 1
+      for (int j = 0; j < n && ok; ++j) {
+        const int buf = L::kSBufs == 2 ? j & 1 : 0;
+        const int unit0 = j * L::kUnits;
+        // the decoding warps' note on missing keys, then the scores
+        ok = mbar_wait(&sm.full[unit0 % kRing], (unit0 / kRing) & 1) && mbar_wait(&sm.s_full[j & 1], (j >> 1) & 1);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        float z[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld<32>(tmem + lanes + L::kTmemS + buf * 128 + i * 32, z[i]);
+        if (L::kSBufs == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_read);
+        }
+        // log2 units over the row's reference; a row that has seen no key yet has none
+        const bool unset = ref == kNegBig;
+        const float shift = unset ? 0.f : ref;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) z[i / 32][i % 32] = fmaf(z[i / 32][i % 32], c, -shift);
+        const int left = my_ctx - (k_first + j * kKeys);  // keys of the tile that the row sees
+        const uint4 gone = *reinterpret_cast<const uint4*>(sm.bad[j & 3]);
+        if (__any_sync(0xFFFFFFFFu, left < kKeys)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) z[i / 32][i % 32] = i < left ? z[i / 32][i % 32] : -INFINITY;
+        }
+        if (gone.x | gone.y | gone.z | gone.w) {
+          const uint32_t g[4] = {gone.x, gone.y, gone.z, gone.w};
+#pragma unroll
+          for (int i = 0; i < 128; ++i) z[i / 32][i % 32] = (g[i / 32] >> (i % 32)) & 1 ? -INFINITY : z[i / 32][i % 32];
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; ++i) top[i % 4] = fmaxf(top[i % 4], z[i / 32][i % 32]);
+        const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (__any_sync(0xFFFFFFFFu, over > kJump || (unset && over > -INFINITY))) {
+          // the largest score so far becomes the reference
+          const float d = unset ? over : fmaxf(over, 0.f);
+          const bool move = d > -INFINITY;
+          const float by = move ? d : 0.f;
+          const float keep = unset ? 0.f : fast_exp2(-by);
+          l *= keep;
+          ref = move ? shift + by : ref;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) z[i / 32][i % 32] -= by;
+          if (j > 0) {
+            ok = mbar_wait(&sm.o_done, (j - 1) & 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const float k = unset ? 1.f : keep;  // an unset row's output is 0
+#pragma unroll 1
+            for (int i = 0; i < D; i += 16) {
+              float o[16];
+              tmem_ld<16>(tmem + lanes + L::kTmemO + i, o);
+              uint32_t v[16];
+#pragma unroll
+              for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(o[x] * k);
+              tmem_st16(tmem + lanes + L::kTmemO + i, v);
+            }
+          }
+        }
+        // weights, rounded to fp16, as A of the second product
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const float p0 = fast_exp2(z[i][x]), p1 = fast_exp2(z[i][x + 1]);
+            part[x % 4] += p0;
+            part[x % 4 + 1] += p1;
+            const __half2 h = __floats2half2_rn(p0, p1);
+            v[x / 2] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st16(tmem + lanes + L::kTmemP + (j & 1) * 64 + i * 16, v);
+        }
+        l += (part[0] + part[1]) + (part[2] + part[3]);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[j & 1]);
+        ok = __all_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int32_t*>(&sm.abort) == 0);
+      }
+      if (n > 0 && ok) {
+        // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's
+        ok = mbar_wait(&sm.drain, 0);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+      }
+      if (!ok) {
+        atomicExch(&sm.abort, 1);
+        if (lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+      }
+      // ------------------------------------------------------------ output
+      float* ws = static_cast<float*>(a.workspace);
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y;
+      float scale = 1.f;
+      if (split) {
+        float* ml = ws + static_cast<int64_t>(gridDim.x) * gridDim.y * 128 * D + slot * 128 * 2;
+        ml[threadIdx.x] = ref;
+        ml[128 + threadIdx.x] = l;
+      } else {
+        float m = ref, all = l, keep = 1.f;
+        if (a.sink && my_flat >= 0) {
+          const float s = a.sink[my_flat % a.H] * kLog2e;
+          const float top = fmaxf(m, s);
+          keep = fast_exp2(m - top);  // 0 where no key was seen
+          all = (l == 0.f ? 0.f : l * keep) + (s == top ? 1.f : fast_exp2(s - top));
+          m = top;
+        }
+        scale = all == 0.f ? 0.f : keep * kUnscale * a.g / all;
+        if (a.lse && my_flat >= 0) a.lse[my_flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+      }
+#pragma unroll 1
+      for (int i = 0; i < D; i += 32) {
+        float o[32];
+        if (n > 0) {
+          tmem_ld<32>(tmem + lanes + L::kTmemO + i, o);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = 0.f;
+        }
+        // decoded channels come in the order of channel_of
+        if (split) {
+          float* to = ws + (slot * 128 + threadIdx.x) * D + i;
+#pragma unroll
+          for (int x = 0; x < 32; x += 8) {
+            *reinterpret_cast<float4*>(to + x) = make_float4(o[x], o[x + 2], o[x + 4], o[x + 6]);
+            *reinterpret_cast<float4*>(to + x + 4) = make_float4(o[x + 1], o[x + 3], o[x + 5], o[x + 7]);
+          }
+        } else {
+          uint8_t* to = smem + threadIdx.x * L::kOutPitch + i * 2;
+#pragma unroll
+          for (int x = 0; x < 32; x += 8)
+            *reinterpret_cast<uint4*>(to + x * 2) =
+                make_uint4(pack_bf16x2_rn(o[x] * scale, o[x + 2] * scale), pack_bf16x2_rn(o[x + 4] * scale, o[x + 6] * scale),
+                           pack_bf16x2_rn(o[x + 1] * scale, o[x + 3] * scale), pack_bf16x2_rn(o[x + 5] * scale, o[x + 7] * scale));
+        }
+      }
+      if (!split) {
+        __syncwarp();  // a warp takes out its own rows
+        constexpr int kRowLanes = D / 8;  // 16-byte pieces of a row
+#pragma unroll 4
+        for (int i = lane; i < 32 * kRowLanes; i += 32) {
+          const int r = warp * 32 + i / kRowLanes, x = i % kRowLanes;
+          const int32_t flat = sm.out[r];
+          if (flat >= 0)
+            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(flat) * D + x * 8) =
+                *reinterpret_cast<const uint4*>(smem + r * L::kOutPitch + x * 16);
+        }
+      }
+      tc_fence_before();
+    }
+  } else if (warp < kRowLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRowMmaRegs));
+    if (warp == kRowMmaWarp && n > 0) {
+      // ------------------------------------------------------- tensor cores
+      if (elect_one()) {
+        constexpr uint32_t kIdescS = idesc_f16(128, false, false), kIdescO = idesc_f16(128, false, true);
+        const uint32_t base = smem_u32(smem);
+        bool ok = mbar_wait(&sm.q_full, 0);
+        auto scores = [&](int j) {
+          const uint32_t d = tmem + L::kTmemS + (L::kSBufs == 2 ? j & 1 : 0) * 128;
+          for (int u = 0; u < L::kUnits && ok; ++u) {
+            const int c = j * L::kUnits + u;
+            ok = mbar_wait(&sm.full[c % kRing], (c / kRing) & 1);
+            tc_fence_after();
+            if (!ok) break;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+              const uint64_t da = smem_desc_sw128(base + L::kQ + (u * 2 + s / 4) * (128 * 128) + (s % 4) * 32, 16, 1024);
+              const uint64_t db = smem_desc_sw128(base + (c % kRing) * kUnitBytes + (s / 4) * 16384 + (s % 4) * 32, 16, 1024);
+              mma_f16_ss(d, da, db, kIdescS, u > 0 || s > 0);
+            }
+          }
+          tc_commit(&sm.s_full[j & 1]);
+        };
+        if (ok) scores(0);
+        for (int j = 0; j < n && ok; ++j) {
+          if (j + 1 < n) {
+            if (L::kSBufs == 1) ok = mbar_wait(&sm.s_read, j & 1);  // with two buffers the weights of tile j - 1 said so
+            tc_fence_after();
+            if (ok) scores(j + 1);
+          }
+          ok = ok && mbar_wait(&sm.p_full[j & 1], (j >> 1) & 1);
+          tc_fence_after();
+          if (!ok) break;
+          for (int u = 0; u < L::kUnits; ++u) {
+            const int c = j * L::kUnits + u;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+              const uint64_t db = smem_desc_sw128(base + (c % kRing) * kUnitBytes + s * 2048, 16384, 1024);
+              mma_f16_ts(tmem + L::kTmemO + u * 128, tmem + L::kTmemP + (j & 1) * 64 + s * 8, db, kIdescO, j > 0 || s > 0);
+            }
+            tc_commit(&sm.empty[c % kRing]);
+          }
+          tc_commit(&sm.o_done);
+        }
+        if (!ok) atomicExch(&sm.abort, 1);
+        // the end of every MMA: the output may be read, and tensor memory given back
+        tc_commit(&sm.drain);
+        if (!mbar_wait(&sm.drain, 0) || !ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRowLoadRegs));
+    if (n > 0) {
+      const bool ok = load_units<D, false, kRing>(a, tile, threadIdx.x - kRowLoadWarp * 32, k_first, k_last, page_shift, shifts, smem, 0u,
+                                                  sm.full, sm.empty, nullptr, sm.bad);
+      if (!ok) {
+        atomicExch(&sm.abort, 1);
+        if (lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+      }
+    }
+  }
+  pdl_trigger();
+  __syncthreads();
+  if (warp == kRowMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc<512>(tmem);
+  }
+}
+
+template <int D>
+cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cudaStream_t s) {
+  cudaError_t e = set_max_smem_once<fp4_attention_rows_kernel<D>>(row_smem_bytes<D>());
+  if (e != cudaSuccess) return e;
+  e = launch_ex(fp4_attention_rows_kernel<D>, dim3(p.tiles, p.splits), dim3(kRowThreads), row_smem_bytes<D>(), use_pdl, s, a, p.chunk,
+                page_shift_of(a.page_size), kShifts);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return launch_ex(fp4_join_kernel<D, 128>, dim3(p.tiles, 128 / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_attention_rows(const Fp4AttentionArgs& a, const Fp4Plan& p, int D, bool use_pdl, cudaStream_t s) {
+  return D == 128 ? launch<128>(a, p, use_pdl, s) : launch<256>(a, p, use_pdl, s);
+}
+
+}  // namespace ckv
