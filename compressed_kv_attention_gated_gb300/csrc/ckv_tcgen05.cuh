@@ -7,6 +7,20 @@
 
 namespace ckv {
 
+// mbar_wait whose first look does not suspend: an already completed phase costs a
+// fraction of the potentially blocking test.
+__device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0 || mbar_wait(bar, parity);
+}
+
 // One thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;

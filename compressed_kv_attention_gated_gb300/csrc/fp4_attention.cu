@@ -276,7 +276,7 @@ uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
       const int key = k_first + j * kKeys + quad * 32 + lane;
       const int unit0 = j * L::kUnits;
       // the decoding warps' note on missing keys, then the scores
-      ok = mbar_wait(&sm.full[unit0 % kRing], (unit0 / kRing) & 1) && mbar_wait(&sm.s_full[j & 1], (j >> 1) & 1);
+      ok = mbar_wait_near(&sm.full[unit0 % kRing], (unit0 / kRing) & 1) && mbar_wait_near(&sm.s_full[j & 1], (j >> 1) & 1);
       if (!ok) atomicExch(&sm.abort, 1);
       __syncwarp();
       tc_fence_after();
@@ -337,7 +337,7 @@ uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
           load_cols<L::kCols>(&sm.keep[col0], z);
 #pragma unroll
           for (int i = 0; i < L::kCols; ++i) l[i] *= z[i];
-          ok = mbar_wait(&sm.o_done, (j - 1) & 1);
+          ok = mbar_wait_near(&sm.o_done, (j - 1) & 1);
           if (!ok) atomicExch(&sm.abort, 1);
           __syncwarp();
           tc_fence_after();
@@ -381,7 +381,7 @@ uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
     // --------------------------------------------------------------- output
     if (n > 0 && ok) {
       // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's
-      ok = mbar_wait(&sm.drain, 0);
+      ok = mbar_wait_near(&sm.drain, 0);
       __syncwarp();
       tc_fence_after();
     }
@@ -465,12 +465,12 @@ uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
     if (elect_one()) {
       constexpr uint32_t kIdescS = idesc_f16(R, false, false), kIdescO = idesc_f16(R, true, true);
       const uint32_t base = smem_u32(smem);
-      bool ok = mbar_wait(&sm.q_full, 0);
+      bool ok = mbar_wait_near(&sm.q_full, 0);
       auto scores = [&](int j) {
         const uint32_t d = tmem + L::kTmemS + (L::kAhead ? j & 1 : 0) * R;
         for (int u = 0; u < L::kUnits && ok; ++u) {
           const int c = j * L::kUnits + u;
-          ok = mbar_wait(&sm.full[c % kRing], (c / kRing) & 1);
+          ok = mbar_wait_near(&sm.full[c % kRing], (c / kRing) & 1);
           tc_fence_after();
           if (!ok) break;
 #pragma unroll
@@ -485,7 +485,7 @@ uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
       if (ok) scores(0);
       for (int j = 0; j < n && ok; ++j) {
         if (L::kAhead && j + 1 < n) scores(j + 1);
-        ok = ok && mbar_wait(&sm.p_full[j & 1], (j >> 1) & 1);
+        ok = ok && mbar_wait_near(&sm.p_full[j & 1], (j >> 1) & 1);
         tc_fence_after();
         if (!ok) break;
         const uint32_t p = base + L::kP + (L::kAhead ? j & 1 : 0) * (kKeys * 128);
@@ -505,7 +505,7 @@ uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
       if (!ok) atomicExch(&sm.abort, 1);
       // the end of every MMA: the output may be read, and tensor memory given back
       tc_commit(&sm.drain);
-      if (!mbar_wait(&sm.drain, 0) || !ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+      if (!mbar_wait_near(&sm.drain, 0) || !ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
     }
     __syncwarp();
     }

@@ -232,8 +232,8 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
       const int c = c0 + i;
       if (c < total && ok) {
         // the ring's last unit in this place has served both products
-        if (c >= kRing) ok = mbar_wait(&empty[i], ((c / kRing) - 1) & 1);
-        if (kCopy && kSlots < kRing && i >= kSlots) ok = ok && mbar_wait(&a_free[c % kSlots], ((c / kSlots) - 1) & 1);
+        if (c >= kRing) ok = mbar_wait_near(&empty[i], ((c / kRing) - 1) & 1);
+        if (kCopy && kSlots < kRing && i >= kSlots) ok = ok && mbar_wait_near(&a_free[c % kSlots], ((c / kSlots) - 1) & 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (ok) {
           if (kCopy) tc_fence_after();

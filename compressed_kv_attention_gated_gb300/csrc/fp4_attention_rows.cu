@@ -3,27 +3,27 @@
 // at D = 128 and 256 (fp4_attention.cu holds the other form and the formulas):
 //   S [128 rows x 128 keys]   = Q [128 x D] K^T
 //   O [128 rows x D]         += P [128 x 128 keys] K
-// A thread owns a row of S: its maximum and sum need no other thread, and its
-// weights go back to tensor memory as A of the second product.  Per 128 keys the
-// softmax warps evaluate 128 x 128 exponentials, which bounds the loop (16 per
-// clock and SM: 1024 clocks); the products take 256 to 512 (D = 128).
+// A thread owns 64 keys of a row of S (two warps share 32 rows): maximum and sum
+// need one other thread at most, and the weights go back to tensor memory as A of
+// the second product.  Per 128 keys the 8 softmax warps evaluate 128 x 128
+// exponentials, as much work as the products (512 clocks at D = 128).
 //
 // As in the other form a row's weights are taken against a reference that moves
-// only when a score exceeds it by 2^8; here that is one warp's own affair.
+// only when a score exceeds it by 2^8; here that is the affair of two warps.
 //
 // At D = 512 the accumulator would fill tensor memory, and with few rows most of
-// M would be idle while one warp does the whole softmax: those take the other form.
+// M would be idle while two warps do the whole softmax: those take the other form.
 #include "fp4_attention.cuh"
 
 namespace ckv {
 namespace {
 
-// Warpgroup 0: softmax; 1: its first warp issues the MMAs; 2 and 3: load and decode.
-constexpr int kRowMmaWarp = 4, kRowLoadWarp = 8;
-constexpr int kRowThreads = 512;
-// Registers per thread: 128 at launch (65,536), then 128 x 224 + 128 x 56 + 256 x 104 = 62,464.
-constexpr int kRowSoftRegs = 224, kRowMmaRegs = 56, kRowLoadRegs = 104;
-static_assert(128 * kRowSoftRegs + 128 * kRowMmaRegs + 256 * kRowLoadRegs <= kRowThreads * 128, "registers of the launch");
+// Warpgroups 0 and 1: softmax; 2: its first warp issues the MMAs; 3 and 4: load and decode.
+constexpr int kRowMmaWarp = 8, kRowLoadWarp = 12;
+constexpr int kRowThreads = 640;
+// Registers per thread: 96 at launch (61,440), then 256 x 120 + 128 x 64 + 256 x 88 = 61,440.
+constexpr int kRowSoftRegs = 120, kRowMmaRegs = 64, kRowLoadRegs = 88;
+static_assert(256 * kRowSoftRegs + 128 * kRowMmaRegs + 256 * kRowLoadRegs <= kRowThreads * 96, "registers of the launch");
 
 template <int D>
 struct RowLayout {
@@ -45,6 +45,7 @@ struct RowSmall {
   int32_t ctx_max;
   alignas(16) uint32_t bad[4][4];
   float c[128];     // score factors
+  float part[2][128];  // what the two warps of a row tell each other
   int64_t q[128];   // where the rows' queries begin, elements
   int32_t out[128]; // flat (token, head) index, -1: none
 };
@@ -54,7 +55,18 @@ constexpr int row_smem_bytes() {
   return RowLayout<D>::kSmall + static_cast<int>(sizeof(RowSmall)) + 1024;
 }
 
-__device__ __forceinline__ void row_barrier() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+// The two warps of 32 rows (quad q) meet; true when p holds for one of the 64 threads.
+__device__ __forceinline__ void pair_barrier(int quad) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + quad) : "memory"); }
+__device__ __forceinline__ bool pair_any(int quad, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p)), "r"(1 + quad)
+      : "memory");
+  return r != 0;
+}
 
 // 16 packed columns of the warp's lanes.
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
@@ -83,10 +95,10 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.s_full[i], 1);
-        mbar_init(&sm.p_full[i], 4);
+        mbar_init(&sm.p_full[i], 8);
       }
-      mbar_init(&sm.s_read, 4);
-      mbar_init(&sm.q_full, 4);
+      mbar_init(&sm.s_read, 8);
+      mbar_init(&sm.q_full, 8);
       mbar_init(&sm.o_done, 1);
       mbar_init(&sm.drain, 1);
       sm.abort = 0;
@@ -106,9 +118,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   tc_fence_after();
   const Tile tile = sm.tile;
   const uint32_t tmem = sm.tmem;
-  int32_t my_ctx = -1, my_flat = -1;  // of thread r < 128: its row
-  if (threadIdx.x < 128) {
-    const int r = threadIdx.x;
+  int32_t my_ctx = -1, my_flat = -1;  // of softmax thread t: row t % 128
+  if (threadIdx.x < 256) {
+    const int r = threadIdx.x & 127;
     if (r < tile.rows) {
       const int t = tile.tok0 + (tile.base + r) / a.H;
       my_ctx = a.ctx_rows[t];
@@ -134,19 +146,20 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   // nothing to add: only the first range answers for rows that see nothing
   const bool idle = n == 0 && (blockIdx.y > 0 || ctx_max < 0);
 
-  if (warp < 4) {
+  if (warp < kRowMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowSoftRegs));
     if (!idle) {
+      const int quad = warp & 3, half = warp >> 2, row = threadIdx.x & 127;
       // ----------------------------------------------------------- queries
-      // eight channels per lane, D/8 lanes per row; every load of a batch is issued before the first is used
+      // eight channels per lane, D/8 lanes per row, 16 rows per warp; every load is issued before the first is used
       if (n > 0) {
-        constexpr int kSpan = D / 8 < 32 ? D / 8 : 32;  // lanes of a row
-        constexpr int kPer = 32 / kSpan;                // rows of a warp at a time
-        constexpr int kBatch = 16;
+        constexpr int kSpan = D / 8;     // lanes of a row
+        constexpr int kPer = 32 / kSpan; // rows of a warp at a time
+        constexpr int kBatch = 8;
         const int sub = lane / kSpan, ch = lane % kSpan * 8;
-        static_assert(D <= 256 && 32 % (kBatch * kPer) == 0, "");
+        static_assert(D <= 256 && 16 % (kBatch * kPer) == 0, "");
 #pragma unroll 1
-        for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += kBatch * kPer) {
+        for (int r0 = warp * 16; r0 < warp * 16 + 16; r0 += kBatch * kPer) {
           uint4 raw[kBatch];
           uint32_t am[kBatch];
 #pragma unroll
@@ -179,26 +192,26 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         }
       }
       fence_proxy_async_smem();
-      __syncwarp();
+      asm volatile("barrier.cta.sync 5, 256;" ::: "memory");  // every row's factor is there
       if (lane == 0) mbar_arrive(&sm.q_full);
 
       // ----------------------------------------------------------- softmax
-      const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-      const float c = n > 0 ? sm.c[threadIdx.x] : 0.f;  // the warp's own rows
-      float ref = kNegBig, l = 0.f;
+      const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+      const float c = n > 0 ? sm.c[row] : 0.f;
+      float ref = kNegBig, l = 0.f;  // the reference is the same in both threads of a row, the sum each one's own
       bool ok = true;
 #pragma unroll 1
-      for (int j = 0; j < n && ok; ++j) {
+      for (int j = 0; j < n; ++j) {
         const int buf = L::kSBufs == 2 ? j & 1 : 0;
         const int unit0 = j * L::kUnits;
         // the decoding warps' note on missing keys, then the scores
-        ok = mbar_wait(&sm.full[unit0 % kRing], (unit0 / kRing) & 1) && mbar_wait(&sm.s_full[j & 1], (j >> 1) & 1);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+        ok = mbar_wait_near(&sm.full[unit0 % kRing], (unit0 / kRing) & 1) && mbar_wait_near(&sm.s_full[j & 1], (j >> 1) & 1);
+        if (!ok) atomicExch(&sm.abort, 1);
+        __syncwarp();
         tc_fence_after();
-        float z[4][32];
+        float z[2][32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld<32>(tmem + lanes + L::kTmemS + buf * 128 + i * 32, z[i]);
+        for (int i = 0; i < 2; ++i) tmem_ld<32>(tmem + lanes + L::kTmemS + buf * 128 + half * 64 + i * 32, z[i]);
         if (L::kSBufs == 1) {
           tc_fence_before();
           __syncwarp();
@@ -208,24 +221,30 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         const bool unset = ref == kNegBig;
         const float shift = unset ? 0.f : ref;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) z[i / 32][i % 32] = fmaf(z[i / 32][i % 32], c, -shift);
-        const int left = my_ctx - (k_first + j * kKeys);  // keys of the tile that the row sees
-        const uint4 gone = *reinterpret_cast<const uint4*>(sm.bad[j & 3]);
-        if (__any_sync(0xFFFFFFFFu, left < kKeys)) {
+        for (int i = 0; i < 64; ++i) z[i / 32][i % 32] = fmaf(z[i / 32][i % 32], c, -shift);
+        const int left = my_ctx - (k_first + j * kKeys + half * 64);  // keys of the thread's that the row sees
+        const uint2 gone = *reinterpret_cast<const uint2*>(&sm.bad[j & 3][half * 2]);
+        if (__any_sync(0xFFFFFFFFu, left < 64)) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) z[i / 32][i % 32] = i < left ? z[i / 32][i % 32] : -INFINITY;
+          for (int i = 0; i < 64; ++i) z[i / 32][i % 32] = i < left ? z[i / 32][i % 32] : -INFINITY;
         }
-        if (gone.x | gone.y | gone.z | gone.w) {
-          const uint32_t g[4] = {gone.x, gone.y, gone.z, gone.w};
+        if (gone.x | gone.y) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) z[i / 32][i % 32] = (g[i / 32] >> (i % 32)) & 1 ? -INFINITY : z[i / 32][i % 32];
+          for (int i = 0; i < 64; ++i) z[i / 32][i % 32] = ((i < 32 ? gone.x : gone.y) >> (i % 32)) & 1 ? -INFINITY : z[i / 32][i % 32];
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 128; ++i) top[i % 4] = fmaxf(top[i % 4], z[i / 32][i % 32]);
-        const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (__any_sync(0xFFFFFFFFu, over > kJump || (unset && over > -INFINITY))) {
+        for (int i = 0; i < 64; ++i) top[i % 4] = fmaxf(top[i % 4], z[i / 32][i % 32]);
+        float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        ok = ok && *reinterpret_cast<volatile int32_t*>(&sm.abort) == 0;
+        if (pair_any(quad, over > kJump || (unset && over > -INFINITY) || !ok)) {
+          ok = !pair_any(quad, !ok);
+          if (!ok) break;
           // the largest score so far becomes the reference
+          sm.part[half][row] = over;
+          pair_barrier(quad);
+          over = fmaxf(over, sm.part[half ^ 1][row]);
+          pair_barrier(quad);  // read, before it is written again
           const float d = unset ? over : fmaxf(over, 0.f);
           const bool move = d > -INFINITY;
           const float by = move ? d : 0.f;
@@ -233,15 +252,15 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           l *= keep;
           ref = move ? shift + by : ref;
 #pragma unroll
-          for (int i = 0; i < 128; ++i) z[i / 32][i % 32] -= by;
+          for (int i = 0; i < 64; ++i) z[i / 32][i % 32] -= by;
           if (j > 0) {
-            ok = mbar_wait(&sm.o_done, (j - 1) & 1);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
+            ok = mbar_wait_near(&sm.o_done, (j - 1) & 1);
+            if (!ok) atomicExch(&sm.abort, 1);
+            __syncwarp();
             tc_fence_after();
             const float k = unset ? 1.f : keep;  // an unset row's output is 0
 #pragma unroll 1
-            for (int i = 0; i < D; i += 16) {
+            for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 16) {
               float o[16];
               tmem_ld<16>(tmem + lanes + L::kTmemO + i, o);
               uint32_t v[16];
@@ -254,7 +273,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         // weights, rounded to fp16, as A of the second product
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           uint32_t v[16];
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
@@ -264,47 +283,49 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             const __half2 h = __floats2half2_rn(p0, p1);
             v[x / 2] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          tmem_st16(tmem + lanes + L::kTmemP + (j & 1) * 64 + i * 16, v);
+          tmem_st16(tmem + lanes + L::kTmemP + (j & 1) * 64 + half * 32 + i * 16, v);
         }
         l += (part[0] + part[1]) + (part[2] + part[3]);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[j & 1]);
-        ok = __all_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int32_t*>(&sm.abort) == 0);
       }
       if (n > 0 && ok) {
         // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's
-        ok = mbar_wait(&sm.drain, 0);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = mbar_wait_near(&sm.drain, 0);
+        __syncwarp();
         tc_fence_after();
       }
-      if (!ok) {
-        atomicExch(&sm.abort, 1);
-        if (lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
-      }
+      if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
       // ------------------------------------------------------------ output
+      pair_barrier(quad);
+      sm.part[half][row] = l;
+      pair_barrier(quad);
+      l += sm.part[half ^ 1][row];
       float* ws = static_cast<float*>(a.workspace);
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y;
       float scale = 1.f;
       if (split) {
-        float* ml = ws + static_cast<int64_t>(gridDim.x) * gridDim.y * 128 * D + slot * 128 * 2;
-        ml[threadIdx.x] = ref;
-        ml[128 + threadIdx.x] = l;
+        if (half == 0) {
+          float* ml = ws + static_cast<int64_t>(gridDim.x) * gridDim.y * 128 * D + slot * 128 * 2;
+          ml[row] = ref;
+          ml[128 + row] = l;
+        }
       } else {
         float m = ref, all = l, keep = 1.f;
         if (a.sink && my_flat >= 0) {
           const float s = a.sink[my_flat % a.H] * kLog2e;
-          const float top = fmaxf(m, s);
-          keep = fast_exp2(m - top);  // 0 where no key was seen
-          all = (l == 0.f ? 0.f : l * keep) + (s == top ? 1.f : fast_exp2(s - top));
-          m = top;
+          const float high = fmaxf(m, s);
+          keep = fast_exp2(m - high);  // 0 where no key was seen
+          all = (l == 0.f ? 0.f : l * keep) + (s == high ? 1.f : fast_exp2(s - high));
+          m = high;
         }
         scale = all == 0.f ? 0.f : keep * kUnscale * a.g / all;
-        if (a.lse && my_flat >= 0) a.lse[my_flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+        if (a.lse && my_flat >= 0 && half == 0) a.lse[my_flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
       }
 #pragma unroll 1
-      for (int i = 0; i < D; i += 32) {
+      for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
         float o[32];
         if (n > 0) {
           tmem_ld<32>(tmem + lanes + L::kTmemO + i, o);
@@ -314,14 +335,14 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         }
         // decoded channels come in the order of channel_of
         if (split) {
-          float* to = ws + (slot * 128 + threadIdx.x) * D + i;
+          float* to = ws + (slot * 128 + row) * D + i;
 #pragma unroll
           for (int x = 0; x < 32; x += 8) {
             *reinterpret_cast<float4*>(to + x) = make_float4(o[x], o[x + 2], o[x + 4], o[x + 6]);
             *reinterpret_cast<float4*>(to + x + 4) = make_float4(o[x + 1], o[x + 3], o[x + 5], o[x + 7]);
           }
         } else {
-          uint8_t* to = smem + threadIdx.x * L::kOutPitch + i * 2;
+          uint8_t* to = smem + row * L::kOutPitch + i * 2;
 #pragma unroll
           for (int x = 0; x < 32; x += 8)
             *reinterpret_cast<uint4*>(to + x * 2) =
@@ -330,11 +351,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         }
       }
       if (!split) {
-        __syncwarp();  // a warp takes out its own rows
-        constexpr int kRowLanes = D / 8;  // 16-byte pieces of a row
+        __syncwarp();  // a warp takes out what it brought: its rows' half
+        constexpr int kPieces = D / 16;  // 16-byte pieces of half a row
 #pragma unroll 4
-        for (int i = lane; i < 32 * kRowLanes; i += 32) {
-          const int r = warp * 32 + i / kRowLanes, x = i % kRowLanes;
+        for (int i = lane; i < 32 * kPieces; i += 32) {
+          const int r = quad * 32 + i / kPieces, x = half * kPieces + i % kPieces;
           const int32_t flat = sm.out[r];
           if (flat >= 0)
             *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(flat) * D + x * 8) =
@@ -350,12 +371,12 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       if (elect_one()) {
         constexpr uint32_t kIdescS = idesc_f16(128, false, false), kIdescO = idesc_f16(128, false, true);
         const uint32_t base = smem_u32(smem);
-        bool ok = mbar_wait(&sm.q_full, 0);
+        bool ok = mbar_wait_near(&sm.q_full, 0);
         auto scores = [&](int j) {
           const uint32_t d = tmem + L::kTmemS + (L::kSBufs == 2 ? j & 1 : 0) * 128;
           for (int u = 0; u < L::kUnits && ok; ++u) {
             const int c = j * L::kUnits + u;
-            ok = mbar_wait(&sm.full[c % kRing], (c / kRing) & 1);
+            ok = mbar_wait_near(&sm.full[c % kRing], (c / kRing) & 1);
             tc_fence_after();
             if (!ok) break;
 #pragma unroll
@@ -370,11 +391,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         if (ok) scores(0);
         for (int j = 0; j < n && ok; ++j) {
           if (j + 1 < n) {
-            if (L::kSBufs == 1) ok = mbar_wait(&sm.s_read, j & 1);  // with two buffers the weights of tile j - 1 said so
+            if (L::kSBufs == 1) ok = mbar_wait_near(&sm.s_read, j & 1);  // with two buffers the weights of tile j - 1 said so
             tc_fence_after();
             if (ok) scores(j + 1);
           }
-          ok = ok && mbar_wait(&sm.p_full[j & 1], (j >> 1) & 1);
+          ok = ok && mbar_wait_near(&sm.p_full[j & 1], (j >> 1) & 1);
           tc_fence_after();
           if (!ok) break;
           for (int u = 0; u < L::kUnits; ++u) {
@@ -391,7 +412,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         if (!ok) atomicExch(&sm.abort, 1);
         // the end of every MMA: the output may be read, and tensor memory given back
         tc_commit(&sm.drain);
-        if (!mbar_wait(&sm.drain, 0) || !ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+        if (!mbar_wait_near(&sm.drain, 0) || !ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
       }
       __syncwarp();
     }
