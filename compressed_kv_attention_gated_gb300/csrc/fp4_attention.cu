@@ -127,7 +127,7 @@ static_assert(kSoftWarps * 32 == 256, "the softmax warps' named barrier");
 
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk,
-                                                                    int page_shift, const __grid_constant__ Shifts shifts) {
+                                                                    int page_shift) {
   using L = Layout<D, R>;
   extern __shared__ uint8_t s_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -252,7 +252,7 @@ uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
         const int se = query_exponent(am[i]);
         const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
         if (lane % kSpan == 0)
-          sm.c[r] = a.softmax_scale * kLog2e * kUnscale * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
+          sm.c[r] = a.softmax_scale * kLog2e * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
         uint8_t* row = smem + L::kQ + (ch / 64) * (R * 128) + r * 128;
 #pragma unroll
         for (int x = 0; x < kC / 8; ++x)
@@ -408,10 +408,10 @@ uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
           const float top = fmaxf(m, s);
           const float keep = fast_exp2(m - top);  // 0 where no key was seen
           all = (total == 0.f ? 0.f : total * keep) + (s == top ? 1.f : fast_exp2(s - top));
-          sm.c[r] = all == 0.f ? 0.f : keep * kUnscale * a.g / all;
+          sm.c[r] = all == 0.f ? 0.f : keep * a.g / all;
           m = top;
         } else {
-          sm.c[r] = all == 0.f ? 0.f : kUnscale * a.g / all;
+          sm.c[r] = all == 0.f ? 0.f : a.g / all;
         }
         if (a.lse && flat >= 0) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
       }
@@ -427,19 +427,19 @@ uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
 #pragma unroll
         for (int i = 0; i < L::kCols; ++i) o[i] = 0.f;
       }
-      const int ch = u * 128 + channel_of(quad * 32 + lane);
+      const int ch = u * 128 + quad * 32 + lane;
       if (split) {
 #pragma unroll
         for (int i = 0; i < L::kCols; ++i) ws[(slot * R + col0 + i) * D + ch] = o[i];
       } else {
-        // through shared memory (the ring is free) so that rows leave in 16-byte pieces; lanes
-        // with channels 2c and 2c + 1 (two apart) trade halves: one has both channels of row i, the other of row i + 1
-        const bool odd = lane & 2;
+        // through shared memory (the ring is free) so that rows leave in 16-byte pieces; neighbouring
+        // lanes (channels) trade halves: the even one has both channels of row i, the odd one of row i + 1
+        const bool odd = lane & 1;
         uint8_t* to = smem + (col0 + (odd ? 1 : 0)) * L::kOutPitch + (ch & ~1) * 2;
 #pragma unroll
         for (int i = 0; i < L::kCols; i += 2) {
           const float v0 = o[i] * l[i], v1 = o[i + 1] * l[i + 1];
-          const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 2);
+          const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
           *reinterpret_cast<uint32_t*>(to + i * L::kOutPitch) = odd ? pack_bf16x2_rn(got, v1) : pack_bf16x2_rn(v0, got);
         }
       }
@@ -513,7 +513,7 @@ uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (n > 0) {
     // ------------------------------------------------------- load and decode
-    const bool ok = load_units<D, true, L::kSlots>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, shifts, smem,
+    const bool ok = load_units<D, true, L::kSlots>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, smem,
                                                    tmem + L::kTmemK, sm.full, sm.empty, sm.a_free, sm.bad);
     if (!ok) {
       atomicExch(&sm.abort, 1);
@@ -534,7 +534,7 @@ cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cu
   cudaError_t e = set_max_smem_once<fp4_attention_kernel<D, R>>(smem_bytes<D, R>());
   if (e != cudaSuccess) return e;
   e = launch_ex(fp4_attention_kernel<D, R>, dim3(p.tiles, p.splits), dim3(kThreads), smem_bytes<D, R>(), use_pdl, s, a, p.chunk,
-                page_shift_of(a.page_size), kShifts);
+                page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_ex(fp4_join_kernel<D, R>, dim3(p.tiles, R / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
 }

@@ -65,21 +65,24 @@ __device__ __forceinline__ Tile find_tile(const Fp4AttentionArgs& a, int32_t til
   return t;
 }
 
-// Decoding on the integer and fp16 pipes (a hardware conversion of two codes
-// runs at an eighth of their rate).  A code's exponent and mantissa bits at bits
-// 11..9 of an fp16 are its value * 2^-14 (a subnormal code lands on a subnormal),
-// an e4m3's bits shifted up by 7 its value * 2^-8; the scale is brought to
-// scale * 2^7 (at most 57344), so that the product is value * 2^-7: at least
-// 2^-17 with 6 significant bits, exact in fp16.  Every byte decodes to a finite
-// number.  The left shifts are multiplications by kernel parameters, which the
-// multiplier pipe does beside the logic pipe.  Codes come out in pairs (i, i + 4) of the word's eight.
-constexpr float kUnscale = 128.f;
-
-struct Shifts {
-  uint32_t by[6];  // 2^9, 2^12, 2^5, 2^8, 2^1, 2^4
-};
-
-constexpr Shifts kShifts{{1u << 9, 1u << 12, 1u << 5, 1u << 8, 1u << 1, 1u << 4}};
+// Decoding: the hardware converts two codes to two fp16, which the block's scale then
+// multiplies.  A value has 2 + 4 significant bits and lies in 2^-10 .. 2688: exact.
+// An e4m3's bits shifted up by 7 are an fp16 of 2^-8 of its value, for every byte (0x7F
+// is 480): every byte of a cache decodes to a finite number.
+__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), s);
+    r[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
 
 // log2 of a page size that is a power of two, else -1
 inline int page_shift_of(int32_t page_size) {
@@ -89,26 +92,13 @@ inline int page_shift_of(int32_t page_size) {
   return s;
 }
 
-__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s, const Shifts& k) {
-  const uint32_t m[4] = {((w * k.by[0]) & 0x0E000E00u) | ((w * k.by[1]) & 0x80008000u),
-                         ((w * k.by[2]) & 0x0E000E00u) | ((w * k.by[3]) & 0x80008000u),
-                         ((w * k.by[4]) & 0x0E000E00u) | ((w * k.by[5]) & 0x80008000u), ((w >> 3) & 0x0E000E00u) | (w & 0x80008000u)};
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&m[i]), s);
-    r[i] = *reinterpret_cast<const uint32_t*>(&p);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
-// Four e4m3 bytes, each twice in a register, times 2^7.
+// Four e4m3 bytes, each twice in a register.
 __device__ __forceinline__ void decode_scales(uint32_t b, __half2 (&s)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t x = b >> (8 * i);  // bytes i and i + 2 in the low byte of each half
     const uint32_t m = ((x & 0x007F007Fu) << 7) | ((x & 0x00800080u) << 8);
-    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&m), __float2half2_rn(32768.f));
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&m), __float2half2_rn(256.f));
     s[i] = __low2half2(v);
     s[i + 2] = __high2half2(v);
   }
@@ -122,23 +112,16 @@ __device__ __forceinline__ int query_exponent(uint32_t am) {
   return am == 0u || e == 255 ? 127 : min(127 + 14 + 127 - e, 253);
 }
 
-// Eight bf16 channels times `up`, as fp16 in the order in which codes are decoded.
+// Eight bf16 channels times `up`, as fp16.
 __device__ __forceinline__ uint4 query8(uint4 raw, float up) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   uint32_t v[4];
 #pragma unroll
-  for (int y = 0; y < 4; ++y) {  // channels y and y + 4
-    const float lo = y & 1 ? bf16_hi(w[y / 2]) : bf16_lo(w[y / 2]), hi = y & 1 ? bf16_hi(w[2 + y / 2]) : bf16_lo(w[2 + y / 2]);
-    const __half2 p = __floats2half2_rn(lo * up, hi * up);
+  for (int y = 0; y < 4; ++y) {
+    const __half2 p = __floats2half2_rn(bf16_lo(w[y]) * up, bf16_hi(w[y]) * up);
     v[y] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-// Where channel c of a row is kept in the decoded tile (and so in Q and O): the
-// eight channels of a word in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ constexpr int channel_of(int place) {
-  return (place & ~7) | ((place & 1) << 2) | ((place >> 1) & 3);
 }
 
 // Columns of a per-row array, 16 bytes at a time.  They are read in one go before
@@ -165,7 +148,7 @@ __device__ __forceinline__ void load_cols(const float* p, float (&v)[n]) {
 // Rows that are not there are zeros.  False when a wait ran out.
 template <int D, bool kCopy, int kSlots>
 __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile& tile, int tid, int k_first, int k_last, int page_shift,
-                                           const Shifts& shifts, uint8_t* ring, uint32_t tmem_k, uint64_t* full, uint64_t* empty,
+                                           uint8_t* ring, uint32_t tmem_k, uint64_t* full, uint64_t* empty,
                                            uint64_t* a_free, uint32_t (*bad)[4]) {
   constexpr int kUnits = D / 128;
   static_assert(kSlots == kRing || kUnits == kRing, "waits");
@@ -244,7 +227,7 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
 #pragma unroll
           for (int b = 0; b < 4; ++b) {  // blocks of 16 channels
             const uint4 x = reg[i].c[b / 2];
-            const uint4 lo = decode8(b & 1 ? x.z : x.x, sc[b], shifts), hi = decode8(b & 1 ? x.w : x.y, sc[b], shifts);
+            const uint4 lo = decode8(b & 1 ? x.z : x.x, sc[b]), hi = decode8(b & 1 ? x.w : x.y, sc[b]);
             *reinterpret_cast<uint4*>(unit + (((2 * b) ^ (key & 7)) * 16)) = lo;
             *reinterpret_cast<uint4*>(unit + (((2 * b + 1) ^ (key & 7)) * 16)) = hi;
             if (kCopy) tmem_st8(a_tile + b * 8, lo, hi);
@@ -318,7 +301,7 @@ __global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ F
       acc[4 * i + 3] = fmaf(v.w, w, acc[4 * i + 3]);
     }
   }
-  const float inv = all == 0.f ? 0.f : kUnscale * a.g / all;
+  const float inv = all == 0.f ? 0.f : a.g / all;
 #pragma unroll
   for (int i = 0; i < D / 128; ++i)
     *reinterpret_cast<uint2*>(a.out + flat * D + i * 128 + lane * 4) =

@@ -79,7 +79,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads, 1)
-    fp4_attention_rows_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int page_shift, const __grid_constant__ Shifts shifts) {
+    fp4_attention_rows_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int page_shift) {
   using L = RowLayout<D>;
   extern __shared__ uint8_t s_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             const int se = query_exponent(am[i]);
             const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
             if (lane % kSpan == 0)
-              sm.c[r] = a.softmax_scale * kLog2e * kUnscale * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
+              sm.c[r] = a.softmax_scale * kLog2e * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
             *reinterpret_cast<uint4*>(smem + L::kQ + (ch / 64) * (128 * 128) + r * 128 + (((ch % 64) / 8) ^ (r & 7)) * 16) =
                 query8(raw[i], up);
           }
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           all = (l == 0.f ? 0.f : l * keep) + (s == high ? 1.f : fast_exp2(s - high));
           m = high;
         }
-        scale = all == 0.f ? 0.f : keep * kUnscale * a.g / all;
+        scale = all == 0.f ? 0.f : keep * a.g / all;
         if (a.lse && my_flat >= 0 && half == 0) a.lse[my_flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
       }
 #pragma unroll 1
@@ -333,21 +333,20 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = 0.f;
         }
-        // decoded channels come in the order of channel_of
         if (split) {
           float* to = ws + (slot * 128 + row) * D + i;
 #pragma unroll
           for (int x = 0; x < 32; x += 8) {
-            *reinterpret_cast<float4*>(to + x) = make_float4(o[x], o[x + 2], o[x + 4], o[x + 6]);
-            *reinterpret_cast<float4*>(to + x + 4) = make_float4(o[x + 1], o[x + 3], o[x + 5], o[x + 7]);
+            *reinterpret_cast<float4*>(to + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+            *reinterpret_cast<float4*>(to + x + 4) = make_float4(o[x + 4], o[x + 5], o[x + 6], o[x + 7]);
           }
         } else {
           uint8_t* to = smem + row * L::kOutPitch + i * 2;
 #pragma unroll
           for (int x = 0; x < 32; x += 8)
             *reinterpret_cast<uint4*>(to + x * 2) =
-                make_uint4(pack_bf16x2_rn(o[x] * scale, o[x + 2] * scale), pack_bf16x2_rn(o[x + 4] * scale, o[x + 6] * scale),
-                           pack_bf16x2_rn(o[x + 1] * scale, o[x + 3] * scale), pack_bf16x2_rn(o[x + 5] * scale, o[x + 7] * scale));
+                make_uint4(pack_bf16x2_rn(o[x] * scale, o[x + 1] * scale), pack_bf16x2_rn(o[x + 2] * scale, o[x + 3] * scale),
+                           pack_bf16x2_rn(o[x + 4] * scale, o[x + 5] * scale), pack_bf16x2_rn(o[x + 6] * scale, o[x + 7] * scale));
         }
       }
       if (!split) {
@@ -419,7 +418,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRowLoadRegs));
     if (n > 0) {
-      const bool ok = load_units<D, false, kRing>(a, tile, threadIdx.x - kRowLoadWarp * 32, k_first, k_last, page_shift, shifts, smem, 0u,
+      const bool ok = load_units<D, false, kRing>(a, tile, threadIdx.x - kRowLoadWarp * 32, k_first, k_last, page_shift, smem, 0u,
                                                   sm.full, sm.empty, nullptr, sm.bad);
       if (!ok) {
         atomicExch(&sm.abort, 1);
@@ -440,7 +439,7 @@ cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cu
   cudaError_t e = set_max_smem_once<fp4_attention_rows_kernel<D>>(row_smem_bytes<D>());
   if (e != cudaSuccess) return e;
   e = launch_ex(fp4_attention_rows_kernel<D>, dim3(p.tiles, p.splits), dim3(kRowThreads), row_smem_bytes<D>(), use_pdl, s, a, p.chunk,
-                page_shift_of(a.page_size), kShifts);
+                page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_ex(fp4_join_kernel<D, 128>, dim3(p.tiles, 128 / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
 }
