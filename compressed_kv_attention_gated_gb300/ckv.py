@@ -613,6 +613,8 @@ def ckv_plan_online_prefill(seq_lens, extend_lens, num_tokens=None, pad_for_grap
 
 
 # ------------------------------------------- a serving step around the cache
+# These launch as programmatic dependents by default: a kernel may be set up while the one
+# before it in the stream still runs, and waits for its end before it touches memory.
 STEP_MAPS = ("row_start", "positions", "batch_ids", "slot_mapping", "cache_loc", "tail_slots", "row_positions",
              "ctx_rows")
 
@@ -638,7 +640,7 @@ def _raw(stream):
 
 
 def ckv_build_step_maps(seq_lens, query_lens, block_table, free_pages, cursor, pool_size, page_size, num_tokens,
-                        tail_blocks=None, cursor_out=None, out=None, use_pdl=False, err_word=None, stream=None):
+                        tail_blocks=None, cursor_out=None, out=None, use_pdl=True, err_word=None, stream=None):
     """Block tables and slot maps of one step; see ckv_build_step_maps in include/ckv.h.
 
     seq_lens/query_lens (and tail_blocks) int32 [B]; block_table int32 [B,
@@ -665,7 +667,7 @@ def ckv_build_step_maps(seq_lens, query_lens, block_table, free_pages, cursor, p
 
 
 def ckv_qk_norm_rope(q, q_positions, cos_sin=None, q_weight=None, q_out=None, k=None, k_positions=None, k_weight=None,
-                     k_out=None, rope_offset=None, interleaved=False, eps=1e-6, use_pdl=False, err_word=None, stream=None):
+                     k_out=None, rope_offset=None, interleaved=False, eps=1e-6, use_pdl=True, err_word=None, stream=None):
     """Norm and rotation of queries and keys (or compressed rows) in one pass;
     see ckv_qk_norm_rope in include/ckv.h.
 
@@ -689,7 +691,7 @@ def ckv_qk_norm_rope(q, q_positions, cos_sin=None, q_weight=None, q_out=None, k=
     return q_out, k_out
 
 
-def ckv_fp4_store(rows, kv_cache, loc, cache_scale=1.0, use_pdl=False, err_word=None, stream=None):
+def ckv_fp4_store(rows, kv_cache, loc, cache_scale=1.0, use_pdl=True, err_word=None, stream=None):
     """Store rows in the 4-bit cache; see ckv_fp4_store in include/ckv.h.
 
     rows float32/bf16 [n, D] (last dim contiguous); kv_cache uint8 [pages,
@@ -701,7 +703,7 @@ def ckv_fp4_store(rows, kv_cache, loc, cache_scale=1.0, use_pdl=False, err_word=
         _check("ckv_fp4_store", status)
 
 
-def ckv_fp4_load(kv_cache, loc, out, cache_scale=1.0, use_pdl=False, err_word=None, stream=None):
+def ckv_fp4_load(kv_cache, loc, out, cache_scale=1.0, use_pdl=True, err_word=None, stream=None):
     """Load rows of the 4-bit cache; see ckv_fp4_load in include/ckv.h.
 
     kv_cache, loc, cache_scale as for ckv_fp4_store; out float32/bf16 [n, D] (last
@@ -719,7 +721,7 @@ def ckv_fp4_attention_workspace(T, B, H, D, max_rows):
 
 
 def ckv_fp4_attention(q, kv_cache, block_table, row_start, ctx_rows, max_rows, softmax_scale, cache_scale=1.0, sink=None,
-                      out=None, lse=None, workspace=None, use_pdl=False, err_word=None, stream=None):
+                      out=None, lse=None, workspace=None, use_pdl=True, err_word=None, stream=None):
     """Attention over the 4-bit cache; see ckv_fp4_attention in include/ckv.h.
 
     q bf16 [T, H, D] (last dim contiguous); kv_cache uint8 [pages, page_size,

@@ -40,8 +40,8 @@ namespace {
 // Warpgroups (4 warps) 0 and 1: softmax; 2: its first warp issues the MMAs; 3 and 4: load and decode.
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 12, kLoadWarps = 8;
 constexpr int kThreads = (kLoadWarp + kLoadWarps) * 32;
-// Registers per thread: 96 at launch (640 x 96 = 61,440), then 256 x 120 + 128 x 64 + 256 x 88 = 61,440.
-constexpr int kSoftRegs = 120, kMmaRegs = 64, kLoadRegs = 88;
+// Registers per thread: 96 at launch (640 x 96 = 61,440), then 256 x 112 + 128 x 64 + 256 x 96 = 61,440.
+constexpr int kSoftRegs = 112, kMmaRegs = 64, kLoadRegs = 96;
 static_assert(256 * kSoftRegs + 128 * kMmaRegs + 256 * kLoadRegs <= kThreads * 96, "registers of the launch");
 template <int D, int R>
 struct Layout {

@@ -21,8 +21,8 @@ namespace {
 // Warpgroups 0 and 1: softmax; 2: its first warp issues the MMAs; 3 and 4: load and decode.
 constexpr int kRowMmaWarp = 8, kRowLoadWarp = 12;
 constexpr int kRowThreads = 640;
-// Registers per thread: 96 at launch (61,440), then 256 x 120 + 128 x 64 + 256 x 88 = 61,440.
-constexpr int kRowSoftRegs = 120, kRowMmaRegs = 64, kRowLoadRegs = 88;
+// Registers per thread: 96 at launch (61,440), then 256 x 112 + 128 x 64 + 256 x 96 = 61,440.
+constexpr int kRowSoftRegs = 112, kRowMmaRegs = 64, kRowLoadRegs = 96;
 static_assert(256 * kRowSoftRegs + 128 * kRowMmaRegs + 256 * kRowLoadRegs <= kRowThreads * 96, "registers of the launch");
 
 template <int D>
@@ -34,7 +34,8 @@ struct RowLayout {
   static constexpr int kTmemO = 0, kTmemS = D, kTmemP = D + kSBufs * 128;  // P: two buffers of 64 columns
   static_assert(kTmemP + 2 * 64 <= 512, "tensor memory");
   static constexpr int kOutPitch = D * 2 + 16;    // output rows on their way out
-  static_assert(128 * kOutPitch <= kRing * kUnitBytes, "output staging");
+  static constexpr int kPartPitch = D * 4 + 16;   // the same of fp32 partials, over the ring and Q
+  static_assert(128 * kPartPitch <= kSmall, "output staging");
 };
 
 struct RowSmall {
@@ -334,12 +335,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           for (int x = 0; x < 32; ++x) o[x] = 0.f;
         }
         if (split) {
-          float* to = ws + (slot * 128 + row) * D + i;
+          uint8_t* to = smem + row * L::kPartPitch + i * 4;
 #pragma unroll
-          for (int x = 0; x < 32; x += 8) {
-            *reinterpret_cast<float4*>(to + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-            *reinterpret_cast<float4*>(to + x + 4) = make_float4(o[x + 4], o[x + 5], o[x + 6], o[x + 7]);
-          }
+          for (int x = 0; x < 32; x += 4) *reinterpret_cast<float4*>(to + x * 4) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
         } else {
           uint8_t* to = smem + row * L::kOutPitch + i * 2;
 #pragma unroll
@@ -349,17 +347,17 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                            pack_bf16x2_rn(o[x + 4] * scale, o[x + 5] * scale), pack_bf16x2_rn(o[x + 6] * scale, o[x + 7] * scale));
         }
       }
-      if (!split) {
-        __syncwarp();  // a warp takes out what it brought: its rows' half
-        constexpr int kPieces = D / 16;  // 16-byte pieces of half a row
+      // a warp takes out what it brought, its rows' half, in 16-byte pieces
+      __syncwarp();
+      const int piece = split ? D / 8 : D / 16, pitch = split ? L::kPartPitch : L::kOutPitch;
+      uint8_t* to = split ? reinterpret_cast<uint8_t*>(ws + slot * 128 * D) : reinterpret_cast<uint8_t*>(a.out);
 #pragma unroll 4
-        for (int i = lane; i < 32 * kPieces; i += 32) {
-          const int r = quad * 32 + i / kPieces, x = half * kPieces + i % kPieces;
-          const int32_t flat = sm.out[r];
-          if (flat >= 0)
-            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(flat) * D + x * 8) =
-                *reinterpret_cast<const uint4*>(smem + r * L::kOutPitch + x * 16);
-        }
+      for (int i = lane; i < 32 * piece; i += 32) {
+        const int r = quad * 32 + i / piece, x = half * piece + i % piece;
+        const int32_t flat = sm.out[r];
+        if (flat >= 0)
+          *reinterpret_cast<uint4*>(to + (static_cast<int64_t>(split ? r : flat) * (2 * piece) + x) * 16) =
+              *reinterpret_cast<const uint4*>(smem + r * pitch + x * 16);
       }
       tc_fence_before();
     }

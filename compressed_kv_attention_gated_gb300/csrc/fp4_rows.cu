@@ -9,6 +9,9 @@
 // quotient lies on the same side of every rounding border as the exact one (a
 // border times scale * g is a float, and the float next to it is off by more
 // than half a step of the quotient): the codes are those of exact arithmetic.
+// The quotients of a block share their divisor: its correctly rounded reciprocal,
+// and per quotient one Newton step on the remainder (Markstein's method: the result
+// is the correctly rounded quotient).
 //
 // Bound by HBM (2-4 bytes in and 9/16 out per channel, or the reverse).  One
 // thread per block of 16 channels: D/16 neighbouring threads write a row's D/2
@@ -65,11 +68,17 @@ __global__ void __launch_bounds__(kRowThreads) fp4_store_kernel(const __grid_con
   const uint32_t sc = __nv_cvt_float_to_fp8(fminf(__fdiv_rn(am, 6.f * a.g), 448.f), __NV_SATFINITE, __NV_E4M3);
   uint32_t lo = 0, hi = 0;
   if (sc != 0) {
-    const float f = e4m3_to_float(sc) * a.g;
+    const float f = e4m3_to_float(sc) * a.g, inv = __frcp_rn(f);
+    // a saturated scale leaves quotients of any size: beyond 8 every one saturates (a NaN becomes finite here)
+    const float most = 8.f * f;
+#pragma unroll
+    for (int i = 0; i < kFp4Block; ++i) {
+      const float y = fminf(fmaxf(x[i], -most), most), q = y * inv;
+      x[i] = copysignf(fmaf(fmaf(-q, f, y), inv, q), y);  // the step turns -0 into 0
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 u = make_float2(__fdiv_rn(x[2 * i], f), __fdiv_rn(x[2 * i + 1], f));
-      const float2 v = make_float2(__fdiv_rn(x[8 + 2 * i], f), __fdiv_rn(x[9 + 2 * i], f));
+      const float2 u = make_float2(x[2 * i], x[2 * i + 1]), v = make_float2(x[8 + 2 * i], x[9 + 2 * i]);
       lo |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(u, __NV_E2M1, cudaRoundNearest)) << (8 * i);
       hi |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest)) << (8 * i);
     }

@@ -29,16 +29,16 @@ namespace {
 
 constexpr int kMapThreads = 1024;
 
-// Block-wide exclusive scan of two 64-bit values per thread.
-struct Pair64 {
-  int64_t a, b;
+// Block-wide exclusive scan of two values per thread.
+struct Pair {
+  uint32_t a, b;
 };
-__device__ __forceinline__ Pair64 block_exclusive_scan(Pair64 v, Pair64* s_warp, Pair64& total) {
+__device__ __forceinline__ Pair block_exclusive_scan(Pair v, Pair* s_warp, Pair& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Pair64 x = v;
+  Pair x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t ya = __shfl_up_sync(0xFFFFFFFFu, x.a, o), yb = __shfl_up_sync(0xFFFFFFFFu, x.b, o);
+    const uint32_t ya = __shfl_up_sync(0xFFFFFFFFu, x.a, o), yb = __shfl_up_sync(0xFFFFFFFFu, x.b, o);
     if (lane >= o) {
       x.a += ya;
       x.b += yb;
@@ -46,25 +46,20 @@ __device__ __forceinline__ Pair64 block_exclusive_scan(Pair64 v, Pair64* s_warp,
   }
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    Pair64 w = s_warp[lane];  // kMapThreads / 32 == 32 warps
+  // every warp scans the 32 warps' totals (kMapThreads / 32 == 32) for itself
+  Pair w = s_warp[lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t ya = __shfl_up_sync(0xFFFFFFFFu, w.a, o), yb = __shfl_up_sync(0xFFFFFFFFu, w.b, o);
-      if (lane >= o) {
-        w.a += ya;
-        w.b += yb;
-      }
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t ya = __shfl_up_sync(0xFFFFFFFFu, w.a, o), yb = __shfl_up_sync(0xFFFFFFFFu, w.b, o);
+    if (lane >= o) {
+      w.a += ya;
+      w.b += yb;
     }
-    s_warp[lane] = w;  // inclusive warp totals
   }
-  __syncthreads();
-  Pair64 before = warp > 0 ? s_warp[warp - 1] : Pair64{0, 0};
-  before.a += x.a - v.a;
-  before.b += x.b - v.b;
-  total = s_warp[31];
-  __syncthreads();
-  return before;
+  total.a = __shfl_sync(0xFFFFFFFFu, w.a, 31);
+  total.b = __shfl_sync(0xFFFFFFFFu, w.b, 31);
+  const uint32_t pa = __shfl_sync(0xFFFFFFFFu, w.a, max(warp - 1, 0)), pb = __shfl_sync(0xFFFFFFFFu, w.b, max(warp - 1, 0));
+  return Pair{(warp > 0 ? pa : 0u) + x.a - v.a, (warp > 0 ? pb : 0u) + x.b - v.b};
 }
 
 // Largest b in [0, B) with pre[b] <= e (pre is non-decreasing, pre[0] = 0).
@@ -84,19 +79,24 @@ __device__ __forceinline__ int32_t next_cursor(int32_t c, int64_t taken, int64_t
   return static_cast<int32_t>(min(c + taken, num_free));
 }
 
+constexpr uint32_t kNarrow = 1u << 21;
+
+template <bool kWide>
 __global__ void __launch_bounds__(kMapThreads) step_maps_kernel(const __grid_constant__ StepMapsArgs a) {
   extern __shared__ __align__(16) int32_t s_maps[];
   int32_t* s_start = s_maps;         // first ragged row [B], clamped to num_tokens
   int32_t* s_first = s_start + a.B;  // position of ragged row 0 if it were the request's: (s - n) - start
   int32_t* s_free = s_first + a.B;   // free-list index of the request's page number 0: c + taken before - pages held
-  __shared__ Pair64 s_warp[32];
+  __shared__ Pair s_warp[2][32];  // by turns: a scan's totals may still be read when the next one begins
 
   pdl_wait();
   const uint32_t P = a.P, ps = a.page_size;
   const int32_t c0 = a.cursor[0];
   const bool lead = blockIdx.x == 0;
   uint32_t flags = 0;
-  Pair64 carry{0, 0};
+  // tokens and pages of the requests so far; 1024 requests are summed in 32 bits at a time
+  int64_t tokens = 0, pages = 0;
+  int turn = 0;
   for (int base = 0; base < a.B; base += kMapThreads) {
     const int b = base + threadIdx.x;
     int32_t n = 0, s = 0, held = 0, need = 0;
@@ -115,27 +115,43 @@ __global__ void __launch_bounds__(kMapThreads) step_maps_kernel(const __grid_con
         held = min(held, need);
       }
     }
-    Pair64 total;
-    const Pair64 at = block_exclusive_scan(Pair64{n, need - held}, s_warp, total);
+    // Counts below 2^21 are summed as they are.  When the call's limits are below that, larger
+    // counts mean "past the limit" wherever they end; else the upper 16 bits go in a scan of their own.
+    const uint32_t take = static_cast<uint32_t>(need - held);
+    Pair total;
+    int64_t before_tokens, before_pages, add_tokens, add_pages;
+    if constexpr (!kWide) {
+      const Pair at = block_exclusive_scan(Pair{min(static_cast<uint32_t>(n), kNarrow), min(take, kNarrow)}, s_warp[turn], total);
+      turn ^= 1;
+      before_tokens = at.a, before_pages = at.b, add_tokens = total.a, add_pages = total.b;
+    } else {
+      const Pair lo = block_exclusive_scan(Pair{n & 0xFFFFu, take & 0xFFFFu}, s_warp[turn], total);
+      turn ^= 1;
+      Pair total_hi;
+      const Pair hi = block_exclusive_scan(Pair{static_cast<uint32_t>(n) >> 16, take >> 16}, s_warp[turn], total_hi);
+      turn ^= 1;
+      before_tokens = lo.a + (static_cast<int64_t>(hi.a) << 16), before_pages = lo.b + (static_cast<int64_t>(hi.b) << 16);
+      add_tokens = total.a + (static_cast<int64_t>(total_hi.a) << 16), add_pages = total.b + (static_cast<int64_t>(total_hi.b) << 16);
+    }
     if (b < a.B) {
-      const int64_t start = min(carry.a + at.a, static_cast<int64_t>(a.num_tokens));
+      const int64_t start = min(tokens + before_tokens, static_cast<int64_t>(a.num_tokens));
       s_start[b] = static_cast<int32_t>(start);
       s_first[b] = static_cast<int32_t>((s - n) - start);
       // clamped: any index at or past num_free is past the list
-      const int64_t f = min(c0 + carry.b + at.b, a.num_free);
+      const int64_t f = min(c0 + pages + before_pages, a.num_free);
       s_free[b] = static_cast<int32_t>(f - held);
       if (lead && a.row_start) a.row_start[b] = static_cast<int32_t>(start);
     }
-    carry.a += total.a;
-    carry.b += total.b;
+    tokens += add_tokens;
+    pages += add_pages;
   }
   __syncthreads();
-  const int32_t live = static_cast<int32_t>(min(carry.a, static_cast<int64_t>(a.num_tokens)));
+  const int32_t live = static_cast<int32_t>(min(tokens, static_cast<int64_t>(a.num_tokens)));
   if (lead && threadIdx.x == 0) {
     if (a.row_start) a.row_start[a.B] = live;
-    if (carry.a > a.num_tokens) flags |= CKV_DEVERR_PLAN;
-    if (carry.b > 0 && (c0 < 0 || c0 + carry.b > a.num_free)) flags |= CKV_DEVERR_PAGES;
-    if (a.cursor_out != a.cursor) a.cursor_out[0] = next_cursor(c0, carry.b, a.num_free);
+    if (tokens > a.num_tokens) flags |= CKV_DEVERR_PLAN;
+    if (pages > 0 && (c0 < 0 || c0 + pages > a.num_free)) flags |= CKV_DEVERR_PAGES;
+    if (a.cursor_out != a.cursor) a.cursor_out[0] = next_cursor(c0, pages, a.num_free);
   }
   if (lead && flags) flag_error(a.err, flags);
   flags = 0;
@@ -202,26 +218,32 @@ __global__ void __launch_bounds__(kMapThreads) step_maps_kernel(const __grid_con
       __threadfence();
       const int32_t arrived = atomicAdd(a.cursor + 1, 1);
       if (arrived == static_cast<int32_t>(gridDim.x) - 1) {
-        a.cursor[0] = next_cursor(c0, carry.b, a.num_free);
+        a.cursor[0] = next_cursor(c0, pages, a.num_free);
         a.cursor[1] = 0;
       }
     }
   }
 }
 
-}  // namespace
-
-cudaError_t launch_step_maps(const StepMapsArgs& a, bool use_pdl, cudaStream_t s) {
+template <bool kWide>
+cudaError_t launch(const StepMapsArgs& a, bool use_pdl, cudaStream_t s) {
   // sized for the largest B the entry point accepts (8192 requests, 96 KB)
-  cudaError_t e = set_max_smem_once<step_maps_kernel>(8192 * 3 * sizeof(int32_t));
+  cudaError_t e = set_max_smem_once<step_maps_kernel<kWide>>(8192 * 3 * sizeof(int32_t));
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int64_t want = (static_cast<int64_t>(a.num_tokens) + kMapThreads - 1) / kMapThreads;
   const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : (want > sms ? sms : want));
-  return launch_ex(step_maps_kernel, dim3(grid), dim3(kMapThreads), static_cast<size_t>(a.B) * 3 * sizeof(int32_t),
-                   use_pdl, s, a);
+  return launch_ex(step_maps_kernel<kWide>, dim3(grid), dim3(kMapThreads), static_cast<size_t>(a.B) * 3 * sizeof(int32_t), use_pdl, s,
+                   a);
+}
+
+}  // namespace
+
+cudaError_t launch_step_maps(const StepMapsArgs& a, bool use_pdl, cudaStream_t s) {
+  const bool narrow = static_cast<uint32_t>(a.num_tokens) < kNarrow && a.num_free < kNarrow;
+  return narrow ? launch<false>(a, use_pdl, s) : launch<true>(a, use_pdl, s);
 }
 
 }  // namespace ckv
