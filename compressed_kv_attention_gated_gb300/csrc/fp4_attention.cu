@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     tmem_alloc<L::kTmem>(&sm.tmem);
     if (lane == 0) {
       for (int i = 0; i < kRing; ++i) {
-        mbar_init(&sm.full[i], kLoadWarps);
+        mbar_init(&sm.full[i], 4);
         mbar_init(&sm.empty[i], 1);
         mbar_init(&sm.a_free[i], 1);
       }

@@ -139,8 +139,9 @@ __device__ __forceinline__ void load_cols(const float* p, float (&v)[n]) {
 // request, 128 at a time and 128 channels at a time, through the ring of units.
 // A unit is two blocks of 128 keys x 64 channels of fp16, 128 bytes per key, with
 // the 128-byte swizzle; with kCopy it also goes to tensor memory (a lane per
-// key, 64 columns, slot c % kSlots from column tmem_k on).
-//   full[c % kRing]    one arrival per warp when unit c is there
+// key, 64 columns, slot c % kSlots from column tmem_k on).  Two groups of 4 warps
+// take units by turns: one's waits and fences lie under the other's decoding.
+//   full[c % kRing]    one arrival per warp of the group (4) when unit c is there
 //   empty[c % kRing]   completed when both products are done with it
 //   a_free[c % kSlots] completed when the first product is done with it (only waited for where
 //                      kSlots < kRing, and there a tile is kRing units: the other waits imply it)
@@ -148,21 +149,23 @@ __device__ __forceinline__ void load_cols(const float* p, float (&v)[n]) {
 // Rows that are not there are zeros.  False when a wait ran out.
 template <int D, bool kCopy, int kSlots>
 __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile& tile, int tid, int k_first, int k_last, int page_shift,
-                                           uint8_t* ring, uint32_t tmem_k, uint64_t* full, uint64_t* empty,
-                                           uint64_t* a_free, uint32_t (*bad)[4]) {
-  constexpr int kUnits = D / 128;
+                                           uint8_t* ring, uint32_t tmem_k, uint64_t* full, uint64_t* empty, uint64_t* a_free,
+                                           uint32_t (*bad)[4]) {
+  constexpr int kUnits = D / 128, kGroups = 2;
+  constexpr int kDeep = kRing / kGroups;  // units of a group in registers: loads run this far ahead
   static_assert(kSlots == kRing || kUnits == kRing, "waits");
-  // a thread has 64 channels of a unit's 128 for one key, that of its lane of tensor memory;
-  // neighbouring lanes have neighbouring keys, whose 16-byte chunks the swizzle spreads over all banks
-  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, key = quad * 32 + lane, part = tid >> 7;
+  // a thread has one key's 128 channels of a unit, that of its lane of tensor memory; neighbouring
+  // lanes have neighbouring keys, whose 16-byte chunks the swizzle spreads over all banks
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, key = quad * 32 + lane, group = tid >> 7;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const int32_t* table = a.table + static_cast<int64_t>(tile.b) * a.table_stride;
   const int64_t page_bytes = fp4_page_bytes<D>(a.page_size);
   struct Unit {
-    uint4 c[2];  // 64 codes
-    uint32_t s;  // 4 scales
+    uint4 c[4];  // 128 codes
+    uint2 s;     // 8 scales
+    uint32_t gone;
   };
-  Unit reg[kRing];
+  Unit reg[kDeep];
   const uint8_t *codes = nullptr, *scales = nullptr;
   bool there = false;
   uint32_t gone = 0;  // the warp's keys without a page
@@ -177,77 +180,71 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
       const int32_t page = table[pg];
       if (page >= 0 && page < a.num_pages) {
         const uint8_t* p = a.cache + page * page_bytes;
-        codes = p + static_cast<int64_t>(row) * (D / 2) + part * 32;
-        scales = p + static_cast<int64_t>(a.page_size) * (D / 2) + static_cast<int64_t>(row) * (D / 16) + part * 4;
+        codes = p + static_cast<int64_t>(row) * (D / 2);
+        scales = p + static_cast<int64_t>(a.page_size) * (D / 2) + static_cast<int64_t>(row) * (D / 16);
         there = true;
       } else {
         missing = true;
-        if (part == 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
+        flag_error(a.err, CKV_DEVERR_CACHE_LOC);
       }
     }
     gone = __ballot_sync(0xFFFFFFFFu, missing);
   };
-  auto load = [&](Unit& x, int u) {
-    x.s = there ? *reinterpret_cast<const uint32_t*>(scales + u * 8) : 0u;
+  const int total = k_last > k_first ? (k_last - k_first + kKeys - 1) / kKeys * kUnits : 0;
+  auto fetch = [&](Unit& x, int c) {
+    if (c < total) {
+      // the group's first unit of a tile
+      if (kUnits <= kGroups || c % kUnits == group) locate(c / kUnits);
+      const int u = c % kUnits;
+      x.gone = gone;
+      x.s = make_uint2(0, 0);
+      if (there) x.s = *reinterpret_cast<const uint2*>(scales + u * 8);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      x.c[i] = make_uint4(0, 0, 0, 0);
-      if (there) x.c[i] = *reinterpret_cast<const uint4*>(codes + u * 64 + i * 16);
+      for (int i = 0; i < 4; ++i) {
+        x.c[i] = make_uint4(0, 0, 0, 0);
+        if (there) x.c[i] = *reinterpret_cast<const uint4*>(codes + u * 64 + i * 16);
+      }
     }
   };
-  const int total = k_last > k_first ? (k_last - k_first + kKeys - 1) / kKeys * kUnits : 0;
-  uint32_t was_gone[kRing / kUnits > 0 ? kRing / kUnits : 1];
 #pragma unroll
-  for (int c = 0; c < kRing; ++c) {
-    if (c < total) {
-      if (c % kUnits == 0) {
-        locate(c / kUnits);
-        was_gone[c / kUnits] = gone;
-      }
-      load(reg[c], c % kUnits);
-    }
-  }
+  for (int i = 0; i < kDeep; ++i) fetch(reg[i], group + i * kGroups);
   bool ok = true;
 #pragma unroll 1
-  for (int c0 = 0; c0 < total && ok; c0 += kRing) {
+  for (int c0 = group; c0 < total && ok; c0 += kRing) {
 #pragma unroll
-    for (int i = 0; i < kRing; ++i) {
-      const int c = c0 + i;
+    for (int i = 0; i < kDeep; ++i) {
+      const int c = c0 + i * kGroups, slot = group + i * kGroups;
       if (c < total && ok) {
         // the ring's last unit in this place has served both products
-        if (c >= kRing) ok = mbar_wait_near(&empty[i], ((c / kRing) - 1) & 1);
-        if (kCopy && kSlots < kRing && i >= kSlots) ok = ok && mbar_wait_near(&a_free[c % kSlots], ((c / kSlots) - 1) & 1);
+        if (c >= kRing) ok = mbar_wait_near(&empty[slot], ((c / kRing) - 1) & 1);
+        if (kCopy && kSlots < kRing && slot >= kSlots) ok = ok && mbar_wait_near(&a_free[c % kSlots], ((c / kSlots) - 1) & 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (ok) {
           if (kCopy) tc_fence_after();
-          uint8_t* unit = ring + i * kUnitBytes + part * 16384 + key * 128;
-          const uint32_t a_tile = tmem_k + lanes + (c % kSlots) * 64 + part * 32;
-          __half2 sc[4];
-          decode_scales(reg[i].s, sc);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {  // blocks of 16 channels
-            const uint4 x = reg[i].c[b / 2];
-            const uint4 lo = decode8(b & 1 ? x.z : x.x, sc[b]), hi = decode8(b & 1 ? x.w : x.y, sc[b]);
-            *reinterpret_cast<uint4*>(unit + (((2 * b) ^ (key & 7)) * 16)) = lo;
-            *reinterpret_cast<uint4*>(unit + (((2 * b + 1) ^ (key & 7)) * 16)) = hi;
-            if (kCopy) tmem_st8(a_tile + b * 8, lo, hi);
+          for (int p = 0; p < 2; ++p) {  // blocks of 64 channels
+            uint8_t* unit = ring + slot * kUnitBytes + p * 16384 + key * 128;
+            const uint32_t a_tile = tmem_k + lanes + (c % kSlots) * 64 + p * 32;
+            __half2 sc[4];
+            decode_scales(p ? reg[i].s.y : reg[i].s.x, sc);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {  // blocks of 16 channels
+              const uint4 x = reg[i].c[p * 2 + b / 2];
+              const uint4 lo = decode8(b & 1 ? x.z : x.x, sc[b]), hi = decode8(b & 1 ? x.w : x.y, sc[b]);
+              *reinterpret_cast<uint4*>(unit + (((2 * b) ^ (key & 7)) * 16)) = lo;
+              *reinterpret_cast<uint4*>(unit + (((2 * b + 1) ^ (key & 7)) * 16)) = hi;
+              if (kCopy) tmem_st8(a_tile + b * 8, lo, hi);
+            }
           }
-          if (i % kUnits == 0 && part == 0 && lane == 0) bad[(c / kUnits) & 3][quad] = was_gone[i / kUnits];
+          if (c % kUnits == 0 && lane == 0) bad[(c / kUnits) & 3][quad] = reg[i].gone;
           if (kCopy) {
             tc_wait_st();
             tc_fence_before();
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[i]);
-          const int next = c + kRing;
-          if (next < total) {
-            if (i % kUnits == 0) {
-              locate(next / kUnits);
-              was_gone[i / kUnits] = gone;
-            }
-            load(reg[i], i % kUnits);
-          }
+          if (lane == 0) mbar_arrive(&full[slot]);
+          fetch(reg[i], c + kRing);
         }
       }
     }

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     tmem_alloc<512>(&sm.tmem);
     if (lane == 0) {
       for (int i = 0; i < kRing; ++i) {
-        mbar_init(&sm.full[i], 8);
+        mbar_init(&sm.full[i], 4);
         mbar_init(&sm.empty[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
