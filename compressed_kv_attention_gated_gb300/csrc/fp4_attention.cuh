@@ -14,6 +14,7 @@
 
 namespace ckv {
 
+constexpr int kSMs = 152;        // of a GB300
 constexpr int kKeys = 128;       // cache rows per tile
 constexpr int kRing = 4;         // units of 128 keys x 128 channels
 constexpr int kUnitBytes = 32768;
