@@ -8,9 +8,10 @@
 // both products on the tensor cores with the cache rows as the M side:
 //   S^T [128 keys x R]     = K [128 x D] Q^T [D x R]
 //   O^T [D channels x R]  += K^T [D x 128] P^T [128 x R]
-// so one decoded tile of K in shared memory (fp16, 128-byte swizzle) serves as
-// A of both, K-major for the first and MN-major for the second, M is always 128
-// whatever the number of heads, and O (D x R) fits tensor memory.
+// so that M is always 128 whatever the number of heads, and O (D x R) fits tensor
+// memory.  A cache row is decoded once, to fp16, into tensor memory (a lane per key,
+// A of the first product) and into shared memory (128-byte swizzle, MN-major A of
+// the second); P goes through shared memory as an MN-major B.
 //
 // Exactness: a decoded value is code * scale (2 + 4 significant bits, 2^-10 ..
 // 2688), exact in fp16; cache_scale goes into the factor of the scores and of
@@ -26,12 +27,24 @@
 // the sums.  Sums stay per thread until the end.
 //
 // Roles: 8 softmax warps (also query load and output), 1 warp that issues the
-// MMAs, 8 warps that load and decode cache rows into a ring of four units of
-// 128 keys x 128 channels.  With D < 512 the ring holds more than a tile, and
-// the scores of the next tile are computed under the softmax of this one.
+// MMAs, 1 that brings the next CTA's first bytes to L2, 8 warps that load and
+// decode cache rows into a ring of four units of 128 keys x 128 channels.  With
+// D < 512 the ring holds more than a tile, and the scores of the next tile are
+// computed under the softmax of this one.
 //
 // Long rows of few tiles are split over CTAs (blockIdx.y), whose partial
 // outputs (fp32) and references a second kernel joins in a fixed order.
+//
+// What bounds it (D = 512, R = 64, 128 keys, in clocks): softmax 1.6 k, then the
+// second product 2.0 k and under it the decoding of the next tile as its units
+// come free, and the first product's tail, 3 k more; the products read 256 KB of
+// shared memory per tile and the decoding writes 128 KB (3.1 k at 128 bytes per
+// clock).  Around its tiles a CTA spends about 20 k clocks (queries, first
+// decoding, output), which one CTA per SM cannot hide.  Measured (GB300): 1024
+// requests x 64 heads x 512 rows on average 239 us (290 TFLOP/s), a prompt of
+// 8750 tokens x 64 heads over 200-1024 rows 1.70 ms (410 TFLOP/s).
+// Slower forms: K as A of both products from shared memory (1.80 ms), decoding
+// twice so that the scores run ahead of the second product (2.21 ms).
 #include "fp4_attention.cuh"
 
 namespace ckv {
@@ -235,323 +248,323 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     if (!idle) {
-    // ------------------------------------------------------------- softmax
-    const int quad = warp & 3, half = warp >> 2;
-    const int col0 = half * L::kCols;
-    // queries: a warp takes R/8 rows, a lane eight channels of a row (16 at D = 512); all
-    // loads are issued before the first is used
-    if (n > 0) {
-      constexpr int kC = D == 512 ? 16 : 8;     // channels of a lane
-      constexpr int kSpan = D / kC;             // lanes of a row
-      constexpr int kLoads = R / kSoftWarps * kSpan / 32;
-      constexpr int kBatch = kLoads < 8 ? kLoads : 8;  // rows in flight (registers)
-      const int sub = lane / kSpan, ch = lane % kSpan * kC;
-      static_assert(kLoads >= 1 && kLoads % kBatch == 0, "");
+      // ------------------------------------------------------------- softmax
+      const int quad = warp & 3, half = warp >> 2;
+      const int col0 = half * L::kCols;
+      // queries: a warp takes R/8 rows, a lane eight channels of a row (16 at D = 512); all
+      // loads are issued before the first is used
+      if (n > 0) {
+        constexpr int kC = D == 512 ? 16 : 8;     // channels of a lane
+        constexpr int kSpan = D / kC;             // lanes of a row
+        constexpr int kLoads = R / kSoftWarps * kSpan / 32;
+        constexpr int kBatch = kLoads < 8 ? kLoads : 8;  // rows in flight (registers)
+        const int sub = lane / kSpan, ch = lane % kSpan * kC;
+        static_assert(kLoads >= 1 && kLoads % kBatch == 0, "");
 #pragma unroll 1
-      for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
-      uint4 raw[kBatch][kC / 8];
+        for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
+          uint4 raw[kBatch][kC / 8];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = warp * (R / kSoftWarps) + (i0 + i) * (32 / kSpan) + sub;
-        const bool on = sm.out[r] >= 0;
-        const uint4* q = reinterpret_cast<const uint4*>(a.q + sm.q[r] + ch);
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = warp * (R / kSoftWarps) + (i0 + i) * (32 / kSpan) + sub;
+            const bool on = sm.out[r] >= 0;
+            const uint4* q = reinterpret_cast<const uint4*>(a.q + sm.q[r] + ch);
 #pragma unroll
-        for (int x = 0; x < kC / 8; ++x) raw[i][x] = on ? q[x] : make_uint4(0, 0, 0, 0);
-      }
-uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        am[i] = 0;
-#pragma unroll
-        for (int x = 0; x < kC / 8; ++x) {
-          const uint32_t w[4] = {raw[i][x].x, raw[i][x].y, raw[i][x].z, raw[i][x].w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) am[i] = max(am[i], max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
-        }
-      }
-#pragma unroll
-      for (int o = 1; o < kSpan; o <<= 1) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) am[i] = max(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = warp * (R / kSoftWarps) + (i0 + i) * (32 / kSpan) + sub;
-        const int se = query_exponent(am[i]);
-        const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
-        if (lane % kSpan == 0)
-          sm.c[r] = a.softmax_scale * kLog2e * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
-        uint8_t* row = smem + L::kQ + (ch / 64) * (R * 128) + r * 128;
-#pragma unroll
-        for (int x = 0; x < kC / 8; ++x)
-          *reinterpret_cast<uint4*>(row + ((((ch % 64) / 8 + x) ^ (r & 7)) * 16)) = query8(raw[i][x], up);
-      }
-      }
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.q_full);
-    soft_barrier();  // every row's factor is there
-
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    float l[L::kCols];
-#pragma unroll
-    for (int i = 0; i < L::kCols; ++i) l[i] = 0.f;
-    bool ok = true;
-#pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      const int buf = L::kAhead ? j & 1 : 0;
-      const int key = k_first + j * kKeys + quad * 32 + lane;
-      const int unit0 = j * L::kUnits;
-      // the decoding warps' note on missing keys, then the scores
-      ok = mbar_wait_near(&sm.full[unit0 % kRing], (unit0 / kRing) & 1) && mbar_wait_near(&sm.s_full[j & 1], (j >> 1) & 1);
-      if (!ok) atomicExch(&sm.abort, 1);
-      __syncwarp();
-      tc_fence_after();
-      const bool gone = (sm.bad[j & 3][quad] >> lane) & 1;
-      const bool masks = gone || key - lane + 32 > ctx_min;
-      const uint32_t at_s = tmem + lanes + L::kTmemS + buf * R + col0;
-      // scores in log2 units, -infinity for keys that a row does not see
-      auto read_scores = [&](float (&z)[L::kCols]) {
-        tmem_ld<L::kCols>(at_s, z);
-#pragma unroll
-        for (int i = 0; i < L::kCols; i += 4) {
-          const float4 c = *reinterpret_cast<const float4*>(&sm.c[col0 + i]);
-          z[i] *= c.x, z[i + 1] *= c.y, z[i + 2] *= c.z, z[i + 3] *= c.w;
-        }
-        if (masks) {
-#pragma unroll
-          for (int i = 0; i < L::kCols; i += 4) {
-            const int4 x = *reinterpret_cast<const int4*>(&sm.ctx[col0 + i]);
-            z[i] = !gone && key < x.x ? z[i] : -INFINITY;
-            z[i + 1] = !gone && key < x.y ? z[i + 1] : -INFINITY;
-            z[i + 2] = !gone && key < x.z ? z[i + 2] : -INFINITY;
-            z[i + 3] = !gone && key < x.w ? z[i + 3] : -INFINITY;
+            for (int x = 0; x < kC / 8; ++x) raw[i][x] = on ? q[x] : make_uint4(0, 0, 0, 0);
           }
-        }
-      };
-      auto over_refs = [&](float (&z)[L::kCols]) {
-        float over = -INFINITY;
+          uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
 #pragma unroll
-        for (int i = 0; i < L::kCols; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sm.ref[col0 + i]);
-          z[i] -= f.x, z[i + 1] -= f.y, z[i + 2] -= f.z, z[i + 3] -= f.w;
-          over = fmaxf(over, fmaxf(fmaxf(z[i], z[i + 1]), fmaxf(z[i + 2], z[i + 3])));
-        }
-        return over;
-      };
-      float z[L::kCols];
-      read_scores(z);
-      const float over = over_refs(z);
-      ok = ok && *reinterpret_cast<volatile int32_t*>(&sm.abort) == 0;
-      if (soft_any(over > kJump || !ok)) {
-        ok = !soft_any(!ok);
-        if (!ok) break;
-        // new references: the largest score so far of each row
-        read_scores(z);
-        const float top = reduce_columns<L::kCols, true>(z, lane);
-        constexpr int kShare = 32 / L::kCols;  // lanes that hold the same row's result
-        if (lane % kShare == 0) sm.part[quad][col0 + lane / kShare] = top;
-        soft_barrier();
-        if (threadIdx.x < R) {
-          const int r = threadIdx.x;
-          const float old = sm.ref[r];
-          const float now = fmaxf(fmaxf(fmaxf(sm.part[0][r], sm.part[1][r]), fmaxf(sm.part[2][r], sm.part[3][r])), old);
-          sm.keep[r] = fast_exp2(old - now);
-          sm.ref[r] = now;
-        }
-        soft_barrier();
-        if (j > 0) {
-          load_cols<L::kCols>(&sm.keep[col0], z);
+          for (int i = 0; i < kBatch; ++i) {
+            am[i] = 0;
 #pragma unroll
-          for (int i = 0; i < L::kCols; ++i) l[i] *= z[i];
-          ok = mbar_wait_near(&sm.o_done, (j - 1) & 1);
-          if (!ok) atomicExch(&sm.abort, 1);
-          __syncwarp();
-          tc_fence_after();
-#pragma unroll 1
-          for (int u = 0; u < L::kUnits; ++u) {
+            for (int x = 0; x < kC / 8; ++x) {
+              const uint32_t w[4] = {raw[i][x].x, raw[i][x].y, raw[i][x].z, raw[i][x].w};
 #pragma unroll
-            for (int i = 0; i < L::kCols; i += 8) {
-              float o[8];
-              const uint32_t at = tmem + lanes + L::kTmemO + u * R + col0 + i;
-              tmem_ld<8>(at, o);
-#pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] *= z[i + x];
-              tmem_st8(at, o);
+              for (int y = 0; y < 4; ++y) am[i] = max(am[i], max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
             }
           }
-          tc_wait_st();
-        }
-        read_scores(z);
-        over_refs(z);
-      }
-      // weights, rounded to fp16, as row `key` of P
-      uint8_t* row = smem + L::kP + buf * (kKeys * 128) + (quad * 32 + lane) * 128;
 #pragma unroll
-      for (int i = 0; i < L::kCols; i += 8) {
-        uint32_t w[4];
+          for (int o = 1; o < kSpan; o <<= 1) {
 #pragma unroll
-        for (int x = 0; x < 8; x += 2) {
-          const float p0 = fast_exp2(z[i + x]), p1 = fast_exp2(z[i + x + 1]);
-          l[i + x] += p0;
-          l[i + x + 1] += p1;
-          const __half2 h = __floats2half2_rn(p0, p1);
-          w[x / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int i = 0; i < kBatch; ++i) am[i] = max(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = warp * (R / kSoftWarps) + (i0 + i) * (32 / kSpan) + sub;
+            const int se = query_exponent(am[i]);
+            const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
+            if (lane % kSpan == 0)
+              sm.c[r] = a.softmax_scale * kLog2e * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
+            uint8_t* row = smem + L::kQ + (ch / 64) * (R * 128) + r * 128;
+#pragma unroll
+            for (int x = 0; x < kC / 8; ++x)
+              *reinterpret_cast<uint4*>(row + ((((ch % 64) / 8 + x) ^ (r & 7)) * 16)) = query8(raw[i][x], up);
+          }
         }
-        *reinterpret_cast<uint4*>(row + ((((col0 + i) / 8) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       fence_proxy_async_smem();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[j & 1]);
-    }
-    // --------------------------------------------------------------- output
-    if (n > 0 && ok) {
-      // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's
-      ok = mbar_wait_near(&sm.drain, 0);
-      __syncwarp();
-      tc_fence_after();
-    }
-    if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
-    const float sum = reduce_columns<L::kCols, false>(l, lane);
-    constexpr int kShare = 32 / L::kCols;
-    soft_barrier();
-    if (lane % kShare == 0) sm.part[quad][col0 + lane / kShare] = sum;
-    soft_barrier();
-    float* ws = static_cast<float*>(a.workspace);
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y;
-    if (threadIdx.x < R) {
-      const int r = threadIdx.x;
-      const float total = sm.part[0][r] + sm.part[1][r] + sm.part[2][r] + sm.part[3][r];
-      const int32_t flat = sm.out[r];
-      if (split) {
-        float* ml = ws + static_cast<int64_t>(gridDim.x) * gridDim.y * R * D + slot * R * 2;
-        ml[r] = sm.ref[r];
-        ml[R + r] = total;
-      } else {
-        float m = sm.ref[r], all = total;
-        if (a.sink) {
-          const float s = sm.sink[r];
-          const float top = fmaxf(m, s);
-          const float keep = fast_exp2(m - top);  // 0 where no key was seen
-          all = (total == 0.f ? 0.f : total * keep) + (s == top ? 1.f : fast_exp2(s - top));
-          sm.c[r] = all == 0.f ? 0.f : keep * a.g / all;
-          m = top;
-        } else {
-          sm.c[r] = all == 0.f ? 0.f : a.g / all;
-        }
-        if (a.lse && flat >= 0) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
-      }
-    }
-    soft_barrier();
-    load_cols<L::kCols>(&sm.c[col0], l);
+      if (lane == 0) mbar_arrive(&sm.q_full);
+      soft_barrier();  // every row's factor is there
+
+      const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+      float l[L::kCols];
+#pragma unroll
+      for (int i = 0; i < L::kCols; ++i) l[i] = 0.f;
+      bool ok = true;
 #pragma unroll 1
-    for (int u = 0; u < L::kUnits; ++u) {
-      float o[L::kCols];
-      if (n > 0) {
-        tmem_ld<L::kCols>(tmem + lanes + L::kTmemO + u * R + col0, o);
-      } else {
+      for (int j = 0; j < n; ++j) {
+        const int buf = L::kAhead ? j & 1 : 0;
+        const int key = k_first + j * kKeys + quad * 32 + lane;
+        const int unit0 = j * L::kUnits;
+        // the decoding warps' note on missing keys, then the scores
+        ok = mbar_wait_near(&sm.full[unit0 % kRing], (unit0 / kRing) & 1) && mbar_wait_near(&sm.s_full[j & 1], (j >> 1) & 1);
+        if (!ok) atomicExch(&sm.abort, 1);
+        __syncwarp();
+        tc_fence_after();
+        const bool gone = (sm.bad[j & 3][quad] >> lane) & 1;
+        const bool masks = gone || key - lane + 32 > ctx_min;
+        const uint32_t at_s = tmem + lanes + L::kTmemS + buf * R + col0;
+        // scores in log2 units, -infinity for keys that a row does not see
+        auto read_scores = [&](float (&z)[L::kCols]) {
+          tmem_ld<L::kCols>(at_s, z);
 #pragma unroll
-        for (int i = 0; i < L::kCols; ++i) o[i] = 0.f;
+          for (int i = 0; i < L::kCols; i += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(&sm.c[col0 + i]);
+            z[i] *= c.x, z[i + 1] *= c.y, z[i + 2] *= c.z, z[i + 3] *= c.w;
+          }
+          if (masks) {
+#pragma unroll
+            for (int i = 0; i < L::kCols; i += 4) {
+              const int4 x = *reinterpret_cast<const int4*>(&sm.ctx[col0 + i]);
+              z[i] = !gone && key < x.x ? z[i] : -INFINITY;
+              z[i + 1] = !gone && key < x.y ? z[i + 1] : -INFINITY;
+              z[i + 2] = !gone && key < x.z ? z[i + 2] : -INFINITY;
+              z[i + 3] = !gone && key < x.w ? z[i + 3] : -INFINITY;
+            }
+          }
+        };
+        auto over_refs = [&](float (&z)[L::kCols]) {
+          float over = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < L::kCols; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&sm.ref[col0 + i]);
+            z[i] -= f.x, z[i + 1] -= f.y, z[i + 2] -= f.z, z[i + 3] -= f.w;
+            over = fmaxf(over, fmaxf(fmaxf(z[i], z[i + 1]), fmaxf(z[i + 2], z[i + 3])));
+          }
+          return over;
+        };
+        float z[L::kCols];
+        read_scores(z);
+        const float over = over_refs(z);
+        ok = ok && *reinterpret_cast<volatile int32_t*>(&sm.abort) == 0;
+        if (soft_any(over > kJump || !ok)) {
+          ok = !soft_any(!ok);
+          if (!ok) break;
+          // new references: the largest score so far of each row
+          read_scores(z);
+          const float top = reduce_columns<L::kCols, true>(z, lane);
+          constexpr int kShare = 32 / L::kCols;  // lanes that hold the same row's result
+          if (lane % kShare == 0) sm.part[quad][col0 + lane / kShare] = top;
+          soft_barrier();
+          if (threadIdx.x < R) {
+            const int r = threadIdx.x;
+            const float old = sm.ref[r];
+            const float now = fmaxf(fmaxf(fmaxf(sm.part[0][r], sm.part[1][r]), fmaxf(sm.part[2][r], sm.part[3][r])), old);
+            sm.keep[r] = fast_exp2(old - now);
+            sm.ref[r] = now;
+          }
+          soft_barrier();
+          if (j > 0) {
+            load_cols<L::kCols>(&sm.keep[col0], z);
+#pragma unroll
+            for (int i = 0; i < L::kCols; ++i) l[i] *= z[i];
+            ok = mbar_wait_near(&sm.o_done, (j - 1) & 1);
+            if (!ok) atomicExch(&sm.abort, 1);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int u = 0; u < L::kUnits; ++u) {
+#pragma unroll
+              for (int i = 0; i < L::kCols; i += 8) {
+                float o[8];
+                const uint32_t at = tmem + lanes + L::kTmemO + u * R + col0 + i;
+                tmem_ld<8>(at, o);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) o[x] *= z[i + x];
+                tmem_st8(at, o);
+              }
+            }
+            tc_wait_st();
+          }
+          read_scores(z);
+          over_refs(z);
+        }
+        // weights, rounded to fp16, as row `key` of P
+        uint8_t* row = smem + L::kP + buf * (kKeys * 128) + (quad * 32 + lane) * 128;
+#pragma unroll
+        for (int i = 0; i < L::kCols; i += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 8; x += 2) {
+            const float p0 = fast_exp2(z[i + x]), p1 = fast_exp2(z[i + x + 1]);
+            l[i + x] += p0;
+            l[i + x + 1] += p1;
+            const __half2 h = __floats2half2_rn(p0, p1);
+            w[x / 2] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          *reinterpret_cast<uint4*>(row + ((((col0 + i) / 8) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[j & 1]);
       }
-      const int ch = u * 128 + quad * 32 + lane;
-      if (split) {
-#pragma unroll
-        for (int i = 0; i < L::kCols; ++i) ws[(slot * R + col0 + i) * D + ch] = o[i];
-      } else {
-        // through shared memory (the ring is free) so that rows leave in 16-byte pieces; neighbouring
-        // lanes (channels) trade halves: the even one has both channels of row i, the odd one of row i + 1
-        const bool odd = lane & 1;
-        uint8_t* to = smem + (col0 + (odd ? 1 : 0)) * L::kOutPitch + (ch & ~1) * 2;
-#pragma unroll
-        for (int i = 0; i < L::kCols; i += 2) {
-          const float v0 = o[i] * l[i], v1 = o[i + 1] * l[i + 1];
-          const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
-          *reinterpret_cast<uint32_t*>(to + i * L::kOutPitch) = odd ? pack_bf16x2_rn(got, v1) : pack_bf16x2_rn(v0, got);
+      // --------------------------------------------------------------- output
+      if (n > 0 && ok) {
+        // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's
+        ok = mbar_wait_near(&sm.drain, 0);
+        __syncwarp();
+        tc_fence_after();
+      }
+      if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+      const float sum = reduce_columns<L::kCols, false>(l, lane);
+      constexpr int kShare = 32 / L::kCols;
+      soft_barrier();
+      if (lane % kShare == 0) sm.part[quad][col0 + lane / kShare] = sum;
+      soft_barrier();
+      float* ws = static_cast<float*>(a.workspace);
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y;
+      if (threadIdx.x < R) {
+        const int r = threadIdx.x;
+        const float total = sm.part[0][r] + sm.part[1][r] + sm.part[2][r] + sm.part[3][r];
+        const int32_t flat = sm.out[r];
+        if (split) {
+          float* ml = ws + static_cast<int64_t>(gridDim.x) * gridDim.y * R * D + slot * R * 2;
+          ml[r] = sm.ref[r];
+          ml[R + r] = total;
+        } else {
+          float m = sm.ref[r], all = total;
+          if (a.sink) {
+            const float s = sm.sink[r];
+            const float top = fmaxf(m, s);
+            const float keep = fast_exp2(m - top);  // 0 where no key was seen
+            all = (total == 0.f ? 0.f : total * keep) + (s == top ? 1.f : fast_exp2(s - top));
+            sm.c[r] = all == 0.f ? 0.f : keep * a.g / all;
+            m = top;
+          } else {
+            sm.c[r] = all == 0.f ? 0.f : a.g / all;
+          }
+          if (a.lse && flat >= 0) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
         }
       }
-    }
-    if (!split) {
       soft_barrier();
-      constexpr int kRowLanes = D / 8;  // 16-byte pieces of a row
-#pragma unroll 4
-      for (int i = threadIdx.x; i < R * kRowLanes; i += kSoftWarps * 32) {
-        const int r = i / kRowLanes, x = i % kRowLanes;
-        const int32_t flat = sm.out[r];
-        if (flat >= 0)
-          *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(flat) * D + x * 8) =
-              *reinterpret_cast<const uint4*>(smem + r * L::kOutPitch + x * 16);
+      load_cols<L::kCols>(&sm.c[col0], l);
+#pragma unroll 1
+      for (int u = 0; u < L::kUnits; ++u) {
+        float o[L::kCols];
+        if (n > 0) {
+          tmem_ld<L::kCols>(tmem + lanes + L::kTmemO + u * R + col0, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < L::kCols; ++i) o[i] = 0.f;
+        }
+        const int ch = u * 128 + quad * 32 + lane;
+        if (split) {
+#pragma unroll
+          for (int i = 0; i < L::kCols; ++i) ws[(slot * R + col0 + i) * D + ch] = o[i];
+        } else {
+          // through shared memory (the ring is free) so that rows leave in 16-byte pieces; neighbouring
+          // lanes (channels) trade halves: the even one has both channels of row i, the odd one of row i + 1
+          const bool odd = lane & 1;
+          uint8_t* to = smem + (col0 + (odd ? 1 : 0)) * L::kOutPitch + (ch & ~1) * 2;
+#pragma unroll
+          for (int i = 0; i < L::kCols; i += 2) {
+            const float v0 = o[i] * l[i], v1 = o[i + 1] * l[i + 1];
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+            *reinterpret_cast<uint32_t*>(to + i * L::kOutPitch) = odd ? pack_bf16x2_rn(got, v1) : pack_bf16x2_rn(v0, got);
+          }
+        }
       }
-    }
-    tc_fence_before();
+      if (!split) {
+        soft_barrier();
+        constexpr int kRowLanes = D / 8;  // 16-byte pieces of a row
+#pragma unroll 4
+        for (int i = threadIdx.x; i < R * kRowLanes; i += kSoftWarps * 32) {
+          const int r = i / kRowLanes, x = i % kRowLanes;
+          const int32_t flat = sm.out[r];
+          if (flat >= 0)
+            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(flat) * D + x * 8) =
+                *reinterpret_cast<const uint4*>(smem + r * L::kOutPitch + x * 16);
+        }
+      }
+      tc_fence_before();
     }
   } else if (warp < kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
     if (warp == kMmaWarp && n > 0) {
-    // ------------------------------------------------------------ tensor cores
-    if (elect_one()) {
-      constexpr uint32_t kIdescS = idesc_f16(R, false, false), kIdescO = idesc_f16(R, true, true);
-      const uint32_t base = smem_u32(smem);
-      bool ok = mbar_wait_near(&sm.q_full, 0);
-      auto scores = [&](int j) {
-        const uint32_t d = tmem + L::kTmemS + (L::kAhead ? j & 1 : 0) * R;
-        for (int u = 0; u < L::kUnits && ok; ++u) {
-          const int c = j * L::kUnits + u;
-          ok = mbar_wait_near(&sm.full[c % kRing], (c / kRing) & 1);
+      // ------------------------------------------------------------ tensor cores
+      if (elect_one()) {
+        constexpr uint32_t kIdescS = idesc_f16(R, false, false), kIdescO = idesc_f16(R, true, true);
+        const uint32_t base = smem_u32(smem);
+        bool ok = mbar_wait_near(&sm.q_full, 0);
+        auto scores = [&](int j) {
+          const uint32_t d = tmem + L::kTmemS + (L::kAhead ? j & 1 : 0) * R;
+          for (int u = 0; u < L::kUnits && ok; ++u) {
+            const int c = j * L::kUnits + u;
+            ok = mbar_wait_near(&sm.full[c % kRing], (c / kRing) & 1);
+            tc_fence_after();
+            if (!ok) break;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+              const uint64_t db = smem_desc_sw128(base + L::kQ + (u * 2 + s / 4) * (R * 128) + (s % 4) * 32, 16, 1024);
+              mma_f16_ts(d, tmem + L::kTmemK + (c % L::kSlots) * 64 + s * 8, db, kIdescS, u > 0 || s > 0);
+            }
+            tc_commit(&sm.a_free[c % L::kSlots]);
+          }
+          tc_commit(&sm.s_full[j & 1]);
+        };
+        if (ok) scores(0);
+        for (int j = 0; j < n && ok; ++j) {
+          if (L::kAhead && j + 1 < n) scores(j + 1);
+          ok = ok && mbar_wait_near(&sm.p_full[j & 1], (j >> 1) & 1);
           tc_fence_after();
           if (!ok) break;
+          const uint32_t p = base + L::kP + (L::kAhead ? j & 1 : 0) * (kKeys * 128);
+          for (int u = 0; u < L::kUnits; ++u) {
+            const int c = j * L::kUnits + u;
 #pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            const uint64_t db = smem_desc_sw128(base + L::kQ + (u * 2 + s / 4) * (R * 128) + (s % 4) * 32, 16, 1024);
-            mma_f16_ts(d, tmem + L::kTmemK + (c % L::kSlots) * 64 + s * 8, db, kIdescS, u > 0 || s > 0);
+            for (int s = 0; s < 8; ++s) {
+              const uint64_t da = smem_desc_sw128(base + (c % kRing) * kUnitBytes + s * 2048, 16384, 1024);
+              const uint64_t db = smem_desc_sw128(p + s * 2048, 16384, 1024);
+              mma_f16_ss(tmem + L::kTmemO + u * R, da, db, kIdescO, j > 0 || s > 0);
+            }
+            tc_commit(&sm.empty[c % kRing]);
           }
-          tc_commit(&sm.a_free[c % L::kSlots]);
+          tc_commit(&sm.o_done);
+          if (!L::kAhead && j + 1 < n) scores(j + 1);
         }
-        tc_commit(&sm.s_full[j & 1]);
-      };
-      if (ok) scores(0);
-      for (int j = 0; j < n && ok; ++j) {
-        if (L::kAhead && j + 1 < n) scores(j + 1);
-        ok = ok && mbar_wait_near(&sm.p_full[j & 1], (j >> 1) & 1);
-        tc_fence_after();
-        if (!ok) break;
-        const uint32_t p = base + L::kP + (L::kAhead ? j & 1 : 0) * (kKeys * 128);
-        for (int u = 0; u < L::kUnits; ++u) {
-          const int c = j * L::kUnits + u;
-#pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            const uint64_t da = smem_desc_sw128(base + (c % kRing) * kUnitBytes + s * 2048, 16384, 1024);
-            const uint64_t db = smem_desc_sw128(p + s * 2048, 16384, 1024);
-            mma_f16_ss(tmem + L::kTmemO + u * R, da, db, kIdescO, j > 0 || s > 0);
-          }
-          tc_commit(&sm.empty[c % kRing]);
-        }
-        tc_commit(&sm.o_done);
-        if (!L::kAhead && j + 1 < n) scores(j + 1);
+        if (!ok) atomicExch(&sm.abort, 1);
+        // the end of every MMA: the output may be read, and tensor memory given back
+        tc_commit(&sm.drain);
+        if (!mbar_wait_near(&sm.drain, 0) || !ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
       }
-      if (!ok) atomicExch(&sm.abort, 1);
-      // the end of every MMA: the output may be read, and tensor memory given back
-      tc_commit(&sm.drain);
-      if (!mbar_wait_near(&sm.drain, 0) || !ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
-    }
-    __syncwarp();
+      __syncwarp();
     } else if (warp == kMmaWarp + 1 && n > 0 && gridDim.y == 1) {
       // The CTA that follows on this SM takes about the tile that lies a wave of CTAs (one per SM)
       // ahead; all SMs begin and end their tiles at much the same time, and its queries and first
       // keys would come from memory in that crowd.  Bring them to L2 now.
-      if (mbar_wait_near(&sm.q_full, 0)) prefetch_tile<D, R>(a, blockIdx.x + kSMs, page_shift);
+      if (__all_sync(0xFFFFFFFFu, mbar_wait_near(&sm.q_full, 0))) prefetch_tile<D, R>(a, blockIdx.x + kSMs, page_shift);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (n > 0) {
-    // ------------------------------------------------------- load and decode
-    const bool ok = load_units<D, true, L::kSlots>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, smem,
-                                                   tmem + L::kTmemK, sm.full, sm.empty, sm.a_free, sm.bad);
-    if (!ok) {
-      atomicExch(&sm.abort, 1);
-      if (lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
-    }
+      // ------------------------------------------------------- load and decode
+      const bool ok = load_units<D, true, L::kSlots>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, smem,
+                                                     tmem + L::kTmemK, sm.full, sm.empty, sm.a_free, sm.bad);
+      if (!ok) {
+        atomicExch(&sm.abort, 1);
+        if (lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+      }
     }
   }
   pdl_trigger();
@@ -574,7 +587,10 @@ cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cu
 
 template <int D>
 cudaError_t launch_d(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cudaStream_t s) {
-  return p.R == 16 ? launch<D, 16>(a, p, use_pdl, s) : p.R == 32 ? launch<D, 32>(a, p, use_pdl, s) : launch<D, 64>(a, p, use_pdl, s);
+  if constexpr (D == 512) {
+    if (p.R == 64) return launch<D, 64>(a, p, use_pdl, s);
+  }
+  return p.R == 16 ? launch<D, 16>(a, p, use_pdl, s) : launch<D, 32>(a, p, use_pdl, s);
 }
 
 // Rows per tile, and into how many ranges of cache rows a tile is split: the count that a model of
