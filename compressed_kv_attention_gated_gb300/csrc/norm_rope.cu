@@ -14,8 +14,9 @@
 // Both channels of a rotated pair belong to one lane: eight neighbours when pairs
 // are neighbours (16-byte accesses), and when they are halves of the span, four
 // of the first half and their four partners (8-byte accesses at bf16, still 256
-// bytes in a row per warp).  Spans and offsets that are not whole groups of eight
-// channels take a channel-by-channel path through shared memory.
+// bytes in a row per warp).  Halves that do not consist of whole groups of four
+// channels exchange partners through shared memory (word (c mod 8) * D/8 + c / 8 for
+// channel c: a lane's eight words and its partners' lie in different banks).
 //
 // Measured (GB300, L2 cold, 6.8 TB/s copy peak): 8192 tokens x 64 heads of 512,
 // bf16: 175-177 us (a copy of the same bytes 167), 65,536 x 24 of 128: 142-146 us
@@ -31,7 +32,7 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr uint32_t kNormShare = 32;  // heads of a token that a warp takes at most
-enum Rotation { kNone, kPairs, kHalves, kAny };
+enum Rotation { kNone, kPairs, kHalves, kOddHalves };
 
 // Blocks per SM: two, because 128 registers hold everything.  (With three and a few
 // spilled registers 8192 x 64 rows of 512 took 220-257 us instead of 173-177.)
@@ -91,7 +92,8 @@ __device__ __forceinline__ void norm_heads(const NormRopeArgs& a, const ckv_norm
   constexpr int kLanes = D >= 256 ? 32 : D / 8;  // of a row
   constexpr int kRows = 32 / kLanes;             // rows of a warp
   constexpr int kGroups = D / (kLanes * 8);
-  constexpr int kBatch = (D == 512 ? 2 : 4) / (kF32 ? 2 : 1);
+  constexpr int kMost = (D == 512 ? 2 : 4) / (kRot == kOddHalves ? 2 : 1) / (kF32 ? 2 : 1);
+  constexpr int kBatch = kMost < 1 ? 1 : kMost;  // rows of a lane in work, and as many in flight (registers)
   const int sl = (threadIdx.x & 31) % kLanes, sub = (threadIdx.x & 31) / kLanes;
   const int half = a.rope_dim >> 1;
   int base[kGroups][2];
@@ -104,10 +106,10 @@ __device__ __forceinline__ void norm_heads(const NormRopeArgs& a, const ckv_norm
       if (q * 8 < a.rope_dim) {
         base[g][0] = a.rope_offset + q * 4;
         base[g][1] = a.rope_offset + half + q * 4;
-      } else {
+      } else {  // the channels around the span, four by four
         const int c = q * 8 - a.rope_dim;
         base[g][0] = c < a.rope_offset ? c : c + a.rope_dim;
-        base[g][1] = base[g][0] + 4;
+        base[g][1] = c + 4 < a.rope_offset ? c + 4 : c + 4 + a.rope_dim;
       }
     }
   }
@@ -148,21 +150,52 @@ __device__ __forceinline__ void norm_heads(const NormRopeArgs& a, const ckv_norm
     return;
   }
   const float* cs = a.cos_sin + static_cast<int64_t>(pos) * a.rope_dim;
-  bool in_span[kGroups];
-  Two c2[kGroups][2], s2[kGroups][2], w[kGroups][4];
+  // angles of the lane's pairs, and which of them lie in the span (a bit each; the others stay as they are)
+  uint32_t in_span[kGroups];
+  constexpr int kA = kRot == kOddHalves ? 4 : 2;
+  Two c2[kGroups][kA], s2[kGroups][kA], w[kGroups][4];
+  int mate[kGroups][kRot == kOddHalves ? 8 : 1];  // where the partner of each channel lies in s_row
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    in_span[g] = false;
-    if constexpr (kRot == kPairs || kRot == kHalves) {
-      in_span[g] = kRot == kPairs ? base[g][0] >= a.rope_offset && base[g][0] < a.rope_offset + a.rope_dim : (g * 32 + sl) * 8 < a.rope_dim;
+    in_span[g] = 0;
+    if constexpr (kRot == kPairs) {
+      float co[4], si[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = base[g][0] + 2 * j - a.rope_offset;
+        const bool in = k >= 0 && k < a.rope_dim;
+        in_span[g] |= in ? 1u << j : 0u;
+        co[j] = in ? __ldg(cs + (k >> 1)) : 1.f;
+        si[j] = in ? __ldg(cs + half + (k >> 1)) : 0.f;
+      }
+      c2[g][0] = Two(co[0], co[1]), c2[g][1] = Two(co[2], co[3]);
+      s2[g][0] = Two(si[0], si[1]), s2[g][1] = Two(si[2], si[3]);
+    } else if constexpr (kRot == kHalves) {
       float4 co = make_float4(1.f, 1.f, 1.f, 1.f), si = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (in_span[g]) {
-        const int p = kRot == kPairs ? (base[g][0] - a.rope_offset) >> 1 : base[g][0] - a.rope_offset;
+      if ((g * 32 + sl) * 8 < a.rope_dim) {
+        const int p = base[g][0] - a.rope_offset;
+        in_span[g] = 1;
         co = __ldg(reinterpret_cast<const float4*>(cs + p));
         si = __ldg(reinterpret_cast<const float4*>(cs + half + p));
       }
       c2[g][0] = Two(co.x, co.y), c2[g][1] = Two(co.z, co.w);
       s2[g][0] = Two(si.x, si.y), s2[g][1] = Two(si.z, si.w);
+    } else if constexpr (kRot == kOddHalves) {
+      float co[8], si[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = base[g][0] + j, k = c - a.rope_offset;
+        const bool in = k >= 0 && k < a.rope_dim, second = k >= half;
+        const int p = second ? k - half : k, o = !in ? c : second ? c - half : c + half;
+        co[j] = in ? __ldg(cs + p) : 1.f;
+        si[j] = !in ? 0.f : second ? __ldg(cs + half + p) : -__ldg(cs + half + p);
+        mate[g][j] = (o & 7) * (D / 8) + (o >> 3);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        c2[g][j] = Two(co[2 * j], co[2 * j + 1]);
+        s2[g][j] = Two(si[2 * j], si[2 * j + 1]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -207,55 +240,48 @@ __device__ __forceinline__ void norm_heads(const NormRopeArgs& a, const ckv_norm
         widen(cur.raw[b][g][0], cur.raw[b][g][kF32 ? 1 : 0], kF32, z);
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[j] = mul(mul(z[j], scale), w[g][j]);
-        if constexpr (kRot == kAny) {
-          // the normalised row, for the partners of other lanes
+        if (kRot == kPairs && in_span[g]) {  // z[j] = (x, y): (x, y) c + (-y, x) s
 #pragma unroll
-          for (int j = 0; j < 4; ++j) z[j].get(s_row[base[g][0] + 2 * j], s_row[base[g][0] + 2 * j + 1]);
-        } else {
-          if (kRot == kPairs && in_span[g]) {  // z[j] = (x, y): (x, y) c + (-y, x) s
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float x, y, c[2], si[2];
-              z[j].get(x, y);
-              c2[g][j >> 1].get(c[0], c[1]);
-              s2[g][j >> 1].get(si[0], si[1]);
-              z[j] = fma(z[j], Two(c[j & 1], c[j & 1]), mul(Two(-y, x), Two(si[j & 1], si[j & 1])));
-            }
-          } else if (kRot == kHalves && in_span[g]) {  // z[j], z[2 + j] = two x and their two y
-            const Two minus(-1.f, -1.f);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const Two x = z[j], y = z[2 + j];
-              z[j] = fma(x, c2[g][j], mul(mul(y, minus), s2[g][j]));
-              z[2 + j] = fma(y, c2[g][j], mul(x, s2[g][j]));
-            }
+          for (int j = 0; j < 4; ++j) {
+            float x, y, c[2], si[2];
+            z[j].get(x, y);
+            c2[g][j >> 1].get(c[0], c[1]);
+            s2[g][j >> 1].get(si[0], si[1]);
+            const Two turned = fma(z[j], Two(c[j & 1], c[j & 1]), mul(Two(-y, x), Two(si[j & 1], si[j & 1])));
+            if ((in_span[g] >> j) & 1) z[j] = turned;
           }
-          float v[8];
+        } else if (kRot == kHalves && in_span[g]) {  // z[j], z[2 + j] = two x and their two y
+          const Two minus(-1.f, -1.f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) z[j].get(v[2 * j], v[2 * j + 1]);
-          if (hh < h1) store_row<kRot == kHalves>(m, out, base[g], v);
+          for (int j = 0; j < 2; ++j) {
+            const Two x = z[j], y = z[2 + j];
+            z[j] = fma(x, c2[g][j], mul(mul(y, minus), s2[g][j]));
+            z[2 + j] = fma(y, c2[g][j], mul(x, s2[g][j]));
+          }
+        }
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j].get(v[2 * j], v[2 * j + 1]);
+        if constexpr (kRot == kOddHalves) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s_row[j * (D / 8) + (base[g][0] >> 3)] = v[j];
+        } else if (hh < h1) {
+          store_row<kRot == kHalves>(m, out, base[g], v);
         }
       }
-      if constexpr (kRot == kAny) {
+      if constexpr (kRot == kOddHalves) {
         __syncwarp();
-        if (hh < h1) {
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            float v[8];
+        for (int g = 0; g < kGroups; ++g) {
+          float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int c = base[g][0] + j, k = c - a.rope_offset;
-              v[j] = s_row[c];
-              if (k >= 0 && k < a.rope_dim) {
-                const bool second = a.interleaved ? (k & 1) : k >= half;
-                const int p = a.interleaved ? k >> 1 : (second ? k - half : k);
-                const int mate = a.interleaved ? (second ? c - 1 : c + 1) : (second ? c - half : c + half);
-                const float cc = __ldg(cs + p), ss = __ldg(cs + half + p);
-                v[j] = second ? v[j] * cc + s_row[mate] * ss : v[j] * cc - s_row[mate] * ss;
-              }
-            }
-            store_row<false>(m, out, base[g], v);
+          for (int j = 0; j < 4; ++j) {
+            const int own = base[g][0] >> 3;
+            const Two x(s_row[2 * j * (D / 8) + own], s_row[(2 * j + 1) * (D / 8) + own]);
+            const Two o(s_row[mate[g][2 * j]], s_row[mate[g][2 * j + 1]]);
+            fma(x, c2[g][j], mul(o, s2[g][j])).get(v[2 * j], v[2 * j + 1]);
           }
+          if (hh < h1) store_row<false>(m, out, base[g], v);
         }
         __syncwarp();
       }
@@ -268,9 +294,9 @@ template <int D, Rotation kRot>
 __global__ void __launch_bounds__(kNormThreads, kNormBlocks)
     norm_rope_kernel(const __grid_constant__ NormRopeArgs a, uint32_t share) {
   constexpr int kRows = D >= 256 ? 1 : 256 / D;  // of a warp
-  __shared__ float s_rows[kRot == kAny ? kNormThreads / 32 * kRows : 1][kRot == kAny ? D : 1];
+  __shared__ float s_rows[kRot == kOddHalves ? kNormThreads / 32 * kRows : 1][kRot == kOddHalves ? D : 1];
   const int warp = threadIdx.x >> 5, sub = (threadIdx.x & 31) / (32 / kRows);
-  float* s_row = s_rows[kRot == kAny ? warp * kRows + sub : 0];
+  float* s_row = s_rows[kRot == kOddHalves ? warp * kRows + sub : 0];
   pdl_wait();
   // a unit is `share` heads of a token
   const uint32_t per_q = (a.set[0].heads + share - 1) / share, per_k = (a.set[1].heads + share - 1) / share;
@@ -309,11 +335,10 @@ cudaError_t launch_rot(const NormRopeArgs& a, bool use_pdl, cudaStream_t s) {
 template <int D>
 cudaError_t launch_d(const NormRopeArgs& a, bool use_pdl, cudaStream_t s) {
   if (a.rope_dim == 0) return launch_rot<D, kNone>(a, use_pdl, s);
-  // whole groups of eight channels, and cos | sin rows that 16-byte loads can start in
-  const bool whole = a.rope_offset % 8 == 0 && a.rope_dim % 8 == 0 &&
-                     reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0;
-  if (!whole) return launch_rot<D, kAny>(a, use_pdl, s);
-  return a.interleaved ? launch_rot<D, kPairs>(a, use_pdl, s) : launch_rot<D, kHalves>(a, use_pdl, s);
+  if (a.interleaved) return launch_rot<D, kPairs>(a, use_pdl, s);
+  // halves of whole groups of four channels, and cos | sin rows that 16-byte loads can start in
+  const bool whole = a.rope_offset % 4 == 0 && a.rope_dim % 8 == 0 && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0;
+  return whole ? launch_rot<D, kHalves>(a, use_pdl, s) : launch_rot<D, kOddHalves>(a, use_pdl, s);
 }
 
 }  // namespace
