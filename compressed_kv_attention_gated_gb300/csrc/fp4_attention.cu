@@ -315,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       for (int j = 0; j < n; ++j) {
         const int buf = L::kAhead ? j & 1 : 0;
         const int key = k_first + j * kKeys + quad * 32 + lane;
-        const int unit0 = j * L::kUnits;
+        const int last = (j + 1) * L::kUnits - 1;
         // the decoding warps' note on missing keys, then the scores
-        ok = mbar_wait_near(&sm.full[unit0 % kRing], (unit0 / kRing) & 1) && mbar_wait_near(&sm.s_full[j & 1], (j >> 1) & 1);
+        ok = mbar_wait_near(&sm.full[last % kRing], (last / kRing) & 1) && mbar_wait_near(&sm.s_full[j & 1], (j >> 1) & 1);
         if (!ok) atomicExch(&sm.abort, 1);
         __syncwarp();
         tc_fence_after();
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (n > 0) {
       // ------------------------------------------------------- load and decode
-      const bool ok = load_units<D, true, L::kSlots>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, smem,
+      const bool ok = load_units<D, true, L::kSlots, kRing>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, 0, smem,
                                                      tmem + L::kTmemK, sm.full, sm.empty, sm.a_free, sm.bad);
       if (!ok) {
         atomicExch(&sm.abort, 1);
@@ -582,7 +582,7 @@ cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cu
   e = launch_ex(fp4_attention_kernel<D, R>, dim3(p.tiles, p.splits), dim3(kThreads), smem_bytes<D, R>(), use_pdl, s, a, p.chunk,
                 page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_ex(fp4_join_kernel<D, R>, dim3(p.tiles, R / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
+  return launch_ex(fp4_join_kernel<D, R, 1>, dim3(p.tiles, R / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
 }
 
 template <int D>
@@ -600,18 +600,20 @@ cudaError_t launch_d(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, 
 Fp4Plan plan_fp4(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
   Fp4Plan p;
   const int64_t rows = (T + B - 1) / B * H;  // of an average request
-  p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : D == 512 ? 64 : 128;
+  p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : D == 512 && rows <= 64 ? 64 : 128;
   p.tiles = static_cast<int>(T * H / p.R + B);
   int64_t busy = (T * H + p.R - 1) / p.R;
   busy = busy < T && busy < B ? (T < B ? T : B) : busy;
   const int64_t most = (max_rows + kKeys - 1) / kKeys;
-  const double around = 5.0, tile = D == 512 ? 3.5 : D == 256 ? 1.6 : 0.9, join = 4.0;
+  const int halves = fp4_row_halves(D, p.R);
+  busy *= halves;
+  const double around = 5.0, tile = D == 512 ? (halves == 2 ? 2.2 : 3.5) : D == 256 ? 1.6 : 0.9, join = 4.0;
   double best = 0;
   int64_t best_s = 1;
   for (int64_t s = 1; s <= most && s <= 64; ++s) {
     const int64_t waves = (busy * s + 151) / 152;
     double us = waves * (around + tile * static_cast<double>((most + s - 1) / s));
-    if (s > 1) us += join + 2.0 * static_cast<double>(busy * s) * p.R * D * 4 / 4e6;
+    if (s > 1) us += join + 2.0 * static_cast<double>(busy / halves * s) * p.R * D * 4 / 4e6;
     if (s == 1 || us < best) {
       best = us;
       best_s = s;
@@ -626,7 +628,7 @@ Fp4Plan plan_fp4(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
 
 int64_t fp4_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
   const Fp4Plan p = plan_fp4(T, B, H, D, max_rows);
-  return p.splits == 1 ? 0 : static_cast<int64_t>(p.tiles) * p.splits * p.R * (D + 2) * static_cast<int64_t>(sizeof(float));
+  return p.splits == 1 ? 0 : static_cast<int64_t>(p.tiles) * p.splits * p.R * (D + 2 * fp4_row_halves(D, p.R)) * static_cast<int64_t>(sizeof(float));
 }
 
 cudaError_t launch_fp4_attention(const Fp4AttentionArgs& a, int D, bool use_pdl, cudaStream_t s) {

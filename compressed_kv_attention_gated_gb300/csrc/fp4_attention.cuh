@@ -28,6 +28,9 @@ struct Fp4Plan {
   int splits;   // ranges of cache rows per tile
   int chunk;    // cache rows per range (multiple of kKeys)
 };
+// CTAs that share a tile and a range, each with as many of the channels: with rows on the M side
+// the accumulator of 512 channels would fill tensor memory.
+constexpr int fp4_row_halves(int D, int R) { return D == 512 && R == 128 ? 2 : 1; }
 cudaError_t launch_fp4_attention_rows(const Fp4AttentionArgs& a, const Fp4Plan& p, int D, bool use_pdl, cudaStream_t s);
 
 namespace {
@@ -142,19 +145,20 @@ __device__ __forceinline__ void load_cols(const float* p, float (&v)[n]) {
 // the 128-byte swizzle; with kCopy it also goes to tensor memory (a lane per
 // key, 64 columns, slot c % kSlots from column tmem_k on).  Two groups of 4 warps
 // take units by turns: one's waits and fences lie under the other's decoding.
-//   full[c % kRing]    one arrival per warp of the group (4) when unit c is there
-//   empty[c % kRing]   completed when both products are done with it
+//   full[c % kRingN]   one arrival per warp of the group (4) when unit c is there
+//   empty[c % kRingN]  completed when both products are done with it
 //   a_free[c % kSlots] completed when the first product is done with it (only waited for where
-//                      kSlots < kRing, and there a tile is kRing units: the other waits imply it)
-//   bad[tile & 3]      a bit per key whose page is not there
-// Rows that are not there are zeros.  False when a wait ran out.
-template <int D, bool kCopy, int kSlots>
+//                      kSlots < kRingN, and there a tile is kRingN units: the other waits imply it)
+//   bad[tile & 3]      a bit per key whose page is not there, written with the tile's last unit
+// A tile's units come in channel order from unit `turn` on.  Rows that are not there are
+// zeros.  False when a wait ran out.
+template <int D, bool kCopy, int kSlots, int kRingN>
 __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile& tile, int tid, int k_first, int k_last, int page_shift,
-                                           uint8_t* ring, uint32_t tmem_k, uint64_t* full, uint64_t* empty, uint64_t* a_free,
-                                           uint32_t (*bad)[4]) {
-  constexpr int kUnits = D / 128, kGroups = 2;
-  constexpr int kDeep = kRing / kGroups;  // units of a group in registers: loads run this far ahead
-  static_assert(kSlots == kRing || kUnits == kRing, "waits");
+                                           int turn, uint8_t* ring, uint32_t tmem_k, uint64_t* full, uint64_t* empty,
+                                           uint64_t* a_free, uint32_t (*bad)[4]) {
+  constexpr int kUnits = D / 128, kGroups = 2, kAhead = 4;
+  constexpr int kDeep = kAhead / kGroups;  // units of a group in registers: loads run this far ahead
+  static_assert(!kCopy || kSlots == kRingN || kUnits == kRingN, "waits");
   // a thread has one key's 128 channels of a unit, that of its lane of tensor memory; neighbouring
   // lanes have neighbouring keys, whose 16-byte chunks the swizzle spreads over all banks
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, key = quad * 32 + lane, group = tid >> 7;
@@ -196,7 +200,7 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
     if (c < total) {
       // the group's first unit of a tile
       if (kUnits <= kGroups || c % kUnits == group) locate(c / kUnits);
-      const int u = c % kUnits;
+      const int u = (c + turn) % kUnits;
       x.gone = gone;
       x.s = make_uint2(0, 0);
       if (there) x.s = *reinterpret_cast<const uint2*>(scales + u * 8);
@@ -211,14 +215,14 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
   for (int i = 0; i < kDeep; ++i) fetch(reg[i], group + i * kGroups);
   bool ok = true;
 #pragma unroll 1
-  for (int c0 = group; c0 < total && ok; c0 += kRing) {
+  for (int c0 = group; c0 < total && ok; c0 += kAhead) {
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) {
-      const int c = c0 + i * kGroups, slot = group + i * kGroups;
+      const int c = c0 + i * kGroups, slot = kRingN == kAhead ? group + i * kGroups : c % kRingN;
       if (c < total && ok) {
         // the ring's last unit in this place has served both products
-        if (c >= kRing) ok = mbar_wait_near(&empty[slot], ((c / kRing) - 1) & 1);
-        if (kCopy && kSlots < kRing && slot >= kSlots) ok = ok && mbar_wait_near(&a_free[c % kSlots], ((c / kSlots) - 1) & 1);
+        if (c >= kRingN) ok = mbar_wait_near(&empty[slot], ((c / kRingN) - 1) & 1);
+        if (kCopy && kSlots < kRingN && slot >= kSlots) ok = ok && mbar_wait_near(&a_free[c % kSlots], ((c / kSlots) - 1) & 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (ok) {
           if (kCopy) tc_fence_after();
@@ -237,7 +241,7 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
               if (kCopy) tmem_st8(a_tile + b * 8, lo, hi);
             }
           }
-          if (c % kUnits == 0 && lane == 0) bad[(c / kUnits) & 3][quad] = reg[i].gone;
+          if (c % kUnits == kUnits - 1 && lane == 0) bad[(c / kUnits) & 3][quad] = reg[i].gone;
           if (kCopy) {
             tc_wait_st();
             tc_fence_before();
@@ -245,7 +249,7 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[slot]);
-          fetch(reg[i], c + kRing);
+          fetch(reg[i], c + kAhead);
         }
       }
     }
@@ -254,7 +258,9 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
 }
 
 // Joins the ranges of a tile: one warp per row, in the order of the ranges.
-template <int D, int R>
+// With kHalves == 2 two CTAs shared a range, each with half of the channels and
+// with references and sums of its own.
+template <int D, int R, int kHalves>
 __global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int splits) {
   const int lane = threadIdx.x & 31;
   pdl_wait();
@@ -270,41 +276,45 @@ __global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ F
   if (a.ctx_rows[t.tok0 + (t.base + r) / a.H] < 0) return;
   const float* ws = static_cast<const float*>(a.workspace);
   const int64_t slot0 = static_cast<int64_t>(blockIdx.x) * splits;
-  const float* ml = ws + static_cast<int64_t>(gridDim.x) * splits * R * D + slot0 * R * 2;
+  const float* ml = ws + static_cast<int64_t>(gridDim.x) * splits * R * D + slot0 * kHalves * R * 2;
   const int64_t flat = static_cast<int64_t>(t.tok0) * a.H + t.base + r;
-  float m = kNegBig;
-  for (int s = lane; s < used; s += 32) m = fmaxf(m, ml[s * 2 * R + r]);
+  const float sink = a.sink ? a.sink[flat % a.H] * kLog2e : -INFINITY;
+  constexpr int kQuads = D / 128 / kHalves;  // a lane's groups of four channels in a half
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  float all = 0.f;
-  if (a.sink) {
-    const float s = a.sink[flat % a.H] * kLog2e;
-    m = fmaxf(m, s);
-    all = s == m ? 1.f : fast_exp2(s - m);
-  }
-  float acc[D / 32];
+  for (int z = 0; z < kHalves; ++z) {
+    float m = kNegBig;
+    for (int s = lane; s < used; s += 32) m = fmaxf(m, ml[(s * kHalves + z) * 2 * R + r]);
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-  for (int s = 0; s < used; ++s) {
-    const float l = ml[s * 2 * R + R + r];
-    const float w = fast_exp2(ml[s * 2 * R + r] - m);
-    all += l == 0.f ? 0.f : l * w;
-    const float4* o = reinterpret_cast<const float4*>(ws + ((slot0 + s) * R + r) * D);
-#pragma unroll
-    for (int i = 0; i < D / 128; ++i) {
-      const float4 v = o[i * 32 + lane];
-      acc[4 * i] = fmaf(v.x, w, acc[4 * i]);
-      acc[4 * i + 1] = fmaf(v.y, w, acc[4 * i + 1]);
-      acc[4 * i + 2] = fmaf(v.z, w, acc[4 * i + 2]);
-      acc[4 * i + 3] = fmaf(v.w, w, acc[4 * i + 3]);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float all = 0.f;
+    if (a.sink) {
+      m = fmaxf(m, sink);
+      all = sink == m ? 1.f : fast_exp2(sink - m);
     }
-  }
-  const float inv = all == 0.f ? 0.f : a.g / all;
+    float acc[4 * kQuads];
 #pragma unroll
-  for (int i = 0; i < D / 128; ++i)
-    *reinterpret_cast<uint2*>(a.out + flat * D + i * 128 + lane * 4) =
-        make_uint2(pack_bf16x2_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack_bf16x2_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
-  if (lane == 0 && a.lse) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+    for (int i = 0; i < 4 * kQuads; ++i) acc[i] = 0.f;
+    for (int s = 0; s < used; ++s) {
+      const float* row = ml + (s * kHalves + z) * 2 * R + r;
+      const float l = row[R], w = fast_exp2(row[0] - m);
+      all += l == 0.f ? 0.f : l * w;
+      const float4* o = reinterpret_cast<const float4*>(ws + ((slot0 + s) * R + r) * D) + z * kQuads * 32;
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        const float4 v = o[i * 32 + lane];
+        acc[4 * i] = fmaf(v.x, w, acc[4 * i]);
+        acc[4 * i + 1] = fmaf(v.y, w, acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(v.z, w, acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(v.w, w, acc[4 * i + 3]);
+      }
+    }
+    const float inv = all == 0.f ? 0.f : a.g / all;
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i)
+      *reinterpret_cast<uint2*>(a.out + flat * D + (z * kQuads + i) * 128 + lane * 4) = make_uint2(
+          pack_bf16x2_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack_bf16x2_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
+    if (z == 0 && lane == 0 && a.lse) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+  }
 }
 
 }  // namespace

@@ -1,6 +1,6 @@
 // fp4_attention_rows.cu -- attention over the 4-bit paged cache with the (token,
 // head) rows on the M side of both products, for requests with more than 32 rows
-// at D = 128 and 256 (fp4_attention.cu holds the other form and the formulas):
+// (64 at D = 512; fp4_attention.cu holds the other form and the formulas):
 //   S [128 rows x 128 keys]   = Q [128 x D] K^T
 //   O [128 rows x D]         += P [128 x 128 keys] K
 // A thread owns 64 keys of a row of S (two warps share 32 rows): maximum and sum
@@ -11,8 +11,22 @@
 // As in the other form a row's weights are taken against a reference that moves
 // only when a score exceeds it by 2^8; here that is the affair of two warps.
 //
-// At D = 512 the accumulator would fill tensor memory, and with few rows most of
-// M would be idle while two warps do the whole softmax: those take the other form.
+// At D = 512 the accumulator would fill tensor memory, so two CTAs share a tile:
+// both form the scores and the softmax, each multiplies with its half of the
+// channels.  A key is decoded twice per 128 rows, as often as in the other form
+// (once per 64), but a product step has twice the rows.  Queries take 128 KB of
+// shared memory there and the ring has three places; only the units of the CTA's
+// own half stay for the second product, so they come last in a tile.
+//
+// What bounds it: with D = 128 the softmax; with D = 512 the chain of a tile, as the
+// ring has no place for the next tile's units before the second product gives
+// them back: softmax 1.6 k clocks, second product 0.5 k, scores 1.5 k (both
+// operands from shared memory, 256 bytes per clock of the products).
+// Measured (GB300): 512 requests x 4 tokens x 32 heads at D = 128, 0-2048 rows 66 us
+// (520 TFLOP/s); D = 512, a prompt of 8750 tokens x 64 heads over 200-1024 rows
+// 1.63 ms (430 TFLOP/s), 256 x 128 heads x 922-1024 rows 161 us; the other form
+// takes 1.70 ms and 180 us.  Slower: D = 128 with two CTAs of 9 warps per SM (109 us,
+// when one took 82).
 #include "fp4_attention.cuh"
 
 namespace ckv {
@@ -28,33 +42,40 @@ static_assert(256 * kRowSoftRegs + 128 * kRowMmaRegs + 256 * kRowLoadRegs <= kRo
 template <int D>
 struct RowLayout {
   static constexpr int kUnits = D / 128;
+  static constexpr int kHalves = fp4_row_halves(D, 128);
+  static constexpr int kDV = D / kHalves;            // channels of the output that a CTA has
+  static constexpr int kKept = kDV / 128;            // a tile's last units, of which they are
+  static constexpr int kRingN = D == 512 ? 3 : 4;
   static constexpr int kSBufs = D == 128 ? 2 : 1;
-  static constexpr int kQ = kRing * kUnitBytes;   // Q: D/64 blocks of 128 rows x 128 bytes
+  static constexpr int kQ = kRingN * kUnitBytes;     // Q: D/64 blocks of 128 rows x 128 bytes
   static constexpr int kSmall = kQ + (D / 64) * 128 * 128;
-  static constexpr int kTmemO = 0, kTmemS = D, kTmemP = D + kSBufs * 128;  // P: two buffers of 64 columns
+  static constexpr int kTmemO = 0, kTmemS = kDV, kTmemP = kDV + kSBufs * 128;  // P: two buffers of 64 columns
   static_assert(kTmemP + 2 * 64 <= 512, "tensor memory");
-  static constexpr int kOutPitch = D * 2 + 16;    // output rows on their way out
-  static constexpr int kPartPitch = D * 4 + 16;   // the same of fp32 partials, over the ring and Q
+  static constexpr int kOutPitch = kDV * 2 + 16;     // output rows on their way out, over the ring and Q
+  static constexpr int kPartPitch = kDV * 4 + 16;    // the same of fp32 partials
   static_assert(128 * kPartPitch <= kSmall, "output staging");
 };
 
 struct RowSmall {
-  uint64_t full[kRing], empty[kRing], s_full[2], s_read, p_full[2], q_full, o_done, drain;
+  uint64_t full[4], empty[4], s_full[2], s_read, p_full[2], q_full, o_done, drain;
   uint32_t tmem;
   int32_t abort;
   Tile tile;
   int32_t ctx_max;
   alignas(16) uint32_t bad[4][4];
-  float c[128];     // score factors
-  float part[2][128];  // what the two warps of a row tell each other
-  int64_t q[128];   // where the rows' queries begin, elements
-  int32_t out[128]; // flat (token, head) index, -1: none
+  float c[128];      // score factors
+  int32_t out[128];  // flat (token, head) index, -1: none
+  union {
+    int64_t q[128];      // where the rows' queries begin, elements (until they are loaded)
+    float part[2][128];  // what the two warps of a row tell each other
+  };
 };
 
 template <int D>
 constexpr int row_smem_bytes() {
-  return RowLayout<D>::kSmall + static_cast<int>(sizeof(RowSmall)) + 1024;
+  return RowLayout<D>::kSmall + static_cast<int>(sizeof(RowSmall));
 }
+static_assert(row_smem_bytes<512>() <= 227 * 1024, "shared memory");
 
 // The two warps of 32 rows (quad q) meet; true when p holds for one of the 64 threads.
 __device__ __forceinline__ void pair_barrier(int quad) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + quad) : "memory"); }
@@ -82,15 +103,21 @@ template <int D>
 __global__ void __launch_bounds__(kRowThreads, 1)
     fp4_attention_rows_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int page_shift) {
   using L = RowLayout<D>;
-  extern __shared__ uint8_t s_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
+  extern __shared__ __align__(1024) uint8_t smem[];
   RowSmall& sm = *reinterpret_cast<RowSmall*>(smem + L::kSmall);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the CTA's half of the channels, and the unit that a tile begins with: the units of that half come last
+  const int half_v = L::kHalves == 2 ? blockIdx.z : 0, turn = L::kHalves == 2 && half_v == 0 ? 2 : 0;
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+    return;
+  }
 
   if (warp == kRowMmaWarp) {
     tmem_alloc<512>(&sm.tmem);
     if (lane == 0) {
-      for (int i = 0; i < kRing; ++i) {
+      for (int i = 0; i < L::kRingN; ++i) {
         mbar_init(&sm.full[i], 4);
         mbar_init(&sm.empty[i], 1);
       }
@@ -152,28 +179,35 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     if (!idle) {
       const int quad = warp & 3, half = warp >> 2, row = threadIdx.x & 127;
       // ----------------------------------------------------------- queries
-      // eight channels per lane, D/8 lanes per row, 16 rows per warp; every load is issued before the first is used
+      // eight channels per lane (16 at D = 512), 16 rows per warp; every load of a batch is issued before the first is used
       if (n > 0) {
-        constexpr int kSpan = D / 8;     // lanes of a row
-        constexpr int kPer = 32 / kSpan; // rows of a warp at a time
-        constexpr int kBatch = 8;
-        const int sub = lane / kSpan, ch = lane % kSpan * 8;
-        static_assert(D <= 256 && 16 % (kBatch * kPer) == 0, "");
+        constexpr int kC = D == 512 ? 16 : 8;  // channels of a lane
+        constexpr int kSpan = D / kC;          // lanes of a row
+        constexpr int kPer = 32 / kSpan;       // rows of a warp at a time
+        constexpr int kBatch = D == 512 ? 4 : 8;
+        const int sub = lane / kSpan, ch = lane % kSpan * kC;
+        static_assert(16 % (kBatch * kPer) == 0, "");
 #pragma unroll 1
         for (int r0 = warp * 16; r0 < warp * 16 + 16; r0 += kBatch * kPer) {
-          uint4 raw[kBatch];
+          uint4 raw[kBatch][kC / 8];
           uint32_t am[kBatch];
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
             const int r = r0 + i * kPer + sub;
-            raw[i] = sm.out[r] >= 0 ? *reinterpret_cast<const uint4*>(a.q + sm.q[r] + ch) : make_uint4(0, 0, 0, 0);
+            const bool on = sm.out[r] >= 0;
+            const uint4* q = reinterpret_cast<const uint4*>(a.q + sm.q[r] + ch);
+#pragma unroll
+            for (int x = 0; x < kC / 8; ++x) raw[i][x] = on ? q[x] : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
             am[i] = 0;  // the largest magnitude: bf16 bits order like the values
 #pragma unroll
-            for (int y = 0; y < 4; ++y) am[i] = max(am[i], max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
+            for (int x = 0; x < kC / 8; ++x) {
+              const uint32_t w[4] = {raw[i][x].x, raw[i][x].y, raw[i][x].z, raw[i][x].w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) am[i] = max(am[i], max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
+            }
           }
 #pragma unroll
           for (int o = 1; o < kSpan; o <<= 1) {
@@ -187,8 +221,10 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
             if (lane % kSpan == 0)
               sm.c[r] = a.softmax_scale * kLog2e * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
-            *reinterpret_cast<uint4*>(smem + L::kQ + (ch / 64) * (128 * 128) + r * 128 + (((ch % 64) / 8) ^ (r & 7)) * 16) =
-                query8(raw[i], up);
+            uint8_t* to = smem + L::kQ + (ch / 64) * (128 * 128) + r * 128;
+#pragma unroll
+            for (int x = 0; x < kC / 8; ++x)
+              *reinterpret_cast<uint4*>(to + ((((ch % 64) / 8 + x) ^ (r & 7)) * 16)) = query8(raw[i][x], up);
           }
         }
       }
@@ -204,9 +240,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         const int buf = L::kSBufs == 2 ? j & 1 : 0;
-        const int unit0 = j * L::kUnits;
-        // the decoding warps' note on missing keys, then the scores
-        ok = mbar_wait_near(&sm.full[unit0 % kRing], (unit0 / kRing) & 1) && mbar_wait_near(&sm.s_full[j & 1], (j >> 1) & 1);
+        const int last = (j + 1) * L::kUnits - 1;
+        // the scores, then (there by now) the decoding warps' note on missing keys
+        ok = mbar_wait_near(&sm.s_full[j & 1], (j >> 1) & 1) && mbar_wait_near(&sm.full[last % L::kRingN], (last / L::kRingN) & 1);
         if (!ok) atomicExch(&sm.abort, 1);
         __syncwarp();
         tc_fence_after();
@@ -261,7 +297,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             tc_fence_after();
             const float k = unset ? 1.f : keep;  // an unset row's output is 0
 #pragma unroll 1
-            for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 16) {
+            for (int i = half * (L::kDV / 2); i < (half + 1) * (L::kDV / 2); i += 16) {
               float o[16];
               tmem_ld<16>(tmem + lanes + L::kTmemO + i, o);
               uint32_t v[16];
@@ -309,7 +345,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       float scale = 1.f;
       if (split) {
         if (half == 0) {
-          float* ml = ws + static_cast<int64_t>(gridDim.x) * gridDim.y * 128 * D + slot * 128 * 2;
+          float* ml = ws + static_cast<int64_t>(gridDim.x) * gridDim.y * 128 * D + (slot * L::kHalves + half_v) * 128 * 2;
           ml[row] = ref;
           ml[128 + row] = l;
         }
@@ -323,10 +359,10 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           m = high;
         }
         scale = all == 0.f ? 0.f : keep * a.g / all;
-        if (a.lse && my_flat >= 0 && half == 0) a.lse[my_flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+        if (a.lse && my_flat >= 0 && half == 0 && half_v == 0) a.lse[my_flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
       }
 #pragma unroll 1
-      for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
+      for (int i = half * (L::kDV / 2); i < (half + 1) * (L::kDV / 2); i += 32) {
         float o[32];
         if (n > 0) {
           tmem_ld<32>(tmem + lanes + L::kTmemO + i, o);
@@ -349,14 +385,15 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       }
       // a warp takes out what it brought, its rows' half, in 16-byte pieces
       __syncwarp();
-      const int piece = split ? D / 8 : D / 16, pitch = split ? L::kPartPitch : L::kOutPitch;
+      const int piece = split ? L::kDV / 8 : L::kDV / 16, pitch = split ? L::kPartPitch : L::kOutPitch;
       uint8_t* to = split ? reinterpret_cast<uint8_t*>(ws + slot * 128 * D) : reinterpret_cast<uint8_t*>(a.out);
+      const int whole = 2 * piece * L::kHalves, first = 2 * piece * half_v;  // of the row, in pieces
 #pragma unroll 4
       for (int i = lane; i < 32 * piece; i += 32) {
         const int r = quad * 32 + i / piece, x = half * piece + i % piece;
         const int32_t flat = sm.out[r];
         if (flat >= 0)
-          *reinterpret_cast<uint4*>(to + (static_cast<int64_t>(split ? r : flat) * (2 * piece) + x) * 16) =
+          *reinterpret_cast<uint4*>(to + (static_cast<int64_t>(split ? r : flat) * whole + first + x) * 16) =
               *reinterpret_cast<const uint4*>(smem + r * pitch + x * 16);
       }
       tc_fence_before();
@@ -369,42 +406,59 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         constexpr uint32_t kIdescS = idesc_f16(128, false, false), kIdescO = idesc_f16(128, false, true);
         const uint32_t base = smem_u32(smem);
         bool ok = mbar_wait_near(&sm.q_full, 0);
-        auto scores = [&](int j) {
+        // Scores run ahead of the last tile's second product as far as the ring goes: all of them, or
+        // (kept units fill all places but one) the first unit's.  Units are given back in their order:
+        // a place's users are of both groups, whose waits tell its phases apart by that.
+        constexpr int kEarly = L::kRingN < 2 * L::kKept ? 1 : L::kUnits;
+        // units i0 .. i1 - 1 of tile j's scores; a unit that the second product does not need is free after them
+        auto scores = [&](int j, int i0, int i1) {
           const uint32_t d = tmem + L::kTmemS + (L::kSBufs == 2 ? j & 1 : 0) * 128;
-          for (int u = 0; u < L::kUnits && ok; ++u) {
-            const int c = j * L::kUnits + u;
-            ok = mbar_wait_near(&sm.full[c % kRing], (c / kRing) & 1);
+          for (int i = i0; i < i1 && ok; ++i) {
+            const int c = j * L::kUnits + i, u = (i + turn) % L::kUnits;
+            ok = mbar_wait_near(&sm.full[c % L::kRingN], (c / L::kRingN) & 1);
             tc_fence_after();
             if (!ok) break;
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
               const uint64_t da = smem_desc_sw128(base + L::kQ + (u * 2 + s / 4) * (128 * 128) + (s % 4) * 32, 16, 1024);
-              const uint64_t db = smem_desc_sw128(base + (c % kRing) * kUnitBytes + (s / 4) * 16384 + (s % 4) * 32, 16, 1024);
-              mma_f16_ss(d, da, db, kIdescS, u > 0 || s > 0);
+              const uint64_t db = smem_desc_sw128(base + (c % L::kRingN) * kUnitBytes + (s / 4) * 16384 + (s % 4) * 32, 16, 1024);
+              mma_f16_ss(d, da, db, kIdescS, i > 0 || s > 0);
             }
+            if (i < L::kUnits - L::kKept && (kEarly == L::kUnits || i > 0)) tc_commit(&sm.empty[c % L::kRingN]);
           }
-          tc_commit(&sm.s_full[j & 1]);
+          if (i1 == L::kUnits) tc_commit(&sm.s_full[j & 1]);
         };
-        if (ok) scores(0);
+        if (ok) {
+          scores(0, 0, kEarly);
+          if (kEarly < L::kUnits) {
+            tc_commit(&sm.empty[0]);
+            scores(0, kEarly, L::kUnits);
+          }
+        }
         for (int j = 0; j < n && ok; ++j) {
           if (j + 1 < n) {
             if (L::kSBufs == 1) ok = mbar_wait_near(&sm.s_read, j & 1);  // with two buffers the weights of tile j - 1 said so
             tc_fence_after();
-            if (ok) scores(j + 1);
+            if (ok) scores(j + 1, 0, kEarly);
           }
           ok = ok && mbar_wait_near(&sm.p_full[j & 1], (j >> 1) & 1);
           tc_fence_after();
           if (!ok) break;
-          for (int u = 0; u < L::kUnits; ++u) {
-            const int c = j * L::kUnits + u;
+          for (int i = L::kUnits - L::kKept; i < L::kUnits; ++i) {
+            const int c = j * L::kUnits + i;
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
-              const uint64_t db = smem_desc_sw128(base + (c % kRing) * kUnitBytes + s * 2048, 16384, 1024);
-              mma_f16_ts(tmem + L::kTmemO + u * 128, tmem + L::kTmemP + (j & 1) * 64 + s * 8, db, kIdescO, j > 0 || s > 0);
+              const uint64_t db = smem_desc_sw128(base + (c % L::kRingN) * kUnitBytes + s * 2048, 16384, 1024);
+              mma_f16_ts(tmem + L::kTmemO + (i - (L::kUnits - L::kKept)) * 128, tmem + L::kTmemP + (j & 1) * 64 + s * 8, db, kIdescO,
+                         j > 0 || s > 0);
             }
-            tc_commit(&sm.empty[c % kRing]);
+            tc_commit(&sm.empty[c % L::kRingN]);
           }
           tc_commit(&sm.o_done);
+          if (kEarly < L::kUnits && j + 1 < n) {
+            tc_commit(&sm.empty[(j + 1) * L::kUnits % L::kRingN]);
+            scores(j + 1, kEarly, L::kUnits);
+          }
         }
         if (!ok) atomicExch(&sm.abort, 1);
         // the end of every MMA: the output may be read, and tensor memory given back
@@ -416,8 +470,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRowLoadRegs));
     if (n > 0) {
-      const bool ok = load_units<D, false, kRing>(a, tile, threadIdx.x - kRowLoadWarp * 32, k_first, k_last, page_shift, smem, 0u,
-                                                  sm.full, sm.empty, nullptr, sm.bad);
+      const bool ok = load_units<D, false, 1, L::kRingN>(a, tile, threadIdx.x - kRowLoadWarp * 32, k_first, k_last, page_shift,
+                                                         turn, smem, 0u, sm.full, sm.empty, nullptr, sm.bad);
       if (!ok) {
         atomicExch(&sm.abort, 1);
         if (lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
@@ -436,16 +490,16 @@ template <int D>
 cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cudaStream_t s) {
   cudaError_t e = set_max_smem_once<fp4_attention_rows_kernel<D>>(row_smem_bytes<D>());
   if (e != cudaSuccess) return e;
-  e = launch_ex(fp4_attention_rows_kernel<D>, dim3(p.tiles, p.splits), dim3(kRowThreads), row_smem_bytes<D>(), use_pdl, s, a, p.chunk,
-                page_shift_of(a.page_size));
+  e = launch_ex(fp4_attention_rows_kernel<D>, dim3(p.tiles, p.splits, RowLayout<D>::kHalves), dim3(kRowThreads), row_smem_bytes<D>(),
+                use_pdl, s, a, p.chunk, page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_ex(fp4_join_kernel<D, 128>, dim3(p.tiles, 128 / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
+  return launch_ex(fp4_join_kernel<D, 128, RowLayout<D>::kHalves>, dim3(p.tiles, 128 / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
 }
 
 }  // namespace
 
 cudaError_t launch_fp4_attention_rows(const Fp4AttentionArgs& a, const Fp4Plan& p, int D, bool use_pdl, cudaStream_t s) {
-  return D == 128 ? launch<128>(a, p, use_pdl, s) : launch<256>(a, p, use_pdl, s);
+  return D == 128 ? launch<128>(a, p, use_pdl, s) : D == 256 ? launch<256>(a, p, use_pdl, s) : launch<512>(a, p, use_pdl, s);
 }
 
 }  // namespace ckv
