@@ -41,10 +41,10 @@
 // shared memory per tile and the decoding writes 128 KB (3.1 k at 128 bytes per
 // clock).  Around its tiles a CTA spends about 20 k clocks (queries, first
 // decoding, output), which one CTA per SM cannot hide.  Measured (GB300): 1024
-// requests x 64 heads x 512 rows on average 239 us (290 TFLOP/s), a prompt of
-// 8750 tokens x 64 heads over 200-1024 rows 1.70 ms (410 TFLOP/s).
-// Slower forms: K as A of both products from shared memory (1.80 ms), decoding
-// twice so that the scores run ahead of the second product (2.21 ms).
+// requests x 64 heads x 512 rows on average 238 us (290 TFLOP/s).  Slower forms,
+// on a prompt that took 1.70 ms: K as A of both products from shared memory
+// (1.80 ms), decoding twice so that the scores run ahead of the second product
+// (2.21 ms).
 #include "fp4_attention.cuh"
 
 namespace ckv {
@@ -559,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (n > 0) {
       // ------------------------------------------------------- load and decode
-      const bool ok = load_units<D, true, L::kSlots, kRing>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, 0, smem,
-                                                     tmem + L::kTmemK, sm.full, sm.empty, sm.a_free, sm.bad);
+      const bool ok = load_units<D, true, L::kSlots, kRing>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, 0,
+                                                            smem, tmem + L::kTmemK, sm.full, sm.empty, sm.a_free, sm.bad);
       if (!ok) {
         atomicExch(&sm.abort, 1);
         if (lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
@@ -628,7 +628,8 @@ Fp4Plan plan_fp4(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
 
 int64_t fp4_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
   const Fp4Plan p = plan_fp4(T, B, H, D, max_rows);
-  return p.splits == 1 ? 0 : static_cast<int64_t>(p.tiles) * p.splits * p.R * (D + 2 * fp4_row_halves(D, p.R)) * static_cast<int64_t>(sizeof(float));
+  const int64_t row = static_cast<int64_t>(sizeof(float)) * (D + 2 * fp4_row_halves(D, p.R));
+  return p.splits == 1 ? 0 : static_cast<int64_t>(p.tiles) * p.splits * p.R * row;
 }
 
 cudaError_t launch_fp4_attention(const Fp4AttentionArgs& a, int D, bool use_pdl, cudaStream_t s) {
