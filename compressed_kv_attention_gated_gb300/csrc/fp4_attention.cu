@@ -582,7 +582,7 @@ cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cu
   e = launch_ex(fp4_attention_kernel<D, R>, dim3(p.tiles, p.splits), dim3(kThreads), smem_bytes<D, R>(), use_pdl, s, a, p.chunk,
                 page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_ex(fp4_join_kernel<D, R, 1>, dim3(p.tiles, R / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
+  return launch_ex(fp4_join_kernel<D, R, 1>, dim3(p.tiles, R * (D / 128) / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
 }
 
 template <int D>
@@ -610,7 +610,7 @@ Fp4Plan plan_fp4(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
   const double around = 5.0, tile = D == 512 ? (halves == 2 ? 2.2 : 3.5) : D == 256 ? 1.6 : 0.9, join = 4.0;
   double best = 0;
   int64_t best_s = 1;
-  for (int64_t s = 1; s <= most && s <= 64; ++s) {
+  for (int64_t s = 1; s <= most && s <= kMaxSplits; ++s) {
     const int64_t waves = (busy * s + 151) / 152;
     double us = waves * (around + tile * static_cast<double>((most + s - 1) / s));
     if (s > 1) us += join + 2.0 * static_cast<double>(busy / halves * s) * p.R * D * 4 / 4e6;

@@ -257,11 +257,14 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
   return ok;
 }
 
-// Joins the ranges of a tile: one warp per row, in the order of the ranges.
-// With kHalves == 2 two CTAs shared a range, each with half of the channels and
-// with references and sums of its own.
+// Joins the ranges of a tile, in their order: one warp per row and 128 channels, since few rows
+// over many ranges would wait for one load after the other (one request of 64 heads over 8192 rows
+// at D = 512: 38.9 us with a warp per row, 25.0 us so).  With kHalves == 2 two CTAs shared a range,
+// each with half of the channels and with references and sums of its own.
+constexpr int kMaxSplits = 64;
 template <int D, int R, int kHalves>
 __global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int splits) {
+  constexpr int kParts = D / 128, kDeep = 8;  // loads in flight
   const int lane = threadIdx.x & 31;
   pdl_wait();
   const Tile t = find_tile(a, blockIdx.x, R);
@@ -271,50 +274,55 @@ __global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ F
     if (i < t.rows) ctx_max = max(ctx_max, min(a.ctx_rows[t.tok0 + (t.base + i) / a.H], a.max_rows));
   ctx_max = __reduce_max_sync(0xFFFFFFFFu, ctx_max);
   const int used = (ctx_max + chunk - 1) / chunk;
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int work = blockIdx.y * 4 + (threadIdx.x >> 5), r = work / kParts, part = work % kParts;
   if (used <= 1 || r >= t.rows) return;
   if (a.ctx_rows[t.tok0 + (t.base + r) / a.H] < 0) return;
   const float* ws = static_cast<const float*>(a.workspace);
   const int64_t slot0 = static_cast<int64_t>(blockIdx.x) * splits;
-  const float* ml = ws + static_cast<int64_t>(gridDim.x) * splits * R * D + slot0 * kHalves * R * 2;
+  const int half = part / (kParts / kHalves);
+  const float* ml = ws + static_cast<int64_t>(gridDim.x) * splits * R * D + (slot0 * kHalves + half) * R * 2 + r;
   const int64_t flat = static_cast<int64_t>(t.tok0) * a.H + t.base + r;
-  const float sink = a.sink ? a.sink[flat % a.H] * kLog2e : -INFINITY;
-  constexpr int kQuads = D / 128 / kHalves;  // a lane's groups of four channels in a half
+  // a lane has the references and sums of ranges lane and lane + 32
+  float ref[2], l[2];
 #pragma unroll
-  for (int z = 0; z < kHalves; ++z) {
-    float m = kNegBig;
-    for (int s = lane; s < used; s += 32) m = fmaxf(m, ml[(s * kHalves + z) * 2 * R + r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    float all = 0.f;
-    if (a.sink) {
-      m = fmaxf(m, sink);
-      all = sink == m ? 1.f : fast_exp2(sink - m);
-    }
-    float acc[4 * kQuads];
-#pragma unroll
-    for (int i = 0; i < 4 * kQuads; ++i) acc[i] = 0.f;
-    for (int s = 0; s < used; ++s) {
-      const float* row = ml + (s * kHalves + z) * 2 * R + r;
-      const float l = row[R], w = fast_exp2(row[0] - m);
-      all += l == 0.f ? 0.f : l * w;
-      const float4* o = reinterpret_cast<const float4*>(ws + ((slot0 + s) * R + r) * D) + z * kQuads * 32;
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const float4 v = o[i * 32 + lane];
-        acc[4 * i] = fmaf(v.x, w, acc[4 * i]);
-        acc[4 * i + 1] = fmaf(v.y, w, acc[4 * i + 1]);
-        acc[4 * i + 2] = fmaf(v.z, w, acc[4 * i + 2]);
-        acc[4 * i + 3] = fmaf(v.w, w, acc[4 * i + 3]);
-      }
-    }
-    const float inv = all == 0.f ? 0.f : a.g / all;
-#pragma unroll
-    for (int i = 0; i < kQuads; ++i)
-      *reinterpret_cast<uint2*>(a.out + flat * D + (z * kQuads + i) * 128 + lane * 4) = make_uint2(
-          pack_bf16x2_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack_bf16x2_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
-    if (z == 0 && lane == 0 && a.lse) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+  for (int i = 0; i < 2; ++i) {
+    const int s = lane + i * 32;
+    ref[i] = s < used ? ml[s * kHalves * 2 * R] : kNegBig;
+    l[i] = s < used ? ml[s * kHalves * 2 * R + R] : 0.f;
   }
+  float m = fmaxf(ref[0], ref[1]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float sink = a.sink ? a.sink[flat % a.H] * kLog2e : -INFINITY;
+  if (a.sink) m = fmaxf(m, sink);
+  float w[2], all = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[i] = fast_exp2(ref[i] - m);
+    all += l[i] == 0.f ? 0.f : l[i] * w[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+  if (a.sink) all += sink == m ? 1.f : fast_exp2(sink - m);
+  const float4* o = reinterpret_cast<const float4*>(ws + (slot0 * R + r) * D + part * 128) + lane;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < used; s0 += kDeep) {
+    float4 v[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) v[i] = s0 + i < used ? o[static_cast<int64_t>(s0 + i) * (R * D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      const float ws_i = __shfl_sync(0xFFFFFFFFu, s0 < 32 ? w[0] : w[1], (s0 + i) % 32);
+      acc[0] = fmaf(v[i].x, ws_i, acc[0]);
+      acc[1] = fmaf(v[i].y, ws_i, acc[1]);
+      acc[2] = fmaf(v[i].z, ws_i, acc[2]);
+      acc[3] = fmaf(v[i].w, ws_i, acc[3]);
+    }
+  }
+  const float inv = all == 0.f ? 0.f : a.g / all;
+  *reinterpret_cast<uint2*>(a.out + flat * D + part * 128 + lane * 4) =
+      make_uint2(pack_bf16x2_rn(acc[0] * inv, acc[1] * inv), pack_bf16x2_rn(acc[2] * inv, acc[3] * inv));
+  if (part == 0 && lane == 0 && a.lse) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
 }
 
 }  // namespace
