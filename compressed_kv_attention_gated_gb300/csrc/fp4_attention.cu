@@ -138,34 +138,6 @@ __device__ __forceinline__ bool soft_any(bool p) {
 }
 static_assert(kSoftWarps * 32 == 256, "the softmax warps' named barrier");
 
-// Queries and first cache rows of a tile, to L2.  By one converged warp.
-template <int D, int R>
-__device__ __forceinline__ void prefetch_tile(const Fp4AttentionArgs& a, uint32_t index, int page_shift) {
-  const int lane = threadIdx.x & 31;
-  if (index >= gridDim.x) return;
-  const Tile tile = find_tile(a, index, R);
-  if (tile.rows <= 0) return;
-  auto line = [](const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); };
-  constexpr int kLines = D * 2 / 128;  // of a query row
-  for (int i = lane; i < tile.rows * kLines; i += 32) {
-    const int r = i / kLines, t = tile.tok0 + (tile.base + r) / a.H, h = tile.base + r - (t - tile.tok0) * a.H;
-    line(a.q + t * a.q_st + h * a.q_sh + i % kLines * 64);
-  }
-  const int seen = min(min(a.ctx_rows[tile.tok0 + tile.base / a.H], a.max_rows), kKeys);
-  const int32_t* table = a.table + static_cast<int64_t>(tile.b) * a.table_stride;
-  const int64_t page_bytes = fp4_page_bytes<D>(a.page_size);
-  for (int k = lane; k < seen; k += 32) {
-    const int pg = page_shift >= 0 ? k >> page_shift : k / a.page_size;
-    const int32_t page = table[pg];
-    if (page < 0 || page >= a.num_pages) continue;
-    const uint8_t* p = a.cache + page * page_bytes;
-    const int64_t row = k - pg * a.page_size;
-#pragma unroll
-    for (int x = 0; x < D / 2; x += 64) line(p + row * (D / 2) + x);
-    line(p + static_cast<int64_t>(a.page_size) * (D / 2) + row * (D / 16));
-  }
-}
-
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk,
                                                                     int page_shift) {
@@ -553,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       // The CTA that follows on this SM takes about the tile that lies a wave of CTAs (one per SM)
       // ahead; all SMs begin and end their tiles at much the same time, and its queries and first
       // keys would come from memory in that crowd.  Bring them to L2 now.
-      if (__all_sync(0xFFFFFFFFu, mbar_wait_near(&sm.q_full, 0))) prefetch_tile<D, R>(a, blockIdx.x + kSMs, page_shift);
+      if (__all_sync(0xFFFFFFFFu, mbar_wait_near(&sm.q_full, 0))) prefetch_tile<D>(a, blockIdx.x + kSMs, gridDim.x, R, page_shift);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));

@@ -257,6 +257,34 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
   return ok;
 }
 
+// Queries and first cache rows of a tile, to L2.  By one converged warp.
+template <int D>
+__device__ __forceinline__ void prefetch_tile(const Fp4AttentionArgs& a, uint32_t index, uint32_t tiles, int R, int page_shift) {
+  const int lane = threadIdx.x & 31;
+  if (index >= tiles) return;
+  const Tile tile = find_tile(a, index, R);
+  if (tile.rows <= 0) return;
+  auto line = [](const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); };
+  constexpr int kLines = D * 2 / 128;  // of a query row
+  for (int i = lane; i < tile.rows * kLines; i += 32) {
+    const int r = i / kLines, t = tile.tok0 + (tile.base + r) / a.H, h = tile.base + r - (t - tile.tok0) * a.H;
+    line(a.q + t * a.q_st + h * a.q_sh + i % kLines * 64);
+  }
+  const int seen = min(min(a.ctx_rows[tile.tok0 + tile.base / a.H], a.max_rows), kKeys);
+  const int32_t* table = a.table + static_cast<int64_t>(tile.b) * a.table_stride;
+  const int64_t page_bytes = fp4_page_bytes<D>(a.page_size);
+  for (int k = lane; k < seen; k += 32) {
+    const int pg = page_shift >= 0 ? k >> page_shift : k / a.page_size;
+    const int32_t page = table[pg];
+    if (page < 0 || page >= a.num_pages) continue;
+    const uint8_t* p = a.cache + page * page_bytes;
+    const int64_t row = k - pg * a.page_size;
+#pragma unroll
+    for (int x = 0; x < D / 2; x += 64) line(p + row * (D / 2) + x);
+    line(p + static_cast<int64_t>(a.page_size) * (D / 2) + row * (D / 16));
+  }
+}
+
 // Joins the ranges of a tile, in their order: one warp per row and 128 channels, since few rows
 // over many ranges would wait for one load after the other (one request of 64 heads over 8192 rows
 // at D = 512: 38.9 us with a warp per row, 25.0 us so).  With kHalves == 2 two CTAs shared a range,

@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   RowSmall& sm = *reinterpret_cast<RowSmall*>(smem + L::kSmall);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the CTA's half of the channels, and the unit that a tile begins with: the units of that half come last
-  const int half_v = L::kHalves == 2 ? blockIdx.z : 0, turn = L::kHalves == 2 && half_v == 0 ? 2 : 0;
+  const int half_v = L::kHalves == 2 ? blockIdx.x & 1 : 0, turn = L::kHalves == 2 && half_v == 0 ? 2 : 0;
+  const uint32_t index = blockIdx.x / L::kHalves, tiles = gridDim.x / L::kHalves;
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
     return;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   }
   pdl_wait();
   if (warp == 0) {
-    const Tile t = find_tile(a, blockIdx.x, 128);
+    const Tile t = find_tile(a, index, 128);
     if (lane == 0) {
       sm.tile = t;
       sm.ctx_max = -1;
@@ -341,11 +342,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       pair_barrier(quad);
       l += sm.part[half ^ 1][row];
       float* ws = static_cast<float*>(a.workspace);
-      const int64_t slot = static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y;
+      const int64_t slot = static_cast<int64_t>(index) * gridDim.y + blockIdx.y;
       float scale = 1.f;
       if (split) {
         if (half == 0) {
-          float* ml = ws + static_cast<int64_t>(gridDim.x) * gridDim.y * 128 * D + (slot * L::kHalves + half_v) * 128 * 2;
+          float* ml = ws + static_cast<int64_t>(tiles) * gridDim.y * 128 * D + (slot * L::kHalves + half_v) * 128 * 2;
           ml[row] = ref;
           ml[128 + row] = l;
         }
@@ -466,6 +467,10 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         if (!mbar_wait_near(&sm.drain, 0) || !ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
       }
       __syncwarp();
+    } else if (warp == kRowMmaWarp + 1 && n > 0 && half_v == 0) {
+      // as in the other form: what the CTA that follows on this SM begins with, to L2
+      if (__all_sync(0xFFFFFFFFu, mbar_wait_near(&sm.q_full, 0)))
+        prefetch_tile<D>(a, index + kSMs / L::kHalves, tiles, 128, page_shift);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRowLoadRegs));
@@ -490,7 +495,7 @@ template <int D>
 cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cudaStream_t s) {
   cudaError_t e = set_max_smem_once<fp4_attention_rows_kernel<D>>(row_smem_bytes<D>());
   if (e != cudaSuccess) return e;
-  e = launch_ex(fp4_attention_rows_kernel<D>, dim3(p.tiles, p.splits, RowLayout<D>::kHalves), dim3(kRowThreads), row_smem_bytes<D>(),
+  e = launch_ex(fp4_attention_rows_kernel<D>, dim3(p.tiles * RowLayout<D>::kHalves, p.splits), dim3(kRowThreads), row_smem_bytes<D>(),
                 use_pdl, s, a, p.chunk, page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_ex(fp4_join_kernel<D, 128, RowLayout<D>::kHalves>, dim3(p.tiles, D / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
