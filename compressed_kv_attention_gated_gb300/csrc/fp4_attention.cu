@@ -223,56 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       // ------------------------------------------------------------- softmax
       const int quad = warp & 3, half = warp >> 2;
       const int col0 = half * L::kCols;
-      // queries: a warp takes R/8 rows, a lane eight channels of a row (16 at D = 512); all
-      // loads are issued before the first is used
-      if (n > 0) {
-        constexpr int kC = D == 512 ? 16 : 8;     // channels of a lane
-        constexpr int kSpan = D / kC;             // lanes of a row
-        constexpr int kLoads = R / kSoftWarps * kSpan / 32;
-        constexpr int kBatch = kLoads < 8 ? kLoads : 8;  // rows in flight (registers)
-        const int sub = lane / kSpan, ch = lane % kSpan * kC;
-        static_assert(kLoads >= 1 && kLoads % kBatch == 0, "");
-#pragma unroll 1
-        for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
-          uint4 raw[kBatch][kC / 8];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int r = warp * (R / kSoftWarps) + (i0 + i) * (32 / kSpan) + sub;
-            const bool on = sm.out[r] >= 0;
-            const uint4* q = reinterpret_cast<const uint4*>(a.q + sm.q[r] + ch);
-#pragma unroll
-            for (int x = 0; x < kC / 8; ++x) raw[i][x] = on ? q[x] : make_uint4(0, 0, 0, 0);
-          }
-          uint32_t am[kBatch];  // the largest magnitude: bf16 bits order like the values
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            am[i] = 0;
-#pragma unroll
-            for (int x = 0; x < kC / 8; ++x) {
-              const uint32_t w[4] = {raw[i][x].x, raw[i][x].y, raw[i][x].z, raw[i][x].w};
-#pragma unroll
-              for (int y = 0; y < 4; ++y) am[i] = max(am[i], max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
-            }
-          }
-#pragma unroll
-          for (int o = 1; o < kSpan; o <<= 1) {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) am[i] = max(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int r = warp * (R / kSoftWarps) + (i0 + i) * (32 / kSpan) + sub;
-            const int se = query_exponent(am[i]);
-            const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
-            if (lane % kSpan == 0)
-              sm.c[r] = a.softmax_scale * kLog2e * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
-            uint8_t* row = smem + L::kQ + (ch / 64) * (R * 128) + r * 128;
-#pragma unroll
-            for (int x = 0; x < kC / 8; ++x)
-              *reinterpret_cast<uint4*>(row + ((((ch % 64) / 8 + x) ^ (r & 7)) * 16)) = query8(raw[i][x], up);
-          }
-        }
-      }
+      if (n > 0) load_queries<D, R, R / kSoftWarps>(a, warp * (R / kSoftWarps), sm.out, sm.q, sm.c, smem + L::kQ);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full);
@@ -531,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (n > 0) {
       // ------------------------------------------------------- load and decode
-      const bool ok = load_units<D, true, L::kSlots, kRing>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, 0,
+      const bool ok = load_units<D, true, L::kSlots, kRing, 2>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, 0,
                                                             smem, tmem + L::kTmemK, sm.full, sm.empty, sm.a_free, sm.bad);
       if (!ok) {
         atomicExch(&sm.abort, 1);

@@ -128,6 +128,124 @@ __device__ __forceinline__ uint4 query8(uint4 raw, float up) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// The largest magnitude of a lane's channels: bf16 bits order like the values.
+template <int n>
+__device__ __forceinline__ uint32_t query_magnitude(const uint4 (&raw)[n]) {
+  uint32_t two = 0;  // of the low halves and of the high ones
+#pragma unroll
+  for (int x = 0; x < n; ++x) {
+    const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) two = __vmaxu2(two, w[y] & 0x7FFF7FFFu);
+  }
+  return max(two & 0xFFFFu, two >> 16);
+}
+
+// A warp's kRows queries, from row0 on, as fp16 in blocks of R rows x 128 bytes (128-byte swizzle)
+// from `to` on, with the factors of their scores in c.  Rows with out < 0 are zeros.  A lane has
+// eight channels of a row (16 at D = 512); a batch's loads are issued before the first is used.
+template <int D, int R, int kRows>
+__device__ __forceinline__ void load_queries(const Fp4AttentionArgs& a, int row0, const int32_t* out, const int64_t* from, float* c,
+                                             uint8_t* to) {
+  constexpr int kX = D == 512 ? 2 : 1;           // 16-byte pieces of a lane
+  constexpr int kSpan = D / 8 / kX;              // lanes of a row
+  constexpr int kLoads = kRows * kSpan / 32;
+  constexpr int kBatch = kLoads < 8 ? kLoads : 8;  // rows in flight (registers)
+  static_assert(kLoads >= 1 && kLoads % kBatch == 0, "");
+  const int lane = threadIdx.x & 31, sub = lane / kSpan, ch = lane % kSpan * kX * 8;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
+    uint4 raw[kBatch][kX];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = row0 + (i0 + i) * (32 / kSpan) + sub;
+      const bool on = out[r] >= 0;
+      const uint4* q = reinterpret_cast<const uint4*>(a.q + from[r] + ch);
+#pragma unroll
+      for (int x = 0; x < kX; ++x) raw[i][x] = on ? q[x] : make_uint4(0, 0, 0, 0);
+    }
+    uint32_t am[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) am[i] = query_magnitude(raw[i]);
+#pragma unroll
+    for (int o = 1; o < kSpan; o <<= 1) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) am[i] = max(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = row0 + (i0 + i) * (32 / kSpan) + sub;
+      const int se = query_exponent(am[i]);
+      const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
+      if (lane % kSpan == 0) c[r] = a.softmax_scale * kLog2e * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
+      uint8_t* row = to + (ch / 64) * (R * 128) + r * 128;
+#pragma unroll
+      for (int x = 0; x < kX; ++x) *reinterpret_cast<uint4*>(row + ((((ch % 64) / 8 + x) ^ (r & 7)) * 16)) = query8(raw[i][x], up);
+    }
+  }
+}
+
+__device__ __forceinline__ void copies_wait(int left) {
+  switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+  }
+}
+
+// The same for more rows than registers hold (128 x 512 channels: 10 k clocks against 12.5 k in four
+// batches; with one batch the registers win): all are copied to their places as bf16 and scaled
+// there by the lanes that copied them.
+template <int D, int R, int kRows>
+__device__ __forceinline__ void copy_queries(const Fp4AttentionArgs& a, int row0, const int32_t* out, const int64_t* from, float* c,
+                                             uint8_t* to) {
+  constexpr int kX = D / 256, kGroups = 4, kDeep = kRows / kGroups;  // 16-byte pieces of a lane; rows that are scaled together
+  static_assert(D % 256 == 0 && kRows % kGroups == 0, "");
+  const int lane = threadIdx.x & 31;
+  auto place = [&](int r, int x) {
+    const int p = lane + x * 32;
+    return to + (p / 8) * (R * 128) + r * 128 + ((p % 8) ^ (r & 7)) * 16;
+  };
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      const int r = row0 + g * kDeep + i;
+      const bool on = out[r] >= 0;
+      const uint16_t* q = on ? a.q + from[r] : a.q;
+#pragma unroll
+      for (int x = 0; x < kX; ++x)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(r, x))), "l"(q + (lane + x * 32) * 8),
+                     "r"(on ? 16 : 0)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    copies_wait(kGroups - 1 - g);
+    uint4 raw[kDeep][kX];
+    uint32_t am[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+#pragma unroll
+      for (int x = 0; x < kX; ++x) raw[i][x] = *reinterpret_cast<const uint4*>(place(row0 + g * kDeep + i, x));
+    }
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) am[i] = __reduce_max_sync(0xFFFFFFFFu, query_magnitude(raw[i]));
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      const int r = row0 + g * kDeep + i;
+      const int se = query_exponent(am[i]);
+      const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
+      if (lane == 0) c[r] = a.softmax_scale * kLog2e * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
+#pragma unroll
+      for (int x = 0; x < kX; ++x) *reinterpret_cast<uint4*>(place(r, x)) = query8(raw[i][x], up);
+    }
+  }
+}
+
 // Columns of a per-row array, 16 bytes at a time.  They are read in one go before
 // anything is stored: the compiler may not move a load over a store that could alias.
 template <int n>
@@ -152,11 +270,11 @@ __device__ __forceinline__ void load_cols(const float* p, float (&v)[n]) {
 //   bad[tile & 3]      a bit per key whose page is not there, written with the tile's last unit
 // A tile's units come in channel order from unit `turn` on.  Rows that are not there are
 // zeros.  False when a wait ran out.
-template <int D, bool kCopy, int kSlots, int kRingN>
+template <int D, bool kCopy, int kSlots, int kRingN, int kGroups>
 __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile& tile, int tid, int k_first, int k_last, int page_shift,
                                            int turn, uint8_t* ring, uint32_t tmem_k, uint64_t* full, uint64_t* empty,
                                            uint64_t* a_free, uint32_t (*bad)[4]) {
-  constexpr int kUnits = D / 128, kGroups = 2, kAhead = 4;
+  constexpr int kUnits = D / 128, kAhead = kGroups == 2 ? 4 : kGroups;
   constexpr int kDeep = kAhead / kGroups;  // units of a group in registers: loads run this far ahead
   static_assert(!kCopy || kSlots == kRingN || kUnits == kRingN, "waits");
   // a thread has one key's 128 channels of a unit, that of its lane of tensor memory; neighbouring
@@ -199,7 +317,7 @@ __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile
   auto fetch = [&](Unit& x, int c) {
     if (c < total) {
       // the group's first unit of a tile
-      if (kUnits <= kGroups || c % kUnits == group) locate(c / kUnits);
+      if (kUnits <= kGroups || c % kUnits < kGroups) locate(c / kUnits);
       const int u = (c + turn) % kUnits;
       x.gone = gone;
       x.s = make_uint2(0, 0);

@@ -34,10 +34,9 @@ namespace {
 
 // Warpgroups 0 and 1: softmax; 2: its first warp issues the MMAs; 3 and 4: load and decode.
 constexpr int kRowMmaWarp = 8, kRowLoadWarp = 12;
-constexpr int kRowThreads = 640;
-// Registers per thread: 96 at launch (61,440), then 256 x 112 + 128 x 64 + 256 x 96 = 61,440.
-constexpr int kRowSoftRegs = 112, kRowMmaRegs = 64, kRowLoadRegs = 96;
-static_assert(256 * kRowSoftRegs + 128 * kRowMmaRegs + 256 * kRowLoadRegs <= kRowThreads * 96, "registers of the launch");
+// Registers per thread at launch: 640 x 96 or (D = 512) 768 x 80, 61,440 both; then 256 x 112 +
+// 128 x 64 and 256 x 96 or 384 x 64, the same.
+constexpr int kRowSoftRegs = 112, kRowMmaRegs = 64;
 
 template <int D>
 struct RowLayout {
@@ -46,6 +45,13 @@ struct RowLayout {
   static constexpr int kDV = D / kHalves;            // channels of the output that a CTA has
   static constexpr int kKept = kDV / 128;            // a tile's last units, of which they are
   static constexpr int kRingN = D == 512 ? 3 : 4;
+  // groups of four decoding warps; at D = 512 one for each place of the ring: what a tile waits for is
+  // the decoding of the units whose places its predecessor's second product gives back
+  static constexpr int kGroups = D == 512 ? 3 : 2;
+  static constexpr int kThreads = (kRowLoadWarp + kGroups * 4) * 32;
+  static constexpr int kLoadRegs = D == 512 ? 64 : 96;
+  static_assert(256 * kRowSoftRegs + 128 * kRowMmaRegs + kGroups * 128 * kLoadRegs <= kThreads * (D == 512 ? 80 : 96),
+                "registers of the launch");
   static constexpr int kSBufs = D == 128 ? 2 : 1;
   static constexpr int kQ = kRingN * kUnitBytes;     // Q: D/64 blocks of 128 rows x 128 bytes
   static constexpr int kSmall = kQ + (D / 64) * 128 * 128;
@@ -100,7 +106,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRowThreads, 1)
+__global__ void __launch_bounds__(RowLayout<D>::kThreads, 1)
     fp4_attention_rows_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int page_shift) {
   using L = RowLayout<D>;
   // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
@@ -180,54 +186,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     if (!idle) {
       const int quad = warp & 3, half = warp >> 2, row = threadIdx.x & 127;
       // ----------------------------------------------------------- queries
-      // eight channels per lane (16 at D = 512), 16 rows per warp; every load of a batch is issued before the first is used
       if (n > 0) {
-        constexpr int kC = D == 512 ? 16 : 8;  // channels of a lane
-        constexpr int kSpan = D / kC;          // lanes of a row
-        constexpr int kPer = 32 / kSpan;       // rows of a warp at a time
-        constexpr int kBatch = D == 512 ? 4 : 8;
-        const int sub = lane / kSpan, ch = lane % kSpan * kC;
-        static_assert(16 % (kBatch * kPer) == 0, "");
-#pragma unroll 1
-        for (int r0 = warp * 16; r0 < warp * 16 + 16; r0 += kBatch * kPer) {
-          uint4 raw[kBatch][kC / 8];
-          uint32_t am[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * kPer + sub;
-            const bool on = sm.out[r] >= 0;
-            const uint4* q = reinterpret_cast<const uint4*>(a.q + sm.q[r] + ch);
-#pragma unroll
-            for (int x = 0; x < kC / 8; ++x) raw[i][x] = on ? q[x] : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            am[i] = 0;  // the largest magnitude: bf16 bits order like the values
-#pragma unroll
-            for (int x = 0; x < kC / 8; ++x) {
-              const uint32_t w[4] = {raw[i][x].x, raw[i][x].y, raw[i][x].z, raw[i][x].w};
-#pragma unroll
-              for (int y = 0; y < 4; ++y) am[i] = max(am[i], max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
-            }
-          }
-#pragma unroll
-          for (int o = 1; o < kSpan; o <<= 1) {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) am[i] = max(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * kPer + sub;
-            const int se = query_exponent(am[i]);
-            const float up = __uint_as_float(static_cast<uint32_t>(se) << 23);
-            if (lane % kSpan == 0)
-              sm.c[r] = a.softmax_scale * kLog2e * a.g * __uint_as_float(static_cast<uint32_t>(254 - se) << 23);
-            uint8_t* to = smem + L::kQ + (ch / 64) * (128 * 128) + r * 128;
-#pragma unroll
-            for (int x = 0; x < kC / 8; ++x)
-              *reinterpret_cast<uint4*>(to + ((((ch % 64) / 8 + x) ^ (r & 7)) * 16)) = query8(raw[i][x], up);
-          }
-        }
+        if constexpr (D == 512)
+          copy_queries<D, 128, 16>(a, warp * 16, sm.out, sm.q, sm.c, smem + L::kQ);
+        else
+          load_queries<D, 128, 16>(a, warp * 16, sm.out, sm.q, sm.c, smem + L::kQ);
       }
       fence_proxy_async_smem();
       asm volatile("barrier.cta.sync 5, 256;" ::: "memory");  // every row's factor is there
@@ -473,9 +436,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         prefetch_tile<D>(a, index + kSMs / L::kHalves, tiles, 128, page_shift);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRowLoadRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLoadRegs));
     if (n > 0) {
-      const bool ok = load_units<D, false, 1, L::kRingN>(a, tile, threadIdx.x - kRowLoadWarp * 32, k_first, k_last, page_shift,
+      const bool ok = load_units<D, false, 1, L::kRingN, L::kGroups>(a, tile, threadIdx.x - kRowLoadWarp * 32, k_first, k_last, page_shift,
                                                          turn, smem, 0u, sm.full, sm.empty, nullptr, sm.bad);
       if (!ok) {
         atomicExch(&sm.abort, 1);
@@ -495,7 +458,7 @@ template <int D>
 cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cudaStream_t s) {
   cudaError_t e = set_max_smem_once<fp4_attention_rows_kernel<D>>(row_smem_bytes<D>());
   if (e != cudaSuccess) return e;
-  e = launch_ex(fp4_attention_rows_kernel<D>, dim3(p.tiles * RowLayout<D>::kHalves, p.splits), dim3(kRowThreads), row_smem_bytes<D>(),
+  e = launch_ex(fp4_attention_rows_kernel<D>, dim3(p.tiles * RowLayout<D>::kHalves, p.splits), dim3(RowLayout<D>::kThreads), row_smem_bytes<D>(),
                 use_pdl, s, a, p.chunk, page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_ex(fp4_join_kernel<D, 128, RowLayout<D>::kHalves>, dim3(p.tiles, D / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
