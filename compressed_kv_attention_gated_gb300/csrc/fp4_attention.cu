@@ -51,14 +51,17 @@ namespace ckv {
 namespace {
 
 // Warpgroups (4 warps) 0 and 1: softmax; 2: its first warp issues the MMAs; 3 and 4: load and decode.
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 12, kLoadWarps = 8;
-constexpr int kThreads = (kLoadWarp + kLoadWarps) * 32;
-// Registers per thread: 96 at launch (640 x 96 = 61,440), then 256 x 112 + 128 x 64 + 256 x 96 = 61,440.
-constexpr int kSoftRegs = 112, kMmaRegs = 64, kLoadRegs = 96;
-static_assert(256 * kSoftRegs + 128 * kMmaRegs + 256 * kLoadRegs <= kThreads * 96, "registers of the launch");
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 12;
+// Registers per thread at launch: 640 x 96 or (D = 512) 768 x 80, 61,440 both; then 256 x 112 +
+// 128 x 64 and 256 x 96 or 384 x 64, the same.
+constexpr int kSoftRegs = 112, kMmaRegs = 64;
 template <int D, int R>
 struct Layout {
   static constexpr int kUnits = D / 128;
+  static constexpr int kGroups = D == 512 ? 3 : 2;          // groups of four decoding warps
+  static constexpr int kThreads = (kLoadWarp + kGroups * 4) * 32;
+  static constexpr int kLoadRegs = D == 512 ? 64 : 96;
+  static_assert(256 * kSoftRegs + 128 * kMmaRegs + kGroups * 128 * kLoadRegs <= kThreads * (D == 512 ? 80 : 96), "registers");
   static constexpr bool kAhead = kUnits < kRing;            // scores of the next tile under this one's softmax
   static constexpr int kBufs = kAhead ? 2 : 1;              // of S and of P
   static constexpr int kCols = R / 2;                       // rows (columns of S^T) of a softmax thread
@@ -139,7 +142,7 @@ __device__ __forceinline__ bool soft_any(bool p) {
 static_assert(kSoftWarps * 32 == 256, "the softmax warps' named barrier");
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk,
+__global__ void __launch_bounds__((Layout<D, R>::kThreads), 1) fp4_attention_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk,
                                                                     int page_shift) {
   using L = Layout<D, R>;
   extern __shared__ uint8_t s_raw[];
@@ -479,10 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
       if (__all_sync(0xFFFFFFFFu, mbar_wait_near(&sm.q_full, 0))) prefetch_tile<D>(a, blockIdx.x + kSMs, gridDim.x, R, page_shift);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLoadRegs));
     if (n > 0) {
       // ------------------------------------------------------- load and decode
-      const bool ok = load_units<D, true, L::kSlots, kRing, 2>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, 0,
+      const bool ok = load_units<D, true, L::kSlots, kRing, L::kGroups>(a, tile, threadIdx.x - kLoadWarp * 32, k_first, k_last, page_shift, 0,
                                                             smem, tmem + L::kTmemK, sm.full, sm.empty, sm.a_free, sm.bad);
       if (!ok) {
         atomicExch(&sm.abort, 1);
@@ -502,7 +505,7 @@ template <int D, int R>
 cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cudaStream_t s) {
   cudaError_t e = set_max_smem_once<fp4_attention_kernel<D, R>>(smem_bytes<D, R>());
   if (e != cudaSuccess) return e;
-  e = launch_ex(fp4_attention_kernel<D, R>, dim3(p.tiles, p.splits), dim3(kThreads), smem_bytes<D, R>(), use_pdl, s, a, p.chunk,
+  e = launch_ex(fp4_attention_kernel<D, R>, dim3(p.tiles, p.splits), dim3(Layout<D, R>::kThreads), smem_bytes<D, R>(), use_pdl, s, a, p.chunk,
                 page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_ex(fp4_join_kernel<D, R, 1>, dim3(p.tiles, R * (D / 128) / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
