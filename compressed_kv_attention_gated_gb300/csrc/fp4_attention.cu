@@ -27,24 +27,26 @@
 // the sums.  Sums stay per thread until the end.
 //
 // Roles: 8 softmax warps (also query load and output), 1 warp that issues the
-// MMAs, 1 that brings the next CTA's first bytes to L2, 8 warps that load and
-// decode cache rows into a ring of four units of 128 keys x 128 channels.  With
-// D < 512 the ring holds more than a tile, and the scores of the next tile are
-// computed under the softmax of this one.
+// MMAs, 1 that brings the next CTA's first bytes to L2, and groups of 4 warps that
+// load and decode cache rows into a ring of four units of 128 keys x 128 channels:
+// two groups, three at D = 512.  With D < 512 the ring holds more than a tile, and
+// the scores of the next tile are computed under the softmax of this one.
 //
 // Long rows of few tiles are split over CTAs (blockIdx.y), whose partial
 // outputs (fp32) and references a second kernel joins in a fixed order.
 //
-// What bounds it (D = 512, R = 64, 128 keys, in clocks): softmax 1.6 k, then the
-// second product 2.0 k and under it the decoding of the next tile as its units
-// come free, and the first product's tail, 3 k more; the products read 256 KB of
-// shared memory per tile and the decoding writes 128 KB (3.1 k at 128 bytes per
-// clock).  Around its tiles a CTA spends about 20 k clocks (queries, first
-// decoding, output), which one CTA per SM cannot hide.  Measured (GB300): 1024
-// requests x 64 heads x 512 rows on average 238 us (290 TFLOP/s).  Slower forms,
+// What bounds it (D = 512, R = 64, 128 keys, 8 k clocks): softmax 2.7 k, then the
+// second product 2.0 k, and what is left of the next tile's decoding (its units
+// come free with the second product) and first product, 3 k; the products read
+// 256 KB of shared memory per tile and the decoding writes 128 KB (3.1 k at 128
+// bytes per clock).  Around its tiles a CTA spends about 20 k clocks (queries,
+// first decoding, output), which one CTA per SM cannot hide.  Measured (GB300):
+// 1024 requests x 64 heads x 512 rows on average 230 us (300 TFLOP/s), 512 requests
+// x 16 heads x 922-1024 rows 110 us, 8 x 64 heads x 8192 rows at D = 128 18.5 us.
+// Slower forms: decoding in one group (249 us for the first of these) or two (237),
+// in four at R <= 32 (116 us for the second; at D = 256 80 us, when two took 68);
 // on a prompt that took 1.70 ms: K as A of both products from shared memory
-// (1.80 ms), decoding twice so that the scores run ahead of the second product
-// (2.21 ms).
+// (1.80 ms), decoding twice so that the scores run ahead of the second product (2.21 ms).
 #include "fp4_attention.cuh"
 
 namespace ckv {
@@ -505,8 +507,8 @@ template <int D, int R>
 cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cudaStream_t s) {
   cudaError_t e = set_max_smem_once<fp4_attention_kernel<D, R>>(smem_bytes<D, R>());
   if (e != cudaSuccess) return e;
-  e = launch_ex(fp4_attention_kernel<D, R>, dim3(p.tiles, p.splits), dim3(Layout<D, R>::kThreads), smem_bytes<D, R>(), use_pdl, s, a, p.chunk,
-                page_shift_of(a.page_size));
+  e = launch_ex(fp4_attention_kernel<D, R>, dim3(p.tiles, p.splits), dim3(Layout<D, R>::kThreads), smem_bytes<D, R>(), use_pdl, s, a,
+                p.chunk, page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_ex(fp4_join_kernel<D, R, 1>, dim3(p.tiles, R * (D / 128) / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
 }
@@ -523,6 +525,11 @@ cudaError_t launch_d(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, 
 // the time finds best.  A CTA costs a few microseconds around its tiles, a tile of 128 rows what D
 // asks for; CTAs run in waves over the 152 SMs; split tiles write and read fp32 partials and need
 // a second launch.  Lengths are known on the host by their bound only, so ranges are of equal size.
+// Rows per tile follow those of an average request: 128 are the M side of the rows form, with two
+// CTAs per tile at D = 512, where 64 rows take the form here (256 requests x 64 heads x 922-1024
+// rows 95 us, in the rows form 156 us) and 80 the other (159 us, here 174 us).  Below D = 512 the
+// rows form's border is where this form's R = 64 would begin: 512 x 4 tokens x 32 heads at D = 128
+// went from 149 to 82 us with it.
 Fp4Plan plan_fp4(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
   Fp4Plan p;
   const int64_t rows = (T + B - 1) / B * H;  // of an average request

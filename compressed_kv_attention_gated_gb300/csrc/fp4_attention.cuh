@@ -257,18 +257,20 @@ __device__ __forceinline__ void load_cols(const float* p, float (&v)[n]) {
   }
 }
 
-// The work of 8 warps (tid 0..255): cache rows k_first .. k_last - 1 of the tile's
+// The work of kGroups x 4 warps (tid from 0): cache rows k_first .. k_last - 1 of the tile's
 // request, 128 at a time and 128 channels at a time, through the ring of units.
 // A unit is two blocks of 128 keys x 64 channels of fp16, 128 bytes per key, with
 // the 128-byte swizzle; with kCopy it also goes to tensor memory (a lane per
-// key, 64 columns, slot c % kSlots from column tmem_k on).  Two groups of 4 warps
-// take units by turns: one's waits and fences lie under the other's decoding.
+// key, 64 columns, slot c % kSlots from column tmem_k on).  The groups of 4 warps
+// take units by turns: one's waits and fences lie under the others' decoding.
 //   full[c % kRingN]   one arrival per warp of the group (4) when unit c is there
 //   empty[c % kRingN]  completed when both products are done with it
 //   a_free[c % kSlots] completed when the first product is done with it (only waited for where
 //                      kSlots < kRingN, and there a tile is kRingN units: the other waits imply it)
 //   bad[tile & 3]      a bit per key whose page is not there, written with the tile's last unit
-// A tile's units come in channel order from unit `turn` on.  Rows that are not there are
+// Units are given back in their order: a place may be used by several groups, and a
+// group tells the phases of its barriers apart because the unit before last there is
+// older than one that it has seen given back.  A tile's units come in channel order from unit `turn` on.  Rows that are not there are
 // zeros.  False when a wait ran out.
 template <int D, bool kCopy, int kSlots, int kRingN, int kGroups>
 __device__ __forceinline__ bool load_units(const Fp4AttentionArgs& a, const Tile& tile, int tid, int k_first, int k_last, int page_shift,

@@ -18,15 +18,16 @@
 // shared memory there and the ring has three places; only the units of the CTA's
 // own half stay for the second product, so they come last in a tile.
 //
-// What bounds it: with D = 128 the softmax; with D = 512 the chain of a tile, as the
-// ring has no place for the next tile's units before the second product gives
-// them back: softmax 1.6 k clocks, second product 0.5 k, scores 1.5 k (both
-// operands from shared memory, 256 bytes per clock of the products).
-// Measured (GB300): 512 requests x 4 tokens x 32 heads at D = 128, 0-2048 rows 66 us
-// (520 TFLOP/s); D = 512, a prompt of 8750 tokens x 64 heads over 200-1024 rows
-// 1.63 ms (430 TFLOP/s), 256 x 128 heads x 922-1024 rows 161 us; the other form
-// takes 1.70 ms and 180 us.  Slower: D = 128 with two CTAs of 9 warps per SM (109 us,
-// when one took 82).
+// What bounds it: with D = 128 the softmax; with D = 512 the chain of a tile (5.5 k
+// clocks), as the ring has no place for the next tile's units before the second
+// product gives them back: softmax 1.6 k, second product 0.8 k, decoding of three
+// units by a group each and scores 3 k.  Around its tiles a CTA of D = 512 spends 20 k
+// clocks: queries 10 k, output 4.5 k, first tile.
+// Measured (GB300): 512 requests x 4 tokens x 32 heads at D = 128, 0-2048 rows 65 us
+// (530 TFLOP/s); D = 512, a prompt of 8750 tokens x 64 heads over 200-1024 rows
+// 1.39 ms (510 TFLOP/s; two decoding groups 1.49 ms, and queries through registers
+// 1.58 ms; the other form 1.70 ms).  Slower: D = 128 with two CTAs of 9 warps per
+// SM (109 us, when one took 82).
 #include "fp4_attention.cuh"
 
 namespace ckv {
