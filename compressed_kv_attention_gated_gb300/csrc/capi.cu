@@ -668,7 +668,7 @@ ckv_status ckv_fp4_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_st
       max_pages < 0 || table_stride < max_pages || !cache_scale_ok(cache_scale) || !std::isfinite(softmax_scale))
     return CKV_ERR_SHAPE;
   if (T == 0 || B == 0) return CKV_OK;
-  if (max_rows < 1 || max_rows > INT32_MAX - 1024 || max_rows > static_cast<int64_t>(max_pages) * page_size ||
+  if (max_rows < 1 || max_rows > INT32_MAX - 16384 || max_rows > static_cast<int64_t>(max_pages) * page_size ||
       T > INT32_MAX / H || q_stride_t < 0 || q_stride_h < 0)
     return CKV_ERR_SHAPE;
   if (!q || !kv_cache || !block_table || !row_start || !ctx_rows || !out) return CKV_ERR_NULL;
@@ -679,6 +679,10 @@ ckv_status ckv_fp4_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_st
   const int64_t need = ckv::fp4_attention_workspace(T, B, H, D, max_rows);
   if (need > 0 && !workspace) return CKV_ERR_NULL;
   if (workspace_bytes < need) return CKV_ERR_SHAPE;
+  // several CTAs read a query row, and one may have written its output before another has read
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t q1 = q0 + ((T - 1) * q_stride_t + (H - 1) * q_stride_h + D) * sizeof(uint16_t), o1 = o0 + T * H * D * sizeof(uint16_t);
+  if (q0 < o1 && o0 < q1) return CKV_ERR_SHAPE;
   ckv::Fp4AttentionArgs a{};
   a.q = q;
   a.q_st = q_stride_t;

@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(RowLayout<D>::kThreads, 1)
   const int half_v = L::kHalves == 2 ? blockIdx.x & 1 : 0, turn = L::kHalves == 2 && half_v == 0 ? 2 : 0;
   const uint32_t index = blockIdx.x / L::kHalves, tiles = gridDim.x / L::kHalves;
   if (smem_u32(smem) & 1023u) {
+    pdl_wait();  // whoever follows in the stream counts on what came before having ended
     if (threadIdx.x == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
     return;
   }

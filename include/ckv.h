@@ -631,11 +631,12 @@ ckv_status ckv_fp4_load(const uint8_t* kv_cache, int64_t num_pages, int32_t page
  * block_table  device int32, request b's row at b * table_stride (>= max_pages).  A page
  *            id outside [0, num_pages) sets CKV_DEVERR_CACHE_LOC; its rows count as unseen.
  * row_start  device int32 [B + 1], non-decreasing from 0 on.   ctx_rows device int32 [T].
- * max_rows   host bound of ctx_rows (1 <= max_rows <= max_pages * page_size): larger entries
+ * max_rows   host bound of ctx_rows (1 <= max_rows <= max_pages * page_size, < 2^31 - 2^14): larger entries
  *            set CKV_DEVERR_SEQ_LEN and are clamped.  It chooses how far the rows are
  *            split over CTAs, so a tight bound is faster.
  * sink       device fp32 [H], nullable.
- * out        device bf16 [T][H][D] contiguous.    lse  device fp32 [T][H], nullable.
+ * out        device bf16 [T][H][D] contiguous, apart from q (the spans of memory from first to
+ *            last element may not overlap).    lse  device fp32 [T][H], nullable.
  * H          1..1024.    D  128, 256 or 512.    B <= 65536.
  * workspace  device, 16-byte aligned, ckv_fp4_attention_workspace() bytes (may be NULL when
  *            that is 0); its contents need no initial value and do not outlive the call.

@@ -115,6 +115,16 @@ def test_fp4_attention_refusals(lib, change, status):
     assert _call(lib.ckv_fp4_attention, ATTN, **change) == status
 
 
+def test_fp4_attention_limits(lib):
+    # ranges of cache rows are counted in 32 bits, rounded up to 128 rows per range
+    wide = dict(mp=2 ** 25, tstride=2 ** 25, ps=64, ws=ONE, wsb=2 ** 62, out=P(1 << 40))
+    assert _call(lib.ckv_fp4_attention, ATTN, **wide, rows=2 ** 31 - 2 ** 14) == 2
+    # an output over the queries: whole, by one element at either end
+    span = ((ATTN["T"] - 1) * 1024 + 7 * 128 + 128) * 2
+    for q, out in ((1 << 20, 1 << 20), (1 << 20, (1 << 20) + span - 16), ((1 << 20) + 4 * 8 * 128 * 2 - 16, 1 << 20)):
+        assert _call(lib.ckv_fp4_attention, ATTN, ws=ONE, wsb=2 ** 62, q=P(q), out=P(out)) == 2
+
+
 def test_fp4_attention_workspace_is_asked_for(lib):
     assert lib.ckv_fp4_attention_workspace(0, 4, 8, 128, 10) == 0
     assert lib.ckv_fp4_attention_workspace(1, 1, 8, 192, 10) == 0
