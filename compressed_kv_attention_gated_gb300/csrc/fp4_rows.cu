@@ -50,14 +50,14 @@ __global__ void __launch_bounds__(kRowThreads) fp4_store_kernel(const __grid_con
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.rows) + r * a.stride + blk * kFp4Block);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 f = __ldg(p + i);
+      const float4 f = p[i];
       x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
     }
   } else {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.rows) + r * a.stride + blk * kFp4Block);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint4 w = __ldg(p + i);
+      const uint4 w = p[i];
       x[8 * i] = bf16_lo(w.x), x[8 * i + 1] = bf16_hi(w.x), x[8 * i + 2] = bf16_lo(w.y), x[8 * i + 3] = bf16_hi(w.y);
       x[8 * i + 4] = bf16_lo(w.z), x[8 * i + 5] = bf16_hi(w.z), x[8 * i + 6] = bf16_lo(w.w), x[8 * i + 7] = bf16_hi(w.w);
     }

@@ -165,8 +165,8 @@ __device__ __forceinline__ void norm_heads(const NormRopeArgs& a, const ckv_norm
         const int k = base[g][0] + 2 * j - a.rope_offset;
         const bool in = k >= 0 && k < a.rope_dim;
         in_span[g] |= in ? 1u << j : 0u;
-        co[j] = in ? __ldg(cs + (k >> 1)) : 1.f;
-        si[j] = in ? __ldg(cs + half + (k >> 1)) : 0.f;
+        co[j] = in ? cs[k >> 1] : 1.f;
+        si[j] = in ? cs[half + (k >> 1)] : 0.f;
       }
       c2[g][0] = Two(co[0], co[1]), c2[g][1] = Two(co[2], co[3]);
       s2[g][0] = Two(si[0], si[1]), s2[g][1] = Two(si[2], si[3]);
@@ -175,8 +175,8 @@ __device__ __forceinline__ void norm_heads(const NormRopeArgs& a, const ckv_norm
       if ((g * 32 + sl) * 8 < a.rope_dim) {
         const int p = base[g][0] - a.rope_offset;
         in_span[g] = 1;
-        co = __ldg(reinterpret_cast<const float4*>(cs + p));
-        si = __ldg(reinterpret_cast<const float4*>(cs + half + p));
+        co = *reinterpret_cast<const float4*>(cs + p);
+        si = *reinterpret_cast<const float4*>(cs + half + p);
       }
       c2[g][0] = Two(co.x, co.y), c2[g][1] = Two(co.z, co.w);
       s2[g][0] = Two(si.x, si.y), s2[g][1] = Two(si.z, si.w);
@@ -187,8 +187,8 @@ __device__ __forceinline__ void norm_heads(const NormRopeArgs& a, const ckv_norm
         const int c = base[g][0] + j, k = c - a.rope_offset;
         const bool in = k >= 0 && k < a.rope_dim, second = k >= half;
         const int p = second ? k - half : k, o = !in ? c : second ? c - half : c + half;
-        co[j] = in ? __ldg(cs + p) : 1.f;
-        si[j] = !in ? 0.f : second ? __ldg(cs + half + p) : -__ldg(cs + half + p);
+        co[j] = in ? cs[p] : 1.f;
+        si[j] = !in ? 0.f : second ? cs[half + p] : -cs[half + p];
         mate[g][j] = (o & 7) * (D / 8) + (o >> 3);
       }
 #pragma unroll
@@ -199,7 +199,7 @@ __device__ __forceinline__ void norm_heads(const NormRopeArgs& a, const ckv_norm
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 f = m.weight ? __ldg(reinterpret_cast<const float4*>(m.weight + base[g][i])) : make_float4(1.f, 1.f, 1.f, 1.f);
+      const float4 f = m.weight ? *reinterpret_cast<const float4*>(m.weight + base[g][i]) : make_float4(1.f, 1.f, 1.f, 1.f);
       w[g][2 * i] = Two(f.x, f.y);
       w[g][2 * i + 1] = Two(f.z, f.w);
     }
