@@ -510,7 +510,7 @@ cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cu
   e = launch_ex(fp4_attention_kernel<D, R>, dim3(p.tiles, p.splits), dim3(Layout<D, R>::kThreads), smem_bytes<D, R>(), use_pdl, s, a,
                 p.chunk, page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_ex(fp4_join_kernel<D, R, 1>, dim3(p.tiles, R * (D / 128) / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
+  return launch_join<D, R, 1>(a, p, s);
 }
 
 template <int D>
@@ -534,19 +534,20 @@ Fp4Plan plan_fp4(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
   Fp4Plan p;
   const int64_t rows = (T + B - 1) / B * H;  // of an average request
   p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : D == 512 && rows <= 64 ? 64 : 128;
-  p.tiles = static_cast<int>(T * H / p.R + B);
+  p.tiles = static_cast<int>((T * H + static_cast<int64_t>(B) * fp4_tile_pad(H, p.R)) / p.R);
   int64_t busy = (T * H + p.R - 1) / p.R;
   busy = busy < T && busy < B ? (T < B ? T : B) : busy;
   const int64_t most = (max_rows + kKeys - 1) / kKeys;
   const int halves = fp4_row_halves(D, p.R);
   busy *= halves;
-  const double around = 5.0, tile = D == 512 ? (halves == 2 ? 2.2 : 3.5) : D == 256 ? 1.6 : 0.9, join = 4.0;
+  const double around = D == 512 ? 8.0 : 6.0;
+  const double tile = D == 512 ? (halves == 2 ? 2.2 : p.R == 64 ? 3.5 : 2.5) : D == 256 ? (p.R == 128 ? 1.4 : 1.2) : p.R == 128 ? 1.0 : 0.6;
   double best = 0;
   int64_t best_s = 1;
   for (int64_t s = 1; s <= most && s <= kMaxSplits; ++s) {
     const int64_t waves = (busy * s + 151) / 152;
     double us = waves * (around + tile * static_cast<double>((most + s - 1) / s));
-    if (s > 1) us += join + 2.0 * static_cast<double>(busy / halves * s) * p.R * D * 4 / 4e6;
+    if (s > 1) us += 2.0 + 0.02 * static_cast<double>(s) + 2.0 * static_cast<double>(busy / halves * s) * p.R * D * 4 / 4e6;
     if (s == 1 || us < best) {
       best = us;
       best_s = s;

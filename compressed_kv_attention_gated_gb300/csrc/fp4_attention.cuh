@@ -35,8 +35,7 @@ cudaError_t launch_fp4_attention_rows(const Fp4AttentionArgs& a, const Fp4Plan& 
 
 namespace {
 
-// Which request and rows a tile has.  Request b's tiles start at
-// floor(row_start[b] * H / R) + b: increasing, and never fewer than it needs.
+// Which request and rows a tile has.
 struct Tile {
   int32_t tok0, ntok;  // the request's ragged rows
   int32_t b;
@@ -47,14 +46,23 @@ __device__ __forceinline__ int32_t start_of(const Fp4AttentionArgs& a, int32_t b
   return min(max(a.row_start[b], 0), static_cast<int32_t>(a.T));
 }
 
+// Tiles begin anew with every request: request b's first tile is (r_b + b (R - g)) / R with r_b
+// the (token, head) rows before it and g = gcd(H, R), which all r_b and R are multiples of.  That
+// leaves it ceil(rows / R) tiles at least, and none over where tokens are whole tiles.
+__host__ __device__ inline int fp4_tile_pad(int H, int R) {
+  const int g = H & -H;  // R is a power of two
+  return g < R ? R - g : 0;
+}
+
 // By one converged warp.
 __device__ __forceinline__ Tile find_tile(const Fp4AttentionArgs& a, int32_t tile, int R) {
   const int lane = threadIdx.x & 31;
+  const int64_t pad = fp4_tile_pad(a.H, R);
   int lo = 0, n = a.B;  // the request is in [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int i = lo + lane * step;
-    const bool le = lane * step < n && start_of(a, i) * static_cast<int64_t>(a.H) / R + i <= tile;
+    const bool le = lane * step < n && (start_of(a, i) * static_cast<int64_t>(a.H) + i * pad) / R <= tile;
     const uint32_t m = __ballot_sync(0xFFFFFFFFu, le);
     const int last = m ? 31 - __clz(m) : 0;
     lo += last * step;
@@ -64,7 +72,7 @@ __device__ __forceinline__ Tile find_tile(const Fp4AttentionArgs& a, int32_t til
   t.b = lo;
   t.tok0 = start_of(a, lo);
   t.ntok = start_of(a, lo + 1) - t.tok0;
-  t.base = (tile - static_cast<int32_t>(t.tok0 * static_cast<int64_t>(a.H) / R + lo)) * R;
+  t.base = (tile - static_cast<int32_t>((t.tok0 * static_cast<int64_t>(a.H) + lo * pad) / R)) * R;
   t.rows = t.base < 0 ? 0 : min(R, t.ntok * a.H - t.base);  // base < 0: row_start does not begin with 0
   return t;
 }
@@ -406,13 +414,15 @@ __device__ __forceinline__ void prefetch_tile(const Fp4AttentionArgs& a, uint32_
 }
 
 // Joins the ranges of a tile, in their order: one warp per row and 128 channels, since few rows
-// over many ranges would wait for one load after the other (one request of 64 heads over 8192 rows
-// at D = 512: 38.9 us with a warp per row, 25.0 us so).  With kHalves == 2 two CTAs shared a range,
-// each with half of the channels and with references and sums of its own.
-constexpr int kMaxSplits = 64;
-template <int D, int R, int kHalves>
-__global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int splits) {
-  constexpr int kParts = D / 128, kDeep = 8;  // loads in flight
+// over many ranges would wait for one load after the other.  One request of 64 heads over 8192 rows
+// at D = 512 takes 38.9 us with a warp per row, 25.0 us so, and 18.5 us with 16 loads in flight
+// instead of what 32 registers hold.  With few ranges many warps hide the latency instead (kFew:
+// 600 tokens x 16 heads over 2048 rows in two ranges at D = 128, 28.1 -> 23.0 us).  With kHalves == 2 two CTAs shared a range, each with half of
+// the channels and with references and sums of its own.
+constexpr int kMaxSplits = 160, kFewSplits = 4;
+template <int D, int R, int kHalves, bool kFew>
+__global__ void __launch_bounds__(128, kFew ? 12 : 4) fp4_join_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int splits) {
+  constexpr int kParts = D / 128, kDeep = kFew ? kFewSplits : 16;  // loads in flight (the second bound leaves them registers)
   const int lane = threadIdx.x & 31;
   pdl_wait();
   const Tile t = find_tile(a, blockIdx.x, R);
@@ -430,22 +440,24 @@ __global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ F
   const int half = part / (kParts / kHalves);
   const float* ml = ws + static_cast<int64_t>(gridDim.x) * splits * R * D + (slot0 * kHalves + half) * R * 2 + r;
   const int64_t flat = static_cast<int64_t>(t.tok0) * a.H + t.base + r;
-  // a lane has the references and sums of ranges lane and lane + 32
-  float ref[2], l[2];
+  // a lane has the references and sums of ranges lane, lane + 32, ...
+  constexpr int kOwn = kFew ? 1 : kMaxSplits / 32;
+  float ref[kOwn], l[kOwn], m = kNegBig;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kOwn; ++i) {
     const int s = lane + i * 32;
     ref[i] = s < used ? ml[s * kHalves * 2 * R] : kNegBig;
     l[i] = s < used ? ml[s * kHalves * 2 * R + R] : 0.f;
   }
-  float m = fmaxf(ref[0], ref[1]);
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) m = fmaxf(m, ref[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   const float sink = a.sink ? a.sink[flat % a.H] * kLog2e : -INFINITY;
   if (a.sink) m = fmaxf(m, sink);
-  float w[2], all = 0.f;
+  float w[kOwn], all = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kOwn; ++i) {
     w[i] = fast_exp2(ref[i] - m);
     all += l[i] == 0.f ? 0.f : l[i] * w[i];
   }
@@ -454,23 +466,34 @@ __global__ void __launch_bounds__(128) fp4_join_kernel(const __grid_constant__ F
   if (a.sink) all += sink == m ? 1.f : fast_exp2(sink - m);
   const float4* o = reinterpret_cast<const float4*>(ws + (slot0 * R + r) * D + part * 128) + lane;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s0 = 0; s0 < used; s0 += kDeep) {
-    float4 v[kDeep];
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i) v[i] = s0 + i < used ? o[static_cast<int64_t>(s0 + i) * (R * D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < kOwn; ++j) {
+    for (int s0 = j * 32; s0 < min(used, j * 32 + 32); s0 += kDeep) {
+      float4 v[kDeep];
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i) {
-      const float ws_i = __shfl_sync(0xFFFFFFFFu, s0 < 32 ? w[0] : w[1], (s0 + i) % 32);
-      acc[0] = fmaf(v[i].x, ws_i, acc[0]);
-      acc[1] = fmaf(v[i].y, ws_i, acc[1]);
-      acc[2] = fmaf(v[i].z, ws_i, acc[2]);
-      acc[3] = fmaf(v[i].w, ws_i, acc[3]);
+      for (int i = 0; i < kDeep; ++i)
+        v[i] = s0 + i < used ? o[static_cast<int64_t>(s0 + i) * (R * D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        const float x = __shfl_sync(0xFFFFFFFFu, w[j], (s0 + i) % 32);
+        acc[0] = fmaf(v[i].x, x, acc[0]);
+        acc[1] = fmaf(v[i].y, x, acc[1]);
+        acc[2] = fmaf(v[i].z, x, acc[2]);
+        acc[3] = fmaf(v[i].w, x, acc[3]);
+      }
     }
   }
   const float inv = all == 0.f ? 0.f : a.g / all;
   *reinterpret_cast<uint2*>(a.out + flat * D + part * 128 + lane * 4) =
       make_uint2(pack_bf16x2_rn(acc[0] * inv, acc[1] * inv), pack_bf16x2_rn(acc[2] * inv, acc[3] * inv));
   if (part == 0 && lane == 0 && a.lse) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+}
+
+template <int D, int R, int kHalves>
+cudaError_t launch_join(const Fp4AttentionArgs& a, const Fp4Plan& p, cudaStream_t s) {
+  const dim3 grid(p.tiles, R * (D / 128) / 4);
+  return p.splits <= kFewSplits ? launch_ex(fp4_join_kernel<D, R, kHalves, true>, grid, dim3(128), 0, true, s, a, p.chunk, p.splits)
+                                : launch_ex(fp4_join_kernel<D, R, kHalves, false>, grid, dim3(128), 0, true, s, a, p.chunk, p.splits);
 }
 
 }  // namespace

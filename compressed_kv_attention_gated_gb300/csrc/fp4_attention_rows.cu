@@ -463,7 +463,7 @@ cudaError_t launch(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, cu
   e = launch_ex(fp4_attention_rows_kernel<D>, dim3(p.tiles * RowLayout<D>::kHalves, p.splits), dim3(RowLayout<D>::kThreads), row_smem_bytes<D>(),
                 use_pdl, s, a, p.chunk, page_shift_of(a.page_size));
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_ex(fp4_join_kernel<D, 128, RowLayout<D>::kHalves>, dim3(p.tiles, D / 4), dim3(128), 0, true, s, a, p.chunk, p.splits);
+  return launch_join<D, 128, RowLayout<D>::kHalves>(a, p, s);
 }
 
 }  // namespace
