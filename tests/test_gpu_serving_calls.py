@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import serving_reference as ref
-from test_gpu_serving_ops import _attn_inputs, _err, _i32, _maps_case, _rope_table
+from test_gpu_serving_ops import _attn_check, _attn_inputs, _err, _i32, _maps_case, _rope_table
 
 pytestmark = pytest.mark.gpu
 GUARD = 4096
@@ -305,3 +305,22 @@ def test_norm_rope_large_strides(ck):
     assert torch.equal(a, b)
     ck.ckv_qk_norm_rope(x, pos, table, q_out=x)
     assert torch.equal(x.contiguous(), b)
+
+
+@pytest.mark.parametrize("D", [128, 512])
+@pytest.mark.parametrize("H", [1, 2, 3, 6, 8, 12, 24, 48, 96, 160])
+def test_fp4_attention_tiles_of_ragged_requests(ck, D, H):
+    """Tiles are counted without room to spare: every row of requests of 0 to 5 tokens has one,
+    whatever the common divisor of the heads and a tile's rows."""
+    rng = np.random.default_rng(H)
+    for most in (1, 2, 5):
+        n = rng.integers(0, most + 1, 33)
+        n[0], n[-1] = most, most
+        _attn_check(ck, rng, n, rng.integers(0, 40, int(n.sum())), H, D, 16, False)
+
+
+@pytest.mark.parametrize("D,H,rows", [(128, 4, 131149), (128, 40, 60000), (512, 4, 50001), (512, 70, 30000)])
+def test_fp4_attention_many_ranges(ck, D, H, rows):
+    """One request over so many rows that they are split into more ranges than a warp has lanes."""
+    rng = np.random.default_rng(rows)
+    _attn_check(ck, rng, np.array([1]), [rows], H, D, 64, True)
