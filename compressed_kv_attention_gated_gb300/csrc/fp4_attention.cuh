@@ -175,10 +175,15 @@ __device__ __forceinline__ void load_queries(const Fp4AttentionArgs& a, int row0
     uint32_t am[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) am[i] = query_magnitude(raw[i]);
+    if constexpr (kSpan == 32) {
 #pragma unroll
-    for (int o = 1; o < kSpan; o <<= 1) {
+      for (int i = 0; i < kBatch; ++i) am[i] = __reduce_max_sync(0xFFFFFFFFu, am[i]);
+    } else {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) am[i] = max(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
+      for (int o = 1; o < kSpan; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) am[i] = max(am[i], __shfl_xor_sync(0xFFFFFFFFu, am[i], o));
+      }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
