@@ -348,13 +348,7 @@ __global__ void __launch_bounds__((Layout<D, R>::kThreads), 1) fp4_attention_ker
         if (lane == 0) mbar_arrive(&sm.p_full[j & 1]);
       }
       // --------------------------------------------------------------- output
-      if (n > 0 && ok) {
-        // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's
-        ok = mbar_wait_near(&sm.drain, 0);
-        __syncwarp();
-        tc_fence_after();
-      }
-      if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+      // the rows' factors while the last products still run
       const float sum = reduce_columns<L::kCols, false>(l, lane);
       constexpr int kShare = 32 / L::kCols;
       soft_barrier();
@@ -387,6 +381,13 @@ __global__ void __launch_bounds__((Layout<D, R>::kThreads), 1) fp4_attention_ker
       }
       soft_barrier();
       load_cols<L::kCols>(&sm.c[col0], l);
+      if (n > 0 && ok) {
+        // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's
+        ok = mbar_wait_near(&sm.drain, 0);
+        __syncwarp();
+        tc_fence_after();
+      }
+      if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
 #pragma unroll 1
       for (int u = 0; u < L::kUnits; ++u) {
         float o[L::kCols];

@@ -294,13 +294,6 @@ __global__ void __launch_bounds__(RowLayout<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[j & 1]);
       }
-      if (n > 0 && ok) {
-        // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's
-        ok = mbar_wait_near(&sm.drain, 0);
-        __syncwarp();
-        tc_fence_after();
-      }
-      if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
       // ------------------------------------------------------------ output
       pair_barrier(quad);
       sm.part[half][row] = l;
@@ -327,6 +320,13 @@ __global__ void __launch_bounds__(RowLayout<D>::kThreads, 1)
         scale = all == 0.f ? 0.f : keep * a.g / all;
         if (a.lse && my_flat >= 0 && half == 0 && half_v == 0) a.lse[my_flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
       }
+      if (n > 0 && ok) {
+        // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's
+        ok = mbar_wait_near(&sm.drain, 0);
+        __syncwarp();
+        tc_fence_after();
+      }
+      if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
 #pragma unroll 1
       for (int i = half * (L::kDV / 2); i < (half + 1) * (L::kDV / 2); i += 32) {
         float o[32];
