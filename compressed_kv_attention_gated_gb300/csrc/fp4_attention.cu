@@ -39,12 +39,13 @@
 // second product 2.0 k, and what is left of the next tile's decoding (its units
 // come free with the second product) and first product, 3 k; the products read
 // 256 KB of shared memory per tile and the decoding writes 128 KB (3.1 k at 128
-// bytes per clock).  Around its tiles a CTA spends about 20 k clocks (queries,
-// first decoding, output), which one CTA per SM cannot hide.  Measured (GB300):
-// 1024 requests x 64 heads x 512 rows on average 230 us (300 TFLOP/s), 512 requests
-// x 16 heads x 922-1024 rows 110 us, 8 x 64 heads x 8192 rows at D = 128 18.5 us.
-// Slower forms: decoding in one group (249 us for the first of these) or two (237),
-// in four at R <= 32 (116 us for the second; at D = 256 80 us, when two took 68);
+// bytes per clock).  Around its tiles a CTA spends about 18 k clocks (setup 3 k,
+// queries 8.5 k, output 5 k), which one CTA per SM cannot hide.  Measured (GB300):
+// 1024 requests x 64 heads x 512 rows on average 203 us (340 TFLOP/s), 512 requests
+// x 16 heads x 922-1024 rows 104 us, one request of 16 heads over 131,072 rows 32 us.
+// Slower forms: decoding in two groups (237 us for the first of these, when three
+// took 230), in four at R <= 32 (116 us for the second, when three took 110; at
+// D = 256 80 us, when two took 68); output straight from registers (211 us, when 206);
 // on a prompt that took 1.70 ms: K as A of both products from shared memory
 // (1.80 ms), decoding twice so that the scores run ahead of the second product (2.21 ms).
 #include "fp4_attention.cuh"
@@ -526,9 +527,11 @@ cudaError_t launch_d(const Fp4AttentionArgs& a, const Fp4Plan& p, bool use_pdl, 
 // the time finds best.  A CTA costs a few microseconds around its tiles, a tile of 128 rows what D
 // asks for; CTAs run in waves over the 152 SMs; split tiles write and read fp32 partials and need
 // a second launch.  Lengths are known on the host by their bound only, so ranges are of equal size.
+// Against counts from 1 to 152 on 48 shapes the model's took at most 5% more than the best for all
+// but three (13%).
 // Rows per tile follow those of an average request: 128 are the M side of the rows form, with two
 // CTAs per tile at D = 512, where 64 rows take the form here (256 requests x 64 heads x 922-1024
-// rows 95 us, in the rows form 156 us) and 80 the other (159 us, here 174 us).  Below D = 512 the
+// rows 95 us, when the rows form took 156) and 80 the other (159 us, when this one took 174).  Below D = 512 the
 // rows form's border is where this form's R = 64 would begin: 512 x 4 tokens x 32 heads at D = 128
 // went from 149 to 82 us with it.
 Fp4Plan plan_fp4(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {

@@ -422,8 +422,9 @@ __device__ __forceinline__ void prefetch_tile(const Fp4AttentionArgs& a, uint32_
 // over many ranges would wait for one load after the other.  One request of 64 heads over 8192 rows
 // at D = 512 takes 38.9 us with a warp per row, 25.0 us so, and 18.5 us with 16 loads in flight
 // instead of what 32 registers hold.  With few ranges many warps hide the latency instead (kFew:
-// 600 tokens x 16 heads over 2048 rows in two ranges at D = 128, 28.1 -> 23.0 us).  With kHalves == 2 two CTAs shared a range, each with half of
-// the channels and with references and sums of its own.
+// 600 tokens x 16 heads over 2048 rows in two ranges at D = 128, 28.1 -> 23.0 us).  With kHalves
+// == 2 two CTAs shared a range, each with half of the channels and with references and sums of
+// its own.
 constexpr int kMaxSplits = 160, kFewSplits = 4;
 template <int D, int R, int kHalves, bool kFew>
 __global__ void __launch_bounds__(128, kFew ? 12 : 4) fp4_join_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int splits) {

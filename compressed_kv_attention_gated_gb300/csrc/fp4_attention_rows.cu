@@ -21,13 +21,15 @@
 // What bounds it: with D = 128 the softmax; with D = 512 the chain of a tile (5.5 k
 // clocks), as the ring has no place for the next tile's units before the second
 // product gives them back: softmax 1.6 k, second product 0.8 k, decoding of three
-// units by a group each and scores 3 k.  Around its tiles a CTA of D = 512 spends 20 k
-// clocks: queries 10 k, output 4.5 k, first tile.
-// Measured (GB300): 512 requests x 4 tokens x 32 heads at D = 128, 0-2048 rows 65 us
-// (530 TFLOP/s); D = 512, a prompt of 8750 tokens x 64 heads over 200-1024 rows
-// 1.39 ms (510 TFLOP/s; two decoding groups 1.49 ms, and queries through registers
-// 1.58 ms; the other form 1.70 ms).  Slower: D = 128 with two CTAs of 9 warps per
-// SM (109 us, when one took 82).
+// units by a group each and scores 3 k.  Around its tiles a CTA of D = 512 spends 18 k
+// clocks: queries 10 k, output 4 k, first tile.
+// Measured (GB300): 512 requests x 4 tokens x 32 heads at D = 128, 0-2048 rows 63 us
+// (540 TFLOP/s); D = 512, a prompt of 8750 tokens x 64 heads over 200-1024 rows
+// 1.36-1.39 ms (510 TFLOP/s; with two decoding groups 1.49 ms, when three took 1.39,
+// with queries through registers 1.58 ms, when copies took 1.49; the other form
+// 1.70 ms).  Slower: D = 128 with two CTAs of 9 warps per SM (109 us, when one took
+// 82), and four lanes per key in the decoding's loads (65.3 us, when one took 64.2;
+// at D = 512 1.37 ms, when one took 1.39).
 #include "fp4_attention.cuh"
 
 namespace ckv {

@@ -13,7 +13,10 @@
 // and per quotient one Newton step on the remainder (Markstein's method: the result
 // is the correctly rounded quotient).
 //
-// Bound by HBM (2-4 bytes in and 9/16 out per channel, or the reverse).  One
+// Bound by HBM (2-4 bytes in and 9/16 out per channel, or the reverse) when there
+// are many rows.  Measured (GB300): 65,536 rows of 128 channels, bf16, 6.7 us a call
+// (3.2 TB/s): launch, two round trips and about 3 us of instructions; two blocks
+// per thread with their loads in flight together gained 1%.  One
 // thread per block of 16 channels: D/16 neighbouring threads write a row's D/2
 // code bytes (8 each) and D/16 scale bytes.
 #include <cstdint>

@@ -17,7 +17,8 @@
 // Every CTA scans the lengths of all requests into shared memory (12 bytes per
 // request), so one launch does it all; then the tokens are spread over the
 // grid.  Bound: launch and two dependent round trips for a decode step, the
-// 28-32 bytes written per token for a long prompt.
+// 28-32 bytes written per token for a long prompt.  Measured (GB300): 512 requests
+// x 4 tokens 3.9 us, 64 requests of 1 to 8192 tokens 5.1 us (7.3 MB).
 #include <cstdint>
 
 #include "ckv_device.cuh"
