@@ -153,24 +153,21 @@ __global__ void __launch_bounds__((Layout<D, R>::kThreads), 1) fp4_attention_ker
   Small<R>& sm = *reinterpret_cast<Small<R>*>(smem + L::kSmall);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (warp == kMmaWarp) {
-    tmem_alloc<L::kTmem>(&sm.tmem);
-    if (lane == 0) {
-      for (int i = 0; i < kRing; ++i) {
-        mbar_init(&sm.full[i], 4);
-        mbar_init(&sm.empty[i], 1);
-        mbar_init(&sm.a_free[i], 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&sm.s_full[i], 1);
-        mbar_init(&sm.p_full[i], kSoftWarps);
-      }
-      mbar_init(&sm.q_full, kSoftWarps);
-      mbar_init(&sm.o_done, 1);
-      mbar_init(&sm.drain, 1);
-      sm.abort = 0;
-      fence_mbar_init();
+  if (warp == kMmaWarp && lane == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sm.full[i], 4);
+      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.a_free[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], kSoftWarps);
+    }
+    mbar_init(&sm.q_full, kSoftWarps);
+    mbar_init(&sm.o_done, 1);
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    fence_mbar_init();
   }
   pdl_wait();
   if (warp == 0) {
@@ -181,11 +178,10 @@ __global__ void __launch_bounds__((Layout<D, R>::kThreads), 1) fp4_attention_ker
       sm.ctx_min = INT32_MAX;
     }
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
   const Tile tile = sm.tile;
-  const uint32_t tmem = sm.tmem;
+  if (tile.rows <= 0) return;  // more tiles than rows need
+  if (warp == kMmaWarp) tmem_alloc<L::kTmem>(&sm.tmem);
   if (threadIdx.x < R) {
     const int r = threadIdx.x;
     int ctx = -1;
@@ -214,7 +210,10 @@ __global__ void __launch_bounds__((Layout<D, R>::kThreads), 1) fp4_attention_ker
       atomicMin(&sm.ctx_min, low);
     }
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
   const int ctx_max = sm.ctx_max, ctx_min = sm.ctx_min;
   const int k_first = blockIdx.y * chunk;
   const int k_last = min(ctx_max, k_first + chunk);

@@ -125,24 +125,21 @@ __global__ void __launch_bounds__(RowLayout<D>::kThreads, 1)
     return;
   }
 
-  if (warp == kRowMmaWarp) {
-    tmem_alloc<512>(&sm.tmem);
-    if (lane == 0) {
-      for (int i = 0; i < L::kRingN; ++i) {
-        mbar_init(&sm.full[i], 4);
-        mbar_init(&sm.empty[i], 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&sm.s_full[i], 1);
-        mbar_init(&sm.p_full[i], 8);
-      }
-      mbar_init(&sm.s_read, 8);
-      mbar_init(&sm.q_full, 8);
-      mbar_init(&sm.o_done, 1);
-      mbar_init(&sm.drain, 1);
-      sm.abort = 0;
-      fence_mbar_init();
+  if (warp == kRowMmaWarp && lane == 0) {
+    for (int i = 0; i < L::kRingN; ++i) {
+      mbar_init(&sm.full[i], 4);
+      mbar_init(&sm.empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 8);
+    }
+    mbar_init(&sm.s_read, 8);
+    mbar_init(&sm.q_full, 8);
+    mbar_init(&sm.o_done, 1);
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    fence_mbar_init();
   }
   pdl_wait();
   if (warp == 0) {
@@ -152,11 +149,10 @@ __global__ void __launch_bounds__(RowLayout<D>::kThreads, 1)
       sm.ctx_max = -1;
     }
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
   const Tile tile = sm.tile;
-  const uint32_t tmem = sm.tmem;
+  if (tile.rows <= 0) return;  // more tiles than rows need
+  if (warp == kRowMmaWarp) tmem_alloc<512>(&sm.tmem);
   int32_t my_ctx = -1, my_flat = -1;  // of softmax thread t: row t % 128
   if (threadIdx.x < 256) {
     const int r = threadIdx.x & 127;
@@ -176,7 +172,10 @@ __global__ void __launch_bounds__(RowLayout<D>::kThreads, 1)
     const int top = __reduce_max_sync(0xFFFFFFFFu, my_ctx);
     if (lane == 0) atomicMax(&sm.ctx_max, top);
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
   const int ctx_max = sm.ctx_max;
   const int k_first = blockIdx.y * chunk;
   const int k_last = min(ctx_max, k_first + chunk);
