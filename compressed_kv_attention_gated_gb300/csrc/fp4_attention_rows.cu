@@ -23,8 +23,8 @@
 // product gives them back: softmax 1.6 k, second product 0.8 k, decoding of three
 // units by a group each and scores 3 k.  Around its tiles a CTA of D = 512 spends 18 k
 // clocks: queries 10 k, output 4 k, first tile.
-// Measured (GB300): 512 requests x 4 tokens x 32 heads at D = 128, 0-2048 rows 63 us
-// (540 TFLOP/s); D = 512, a prompt of 8750 tokens x 64 heads over 200-1024 rows
+// Measured (GB300): 512 requests x 4 tokens x 32 heads at D = 128, 0-2048 rows 62 us
+// (555 TFLOP/s); D = 512, a prompt of 8750 tokens x 64 heads over 200-1024 rows
 // 1.36-1.39 ms (510 TFLOP/s; with two decoding groups 1.49 ms, when three took 1.39,
 // with queries through registers 1.58 ms, when copies took 1.49; the other form
 // 1.70 ms).  Slower: D = 128 with two CTAs of 9 warps per SM (109 us, when one took
