@@ -28,8 +28,8 @@
 // 1.36-1.39 ms (510 TFLOP/s; with two decoding groups 1.49 ms, when three took 1.39,
 // with queries through registers 1.58 ms, when copies took 1.49; the other form
 // 1.70 ms).  Slower: D = 128 with two CTAs of 9 warps per SM (109 us, when one took
-// 82), and four lanes per key in the decoding's loads (65.3 us, when one took 64.2;
-// at D = 512 1.37 ms, when one took 1.39).
+// 82), 16 softmax warps (63.7 us, when 8 took 61.4), and four lanes per key in the
+// decoding's loads (65.3 us, when one took 64.2; at D = 512 1.37 ms, when one took 1.39).
 #include "fp4_attention.cuh"
 
 namespace ckv {
