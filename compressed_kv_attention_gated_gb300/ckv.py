@@ -725,7 +725,8 @@ def ckv_fp4_attention(q, kv_cache, block_table, row_start, ctx_rows, max_rows, s
     """Attention over the 4-bit cache; see ckv_fp4_attention in include/ckv.h.
 
     q bf16 [T, H, D] (last dim contiguous); kv_cache uint8 [pages, page_size,
-    D/2 + D/16]; block_table int32 [B, max_pages] (last dim contiguous);
+    D/2 + D/16]; block_table int32 [B, max_pages] (last dim contiguous; rows apart,
+    or one row expanded over all requests);
     row_start int32 [B + 1]; ctx_rows int32 [T], at most max_rows; sink
     float32 [H] or None.  Returns (out, lse): bf16 [T, H, D] and float32 [T, H].
     workspace: a uint8 tensor of ckv_fp4_attention_workspace() bytes, by default

@@ -105,10 +105,14 @@ ckv_dtype dtype_of(const at::Tensor& t) {
   return t.scalar_type() == at::kFloat ? CKV_F32 : CKV_BF16;
 }
 
-// A table of int32 rows, last dimension contiguous, and the step between its rows.
-int64_t table_rows(const at::Tensor& t, int64_t B, const char* what) {
+// A table of int32 rows, last dimension contiguous, and the step between its rows: 0 when all B > 1
+// requests share one row (only where `shared`), else at least the width.
+int64_t table_rows(const at::Tensor& t, int64_t B, bool shared, const char* what) {
   need(t.scalar_type() == at::kInt && t.dim() == 2 && t.size(0) == B && (t.stride(1) == 1 || t.size(1) <= 1), what);
-  return std::max<int64_t>(t.stride(0), t.size(1));
+  if (B <= 1) return t.size(1);  // the step of a dimension of one entry is never used
+  if (shared && t.stride(0) == 0) return 0;
+  need(t.stride(0) >= t.size(1), "rows of block_table overlap");
+  return t.stride(0);
 }
 
 const char kStepNames[][16] = {"row_start",  "positions",  "batch_ids",     "slot_mapping",
@@ -143,8 +147,7 @@ PyObject* step_maps(PyObject*, PyObject* const* v, Py_ssize_t n) {
     need(vec(seq, at::kInt, B) && vec(query, at::kInt, B) && (!tails || vec(*tails, at::kInt, B)),
          "seq_lens, query_lens and tail_blocks must be contiguous int32 [B]");
     need(B <= INT32_MAX, "too many requests");
-    const int64_t stride = table_rows(table, B, "block_table must be int32 [B, max_pages], last dim contiguous");
-    need(B <= 1 || table.stride(0) >= table.size(1), "rows of block_table overlap");
+    const int64_t stride = table_rows(table, B, false, "block_table must be int32 [B, max_pages], last dim contiguous");
     need(table.size(1) <= INT32_MAX, "block_table is too wide");
     need(free.scalar_type() == at::kInt && free.is_contiguous(), "free_pages must be contiguous int32");
     const bool inplace = !cursor_out || cursor_out->data_ptr() == cursor.data_ptr();
@@ -333,7 +336,7 @@ PyObject* fp4_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
     need(start.scalar_type() == at::kInt && start.is_contiguous() && start.numel() >= 1 && start.numel() <= INT32_MAX,
          "row_start must be contiguous int32 [B + 1]");
     const int64_t B = start.numel() - 1;
-    const int64_t stride = table_rows(table, B, "block_table must be int32 [B, max_pages], last dim contiguous");
+    const int64_t stride = table_rows(table, B, true, "block_table must be int32 [B, max_pages], last dim contiguous");
     need(table.size(1) <= INT32_MAX, "block_table is too wide");
     need(vec(ctx, at::kInt, T), "ctx_rows must be contiguous int32 [T]");
     need(!sink || vec(*sink, at::kFloat, H), "sink must be contiguous float32 [H]");

@@ -665,7 +665,8 @@ ckv_status ckv_fp4_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_st
                              void* workspace, int64_t workspace_bytes, int32_t use_pdl,
                              int32_t* err_word, void* stream) {
   if (T < 0 || B < 0 || B > 65536 || H < 1 || H > 1024 || !head_dim_ok(D) || num_pages < 0 || page_size < 1 ||
-      max_pages < 0 || table_stride < max_pages || !cache_scale_ok(cache_scale) || !std::isfinite(softmax_scale))
+      max_pages < 0 || (table_stride < max_pages && table_stride != 0) || !cache_scale_ok(cache_scale) ||
+      !std::isfinite(softmax_scale))
     return CKV_ERR_SHAPE;
   if (T == 0 || B == 0) return CKV_OK;
   if (max_rows < 1 || max_rows > INT32_MAX - 16384 || max_rows > static_cast<int64_t>(max_pages) * page_size ||

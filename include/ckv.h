@@ -628,8 +628,9 @@ ckv_status ckv_fp4_load(const uint8_t* kv_cache, int64_t num_pages, int32_t page
  * One token per request is the decode form, several the verify and prompt forms.
  * q          device bf16, row (t, h) at t*q_stride_t + h*q_stride_h elements, 16-byte aligned.
  * kv_cache, page_size, num_pages, cache_scale  as for ckv_fp4_store.
- * block_table  device int32, request b's row at b * table_stride (>= max_pages).  A page
- *            id outside [0, num_pages) sets CKV_DEVERR_CACHE_LOC; its rows count as unseen.
+ * block_table  device int32, request b's row at b * table_stride (>= max_pages, or 0: one row
+ *            that all requests share).  A page id outside [0, num_pages) sets
+ *            CKV_DEVERR_CACHE_LOC; its rows count as unseen.
  * row_start  device int32 [B + 1], non-decreasing from 0 on.   ctx_rows device int32 [T].
  * max_rows   host bound of ctx_rows (1 <= max_rows <= max_pages * page_size, < 2^31 - 2^14): larger entries
  *            set CKV_DEVERR_SEQ_LEN and are clamped.  It chooses how far the rows are
