@@ -157,13 +157,14 @@ __global__ void __launch_bounds__(kMapThreads) step_maps_kernel(const __grid_con
   if (lead && flags) flag_error(a.err, flags);
   flags = 0;
 
-  const int stride = gridDim.x * kMapThreads;
-  for (int i = blockIdx.x * kMapThreads + threadIdx.x; i < a.num_tokens; i += stride) {
+  // unsigned: num_tokens goes to 2^31 - 1, and the step past the last token would leave 32 signed bits
+  const uint32_t stride = gridDim.x * kMapThreads, places = a.num_tokens;
+  for (uint32_t i = blockIdx.x * kMapThreads + threadIdx.x; i < places; i += stride) {
     int32_t pos = -1, req = -1, ctx = -1, rpos = -1, tail = -1, loc32 = -1;
     int64_t loc = -1;
-    if (i < live) {
-      req = find_request(s_start, a.B, i);
-      pos = s_first[req] + i;
+    if (i < static_cast<uint32_t>(live)) {
+      req = find_request(s_start, a.B, static_cast<int32_t>(i));
+      pos = s_first[req] + static_cast<int32_t>(i);
       const uint32_t row = static_cast<uint32_t>(pos) / P;
       const uint32_t slot = static_cast<uint32_t>(pos) - row * P;
       ctx = static_cast<int32_t>(row);

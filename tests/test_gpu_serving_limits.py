@@ -63,3 +63,30 @@ def test_fp4_attention_and_maps_refuse_overlapping_table_rows(ck):
     ck.ckv_fp4_attention(q, cache, wide.as_strided((3, 8), (8, 1)), st, cx, 128, 1.0)
     ck.ckv_fp4_attention(q, cache, wide.as_strided((3, 8), (20, 1)), st, cx, 128, 1.0)
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------ step maps
+@pytest.mark.parametrize("T,lens", [(2 ** 31 - 1, [2 ** 31 - 1]), (2 ** 31 - 1, [5, 2 ** 30, 7]), (2 ** 31 - 152 * 1024, [3])])
+def test_step_maps_of_the_most_tokens(ck, T, lens):
+    """Maps of up to 2^31 - 1 tokens: each place is written once, and nothing before or behind them."""
+    guard = 1 << 20
+    raw = torch.full((T + 2 * guard,), -9, dtype=torch.int32, device="cuda")
+    pos = raw[guard:guard + T]
+    B, err = len(lens), _err()
+    width = -(-max(lens) // 1024)
+    ps = 1 << 16
+    tab = torch.full((B, -(-width // ps)), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(100, 100 + tab.numel(), dtype=torch.int32, device="cuda")
+    ck.ckv_build_step_maps(_i32(lens), _i32(lens), tab, free, _i32([0, 0]), 1024, ps, T, out={"positions": pos}, err_word=err)
+    assert int(err) == 0
+    assert bool((raw[:guard] == -9).all()) and bool((raw[guard + T:] == -9).all())
+    at, piece = 0, 1 << 27
+    for n in [*lens, None]:  # the last stretch: places without a token
+        end = T if n is None else at + n
+        for i in range(at, end, piece):
+            j = min(i + piece, end)
+            want = torch.arange(i - at, j - at, dtype=torch.int32, device="cuda") if n is not None else -1
+            assert bool((pos[i:j] == want).all())
+        at = end
+    need = [-(-(n // 1024) // ps) for n in lens]
+    assert (tab >= 0).sum(1).tolist() == need
