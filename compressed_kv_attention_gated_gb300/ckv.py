@@ -716,7 +716,7 @@ def ckv_fp4_load(kv_cache, loc, out, cache_scale=1.0, use_pdl=True, err_word=Non
 
 
 def ckv_fp4_attention_workspace(T, B, H, D, max_rows):
-    """Bytes of workspace that ckv_fp4_attention needs for these sizes."""
+    """Bytes of workspace that ckv_fp4_attention needs for these sizes (0 for those that it refuses)."""
     return load().ckv_fp4_attention_workspace(int(T), int(B), int(H), int(D), int(max_rows))
 
 

@@ -47,6 +47,14 @@ bool cache_scale_ok(float g) {
   return g > 0.f && std::frexp(g, &e) == 0.5f && e >= -63 && e <= 65;
 }
 
+// Sizes of ckv_fp4_attention with work to do: (token, head) rows and cache rows are counted in 32
+// bits, the latter rounded up to whole tiles and ranges.
+constexpr int32_t kMaxAttentionRequests = 65536;
+bool attention_sizes_ok(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
+  return B <= kMaxAttentionRequests && H >= 1 && H <= 1024 && T <= INT32_MAX / H && head_dim_ok(D) && max_rows >= 1 &&
+         max_rows <= INT32_MAX - 16384;
+}
+
 // One row set of ckv_qk_norm_rope.
 ckv_status check_norm_rows(const ckv_norm_rows& r) {
   if (r.tokens < 0 || r.heads < 0 || r.reserved != 0) return CKV_ERR_SHAPE;
@@ -652,7 +660,7 @@ ckv_status ckv_fp4_load(const uint8_t* kv_cache, int64_t num_pages, int32_t page
 }
 
 int64_t ckv_fp4_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
-  if (T <= 0 || B <= 0 || H < 1 || H > 1024 || T > INT32_MAX / H || !head_dim_ok(D) || max_rows < 1) return 0;
+  if (T <= 0 || B <= 0 || !attention_sizes_ok(T, B, H, D, max_rows)) return 0;
   return ckv::fp4_attention_workspace(T, B, H, D, max_rows);
 }
 
@@ -664,13 +672,13 @@ ckv_status ckv_fp4_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_st
                              float softmax_scale, const float* sink, uint16_t* out, float* lse,
                              void* workspace, int64_t workspace_bytes, int32_t use_pdl,
                              int32_t* err_word, void* stream) {
-  if (T < 0 || B < 0 || B > 65536 || H < 1 || H > 1024 || !head_dim_ok(D) || num_pages < 0 || page_size < 1 ||
+  if (T < 0 || B < 0 || B > kMaxAttentionRequests || H < 1 || H > 1024 || !head_dim_ok(D) || num_pages < 0 || page_size < 1 ||
       max_pages < 0 || (table_stride < max_pages && table_stride != 0) || !cache_scale_ok(cache_scale) ||
       !std::isfinite(softmax_scale))
     return CKV_ERR_SHAPE;
   if (T == 0 || B == 0) return CKV_OK;
-  if (max_rows < 1 || max_rows > INT32_MAX - 16384 || max_rows > static_cast<int64_t>(max_pages) * page_size ||
-      T > INT32_MAX / H || q_stride_t < 0 || q_stride_h < 0)
+  if (!attention_sizes_ok(T, B, H, D, max_rows) || max_rows > static_cast<int64_t>(max_pages) * page_size || q_stride_t < 0 ||
+      q_stride_h < 0)
     return CKV_ERR_SHAPE;
   if (!q || !kv_cache || !block_table || !row_start || !ctx_rows || !out) return CKV_ERR_NULL;
   if (!aligned(q, 16) || q_stride_t % 8 || q_stride_h % 8 || !aligned(kv_cache, 16) || !aligned(block_table, 4) ||

@@ -643,7 +643,7 @@ ckv_status ckv_fp4_load(const uint8_t* kv_cache, int64_t num_pages, int32_t page
  *            that is 0); its contents need no initial value and do not outlive the call.
  *            Calls that overlap on the GPU need one each.  The bytes follow how the rows are
  *            split and do not grow with every size: a workspace for several sizes is as large
- *            as the largest answer for them.
+ *            as the largest answer for them.  For sizes that the call refuses the answer is 0.
  */
 int64_t ckv_fp4_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows);
 ckv_status ckv_fp4_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T,

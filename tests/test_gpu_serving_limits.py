@@ -65,6 +65,18 @@ def test_fp4_attention_and_maps_refuse_overlapping_table_rows(ck):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("max_rows", [0, -1, 65, 2 ** 31, 2 ** 40, 160 * 2 ** 32, 2 ** 63 - 1])
+def test_fp4_attention_refuses_bounds_of_its_rows(ck, max_rows):
+    """max_rows past the table's pages or past 32 bits: a refusal, before any workspace is asked for."""
+    for B, H in ((1, 4), (19, 16)):
+        q = torch.zeros(B, H, 128, dtype=torch.bfloat16, device="cuda")
+        cache = torch.zeros(4, 16, 72, dtype=torch.uint8, device="cuda")
+        args = (q, cache, torch.zeros(B, 4, dtype=torch.int32, device="cuda"), _i32(np.arange(B + 1)), _i32(np.ones(B)))
+        for stream in (None, torch.cuda.Stream()):
+            with pytest.raises(ck.CkvError):
+                ck.ckv_fp4_attention(*args, max_rows, 1.0, stream=stream)
+
+
 # ------------------------------------------------------------ step maps
 @pytest.mark.parametrize("T,lens", [(2 ** 31 - 1, [2 ** 31 - 1]), (2 ** 31 - 1, [5, 2 ** 30, 7]), (2 ** 31 - 152 * 1024, [3])])
 def test_step_maps_of_the_most_tokens(ck, T, lens):
