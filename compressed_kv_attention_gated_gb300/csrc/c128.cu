@@ -216,19 +216,27 @@ __global__ void __launch_bounds__(kPrefillWarps * 32, 2)
   // indices and tokens before the dependency wait (none of them is written by
   // the compress pass, and everything before that pass was complete when it
   // let this grid launch), so its token reduction overlaps the compress pass;
-  // it waits only before the state.  Otherwise: wait first.
+  // it waits only before the state, or where it has nothing to do before it
+  // leaves: what follows in the stream waits for this grid alone, which must
+  // not end before the compress pass.  Otherwise: wait first.
   const bool early = kWrite && a.write_early;
   if (!early) pdl_wait();
   const uint32_t plan_id = blockIdx.x / S;
   const int slice = blockIdx.x % S;
   const uint32_t n_host = kWrite ? a.num_write : a.num_compress;
   const uint32_t n_plans = a.counts ? min(a.counts[kWrite ? 1 : 0], n_host) : n_host;
-  if (plan_id >= n_plans) return;
+  if (plan_id >= n_plans) {
+    if (early) pdl_wait();
+    return;
+  }
   const uint4 raw = *reinterpret_cast<const uint4*>(kWrite ? a.write_plan + plan_id
                                                            : a.compress_plan + plan_id);
   pdl_trigger();
   const uint32_t ragged_id = raw.x, batch = raw.y, position = raw.z, window = raw.w;
-  if (ragged_id == 0xFFFFFFFFu) return;  // sentinel (graph padding)
+  if (ragged_id == 0xFFFFFFFFu) {  // sentinel (graph padding)
+    if (early) pdl_wait();
+    return;
+  }
 
   const uint32_t pic = position & 127u;  // chunk position of the last token
   const bool plan_ok = batch < static_cast<uint32_t>(a.B) && window >= 1 && window <= pic + 1 &&
@@ -236,6 +244,7 @@ __global__ void __launch_bounds__(kPrefillWarps * 32, 2)
                        (kWrite ? (pic != 127u) : (pic == 127u));
   if (!plan_ok) {
     if (threadIdx.x == 0) flag_error(a.err, CKV_DEVERR_PLAN);
+    if (early) pdl_wait();
     return;
   }
   const int chunk_offset = static_cast<int>(pic + 1 - window);
@@ -251,6 +260,7 @@ __global__ void __launch_bounds__(kPrefillWarps * 32, 2)
   if ((chunk_offset != 0 && (load_index < 0 || load_index >= a.num_slots)) ||
       (kWrite && (store_index < 0 || store_index >= a.num_slots))) {
     if (threadIdx.x == 0) flag_error(a.err, CKV_DEVERR_SLOT);
+    if (early) pdl_wait();
     return;
   }
 

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import serving_reference as ref
-from test_gpu_serving_ops import _attn_inputs, _err, _i32
+from test_gpu_serving_ops import _attn_inputs, _err, _i32, _rope_table
 
 pytestmark = pytest.mark.gpu
 
@@ -21,6 +21,64 @@ def ck():
         pytest.skip("no CUDA device")
     ck.load()
     return ck
+
+
+# ------------------------------------------------------------ prefill, then the step's calls
+@pytest.mark.parametrize("variant", [1, 2])
+@pytest.mark.parametrize("early_out", ["no_segment", "sentinels", "refused"])
+def test_prefill_write_pass_without_work_orders_what_follows(ck, variant, early_out):
+    """Prompts of whole chunks leave nothing to the prefill's write pass.  What follows it as a
+    programmatic dependent must still see every row that the compress pass wrote."""
+    B, D, n, P, ps = 32, 512, 1024, 128, 32
+    T = B * n
+    g = torch.Generator(device="cuda").manual_seed(0)
+    inp = torch.randn(T, 2 * D, generator=g, device="cuda")
+    ape = torch.randn(128, D, generator=g, device="cuda") * 0.1
+    state = torch.rand(B, 3, D, generator=g, device="cuda") + 0.5
+    w = 1 + 0.1 * torch.randn(D, generator=g, device="cuda")
+    rope = _rope_table(n, 64, torch.Generator().manual_seed(1)).cuda()
+    idx = torch.arange(B, dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), n, dtype=torch.int64, device="cuda")
+    # as a captured graph plans: entries past the segments, here all of the write pass's, are sentinels
+    cp, wp, counts = ck.ckv_plan_online_prefill_device(lens, lens, T, pad_for_graph=True)
+    assert bool((wp.view(torch.int32) == -1).all())
+    if early_out == "no_segment":
+        counts[1] = 0
+    elif early_out == "refused":  # windows of no tokens, which the kernel flags and leaves
+        wp.zero_()
+    closing = torch.arange(T, dtype=torch.int32, device="cuda")
+    rpos = torch.where(closing % P == P - 1, closing % n - (P - 1), torch.full_like(closing, -1))
+    loc = torch.where(rpos >= 0, closing.long() // P, torch.full((T,), -1, device="cuda"))
+
+    def chain(rows, kn, back, pdl):
+        cache = torch.zeros(T // P // ps, ps, D // 2 + D // 16, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        ck.ckv_c128_online_prefill_counted(state, inp, rows, ape, idx, cp, wp, counts, use_pdl=pdl)
+        ck.ckv_qk_norm_rope(rows.view(T, 1, D), rpos, rope, q_weight=w, q_out=kn, interleaved=True, use_pdl=pdl)
+        ck.ckv_fp4_store(kn.view(T, D), cache, loc, use_pdl=pdl)
+        ck.ckv_fp4_load(cache, loc, back, use_pdl=pdl)
+        torch.cuda.synchronize()
+        return cache
+
+    def buffers():
+        return (torch.full((T, D), 3.0, device="cuda"), torch.zeros(T, 1, D, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(T, D, dtype=torch.bfloat16, device="cuda"))
+
+    prev = ck.ckv_c128_prefill_set_variant(variant)
+    try:
+        want = buffers()
+        cache = chain(*want, False)
+        assert bool((want[0][rpos >= 0] != 3).any(1).all())
+        flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+        got = buffers()
+        for i in range(8):
+            got[0].fill_(3.0), got[1].zero_(), got[2].zero_(), flush.fill_(i)
+            c = chain(*got, True)
+            for a, b in zip(want, got):
+                assert torch.equal(a, b)
+            assert torch.equal(cache, c)
+    finally:
+        ck.ckv_c128_prefill_set_variant(prev)
 
 
 # ------------------------------------------------------------ block tables
