@@ -47,12 +47,11 @@ bool cache_scale_ok(float g) {
   return g > 0.f && std::frexp(g, &e) == 0.5f && e >= -63 && e <= 65;
 }
 
-// Sizes of ckv_fp4_attention with work to do: (token, head) rows and cache rows are counted in 32
-// bits, the latter rounded up to whole tiles and ranges.
+// Sizes of ckv_fp4_attention with work to do: (token, head) rows are counted in 32 bits.
 constexpr int32_t kMaxAttentionRequests = 65536;
 bool attention_sizes_ok(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows) {
   return B <= kMaxAttentionRequests && H >= 1 && H <= 1024 && T <= INT32_MAX / H && head_dim_ok(D) && max_rows >= 1 &&
-         max_rows <= INT32_MAX - 16384;
+         max_rows <= CKV_FP4_ATTENTION_MAX_ROWS;
 }
 
 // One row set of ckv_qk_norm_rope.

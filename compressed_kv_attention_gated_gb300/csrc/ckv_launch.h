@@ -190,6 +190,10 @@ struct Fp4AttentionArgs {
   float g, softmax_scale;
 };
 
+// Ranges of cache rows that a call is split into at most, and rows of a range (why: plan_fp4).
+constexpr int kFp4MaxSplits = 160, kFp4MaxRange = 1 << 17;
+static_assert(kFp4MaxSplits * kFp4MaxRange == CKV_FP4_ATTENTION_MAX_ROWS, "header");
+
 cudaError_t launch_step_maps(const StepMapsArgs& a, bool use_pdl, cudaStream_t s);
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int D, bool use_pdl, cudaStream_t s);
 cudaError_t launch_fp4_store(const Fp4RowsArgs& a, int D, int dtype, bool use_pdl, cudaStream_t s);

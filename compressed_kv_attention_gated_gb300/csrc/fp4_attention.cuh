@@ -425,7 +425,7 @@ __device__ __forceinline__ void prefetch_tile(const Fp4AttentionArgs& a, uint32_
 // 600 tokens x 16 heads over 2048 rows in two ranges at D = 128, 28.1 -> 23.0 us).  With kHalves
 // == 2 two CTAs shared a range, each with half of the channels and with references and sums of
 // its own.
-constexpr int kMaxSplits = 160, kFewSplits = 4;
+constexpr int kFewSplits = 4;
 template <int D, int R, int kHalves, bool kFew>
 __global__ void __launch_bounds__(128, kFew ? 12 : 4) fp4_join_kernel(const __grid_constant__ Fp4AttentionArgs a, int chunk, int splits) {
   constexpr int kParts = D / 128, kDeep = kFew ? kFewSplits : 16;  // loads in flight (the second bound leaves them registers)
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(128, kFew ? 12 : 4) fp4_join_kernel(const __gr
   const float* ml = ws + static_cast<int64_t>(gridDim.x) * splits * R * D + (slot0 * kHalves + half) * R * 2 + r;
   const int64_t flat = static_cast<int64_t>(t.tok0) * a.H + t.base + r;
   // a lane has the references and sums of ranges lane, lane + 32, ...
-  constexpr int kOwn = kFew ? 1 : kMaxSplits / 32;
+  constexpr int kOwn = kFew ? 1 : kFp4MaxSplits / 32;
   float ref[kOwn], l[kOwn], m = kNegBig;
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {

@@ -632,9 +632,10 @@ ckv_status ckv_fp4_load(const uint8_t* kv_cache, int64_t num_pages, int32_t page
  *            that all requests share).  A page id outside [0, num_pages) sets
  *            CKV_DEVERR_CACHE_LOC; its rows count as unseen.
  * row_start  device int32 [B + 1], non-decreasing from 0 on.   ctx_rows device int32 [T].
- * max_rows   host bound of ctx_rows (1 <= max_rows <= max_pages * page_size, < 2^31 - 2^14): larger entries
- *            set CKV_DEVERR_SEQ_LEN and are clamped.  It chooses how far the rows are
- *            split over CTAs, so a tight bound is faster.
+ * max_rows   host bound of ctx_rows (1 <= max_rows <= max_pages * page_size and
+ *            CKV_FP4_ATTENTION_MAX_ROWS): larger entries set CKV_DEVERR_SEQ_LEN and are
+ *            clamped.  It chooses how far the rows are split over CTAs, so a tight bound is
+ *            faster.
  * sink       device fp32 [H], nullable.
  * out        device bf16 [T][H][D] contiguous, apart from q (the spans of memory from first to
  *            last element may not overlap).    lse  device fp32 [T][H], nullable.
@@ -645,6 +646,7 @@ ckv_status ckv_fp4_load(const uint8_t* kv_cache, int64_t num_pages, int32_t page
  *            split and do not grow with every size: a workspace for several sizes is as large
  *            as the largest answer for them.  For sizes that the call refuses the answer is 0.
  */
+#define CKV_FP4_ATTENTION_MAX_ROWS 20971520 /* 160 ranges of 2^17 rows, the longest that one sum runs over */
 int64_t ckv_fp4_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t D, int64_t max_rows);
 ckv_status ckv_fp4_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T,
                              int32_t H, int32_t D, const uint8_t* kv_cache, int64_t num_pages,

@@ -23,6 +23,13 @@ def ck():
     return ck
 
 
+def _page(rows, D):
+    """A cache of one page that holds the given rows (exactly: multiples of code values, scale 1)."""
+    codes, scales = ref.fp4_rows(np.asarray(rows, np.float64), 1.0)
+    assert np.array_equal(ref.E2M1[codes] * np.repeat(ref.E4M3[scales], 16, axis=1), rows)
+    return torch.from_numpy(ref.pack_page(codes, scales).reshape(1, len(rows), D // 2 + D // 16)).cuda()
+
+
 # ------------------------------------------------------------ prefill, then the step's calls
 @pytest.mark.parametrize("variant", [1, 2])
 @pytest.mark.parametrize("early_out", ["no_segment", "sentinels", "refused"])
@@ -160,3 +167,50 @@ def test_step_maps_of_the_most_tokens(ck, T, lens):
         at = end
     need = [-(-(n // 1024) // ps) for n in lens]
     assert (tab >= 0).sum(1).tolist() == need
+
+
+# ------------------------------------------------------------ long rows
+@pytest.mark.parametrize("D,H", [(128, 4), (128, 40), (256, 24), (512, 48), (512, 80)])
+def test_fp4_attention_sums_of_long_rows(ck, D, H):
+    """2^21 rows (one page again and again) for as many requests as there are SMs.  Two channels of the
+    cache are constant, so the output is that constant whatever the weights.
+
+    The accumulator cuts sums off, by 2^-9 of a value at most over the 2^17 rows of a range; weights
+    are rounded to 2^-11 and the output to 2^-8: 2^-8 + 2^-9 + 2^-11 of the constants."""
+    L, B, ps = 1 << 21, 152, 1 << 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(ps, D, generator=g, device="cuda").clamp(-5, 5)
+    x[:, 0], x[:, D - 1], x[:, D - 16] = 6, -1.5, 6
+    cache = torch.zeros(1, ps, D // 2 + D // 16, dtype=torch.uint8, device="cuda")
+    ck.ckv_fp4_store(x, cache, torch.arange(ps, device="cuda"))
+    k = torch.empty(ps, D, device="cuda")
+    ck.ckv_fp4_load(cache, torch.arange(ps, device="cuda"), k)
+    assert bool((k[:, 0] == 6).all()) and bool((k[:, D - 1] == -1.5).all())
+    q = torch.randn(1, H, D, generator=g, device="cuda").bfloat16()
+    table = torch.zeros(1, L // ps, dtype=torch.int32, device="cuda").expand(B, -1)
+    out, lse = ck.ckv_fp4_attention(q.expand(B, H, D), cache, table, _i32(np.arange(B + 1)), _i32(np.full(B, L)), L, D ** -0.5)
+    tol = 2.0 ** -8 + 2.0 ** -9 + 2.0 ** -11
+    assert bool(((out[..., 0].double() - 6).abs() <= 6 * tol).all())
+    assert bool(((out[..., D - 1].double() + 1.5).abs() <= 1.5 * tol).all())
+    want = torch.logsumexp(q[0].double() @ k.double().T * D ** -0.5, -1) + np.log(L // ps)
+    assert bool(((lse.double() - want).abs() <= 2.0 ** -16 * (10 + want.abs())).all())
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
+
+
+@pytest.mark.parametrize("D,H", [(128, 1), (128, 64), (512, 8), (512, 128)])
+def test_fp4_attention_of_the_longest_rows(ck, D, H):
+    """One request over 160 x 2^17 rows, the most that a call takes (one page again and again).
+    Every row is the same, so every weight and sum is a power of two times the number of rows."""
+    ps, L = 1 << 16, 160 * 2 ** 17
+    row = np.tile([1.0, -2, 0.5, 6, 0, 3, -1.5, 4] * 2, D // 16)
+    cache = _page(np.tile(row, (ps, 1)), D)
+    table = torch.zeros(1, L // ps, dtype=torch.int32, device="cuda")
+    q = torch.full((1, H, D), 0.25).bfloat16().cuda()
+    out = torch.full((1, H, D), -7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((1, H), -7.0, device="cuda")
+    err = _err()
+    ck.ckv_fp4_attention(q, cache, table, _i32([0, 1]), _i32([L]), L, 1.0 / D, out=out, lse=lse, err_word=err)
+    assert int(err) == 0
+    assert bool((out.double() == torch.from_numpy(row).cuda()).all())
+    want = float(row.sum()) * 0.25 / D + np.log(L)
+    assert bool(((lse.double() - want).abs() <= 2.0 ** -16 * want).all())
