@@ -17,14 +17,14 @@
 // 2688), exact in fp16; cache_scale goes into the factor of the scores and of
 // the output.  A query row is scaled by a power of two to fp16's top, which
 // keeps its 8 bits for every channel above 2^-28 of its largest.  Scores, sums
-// and outputs are fp32.  Only the weights are rounded, to fp16 (2^-11).
+// and outputs are fp32.  Only the weights are rounded, to fp16: by 2^-11 of their
+// value, and those below 2^-21 of the row's largest by 2^-32 of that.
 //
 // Softmax: in S^T a thread holds one key for R/2 rows, so a row's maximum is
 // spread over 128 threads.  It is not formed per tile: weights are taken
-// against a reference that is the maximum of the tile that set it, and only
-// when some score exceeds its reference by more than 2^8 (weights up to 256 are
-// harmless in fp16 and fp32) the CTA forms the true maxima and rescales O and
-// the sums.  Sums stay per thread until the end.
+// against a reference that is 2^7 below the largest of the tile that set it, and
+// only when some weight exceeds 2^15 (fp16 goes to 65504) the CTA forms the true
+// maxima and rescales O and the sums.  Sums stay per thread until the end.
 //
 // Roles: 8 softmax warps (also query load and output), 1 warp that issues the
 // MMAs, 1 that brings the next CTA's first bytes to L2, and groups of 4 warps that
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__((Layout<D, R>::kThreads), 1) fp4_attention_ker
         if (soft_any(over > kJump || !ok)) {
           ok = !soft_any(!ok);
           if (!ok) break;
-          // new references: the largest score so far of each row
+          // new references: kTop below the largest score so far of each row
           read_scores(z);
           const float top = reduce_columns<L::kCols, true>(z, lane);
           constexpr int kShare = 32 / L::kCols;  // lanes that hold the same row's result
@@ -297,7 +297,8 @@ __global__ void __launch_bounds__((Layout<D, R>::kThreads), 1) fp4_attention_ker
           if (threadIdx.x < R) {
             const int r = threadIdx.x;
             const float old = sm.ref[r];
-            const float now = fmaxf(fmaxf(fmaxf(sm.part[0][r], sm.part[1][r]), fmaxf(sm.part[2][r], sm.part[3][r])), old);
+            const float high = fmaxf(fmaxf(sm.part[0][r], sm.part[1][r]), fmaxf(sm.part[2][r], sm.part[3][r]));
+            const float now = fmaxf(high - kTop, old);
             sm.keep[r] = fast_exp2(old - now);
             sm.ref[r] = now;
           }

@@ -18,7 +18,11 @@ constexpr int kSMs = 152;        // of a GB300
 constexpr int kKeys = 128;       // cache rows per tile
 constexpr int kRing = 4;         // units of 128 keys x 128 channels
 constexpr int kUnitBytes = 32768;
-constexpr float kJump = 8.f;     // log2 of the largest weight before a row's reference moves
+// log2 of a row's largest weight when its reference is set, and before it moves (2^8 over that): as
+// high as fp16 goes, so that weights keep their 11 bits down to 2^-21 of the largest one's and below
+// that are off by 2^-32 of it at most.  With a reference at the largest score itself, 131,071 keys of
+// weight 2^-25.1, 0.36% of their row together, were lost whole.
+constexpr float kTop = 7.f, kJump = 15.f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 // How a call is cut up (fp4_attention.cu).

@@ -9,7 +9,7 @@
 // exponentials, as much work as the products (512 clocks at D = 128).
 //
 // As in the other form a row's weights are taken against a reference that moves
-// only when a score exceeds it by 2^8; here that is the affair of two warps.
+// only when a weight exceeds 2^15; here that is the affair of two warps.
 //
 // At D = 512 the accumulator would fill tensor memory, so two CTAs share a tile:
 // both form the scores and the softmax, each multiplies with its half of the
@@ -244,12 +244,12 @@ __global__ void __launch_bounds__(RowLayout<D>::kThreads, 1)
         if (pair_any(quad, over > kJump || (unset && over > -INFINITY) || !ok)) {
           ok = !pair_any(quad, !ok);
           if (!ok) break;
-          // the largest score so far becomes the reference
+          // the reference goes to kTop below the largest score so far
           sm.part[half][row] = over;
           pair_barrier(quad);
           over = fmaxf(over, sm.part[half ^ 1][row]);
           pair_barrier(quad);  // read, before it is written again
-          const float d = unset ? over : fmaxf(over, 0.f);
+          const float d = unset ? over - kTop : fmaxf(over - kTop, 0.f);
           const bool move = d > -INFINITY;
           const float by = move ? d : 0.f;
           const float keep = unset ? 0.f : fast_exp2(-by);

@@ -170,6 +170,34 @@ def test_step_maps_of_the_most_tokens(ck, T, lens):
 
 
 # ------------------------------------------------------------ long rows
+@pytest.mark.parametrize("D,H", [(128, 4), (128, 24), (128, 40), (256, 8), (512, 48), (512, 80)])
+def test_fp4_attention_one_large_weight_over_a_long_tail(ck, D, H):
+    """131,072 rows whose weights are 2^-25.1 of the first one's: together 0.36% of the sum.
+
+    Weights are rounded by 2^-11 of their value, or by 2^-32 of the largest one's: with values up to
+    6 the output is off by 6 (L 2^-32 + 2^-11) at most, and its rounding."""
+    L, B = 131072, 152
+    assert ck.ckv_fp4_attention_workspace(B, B, H, D, L) == 0  # not split: a range of its own would have a maximum of its own
+    x = np.zeros((L, D))
+    x[0, 0], x[1:, 1], x[:, 16] = 6, 6, 1.5
+    cache = _page(x, D)
+    z0 = 25.1 * np.log(2)
+    q = torch.zeros(B, H, D)
+    q[:, :, 0] = 2.875
+    q = q.bfloat16()
+    scale = z0 / (2.875 * 6)
+    out, lse = ck.ckv_fp4_attention(q.cuda(), cache, torch.zeros(B, 1, dtype=torch.int32, device="cuda"), _i32(np.arange(B + 1)),
+                                    _i32(np.full(B, L)), L, scale)
+    z = np.zeros(L)
+    z[0] = np.float64(np.float32(scale)) * 2.875 * 6
+    p = np.exp(z - z[0])
+    want = p @ x / p.sum()
+    assert 0.02 < want[1] < 0.03
+    tol = 2.0 ** -8 * np.abs(want) + 6 * (L * 2.0 ** -32 + 2.0 ** -11)
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol)
+    assert np.all(np.abs(lse.double().cpu().numpy() - (z[0] + np.log(p.sum()))) <= 2.0 ** -16 * z[0])
+
+
 @pytest.mark.parametrize("D,H", [(128, 4), (128, 40), (256, 24), (512, 48), (512, 80)])
 def test_fp4_attention_sums_of_long_rows(ck, D, H):
     """2^21 rows (one page again and again) for as many requests as there are SMs.  Two channels of the
