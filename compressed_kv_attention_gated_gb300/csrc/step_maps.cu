@@ -11,8 +11,9 @@
 // pos / P when (pos + 1) % P == 0, which lies in page r / ps of the request.
 // The token that closes the first row of a taken page writes the page's table
 // entry (pages are taken for rows that close in this step, so every taken page
-// has such a token), and every token of a taken page derives the page id from
-// the free list itself: no CTA waits for another's table entries.
+// has such a token; for tokens past num_tokens the scan does it), and every
+// token of a taken page derives the page id from the free list itself: no CTA
+// waits for another's table entries.
 //
 // Every CTA scans the lengths of all requests into shared memory (12 bytes per
 // request), so one launch does it all; then the tokens are spread over the
@@ -141,6 +142,15 @@ __global__ void __launch_bounds__(kMapThreads) step_maps_kernel(const __grid_con
       // clamped: any index at or past num_free is past the list
       const int64_t f = min(c0 + pages + before_pages, a.num_free);
       s_free[b] = static_cast<int32_t>(f - held);
+      // Tokens past num_tokens are dropped, their pages are taken all the same (a call with more
+      // room takes the same ones): entered here, as no token does it.
+      if (lead && c0 >= 0 && tokens + before_tokens + n > a.num_tokens) {
+        for (int32_t pg = held; pg < need && f + (pg - held) < a.num_free; ++pg) {
+          const int64_t closes = (static_cast<int64_t>(pg) * ps + 1) * P - 1;  // position that closes the page's first row
+          if (tokens + before_tokens + closes - (s - n) >= a.num_tokens)
+            a.block_table[b * a.table_stride + pg] = a.free_pages[f + (pg - held)];
+        }
+      }
       if (lead && a.row_start) a.row_start[b] = static_cast<int32_t>(start);
     }
     tokens += add_tokens;

@@ -533,8 +533,9 @@ ckv_status ckv_latency_probe(int32_t hops, const int32_t* idx, const void* rows,
  * P            1..1024.
  * Errors (err_word): a length < 0 or n > s sets CKV_DEVERR_SEQ_LEN and the
  * request counts as having no tokens; more than num_tokens tokens set
- * CKV_DEVERR_PLAN and those past it are dropped (row_start is clamped too); a
- * page past max_pages, past the free list, or < 0 in the table sets
+ * CKV_DEVERR_PLAN and those past it are dropped (row_start is clamped too; the
+ * pages of their rows are taken and entered in the table all the same); a page
+ * past max_pages, past the free list, or < 0 in the table sets
  * CKV_DEVERR_PAGES, and locations in it are -1; a location or tail slot that
  * does not fit 32 bits sets CKV_DEVERR_CACHE_LOC / CKV_DEVERR_TAIL_BLOCK and
  * is -1 in the 32-bit map.

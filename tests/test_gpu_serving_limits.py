@@ -169,6 +169,56 @@ def test_step_maps_of_the_most_tokens(ck, T, lens):
     assert (tab >= 0).sum(1).tolist() == need
 
 
+def test_step_maps_pages_of_dropped_tokens_are_entered(ck):
+    """More tokens than the maps have room for: the pages that the requests take stand in their
+    block tables all the same, so that none is lost."""
+    rng = np.random.default_rng(0)
+    for P, ps, B in ((2, 2, 5), (4, 1, 40), (1, 3, 1500)):
+        n = rng.integers(0, 30, B)
+        s = n + rng.integers(0, 20, B)
+        width = -(-(int(s.max()) // P) // ps)
+        table = np.full((B, width), -1)
+        for b in range(B):
+            table[b, :-(-((s[b] - n[b]) // P) // ps)] = 5
+        free = 100 + rng.permutation(B * width)
+        live = int(n.sum())
+        want, wtable, wcur = ref.step_maps(s, n, table, free, 0, P, ps, live)
+        for T in (live - 1, live // 2, 1, 0):
+            tab, cur, err = _i32(table), _i32([0, 0]), _err()
+            got = ck.ckv_build_step_maps(_i32(s), _i32(n), tab, _i32(free), cur, P, ps, T, err_word=err)
+            assert int(err) == 0x8 and cur.tolist() == [wcur, 0]
+            for k in want:
+                w = np.minimum(want[k], T) if k == "row_start" else want[k][:T]
+                np.testing.assert_array_equal(got[k].cpu().numpy(), w, err_msg=k)
+            np.testing.assert_array_equal(tab.cpu().numpy(), wtable)
+
+
+@pytest.mark.parametrize("T", [0, 1000, (1 << 21) + 7])
+def test_step_maps_pages_of_dropped_tokens_of_a_long_prompt(ck, T):
+    """A prompt of more tokens than the narrow sums hold, dropped in part, with a request behind it;
+    and a free list that ends inside it."""
+    P, ps = 16, 1024
+    n, s = np.array([3, (1 << 21) + 5, 40000]), np.array([3, (1 << 21) + 9, 50000])
+    held = -(-((s - n) // P) // ps)
+    need = -(-(s // P) // ps)
+    for num_free in (200, 100):
+        free = 1000 + np.random.default_rng(0).permutation(num_free)
+        want, at = np.full((3, 130), -1), 0
+        for b in range(3):
+            want[b, :held[b]] = 7
+        table = want.copy()
+        for b in range(3):
+            for pg in range(held[b], need[b]):
+                if at < num_free:
+                    want[b, pg] = free[at]
+                at += 1
+        tab, cur, err = _i32(table), _i32([0, 0]), _err()
+        ck.ckv_build_step_maps(_i32(s), _i32(n), tab, _i32(free), cur, P, ps, T, err_word=err)
+        assert int(err) == 0x8 | (0x80 if at > num_free else 0)
+        assert cur.tolist() == [min(at, num_free), 0]
+        np.testing.assert_array_equal(tab.cpu().numpy(), want)
+
+
 # ------------------------------------------------------------ long rows
 @pytest.mark.parametrize("D,H", [(128, 4), (128, 24), (128, 40), (256, 8), (512, 48), (512, 80)])
 def test_fp4_attention_one_large_weight_over_a_long_tail(ck, D, H):
