@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import serving_reference as ref
+from test_gpu_serving_calls import _attn_ref64
 from test_gpu_serving_ops import _attn_inputs, _err, _i32, _rope_table
 
 pytestmark = pytest.mark.gpu
@@ -292,3 +293,74 @@ def test_fp4_attention_of_the_longest_rows(ck, D, H):
     assert bool((out.double() == torch.from_numpy(row).cuda()).all())
     want = float(row.sum()) * 0.25 / D + np.log(L)
     assert bool(((lse.double() - want).abs() <= 2.0 ** -16 * want).all())
+
+
+@pytest.mark.parametrize("D,H,B", [(128, 5, 300), (128, 64, 160), (256, 24, 160), (512, 48, 160), (512, 80, 80)])
+def test_fp4_attention_ranges_of_ragged_requests(ck, D, H, B):
+    """Bounds past 2^17 rows split every request: those that see few rows, one more or less than a range,
+    none, or are padding among those that see most."""
+    ps, most = 4096, 140000
+    rng = np.random.default_rng(D + H)
+    half = -(-(-(-most // 128)) // 2) * 128  # two ranges
+    ctx = rng.choice([0, 1, 100, half - 1, half, half + 1, 2 ** 17, most, -1], B)
+    ctx[:8] = [most, half, half + 1, 0, -1, half - 1, 2 ** 17 + 1, 5]
+    g = torch.Generator(device="cuda").manual_seed(0)
+    cache = torch.zeros(5, ps, D // 2 + D // 16, dtype=torch.uint8, device="cuda")
+    ck.ckv_fp4_store(torch.randn(5 * ps, D, generator=g, device="cuda"), cache, torch.arange(5 * ps, device="cuda"), cache_scale=2.0 ** -6)
+    table = _i32(rng.integers(0, 5, (B, -(-most // ps))))
+    q = (torch.randn(B, H, D, generator=g, device="cuda") * 2).bfloat16()
+    sink = torch.randn(H, generator=g, device="cuda") + 10
+    out = torch.full((B, H, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, H), 9.0, device="cuda")
+    err = _err()
+    ck.ckv_fp4_attention(q, cache, table, _i32(np.arange(B + 1)), _i32(ctx), most, D ** -0.5, cache_scale=2.0 ** -6, sink=sink, out=out,
+                         lse=lse, err_word=err)
+    assert int(err) == 0
+    off = torch.from_numpy(ctx < 0).cuda()
+    assert bool((out[off] == 9).all()) and bool((lse[off] == 9).all())
+    for b in [*range(8), *rng.integers(8, B, 4)]:
+        if ctx[b] < 0:
+            continue
+        want, wlse = _attn_ref64(q[b:b + 1, :6], cache, table[b:b + 1], [0, 1], torch.tensor([int(ctx[b])], device="cuda"), D ** -0.5,
+                                 2.0 ** -6, sink[:6])
+        assert bool(((out[b:b + 1, :6].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -9 * 6).all())
+        assert bool(((lse[b:b + 1, :6].double() - wlse).abs() <= 2.0 ** -16 * (10 + wlse.abs())).all())
+
+
+# ------------------------------------------------------------ many heads, many requests
+@pytest.mark.parametrize("D", [128, 256, 512])
+def test_fp4_attention_of_1024_heads(ck, D):
+    rng = np.random.default_rng(D)
+    ctx = np.array([130, 0, 129, 7])
+    start, T, table, cache, q, width = _attn_inputs(rng, np.array([1, 0, 3]), ctx, 1024, D, 16)
+    c, tab = torch.from_numpy(cache).cuda(), _i32(table)
+    out, lse = ck.ckv_fp4_attention(q.cuda(), c, tab, _i32(start), _i32(ctx), 130, D ** -0.5)
+    want, wlse = _attn_ref64(q.cuda(), c, tab, start, _i32(ctx), D ** -0.5, 1.0)
+    assert bool(((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -9 * 6).all())
+    fin = torch.isfinite(wlse)
+    assert torch.equal(fin, torch.isfinite(lse)) and bool(((lse.double() - wlse)[fin].abs() <= 2.0 ** -16 * (10 + wlse[fin].abs())).all())
+
+
+@pytest.mark.parametrize("D,H", [(128, 1), (128, 33), (512, 3)])
+def test_fp4_attention_of_65536_requests(ck, D, H):
+    """The most requests that a call takes: a token each, or a token for one in a thousand; each sees one
+    row, whose values come out."""
+    B, ps = 65536, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    cache = torch.zeros(B // ps, ps, D // 2 + D // 16, dtype=torch.uint8, device="cuda")
+    ck.ckv_fp4_store(torch.randn(B, D, generator=g, device="cuda"), cache, torch.arange(B, device="cuda"), cache_scale=2.0 ** -6)
+    rows = torch.empty(B, D, dtype=torch.bfloat16, device="cuda")
+    ck.ckv_fp4_load(cache, torch.arange(B, device="cuda"), rows, cache_scale=2.0 ** -6)
+    table = torch.randint(0, B // ps, (B, 1), generator=g, dtype=torch.int32, device="cuda")
+    for every in (1, 1000):
+        n = (torch.arange(B) % every == every // 2).int()
+        start = torch.cat([torch.zeros(1, dtype=torch.int32), torch.cumsum(n, 0).int()]).cuda()
+        T = int(n.sum())
+        q = torch.randn(T, H, D, generator=g, device="cuda").bfloat16()
+        out, _ = ck.ckv_fp4_attention(q, cache, table, start, torch.ones(T, dtype=torch.int32, device="cuda"), 1, D ** -0.5,
+                                      cache_scale=2.0 ** -6)
+        want = rows[table[n.bool().cuda(), 0].long() * ps]
+        assert torch.equal(out, want[:, None].expand(T, H, D))
+    with pytest.raises(ck.CkvError):
+        ck.ckv_fp4_attention(q[:1], cache, torch.zeros(B + 1, 1, dtype=torch.int32, device="cuda"),
+                             torch.ones(B + 2, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda"), 1, 1.0)
