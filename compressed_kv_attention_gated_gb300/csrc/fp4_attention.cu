@@ -41,7 +41,7 @@
 // 256 KB of shared memory per tile and the decoding writes 128 KB (3.1 k at 128
 // bytes per clock).  Around its tiles a CTA spends about 18 k clocks (setup 3 k,
 // queries 8.5 k, output 5 k), which one CTA per SM cannot hide.  Measured (GB300):
-// 1024 requests x 64 heads x 512 rows on average 203 us (340 TFLOP/s), 512 requests
+// 1024 requests x 64 heads x 512 rows on average 206 us (334 TFLOP/s), 512 requests
 // x 16 heads x 922-1024 rows 104 us, one request of 16 heads over 131,072 rows 32 us.
 // Slower forms: decoding in two groups (237 us for the first of these, when three
 // took 230), in four at R <= 32 (116 us for the second, when three took 110; at
@@ -56,7 +56,8 @@ namespace {
 // Warpgroups (4 warps) 0 and 1: softmax; 2: its first warp issues the MMAs; 3 and 4: load and decode.
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 12;
 // Registers per thread at launch: 640 x 96 or (D = 512) 768 x 80, 61,440 both; then 256 x 112 +
-// 128 x 64 and 256 x 96 or 384 x 64, the same.
+// 128 x 64 and 256 x 96 or 384 x 64, the same.  All kernels of this form but <128, 16> spill
+// (6 to 42 bytes stored, 2 to 110 loaded per thread).
 constexpr int kSoftRegs = 112, kMmaRegs = 64;
 template <int D, int R>
 struct Layout {

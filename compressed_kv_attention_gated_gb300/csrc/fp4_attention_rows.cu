@@ -6,7 +6,7 @@
 // A thread owns 64 keys of a row of S (two warps share 32 rows): maximum and sum
 // need one other thread at most, and the weights go back to tensor memory as A of
 // the second product.  Per 128 keys the 8 softmax warps evaluate 128 x 128
-// exponentials, as much work as the products (512 clocks at D = 128).
+// exponentials, half as long as the products take (1,024 clocks at D = 128).
 //
 // As in the other form a row's weights are taken against a reference that moves
 // only when a weight exceeds 2^15; here that is the affair of two warps.
@@ -18,13 +18,17 @@
 // shared memory there and the ring has three places; only the units of the CTA's
 // own half stay for the second product, so they come last in a tile.
 //
-// What bounds it: with D = 128 the softmax; with D = 512 the chain of a tile (5.5 k
-// clocks), as the ring has no place for the next tile's units before the second
+// What bounds it: neither the tensor cores (30% of the active cycles at D = 128) nor
+// the exponentials (15%).  With D = 128 128 keys take 0.9-1.2 us where their products
+// take 0.5, and a CTA 7 us besides them, of which one CTA per SM hides nothing (456
+// requests x 4 tokens x 32 heads, three CTAs on each SM: 27.7 us over 128 rows, 52.0
+// over 1024, 73.2 over 2048); requests of different lengths leave SMs idle at the
+// launch's end.  With D = 512 the chain of a tile (5.5 k clocks), as the ring has no place for the next tile's units before the second
 // product gives them back: softmax 1.6 k, second product 0.8 k, decoding of three
 // units by a group each and scores 3 k.  Around its tiles a CTA of D = 512 spends 18 k
 // clocks: queries 10 k, output 4 k, first tile.
-// Measured (GB300): 512 requests x 4 tokens x 32 heads at D = 128, 0-2048 rows 62 us
-// (555 TFLOP/s); D = 512, a prompt of 8750 tokens x 64 heads over 200-1024 rows
+// Measured (GB300): 512 requests x 4 tokens x 32 heads at D = 128, 0-2048 rows 61 us
+// (560 TFLOP/s); D = 512, a prompt of 8750 tokens x 64 heads over 200-1024 rows
 // 1.36-1.39 ms (510 TFLOP/s; with two decoding groups 1.49 ms, when three took 1.39,
 // with queries through registers 1.58 ms, when copies took 1.49; the other form
 // 1.70 ms).  Slower: D = 128 with two CTAs of 9 warps per SM (109 us, when one took
