@@ -199,7 +199,9 @@ def _on(stream):
     on torch's current stream, so tensors made here for another one are made with it current."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    if isinstance(stream, int):  # 0 is the default stream, which ExternalStream(0) is not
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _cuda(name, *ts):

@@ -364,3 +364,34 @@ def test_fp4_attention_of_65536_requests(ck, D, H):
     with pytest.raises(ck.CkvError):
         ck.ckv_fp4_attention(q[:1], cache, torch.zeros(B + 1, 1, dtype=torch.int32, device="cuda"),
                              torch.ones(B + 2, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda"), 1, 1.0)
+
+
+# ------------------------------------------------------------ streams
+def test_outputs_and_workspaces_belong_to_the_stream_of_the_call(ck, monkeypatch):
+    """What a call makes for itself on a given stream (a torch stream or its handle; the default
+    stream's is 0) is allocated for that stream: another stream's pool would hand it out too early."""
+    rng = np.random.default_rng(0)
+    start, T, table, cache, q, width = _attn_inputs(rng, np.array([1]), np.array([9000]), 16, 128, 64)
+    args = (q.cuda(), torch.from_numpy(cache).cuda(), _i32(table), _i32(start), _i32([9000]), 9000, 0.1)
+    assert ck.ckv_fp4_attention_workspace(1, 1, 16, 128, 9000) > 0
+    want = ck.ckv_fp4_attention(*args)
+    side, made, empty = torch.cuda.Stream(), [], torch.empty
+
+    def record(*a, **k):
+        made.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **k)
+
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", record)
+    for current in (torch.cuda.default_stream(), side):
+        for stream in (0, torch.cuda.default_stream(), side, side.cuda_stream):
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
+            with torch.cuda.stream(current):
+                made.clear()
+                got = ck.ckv_fp4_attention(*args, stream=stream)
+                ck.ckv_qk_norm_rope(args[0], args[4], k=args[0], k_positions=args[4], stream=stream)
+                ck.ckv_build_step_maps(_i32([5]), _i32([1]), _i32([[-1]]), _i32([3]), _i32([0, 0]), 4, 4, 1, stream=stream)
+                assert torch.cuda.current_stream() == current
+            torch.cuda.synchronize()
+            assert len(made) == 3 + 2 + 7 and set(made) == {handle}
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
