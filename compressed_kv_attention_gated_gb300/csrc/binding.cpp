@@ -220,7 +220,8 @@ ckv_norm_rows row_set(const at::Tensor& x, const at::Tensor& positions, const at
   need(H <= INT32_MAX, "too many heads");
   const int64_t st = out.stride(0), sh = out.stride(1);
   // rows that share memory would be written over one another
-  need((T <= 1 || st >= D) && (H <= 1 || sh >= D) && (T <= 1 || H <= 1 || st >= H * sh || sh >= T * st), "rows of an output overlap");
+  need((T <= 1 || st >= D) && (H <= 1 || sh >= D) && (T <= 1 || H <= 1 || st >= (H - 1) * sh + D || sh >= (T - 1) * st + D),
+       "rows of an output overlap");
   ckv_norm_rows r{};
   r.x = x.data_ptr();
   r.out = out.data_ptr();

@@ -89,6 +89,38 @@ def test_prefill_write_pass_without_work_orders_what_follows(ck, variant, early_
         ck.ckv_c128_prefill_set_variant(prev)
 
 
+# ------------------------------------------------------------ norm + rotation
+@pytest.mark.parametrize("D", [128, 512])
+def test_norm_rope_outputs_with_gaps(ck, D):
+    """Every other head of an odd number, every other token under heads that lie apart: rows that do
+    not overlap, as outputs and in place; rows that do are refused."""
+    T, g = 5, torch.Generator(device="cuda").manual_seed(0)
+    rope, pos = _rope_table(9, 64, torch.Generator().manual_seed(1)).cuda(), _i32([0, 3, 8, 1, 7])
+    heads = lambda: torch.zeros(T, 5, D, dtype=torch.bfloat16, device="cuda")[:, ::2]  # noqa: E731
+    tokens = lambda: torch.zeros(3, 2 * T - 1, D, dtype=torch.bfloat16, device="cuda").transpose(0, 1)[::2]  # noqa: E731
+    flat = torch.zeros(64 * D, dtype=torch.bfloat16, device="cuda")
+    for make in (heads, tokens):
+        x = make().copy_(torch.randn(T, 3, D, generator=g, device="cuda"))
+        want, _ = ck.ckv_qk_norm_rope(x.contiguous(), pos, rope)
+        out, _ = ck.ckv_qk_norm_rope(x, pos, rope, q_out=make())
+        assert torch.equal(out, want)
+        base = x._base
+        rest = base.clone()
+        ck.ckv_qk_norm_rope(x, pos, rope, q_out=x)
+        assert torch.equal(x, want)
+        x.zero_()
+        mask = torch.ones_like(base)
+        mask.as_strided(x.shape, x.stride()).zero_()
+        assert torch.equal(base, rest * mask)  # nothing beside the rows
+    x = torch.zeros(T, 3, D, dtype=torch.bfloat16, device="cuda")
+    for st, sh in ((2 * D, D), (D, D), (D, 2 * D), (4 * D, 2 * D), (0, D), (3 * D, D - 8), (D, 4 * D)):
+        with pytest.raises(ValueError):
+            ck.ckv_qk_norm_rope(x, pos, rope, q_out=flat.as_strided((T, 3, D), (st, sh, 1)))
+    for st, sh in ((3 * D, D), (5 * D, 2 * D), (D, 5 * D), (2 * D, 9 * D)):
+        ck.ckv_qk_norm_rope(x, pos, rope, q_out=flat.as_strided((T, 3, D), (st, sh, 1)))
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------ block tables
 @pytest.mark.parametrize("D,H", [(128, 5), (128, 40), (256, 8), (512, 48), (512, 80)])
 def test_fp4_attention_one_table_row_for_all_requests(ck, D, H):
