@@ -7,6 +7,7 @@ inputs of the workloads the library is measured on.
 from .ckv import (  # noqa: F401
     CkvError,
     ckv_build_step_maps,
+    ckv_build_tree_masks,
     ckv_c128_online_decode,
     ckv_c128_online_decode_fp8,
     ckv_c128_online_prefill,
@@ -25,7 +26,11 @@ from .ckv import (  # noqa: F401
     ckv_kpool_compress_set_variant,
     ckv_kpool_decode_update,
     ckv_kpool_seed_tail,
+    ckv_kv_append,
+    ckv_kv_attention,
+    ckv_kv_attention_workspace,
     ckv_latency_probe,
+    ckv_merge_attention,
     ckv_plan_online_prefill,
     ckv_plan_online_prefill_device,
     ckv_qk_norm_rope,

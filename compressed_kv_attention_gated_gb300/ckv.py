@@ -50,10 +50,14 @@ _STATUS_FUNCS = {
     "ckv_fp4_store": 13,
     "ckv_fp4_load": 13,
     "ckv_fp4_attention": 26,
+    "ckv_kv_append": 18,
+    "ckv_build_tree_masks": 11,
+    "ckv_kv_attention": 26,
+    "ckv_merge_attention": 12,
 }
 EXPORTED = tuple(_STATUS_FUNCS) + ("ckv_status_string", "ckv_last_cuda_error", "ckv_abi_version",
                                     "ckv_c128_prefill_set_variant", "ckv_kpool_compress_set_variant",
-                                    "ckv_fp4_attention_workspace")
+                                    "ckv_fp4_attention_workspace", "ckv_kv_attention_workspace")
 
 
 class NormRows(ctypes.Structure):
@@ -64,6 +68,29 @@ class NormRows(ctypes.Structure):
                 ("out_stride_t", ctypes.c_int64), ("out_stride_h", ctypes.c_int64), ("tokens", ctypes.c_int64),
                 ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class KvCache(ctypes.Structure):
+    """ckv_kv_cache of include/ckv.h."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride_page", ctypes.c_int64),
+                ("k_stride_row", ctypes.c_int64), ("k_stride_head", ctypes.c_int64), ("v_stride_page", ctypes.c_int64),
+                ("v_stride_row", ctypes.c_int64), ("v_stride_head", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class KvRows(ctypes.Structure):
+    """ckv_kv_rows of include/ckv.h."""
+
+    _fields_ = [("x", ctypes.c_void_p), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class AttentionPart(ctypes.Structure):
+    """ckv_attention_part of include/ckv.h."""
+
+    _fields_ = [("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
 class CkvError(RuntimeError):
@@ -170,6 +197,16 @@ def load():
             L.ckv_fp4_attention_workspace.argtypes = [i64, i32, i32, i32, i64]
             L.ckv_fp4_attention.argtypes = [vp, i64, i64, i64, i32, i32, vp, i64, i32, f32, vp, i64, i32, vp, i32, vp,
                                             i64, f32, vp, vp, vp, vp, i64, i32, vp, vp]
+            cache, rows = ctypes.POINTER(KvCache), ctypes.POINTER(KvRows)
+            L.ckv_kv_append.argtypes = [rows, rows, rows, vp, i64, i64, i64, cache, vp, vp, vp, i64, i32, i32, i32, i32,
+                                        vp, vp]
+            L.ckv_build_tree_masks.argtypes = [vp, vp, i32, vp, i64, i32, vp, vp, i32, vp, vp]
+            L.ckv_kv_attention_workspace.restype = ctypes.c_int64
+            L.ckv_kv_attention_workspace.argtypes = [i64, i32, i32, i32, i32, i64, i32, i32, i32]
+            L.ckv_kv_attention.argtypes = [vp, i64, i64, i64, i32, cache, vp, i64, i32, vp, i32, vp, i64, i32, i32, vp,
+                                           i32, f32, vp, vp, vp, vp, i64, i32, vp, vp]
+            L.ckv_merge_attention.argtypes = [ctypes.POINTER(AttentionPart), i32, i32, i64, i32, i32, vp, vp, i32, vp,
+                                              i32, vp]
             L.ckv_status_string.restype = ctypes.c_char_p
             L.ckv_status_string.argtypes = [ctypes.c_int32]
             L.ckv_last_cuda_error.restype = ctypes.c_int32
@@ -748,6 +785,110 @@ def ckv_fp4_attention(q, kv_cache, block_table, row_start, ctx_rows, max_rows, s
                                             cache_scale, sink, out, lse, workspace, use_pdl, err_word, _raw(stream))
     if status:
         _check("ckv_fp4_attention", status)
+    return out, lse
+
+
+# ------------------------------------------- the tokens that are not compressed yet
+def ckv_kv_append(k, v, k_cache, v_cache, loc, positions=None, cos_sin=None, rope_offset=None, interleaved=False, q=None,
+                  q_out=None, use_pdl=True, err_word=None, stream=None):
+    """Append keys (rotated) and values to a paged cache and rotate queries in the same pass; see
+    ckv_kv_append in include/ckv.h.
+
+    k, v [T, KH, D] and q [T, H, D] float32/bf16 of one type (last dim contiguous); v None: only
+    keys are stored; caches bf16 [pages, page_size, KH, D] (last dim contiguous, any other
+    strides without overlap, e.g. a transposed [pages, KH, page_size, D]); loc int64 [T], < 0: not
+    stored; positions int32 [T], < 0 skips a token; cos_sin float32 [positions, rope_dim] or
+    None (no rotation); rope_offset defaults to the last rope_dim channels.  Returns q_out: a new
+    bf16 tensor, or the one given (it may be q), or None without q.
+    """
+    native = _binding or _native()
+    if stream is not None and q is not None and q_out is None:
+        _cuda("ckv_kv_append", k, q)
+        with _on(stream):
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    status, q_out = native.kv_append(k, v, k_cache, v_cache, loc, positions, cos_sin, rope_offset, interleaved, q, q_out,
+                                     use_pdl, err_word, _raw(stream))
+    if status:
+        _check("ckv_kv_append", status)
+    return q_out
+
+
+def ckv_build_tree_masks(parents, row_start, ctx_rows=None, words=1, tree_mask=None, positions=None, use_pdl=True,
+                         err_word=None, stream=None):
+    """Masks and positions of trees of drafted tokens; see ckv_build_tree_masks in include/ckv.h.
+
+    parents int32 [T]: index within its request, or -1; row_start int32 [B + 1]; ctx_rows int32 [T]
+    or None; words 1..16, 64 drafts each.  Returns (tree_mask, positions): int64 [T, words] and
+    int32 [T], new or the ones given.
+    """
+    native = _binding or _native()
+    if stream is not None:
+        _cuda("ckv_build_tree_masks", parents)
+        T = parents.numel()
+        with _on(stream):
+            tree_mask = torch.empty((T, words), dtype=torch.int64, device=parents.device) if tree_mask is None else tree_mask
+            positions = torch.empty(T, dtype=torch.int32, device=parents.device) if positions is None else positions
+    status, tree_mask, positions = native.tree_masks(parents, row_start, ctx_rows, words, tree_mask, positions, use_pdl,
+                                                     err_word, _raw(stream))
+    if status:
+        _check("ckv_build_tree_masks", status)
+    return tree_mask, positions
+
+
+def ckv_kv_attention_workspace(T, B, H, KH, D, max_rows, window=0, first_rows=0, mask_words=0):
+    """Bytes of workspace that ckv_kv_attention needs for these sizes (0 for those that it refuses)."""
+    return load().ckv_kv_attention_workspace(int(T), int(B), int(H), int(KH), int(D), int(max_rows), int(window),
+                                             int(first_rows), int(mask_words))
+
+
+def ckv_kv_attention(q, k_cache, v_cache, block_table, row_start, ctx_rows, max_rows, softmax_scale, window=0, first_rows=0,
+                     tree_mask=None, sink=None, out=None, lse=None, workspace=None, use_pdl=True, err_word=None, stream=None):
+    """Attention over the uncompressed cache; see ckv_kv_attention in include/ckv.h.
+
+    q bf16 [T, H, D] (last dim contiguous); caches as for ckv_kv_append, one tensor for both where
+    rows are key and value; block_table int32 [B, max_pages] (last dim contiguous; rows apart, or
+    one row expanded over all requests); row_start int32 [B + 1]; ctx_rows int32 [T]: rows of the
+    context, with the token itself, or with tree_mask the committed rows alone; max_rows at least
+    the rows of every request, drafts included; window 0 or the rows of the window, first_rows that
+    stay visible beside it; tree_mask int64 [T, words] or None; sink float32 [H] or None.  Returns
+    (out, lse): bf16 [T, H, D] and float32 [T, H].  workspace: a uint8 tensor of
+    ckv_kv_attention_workspace() bytes, by default taken from the caching allocator of torch.
+    """
+    native = _binding or _native()
+    if stream is not None:
+        _cuda("ckv_kv_attention", q)
+        T, H, D = q.shape
+        words = 0 if tree_mask is None else tree_mask.shape[1]
+        need = ckv_kv_attention_workspace(T, row_start.numel() - 1, H, k_cache.shape[2], D, max_rows, window, first_rows, words)
+        with _on(stream):
+            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+            lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if lse is None else lse
+            if workspace is None and need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    status, out, lse = native.kv_attention(q, k_cache, v_cache, block_table, row_start, ctx_rows, max_rows, softmax_scale,
+                                           window, first_rows, tree_mask, sink, out, lse, workspace, use_pdl, err_word,
+                                           _raw(stream))
+    if status:
+        _check("ckv_kv_attention", status)
+    return out, lse
+
+
+def ckv_merge_attention(outs, lses, out=None, lse=None, positions=None, use_pdl=True, stream=None):
+    """One attention from those over several sets of rows; see ckv_merge_attention in include/ckv.h.
+
+    outs: 1..8 float32/bf16 [T, H, D] of one type, lses: as many float32 [T, H], contiguous;
+    positions int32 [T] or None, < 0: a token's rows are left as they are.  Returns (out, lse):
+    a new bf16 tensor and a float32 one, or those given (out float32/bf16, it may be one of outs).
+    """
+    native = _binding or _native()
+    if stream is not None:
+        _cuda("ckv_merge_attention", *outs)
+        with _on(stream):
+            out = torch.empty(outs[0].shape, dtype=torch.bfloat16, device=outs[0].device) if out is None else out
+            lse = torch.empty(outs[0].shape[:2], dtype=torch.float32, device=outs[0].device) if lse is None else lse
+    status, out, lse = native.merge_attention(outs, lses, positions, out, lse, use_pdl, _raw(stream))
+    if status:
+        _check("ckv_merge_attention", status)
     return out, lse
 
 

@@ -7,6 +7,7 @@
 // which ckv.py turns into CkvError.  No arithmetic, nothing kept between calls.
 #include <Python.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <stdexcept>
 
@@ -360,12 +361,231 @@ PyObject* fp4_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// A paged cache of uncompressed rows [pages, page_size, KH, D] and its strides; `written`: its rows
+// may not share memory.
+void kv_side(const at::Tensor& t, bool written, uint16_t*& p, int64_t& page, int64_t& row, int64_t& head) {
+  need(t.scalar_type() == at::kBFloat16 && t.dim() == 4 && (t.stride(3) == 1 || t.numel() == 0),
+       "a cache must be bf16 [pages, page_size, KH, D], last dim contiguous");
+  p = static_cast<uint16_t*>(t.data_ptr());
+  int64_t* to[3] = {&page, &row, &head};
+  for (int i = 0; i < 3; ++i) *to[i] = t.size(i) > 1 ? t.stride(i) : 0;  // the step of a dimension of one entry is never used
+  if (!written || t.numel() == 0) return;
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int x, int y) { return t.stride(x) < t.stride(y); });
+  int64_t span = t.size(3);
+  for (int i : order) {
+    if (t.size(i) == 1) continue;
+    need(t.stride(i) >= span, "rows of a cache overlap");
+    span += (t.size(i) - 1) * t.stride(i);
+  }
+}
+ckv_kv_cache kv_cache(const at::Tensor& k, const at::Tensor* v, bool written) {
+  ckv_kv_cache c{};
+  kv_side(k, written, c.k, c.k_stride_page, c.k_stride_row, c.k_stride_head);
+  if (v) {
+    need(v->sizes() == k.sizes(), "the caches of keys and values must have one shape");
+    kv_side(*v, written, c.v, c.v_stride_page, c.v_stride_row, c.v_stride_head);
+  }
+  need(k.size(1) <= INT32_MAX && k.size(2) <= INT32_MAX && k.size(3) <= 1024, "unsupported page_size, heads or D");
+  c.num_pages = k.size(0);
+  c.page_size = static_cast<int32_t>(k.size(1));
+  c.heads = static_cast<int32_t>(k.size(2));
+  c.D = static_cast<int32_t>(k.size(3));
+  return c;
+}
+
+ckv_kv_rows kv_rows(const at::Tensor& x, int64_t T, int64_t D) {
+  need(x.dim() == 3 && x.size(0) == T && x.size(2) == D && (x.stride(2) == 1 || x.numel() == 0),
+       "q, k and v must be [T, heads, D], last dim contiguous");
+  need(x.size(1) <= INT32_MAX, "too many heads");
+  ckv_kv_rows r{};
+  r.x = x.data_ptr();
+  r.stride_t = T > 1 ? x.stride(0) : 0;
+  r.stride_h = x.size(1) > 1 ? x.stride(1) : 0;
+  r.heads = static_cast<int32_t>(x.size(1));
+  r.dtype = dtype_of(x);
+  return r;
+}
+
+PyObject* kv_append(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(v, n, 14);
+    const at::Tensor& k = a.tensor();
+    const at::Tensor* val = a.optional();
+    const at::Tensor& kc = a.tensor();
+    const at::Tensor* vc = a.optional();
+    const at::Tensor& loc = a.tensor();
+    const at::Tensor *pos = a.optional(), *cs = a.optional();
+    PyObject* at_arg = a.object();
+    const int interleaved = a.flag();
+    const at::Tensor *q = a.optional(), *qo = a.optional();
+    const int pdl = a.flag();
+    const at::Tensor* err = a.optional();
+    a.on_device();
+    need(k.dim() == 3, "q, k and v must be [T, heads, D], last dim contiguous");
+    need(!val || vc, "v needs v_cache");
+    need(!qo || q, "q_out needs q");
+    const ckv_kv_cache c = kv_cache(kc, val ? vc : nullptr, true);
+    const int64_t T = k.size(0), D = c.D;
+    need(vec(loc, at::kLong, T), "loc must be contiguous int64 [T]");
+    need(!pos || vec(*pos, at::kInt, T), "positions must be contiguous int32 [T]");
+    need(!cs || (cs->scalar_type() == at::kFloat && cs->dim() == 2 && cs->is_contiguous()), "cos_sin must be contiguous float32 [positions, rope_dim]");
+    const int64_t R = cs ? cs->size(1) : 0;
+    need(R <= D, "rope_dim must be at most D");
+    need(!err || err->scalar_type() == at::kInt, "err_word must be int32");
+    int64_t at = D - R;
+    if (at_arg != Py_None) {
+      at = PyLong_AsLongLong(at_arg);
+      if (at == -1 && PyErr_Occurred()) return nullptr;
+      need(at >= 0 && at <= D, "rope_offset must be in 0..D - rope_dim");
+    }
+    const ckv_kv_rows rk = kv_rows(k, T, D);
+    ckv_kv_rows rv{}, rq{};
+    if (val) rv = kv_rows(*val, T, D);
+    at::Tensor out;
+    int64_t st = 0, sh = 0;
+    if (q) {
+      rq = kv_rows(*q, T, D);
+      out = qo ? *qo : at::empty({T, q->size(1), D}, q->options().dtype(at::kBFloat16));
+      need(out.scalar_type() == at::kBFloat16 && out.sizes() == q->sizes() && (out.stride(2) == 1 || out.numel() == 0),
+           "q_out must be bf16 with the shape of q, last dim contiguous");
+      const int64_t H = q->size(1);
+      st = T > 1 ? out.stride(0) : 0;
+      sh = H > 1 ? out.stride(1) : 0;
+      need((T <= 1 || st >= D) && (H <= 1 || sh >= D) && (T <= 1 || H <= 1 || st >= (H - 1) * sh + D || sh >= (T - 1) * st + D),
+           "rows of an output overlap");
+    }
+    const ckv_status s = ckv_kv_append(&rk, val ? &rv : nullptr, q ? &rq : nullptr, q ? static_cast<uint16_t*>(out.data_ptr()) : nullptr, st, sh,
+                                       T, &c, ptr<int64_t>(loc), ptr<int32_t>(pos), ptr<float>(cs), cs ? cs->size(0) : 0,
+                                       static_cast<int32_t>(R), static_cast<int32_t>(at), interleaved, pdl, ptr<int32_t>(err), a.stream());
+    PyObject* made = Py_None;
+    if (q) made = THPVariable_Wrap(out);
+    else Py_INCREF(made);
+    return Py_BuildValue("iN", static_cast<int>(s), made);
+  });
+}
+
+PyObject* tree_masks(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(v, n, 9);
+    const at::Tensor &parents = a.tensor(), &start = a.tensor();
+    const at::Tensor* ctx = a.optional();
+    const int32_t words = a.integer32("words");
+    const at::Tensor *mask = a.optional(), *pos = a.optional();
+    const int pdl = a.flag();
+    const at::Tensor* err = a.optional();
+    a.on_device();
+    const int64_t T = parents.numel();
+    need(vec(parents, at::kInt, T) && (!ctx || vec(*ctx, at::kInt, T)), "parents and ctx_rows must be contiguous int32 [T]");
+    need(start.scalar_type() == at::kInt && start.is_contiguous() && start.numel() >= 1 && start.numel() <= INT32_MAX,
+         "row_start must be contiguous int32 [B + 1]");
+    need(words >= 1 && words <= 16, "words must be in 1..16");
+    need(!err || err->scalar_type() == at::kInt, "err_word must be int32");
+    at::Tensor m = mask ? *mask : at::empty({T, words}, parents.options().dtype(at::kLong));
+    at::Tensor p = pos ? *pos : at::empty({T}, parents.options());
+    need(m.scalar_type() == at::kLong && m.is_contiguous() && m.dim() == 2 && m.size(0) == T && m.size(1) == words,
+         "tree_mask must be contiguous int64 [T, words]");
+    need(vec(p, at::kInt, T), "positions must be contiguous int32 [T]");
+    const ckv_status s = ckv_build_tree_masks(ptr<int32_t>(parents), ptr<int32_t>(start), static_cast<int32_t>(start.numel() - 1),
+                                              ptr<int32_t>(ctx), T, words, ptr<uint64_t>(m), ptr<int32_t>(p), pdl, ptr<int32_t>(err), a.stream());
+    return Py_BuildValue("iNN", static_cast<int>(s), THPVariable_Wrap(m), THPVariable_Wrap(p));
+  });
+}
+
+PyObject* kv_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(v, n, 18);
+    const at::Tensor &q = a.tensor(), &kc = a.tensor(), &vc = a.tensor(), &table = a.tensor(), &start = a.tensor(), &ctx = a.tensor();
+    const int64_t max_rows = a.integer();
+    const float scale = static_cast<float>(a.number());
+    const int32_t window = a.integer32("window"), first = a.integer32("first_rows");
+    const at::Tensor *mask = a.optional(), *sink = a.optional(), *out = a.optional(), *lse = a.optional(), *ws = a.optional();
+    const int pdl = a.flag();
+    const at::Tensor* err = a.optional();
+    a.on_device();
+    need(q.scalar_type() == at::kBFloat16 && q.dim() == 3 && (q.stride(2) == 1 || q.numel() == 0),
+         "q must be bf16 [T, H, D], last dim contiguous");
+    const ckv_kv_cache c = kv_cache(kc, &vc, false);
+    const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
+    need(D == c.D, "q and the caches must have one D");
+    need(H <= INT32_MAX, "unsupported H");
+    need(start.scalar_type() == at::kInt && start.is_contiguous() && start.numel() >= 1 && start.numel() <= INT32_MAX,
+         "row_start must be contiguous int32 [B + 1]");
+    const int64_t B = start.numel() - 1;
+    const int64_t stride = table_rows(table, B, true, "block_table must be int32 [B, max_pages], last dim contiguous");
+    need(table.size(1) <= INT32_MAX, "block_table is too wide");
+    need(vec(ctx, at::kInt, T), "ctx_rows must be contiguous int32 [T]");
+    need(!mask || (mask->scalar_type() == at::kLong && mask->is_contiguous() && mask->dim() == 2 && mask->size(0) == T && mask->size(1) >= 1 &&
+                   mask->size(1) <= 16),
+         "tree_mask must be contiguous int64 [T, 1..16]");
+    need(!sink || vec(*sink, at::kFloat, H), "sink must be contiguous float32 [H]");
+    need(!err || err->scalar_type() == at::kInt, "err_word must be int32");
+    const int32_t words = mask ? static_cast<int32_t>(mask->size(1)) : 0;
+    at::Tensor o = out ? *out : at::empty({T, H, D}, q.options());
+    at::Tensor l = lse ? *lse : at::empty({T, H}, q.options().dtype(at::kFloat));
+    need(o.scalar_type() == at::kBFloat16 && o.is_contiguous() && o.sizes() == q.sizes(), "out must be contiguous bf16 [T, H, D]");
+    need(l.scalar_type() == at::kFloat && l.is_contiguous() && l.dim() == 2 && l.size(0) == T && l.size(1) == H,
+         "lse must be contiguous float32 [T, H]");
+    need(!ws || ws->is_contiguous(), "workspace must be contiguous");
+    const int64_t bytes = ckv_kv_attention_workspace(T, static_cast<int32_t>(std::min<int64_t>(B, INT32_MAX)), static_cast<int32_t>(H), c.heads,
+                                                     c.D, max_rows, window, first, words);
+    at::Tensor w = ws ? *ws : bytes > 0 ? at::empty({bytes}, q.options().dtype(at::kByte)) : at::Tensor();
+    const ckv_status s = ckv_kv_attention(
+        ptr<uint16_t>(q), T > 1 ? q.stride(0) : 0, H > 1 ? q.stride(1) : 0, T, static_cast<int32_t>(H), &c, ptr<int32_t>(table), stride,
+        static_cast<int32_t>(table.size(1)), ptr<int32_t>(start), static_cast<int32_t>(B), ptr<int32_t>(ctx), max_rows, window, first,
+        ptr<uint64_t>(mask), words, scale, ptr<float>(sink), ptr<uint16_t>(o), ptr<float>(l), w.defined() ? w.data_ptr() : nullptr,
+        w.defined() ? static_cast<int64_t>(w.nbytes()) : 0, pdl, ptr<int32_t>(err), a.stream());
+    return Py_BuildValue("iNN", static_cast<int>(s), THPVariable_Wrap(o), THPVariable_Wrap(l));
+  });
+}
+
+PyObject* merge_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Args a(v, n, 7);
+    PyObject *outs = a.object(), *lses = a.object();
+    const at::Tensor *pos = a.optional(), *out = a.optional(), *lse = a.optional();
+    const int pdl = a.flag();
+    need((PyList_Check(outs) || PyTuple_Check(outs)) && (PyList_Check(lses) || PyTuple_Check(lses)), "outs and lses must be lists of tensors");
+    const Py_ssize_t parts = PySequence_Fast_GET_SIZE(outs);
+    need(parts >= 1 && parts <= 8 && PySequence_Fast_GET_SIZE(lses) == parts, "1..8 outs, and as many lses");
+    ckv_attention_part p[8];
+    const at::Tensor& o0 = *a.check(PySequence_Fast_GET_ITEM(outs, 0), false);
+    need(o0.dim() == 3, "outs must be contiguous [T, H, D] of one type");
+    const int64_t T = o0.size(0), H = o0.size(1), D = o0.size(2);
+    for (Py_ssize_t i = 0; i < parts; ++i) {
+      const at::Tensor& o = *a.check(PySequence_Fast_GET_ITEM(outs, i), false);
+      const at::Tensor& l = *a.check(PySequence_Fast_GET_ITEM(lses, i), false);
+      need(o.is_contiguous() && o.sizes() == o0.sizes() && o.scalar_type() == o0.scalar_type(), "outs must be contiguous [T, H, D] of one type");
+      need(l.scalar_type() == at::kFloat && l.is_contiguous() && l.dim() == 2 && l.size(0) == T && l.size(1) == H,
+           "lses must be contiguous float32 [T, H]");
+      p[i] = {o.data_ptr(), static_cast<const float*>(l.data_ptr())};
+    }
+    a.on_device();
+    need(H <= INT32_MAX && D <= 1024, "unsupported H or D");
+    need(!pos || vec(*pos, at::kInt, T), "positions must be contiguous int32 [T]");
+    at::Tensor o = out ? *out : at::empty({T, H, D}, o0.options().dtype(at::kBFloat16));
+    at::Tensor l = lse ? *lse : at::empty({T, H}, o0.options().dtype(at::kFloat));
+    need(o.is_contiguous() && o.sizes() == o0.sizes(), "out must be contiguous [T, H, D]");
+    need(l.scalar_type() == at::kFloat && l.is_contiguous() && l.dim() == 2 && l.size(0) == T && l.size(1) == H,
+         "lse must be contiguous float32 [T, H]");
+    const ckv_status s = ckv_merge_attention(p, static_cast<int32_t>(parts), dtype_of(o0), T, static_cast<int32_t>(H), static_cast<int32_t>(D),
+                                             ptr<int32_t>(pos), o.data_ptr(), dtype_of(o), ptr<float>(l), pdl, a.stream());
+    return Py_BuildValue("iNN", static_cast<int>(s), THPVariable_Wrap(o), THPVariable_Wrap(l));
+  });
+}
+
+#define METHOD(name) \
+  {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {
     {"step_maps", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(step_maps)), METH_FASTCALL, nullptr},
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(qk_norm_rope)), METH_FASTCALL, nullptr},
     {"fp4_store", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fp4_store)), METH_FASTCALL, nullptr},
     {"fp4_load", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fp4_load)), METH_FASTCALL, nullptr},
     {"fp4_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fp4_attention)), METH_FASTCALL, nullptr},
+    METHOD(kv_append),
+    METHOD(tree_masks),
+    METHOD(kv_attention),
+    METHOD(merge_attention),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "ckv_binding", "Tensor checks and calls of libckv's serving-step entry points.", -1,
                        kMethods, nullptr, nullptr, nullptr, nullptr};

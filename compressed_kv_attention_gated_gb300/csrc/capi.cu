@@ -97,6 +97,30 @@ ckv_status check_fp4_rows(ckv::Fp4RowsArgs& a, const void* rows, ckv_dtype dtype
   return CKV_OK;
 }
 
+// A cache of uncompressed rows; `values`: its v is used.
+ckv_status check_kv_cache(const ckv_kv_cache* c, bool values) {
+  if (!c) return CKV_ERR_NULL;
+  if (c->num_pages < 0 || c->num_pages > INT32_MAX || c->page_size < 1 || c->heads < 1 || c->heads > 1024 || !head_dim_ok(c->D) ||
+      c->reserved != 0 || c->k_stride_page < 0 || c->k_stride_row < 0 || c->k_stride_head < 0 ||
+      (values && (c->v_stride_page < 0 || c->v_stride_row < 0 || c->v_stride_head < 0)))
+    return CKV_ERR_SHAPE;
+  return CKV_OK;
+}
+ckv_status check_kv_pointers(const ckv_kv_cache* c, bool values) {
+  if (!c->k || (values && !c->v)) return CKV_ERR_NULL;
+  if (!aligned(c->k, 16) || c->k_stride_page % 8 || c->k_stride_row % 8 || c->k_stride_head % 8 ||
+      (values && (!aligned(c->v, 16) || c->v_stride_page % 8 || c->v_stride_row % 8 || c->v_stride_head % 8)))
+    return CKV_ERR_ALIGN;
+  return CKV_OK;
+}
+
+// Sizes of ckv_kv_attention with work to do: (token, head) rows are counted in 32 bits.
+bool kv_attention_sizes_ok(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows, int32_t window, int32_t first_rows,
+                           int32_t words) {
+  return B <= kMaxAttentionRequests && H >= 1 && H <= 1024 && KH >= 1 && H % KH == 0 && T <= INT32_MAX / H && head_dim_ok(D) &&
+         max_rows >= 1 && max_rows <= CKV_KV_ATTENTION_MAX_ROWS && window >= 0 && first_rows >= 0 && words >= 0 && words <= 16;
+}
+
 }  // namespace
 
 namespace ckv {
@@ -714,6 +738,176 @@ ckv_status ckv_fp4_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_st
   a.g = cache_scale;
   a.softmax_scale = softmax_scale;
   return cuda_status(ckv::launch_fp4_attention(a, D, use_pdl != 0, static_cast<cudaStream_t>(stream)));
+}
+
+ckv_status ckv_kv_append(const ckv_kv_rows* k, const ckv_kv_rows* v, const ckv_kv_rows* q, uint16_t* q_out,
+                         int64_t q_out_stride_t, int64_t q_out_stride_h, int64_t T, const ckv_kv_cache* cache,
+                         const int64_t* loc, const int32_t* positions, const float* cos_sin, int64_t num_positions,
+                         int32_t rope_dim, int32_t rope_offset, int32_t interleaved, int32_t use_pdl, int32_t* err_word,
+                         void* stream) {
+  if (!k) return CKV_ERR_NULL;
+  if (ckv_status c = check_kv_cache(cache, v != nullptr)) return c;
+  const int32_t D = cache->D;
+  if (T < 0 || rope_dim < 0 || rope_dim % 2 || rope_offset < 0 || rope_offset % 2 || rope_dim > D || rope_offset > D - rope_dim ||
+      num_positions < 0)
+    return CKV_ERR_SHAPE;
+  ckv::KvAppendArgs a{};
+  const ckv_kv_rows* sets[3] = {q, k, v};
+  int64_t heads = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (!sets[i]) continue;
+    const ckv_kv_rows& r = *sets[i];
+    if (!dtype_ok(r.dtype) || r.dtype != k->dtype) return CKV_ERR_DTYPE;
+    if (r.heads < 0 || r.stride_t < 0 || r.stride_h < 0 || (i > 0 && r.heads != cache->heads)) return CKV_ERR_SHAPE;
+    heads += r.heads;
+    a.set[i] = r;
+  }
+  if (heads > (1 << 30)) return CKV_ERR_SHAPE;
+  if (T == 0) return CKV_OK;
+  if (T > (1 << 30) / heads) return CKV_ERR_SHAPE;  // rows are counted in 32 bits
+  const int64_t step = k->dtype == CKV_F32 ? 4 : 8;
+  for (const ckv_kv_rows* r : sets) {
+    if (!r || r->heads == 0) continue;
+    if (!r->x) return CKV_ERR_NULL;
+    if (!aligned(r->x, 16) || r->stride_t % step || r->stride_h % step) return CKV_ERR_ALIGN;
+  }
+  if (ckv_status c = check_kv_pointers(cache, v != nullptr)) return c;
+  if (v && cache->v == cache->k) return CKV_ERR_SHAPE;  // keys and values written to the same rows
+  if (!loc || (rope_dim > 0 && (!cos_sin || !positions))) return CKV_ERR_NULL;
+  if (!aligned(loc, 8) || !aligned(positions, 4) || !aligned(cos_sin, 4) || !aligned(err_word, 4)) return CKV_ERR_ALIGN;
+  if (q && q->heads > 0) {
+    if (!q_out) return CKV_ERR_NULL;
+    if (q_out_stride_t < 0 || q_out_stride_h < 0) return CKV_ERR_SHAPE;
+    if (!aligned(q_out, 16) || q_out_stride_t % 8 || q_out_stride_h % 8) return CKV_ERR_ALIGN;
+    // rows read and rows written at the same place have to be the same rows
+    if (q_out == q->x && (q->dtype != CKV_BF16 || q_out_stride_t != q->stride_t || q_out_stride_h != q->stride_h)) return CKV_ERR_SHAPE;
+  }
+  a.q_out = q_out;
+  a.qo_st = q_out_stride_t;
+  a.qo_sh = q_out_stride_h;
+  a.T = T;
+  a.cache = *cache;
+  a.loc = loc;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.num_positions = num_positions;
+  a.err = err_word;
+  a.rope_dim = rope_dim;
+  a.rope_offset = rope_offset;
+  a.interleaved = interleaved != 0;
+  a.page_shift = pow2_shift(cache->page_size);
+  return cuda_status(ckv::launch_kv_append(a, D, k->dtype, use_pdl != 0, static_cast<cudaStream_t>(stream)));
+}
+
+ckv_status ckv_build_tree_masks(const int32_t* parents, const int32_t* row_start, int32_t B, const int32_t* ctx_rows,
+                                int64_t T, int32_t words, uint64_t* tree_mask, int32_t* positions, int32_t use_pdl,
+                                int32_t* err_word, void* stream) {
+  if (B < 0 || B > kMaxAttentionRequests || T < 0 || T > INT32_MAX || words < 1 || words > 16) return CKV_ERR_SHAPE;
+  if (T == 0) return CKV_OK;
+  if (!tree_mask || (B > 0 && (!parents || !row_start))) return CKV_ERR_NULL;
+  if (!aligned(parents, 4) || !aligned(row_start, 4) || !aligned(ctx_rows, 4) || !aligned(tree_mask, 8) || !aligned(positions, 4) ||
+      !aligned(err_word, 4))
+    return CKV_ERR_ALIGN;
+  ckv::TreeMasksArgs a{};
+  a.parents = parents;
+  a.row_start = row_start;
+  a.ctx_rows = ctx_rows;
+  a.mask = tree_mask;
+  a.positions = positions;
+  a.err = err_word;
+  a.T = T;
+  a.B = B;
+  a.words = words;
+  return cuda_status(ckv::launch_tree_masks(a, use_pdl != 0, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t ckv_kv_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows,
+                                   int32_t window, int32_t first_rows, int32_t mask_words) {
+  if (T <= 0 || B <= 0 || !kv_attention_sizes_ok(T, B, H, KH, D, max_rows, window, first_rows, mask_words)) return 0;
+  return ckv::kv_attention_workspace(T, B, H, KH, D, max_rows, window, first_rows, mask_words);
+}
+
+ckv_status ckv_kv_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T, int32_t H,
+                            const ckv_kv_cache* cache, const int32_t* block_table, int64_t table_stride,
+                            int32_t max_pages, const int32_t* row_start, int32_t B, const int32_t* ctx_rows,
+                            int64_t max_rows, int32_t window, int32_t first_rows, const uint64_t* tree_mask,
+                            int32_t mask_words, float softmax_scale, const float* sink, uint16_t* out, float* lse,
+                            void* workspace, int64_t workspace_bytes, int32_t use_pdl, int32_t* err_word, void* stream) {
+  if (ckv_status c = check_kv_cache(cache, true)) return c;
+  const int32_t D = cache->D, KH = cache->heads;
+  if (T < 0 || B < 0 || B > kMaxAttentionRequests || H < 1 || H > 1024 || H % KH || max_pages < 0 ||
+      (table_stride < max_pages && table_stride != 0) || window < 0 || first_rows < 0 || mask_words < 0 || mask_words > 16 ||
+      !std::isfinite(softmax_scale))
+    return CKV_ERR_SHAPE;
+  if (T == 0 || B == 0) return CKV_OK;
+  if (!kv_attention_sizes_ok(T, B, H, KH, D, max_rows, window, first_rows, mask_words) ||
+      max_rows > static_cast<int64_t>(max_pages) * cache->page_size || q_stride_t < 0 || q_stride_h < 0)
+    return CKV_ERR_SHAPE;
+  if (!q || !block_table || !row_start || !ctx_rows || !out || (mask_words > 0 && !tree_mask)) return CKV_ERR_NULL;
+  if (ckv_status c = check_kv_pointers(cache, true)) return c;
+  if (!aligned(q, 16) || q_stride_t % 8 || q_stride_h % 8 || !aligned(block_table, 4) || !aligned(row_start, 4) || !aligned(ctx_rows, 4) ||
+      !aligned(tree_mask, 8) || !aligned(sink, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
+      !aligned(err_word, 4))
+    return CKV_ERR_ALIGN;
+  const int64_t need = ckv::kv_attention_workspace(T, B, H, KH, D, max_rows, window, first_rows, mask_words);
+  if (need > 0 && !workspace) return CKV_ERR_NULL;
+  if (workspace_bytes < need) return CKV_ERR_SHAPE;
+  // several CTAs read a query row, and one may have written its output before another has read
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t q1 = q0 + ((T - 1) * q_stride_t + (H - 1) * q_stride_h + D) * sizeof(uint16_t), o1 = o0 + T * H * D * sizeof(uint16_t);
+  if (q0 < o1 && o0 < q1) return CKV_ERR_SHAPE;
+  ckv::KvAttentionArgs a{};
+  a.q = q;
+  a.q_st = q_stride_t;
+  a.q_sh = q_stride_h;
+  a.cache = *cache;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.row_start = row_start;
+  a.ctx_rows = ctx_rows;
+  a.mask = mask_words > 0 ? tree_mask : nullptr;
+  a.sink = sink;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.err = err_word;
+  a.T = T;
+  a.H = H;
+  a.KH = KH;
+  a.G = H / KH;
+  a.B = B;
+  a.max_rows = static_cast<int32_t>(max_rows);
+  a.page_shift = pow2_shift(cache->page_size);
+  a.window = window;
+  a.first = window > 0 ? first_rows : 0;
+  a.words = mask_words;
+  a.softmax_scale = softmax_scale;
+  return cuda_status(ckv::launch_kv_attention(a, use_pdl != 0, static_cast<cudaStream_t>(stream)));
+}
+
+ckv_status ckv_merge_attention(const ckv_attention_part* parts, int32_t num_parts, ckv_dtype dtype, int64_t T, int32_t H,
+                               int32_t D, const int32_t* positions, void* out, ckv_dtype out_dtype, float* lse,
+                               int32_t use_pdl, void* stream) {
+  if (!parts) return CKV_ERR_NULL;
+  if (num_parts < 1 || num_parts > 8 || T < 0 || H < 1 || H > 1024 || T > INT32_MAX / H || !head_dim_ok(D)) return CKV_ERR_SHAPE;
+  if (!dtype_ok(dtype) || !dtype_ok(out_dtype)) return CKV_ERR_DTYPE;
+  if (T == 0) return CKV_OK;
+  if (!out) return CKV_ERR_NULL;
+  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(positions, 4)) return CKV_ERR_ALIGN;
+  ckv::MergeArgs a{};
+  for (int i = 0; i < num_parts; ++i) {
+    if (!parts[i].out || !parts[i].lse) return CKV_ERR_NULL;
+    if (!aligned(parts[i].out, 16) || !aligned(parts[i].lse, 4)) return CKV_ERR_ALIGN;
+    if (parts[i].out == out && dtype != out_dtype) return CKV_ERR_SHAPE;  // rows written over ones that are still to be read
+    a.part[i] = parts[i];
+  }
+  a.positions = positions;
+  a.out = out;
+  a.lse = lse;
+  a.rows = T * H;
+  a.n = num_parts;
+  a.H = H;
+  return cuda_status(ckv::launch_merge_attention(a, D, dtype, out_dtype, use_pdl != 0, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -194,6 +194,69 @@ struct Fp4AttentionArgs {
 constexpr int kFp4MaxSplits = 160, kFp4MaxRange = 1 << 17;
 static_assert(kFp4MaxSplits * kFp4MaxRange == CKV_FP4_ATTENTION_MAX_ROWS, "header");
 
+struct KvAppendArgs {
+  ckv_kv_rows set[3];  // queries, keys, values (heads == 0: none)
+  uint16_t* q_out;
+  int64_t qo_st, qo_sh;
+  int64_t T;
+  ckv_kv_cache cache;
+  const int64_t* loc;
+  const int32_t* positions;
+  const float* cos_sin;
+  int64_t num_positions;
+  int32_t* err;
+  int32_t rope_dim, rope_offset, interleaved, page_shift;
+};
+
+struct TreeMasksArgs {
+  const int32_t* parents;
+  const int32_t* row_start;
+  const int32_t* ctx_rows;
+  uint64_t* mask;
+  int32_t* positions;
+  int32_t* err;
+  int64_t T;
+  int32_t B, words;
+};
+
+struct MergeArgs {
+  ckv_attention_part part[8];
+  const int32_t* positions;
+  void* out;
+  float* lse;
+  int64_t rows;  // T * H
+  int32_t n, H;
+};
+
+struct KvAttentionArgs {
+  const uint16_t* q;
+  int64_t q_st, q_sh;
+  ckv_kv_cache cache;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* row_start;
+  const int32_t* ctx_rows;
+  const uint64_t* mask;  // [T][words]
+  const float* sink;
+  uint16_t* out;
+  float* lse;
+  void* workspace;
+  int32_t* err;
+  int64_t T;
+  int32_t H, KH, G, B, max_rows, page_shift;
+  int32_t window, first, words;
+  float softmax_scale;
+};
+constexpr int kKvMaxSplits = 160, kKvMaxRange = 1 << 17;
+static_assert(kKvMaxSplits * kKvMaxRange == CKV_KV_ATTENTION_MAX_ROWS, "header");
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, int D, int dtype, bool use_pdl, cudaStream_t s);
+cudaError_t launch_tree_masks(const TreeMasksArgs& a, bool use_pdl, cudaStream_t s);
+cudaError_t launch_merge_attention(const MergeArgs& a, int D, int dtype, int out_dtype, bool use_pdl, cudaStream_t s);
+int64_t kv_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows, int32_t window,
+                               int32_t first_rows, int32_t words);
+cudaError_t launch_kv_attention(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s);
+
 cudaError_t launch_step_maps(const StepMapsArgs& a, bool use_pdl, cudaStream_t s);
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int D, bool use_pdl, cudaStream_t s);
 cudaError_t launch_fp4_store(const Fp4RowsArgs& a, int D, int dtype, bool use_pdl, cudaStream_t s);

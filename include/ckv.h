@@ -658,6 +658,157 @@ ckv_status ckv_fp4_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_st
                              void* workspace, int64_t workspace_bytes, int32_t use_pdl,
                              int32_t* err_word, void* stream);
 
+/* ======================================================================
+ * The tokens that are not compressed yet (no counterpart in the sources): a
+ * paged cache of uncompressed keys and values, attention over it with a
+ * sliding window, first rows that stay visible and trees of drafted tokens,
+ * and the merging of that attention with the one over the compressed rows.
+ * The step maps of such a cache are those of ckv_build_step_maps with P = 1.
+ * ====================================================================== */
+
+/*
+ * A paged cache of bf16 rows of D channels.  Key row r (0..page_size - 1) of head h
+ * on page p begins at k + p*k_stride_page + r*k_stride_row + h*k_stride_head elements,
+ * a value row alike.  v == k with the same strides: every row is key and value.
+ * Bases are 16-byte aligned, strides are multiples of 8 elements and >= 0.
+ */
+typedef struct ckv_kv_cache {
+  uint16_t* k; /* device */
+  uint16_t* v; /* device */
+  int64_t k_stride_page, k_stride_row, k_stride_head;
+  int64_t v_stride_page, v_stride_row, v_stride_head;
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t heads; /* KH, of keys and values */
+  int32_t D;     /* 128, 256 or 512 */
+  int32_t reserved; /* 0 */
+} ckv_kv_cache;
+
+/* Rows of ckv_kv_append: row (t, h) at x + t*stride_t + h*stride_h elements, 16-byte aligned. */
+typedef struct ckv_kv_rows {
+  const void* x; /* device */
+  int64_t stride_t, stride_h;
+  int32_t heads;
+  ckv_dtype dtype; /* CKV_F32 or CKV_BF16, the same in all sets of a call */
+} ckv_kv_rows;
+
+/*
+ * Appends the keys and values of T tokens to the cache, the keys rotated by their
+ * positions on the way, and rotates queries in the same pass.  Token t's rows go to
+ * cache location loc[t] = page * page_size + row.  The rotation is that of
+ * ckv_qk_norm_rope (cos_sin, rope_dim, rope_offset, interleaved; no norm); fp32
+ * arithmetic, one rounding to bf16.  Values are only rounded.
+ * k          host struct; k->heads == cache->heads.
+ * v          host struct, v->heads == cache->heads, or NULL: only keys are stored (a cache
+ *            whose rows are key and value, or one without values; cache->v is not used).
+ *            With v, cache->v differs from cache->k.
+ * q          host struct or NULL; q_out device bf16, row (t, h) at t*q_out_stride_t +
+ *            h*q_out_stride_h, 16-byte aligned; may be q->x itself when that is bf16 with
+ *            the same strides, any other overlap is a race.
+ * loc        device int64 [T]; < 0: the token's keys and values are not stored; >= num_pages *
+ *            page_size: neither, and CKV_DEVERR_CACHE_LOC is set.  Locations of a call are distinct.
+ * positions  device int32 [T]; < 0: nothing of the token is read or written.  NULL only with
+ *            rope_dim == 0: every token counts.  A position >= num_positions (with
+ *            rope_dim > 0) sets CKV_DEVERR_SEQ_LEN, and the token is skipped.
+ * cos_sin    device fp32 [num_positions][rope_dim] (NULL with rope_dim == 0).
+ * T * (all heads) <= 2^30.
+ */
+ckv_status ckv_kv_append(const ckv_kv_rows* k, const ckv_kv_rows* v, const ckv_kv_rows* q, uint16_t* q_out,
+                         int64_t q_out_stride_t, int64_t q_out_stride_h, int64_t T, const ckv_kv_cache* cache,
+                         const int64_t* loc, const int32_t* positions, const float* cos_sin, int64_t num_positions,
+                         int32_t rope_dim, int32_t rope_offset, int32_t interleaved, int32_t use_pdl, int32_t* err_word,
+                         void* stream);
+
+/*
+ * Which drafted tokens see which.  The drafts of request b are the ragged rows row_start[b] ..
+ * row_start[b+1] - 1; draft i of a request has parent parents[t] (t = row_start[b] + i), an
+ * index of the same request below i, or -1: it follows the request's last committed token.
+ *   tree_mask  device uint64 [T][words]: bit a (bit a % 64 of word a / 64) is set for the draft
+ *              itself and for each of its ancestors a.
+ *   positions  device int32 [T], nullable: ctx_rows[t] + the number of its ancestors, the
+ *              position of its rotation.
+ * ctx_rows   device int32 [T], nullable (= 0): committed tokens before the draft; < 0: padding.
+ * words      1..16; a request has 64 * words drafts at most.
+ * Rows with ctx_rows < 0 and rows from row_start[B] to T - 1 get an empty mask and position -1.
+ * A parent that is not -1 and not below its draft sets CKV_DEVERR_PLAN and counts as -1; drafts from
+ * 64 * words on set it too and get an empty mask and position -1.
+ */
+ckv_status ckv_build_tree_masks(const int32_t* parents, const int32_t* row_start, int32_t B, const int32_t* ctx_rows,
+                                int64_t T, int32_t words, uint64_t* tree_mask, int32_t* positions, int32_t use_pdl,
+                                int32_t* err_word, void* stream);
+
+/*
+ * Attention over the uncompressed cache.  H query heads share the KH key heads in groups of
+ * H / KH neighbours.  Token t of request b (ragged rows row_start[b] .. row_start[b+1] - 1) sees of
+ * its request's cache rows, row j being row j % page_size of page block_table[b][j / page_size],
+ *   without tree_mask:  the rows j < c, c = ctx_rows[t], that are in its window (j >= c - window)
+ *                       or among the first (j < first_rows);
+ *   with tree_mask:     the committed rows j < c that are in its window (j >= c + n - window, n the
+ *                       bits set in its mask: itself and its ancestors) or among the first, and
+ *                       draft row c + a for every bit a of its mask, whatever the window.
+ * window == 0: no limit.  Then
+ *     z_j = softmax_scale * <q[t][h], k_j>,   lse[t][h] = log(sum_j e^z_j [+ e^sink[h]]),
+ *     out[t][h] = sum_j e^(z_j - lse) v_j.
+ * A token that sees nothing gets zeros and lse = sink[h], or -infinity without sink.  Rows with
+ * ctx_rows[t] < 0, and rows from row_start[B] on, are left as they were.  Pages that no token of
+ * the call sees need not be there: their table entries are not used.
+ * q          device bf16, row (t, h) at t*q_stride_t + h*q_stride_h elements, 16-byte aligned.
+ * cache      host struct.  A cache row that some token of the request sees has finite values: what
+ *            is not finite in it may reach other tokens of that request.  Rows that none
+ *            sees may hold anything.
+ * block_table  device int32, request b's row at b * table_stride (>= max_pages, or 0: one row that
+ *            all requests share).  A page id outside [0, num_pages) where a token's row should be
+ *            sets CKV_DEVERR_CACHE_LOC; its rows count as unseen.
+ * row_start  device int32 [B + 1], non-decreasing from 0 on.   ctx_rows device int32 [T].
+ * max_rows   host bound of the rows of a request, drafts included (1 <= max_rows <= max_pages *
+ *            page_size and CKV_KV_ATTENTION_MAX_ROWS): larger ctx_rows set CKV_DEVERR_SEQ_LEN and are
+ *            clamped, drafts beyond set it too and are unseen.  It chooses how far the rows are
+ *            split over CTAs, so a tight bound is faster.
+ * window, first_rows  >= 0; first_rows means nothing without a window.
+ * tree_mask  device uint64 [T][mask_words], nullable (mask_words == 0); mask_words 1..16.
+ * sink       device fp32 [H], nullable.
+ * out        device bf16 [T][H][D] contiguous, apart from q (the spans of memory from first to
+ *            last element may not overlap).    lse  device fp32 [T][H], nullable.
+ * H          1..1024, a multiple of KH.   B <= 65536.   T * H < 2^31.
+ * workspace  device, 16-byte aligned, ckv_kv_attention_workspace() bytes (may be NULL when that
+ *            is 0); its contents need no initial value and do not outlive the call.  Calls that
+ *            overlap on the GPU need one each.  The bytes follow how the rows are split and do not
+ *            grow with every size: a workspace for several sizes is as large as the largest
+ *            answer for them.  For sizes that the call refuses the answer is 0.
+ */
+#define CKV_KV_ATTENTION_MAX_ROWS 20971520
+int64_t ckv_kv_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows,
+                                   int32_t window, int32_t first_rows, int32_t mask_words);
+ckv_status ckv_kv_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T, int32_t H,
+                            const ckv_kv_cache* cache, const int32_t* block_table, int64_t table_stride,
+                            int32_t max_pages, const int32_t* row_start, int32_t B, const int32_t* ctx_rows,
+                            int64_t max_rows, int32_t window, int32_t first_rows, const uint64_t* tree_mask,
+                            int32_t mask_words, float softmax_scale, const float* sink, uint16_t* out, float* lse,
+                            void* workspace, int64_t workspace_bytes, int32_t use_pdl, int32_t* err_word, void* stream);
+
+/* One part of ckv_merge_attention. */
+typedef struct ckv_attention_part {
+  const void* out;  /* device [T][H][D], 16-byte aligned */
+  const float* lse; /* device [T][H] */
+} ckv_attention_part;
+
+/*
+ * The attention over several sets of rows together, from the attentions over each of them:
+ *     lse = log(sum_i e^lse_i),   out = sum_i e^(lse_i - lse) out_i
+ * for every token and head (a sink belongs in one of the parts only).  A part with lse_i =
+ * -infinity counts for nothing, whatever its out_i holds; where every part has it, out is zero and
+ * lse -infinity.  fp32 arithmetic, one rounding.
+ * parts      host array of num_parts (1..8).    dtype  of all out_i: CKV_F32 or CKV_BF16.
+ * positions  device int32 [T], nullable; < 0: the token's rows are left as they were.
+ * out        device [T][H][D] of out_dtype, 16-byte aligned; may be one of the out_i when the
+ *            types are equal, any other overlap is a race.
+ * lse        device fp32 [T][H], nullable; may be one of the lse_i.
+ * D          128, 256 or 512.   T * H < 2^31.
+ */
+ckv_status ckv_merge_attention(const ckv_attention_part* parts, int32_t num_parts, ckv_dtype dtype, int64_t T, int32_t H,
+                               int32_t D, const int32_t* positions, void* out, ckv_dtype out_dtype, float* lse,
+                               int32_t use_pdl, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,425 @@
+"""The operators around the uncompressed cache on the GPU against 64-bit references:
+appending with rotation, tree masks, attention (window, first rows, drafts), merging,
+and a step that runs them together with the compressed rows.
+
+Tolerances, from the operators' arithmetic:
+  * masks, positions, values stored as they are: exact
+  * rotation: two fp32 products and a sum (2^-22 of |a| + |b|), then one rounding to
+    bf16, 2^-8 of the value
+  * attention: scores are fp32 sums of D products: e = D 2^-24 sum |q k| scale, which moves
+    a weight by e of its value; exp2 and the sums another 2^-18; weights are rounded to bf16,
+    2^-8 of each: (2 e + 2^-17 + 2^-8) sum w |v|, then one rounding, 2^-8 of the value;
+    lse: e + 2^-18 + 2^-22 of its value
+  * merging: fp32 weights (2^-18 of each), then one rounding (bf16 2^-8, fp32 2^-24)
+"""
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ck():
+    import compressed_kv_attention_gated_gb300 as ck
+
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ck.load()
+    return ck
+
+
+def _err():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def _i32(a):
+    return torch.as_tensor(np.asarray(a), dtype=torch.int32).cuda()
+
+
+def _angles(n, R):
+    a = torch.arange(n, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, R, 2, dtype=torch.float64) / max(R, 1))
+    return torch.cat([a.cos(), a.sin()], 1).float().cuda()
+
+
+def _cache(pages, ps, KH, D, layout, fill=0.0):
+    """A cache [pages, ps, KH, D]: rows outermost, heads outermost, or keys and values interleaved in one tensor."""
+    if layout == "heads":
+        return torch.full((pages, KH, ps, D), fill, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    if layout == "halves":
+        return torch.full((pages, 2, ps, KH, D), fill, dtype=torch.bfloat16, device="cuda")[:, 1]
+    return torch.full((pages, ps, KH, D), fill, dtype=torch.bfloat16, device="cuda")
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("D,H,KH,T,R,at,pairs", [
+    (128, 16, 2, 4, 128, 0, False), (128, 5, 1, 37, 64, 64, False), (256, 8, 8, 3, 64, 192, True), (512, 64, 1, 9, 64, 448, True),
+    (128, 4, 2, 11, 44, 24, False), (256, 3, 3, 5, 30, 98, False), (512, 7, 7, 6, 512, 0, False), (512, 2, 1, 5, 6, 2, True),
+    (128, 24, 8, 700, 128, 0, False), (256, 1, 1, 1, 0, 0, False), (512, 130, 2, 3, 10, 500, False)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["rows", "heads", "halves"])
+def test_append(ck, D, H, KH, T, R, at, pairs, dtype, layout):
+    g = torch.Generator(device="cuda").manual_seed(D + T + R)
+    ps, pages = (7, -(-T // 7) + 2)
+    both = torch.randn(T, H + 2 * KH, D, generator=g, device="cuda").to(dtype)
+    q, k, v = both[:, :H], both[:, H:H + KH], both[:, H + KH:]
+    loc = torch.randperm(pages * ps, generator=g, device="cuda")[:T]
+    pos = torch.randint(0, 50, (T,), generator=g, device="cuda", dtype=torch.int32)
+    if T > 2:
+        loc[1], pos[2] = -1, -1  # not stored; skipped
+    kc, vc = _cache(pages, ps, KH, D, layout, 7.0), _cache(pages, ps, KH, D, layout, 7.0)
+    table = _angles(50, R) if R else None
+    err = _err()
+    q_out = torch.full((T, H, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    got = ck.ckv_kv_append(k, v, kc, vc, loc, positions=pos, cos_sin=table, rope_offset=at, interleaved=pairs, q=q, q_out=q_out, err_word=err)
+    assert got is q_out and int(err) == 0
+    tab = table if R else torch.zeros(50, 0, device="cuda")
+    turned = torch.zeros(D, dtype=torch.bool, device="cuda")
+    turned[at:at + R] = True
+
+    def check(a, x):
+        want = ref.rotate(x, pos, tab, at, pairs)
+        size = x.double().abs()
+        big = torch.where(turned, size[..., at:at + R].amax(-1, keepdim=True) * 2 if R else size, size)
+        assert torch.all((a.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -22 * big * turned)
+
+    live = pos >= 0
+    check(torch.where(live[:, None, None], q_out, q.bfloat16()), q)
+    if T > 2:
+        assert torch.all(q_out[2] == 3.0)
+    kw, vw = torch.full((pages, ps, KH, D), 7.0, device="cuda").bfloat16(), torch.full((pages, ps, KH, D), 7.0, device="cuda").bfloat16()
+    on = live & (loc >= 0)
+    check(torch.where(on[:, None, None], kc[loc.clamp(min=0) // ps, loc.clamp(min=0) % ps], ref.rotate(k, pos, tab, at, pairs).bfloat16()), k)
+    kw[loc[on] // ps, loc[on] % ps] = kc[loc[on] // ps, loc[on] % ps]
+    vw[loc[on] // ps, loc[on] % ps] = v[on].bfloat16()
+    assert torch.equal(kc, kw) and torch.equal(vc, vw)
+
+
+def test_append_keys_alone_and_queries_in_place(ck):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for R, at, pairs in ((64, 64, False), (44, 24, False), (20, 6, True)):
+        T, H, KH, D, ps = 33, 6, 2, 128, 16
+        q = torch.randn(T, H, D, generator=g, device="cuda").bfloat16()
+        k = torch.randn(T, KH, D, generator=g, device="cuda").bfloat16()
+        pos = torch.randint(0, 50, (T,), generator=g, device="cuda", dtype=torch.int32)
+        loc = torch.randperm(5 * ps, generator=g, device="cuda")[:T]
+        a, b = _cache(5, ps, KH, D, "rows"), _cache(5, ps, KH, D, "rows")
+        table = _angles(50, R)
+        apart = ck.ckv_kv_append(k, None, a, None, loc, positions=pos, cos_sin=table, rope_offset=at, interleaved=pairs, q=q)
+        same = ck.ckv_kv_append(k, None, b, None, loc, positions=pos, cos_sin=table, rope_offset=at, interleaved=pairs, q=q, q_out=q)
+        assert same is q and torch.equal(apart, q) and torch.equal(a, b)
+    # no rotation, no positions: the rows as they are
+    assert ck.ckv_kv_append(k, None, a, None, loc) is None
+    assert torch.equal(a[loc // ps, loc % ps], k)
+
+
+def test_append_flags_locations_and_positions(ck):
+    k = torch.ones(3, 1, 128, device="cuda").bfloat16()
+    c, err = _cache(2, 4, 1, 128, "rows"), _err()
+    ck.ckv_kv_append(k, None, c, None, torch.tensor([8, 3, 1 << 40], device="cuda"), err_word=err)
+    assert int(err) == 4 and int((c != 0).any(-1).sum()) == 1 and torch.all(c[0, 3] == 1)
+    err.zero_()
+    ck.ckv_kv_append(k, None, c, None, torch.tensor([0, 1, 2], device="cuda"), positions=_i32([9, 10, 11]), cos_sin=_angles(10, 64), err_word=err)
+    assert int(err) == 16 and torch.all(c[0, 1] == 0) and torch.all(c[0, 2] == 0) and torch.any(c[0, 0] != 0)
+
+
+# ------------------------------------------------------------------ tree masks
+@pytest.mark.parametrize("B,n_lo,n_hi,words", [(1, 1, 1, 1), (8, 16, 16, 1), (5, 0, 64, 1), (3, 60, 130, 3), (2, 1000, 1024, 16), (300, 0, 9, 2),
+                                               (1, 64, 64, 1), (1, 65, 65, 2)])
+@pytest.mark.parametrize("kind", ["random", "chain", "star"])
+def test_tree_masks(ck, B, n_lo, n_hi, words, kind):
+    rng = np.random.default_rng(B + n_hi)
+    n = rng.integers(n_lo, n_hi + 1, B)
+    start = np.concatenate([[0], np.cumsum(n)])
+    T = int(start[-1]) + 5
+    parents = np.full(T, 77)
+    for b in range(B):
+        i = np.arange(n[b])
+        parents[start[b]:start[b + 1]] = i - 1 if kind == "chain" else -1 if kind == "star" else [rng.integers(-1, x) if x else -1 for x in i]
+    ctx = rng.integers(0, 1000, T)
+    ctx[start[-1] // 2] = -1
+    masks, pos = ref.tree(parents.tolist(), start.tolist(), ctx.tolist(), words)
+    err = _err()
+    m, p = ck.ckv_build_tree_masks(_i32(parents), _i32(start), _i32(ctx), words, err_word=err)
+    assert int(err) == 0
+    assert torch.equal(m.cpu(), ref.pack(masks, words)) and p.tolist() == pos
+
+
+def test_tree_masks_bad_parents_and_too_many_drafts(ck):
+    parents, start = [0, 0, 5, -2, 2, -1], [0, 6]
+    err = _err()
+    m, p = ck.ckv_build_tree_masks(_i32(parents), _i32(start), None, 1, err_word=err)
+    masks, pos = ref.tree(parents, start, None, 1)
+    assert int(err) == 8 and torch.equal(m.cpu(), ref.pack(masks, 1)) and p.tolist() == pos
+    err.zero_()
+    parents = list(range(-1, 69))
+    m, p = ck.ckv_build_tree_masks(_i32(parents), _i32([0, 70]), None, 1, err_word=err)
+    masks, pos = ref.tree(parents, [0, 70], None, 1)
+    assert int(err) == 8 and torch.equal(m.cpu(), ref.pack(masks, 1)) and p.tolist() == pos and pos[64:] == [-1] * 6
+
+
+# ------------------------------------------------------------------ attention
+class Step:
+    """Requests with contexts in a paged cache, and tokens of a step.  Rows that no token sees are NaN,
+    pages that none sees are not there."""
+
+    def __init__(self, D, H, KH, n, before, ps=16, window=0, first=0, tree=False, layout="rows", shared=False, sink=False, words=0, seed=0,
+                 spread=1.5, width_more=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        B = len(n)
+        self.start = np.concatenate([[0], np.cumsum(n)]).astype(int)
+        T = int(self.start[-1])
+        b = np.repeat(np.arange(B), n)
+        i = np.arange(T) - self.start[b]
+        before = np.asarray(before)
+        self.mask = None
+        if tree:
+            parents = np.array([rng.integers(-1, x) if x else -1 for x in i], dtype=int)
+            words = words or max(1, -(-max(n) // 64))
+            masks, _ = ref.tree(parents.tolist(), self.start.tolist(), None, words)
+            self.mask = ref.pack(masks, words).cuda()
+            self.ctx = before[b]
+        else:
+            self.ctx = before[b] + i + 1
+        total = before + np.asarray(n)
+        self.max_rows = max(1, int(total.max()))
+        width = -(-self.max_rows // ps) + width_more
+        seen = [set() for _ in range(B)]
+        for t in range(T):
+            seen[b[t]] |= set(ref.seen_rows(int(self.ctx[t]), window, first, None if self.mask is None else sorted(masks[t])))
+        held = np.array([[any(r // ps == x for r in seen[y]) for x in range(width)] for y in range(B)]).reshape(B, width)
+        pages = int(held.sum()) + 3
+        order = iter(rng.permutation(pages).tolist())
+        self.table = torch.tensor([[next(order) if held[y, x] else -1 for x in range(width)] for y in range(B)], dtype=torch.int32,
+                                  device="cuda").view(B, width)
+        self.k = _cache(pages, ps, KH, D, layout, float("nan"))
+        self.v = self.k if shared else _cache(pages, ps, KH, D, layout, float("nan"))
+        for y in range(B):
+            rows = torch.tensor(sorted(seen[y]), dtype=torch.int64, device="cuda")
+            if rows.numel():
+                pg = self.table[y].long()[rows // ps]
+                for c in ((self.k,) if shared else (self.k, self.v)):
+                    c[pg, rows % ps] = torch.randn(rows.numel(), KH, D, generator=g, device="cuda").bfloat16()
+        self.q = (torch.randn(T, H, D, generator=g, device="cuda") * spread).bfloat16()
+        self.sink = torch.randn(H, generator=g, device="cuda") if sink else None
+        self.window, self.first, self.scale = window, first, D ** -0.5
+
+    def run(self, ck, max_rows=None, **more):
+        err = _err()
+        out, lse = ck.ckv_kv_attention(self.q, self.k, self.v, self.table, _i32(self.start), _i32(self.ctx), max_rows or self.max_rows,
+                                       self.scale, window=self.window, first_rows=self.first, tree_mask=self.mask, sink=self.sink,
+                                       err_word=err, **more)
+        return out, lse, err
+
+    def check(self, out, lse):
+        want, wl, seen, spread, slack = ref.attention(self.q, self.k, self.v, self.table, self.start, self.ctx, self.scale, self.window,
+                                                      self.first, self.mask, self.sink)
+        close(out[seen], lse[seen], want[seen], wl[seen], spread[seen], slack[seen], self.q.shape[2])
+
+
+def close(out, lse, want, wl, spread, slack, D):
+    e = slack * D * 2.0 ** -24
+    tol = 2.0 ** -8 * want.abs() + (2 * e[..., None] + 2.0 ** -17 + 2.0 ** -8) * spread
+    bad = ~((out.double() - want).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[0].tolist(), float(out[bad][0]), float(want[bad][0]))
+    none = torch.isneginf(wl)
+    assert torch.equal(torch.isneginf(lse), none)
+    d = (lse.double() - wl).abs()[~none]
+    assert torch.all(d <= (e + 2.0 ** -18 + 2.0 ** -22 * wl.abs())[~none]), float(d.max())
+
+
+SIZES = [
+    # D, H, KH, tokens of the requests, rows before them, page size
+    (128, 16, 2, [1, 1, 1, 1], [0, 7, 130, 299], 16),
+    (128, 5, 1, [3, 0, 1, 40], [0, 5, 127, 90], 7),
+    (128, 32, 8, [200, 1, 77], [50, 600, 0], 64),
+    (128, 64, 1, [1, 2], [511, 128], 48),
+    (256, 8, 8, [4, 1, 150], [300, 0, 33], 16),
+    (256, 24, 3, [1, 9], [255, 256], 100),
+    (512, 64, 1, [1, 1, 3], [700, 0, 129], 64),
+    (512, 7, 7, [2, 30], [140, 1], 5),
+    (512, 130, 1, [5], [260], 32)]
+
+
+@pytest.mark.parametrize("D,H,KH,n,before,ps", SIZES)
+@pytest.mark.parametrize("window,first", [(0, 0), (1, 0), (100, 0), (128, 4), (37, 150), (5000, 3)])
+def test_window(ck, D, H, KH, n, before, ps, window, first):
+    s = Step(D, H, KH, n, before, ps, window, first, layout=("rows", "heads", "halves")[(window + D) % 3], shared=D == 512 and window != 1,
+             sink=first > 0, seed=D + window)
+    out, lse, err = s.run(ck)
+    assert int(err) == 0
+    s.check(out, lse)
+
+
+@pytest.mark.parametrize("D,H,KH,n,before,ps", SIZES)
+@pytest.mark.parametrize("window,first", [(0, 0), (64, 3), (300, 0)])
+def test_tree(ck, D, H, KH, n, before, ps, window, first):
+    s = Step(D, H, KH, n, before, ps, window, first, tree=True, layout=("rows", "heads")[D % 3 % 2], sink=window == 64, seed=D + window,
+             words=5 if D == 256 else 0)
+    out, lse, err = s.run(ck)
+    assert int(err) == 0
+    s.check(out, lse)
+
+
+@pytest.mark.parametrize("D,H,KH,before,window", [(128, 8, 1, 9000, 0), (512, 16, 1, 5000, 0), (256, 4, 2, 20000, 7000), (128, 128, 1, 3000, 0)])
+def test_long_rows_of_few_tokens(ck, D, H, KH, before, window):
+    s = Step(D, H, KH, [1, 2], [before, before // 3], 64, window, 20, sink=True, seed=before)
+    out, lse, err = s.run(ck)
+    assert int(err) == 0
+    s.check(out, lse)
+
+
+def test_rows_left_alone(ck):
+    s = Step(128, 8, 2, [3, 2, 2], [20, 140, 3], seed=3)
+    T = s.q.shape[0]
+    s.ctx[[1, 4]] = -1
+    s.start = s.start.copy()
+    s.start[-1] = T - 1  # the last token belongs to nobody
+    out, lse = torch.full((T, 8, 128), 5.0, device="cuda").bfloat16(), torch.full((T, 8), 5.0, device="cuda")
+    got, gl, err = s.run(ck, out=out, lse=lse)
+    assert got is out and gl is lse and int(err) == 0
+    s.check(out, lse)
+    for t in (1, 4, T - 1):
+        assert torch.all(out[t] == 5) and torch.all(lse[t] == 5)
+
+
+def test_tokens_that_see_nothing(ck):
+    for sink in (False, True):
+        s = Step(128, 8, 2, [3, 2], [20, 140], seed=4, sink=sink)
+        s.ctx[0] = 0
+        s.ctx[3:] = 0
+        out, lse, err = s.run(ck)
+        s.check(out, lse)
+        assert int(err) == 0 and torch.all(out[0] == 0) and torch.all(out[3:] == 0)
+        assert torch.equal(lse[0], s.sink) if sink else torch.all(torch.isneginf(lse[3:]))
+
+
+def test_missing_pages_and_long_contexts_are_flagged(ck):
+    for bad in (-1, 10 ** 6):
+        s = Step(128, 8, 2, [3, 2], [90, 140], seed=5)
+        s.table[0, 2] = bad
+        out, lse, err = s.run(ck)
+        assert int(err) == 4
+        s.check(out, lse)
+    s = Step(128, 8, 2, [3], [90], seed=6, width_more=2)
+    s.ctx[1] = 10 ** 9
+    s.k[torch.isnan(s.k)] = 0
+    s.v[torch.isnan(s.v)] = 0
+    out, lse, err = s.run(ck)
+    assert int(err) == 16
+    s.ctx[1] = s.max_rows
+    s.check(out, lse)
+
+
+def test_drafts_behind_max_rows_are_flagged(ck):
+    s = Step(128, 4, 4, [10], [50], tree=True, seed=7)
+    out, lse, err = s.run(ck, max_rows=55)
+    assert int(err) == 16
+    want = ref.attention(s.q, s.k, s.v, s.table, s.start, s.ctx, s.scale, mask=s.mask, max_rows=55)
+    close(out, lse, want[0], want[1], want[3], want[4], 128)
+
+
+def test_large_scores_and_constant_values(ck):
+    """Rows whose weights are far apart, ascending and descending, and values that are all the same: the
+    output is that value to its rounding."""
+    for order in (1, -1):
+        s = Step(128, 16, 2, [1, 30], [500, 400], seed=8, spread=30.0)
+        out, lse, err = s.run(ck)
+        s.check(out, lse)
+        ramp = torch.arange(s.max_rows, device="cuda") * order + (s.max_rows if order < 0 else 0)
+        for b in range(2):
+            rows = torch.arange(min(int(s.start[b + 1] - s.start[b]) + (500, 400)[b], s.max_rows), device="cuda")
+            pg = s.table[b].long()[rows // 16]
+            s.k[pg, rows % 16] = (ramp[rows].float() / 8).bfloat16()[:, None, None]
+            s.v[pg, rows % 16] = 1.75
+        s.q = torch.ones_like(s.q)
+        out, lse, err = s.run(ck)
+        s.check(out, lse)
+        assert torch.all((out.double() - 1.75).abs() <= 1.75 * (2.0 ** -8 + 2.0 ** -8))
+
+
+def test_one_table_row_for_all_and_permuted_queries(ck):
+    s = Step(128, 8, 2, [1, 1, 1], [80, 80, 80], seed=9)
+    s.table = s.table[:1].expand(3, -1)
+    s.q = s.q.transpose(0, 1).contiguous().transpose(0, 1)
+    out, lse, err = s.run(ck)
+    assert int(err) == 0
+    s.check(out, lse)
+
+
+# ------------------------------------------------------------------ merge
+@pytest.mark.parametrize("D", [128, 256, 512])
+@pytest.mark.parametrize("parts", [1, 2, 3, 8])
+@pytest.mark.parametrize("dtype,out_dtype", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32), (torch.float32, torch.bfloat16),
+                                             (torch.bfloat16, torch.float32)])
+def test_merge(ck, D, parts, dtype, out_dtype):
+    g = torch.Generator(device="cuda").manual_seed(D + parts)
+    T, H = 13, 5
+    outs = [torch.randn(T, H, D, generator=g, device="cuda").to(dtype) for _ in range(parts)]
+    lses = [4 * torch.randn(T, H, generator=g, device="cuda") for _ in range(parts)]
+    for i in range(parts):  # what a part without rows holds does not count
+        lses[i][i % T] = -torch.inf
+        outs[i][i % T] = float("nan")
+        lses[i][T - 1] = -torch.inf
+    lses[0][5] = 100.0
+    lses[parts - 1][6] = -300.0
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    pos[4] = -1
+    out, lse = torch.full((T, H, D), 9.0, device="cuda").to(out_dtype), torch.full((T, H), 9.0, device="cuda")
+    got, gl = ck.ckv_merge_attention(outs, lses, out=out, lse=lse, positions=pos)
+    assert got is out and gl is lse
+    want, wl, spread = ref.merge(outs, lses)
+    on = pos >= 0
+    tol = (2.0 ** -8 if out_dtype == torch.bfloat16 else 2.0 ** -24) * want.abs() + 2.0 ** -18 * spread
+    assert torch.all(((out.double() - want).abs() <= tol)[on])
+    none = torch.isneginf(wl)
+    assert torch.equal(torch.isneginf(lse)[on], none[on])
+    assert torch.all(((lse.double() - wl).abs() <= 2.0 ** -18 + 2.0 ** -22 * wl.abs())[on & ~none.any(1)])
+    assert torch.all(out[4] == 9) and torch.all(lse[4] == 9)
+    # over one of the parts
+    if dtype == out_dtype:
+        fresh = ck.ckv_merge_attention(outs, lses, out=torch.empty_like(out))
+        same, _ = ck.ckv_merge_attention(outs, lses, out=outs[-1], lse=lses[-1])
+        assert torch.equal(fresh[0], same) and torch.equal(fresh[1], lses[-1])
+
+
+# ------------------------------------------------------------------ together
+def test_a_step_over_the_window_and_the_compressed_rows(ck):
+    """Maps, rotation and append, attention over the last rows and over the compressed ones, and their merge."""
+    B, H, D, P, ps = 3, 8, 128, 4, 8
+    g = torch.Generator(device="cuda").manual_seed(0)
+    seq, one = _i32([160, 3, 24]), _i32([1, 1, 1])
+    err = _err()
+    raw_table, raw_free, raw_cur = torch.full((B, 20), -1, dtype=torch.int32, device="cuda"), torch.randperm(60, device="cuda").int(), _i32([0, 0])
+    table, free, cur = torch.full((B, 5), -1, dtype=torch.int32, device="cuda"), torch.randperm(15, device="cuda").int(), _i32([0, 0])
+    cache = torch.zeros(15, ps, D // 2 + D // 16, dtype=torch.uint8, device="cuda")
+    kc = _cache(60, ps, 1, D, "rows", float("nan"))
+    cs = _angles(200, 64)
+    # prefix, then one token each
+    for s, n in ((seq - 1, seq - 1), (seq, one)):
+        T = int(n.sum())
+        m = ck.ckv_build_step_maps(s, n, raw_table, raw_free, raw_cur, 1, ps, T, err_word=err)
+        c = ck.ckv_build_step_maps(s, n, table, free, cur, P, ps, T, err_word=err)
+        k, q = torch.randn(T, 1, D, generator=g, device="cuda"), torch.randn(T, H, D, generator=g, device="cuda")
+        q = ck.ckv_kv_append(k, None, kc, None, m["cache_loc"], positions=m["positions"], cos_sin=cs, q=q, err_word=err)
+        ck.ckv_fp4_store(torch.randn(T, D, generator=g, device="cuda"), cache, c["cache_loc"], cache_scale=2.0 ** -6, err_word=err)
+    near = ck.ckv_kv_attention(q, kc, kc, raw_table, m["row_start"], m["ctx_rows"], 160, D ** -0.5, window=P, err_word=err)
+    far = ck.ckv_fp4_attention(q, cache, table, c["row_start"], c["ctx_rows"], 40, D ** -0.5, cache_scale=2.0 ** -6, err_word=err)
+    out, lse = ck.ckv_merge_attention([near[0], far[0]], [near[1], far[1]], positions=m["positions"])
+    assert int(err) == 0
+    wn = ref.attention(q, kc, kc, raw_table, [0, 1, 2, 3], [160, 3, 24], D ** -0.5, window=P)
+    for b, rows in enumerate((40, 0, 6)):
+        j = torch.arange(rows, device="cuda")
+        far64 = torch.empty(rows, D, device="cuda")
+        if rows:
+            ck.ckv_fp4_load(cache, table[b].long()[j // ps] * ps + j % ps, far64, cache_scale=2.0 ** -6)
+        z = q[b].double() @ far64.double().T * D ** -0.5
+        total = torch.logsumexp(torch.cat([z, wn[1][b][:, None]], 1), 1)
+        want = torch.exp(z - total[:, None]) @ far64.double() + torch.exp(wn[1][b] - total)[:, None] * wn[0][b]
+        size = torch.exp(z - total[:, None]) @ far64.double().abs() + torch.exp(wn[1][b] - total)[:, None] * wn[3][b]
+        # both parts' weights and outputs are rounded to bf16, then the result
+        assert torch.all((out[b].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -7 + 2.0 ** -10) * size)
+        assert torch.all((lse[b].double() - total).abs() <= 2.0 ** -12 * (1 + total.abs()))
