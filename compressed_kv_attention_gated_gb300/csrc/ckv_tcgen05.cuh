@@ -7,9 +7,8 @@
 
 namespace ckv {
 
-// mbar_wait whose first look does not suspend: an already completed phase costs a
-// fraction of the potentially blocking test.
-__device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity) {
+// Whether the phase is completed, without suspending.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n"
@@ -18,7 +17,12 @@ __device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity) {
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
-  return ok != 0 || mbar_wait(bar, parity);
+  return ok != 0;
+}
+// mbar_wait whose first look does not suspend: an already completed phase costs a
+// fraction of the potentially blocking test.
+__device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity) {
+  return mbar_test(bar, parity) || mbar_wait(bar, parity);
 }
 
 // One thread of a converged warp.

@@ -1,120 +1,875 @@
 // kv_attention.cu -- attention over the uncompressed paged cache (no counterpart in the
-// sources).
+// sources):
+//   z_j = scale <q, k_j>,  lse = log(sum_j e^z_j [+ e^sink]),  out = sum_j e^(z_j - lse) v_j
+// over the rows j that a token sees: those of its window, the first ones, its drafts.
+//
+// The (token, head) rows that share a key head are cut into tiles of 128, the M side of
+// both products, which run on the tensor cores:
+//   S [128 rows x 128 keys] = Q [128 x D] K^T        O [128 rows x D] += P [128 x 128 keys] V
+// A tile's keys are the rows that any of its tokens sees: the first ones, then those from the
+// lowest window to the last row, cut into 128s as one list, so that a window of 128 is one
+// tile of keys wherever it begins.  What single tokens do not see of it is masked.
+//
+// Roles of a CTA (one per SM, taking jobs until none is left): 8 softmax warps, a
+// thread per row of S; one warp that issues the products; one that looks up the jobs (request, rows,
+// keys) ahead of the others; 4 that copy queries, keys and values (cp.async, 16 bytes at a
+// time: pages begin anywhere in a tile and rows have any stride) into a ring of units of 128
+// rows x 128 channels, across the jobs, so that memory is busy while a job ends.
+//
+// The two groups of four softmax warps have a buffer of S each.  With more than 128 rows (D =
+// 128) each has a tile of its own, and keys and values serve both: one's softmax runs under
+// the other's products.  Otherwise they take tiles of keys by turns, and share O and the
+// references of its rows.
+//
+// Softmax: weights are taken against a reference, the maximum of the tile that set it, which moves
+// only when a weight exceeds 2^16; then O is rescaled.  The weights are rounded to bf16, the type
+// of the values that they multiply (by 2^-9 of their value on average); sums are of unrounded
+// ones, in fp32, as are scores and outputs.
+//
+// At D = 512 two CTAs have a tile, each forming the scores and half of the channels of the output,
+// which would fill tensor memory.
+//
+// Few tiles with many keys are split into ranges of keys; their results (fp32, and lse) go through
+// the workspace and are joined by a second kernel in a fixed order.
+#include <algorithm>
+
+#include "ckv_tcgen05.cuh"
 #include "kv_attention.cuh"
 
 namespace ckv {
 namespace {
 
-constexpr int kWarps = 4, kHeads = 4;  // query heads that a warp works on together
+constexpr int kKvKeys = 128, kKvUnit = 32768;  // keys of a tile; bytes of a unit
+constexpr float kKvJump = 16.f;                // log2 of the largest weight over its reference
+constexpr int kMmaWarp = 8, kPlanWarp = 9, kCopyWarp = 12, kKvThreads = 512;
+// Registers per thread: 512 x 128 at launch; then 256 x 192 + 256 x 64, the same.
+constexpr int kSoftRegs = 192, kOtherRegs = 64;
 
-// One CTA per token and key head, its warps taking the rows by turns.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_attention_kernel(const __grid_constant__ KvAttentionArgs a) {
-  constexpr int kCh = D / 32;  // channels of a lane
-  __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
-  __shared__ __align__(16) float s_o[kWarps][kHeads][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t t = blockIdx.x, kh = blockIdx.y;
-  pdl_wait();
-  int32_t b = 0;
-  for (int32_t n = a.B; n > 1;) {
-    const int32_t step = (n + 31) / 32, i = lane * step;
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, i < n && kv_start_of(a, b + i) <= t);
-    const int32_t last = m ? 31 - __clz(m) : 0;
-    b += last * step;
-    n = min(step, n - last * step);
+struct KvLayout {
+  static constexpr int kHalves = D == 512 ? 2 : 1;
+  static constexpr int kDV = D / kHalves;               // channels of the output that a CTA has
+  static constexpr int kKU = D / 128, kVU = kDV / 128;  // units of a tile's keys and values
+  static constexpr int kTile = D == 128 ? 256 : 128;    // rows of a job
+  static constexpr int kQSlots = D == 128 ? 2 : 1;      // of 128 rows
+  static constexpr int kRing = D == 512 ? 3 : 4;
+  static constexpr int kQ = kRing * kKvUnit;
+  static constexpr int kSmall = kQ + kQSlots * kKU * kKvUnit;
+  static constexpr int kTmemO = 0, kTmemS = 256;        // O: 256 columns; S: two buffers of 128, P over the first half of each
+};
+
+struct Job {
+  KvTile tile;
+  int32_t kh, half, split;
+  int32_t first, low;  // the list of keys: rows 0 .. first - 1, then low, low + 1, ...
+  int32_t v0, v1;      // of the list
+  int32_t n;           // tiles of keys
+  int32_t two;         // each softmax group has a tile of rows of its own
+  int32_t live;        // 0: no more jobs
+};
+
+// Barriers.  `Uses` are numbered from 0 over the whole kernel, so that everyone counts alike.
+//   full, empty     of a unit of the ring: 4 copying warps; the products that read it
+//   q_full, q_empty of a slot of queries, alike
+//   s_full[w]       scores of group w are there (and all products issued before them are done)
+//   p_full[w]       weights of group w are there: 4 warps
+//   o_full[w]       every product of a job that group w waits for: once per job with keys
+//   noted           missing keys of a tile are noted: 4 copying warps
+// and where the groups share the rows:
+//   decided[w][q]   warp q of group w knows the references under which its tile is taken
+//   pv_done[w]      second product of a tile of group w
+//   met             both groups have got there: 8 warps, twice per job
+struct KvSmall {
+  uint64_t full[4], empty[4], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], job_full[2], job_empty[2], noted[4];
+  uint64_t decided[2][4], pv_done[2], met, drain;
+  uint32_t tmem;
+  Job job[2];
+  alignas(16) uint32_t bad[4][4];  // a bit per key of a tile whose page is not there (ring over tiles of keys)
+  float ref[128];                  // references of the shared rows
+  float sum[2][128], sum_ref[2][128];
+};
+
+template <int D>
+constexpr int kv_smem_bytes() {
+  return KvLayout<D>::kSmall + static_cast<int>(sizeof(KvSmall));
+}
+static_assert(kv_smem_bytes<128>() <= 227 * 1024 && kv_smem_bytes<256>() <= 227 * 1024 && kv_smem_bytes<512>() <= 227 * 1024, "shared memory");
+
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn_major) { return idesc_f16(n, false, b_mn_major) | (1u << 7) | (1u << 10); }
+
+// 32 columns of the warp's lanes; the values are there after tc_wait_ld() and settled32().
+__device__ __forceinline__ void tmem_ld32_async(uint32_t addr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr));
+}
+// Arithmetic on loaded values may not be moved over the wait: here they change as far as the compiler knows.
+__device__ __forceinline__ void settled32(float* v) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+               "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+  asm volatile("" : "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+               "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
+__device__ __forceinline__ void kv_tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Bits x0 .. x1 - 1 of a 32-bit word (any of them outside it).
+__device__ __forceinline__ uint32_t bits_between(int32_t x0, int32_t x1) {
+  const int lo = min(max(x0, 0), 32), hi = min(max(x1, 0), 32);
+  return static_cast<uint32_t>(((1ull << hi) - 1ull) & ~((1ull << lo) - 1ull));
+}
+
+// Wait for use `n` of a barrier, by a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t n) { return __all_sync(0xFFFFFFFFu, mbar_wait_near(bar, n & 1u)); }
+
+__device__ __forceinline__ void copies_wait_for(int left) {
+  switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
   }
-  if (t >= kv_start_of(a, b + 1) || t < kv_start_of(a, b)) return;
-  const Seen s = seen_by(a, t);
-  if (s.c < 0) return;
-  const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
-  for (int g0 = 0; g0 < a.G; g0 += kHeads) {
-    float q[kHeads][kCh], o[kHeads][kCh], m[kHeads], l[kHeads];
-#pragma unroll
-    for (int g = 0; g < kHeads; ++g) {
-      const uint16_t* from = a.q + t * a.q_st + (kh * a.G + min(g0 + g, a.G - 1)) * a.q_sh + lane * kCh;
-#pragma unroll
-      for (int x = 0; x < kCh; ++x) {
-        q[g][x] = __uint_as_float(static_cast<uint32_t>(from[x]) << 16);
-        o[g][x] = 0.f;
-      }
-      m[g] = kNegBig;
-      l[g] = 0.f;
+}
+
+struct KvPlan {
+  int tiles;   // bound of the number of tiles of rows
+  int splits;  // ranges of keys
+  int chunk;   // keys of a range (a multiple of kKvKeys); the last range takes all that are left
+};
+
+// ---------------------------------------------------------------------- jobs
+// Job `id`, by one converged warp; rows <= 0 when there is nothing to do in it.
+template <int D>
+__device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& p, int64_t id) {
+  using L = KvLayout<D>;
+  const int lane = threadIdx.x & 31;
+  Job j;
+  j.half = static_cast<int32_t>(id % L::kHalves);
+  id /= L::kHalves;
+  j.kh = static_cast<int32_t>(id % a.KH);
+  id /= a.KH;
+  j.split = static_cast<int32_t>(id % p.splits);
+  j.tile = kv_find_tile(a, static_cast<int32_t>(id / p.splits), L::kTile);
+  j.live = 1;
+  j.two = j.tile.rows > 128;
+  j.first = j.low = j.v0 = j.v1 = j.n = 0;
+  if (j.tile.rows <= 0) return j;
+  // what its tokens see together
+  const int32_t t0 = j.tile.tok0 + j.tile.base / a.G, t1 = j.tile.tok0 + (j.tile.base + j.tile.rows - 1) / a.G;
+  int32_t low = INT32_MAX, end = -1;
+  for (int32_t t = t0 + lane; t <= t1; t += 32) {
+    const Seen s = seen_by(a, t);
+    if (s.c < 0) continue;
+    end = max(end, s.end);
+    if (s.end > 0) low = min(low, s.low);  // a token that sees nothing does not widen the list
+  }
+  low = __reduce_min_sync(0xFFFFFFFFu, low);
+  end = __reduce_max_sync(0xFFFFFFFFu, end);
+  if (end < 0) j.tile.rows = 0;  // every token is left as it is
+  end = max(end, 0);
+  j.low = min(low, end);
+  j.first = min(a.first, j.low);
+  const int32_t count = end - j.low + j.first;
+  j.v0 = static_cast<int32_t>(min(static_cast<int64_t>(j.split) * p.chunk, static_cast<int64_t>(count)));
+  j.v1 = j.split == p.splits - 1 ? count : min(count, j.v0 + p.chunk);
+  j.n = (j.v1 - j.v0 + kKvKeys - 1) / kKvKeys;
+  return j;
+}
+
+// The part of the softmax warps: see the roles above.
+template <int D>
+__device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan& p, KvSmall& sm, uint32_t tmem) {
+  using L = KvLayout<D>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, w = warp >> 2, row = threadIdx.x & 127;
+  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128;
+  const float c = a.softmax_scale * kLog2e;
+  uint32_t s_use = 0, o_use = 0, met_use = 0, keys_before = 0;  // tiles of keys of earlier jobs
+  uint32_t other_tiles = 0;                                     // of the other group, in jobs whose rows they share
+#pragma unroll 1
+  for (uint32_t job_use = 0;; ++job_use) {
+    if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
+    const Job& job = sm.job[job_use & 1];
+    if (!job.live) return true;
+    const bool two = L::kQSlots == 2 && job.two;
+    const int32_t n = job.n, kh = job.kh, half = job.half, range = job.split;
+    const int32_t r = job.tile.base + (two ? w * 128 : 0) + row;
+    int32_t t = 0, flat = -1;
+    Seen see{-1, 0, 0, 0};
+    if (r < job.tile.base + job.tile.rows) {
+      const int32_t tok = r / a.G;
+      t = job.tile.tok0 + tok;
+      see = seen_by(a, t);
+      if (see.c >= 0) flat = t * a.H + kh * a.G + r - tok * a.G;
     }
-    for (int32_t i = warp; i < s.end - s.low + s.first; i += kWarps) {
-      const int32_t j = i < s.first ? i : s.low + i - s.first;
-      if (j >= s.c && !((a.mask[static_cast<int64_t>(t) * a.words + (j - s.c) / 64] >> ((j - s.c) & 63)) & 1)) continue;
-      const int32_t pg = a.page_shift >= 0 ? j >> a.page_shift : j / a.cache.page_size, row = j - pg * a.cache.page_size;
-      const int32_t page = table[pg];
-      if (page < 0 || page >= a.cache.num_pages) {
-        if (lane == 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
-        continue;
-      }
-      const uint16_t* k = a.cache.k + page * a.cache.k_stride_page + row * a.cache.k_stride_row + kh * a.cache.k_stride_head + lane * kCh;
-      const uint16_t* v = a.cache.v + page * a.cache.v_stride_page + row * a.cache.v_stride_row + kh * a.cache.v_stride_head + lane * kCh;
-      float kv[kCh], z[kHeads];
+    const bool any = __any_sync(0xFFFFFFFFu, flat >= 0);
+    const uint32_t at_o = tmem + lanes + L::kTmemO + (two ? w * 128 : 0);
+    float ref = flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
+    const int step = two ? 1 : 2;
+#pragma unroll 1
+    for (int j = two ? 0 : w; j < n; j += step) {
+      const uint32_t jt = keys_before + j;
+      if (!warp_wait(&sm.s_full[w], s_use++) || !warp_wait(&sm.noted[jt & 3], jt >> 2)) return false;
+      tc_fence_after();
+      if (any) {
+        float z[128];
 #pragma unroll
-      for (int x = 0; x < kCh; ++x) kv[x] = __uint_as_float(static_cast<uint32_t>(k[x]) << 16);
+        for (int i = 0; i < 4; ++i) tmem_ld32_async(at_s + i * 32, z + i * 32);
+        // which keys the row sees, a bit each
+        const int32_t v = job.v0 + j * kKvKeys, here = min(kKvKeys, job.v1 - v);
+        const int32_t head = job.first - v, k0 = job.low - head;  // places of first rows; the row of place 0, were it none of them
+        const bool whole = flat < 0 || (here == kKvKeys && k0 + kKvKeys <= see.c && (head <= 0 ? k0 : job.low) >= see.low);
+        const uint4 gone = *reinterpret_cast<const uint4*>(sm.bad[jt & 3]);
+        uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+        const bool masks = __any_sync(0xFFFFFFFFu, !whole) || (gone.x | gone.y | gone.z | gone.w);
+        if (masks) {
+          const uint32_t lost[4] = {gone.x, gone.y, gone.z, gone.w};
+          uint32_t missed = 0;
 #pragma unroll
-      for (int g = 0; g < kHeads; ++g) {
-        z[g] = 0.f;
-#pragma unroll
-        for (int x = 0; x < kCh; ++x) z[g] = fmaf(q[g][x], kv[x], z[g]);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-#pragma unroll
-        for (int g = 0; g < kHeads; ++g) z[g] += __shfl_xor_sync(0xFFFFFFFFu, z[g], d);
-      }
-#pragma unroll
-      for (int x = 0; x < kCh; ++x) kv[x] = __uint_as_float(static_cast<uint32_t>(v[x]) << 16);
-#pragma unroll
-      for (int g = 0; g < kHeads; ++g) {
-        const float y = z[g] * (a.softmax_scale * kLog2e), top = fmaxf(m[g], y);
-        const float keep = fast_exp2(m[g] - top), w = fast_exp2(y - top);
-        m[g] = top;
-        l[g] = l[g] * keep + w;
-#pragma unroll
-        for (int x = 0; x < kCh; ++x) o[g][x] = fmaf(w, kv[x], o[g][x] * keep);
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < kHeads; ++g) {
-      if (lane == 0) s_m[warp][g] = m[g], s_l[warp][g] = l[g];
-#pragma unroll
-      for (int x = 0; x < kCh; ++x) s_o[warp][g][lane * kCh + x] = o[g][x];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kHeads * D; i += kWarps * 32) {
-      const int g = i / D, ch = i % D;
-      if (g0 + g < a.G) {
-        const int h = kh * a.G + g0 + g;
-        float top = a.sink ? a.sink[h] * kLog2e : kNegBig, all = 0.f, acc = 0.f;
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_l[w][g] > 0.f ? s_m[w][g] : kNegBig);
-        for (int w = 0; w < kWarps; ++w) {
-          if (s_l[w][g] == 0.f) continue;
-          const float x = fast_exp2(s_m[w][g] - top);
-          all += s_l[w][g] * x;
-          acc += s_o[w][g][ch] * x;
+          for (int i = 0; i < 4; ++i) {
+            const int32_t x = k0 + i * 32, y = i * 32;
+            uint32_t m = bits_between(see.low - x, see.c - x) | bits_between(-x, see.first - x);
+            if (a.words > 0 && x + 32 > see.c && x < see.end) {  // 32 bits of the drafts' mask, from bit x - c on
+              const int32_t d = x - see.c, at = d >> 5;          // rounded down
+              const uint32_t* words = reinterpret_cast<const uint32_t*>(a.mask + static_cast<int64_t>(t) * a.words);
+              const uint32_t lo = at >= 0 && at < 2 * a.words ? words[at] : 0u, hi = at + 1 >= 0 && at + 1 < 2 * a.words ? words[at + 1] : 0u;
+              m |= __funnelshift_r(lo, hi, d & 31) & bits_between(0, see.end - x);
+            }
+            const uint32_t heads = bits_between(0, head - y);
+            m = (m & ~heads) | (heads & bits_between(0, see.c - v - y));  // first rows: below low of everyone who sees any
+            m &= bits_between(0, here - y);
+            missed |= m & lost[i];
+            bits[i] = m & ~lost[i];
+          }
+          if (missed && flat >= 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
         }
-        if (a.sink) all += fast_exp2(a.sink[h] * kLog2e - top);
-        const int64_t flat = static_cast<int64_t>(t) * a.H + h;
-        a.out[flat * D + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(all == 0.f ? 0.f : acc / all));
-        if (a.lse && ch == 0) a.lse[flat] = all == 0.f ? -INFINITY : (top + log2f(all)) * kKvLn2;
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) settled32(z + i * 32);
+        const uint32_t others = other_tiles + (j + 1) / 2;  // tiles of the other group before this one
+        if (!two && j > 0) {                                // the reference as it left it
+          if (!warp_wait(&sm.decided[w ^ 1][quad], others - 1)) return false;
+          const float now = sm.ref[row];
+          if (now != ref) {
+            l = l == 0.f ? 0.f : l * fast_exp2(ref - now);
+            ref = now;
+          }
+        }
+        const bool unset = ref == kNegBig;
+        const float shift = unset ? 0.f : ref;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) z[i] = fmaf(z[i], c, -shift);
+        if (masks) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) z[i] = (bits[i / 32] >> (i % 32)) & 1 ? z[i] : -INFINITY;
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; ++i) top[i % 4] = fmaxf(top[i % 4], z[i]);
+        const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (__any_sync(0xFFFFFFFFu, over > kKvJump || (unset && over > -INFINITY))) {
+          // the reference goes to the largest score so far
+          const float by = unset ? (over > -INFINITY ? over : 0.f) : fmaxf(over, 0.f);
+          const float keep = unset ? 1.f : fast_exp2(-by);  // an unset row's output is 0
+          if (!unset || over > -INFINITY) ref = shift + by;
+          l *= keep;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) z[i] -= by;
+          if (j > 0 && __any_sync(0xFFFFFFFFu, keep != 1.f)) {
+            // the products of the tiles before have to be done: those of a group with a tile of its own
+            // came before these scores, else the last one is the other group's
+            if (!two && !warp_wait(&sm.pv_done[w ^ 1], others - 1)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < (two ? 128 : L::kDV); i += 16) {
+              float o[16];
+              tmem_ld<16>(at_o + i, o);
+              uint32_t x[16];
+#pragma unroll
+              for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(o[y] * keep);
+              kv_tmem_st16(at_o + i, x);
+            }
+            tc_wait_st();
+          }
+        }
+        if (!two) {
+          sm.ref[row] = ref;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.decided[w][quad]);
+        }
+        // weights, rounded to bf16, as A of the second product
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[16];
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) {
+            const float p0 = fast_exp2(z[i * 32 + y]), p1 = fast_exp2(z[i * 32 + y + 1]);
+            part[y % 4] += p0;
+            part[y % 4 + 1] += p1;
+            x[y / 2] = pack_bf16x2_rn(p0, p1);
+          }
+          kv_tmem_st16(at_s + i * 16, x);
+        }
+        l += (part[0] + part[1]) + (part[2] + part[3]);
+        tc_wait_st();
+      } else if (!two && lane == 0) {
+        mbar_arrive(&sm.decided[w][quad]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[w]);
+    }
+    keys_before += n;
+    // ------------------------------------------------------------------ output
+    const bool split = p.splits > 1;
+    float all = l, m = ref;
+    if (!two) {
+      other_tiles += (n + w) / 2;
+      sm.sum[w][row] = l;
+      sm.sum_ref[w][row] = ref;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.met);
+      if (!warp_wait(&sm.met, met_use++)) return false;
+      // O has the larger reference of the two: the tile that set it has a weight of 1 at least
+      const float l1 = sm.sum[w ^ 1][row], m1 = sm.sum_ref[w ^ 1][row];
+      m = fmaxf(l == 0.f ? kNegBig : ref, l1 == 0.f ? kNegBig : m1);
+      all = (l == 0.f ? 0.f : l * fast_exp2(ref - m)) + (l1 == 0.f ? 0.f : l1 * fast_exp2(m1 - m));
+    }
+    const bool none = all == 0.f;
+    float keep = 1.f;
+    if (a.sink && !split && flat >= 0) {
+      const float s = a.sink[flat % a.H] * kLog2e, high = fmaxf(none ? kNegBig : m, s);
+      keep = none ? 0.f : fast_exp2(m - high);
+      all = (none ? 0.f : all * keep) + (s == high ? 1.f : fast_exp2(s - high));
+      m = high;
+    }
+    const float scale = none ? 0.f : keep / all;
+    const int64_t rows = a.T * a.H, place = flat + (split ? range * rows : 0);
+    float* part_out = static_cast<float*>(a.workspace);
+    if (flat >= 0 && (two || w == 0) && half == 0) {
+      const float lse = all == 0.f ? -INFINITY : (m + log2f(all)) * kKvLn2;
+      if (split) part_out[p.splits * rows * D + place] = lse;
+      else if (a.lse) a.lse[flat] = lse;
+    }
+    if (n > 0) {
+      if (!warp_wait(&sm.o_full[w], o_use++)) return false;
+      tc_fence_after();
+    }
+    if (any) {
+      const int c0 = two ? 0 : w * (L::kDV / 2), c1 = two ? 128 : c0 + L::kDV / 2;
+#pragma unroll 1
+      for (int i = c0; i < c1; i += 32) {
+        float o[32];
+        if (n > 0) tmem_ld<32>(at_o + i, o);
+        if (n == 0 || none) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = 0.f;
+        }
+        if (flat >= 0) {
+          const int ch = half * L::kDV + i;
+          if (split) {
+            float4* to = reinterpret_cast<float4*>(part_out + place * D + ch);
+            if (!none) {  // else the join does not look at it
+#pragma unroll
+              for (int x = 0; x < 8; ++x) to[x] = make_float4(o[4 * x] * scale, o[4 * x + 1] * scale, o[4 * x + 2] * scale, o[4 * x + 3] * scale);
+            }
+          } else {
+            uint4* to = reinterpret_cast<uint4*>(a.out + place * D + ch);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              to[x] = make_uint4(pack_bf16x2_rn(o[8 * x] * scale, o[8 * x + 1] * scale), pack_bf16x2_rn(o[8 * x + 2] * scale, o[8 * x + 3] * scale),
+                                 pack_bf16x2_rn(o[8 * x + 4] * scale, o[8 * x + 5] * scale), pack_bf16x2_rn(o[8 * x + 6] * scale, o[8 * x + 7] * scale));
+          }
+        }
       }
     }
-    __syncthreads();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sm.job_empty[job_use & 1]);
+      if (!two) mbar_arrive(&sm.met);
+    }
+    if (!two && !warp_wait(&sm.met, met_use++)) return false;  // O and the sums are read
   }
+}
+
+// One thread: the products, in the order of their units.
+template <int D>
+__device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tmem) {
+  using L = KvLayout<D>;
+  constexpr uint32_t kIdescS = idesc_bf16(128, false), kIdescO = idesc_bf16(128, true);
+  uint32_t unit = 0, q_use = 0, p_use[2] = {0, 0};
+  auto wait = [](uint64_t* bar, uint32_t n) { return mbar_wait_near(bar, n & 1u); };
+  auto unit_there = [&](uint32_t c) {
+    const bool ok = wait(&sm.full[c % L::kRing], c / L::kRing);
+    tc_fence_after();
+    return ok;
+  };
+  // scores of group w: queries in slot q, with unit c for channels 128 u ...
+  auto scores = [&](int w, uint32_t q, uint32_t c, int u) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const uint64_t da = smem_desc_sw128(base + L::kQ + (q * L::kKU + u) * kKvUnit + (s / 4) * 16384 + (s % 4) * 32, 16, 1024);
+      const uint64_t db = smem_desc_sw128(base + (c % L::kRing) * kKvUnit + (s / 4) * 16384 + (s % 4) * 32, 16, 1024);
+      mma_f16_ss(tmem + L::kTmemS + w * 128, da, db, kIdescS, u > 0 || s > 0);
+    }
+  };
+  // weights of group w with unit c, into 128 columns of the output
+  auto values = [&](int w, uint32_t column, uint32_t c, bool more) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const uint64_t db = smem_desc_sw128(base + (c % L::kRing) * kKvUnit + s * 2048, 16384, 1024);
+      mma_f16_ts(tmem + L::kTmemO + column, tmem + L::kTmemS + w * 128 + s * 8, db, kIdescO, more || s > 0);
+    }
+  };
+#pragma unroll 1
+  for (uint32_t job_use = 0;; ++job_use) {
+    if (!wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
+    const Job& job = sm.job[job_use & 1];
+    if (!job.live) return true;
+    const int n = job.n;
+    const bool two = L::kQSlots == 2 && job.two;
+    mbar_arrive(&sm.job_empty[job_use & 1]);
+    if (n == 0) continue;
+    if (two) {
+      const uint32_t slot[2] = {q_use & 1, (q_use + 1) & 1};
+      for (int w = 0; w < 2; ++w) {
+        if (!wait(&sm.q_full[slot[w]], (q_use + w) >> 1) || !unit_there(unit)) return false;
+        scores(w, slot[w], unit, 0);
+        tc_commit(&sm.s_full[w]);
+        if (n == 1) tc_commit(&sm.q_empty[slot[w]]);
+      }
+      tc_commit(&sm.empty[unit % L::kRing]);
+      for (int j = 0; j < n; ++j) {
+        const uint32_t v = unit + 2 * j + 1, k = v + 1;  // values of this tile, keys of the next
+        for (int w = 0; w < 2; ++w) {
+          if (!unit_there(v) || !wait(&sm.p_full[w], p_use[w]++)) return false;
+          tc_fence_after();
+          values(w, w * 128, v, j > 0);
+          if (w == 1) tc_commit(&sm.empty[v % L::kRing]);
+          if (j + 1 < n) {
+            if (!unit_there(k)) return false;
+            scores(w, slot[w], k, 0);
+            tc_commit(&sm.s_full[w]);
+            if (j + 2 == n) tc_commit(&sm.q_empty[slot[w]]);
+            if (w == 1) tc_commit(&sm.empty[k % L::kRing]);
+          } else {
+            tc_commit(&sm.o_full[w]);
+          }
+        }
+      }
+      unit += 2 * n;
+      q_use += 2;
+    } else {
+      const uint32_t slot = q_use % L::kQSlots;
+      if (!wait(&sm.q_full[slot], q_use / L::kQSlots)) return false;
+      auto tile_scores = [&](int j) {
+        for (int u = 0; u < L::kKU; ++u, ++unit) {
+          if (!unit_there(unit)) return false;
+          scores(j & 1, slot, unit, u);
+          tc_commit(&sm.empty[unit % L::kRing]);
+        }
+        tc_commit(&sm.s_full[j & 1]);
+        if (j == n - 1) tc_commit(&sm.q_empty[slot]);
+        return true;
+      };
+      if (!tile_scores(0) || (n > 1 && !tile_scores(1))) return false;
+      for (int j = 0; j < n; ++j) {
+        if (!wait(&sm.p_full[j & 1], p_use[j & 1]++)) return false;
+        tc_fence_after();
+        for (int u = 0; u < L::kVU; ++u, ++unit) {
+          if (!unit_there(unit)) return false;
+          values(j & 1, u * 128, unit, j > 0);
+          tc_commit(&sm.empty[unit % L::kRing]);
+        }
+        tc_commit(&sm.pv_done[j & 1]);
+        if (j + 2 < n && !tile_scores(j + 2)) return false;
+      }
+      tc_commit(&sm.o_full[0]);
+      tc_commit(&sm.o_full[1]);
+      ++q_use;
+    }
+  }
+}
+
+// Four warps: queries, keys and values of the jobs, unit by unit, as many ahead as the ring has places.
+template <int D>
+__device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvSmall& sm, uint8_t* smem) {
+  using L = KvLayout<D>;
+  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - kCopyWarp;
+  uint32_t unit = 0, q_use = 0, keys_before = 0;
+  // copies on their way: barriers of their units (4 bits each: 8 + a slot of queries, or a place of the ring), oldest lowest
+  uint32_t on_way = 0;
+  int ways = 0;
+  auto land = [&](int keep) {  // until no more than `keep` units are on their way
+    while (ways > keep) {
+      copies_wait_for(ways - 1);
+      fence_proxy_async_smem();
+      __syncwarp();
+      const uint32_t i = on_way & 15u;
+      if (lane == 0) mbar_arrive(i >= 8 ? &sm.q_full[i - 8] : &sm.full[i]);
+      on_way >>= 4;
+      --ways;
+    }
+  };
+  // Wait for a barrier, and hand on what lands meanwhile: whoever is to complete it may wait for that.
+  auto wait = [&](uint64_t* bar, uint32_t n) {
+    while (ways > 0) {
+      if (__all_sync(0xFFFFFFFFu, mbar_test(bar, n & 1u))) return true;
+      land(ways - 1);
+    }
+    return warp_wait(bar, n);
+  };
+  // 128 rows x 256 bytes, 32 of the rows by this warp: row `lane` of them begins at from + off elements
+  // (off < 0: zeros).  16 lanes copy a row.
+  auto copy = [&](uint8_t* to, const uint16_t* from, int64_t off, uint32_t name) {
+    const int x = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int from_lane = 2 * i + (lane >> 4), r = cw * 32 + from_lane;
+      const int64_t o = __shfl_sync(0xFFFFFFFFu, off, from_lane);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       smem_u32(to + (x >> 3) * 16384 + r * 128 + (((x & 7) ^ (r & 7)) * 16))),
+                   "l"(from + (o >= 0 ? o : 0) + x * 8), "r"(o >= 0 ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    on_way |= name << (4 * ways);
+    ++ways;
+    land(5);
+  };
+  auto copy_unit = [&](const uint16_t* from, int64_t off) {
+    const uint32_t place = unit % L::kRing;
+    if (unit >= L::kRing && !wait(&sm.empty[place], unit / L::kRing - 1)) return false;
+    copy(smem + place * kKvUnit, from, off, place);
+    ++unit;
+    return true;
+  };
+  bool ok = true;
+#pragma unroll 1
+  for (uint32_t job_use = 0;; ++job_use) {
+    if (!wait(&sm.job_full[job_use & 1], job_use >> 1)) ok = false;
+    if (!ok) break;
+    const Job job = sm.job[job_use & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.job_empty[job_use & 1]);
+    if (!job.live) break;
+    if (job.n == 0) continue;
+    const bool two = L::kQSlots == 2 && job.two;
+    const int32_t* table = a.table + static_cast<int64_t>(job.tile.b) * a.table_stride;
+    // the row of the cache in this lane's place of a tile, -1: none; and its page
+    auto key_of = [&](int j) {
+      const int32_t v = job.v0 + j * kKvKeys + cw * 32 + lane;
+      return j >= job.n || v >= job.v1 ? -1 : v < job.first ? v : job.low + v - job.first;
+    };
+    auto page_of = [&](int32_t key) { return a.page_shift >= 0 ? key >> a.page_shift : key / a.cache.page_size; };
+    int32_t key = key_of(0), page = key >= 0 ? table[page_of(key)] : 0;
+    for (int w = 0; w < (two ? 2 : 1); ++w, ++q_use) {
+      const uint32_t slot = q_use % L::kQSlots;
+      if (q_use >= L::kQSlots && !wait(&sm.q_empty[slot], q_use / L::kQSlots - 1)) ok = false;
+      if (!ok) break;
+      const int32_t i = w * 128 + cw * 32 + lane, r = job.tile.base + i;
+      int64_t off = -1;
+      if (i < job.tile.rows) {
+        const int32_t tok = r / a.G;
+        off = (job.tile.tok0 + tok) * a.q_st + (job.kh * a.G + r - tok * a.G) * a.q_sh;
+      }
+      for (int u = 0; u < L::kKU; ++u) {
+        // the units of a slot make one group: its barrier is told of the last
+        const bool last = u == L::kKU - 1;
+        uint8_t* to = smem + L::kQ + (slot * L::kKU + u) * kKvUnit;
+        const int x = lane & 15;
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+          const int from_lane = 2 * k + (lane >> 4), rr = cw * 32 + from_lane;
+          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, from_lane);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           smem_u32(to + (x >> 3) * 16384 + rr * 128 + (((x & 7) ^ (rr & 7)) * 16))),
+                       "l"(a.q + (o >= 0 ? o : 0) + u * 128 + x * 8), "r"(o >= 0 ? 16 : 0)
+                       : "memory");
+        }
+        if (last) {
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          on_way |= (8u + slot) << (4 * ways);
+          ++ways;
+          land(5);
+        }
+      }
+    }
+    if (!ok) break;
+    int64_t v_off = -1, v_next = -1;
+#pragma unroll 1
+    for (int j = 0; j <= job.n; ++j) {
+      if (j < job.n) {
+        const uint32_t jt = keys_before + j;
+        int64_t k_off = -1;
+        v_next = -1;
+        bool missing = false;
+        if (key >= 0) {
+          const int32_t at = key - page_of(key) * a.cache.page_size;
+          if (page >= 0 && page < a.cache.num_pages) {
+            k_off = page * a.cache.k_stride_page + at * a.cache.k_stride_row + job.kh * a.cache.k_stride_head;
+            v_next = page * a.cache.v_stride_page + at * a.cache.v_stride_row + job.kh * a.cache.v_stride_head + job.half * L::kDV;
+          } else {
+            missing = true;
+          }
+        }
+        const uint32_t gone = __ballot_sync(0xFFFFFFFFu, missing);
+        key = key_of(j + 1);
+        page = key >= 0 ? table[page_of(key)] : 0;
+        for (int u = 0; u < L::kKU && ok; ++u) {
+          // Three tiles of keys lie behind the place of `bad` once a unit of this one has a place in the ring:
+          // its softmax is over.
+          if (unit >= L::kRing && !wait(&sm.empty[unit % L::kRing], unit / L::kRing - 1)) ok = false;
+          if (u == 0 && ok && lane == 0) {
+            sm.bad[jt & 3][cw] = gone;
+            mbar_arrive(&sm.noted[jt & 3]);
+          }
+          if (ok) ok = copy_unit(a.cache.k + u * 128, k_off);
+        }
+        if (!ok) break;
+      }
+      if (two ? j < job.n : j > 0) {
+        const int64_t off = two ? v_next : v_off;
+        for (int u = 0; u < L::kVU && ok; ++u) ok = copy_unit(a.cache.v + u * 128, off);
+        if (!ok) break;
+      }
+      v_off = v_next;
+    }
+    if (!ok) break;
+    keys_before += job.n;
+  }
+  land(0);
+  return ok;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kKvThreads, 1)
+    kv_attention_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ KvPlan p, int64_t jobs) {
+  using L = KvLayout<D>;
+  // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  KvSmall& sm = *reinterpret_cast<KvSmall*>(smem + L::kSmall);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (smem_u32(smem) & 1023u) {
+    pdl_wait();  // whoever follows in the stream counts on what came before having ended
+    if (threadIdx.x == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+    return;
+  }
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&sm.full[i], 4);
+        mbar_init(&sm.empty[i], 1);
+        mbar_init(&sm.noted[i], 4);
+        mbar_init(&sm.decided[0][i], 1);
+        mbar_init(&sm.decided[1][i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sm.q_full[i], 4);
+        mbar_init(&sm.q_empty[i], 1);
+        mbar_init(&sm.s_full[i], 1);
+        mbar_init(&sm.p_full[i], 4);
+        mbar_init(&sm.o_full[i], 1);
+        mbar_init(&sm.pv_done[i], 1);
+        mbar_init(&sm.job_full[i], 1);
+        mbar_init(&sm.job_empty[i], 13);
+      }
+      mbar_init(&sm.met, 8);
+      mbar_init(&sm.drain, 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc<512>(&sm.tmem);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  pdl_wait();
+
+  bool ok = true;
+  if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    ok = soft_jobs<D>(a, p, sm, tmem);
+    tc_fence_before();
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kMmaWarp) {
+      if (elect_one()) {
+        ok = mma_jobs<D>(sm, smem_u32(smem), tmem);
+        // the end of every product: tensor memory may be given back
+        tc_commit(&sm.drain);
+        ok = mbar_wait_near(&sm.drain, 0) && ok;
+        if (!ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+      }
+      __syncwarp();
+    } else if (warp == kPlanWarp) {
+      uint32_t use = 0;
+      for (int64_t id = blockIdx.x; ok; id += gridDim.x) {
+        Job j;
+        j.live = 0;
+        if (id < jobs) {
+          j = make_job<D>(a, p, id);
+          if (j.tile.rows <= 0) continue;
+        }
+        if (use >= 2) ok = warp_wait(&sm.job_empty[use & 1], (use >> 1) - 1);
+        if (!ok) break;
+        if (lane == 0) {
+          sm.job[use & 1] = j;
+          mbar_arrive(&sm.job_full[use & 1]);
+        }
+        __syncwarp();
+        ++use;
+        if (!j.live) break;
+      }
+    } else if (warp >= kCopyWarp) {
+      ok = copy_jobs<D>(a, sm, smem);
+    }
+  }
+  if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
+  pdl_trigger();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc<512>(tmem);
+  }
+}
+
+// Joins the ranges of a row, in their order: one warp per row and 128 channels.
+template <int D, bool kFew>
+__global__ void __launch_bounds__(128, kFew ? 12 : 4) kv_join_kernel(const __grid_constant__ KvAttentionArgs a, int splits) {
+  constexpr int kParts = D / 128, kDeep = kFew ? 4 : 16, kOwn = kFew ? 1 : kKvMaxSplits / 32;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  const int64_t work = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5), flat = work / kParts, rows = a.T * a.H;
+  const int part = static_cast<int>(work % kParts);
+  if (flat >= rows) return;
+  const int32_t t = static_cast<int32_t>(flat / a.H);
+  if (a.ctx_rows[t] < 0 || t < kv_start_of(a, 0) || t >= kv_start_of(a, a.B)) return;
+  const float* ws = static_cast<const float*>(a.workspace);
+  const float* part_lse = ws + splits * rows * D + flat;
+  float lse[kOwn], m = -INFINITY;  // of ranges lane, lane + 32, ...
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int s = lane + i * 32;
+    lse[i] = s < splits ? part_lse[s * rows] : -INFINITY;
+    m = fmaxf(m, lse[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float sink = a.sink ? a.sink[flat % a.H] : -INFINITY;
+  m = fmaxf(m, sink);
+  const float safe = m == -INFINITY ? 0.f : m;
+  float all = 0.f;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    lse[i] = fast_exp2((lse[i] - safe) * kLog2e);  // its weight from here on
+    all += lse[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+  if (a.sink) all += sink == m ? 1.f : fast_exp2((sink - safe) * kLog2e);
+  const float4* o = reinterpret_cast<const float4*>(ws + flat * D + part * 128) + lane;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j) {
+    for (int s0 = j * 32; s0 < min(splits, j * 32 + 32); s0 += kDeep) {
+      float4 v[kDeep];
+      float x[kDeep];
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        x[i] = __shfl_sync(0xFFFFFFFFu, lse[j], (s0 + i) % 32);
+        v[i] = s0 + i < splits && x[i] != 0.f ? o[(s0 + i) * (rows * D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        if (s0 + i >= splits) x[i] = 0.f;
+        acc[0] = fmaf(v[i].x, x[i], acc[0]);
+        acc[1] = fmaf(v[i].y, x[i], acc[1]);
+        acc[2] = fmaf(v[i].z, x[i], acc[2]);
+        acc[3] = fmaf(v[i].w, x[i], acc[3]);
+      }
+    }
+  }
+  const float inv = all == 0.f ? 0.f : 1.f / all;
+  *reinterpret_cast<uint2*>(a.out + flat * D + part * 128 + lane * 4) =
+      make_uint2(pack_bf16x2_rn(acc[0] * inv, acc[1] * inv), pack_bf16x2_rn(acc[2] * inv, acc[3] * inv));
+  if (part == 0 && lane == 0 && a.lse) a.lse[flat] = all == 0.f ? -INFINITY : safe + log2f(all) * kKvLn2;
+}
+
+// Rows of tiles, and into how many ranges of keys a tile is split: the count that a model of the time
+// finds best.  CTAs take their jobs one after the other.  Lengths are known on the host by their
+// bound only, so ranges are of equal size, and of 2^17 keys at most (the tensor cores cut each sum
+// off towards 0: fp4_attention.cu has the figures).
+KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows, int32_t window, int32_t first, int32_t words) {
+  KvPlan p;
+  const int R = D == 128 ? 256 : 128, G = H / KH;
+  const int64_t pad = kv_tile_pad(G, R);
+  p.tiles = static_cast<int>((T * G + static_cast<int64_t>(B) * pad) / R);
+  int64_t busy = (T * G + R - 1) / R;
+  busy = busy < T && busy < B ? (T < B ? T : B) : busy;
+  busy *= static_cast<int64_t>(KH) * (D == 512 ? 2 : 1);
+  // keys that a tile's tokens see together when they follow each other
+  int64_t span = max_rows;
+  if (window > 0) span = std::min<int64_t>(max_rows, static_cast<int64_t>(window) + first + R / G + 64 * words);
+  const int64_t most = (span + kKvKeys - 1) / kKvKeys;
+  const double around = 2.0, tile = D == 512 ? 2.0 : D == 256 ? 1.2 : 0.8;
+  const int64_t least = (span + kKvMaxRange - 1) / kKvMaxRange;  // <= kKvMaxSplits: the callers' bound of max_rows
+  int64_t best_s = least;
+  double best = 0;
+  for (int64_t s = least; s <= most && s <= kKvMaxSplits; ++s) {
+    const int64_t waves = (busy * s + 151) / 152;
+    double us = static_cast<double>(waves) * (around + tile * static_cast<double>((most + s - 1) / s));
+    if (s > 1) us += 2.5 + 0.02 * static_cast<double>(s) + 2.0 * static_cast<double>(T * H * s) * D * 4 / 4e6;
+    if (s == least || us < best) {
+      best = us;
+      best_s = s;
+    }
+  }
+  p.chunk = static_cast<int>((most + best_s - 1) / best_s * kKvKeys);
+  p.splits = static_cast<int>((span + p.chunk - 1) / p.chunk);
+  return p;
 }
 
 template <int D>
 cudaError_t launch(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s) {
-  return launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(a.T), a.KH), dim3(kWarps * 32), 0, use_pdl, s, a);
+  const KvPlan p = plan_kv(a.T, a.B, a.H, a.KH, D, a.max_rows, a.window, a.first, a.words);
+  int dev = 0, sms = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  if ((e = set_max_smem_once<kv_attention_kernel<D>>(kv_smem_bytes<D>())) != cudaSuccess) return e;
+  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * a.KH * KvLayout<D>::kHalves;
+  if (jobs == 0) return cudaSuccess;
+  e = launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(jobs < sms ? jobs : sms)), dim3(kKvThreads), kv_smem_bytes<D>(), use_pdl, s, a,
+                p, jobs);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const int64_t ctas = (a.T * a.H * (D / 128) + 3) / 4;
+  return p.splits <= 4 ? launch_ex(kv_join_kernel<D, true>, dim3(static_cast<unsigned>(ctas)), dim3(128), 0, true, s, a, p.splits)
+                       : launch_ex(kv_join_kernel<D, false>, dim3(static_cast<unsigned>(ctas)), dim3(128), 0, true, s, a, p.splits);
 }
 
 }  // namespace
 
-int64_t kv_attention_workspace(int64_t, int32_t, int32_t, int32_t, int32_t, int64_t, int32_t, int32_t, int32_t) { return 0; }
+int64_t kv_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows, int32_t window, int32_t first_rows,
+                               int32_t words) {
+  const KvPlan p = plan_kv(T, B, H, KH, D, max_rows, window, window > 0 ? first_rows : 0, words);
+  return p.splits == 1 ? 0 : static_cast<int64_t>(p.splits) * T * H * (D + 1) * static_cast<int64_t>(sizeof(float));
+}
 
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s) {
   return a.cache.D == 128 ? launch<128>(a, use_pdl, s) : a.cache.D == 256 ? launch<256>(a, use_pdl, s) : launch<512>(a, use_pdl, s);
