@@ -32,6 +32,7 @@
 // Few tiles with many keys are split into ranges of keys; their results (fp32, and lse) go through
 // the workspace and are joined by a second kernel in a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include "ckv_tcgen05.cuh"
 #include "kv_attention.cuh"
@@ -40,21 +41,27 @@ namespace ckv {
 namespace {
 
 constexpr int kKvKeys = 128, kKvUnit = 32768;  // keys of a tile; bytes of a unit
+constexpr int kKvRoom = 7 * kKvUnit, kKvMaxRing = 6;  // for units and queries; places of the ring
 constexpr float kKvJump = 16.f;                // log2 of the largest weight over its reference
 constexpr int kMmaWarp = 8, kPlanWarp = 9, kCopyWarp = 12, kKvThreads = 512;
 // Registers per thread: 512 x 128 at launch; then 256 x 192 + 256 x 64, the same.
 constexpr int kSoftRegs = 192, kOtherRegs = 64;
 
-template <int D>
+// R: rows of a job.  With R = 256 (D = 128) there are two tiles of queries; with fewer than 128 rows the
+// products read past the queries into whatever lies there, for rows that nobody looks at.
+template <int D, int R>
 struct KvLayout {
   static constexpr int kHalves = D == 512 ? 2 : 1;
-  static constexpr int kDV = D / kHalves;               // channels of the output that a CTA has
-  static constexpr int kKU = D / 128, kVU = kDV / 128;  // units of a tile's keys and values
-  static constexpr int kTile = D == 128 ? 256 : 128;    // rows of a job
-  static constexpr int kQSlots = D == 128 ? 2 : 1;      // of 128 rows
-  static constexpr int kRing = D == 512 ? 3 : 4;
-  static constexpr int kQ = kRing * kKvUnit;
-  static constexpr int kSmall = kQ + kQSlots * kKU * kKvUnit;
+  static constexpr int kDV = D / kHalves;                // channels of the output that a CTA has
+  static constexpr int kKU = D / 128, kVU = kDV / 128;   // units of a tile's keys and values
+  static constexpr int kQRows = R < 128 ? R : 128;       // of a slot of queries
+  static constexpr int kQBlock = kQRows * 128;           // 64 channels of them
+  static constexpr int kQSlot = kQBlock * (D / 64);
+  static constexpr int kQSlots = R == 256 || kQSlot <= 16384 ? 2 : 1;
+  static constexpr int kRing = (kKvRoom - kQSlots * kQSlot) / kKvUnit;
+  static constexpr int kUnits = kQSlots * kQSlot;  // where the ring begins, behind the queries
+  static constexpr int kSmall = kUnits + kRing * kKvUnit;
+  static_assert(kRing >= 3 && kRing <= kKvMaxRing, "shared memory");
   static constexpr int kTmemO = 0, kTmemS = 256;        // O: 256 columns; S: two buffers of 128, P over the first half of each
 };
 
@@ -69,7 +76,7 @@ struct Job {
 };
 
 // Barriers.  `Uses` are numbered from 0 over the whole kernel, so that everyone counts alike.
-//   full, empty     of a unit of the ring: 4 copying warps; the products that read it
+//   full, empty     of a unit of the ring: 128 copying threads; the products that read it
 //   q_full, q_empty of a slot of queries, alike
 //   s_full[w]       scores of group w are there (and all products issued before them are done)
 //   p_full[w]       weights of group w are there: 4 warps
@@ -80,20 +87,20 @@ struct Job {
 //   pv_done[w]      second product of a tile of group w
 //   met             both groups have got there: 8 warps, twice per job
 struct KvSmall {
-  uint64_t full[4], empty[4], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], job_full[2], job_empty[2], noted[4];
+  uint64_t full[kKvMaxRing], empty[kKvMaxRing], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], job_full[2], job_empty[2], noted[4];
   uint64_t decided[2][4], pv_done[2], met, drain;
   uint32_t tmem;
   Job job[2];
   alignas(16) uint32_t bad[4][4];  // a bit per key of a tile whose page is not there (ring over tiles of keys)
   float ref[128];                  // references of the shared rows
-  float sum[2][128], sum_ref[2][128];
+  float sum[2][128];
 };
 
-template <int D>
+template <int D, int R>
 constexpr int kv_smem_bytes() {
-  return KvLayout<D>::kSmall + static_cast<int>(sizeof(KvSmall));
+  return KvLayout<D, R>::kSmall + static_cast<int>(sizeof(KvSmall));
 }
-static_assert(kv_smem_bytes<128>() <= 227 * 1024 && kv_smem_bytes<256>() <= 227 * 1024 && kv_smem_bytes<512>() <= 227 * 1024, "shared memory");
+static_assert(kKvRoom + sizeof(KvSmall) <= 227 * 1024, "shared memory");
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn_major) { return idesc_f16(n, false, b_mn_major) | (1u << 7) | (1u << 10); }
 
@@ -132,28 +139,18 @@ __device__ __forceinline__ uint32_t bits_between(int32_t x0, int32_t x1) {
 // Wait for use `n` of a barrier, by a whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t n) { return __all_sync(0xFFFFFFFFu, mbar_wait_near(bar, n & 1u)); }
 
-__device__ __forceinline__ void copies_wait_for(int left) {
-  switch (left) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-  }
-}
-
 struct KvPlan {
-  int tiles;   // bound of the number of tiles of rows
+  int R;       // rows of a tile
+  int tiles;   // bound of the number of tiles
   int splits;  // ranges of keys
   int chunk;   // keys of a range (a multiple of kKvKeys); the last range takes all that are left
 };
 
 // ---------------------------------------------------------------------- jobs
 // Job `id`, by one converged warp; rows <= 0 when there is nothing to do in it.
-template <int D>
+template <int D, int R>
 __device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& p, int64_t id) {
-  using L = KvLayout<D>;
+  using L = KvLayout<D, R>;
   const int lane = threadIdx.x & 31;
   Job j;
   j.half = static_cast<int32_t>(id % L::kHalves);
@@ -161,9 +158,9 @@ __device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& 
   j.kh = static_cast<int32_t>(id % a.KH);
   id /= a.KH;
   j.split = static_cast<int32_t>(id % p.splits);
-  j.tile = kv_find_tile(a, static_cast<int32_t>(id / p.splits), L::kTile);
+  j.tile = kv_find_tile(a, static_cast<int32_t>(id / p.splits), R);
   j.live = 1;
-  j.two = j.tile.rows > 128;
+  j.two = R == 256 && j.tile.rows > 128;
   j.first = j.low = j.v0 = j.v1 = j.n = 0;
   if (j.tile.rows <= 0) return j;
   // what its tokens see together
@@ -189,9 +186,9 @@ __device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& 
 }
 
 // The part of the softmax warps: see the roles above.
-template <int D>
+template <int D, int R>
 __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan& p, KvSmall& sm, uint32_t tmem) {
-  using L = KvLayout<D>;
+  using L = KvLayout<D, R>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, w = warp >> 2, row = threadIdx.x & 127;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128;
@@ -203,7 +200,7 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
     if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
     const Job& job = sm.job[job_use & 1];
     if (!job.live) return true;
-    const bool two = L::kQSlots == 2 && job.two;
+    const bool two = R == 256 && job.two;
     const int32_t n = job.n, kh = job.kh, half = job.half, range = job.split;
     const int32_t r = job.tile.base + (two ? w * 128 : 0) + row;
     int32_t t = 0, flat = -1;
@@ -338,15 +335,17 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
     float all = l, m = ref;
     if (!two) {
       other_tiles += (n + w) / 2;
+      // both sums against the references that O has in the end: the last tile's
+      if (n > 0) {
+        if (((n - 1) & 1) != w && !warp_wait(&sm.decided[w ^ 1][quad], other_tiles - 1)) return false;
+        m = any ? sm.ref[row] : 0.f;
+        l = l == 0.f ? 0.f : l * fast_exp2(ref - m);
+      }
       sm.sum[w][row] = l;
-      sm.sum_ref[w][row] = ref;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.met);
       if (!warp_wait(&sm.met, met_use++)) return false;
-      // O has the larger reference of the two: the tile that set it has a weight of 1 at least
-      const float l1 = sm.sum[w ^ 1][row], m1 = sm.sum_ref[w ^ 1][row];
-      m = fmaxf(l == 0.f ? kNegBig : ref, l1 == 0.f ? kNegBig : m1);
-      all = (l == 0.f ? 0.f : l * fast_exp2(ref - m)) + (l1 == 0.f ? 0.f : l1 * fast_exp2(m1 - m));
+      all = l + sm.sum[w ^ 1][row];
     }
     const bool none = all == 0.f;
     float keep = 1.f;
@@ -407,14 +406,15 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
 }
 
 // One thread: the products, in the order of their units.
-template <int D>
+template <int D, int R>
 __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tmem) {
-  using L = KvLayout<D>;
+  using L = KvLayout<D, R>;
   constexpr uint32_t kIdescS = idesc_bf16(128, false), kIdescO = idesc_bf16(128, true);
   uint32_t unit = 0, q_use = 0, p_use[2] = {0, 0};
   auto wait = [](uint64_t* bar, uint32_t n) { return mbar_wait_near(bar, n & 1u); };
   auto unit_there = [&](uint32_t c) {
     const bool ok = wait(&sm.full[c % L::kRing], c / L::kRing);
+    fence_proxy_async_smem();  // the copies are ordinary writes of other threads, done when the barrier says so
     tc_fence_after();
     return ok;
   };
@@ -422,8 +422,8 @@ __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tm
   auto scores = [&](int w, uint32_t q, uint32_t c, int u) {
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
-      const uint64_t da = smem_desc_sw128(base + L::kQ + (q * L::kKU + u) * kKvUnit + (s / 4) * 16384 + (s % 4) * 32, 16, 1024);
-      const uint64_t db = smem_desc_sw128(base + (c % L::kRing) * kKvUnit + (s / 4) * 16384 + (s % 4) * 32, 16, 1024);
+      const uint64_t da = smem_desc_sw128(base + q * L::kQSlot + (u * 2 + s / 4) * L::kQBlock + (s % 4) * 32, 16, 1024);
+      const uint64_t db = smem_desc_sw128(base + L::kUnits + (c % L::kRing) * kKvUnit + (s / 4) * 16384 + (s % 4) * 32, 16, 1024);
       mma_f16_ss(tmem + L::kTmemS + w * 128, da, db, kIdescS, u > 0 || s > 0);
     }
   };
@@ -431,7 +431,7 @@ __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tm
   auto values = [&](int w, uint32_t column, uint32_t c, bool more) {
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
-      const uint64_t db = smem_desc_sw128(base + (c % L::kRing) * kKvUnit + s * 2048, 16384, 1024);
+      const uint64_t db = smem_desc_sw128(base + L::kUnits + (c % L::kRing) * kKvUnit + s * 2048, 16384, 1024);
       mma_f16_ts(tmem + L::kTmemO + column, tmem + L::kTmemS + w * 128 + s * 8, db, kIdescO, more || s > 0);
     }
   };
@@ -441,13 +441,13 @@ __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tm
     const Job& job = sm.job[job_use & 1];
     if (!job.live) return true;
     const int n = job.n;
-    const bool two = L::kQSlots == 2 && job.two;
+    const bool two = R == 256 && job.two;
     mbar_arrive(&sm.job_empty[job_use & 1]);
     if (n == 0) continue;
     if (two) {
       const uint32_t slot[2] = {q_use & 1, (q_use + 1) & 1};
       for (int w = 0; w < 2; ++w) {
-        if (!wait(&sm.q_full[slot[w]], (q_use + w) >> 1) || !unit_there(unit)) return false;
+        if (!wait(&sm.q_full[slot[w]], (q_use + w) >> 1) || !unit_there(unit)) return false;  // (with the fence)
         scores(w, slot[w], unit, 0);
         tc_commit(&sm.s_full[w]);
         if (n == 1) tc_commit(&sm.q_empty[slot[w]]);
@@ -506,69 +506,46 @@ __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tm
 }
 
 // Four warps: queries, keys and values of the jobs, unit by unit, as many ahead as the ring has places.
-template <int D>
+// Every thread's copies arrive at the unit's barrier by themselves.
+template <int D, int R>
 __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvSmall& sm, uint8_t* smem) {
-  using L = KvLayout<D>;
-  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - kCopyWarp;
+  using L = KvLayout<D, R>;
+  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - kCopyWarp, x = lane & 15;
   uint32_t unit = 0, q_use = 0, keys_before = 0;
-  // copies on their way: barriers of their units (4 bits each: 8 + a slot of queries, or a place of the ring), oldest lowest
-  uint32_t on_way = 0;
-  int ways = 0;
-  auto land = [&](int keep) {  // until no more than `keep` units are on their way
-    while (ways > keep) {
-      copies_wait_for(ways - 1);
-      fence_proxy_async_smem();
-      __syncwarp();
-      const uint32_t i = on_way & 15u;
-      if (lane == 0) mbar_arrive(i >= 8 ? &sm.q_full[i - 8] : &sm.full[i]);
-      on_way >>= 4;
-      --ways;
-    }
-  };
-  // Wait for a barrier, and hand on what lands meanwhile: whoever is to complete it may wait for that.
-  auto wait = [&](uint64_t* bar, uint32_t n) {
-    while (ways > 0) {
-      if (__all_sync(0xFFFFFFFFu, mbar_test(bar, n & 1u))) return true;
-      land(ways - 1);
-    }
-    return warp_wait(bar, n);
-  };
-  // 128 rows x 256 bytes, 32 of the rows by this warp: row `lane` of them begins at from + off elements
-  // (off < 0: zeros).  16 lanes copy a row.
-  auto copy = [&](uint8_t* to, const uint16_t* from, int64_t off, uint32_t name) {
-    const int x = lane & 15;
+  auto arrive = [](uint64_t* bar) { asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory"); };
+  // kRows / 4 rows x 256 bytes by this warp, 16 lanes to a row, into blocks of 64 channels: the row in lane i
+  // begins at from + off elements (off < 0: zeros)
+  auto copy = [&](auto rows, uint8_t* to, int block, const uint16_t* from, int64_t off) {
+    constexpr int kRows = decltype(rows)::value / 4;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int from_lane = 2 * i + (lane >> 4), r = cw * 32 + from_lane;
+    for (int i = 0; i < kRows / 2; ++i) {
+      const int from_lane = 2 * i + (lane >> 4), r = cw * kRows + from_lane;
       const int64_t o = __shfl_sync(0xFFFFFFFFu, off, from_lane);
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                       smem_u32(to + (x >> 3) * 16384 + r * 128 + (((x & 7) ^ (r & 7)) * 16))),
+                       smem_u32(to + (x >> 3) * block + r * 128 + (((x & 7) ^ (r & 7)) * 16))),
                    "l"(from + (o >= 0 ? o : 0) + x * 8), "r"(o >= 0 ? 16 : 0)
                    : "memory");
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    on_way |= name << (4 * ways);
-    ++ways;
-    land(5);
   };
   auto copy_unit = [&](const uint16_t* from, int64_t off) {
     const uint32_t place = unit % L::kRing;
-    if (unit >= L::kRing && !wait(&sm.empty[place], unit / L::kRing - 1)) return false;
-    copy(smem + place * kKvUnit, from, off, place);
+    if (unit >= L::kRing && !warp_wait(&sm.empty[place], unit / L::kRing - 1)) return false;
+    copy(std::integral_constant<int, 128>(), smem + L::kUnits + place * kKvUnit, 16384, from, off);
+    arrive(&sm.full[place]);
     ++unit;
     return true;
   };
   bool ok = true;
 #pragma unroll 1
   for (uint32_t job_use = 0;; ++job_use) {
-    if (!wait(&sm.job_full[job_use & 1], job_use >> 1)) ok = false;
+    ok = warp_wait(&sm.job_full[job_use & 1], job_use >> 1);
     if (!ok) break;
     const Job job = sm.job[job_use & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.job_empty[job_use & 1]);
     if (!job.live) break;
     if (job.n == 0) continue;
-    const bool two = L::kQSlots == 2 && job.two;
+    const bool two = R == 256 && job.two;
     const int32_t* table = a.table + static_cast<int64_t>(job.tile.b) * a.table_stride;
     // the row of the cache in this lane's place of a tile, -1: none; and its page
     auto key_of = [&](int j) {
@@ -577,42 +554,23 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvSmall& sm,
     };
     auto page_of = [&](int32_t key) { return a.page_shift >= 0 ? key >> a.page_shift : key / a.cache.page_size; };
     int32_t key = key_of(0), page = key >= 0 ? table[page_of(key)] : 0;
-    for (int w = 0; w < (two ? 2 : 1); ++w, ++q_use) {
+    for (int w = 0; w < (two ? 2 : 1) && ok; ++w, ++q_use) {
       const uint32_t slot = q_use % L::kQSlots;
-      if (q_use >= L::kQSlots && !wait(&sm.q_empty[slot], q_use / L::kQSlots - 1)) ok = false;
+      ok = q_use < L::kQSlots || warp_wait(&sm.q_empty[slot], q_use / L::kQSlots - 1);
       if (!ok) break;
-      const int32_t i = w * 128 + cw * 32 + lane, r = job.tile.base + i;
+      const int32_t i = w * 128 + cw * (L::kQRows / 4) + lane, r = job.tile.base + i;
       int64_t off = -1;
-      if (i < job.tile.rows) {
+      if (lane < L::kQRows / 4 && i < job.tile.rows) {
         const int32_t tok = r / a.G;
         off = (job.tile.tok0 + tok) * a.q_st + (job.kh * a.G + r - tok * a.G) * a.q_sh;
       }
-      for (int u = 0; u < L::kKU; ++u) {
-        // the units of a slot make one group: its barrier is told of the last
-        const bool last = u == L::kKU - 1;
-        uint8_t* to = smem + L::kQ + (slot * L::kKU + u) * kKvUnit;
-        const int x = lane & 15;
-#pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
-          const int from_lane = 2 * k + (lane >> 4), rr = cw * 32 + from_lane;
-          const int64_t o = __shfl_sync(0xFFFFFFFFu, off, from_lane);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                           smem_u32(to + (x >> 3) * 16384 + rr * 128 + (((x & 7) ^ (rr & 7)) * 16))),
-                       "l"(a.q + (o >= 0 ? o : 0) + u * 128 + x * 8), "r"(o >= 0 ? 16 : 0)
-                       : "memory");
-        }
-        if (last) {
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          on_way |= (8u + slot) << (4 * ways);
-          ++ways;
-          land(5);
-        }
-      }
+      for (int u = 0; u < L::kKU; ++u)
+        copy(std::integral_constant<int, L::kQRows>(), smem + slot * L::kQSlot + u * 2 * L::kQBlock, L::kQBlock, a.q + u * 128, off);
+      arrive(&sm.q_full[slot]);
     }
-    if (!ok) break;
     int64_t v_off = -1, v_next = -1;
 #pragma unroll 1
-    for (int j = 0; j <= job.n; ++j) {
+    for (int j = 0; j <= job.n && ok; ++j) {
       if (j < job.n) {
         const uint32_t jt = keys_before + j;
         int64_t k_off = -1;
@@ -630,36 +588,33 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvSmall& sm,
         const uint32_t gone = __ballot_sync(0xFFFFFFFFu, missing);
         key = key_of(j + 1);
         page = key >= 0 ? table[page_of(key)] : 0;
-        for (int u = 0; u < L::kKU && ok; ++u) {
-          // Three tiles of keys lie behind the place of `bad` once a unit of this one has a place in the ring:
-          // its softmax is over.
-          if (unit >= L::kRing && !wait(&sm.empty[unit % L::kRing], unit / L::kRing - 1)) ok = false;
-          if (u == 0 && ok && lane == 0) {
-            sm.bad[jt & 3][cw] = gone;
-            mbar_arrive(&sm.noted[jt & 3]);
-          }
-          if (ok) ok = copy_unit(a.cache.k + u * 128, k_off);
-        }
+        // A tile of keys whose notes lay in this place of `bad` is four tiles back: with a place in the ring for a
+        // unit of this tile its softmax is over.
+        ok = unit < L::kRing || warp_wait(&sm.empty[unit % L::kRing], unit / L::kRing - 1);
         if (!ok) break;
+        if (lane == 0) {
+          sm.bad[jt & 3][cw] = gone;
+          mbar_arrive(&sm.noted[jt & 3]);
+        }
+        for (int u = 0; u < L::kKU && ok; ++u) ok = copy_unit(a.cache.k + u * 128, k_off);
       }
       if (two ? j < job.n : j > 0) {
         const int64_t off = two ? v_next : v_off;
         for (int u = 0; u < L::kVU && ok; ++u) ok = copy_unit(a.cache.v + u * 128, off);
-        if (!ok) break;
       }
       v_off = v_next;
     }
     if (!ok) break;
     keys_before += job.n;
   }
-  land(0);
+  asm volatile("cp.async.wait_all;" ::: "memory");
   return ok;
 }
 
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(kKvThreads, 1)
     kv_attention_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ KvPlan p, int64_t jobs) {
-  using L = KvLayout<D>;
+  using L = KvLayout<D, R>;
   // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
   extern __shared__ __align__(1024) uint8_t smem[];
   KvSmall& sm = *reinterpret_cast<KvSmall*>(smem + L::kSmall);
@@ -671,15 +626,17 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   }
   if (warp == kMmaWarp) {
     if (lane == 0) {
-      for (int i = 0; i < 4; ++i) {
-        mbar_init(&sm.full[i], 4);
+      for (int i = 0; i < L::kRing; ++i) {
+        mbar_init(&sm.full[i], 128);
         mbar_init(&sm.empty[i], 1);
+      }
+      for (int i = 0; i < 4; ++i) {
         mbar_init(&sm.noted[i], 4);
         mbar_init(&sm.decided[0][i], 1);
         mbar_init(&sm.decided[1][i], 1);
       }
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&sm.q_full[i], 4);
+        mbar_init(&sm.q_full[i], 128);
         mbar_init(&sm.q_empty[i], 1);
         mbar_init(&sm.s_full[i], 1);
         mbar_init(&sm.p_full[i], 4);
@@ -704,13 +661,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   bool ok = true;
   if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    ok = soft_jobs<D>(a, p, sm, tmem);
+    ok = soft_jobs<D, R>(a, p, sm, tmem);
     tc_fence_before();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kMmaWarp) {
       if (elect_one()) {
-        ok = mma_jobs<D>(sm, smem_u32(smem), tmem);
+        ok = mma_jobs<D, R>(sm, smem_u32(smem), tmem);
         // the end of every product: tensor memory may be given back
         tc_commit(&sm.drain);
         ok = mbar_wait_near(&sm.drain, 0) && ok;
@@ -723,7 +680,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         Job j;
         j.live = 0;
         if (id < jobs) {
-          j = make_job<D>(a, p, id);
+          j = make_job<D, R>(a, p, id);
           if (j.tile.rows <= 0) continue;
         }
         if (use >= 2) ok = warp_wait(&sm.job_empty[use & 1], (use >> 1) - 1);
@@ -737,7 +694,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         if (!j.live) break;
       }
     } else if (warp >= kCopyWarp) {
-      ok = copy_jobs<D>(a, sm, smem);
+      ok = copy_jobs<D, R>(a, sm, smem);
     }
   }
   if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
@@ -817,7 +774,9 @@ __global__ void __launch_bounds__(128, kFew ? 12 : 4) kv_join_kernel(const __gri
 // off towards 0: fp4_attention.cu has the figures).
 KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows, int32_t window, int32_t first, int32_t words) {
   KvPlan p;
-  const int R = D == 128 ? 256 : 128, G = H / KH;
+  const int G = H / KH;
+  const int64_t rows = (T + B - 1) / B * G;  // of an average request and key head
+  const int R = p.R = rows <= 32 ? 32 : rows <= 64 && D == 512 ? 64 : D == 128 ? 256 : 128;
   const int64_t pad = kv_tile_pad(G, R);
   p.tiles = static_cast<int>((T * G + static_cast<int64_t>(B) * pad) / R);
   int64_t busy = (T * G + R - 1) / R;
@@ -845,22 +804,31 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
   return p;
 }
 
-template <int D>
-cudaError_t launch(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s) {
-  const KvPlan p = plan_kv(a.T, a.B, a.H, a.KH, D, a.max_rows, a.window, a.first, a.words);
+template <int D, int R>
+cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = set_max_smem_once<kv_attention_kernel<D>>(kv_smem_bytes<D>())) != cudaSuccess) return e;
-  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * a.KH * KvLayout<D>::kHalves;
+  if ((e = set_max_smem_once<kv_attention_kernel<D, R>>(kv_smem_bytes<D, R>())) != cudaSuccess) return e;
+  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * a.KH * KvLayout<D, R>::kHalves;
   if (jobs == 0) return cudaSuccess;
-  e = launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(jobs < sms ? jobs : sms)), dim3(kKvThreads), kv_smem_bytes<D>(), use_pdl, s, a,
-                p, jobs);
+  e = launch_ex(kv_attention_kernel<D, R>, dim3(static_cast<unsigned>(jobs < sms ? jobs : sms)), dim3(kKvThreads), kv_smem_bytes<D, R>(), use_pdl,
+                s, a, p, jobs);
   if (e != cudaSuccess || p.splits == 1) return e;
   const int64_t ctas = (a.T * a.H * (D / 128) + 3) / 4;
   return p.splits <= 4 ? launch_ex(kv_join_kernel<D, true>, dim3(static_cast<unsigned>(ctas)), dim3(128), 0, true, s, a, p.splits)
                        : launch_ex(kv_join_kernel<D, false>, dim3(static_cast<unsigned>(ctas)), dim3(128), 0, true, s, a, p.splits);
+}
+
+template <int D>
+cudaError_t launch_d(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s) {
+  const KvPlan p = plan_kv(a.T, a.B, a.H, a.KH, D, a.max_rows, a.window, a.first, a.words);
+  if (p.R == 32) return launch<D, 32>(a, p, use_pdl, s);
+  if constexpr (D == 512) {
+    if (p.R == 64) return launch<D, 64>(a, p, use_pdl, s);
+  }
+  return launch<D, D == 128 ? 256 : 128>(a, p, use_pdl, s);
 }
 
 }  // namespace
@@ -872,7 +840,7 @@ int64_t kv_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t KH, int3
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s) {
-  return a.cache.D == 128 ? launch<128>(a, use_pdl, s) : a.cache.D == 256 ? launch<256>(a, use_pdl, s) : launch<512>(a, use_pdl, s);
+  return a.cache.D == 128 ? launch_d<128>(a, use_pdl, s) : a.cache.D == 256 ? launch_d<256>(a, use_pdl, s) : launch_d<512>(a, use_pdl, s);
 }
 
 }  // namespace ckv

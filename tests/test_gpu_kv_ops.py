@@ -45,7 +45,10 @@ def _angles(n, R):
 
 
 def _cache(pages, ps, KH, D, layout, fill=0.0):
-    """A cache [pages, ps, KH, D]: rows outermost, heads outermost, or keys and values interleaved in one tensor."""
+    """A cache [pages, ps, KH, D]: rows outermost, heads outermost, keys and values interleaved in one tensor, or rows
+    that begin at odd places of 16 bytes."""
+    if layout == "padded":
+        return torch.full((pages, ps, KH, D + 8), fill, dtype=torch.bfloat16, device="cuda")[..., 8:]
     if layout == "heads":
         return torch.full((pages, KH, ps, D), fill, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
     if layout == "halves":
@@ -59,7 +62,7 @@ def _cache(pages, ps, KH, D, layout, fill=0.0):
     (128, 4, 2, 11, 44, 24, False), (256, 3, 3, 5, 30, 98, False), (512, 7, 7, 6, 512, 0, False), (512, 2, 1, 5, 6, 2, True),
     (128, 24, 8, 700, 128, 0, False), (256, 1, 1, 1, 0, 0, False), (512, 130, 2, 3, 10, 500, False)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("layout", ["rows", "heads", "halves"])
+@pytest.mark.parametrize("layout", ["rows", "heads", "halves", "padded"])
 def test_append(ck, D, H, KH, T, R, at, pairs, dtype, layout):
     g = torch.Generator(device="cuda").manual_seed(D + T + R)
     ps, pages = (7, -(-T // 7) + 2)
@@ -247,7 +250,7 @@ SIZES = [
 @pytest.mark.parametrize("D,H,KH,n,before,ps", SIZES)
 @pytest.mark.parametrize("window,first", [(0, 0), (1, 0), (100, 0), (128, 4), (37, 150), (5000, 3)])
 def test_window(ck, D, H, KH, n, before, ps, window, first):
-    s = Step(D, H, KH, n, before, ps, window, first, layout=("rows", "heads", "halves")[(window + D) % 3], shared=D == 512 and window != 1,
+    s = Step(D, H, KH, n, before, ps, window, first, layout=("rows", "heads", "halves", "padded")[(window + n[0]) % 4], shared=D == 512 and window != 1,
              sink=first > 0, seed=D + window)
     out, lse, err = s.run(ck)
     assert int(err) == 0
@@ -257,7 +260,7 @@ def test_window(ck, D, H, KH, n, before, ps, window, first):
 @pytest.mark.parametrize("D,H,KH,n,before,ps", SIZES)
 @pytest.mark.parametrize("window,first", [(0, 0), (64, 3), (300, 0)])
 def test_tree(ck, D, H, KH, n, before, ps, window, first):
-    s = Step(D, H, KH, n, before, ps, window, first, tree=True, layout=("rows", "heads")[D % 3 % 2], sink=window == 64, seed=D + window,
+    s = Step(D, H, KH, n, before, ps, window, first, tree=True, layout=("rows", "padded")[before[0] % 2], sink=window == 64, seed=D + window,
              words=5 if D == 256 else 0)
     out, lse, err = s.run(ck)
     assert int(err) == 0
