@@ -28,7 +28,8 @@ BINDING_OF = os.path.join(LIBDIR, "ckv_binding.txt")  # the torch that it was bu
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 CUDA_SOURCES = ["kpool.cu", "c128.cu", "prefill_tma.cu", "planner_device.cu", "validate.cu", "probe.cu",
                 "step_maps.cu", "norm_rope.cu", "fp4_rows.cu", "fp4_attention.cu",
-                "fp4_attention_rows.cu", "kv_append.cu", "kv_attention.cu", "tree_masks.cu",
+                "fp4_attention_rows.cu", "kv_append.cu", "kv_attention.cu", "kv_attention_few.cu",
+                "tree_masks.cu",
                 "merge_attention.cu", "capi.cu"]
 CXX_SOURCES = ["planner.cpp"]
 BINDING_SOURCE = "binding.cpp"  # CPython module over torch tensors, linked against the library

@@ -39,6 +39,33 @@ __device__ __forceinline__ float round_bf16(float x) {
   return __bfloat162float(__float2bfloat16_rn(x));
 }
 
+// Reduce n values per lane over the warp's lanes; afterwards lane l holds the
+// result of value (l * n / 32): halves the values while lanes differ in a bit.
+template <int n, bool kMax>
+__device__ __forceinline__ float reduce_columns(float (&v)[n], int lane) {
+  int width = n;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (width > 1) {
+      const int half = width / 2;
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) {
+        if (i < half) {
+          const float mine = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
+          const float got = __shfl_xor_sync(0xFFFFFFFFu, send, o);
+          v[i] = kMax ? fmaxf(mine, got) : mine + got;
+        }
+      }
+      width = half;
+    } else {
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+      v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+    }
+  }
+  return v[0];
+}
+
 // ---- memory access with cache hints ---------------------------------------
 // Streaming, read-only data (read once): do not allocate it in L1.
 __device__ __forceinline__ float4 ld_stream_f4(const float* p) {

@@ -245,6 +245,7 @@ struct KvAttentionArgs {
   int64_t T;
   int32_t H, KH, G, B, max_rows, page_shift;
   int32_t window, first, words;
+  int32_t same;  // one row is key and value, and the form keeps its units for both products
   float softmax_scale;
 };
 constexpr int kKvMaxSplits = 160, kKvMaxRange = 1 << 17;

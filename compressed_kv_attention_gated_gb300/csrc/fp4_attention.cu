@@ -105,33 +105,6 @@ constexpr int smem_bytes() {
   return Layout<D, R>::kSmall + static_cast<int>(sizeof(Small<R>)) + 1024;  // 1024: alignment of the swizzled tiles
 }
 
-// Reduce n values per lane over the warp's lanes; afterwards lane l holds the
-// result of value (l * n / 32): halves the values while lanes differ in a bit.
-template <int n, bool kMax>
-__device__ __forceinline__ float reduce_columns(float (&v)[n], int lane) {
-  int width = n;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    if (width > 1) {
-      const int half = width / 2;
-      const bool up = lane & o;
-#pragma unroll
-      for (int i = 0; i < n / 2; ++i) {
-        if (i < half) {
-          const float mine = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
-          const float got = __shfl_xor_sync(0xFFFFFFFFu, send, o);
-          v[i] = kMax ? fmaxf(mine, got) : mine + got;
-        }
-      }
-      width = half;
-    } else {
-      const float got = __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
-      v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
-    }
-  }
-  return v[0];
-}
-
 __device__ __forceinline__ void soft_barrier() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool p) {
   uint32_t r;

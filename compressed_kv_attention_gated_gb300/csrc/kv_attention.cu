@@ -32,77 +32,46 @@
 // Few tiles with many keys are split into ranges of keys; their results (fp32, and lse) go through
 // the workspace and are joined by a second kernel in a fixed order.
 #include <algorithm>
-#include <type_traits>
 
-#include "ckv_tcgen05.cuh"
 #include "kv_attention.cuh"
 
 namespace ckv {
 namespace {
 
-constexpr int kKvKeys = 128, kKvUnit = 32768;  // keys of a tile; bytes of a unit
-constexpr int kKvRoom = 7 * kKvUnit, kKvMaxRing = 6;  // for units and queries; places of the ring
-constexpr float kKvJump = 16.f;                // log2 of the largest weight over its reference
-constexpr int kMmaWarp = 8, kPlanWarp = 9, kCopyWarp = 12, kKvThreads = 512;
 // Registers per thread: 512 x 128 at launch; then 256 x 192 + 256 x 64, the same.
 constexpr int kSoftRegs = 192, kOtherRegs = 64;
 
-// R: rows of a job.  With R = 256 (D = 128) there are two tiles of queries; with fewer than 128 rows the
-// products read past the queries into whatever lies there, for rows that nobody looks at.
-template <int D, int R>
+template <int D_>
 struct KvLayout {
+  static constexpr int D = D_;
+  static constexpr int kRows = D == 128 ? 256 : 128;    // of a job
   static constexpr int kHalves = D == 512 ? 2 : 1;
-  static constexpr int kDV = D / kHalves;                // channels of the output that a CTA has
-  static constexpr int kKU = D / 128, kVU = kDV / 128;   // units of a tile's keys and values
-  static constexpr int kQRows = R < 128 ? R : 128;       // of a slot of queries
-  static constexpr int kQBlock = kQRows * 128;           // 64 channels of them
+  static constexpr int kDV = D / kHalves;               // channels of the output that a CTA has
+  static constexpr int kKU = D / 128, kVU = kDV / 128;  // units of a tile's keys and values
+  static constexpr int kQRows = 128;                    // of a slot of queries
+  static constexpr int kQBlock = kQRows * 128;          // 64 channels of them
   static constexpr int kQSlot = kQBlock * (D / 64);
-  static constexpr int kQSlots = R == 256 || kQSlot <= 16384 ? 2 : 1;
-  static constexpr int kRing = (kKvRoom - kQSlots * kQSlot) / kKvUnit;
+  static constexpr int kQSlots = D == 128 ? 2 : 1;
+  static constexpr int kRing = 7 - kQSlots * kKU;
   static constexpr int kUnits = kQSlots * kQSlot;  // where the ring begins, behind the queries
   static constexpr int kSmall = kUnits + kRing * kKvUnit;
-  static_assert(kRing >= 3 && kRing <= kKvMaxRing, "shared memory");
-  static constexpr int kTmemO = 0, kTmemS = 256;        // O: 256 columns; S: two buffers of 128, P over the first half of each
+  static constexpr int kTmemO = 0, kTmemS = 256;  // O: 256 columns; S: two buffers of 128, P over the first half of each
 };
 
-struct Job {
-  KvTile tile;
-  int32_t kh, half, split;
-  int32_t first, low;  // the list of keys: rows 0 .. first - 1, then low, low + 1, ...
-  int32_t v0, v1;      // of the list
-  int32_t n;           // tiles of keys
-  int32_t two;         // each softmax group has a tile of rows of its own
-  int32_t live;        // 0: no more jobs
-};
-
-// Barriers.  `Uses` are numbered from 0 over the whole kernel, so that everyone counts alike.
-//   full, empty     of a unit of the ring: 128 copying threads; the products that read it
-//   q_full, q_empty of a slot of queries, alike
-//   s_full[w]       scores of group w are there (and all products issued before them are done)
-//   p_full[w]       weights of group w are there: 4 warps
-//   o_full[w]       every product of a job that group w waits for: once per job with keys
-//   noted           missing keys of a tile are noted: 4 copying warps
-// and where the groups share the rows:
-//   decided[w][q]   warp q of group w knows the references under which its tile is taken
-//   pv_done[w]      second product of a tile of group w
-//   met             both groups have got there: 8 warps, twice per job
-struct KvSmall {
-  uint64_t full[kKvMaxRing], empty[kKvMaxRing], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], job_full[2], job_empty[2], noted[4];
-  uint64_t decided[2][4], pv_done[2], met, drain;
-  uint32_t tmem;
-  Job job[2];
-  alignas(16) uint32_t bad[4][4];  // a bit per key of a tile whose page is not there (ring over tiles of keys)
-  float ref[128];                  // references of the shared rows
+// Beside the common ones (s_full[w], p_full[w] and, with a tile of rows of its own, o_full[w] are group w's;
+// p_full: 4 warps), where the groups share the rows:
+struct KvSmall : KvCommon {
+  uint64_t decided[2][4];  // warp q of group w knows the references under which its tile is taken
+  uint64_t met;            // both groups have got there: 8 warps, twice per job
+  float ref[128];          // references of the shared rows
   float sum[2][128];
 };
 
-template <int D, int R>
+template <int D>
 constexpr int kv_smem_bytes() {
-  return KvLayout<D, R>::kSmall + static_cast<int>(sizeof(KvSmall));
+  return KvLayout<D>::kSmall + static_cast<int>(sizeof(KvSmall));
 }
-static_assert(kKvRoom + sizeof(KvSmall) <= 227 * 1024, "shared memory");
-
-__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn_major) { return idesc_f16(n, false, b_mn_major) | (1u << 7) | (1u << 10); }
+static_assert(kv_smem_bytes<128>() <= 227 * 1024 && kv_smem_bytes<256>() <= 227 * 1024 && kv_smem_bytes<512>() <= 227 * 1024, "shared memory");
 
 // 32 columns of the warp's lanes; the values are there after tc_wait_ld() and settled32().
 __device__ __forceinline__ void tmem_ld32_async(uint32_t addr, float* v) {
@@ -136,59 +105,10 @@ __device__ __forceinline__ uint32_t bits_between(int32_t x0, int32_t x1) {
   return static_cast<uint32_t>(((1ull << hi) - 1ull) & ~((1ull << lo) - 1ull));
 }
 
-// Wait for use `n` of a barrier, by a whole warp.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t n) { return __all_sync(0xFFFFFFFFu, mbar_wait_near(bar, n & 1u)); }
-
-struct KvPlan {
-  int R;       // rows of a tile
-  int tiles;   // bound of the number of tiles
-  int splits;  // ranges of keys
-  int chunk;   // keys of a range (a multiple of kKvKeys); the last range takes all that are left
-};
-
-// ---------------------------------------------------------------------- jobs
-// Job `id`, by one converged warp; rows <= 0 when there is nothing to do in it.
-template <int D, int R>
-__device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& p, int64_t id) {
-  using L = KvLayout<D, R>;
-  const int lane = threadIdx.x & 31;
-  Job j;
-  j.half = static_cast<int32_t>(id % L::kHalves);
-  id /= L::kHalves;
-  j.kh = static_cast<int32_t>(id % a.KH);
-  id /= a.KH;
-  j.split = static_cast<int32_t>(id % p.splits);
-  j.tile = kv_find_tile(a, static_cast<int32_t>(id / p.splits), R);
-  j.live = 1;
-  j.two = R == 256 && j.tile.rows > 128;
-  j.first = j.low = j.v0 = j.v1 = j.n = 0;
-  if (j.tile.rows <= 0) return j;
-  // what its tokens see together
-  const int32_t t0 = j.tile.tok0 + j.tile.base / a.G, t1 = j.tile.tok0 + (j.tile.base + j.tile.rows - 1) / a.G;
-  int32_t low = INT32_MAX, end = -1;
-  for (int32_t t = t0 + lane; t <= t1; t += 32) {
-    const Seen s = seen_by(a, t);
-    if (s.c < 0) continue;
-    end = max(end, s.end);
-    if (s.end > 0) low = min(low, s.low);  // a token that sees nothing does not widen the list
-  }
-  low = __reduce_min_sync(0xFFFFFFFFu, low);
-  end = __reduce_max_sync(0xFFFFFFFFu, end);
-  if (end < 0) j.tile.rows = 0;  // every token is left as it is
-  end = max(end, 0);
-  j.low = min(low, end);
-  j.first = min(a.first, j.low);
-  const int32_t count = end - j.low + j.first;
-  j.v0 = static_cast<int32_t>(min(static_cast<int64_t>(j.split) * p.chunk, static_cast<int64_t>(count)));
-  j.v1 = j.split == p.splits - 1 ? count : min(count, j.v0 + p.chunk);
-  j.n = (j.v1 - j.v0 + kKvKeys - 1) / kKvKeys;
-  return j;
-}
-
 // The part of the softmax warps: see the roles above.
-template <int D, int R>
+template <int D>
 __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan& p, KvSmall& sm, uint32_t tmem) {
-  using L = KvLayout<D, R>;
+  using L = KvLayout<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, w = warp >> 2, row = threadIdx.x & 127;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128;
@@ -200,7 +120,7 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
     if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
     const Job& job = sm.job[job_use & 1];
     if (!job.live) return true;
-    const bool two = R == 256 && job.two;
+    const bool two = L::kRows == 256 && job.two;
     const int32_t n = job.n, kh = job.kh, half = job.half, range = job.split;
     const int32_t r = job.tile.base + (two ? w * 128 : 0) + row;
     int32_t t = 0, flat = -1;
@@ -218,7 +138,7 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
 #pragma unroll 1
     for (int j = two ? 0 : w; j < n; j += step) {
       const uint32_t jt = keys_before + j;
-      if (!warp_wait(&sm.s_full[w], s_use++) || !warp_wait(&sm.noted[jt & 3], jt >> 2)) return false;
+      if (!warp_wait(&sm.s_full[w], s_use++) || !warp_wait(&sm.noted[jt % kKvNotes], jt / kKvNotes)) return false;
       tc_fence_after();
       if (any) {
         float z[128];
@@ -228,7 +148,7 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
         const int32_t v = job.v0 + j * kKvKeys, here = min(kKvKeys, job.v1 - v);
         const int32_t head = job.first - v, k0 = job.low - head;  // places of first rows; the row of place 0, were it none of them
         const bool whole = flat < 0 || (here == kKvKeys && k0 + kKvKeys <= see.c && (head <= 0 ? k0 : job.low) >= see.low);
-        const uint4 gone = *reinterpret_cast<const uint4*>(sm.bad[jt & 3]);
+        const uint4 gone = *reinterpret_cast<const uint4*>(sm.bad[jt % kKvNotes]);
         uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
         const bool masks = __any_sync(0xFFFFFFFFu, !whole) || (gone.x | gone.y | gone.z | gone.w);
         if (masks) {
@@ -406,9 +326,9 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
 }
 
 // One thread: the products, in the order of their units.
-template <int D, int R>
+template <int D>
 __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tmem) {
-  using L = KvLayout<D, R>;
+  using L = KvLayout<D>;
   constexpr uint32_t kIdescS = idesc_bf16(128, false), kIdescO = idesc_bf16(128, true);
   uint32_t unit = 0, q_use = 0, p_use[2] = {0, 0};
   auto wait = [](uint64_t* bar, uint32_t n) { return mbar_wait_near(bar, n & 1u); };
@@ -441,7 +361,7 @@ __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tm
     const Job& job = sm.job[job_use & 1];
     if (!job.live) return true;
     const int n = job.n;
-    const bool two = R == 256 && job.two;
+    const bool two = L::kRows == 256 && job.two;
     mbar_arrive(&sm.job_empty[job_use & 1]);
     if (n == 0) continue;
     if (two) {
@@ -505,116 +425,10 @@ __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tm
   }
 }
 
-// Four warps: queries, keys and values of the jobs, unit by unit, as many ahead as the ring has places.
-// Every thread's copies arrive at the unit's barrier by themselves.
-template <int D, int R>
-__device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvSmall& sm, uint8_t* smem) {
-  using L = KvLayout<D, R>;
-  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - kCopyWarp, x = lane & 15;
-  uint32_t unit = 0, q_use = 0, keys_before = 0;
-  auto arrive = [](uint64_t* bar) { asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory"); };
-  // kRows / 4 rows x 256 bytes by this warp, 16 lanes to a row, into blocks of 64 channels: the row in lane i
-  // begins at from + off elements (off < 0: zeros)
-  auto copy = [&](auto rows, uint8_t* to, int block, const uint16_t* from, int64_t off) {
-    constexpr int kRows = decltype(rows)::value / 4;
-#pragma unroll
-    for (int i = 0; i < kRows / 2; ++i) {
-      const int from_lane = 2 * i + (lane >> 4), r = cw * kRows + from_lane;
-      const int64_t o = __shfl_sync(0xFFFFFFFFu, off, from_lane);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                       smem_u32(to + (x >> 3) * block + r * 128 + (((x & 7) ^ (r & 7)) * 16))),
-                   "l"(from + (o >= 0 ? o : 0) + x * 8), "r"(o >= 0 ? 16 : 0)
-                   : "memory");
-    }
-  };
-  auto copy_unit = [&](const uint16_t* from, int64_t off) {
-    const uint32_t place = unit % L::kRing;
-    if (unit >= L::kRing && !warp_wait(&sm.empty[place], unit / L::kRing - 1)) return false;
-    copy(std::integral_constant<int, 128>(), smem + L::kUnits + place * kKvUnit, 16384, from, off);
-    arrive(&sm.full[place]);
-    ++unit;
-    return true;
-  };
-  bool ok = true;
-#pragma unroll 1
-  for (uint32_t job_use = 0;; ++job_use) {
-    ok = warp_wait(&sm.job_full[job_use & 1], job_use >> 1);
-    if (!ok) break;
-    const Job job = sm.job[job_use & 1];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.job_empty[job_use & 1]);
-    if (!job.live) break;
-    if (job.n == 0) continue;
-    const bool two = R == 256 && job.two;
-    const int32_t* table = a.table + static_cast<int64_t>(job.tile.b) * a.table_stride;
-    // the row of the cache in this lane's place of a tile, -1: none; and its page
-    auto key_of = [&](int j) {
-      const int32_t v = job.v0 + j * kKvKeys + cw * 32 + lane;
-      return j >= job.n || v >= job.v1 ? -1 : v < job.first ? v : job.low + v - job.first;
-    };
-    auto page_of = [&](int32_t key) { return a.page_shift >= 0 ? key >> a.page_shift : key / a.cache.page_size; };
-    int32_t key = key_of(0), page = key >= 0 ? table[page_of(key)] : 0;
-    for (int w = 0; w < (two ? 2 : 1) && ok; ++w, ++q_use) {
-      const uint32_t slot = q_use % L::kQSlots;
-      ok = q_use < L::kQSlots || warp_wait(&sm.q_empty[slot], q_use / L::kQSlots - 1);
-      if (!ok) break;
-      const int32_t i = w * 128 + cw * (L::kQRows / 4) + lane, r = job.tile.base + i;
-      int64_t off = -1;
-      if (lane < L::kQRows / 4 && i < job.tile.rows) {
-        const int32_t tok = r / a.G;
-        off = (job.tile.tok0 + tok) * a.q_st + (job.kh * a.G + r - tok * a.G) * a.q_sh;
-      }
-      for (int u = 0; u < L::kKU; ++u)
-        copy(std::integral_constant<int, L::kQRows>(), smem + slot * L::kQSlot + u * 2 * L::kQBlock, L::kQBlock, a.q + u * 128, off);
-      arrive(&sm.q_full[slot]);
-    }
-    int64_t v_off = -1, v_next = -1;
-#pragma unroll 1
-    for (int j = 0; j <= job.n && ok; ++j) {
-      if (j < job.n) {
-        const uint32_t jt = keys_before + j;
-        int64_t k_off = -1;
-        v_next = -1;
-        bool missing = false;
-        if (key >= 0) {
-          const int32_t at = key - page_of(key) * a.cache.page_size;
-          if (page >= 0 && page < a.cache.num_pages) {
-            k_off = page * a.cache.k_stride_page + at * a.cache.k_stride_row + job.kh * a.cache.k_stride_head;
-            v_next = page * a.cache.v_stride_page + at * a.cache.v_stride_row + job.kh * a.cache.v_stride_head + job.half * L::kDV;
-          } else {
-            missing = true;
-          }
-        }
-        const uint32_t gone = __ballot_sync(0xFFFFFFFFu, missing);
-        key = key_of(j + 1);
-        page = key >= 0 ? table[page_of(key)] : 0;
-        // A tile of keys whose notes lay in this place of `bad` is four tiles back: with a place in the ring for a
-        // unit of this tile its softmax is over.
-        ok = unit < L::kRing || warp_wait(&sm.empty[unit % L::kRing], unit / L::kRing - 1);
-        if (!ok) break;
-        if (lane == 0) {
-          sm.bad[jt & 3][cw] = gone;
-          mbar_arrive(&sm.noted[jt & 3]);
-        }
-        for (int u = 0; u < L::kKU && ok; ++u) ok = copy_unit(a.cache.k + u * 128, k_off);
-      }
-      if (two ? j < job.n : j > 0) {
-        const int64_t off = two ? v_next : v_off;
-        for (int u = 0; u < L::kVU && ok; ++u) ok = copy_unit(a.cache.v + u * 128, off);
-      }
-      v_off = v_next;
-    }
-    if (!ok) break;
-    keys_before += job.n;
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  return ok;
-}
-
-template <int D, int R>
+template <int D>
 __global__ void __launch_bounds__(kKvThreads, 1)
     kv_attention_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ KvPlan p, int64_t jobs) {
-  using L = KvLayout<D, R>;
+  using L = KvLayout<D>;
   // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
   extern __shared__ __align__(1024) uint8_t smem[];
   KvSmall& sm = *reinterpret_cast<KvSmall*>(smem + L::kSmall);
@@ -630,8 +444,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_init(&sm.full[i], 128);
         mbar_init(&sm.empty[i], 1);
       }
+      for (int i = 0; i < kKvNotes; ++i) mbar_init(&sm.noted[i], 4);
       for (int i = 0; i < 4; ++i) {
-        mbar_init(&sm.noted[i], 4);
         mbar_init(&sm.decided[0][i], 1);
         mbar_init(&sm.decided[1][i], 1);
       }
@@ -661,13 +475,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   bool ok = true;
   if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    ok = soft_jobs<D, R>(a, p, sm, tmem);
+    ok = soft_jobs<D>(a, p, sm, tmem);
     tc_fence_before();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kMmaWarp) {
       if (elect_one()) {
-        ok = mma_jobs<D, R>(sm, smem_u32(smem), tmem);
+        ok = mma_jobs<D>(sm, smem_u32(smem), tmem);
         // the end of every product: tensor memory may be given back
         tc_commit(&sm.drain);
         ok = mbar_wait_near(&sm.drain, 0) && ok;
@@ -675,26 +489,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       }
       __syncwarp();
     } else if (warp == kPlanWarp) {
-      uint32_t use = 0;
-      for (int64_t id = blockIdx.x; ok; id += gridDim.x) {
-        Job j;
-        j.live = 0;
-        if (id < jobs) {
-          j = make_job<D, R>(a, p, id);
-          if (j.tile.rows <= 0) continue;
-        }
-        if (use >= 2) ok = warp_wait(&sm.job_empty[use & 1], (use >> 1) - 1);
-        if (!ok) break;
-        if (lane == 0) {
-          sm.job[use & 1] = j;
-          mbar_arrive(&sm.job_full[use & 1]);
-        }
-        __syncwarp();
-        ++use;
-        if (!j.live) break;
-      }
+      ok = plan_jobs<L>(a, p, sm, jobs, [](const Job&, uint32_t) {});
     } else if (warp >= kCopyWarp) {
-      ok = copy_jobs<D, R>(a, sm, smem);
+      ok = copy_jobs<L>(a, sm, smem);
     }
   }
   if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
@@ -776,7 +573,7 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
   KvPlan p;
   const int G = H / KH;
   const int64_t rows = (T + B - 1) / B * G;  // of an average request and key head
-  const int R = p.R = rows <= 32 ? 32 : rows <= 64 && D == 512 ? 64 : D == 128 ? 256 : 128;
+  const int R = p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : D == 128 ? 256 : 128;
   const int64_t pad = kv_tile_pad(G, R);
   p.tiles = static_cast<int>((T * G + static_cast<int64_t>(B) * pad) / R);
   int64_t busy = (T * G + R - 1) / R;
@@ -804,18 +601,20 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
   return p;
 }
 
-template <int D, int R>
+template <int D>
 cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = set_max_smem_once<kv_attention_kernel<D, R>>(kv_smem_bytes<D, R>())) != cudaSuccess) return e;
-  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * a.KH * KvLayout<D, R>::kHalves;
-  if (jobs == 0) return cudaSuccess;
-  e = launch_ex(kv_attention_kernel<D, R>, dim3(static_cast<unsigned>(jobs < sms ? jobs : sms)), dim3(kKvThreads), kv_smem_bytes<D, R>(), use_pdl,
-                s, a, p, jobs);
-  if (e != cudaSuccess || p.splits == 1) return e;
+  if ((e = set_max_smem_once<kv_attention_kernel<D>>(kv_smem_bytes<D>())) != cudaSuccess) return e;
+  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * a.KH * KvLayout<D>::kHalves;
+  return launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(jobs < sms ? jobs : sms)), dim3(kKvThreads), kv_smem_bytes<D>(), use_pdl,
+                   s, a, p, jobs);
+}
+
+template <int D>
+cudaError_t launch_join(const KvAttentionArgs& a, const KvPlan& p, cudaStream_t s) {
   const int64_t ctas = (a.T * a.H * (D / 128) + 3) / 4;
   return p.splits <= 4 ? launch_ex(kv_join_kernel<D, true>, dim3(static_cast<unsigned>(ctas)), dim3(128), 0, true, s, a, p.splits)
                        : launch_ex(kv_join_kernel<D, false>, dim3(static_cast<unsigned>(ctas)), dim3(128), 0, true, s, a, p.splits);
@@ -824,11 +623,9 @@ cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cuda
 template <int D>
 cudaError_t launch_d(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s) {
   const KvPlan p = plan_kv(a.T, a.B, a.H, a.KH, D, a.max_rows, a.window, a.first, a.words);
-  if (p.R == 32) return launch<D, 32>(a, p, use_pdl, s);
-  if constexpr (D == 512) {
-    if (p.R == 64) return launch<D, 64>(a, p, use_pdl, s);
-  }
-  return launch<D, D == 128 ? 256 : 128>(a, p, use_pdl, s);
+  if (p.tiles == 0) return cudaSuccess;
+  const cudaError_t e = p.R <= 64 ? launch_kv_attention_few(a, p, use_pdl, s) : launch<D>(a, p, use_pdl, s);
+  return e != cudaSuccess || p.splits == 1 ? e : launch_join<D>(a, p, s);
 }
 
 }  // namespace

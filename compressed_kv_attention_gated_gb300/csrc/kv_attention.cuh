@@ -1,14 +1,28 @@
-// kv_attention.cuh -- what a token of ckv_kv_attention sees, and where its rows are.
+// kv_attention.cuh -- what the two forms of ckv_kv_attention share: what a token sees, jobs
+// (tiles of rows with the keys that their tokens see together), and the copying of queries,
+// keys and values into shared memory.
 #pragma once
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "ckv_device.cuh"
 #include "ckv_launch.h"
 #include "ckv_launch_util.cuh"
+#include "ckv_tcgen05.cuh"
 
 namespace ckv {
+
+// How a call is cut up (kv_attention.cu).
+struct KvPlan {
+  int R;       // rows of a tile: 16, 32 or 64 (keys on the M side), 128 or 256 (rows on the M side)
+  int tiles;   // bound of the number of tiles
+  int splits;  // ranges of keys
+  int chunk;   // keys of a range (a multiple of kKvKeys); the last range takes all that are left
+};
+cudaError_t launch_kv_attention_few(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cudaStream_t s);
+
 namespace {
 
 constexpr float kKvLn2 = 0.69314718055994531f;
@@ -86,6 +100,210 @@ __device__ __forceinline__ KvTile kv_find_tile(const KvAttentionArgs& a, int32_t
   t.rows = base < 0 || left <= 0 ? 0 : static_cast<int32_t>(left < R ? left : R);  // base < 0: row_start does not begin with 0
   t.base = static_cast<int32_t>(base);
   return t;
+}
+
+constexpr int kKvKeys = 128, kKvUnit = 32768;  // keys of a tile; bytes of a unit
+constexpr int kKvMaxRing = 6, kKvNotes = 8;    // places of the ring; tiles of keys whose missing keys are kept
+constexpr float kKvJump = 16.f;                // log2 of the largest weight over its reference
+constexpr int kMmaWarp = 8, kPlanWarp = 9, kCopyWarp = 12, kKvThreads = 512;
+
+struct Job {
+  KvTile tile;
+  int32_t kh, half, split;
+  int32_t first, low;  // the list of keys: rows 0 .. first - 1, then low, low + 1, ...
+  int32_t v0, v1;      // of the list
+  int32_t n;           // tiles of keys
+  int32_t two;         // each softmax group has a tile of rows of its own
+  int32_t live;        // 0: no more jobs
+};
+
+
+// Barriers of both forms.  Uses of a barrier are numbered from 0 over the whole kernel, so that everyone
+// counts alike.
+struct KvCommon {
+  uint64_t full[kKvMaxRing], empty[kKvMaxRing];  // of a unit of the ring: 128 copying threads; the products that read it
+  uint64_t q_full[2], q_empty[2];                // of a slot of queries, alike
+  uint64_t s_full[2], p_full[2];                 // of a buffer of scores: the products; the softmax warps that made weights of it
+  uint64_t o_full[2];                            // every product of a job: once per job with keys
+  uint64_t pv_done[2];                           // second products of a tile of keys
+  uint64_t job_full[2], job_empty[2];
+  uint64_t noted[kKvNotes];  // missing keys of a tile of keys are noted: 4 copying warps
+  uint64_t drain;
+  uint32_t tmem;
+  Job job[2];
+  alignas(16) uint32_t bad[kKvNotes][4];  // a bit per key of a tile whose page is not there
+};
+
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn_major) { return idesc_f16(n, false, b_mn_major) | (1u << 7) | (1u << 10); }
+
+// Wait for use `n` of a barrier, by a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t n) { return __all_sync(0xFFFFFFFFu, mbar_wait_near(bar, n & 1u)); }
+
+// ---------------------------------------------------------------------- jobs
+// Job `id`, by one converged warp; rows <= 0 when there is nothing to do in it.
+template <typename L>
+__device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& p, int64_t id) {
+  const int lane = threadIdx.x & 31;
+  Job j;
+  j.half = static_cast<int32_t>(id % L::kHalves);
+  id /= L::kHalves;
+  j.kh = static_cast<int32_t>(id % a.KH);
+  id /= a.KH;
+  j.split = static_cast<int32_t>(id % p.splits);
+  j.tile = kv_find_tile(a, static_cast<int32_t>(id / p.splits), L::kRows);
+  j.live = 1;
+  j.two = L::kRows == 256 && j.tile.rows > 128;
+  j.first = j.low = j.v0 = j.v1 = j.n = 0;
+  if (j.tile.rows <= 0) return j;
+  // what its tokens see together
+  const int32_t t0 = j.tile.tok0 + j.tile.base / a.G, t1 = j.tile.tok0 + (j.tile.base + j.tile.rows - 1) / a.G;
+  int32_t low = INT32_MAX, end = -1;
+  for (int32_t t = t0 + lane; t <= t1; t += 32) {
+    const Seen s = seen_by(a, t);
+    if (s.c < 0) continue;
+    end = max(end, s.end);
+    if (s.end > 0) low = min(low, s.low);  // a token that sees nothing does not widen the list
+  }
+  low = __reduce_min_sync(0xFFFFFFFFu, low);
+  end = __reduce_max_sync(0xFFFFFFFFu, end);
+  if (end < 0) j.tile.rows = 0;  // every token is left as it is
+  end = max(end, 0);
+  j.low = min(low, end);
+  j.first = min(a.first, j.low);
+  const int32_t count = end - j.low + j.first;
+  j.v0 = static_cast<int32_t>(min(static_cast<int64_t>(j.split) * p.chunk, static_cast<int64_t>(count)));
+  j.v1 = j.split == p.splits - 1 ? count : min(count, j.v0 + p.chunk);
+  j.n = (j.v1 - j.v0 + kKvKeys - 1) / kKvKeys;
+  return j;
+}
+
+// The planning warp: jobs that have something to do, one after the other; more(job, i) adds what a form wants to
+// know of the job in place i.
+template <typename L, typename F>
+__device__ __forceinline__ bool plan_jobs(const KvAttentionArgs& a, const KvPlan& p, KvCommon& sm, int64_t jobs, F&& more) {
+  const int lane = threadIdx.x & 31;
+  uint32_t use = 0;
+  for (int64_t id = blockIdx.x;; id += gridDim.x) {
+    Job j;
+    j.live = 0;
+    if (id < jobs) {
+      j = make_job<L>(a, p, id);
+      if (j.tile.rows <= 0) continue;
+    }
+    if (use >= 2 && !warp_wait(&sm.job_empty[use & 1], (use >> 1) - 1)) return false;
+    if (j.live) more(j, use & 1);
+    if (lane == 0) sm.job[use & 1] = j;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.job_full[use & 1]);
+    ++use;
+    if (!j.live) return true;
+  }
+}
+
+// Four warps: queries, keys and values of the jobs, unit by unit, as many ahead as the ring has places.
+// Every thread's copies arrive at the unit's barrier by themselves.
+template <typename L>
+__device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm, uint8_t* smem) {
+  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - kCopyWarp, x = lane & 15;
+  uint32_t unit = 0, q_use = 0, keys_before = 0;
+  auto arrive = [](uint64_t* bar) { asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory"); };
+  // kRows / 4 rows x 256 bytes by this warp, 16 lanes to a row, into blocks of 64 channels: the row in lane i
+  // begins at from + off elements (off < 0: zeros)
+  auto copy = [&](auto rows, uint8_t* to, int block, const uint16_t* from, int64_t off) {
+    constexpr int kRows = decltype(rows)::value / 4;
+#pragma unroll
+    for (int i = 0; i < kRows / 2; ++i) {
+      const int from_lane = 2 * i + (lane >> 4), r = cw * kRows + from_lane;
+      const int64_t o = __shfl_sync(0xFFFFFFFFu, off, from_lane);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       smem_u32(to + (x >> 3) * block + r * 128 + (((x & 7) ^ (r & 7)) * 16))),
+                   "l"(from + (o >= 0 ? o : 0) + x * 8), "r"(o >= 0 ? 16 : 0)
+                   : "memory");
+    }
+  };
+  auto copy_unit = [&](const uint16_t* from, int64_t off) {
+    const uint32_t place = unit % L::kRing;
+    if (unit >= L::kRing && !warp_wait(&sm.empty[place], unit / L::kRing - 1)) return false;
+    copy(std::integral_constant<int, 128>(), smem + L::kUnits + place * kKvUnit, 16384, from, off);
+    arrive(&sm.full[place]);
+    ++unit;
+    return true;
+  };
+  bool ok = true;
+#pragma unroll 1
+  for (uint32_t job_use = 0;; ++job_use) {
+    ok = warp_wait(&sm.job_full[job_use & 1], job_use >> 1);
+    if (!ok) break;
+    const Job job = sm.job[job_use & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.job_empty[job_use & 1]);
+    if (!job.live) break;
+    if (job.n == 0) continue;
+    const bool two = L::kRows == 256 && job.two;
+    const int32_t* table = a.table + static_cast<int64_t>(job.tile.b) * a.table_stride;
+    // the row of the cache in this lane's place of a tile, -1: none; and its page
+    auto key_of = [&](int j) {
+      const int32_t v = job.v0 + j * kKvKeys + cw * 32 + lane;
+      return j >= job.n || v >= job.v1 ? -1 : v < job.first ? v : job.low + v - job.first;
+    };
+    auto page_of = [&](int32_t key) { return a.page_shift >= 0 ? key >> a.page_shift : key / a.cache.page_size; };
+    int32_t key = key_of(0), page = key >= 0 ? table[page_of(key)] : 0;
+    for (int w = 0; w < (two ? 2 : 1) && ok; ++w, ++q_use) {
+      const uint32_t slot = q_use % L::kQSlots;
+      ok = q_use < L::kQSlots || warp_wait(&sm.q_empty[slot], q_use / L::kQSlots - 1);
+      if (!ok) break;
+      const int32_t i = w * 128 + cw * (L::kQRows / 4) + lane, r = job.tile.base + i;
+      int64_t off = -1;
+      if (lane < L::kQRows / 4 && i < job.tile.rows) {
+        const int32_t tok = r / a.G;
+        off = (job.tile.tok0 + tok) * a.q_st + (job.kh * a.G + r - tok * a.G) * a.q_sh;
+      }
+      for (int u = 0; u < L::kKU; ++u)
+        copy(std::integral_constant<int, L::kQRows>(), smem + slot * L::kQSlot + u * 2 * L::kQBlock, L::kQBlock, a.q + u * 128, off);
+      arrive(&sm.q_full[slot]);
+    }
+    int64_t v_off = -1, v_next = -1;
+#pragma unroll 1
+    for (int j = 0; j <= job.n && ok; ++j) {
+      if (j < job.n) {
+        const uint32_t jt = keys_before + j;
+        int64_t k_off = -1;
+        v_next = -1;
+        bool missing = false;
+        if (key >= 0) {
+          const int32_t at = key - page_of(key) * a.cache.page_size;
+          if (page >= 0 && page < a.cache.num_pages) {
+            k_off = page * a.cache.k_stride_page + at * a.cache.k_stride_row + job.kh * a.cache.k_stride_head;
+            v_next = page * a.cache.v_stride_page + at * a.cache.v_stride_row + job.kh * a.cache.v_stride_head + job.half * L::kDV;
+          } else {
+            missing = true;
+          }
+        }
+        const uint32_t gone = __ballot_sync(0xFFFFFFFFu, missing);
+        key = key_of(j + 1);
+        page = key >= 0 ? table[page_of(key)] : 0;
+        // The tile of keys whose notes lay in this place of `bad` is eight tiles back: with a place in the ring
+        // for a unit of this tile its softmax is over.
+        ok = unit < L::kRing || warp_wait(&sm.empty[unit % L::kRing], unit / L::kRing - 1);
+        if (!ok) break;
+        if (lane == 0) {
+          sm.bad[jt % kKvNotes][cw] = gone;
+          mbar_arrive(&sm.noted[jt % kKvNotes]);
+        }
+        for (int u = 0; u < L::kKU && ok; ++u) ok = copy_unit(a.cache.k + u * 128, k_off);
+      }
+      if (a.same) continue;  // the keys' units are the values'
+      if (two ? j < job.n : j > 0) {
+        const int64_t off = two ? v_next : v_off;
+        for (int u = 0; u < L::kVU && ok; ++u) ok = copy_unit(a.cache.v + u * 128, off);
+      }
+      v_off = v_next;
+    }
+    if (!ok) break;
+    keys_before += job.n;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  return ok;
 }
 
 }  // namespace
