@@ -40,6 +40,7 @@ namespace {
 
 // Registers per thread: 512 x 128 at launch; then 256 x 192 + 256 x 64, the same.
 constexpr int kSoftRegs = 192, kOtherRegs = 64;
+constexpr float kKvMost = 65536.f;  // D = 128: sum of a tile's weights from which on the reference moves
 
 template <int D_>
 struct KvLayout {
@@ -52,24 +53,31 @@ struct KvLayout {
   static constexpr int kQBlock = kQRows * 128;          // 64 channels of them
   static constexpr int kQSlot = kQBlock * (D / 64);
   static constexpr int kQSlots = D == 128 ? 2 : 1;
-  static constexpr int kRing = 7 - kQSlots * kKU;
+  static constexpr int kRing = D == 256 ? 5 : D == 128 ? 4 : 3;
   static constexpr int kUnits = kQSlots * kQSlot;  // where the ring begins, behind the queries
   static constexpr int kSmall = kUnits + kRing * kKvUnit;
   static constexpr int kTmemO = 0, kTmemS = 256;  // O: 256 columns; S: two buffers of 128, P over the first half of each
 };
 
-// Beside the common ones (s_full[w], p_full[w] and, with a tile of rows of its own, o_full[w] are group w's;
-// p_full: 4 warps), where the groups share the rows:
+// What a job's rows see, by the planning warp.
+template <int R>
+struct SeenRows {
+  int32_t c[R], low[R], end[R];
+};
+
+// Beside the common ones (s_full[w], p_full[w], o_full[w] and pv_done[w] are group w's; p_full: 4 warps):
+template <int D>
 struct KvSmall : KvCommon {
-  uint64_t decided[2][4];  // warp q of group w knows the references under which its tile is taken
-  uint64_t met;            // both groups have got there: 8 warps, twice per job
-  float ref[128];          // references of the shared rows
+  uint64_t decided[2][4];         // D > 128: warp q of group w knows the references under which its tile is taken
+  uint64_t met;                   // both groups have got there: 8 warps, twice per job of shared rows
+  float ref[D == 128 ? 2 : 1][128];  // references of shared rows (each group's own at D = 128)
   float sum[2][128];
+  SeenRows<D == 128 ? KvLayout<D>::kRows : 1> rows[2];
 };
 
 template <int D>
 constexpr int kv_smem_bytes() {
-  return KvLayout<D>::kSmall + static_cast<int>(sizeof(KvSmall));
+  return KvLayout<D>::kSmall + static_cast<int>(sizeof(KvSmall<D>));
 }
 static_assert(kv_smem_bytes<128>() <= 227 * 1024 && kv_smem_bytes<256>() <= 227 * 1024 && kv_smem_bytes<512>() <= 227 * 1024, "shared memory");
 
@@ -105,38 +113,203 @@ __device__ __forceinline__ uint32_t bits_between(int32_t x0, int32_t x1) {
   return static_cast<uint32_t>(((1ull << hi) - 1ull) & ~((1ull << lo) - 1ull));
 }
 
-// The part of the softmax warps: see the roles above.
-template <int D>
-__device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan& p, KvSmall& sm, uint32_t tmem) {
-  using L = KvLayout<D>;
+// Two fp32 values for the packed instructions (each half an ordinary IEEE operation).
+__device__ __forceinline__ void fma2(float& x, float& y, uint64_t scale, uint64_t shift) {
+  asm("{\n .reg .b64 v;\n mov.b64 v, {%0, %1};\n fma.rn.f32x2 v, v, %2, %3;\n mov.b64 {%0, %1}, v;\n}\n" : "+f"(x), "+f"(y) : "l"(scale), "l"(shift));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float p, float q) {
+  asm("{\n .reg .b64 v, w;\n mov.b64 v, {%0, %1};\n mov.b64 w, {%2, %3};\n add.rn.f32x2 v, v, w;\n mov.b64 {%0, %1}, v;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(p), "f"(q));
+}
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "f"(x));
+  return v;
+}
+
+// A softmax thread's row.
+struct SoftRow {
+  Seen see;
+  int32_t t, flat;  // token; (token, head) index, -1: none
+};
+
+__device__ __forceinline__ SoftRow soft_row(const KvAttentionArgs& a, const Job& job, int32_t i) {
+  SoftRow x{{-1, 0, 0, 0}, 0, -1};
+  if (i < job.tile.rows) {
+    const int32_t r = job.tile.base + i, tok = r / a.G;
+    x.t = job.tile.tok0 + tok;
+    x.flat = x.t * a.H + job.kh * a.G + r - tok * a.G;
+  }
+  return x;
+}
+
+// The keys of a tile (its places v .. v + 127 of the list) that the row sees, a bit each; true when that is not
+// every one of them for every row of the warp.
+__device__ __forceinline__ bool tile_bits(const KvAttentionArgs& a, const SoftRow& x, int32_t first, int32_t low, int32_t v, int32_t v1, uint4 gone,
+                                          uint32_t (&bits)[4]) {
+  const int32_t here = min(kKvKeys, v1 - v), head = first - v, k0 = low - head;  // places; those of first rows; the row of place 0, were it none
+  const Seen& see = x.see;
+  const bool whole = x.flat < 0 || (here == kKvKeys && k0 + kKvKeys <= see.c && (head <= 0 ? k0 : low) >= see.low);
+  if (!__any_sync(0xFFFFFFFFu, !whole) && !(gone.x | gone.y | gone.z | gone.w)) return false;
+  const uint32_t lost[4] = {gone.x, gone.y, gone.z, gone.w};
+  uint32_t missed = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t k = k0 + i * 32, y = i * 32;
+    uint32_t m = bits_between(see.low - k, see.c - k) | bits_between(-k, see.first - k);
+    if (a.words > 0 && k + 32 > see.c && k < see.end) {  // 32 bits of the drafts' mask, from bit k - c on
+      const int32_t d = k - see.c, at = d >> 5;          // rounded down
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(a.mask + static_cast<int64_t>(x.t) * a.words);
+      const uint32_t lo = at >= 0 && at < 2 * a.words ? words[at] : 0u, hi = at + 1 >= 0 && at + 1 < 2 * a.words ? words[at + 1] : 0u;
+      m |= __funnelshift_r(lo, hi, d & 31) & bits_between(0, see.end - k);
+    }
+    const uint32_t heads = bits_between(0, head - y);
+    m = (m & ~heads) | (heads & bits_between(0, see.c - v - y));  // first rows: below low of everyone who sees any
+    m &= bits_between(0, here - y);
+    missed |= m & lost[i];
+    bits[i] = m & ~lost[i];
+  }
+  if (missed && x.flat >= 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
+  return true;
+}
+
+__device__ __forceinline__ float largest(const float (&z)[128]) {
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 128; ++i) top[i % 4] = fmaxf(top[i % 4], z[i]);
+  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+// Scores of the warp's rows in log2 units over their references; -infinity for what a row does not see.
+__device__ __forceinline__ void over_reference(float (&z)[128], float c, float ref, bool masks, const uint32_t (&bits)[4]) {
+  const uint64_t scale = twice(c), shift = twice(-ref);
+#pragma unroll
+  for (int i = 0; i < 128; i += 2) fma2(z[i], z[i + 1], scale, shift);
+  if (masks) {
+#pragma unroll
+    for (int i = 0; i < 128; ++i) z[i] = (bits[i / 32] >> (i % 32)) & 1 ? z[i] : -INFINITY;
+  }
+}
+
+// Their weights, rounded to bf16, to tensor memory as A of the second product; returns the sum.
+__device__ __forceinline__ float weights(const float (&z)[128], uint32_t at) {
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x[16];
+#pragma unroll
+    for (int y = 0; y < 32; y += 4) {
+      const float p0 = fast_exp2(z[i * 32 + y]), p1 = fast_exp2(z[i * 32 + y + 1]);
+      const float p2 = fast_exp2(z[i * 32 + y + 2]), p3 = fast_exp2(z[i * 32 + y + 3]);
+      add2(s0, s1, p0, p1);
+      add2(s2, s3, p2, p3);
+      x[y / 2] = pack_bf16x2_rn(p0, p1);
+      x[y / 2 + 1] = pack_bf16x2_rn(p2, p3);
+    }
+    kv_tmem_st16(at + i * 16, x);
+  }
+  return (s0 + s1) + (s2 + s3);
+}
+
+// Columns of O times what a move of the rows' references leaves.
+template <int kColumns>
+__device__ __forceinline__ void rescale(uint32_t at, float keep) {
+#pragma unroll 1
+  for (int i = 0; i < kColumns; i += 16) {
+    float o[16];
+    tmem_ld<16>(at + i, o);
+    uint32_t x[16];
+#pragma unroll
+    for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(o[y] * keep);
+    kv_tmem_st16(at + i, x);
+  }
+  tc_wait_st();
+}
+
+// Sum and reference of a row -> the scale of its output; stores lse (of the range when the row is split).
+__device__ __forceinline__ float finish_row(const KvAttentionArgs& a, const KvPlan& p, int D, int32_t range, int32_t flat, float all, float m, bool tell) {
+  const bool none = all == 0.f, split = p.splits > 1;
+  float keep = 1.f;
+  if (a.sink && !split && flat >= 0) {
+    const float s = a.sink[flat % a.H] * kLog2e, high = fmaxf(none ? kNegBig : m, s);
+    keep = none ? 0.f : fast_exp2(m - high);
+    all = (none ? 0.f : all * keep) + (s == high ? 1.f : fast_exp2(s - high));
+    m = high;
+  }
+  if (flat >= 0 && tell) {
+    const float lse = all == 0.f ? -INFINITY : (m + log2f(all)) * kKvLn2;
+    if (split) static_cast<float*>(a.workspace)[a.T * a.H * (p.splits * D + static_cast<int64_t>(range)) + flat] = lse;
+    else if (a.lse) a.lse[flat] = lse;
+  }
+  return none ? 0.f : keep / all;
+}
+
+// 32 channels from `ch` on of the warp's rows.  Four neighbouring lanes trade pieces of 16 bytes, so that a row's
+// 64 bytes are written together.
+__device__ __forceinline__ void put_row(const KvAttentionArgs& a, const KvPlan& p, int D, int32_t range, int32_t flat, int ch, const float (&o)[32]) {
+  const int lane = threadIdx.x & 31;
+  if (p.splits > 1) {
+    if (flat >= 0) {
+      float4* to = reinterpret_cast<float4*>(static_cast<float*>(a.workspace) + (a.T * a.H * static_cast<int64_t>(range) + flat) * D + ch);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) to[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+    }
+    return;
+  }
+  uint4 x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    x[i] = make_uint4(pack_bf16x2_rn(o[8 * i], o[8 * i + 1]), pack_bf16x2_rn(o[8 * i + 2], o[8 * i + 3]),
+                      pack_bf16x2_rn(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2_rn(o[8 * i + 6], o[8 * i + 7]));
+  auto trade = [&](uint4& lo, uint4& hi, int bit) {  // the lane with the bit keeps the upper piece
+    const bool up = lane & bit;
+    uint4 y = up ? lo : hi;
+    y.x = __shfl_xor_sync(0xFFFFFFFFu, y.x, bit);
+    y.y = __shfl_xor_sync(0xFFFFFFFFu, y.y, bit);
+    y.z = __shfl_xor_sync(0xFFFFFFFFu, y.z, bit);
+    y.w = __shfl_xor_sync(0xFFFFFFFFu, y.w, bit);
+    if (up) lo = y;
+    else hi = y;
+  };
+  trade(x[0], x[1], 1);
+  trade(x[2], x[3], 1);
+  trade(x[0], x[2], 2);
+  trade(x[1], x[3], 2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t f = __shfl_sync(0xFFFFFFFFu, flat, (lane & ~3) + i);
+    if (f >= 0) *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(f) * D + ch + (lane & 3) * 8) = x[i];
+  }
+}
+
+// The part of the softmax warps at D = 128: every group has an output of its own.
+__device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPlan& p, KvSmall<128>& sm, uint32_t tmem) {
+  using L = KvLayout<128>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, w = warp >> 2, row = threadIdx.x & 127;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-  const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128;
+  const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128, at_o = tmem + lanes + L::kTmemO + w * 128;
   const float c = a.softmax_scale * kLog2e;
-  uint32_t s_use = 0, o_use = 0, met_use = 0, keys_before = 0;  // tiles of keys of earlier jobs
-  uint32_t other_tiles = 0;                                     // of the other group, in jobs whose rows they share
+  uint32_t s_use = 0, o_use = 0, met_use = 0, keys_before = 0;
 #pragma unroll 1
   for (uint32_t job_use = 0;; ++job_use) {
     if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
     const Job& job = sm.job[job_use & 1];
     if (!job.live) return true;
-    const bool two = L::kRows == 256 && job.two;
-    const int32_t n = job.n, kh = job.kh, half = job.half, range = job.split;
-    const int32_t r = job.tile.base + (two ? w * 128 : 0) + row;
-    int32_t t = 0, flat = -1;
-    Seen see{-1, 0, 0, 0};
-    if (r < job.tile.base + job.tile.rows) {
-      const int32_t tok = r / a.G;
-      t = job.tile.tok0 + tok;
-      see = seen_by(a, t);
-      if (see.c >= 0) flat = t * a.H + kh * a.G + r - tok * a.G;
-    }
-    const bool any = __any_sync(0xFFFFFFFFu, flat >= 0);
-    const uint32_t at_o = tmem + lanes + L::kTmemO + (two ? w * 128 : 0);
-    float ref = flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
-    const int step = two ? 1 : 2;
+    const bool two = job.two;  // a tile of rows of its own; otherwise the groups take tiles of keys of the same rows by turns
+    const int32_t n = job.n, v0 = job.v0, v1 = job.v1, first = job.first, low = job.low, range = job.split;
+    const int i0 = (two ? w * 128 : 0) + row;
+    SoftRow x = soft_row(a, job, i0);
+    x.see.c = sm.rows[job_use & 1].c[i0];
+    x.see.low = sm.rows[job_use & 1].low[i0];
+    x.see.end = sm.rows[job_use & 1].end[i0];
+    x.see.first = min(a.first, x.see.low);
+    if (x.see.c < 0) x.flat = -1;
+    const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
+    float ref = x.flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
+    const int j0 = two ? 0 : w, step = two ? 1 : 2;
 #pragma unroll 1
-    for (int j = two ? 0 : w; j < n; j += step) {
+    for (int j = j0; j < n; j += step) {
       const uint32_t jt = keys_before + j;
       if (!warp_wait(&sm.s_full[w], s_use++) || !warp_wait(&sm.noted[jt % kKvNotes], jt / kKvNotes)) return false;
       tc_fence_after();
@@ -144,41 +317,133 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
         float z[128];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32_async(at_s + i * 32, z + i * 32);
-        // which keys the row sees, a bit each
-        const int32_t v = job.v0 + j * kKvKeys, here = min(kKvKeys, job.v1 - v);
-        const int32_t head = job.first - v, k0 = job.low - head;  // places of first rows; the row of place 0, were it none of them
-        const bool whole = flat < 0 || (here == kKvKeys && k0 + kKvKeys <= see.c && (head <= 0 ? k0 : job.low) >= see.low);
-        const uint4 gone = *reinterpret_cast<const uint4*>(sm.bad[jt % kKvNotes]);
-        uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
-        const bool masks = __any_sync(0xFFFFFFFFu, !whole) || (gone.x | gone.y | gone.z | gone.w);
-        if (masks) {
-          const uint32_t lost[4] = {gone.x, gone.y, gone.z, gone.w};
-          uint32_t missed = 0;
+        uint32_t bits[4];
+        const bool masks = tile_bits(a, x, first, low, v0 + j * kKvKeys, v1, *reinterpret_cast<const uint4*>(sm.bad[jt % kKvNotes]), bits);
+        tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int32_t x = k0 + i * 32, y = i * 32;
-            uint32_t m = bits_between(see.low - x, see.c - x) | bits_between(-x, see.first - x);
-            if (a.words > 0 && x + 32 > see.c && x < see.end) {  // 32 bits of the drafts' mask, from bit x - c on
-              const int32_t d = x - see.c, at = d >> 5;          // rounded down
-              const uint32_t* words = reinterpret_cast<const uint32_t*>(a.mask + static_cast<int64_t>(t) * a.words);
-              const uint32_t lo = at >= 0 && at < 2 * a.words ? words[at] : 0u, hi = at + 1 >= 0 && at + 1 < 2 * a.words ? words[at + 1] : 0u;
-              m |= __funnelshift_r(lo, hi, d & 31) & bits_between(0, see.end - x);
-            }
-            const uint32_t heads = bits_between(0, head - y);
-            m = (m & ~heads) | (heads & bits_between(0, see.c - v - y));  // first rows: below low of everyone who sees any
-            m &= bits_between(0, here - y);
-            missed |= m & lost[i];
-            bits[i] = m & ~lost[i];
+        for (int i = 0; i < 4; ++i) settled32(z + i * 32);
+        const bool unset = ref == kNegBig;
+        over_reference(z, c, unset ? 0.f : ref, masks, bits);
+        if (__any_sync(0xFFFFFFFFu, unset)) {  // its output is 0: the reference is just set
+          const float top = largest(z);
+          if (unset && top > -INFINITY) {
+            ref = top;
+#pragma unroll
+            for (int i = 0; i < 128; ++i) z[i] -= top;
           }
-          if (missed && flat >= 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
         }
+        // Weights under the reference as it is; when a row's sum shows that it has grown too old, once more.
+        float sum = weights(z, at_s);
+        while (__any_sync(0xFFFFFFFFu, sum > kKvMost)) {
+          const bool old = sum > kKvMost;
+          const float by = old ? largest(z) : 0.f, keep = fast_exp2(-by);
+          ref += by;
+          l *= keep;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) z[i] -= by;
+          if (j > j0) rescale<128>(at_o, keep);  // the products before this tile's scores are done
+          tc_wait_st();
+          sum = weights(z, at_s);
+        }
+        l += sum;
+        tc_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[w]);
+    }
+    keys_before += n;
+    // ------------------------------------------------------------------ output
+    float all = l, m = ref, mine = 1.f, other = 0.f;  // shares of the two outputs
+    if (!two) {
+      sm.sum[w][row] = l;
+      sm.ref[w][row] = ref;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.met);
+      if (!warp_wait(&sm.met, met_use++)) return false;
+      const float l1 = sm.sum[w ^ 1][row], m1 = sm.ref[w ^ 1][row];
+      m = fmaxf(l == 0.f ? kNegBig : ref, l1 == 0.f ? kNegBig : m1);
+      mine = l == 0.f ? 0.f : fast_exp2(ref - m);
+      other = l1 == 0.f ? 0.f : fast_exp2(m1 - m);
+      all = l * mine + l1 * other;
+    }
+    const float scale = finish_row(a, p, 128, range, x.flat, all, m, two || w == 0);
+    mine *= scale;
+    other *= scale;
+    if (n > 0) {
+      if (!warp_wait(&sm.o_full[w], o_use++)) return false;
+      tc_fence_after();
+    }
+    if (any) {
+#pragma unroll 1
+      for (int i = two ? 0 : w * 64; i < (two ? 128 : w * 64 + 64); i += 32) {
+        float o[32];
+        if (n > j0) {
+          tmem_ld<32>(at_o + i, o);
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = mine == 0.f ? 0.f : o[y] * mine;
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = 0.f;
+        }
+        if (!two && n > (w ^ 1)) {
+          float o1[32];
+          tmem_ld<32>(tmem + lanes + L::kTmemO + (w ^ 1) * 128 + i, o1);
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = other == 0.f ? o[y] : fmaf(o1[y], other, o[y]);
+        }
+        put_row(a, p, 128, range, x.flat, i, o);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sm.job_empty[job_use & 1]);
+      if (!two) mbar_arrive(&sm.met);
+    }
+    if (!two && !warp_wait(&sm.met, met_use++)) return false;  // both outputs and the sums are read
+  }
+}
+
+// The part of the softmax warps at D = 256 and 512: the groups take tiles of keys by turns and share the output.
+template <int D>
+__device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPlan& p, KvSmall<D>& sm, uint32_t tmem) {
+  using L = KvLayout<D>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, w = warp >> 2, row = threadIdx.x & 127;
+  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128, at_o = tmem + lanes + L::kTmemO;
+  const float c = a.softmax_scale * kLog2e;
+  uint32_t s_use = 0, o_use = 0, met_use = 0, keys_before = 0;
+  uint32_t other_tiles = 0;  // of the other group so far
+#pragma unroll 1
+  for (uint32_t job_use = 0;; ++job_use) {
+    if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
+    const Job& job = sm.job[job_use & 1];
+    if (!job.live) return true;
+    const int32_t n = job.n, v0 = job.v0, v1 = job.v1, first = job.first, low = job.low, range = job.split, half = job.half;
+    SoftRow x = soft_row(a, job, row);
+    if (x.flat >= 0) x.see = seen_by(a, x.t);
+    if (x.see.c < 0) x.flat = -1;
+    const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
+    float ref = x.flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
+#pragma unroll 1
+    for (int j = w; j < n; j += 2) {
+      const uint32_t jt = keys_before + j;
+      if (!warp_wait(&sm.s_full[w], s_use++) || !warp_wait(&sm.noted[jt % kKvNotes], jt / kKvNotes)) return false;
+      tc_fence_after();
+      if (any) {
+        float z[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32_async(at_s + i * 32, z + i * 32);
+        uint32_t bits[4];
+        const bool masks = tile_bits(a, x, first, low, v0 + j * kKvKeys, v1, *reinterpret_cast<const uint4*>(sm.bad[jt % kKvNotes]), bits);
         tc_wait_ld();
 #pragma unroll
         for (int i = 0; i < 4; ++i) settled32(z + i * 32);
         const uint32_t others = other_tiles + (j + 1) / 2;  // tiles of the other group before this one
-        if (!two && j > 0) {                                // the reference as it left it
+        if (j > 0) {                                        // the reference as it left it
           if (!warp_wait(&sm.decided[w ^ 1][quad], others - 1)) return false;
-          const float now = sm.ref[row];
+          const float now = sm.ref[0][row];
           if (now != ref) {
             l = l == 0.f ? 0.f : l * fast_exp2(ref - now);
             ref = now;
@@ -186,16 +451,8 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
         }
         const bool unset = ref == kNegBig;
         const float shift = unset ? 0.f : ref;
-#pragma unroll
-        for (int i = 0; i < 128; ++i) z[i] = fmaf(z[i], c, -shift);
-        if (masks) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) z[i] = (bits[i / 32] >> (i % 32)) & 1 ? z[i] : -INFINITY;
-        }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < 128; ++i) top[i % 4] = fmaxf(top[i % 4], z[i]);
-        const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        over_reference(z, c, shift, masks, bits);
+        const float over = largest(z);
         if (__any_sync(0xFFFFFFFFu, over > kKvJump || (unset && over > -INFINITY))) {
           // the reference goes to the largest score so far
           const float by = unset ? (over > -INFINITY ? over : 0.f) : fmaxf(over, 0.f);
@@ -205,44 +462,17 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
 #pragma unroll
           for (int i = 0; i < 128; ++i) z[i] -= by;
           if (j > 0 && __any_sync(0xFFFFFFFFu, keep != 1.f)) {
-            // the products of the tiles before have to be done: those of a group with a tile of its own
-            // came before these scores, else the last one is the other group's
-            if (!two && !warp_wait(&sm.pv_done[w ^ 1], others - 1)) return false;
+            if (!warp_wait(&sm.pv_done[w ^ 1], others - 1)) return false;  // the products of the tile before
             tc_fence_after();
-#pragma unroll 1
-            for (int i = 0; i < (two ? 128 : L::kDV); i += 16) {
-              float o[16];
-              tmem_ld<16>(at_o + i, o);
-              uint32_t x[16];
-#pragma unroll
-              for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(o[y] * keep);
-              kv_tmem_st16(at_o + i, x);
-            }
-            tc_wait_st();
+            rescale<L::kDV>(at_o, keep);
           }
         }
-        if (!two) {
-          sm.ref[row] = ref;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.decided[w][quad]);
-        }
-        // weights, rounded to bf16, as A of the second product
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t x[16];
-#pragma unroll
-          for (int y = 0; y < 32; y += 2) {
-            const float p0 = fast_exp2(z[i * 32 + y]), p1 = fast_exp2(z[i * 32 + y + 1]);
-            part[y % 4] += p0;
-            part[y % 4 + 1] += p1;
-            x[y / 2] = pack_bf16x2_rn(p0, p1);
-          }
-          kv_tmem_st16(at_s + i * 16, x);
-        }
-        l += (part[0] + part[1]) + (part[2] + part[3]);
+        sm.ref[0][row] = ref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.decided[w][quad]);
+        l += weights(z, at_s);
         tc_wait_st();
-      } else if (!two && lane == 0) {
+      } else if (lane == 0) {
         mbar_arrive(&sm.decided[w][quad]);
       }
       tc_fence_before();
@@ -251,83 +481,50 @@ __device__ __forceinline__ bool soft_jobs(const KvAttentionArgs& a, const KvPlan
     }
     keys_before += n;
     // ------------------------------------------------------------------ output
-    const bool split = p.splits > 1;
-    float all = l, m = ref;
-    if (!two) {
-      other_tiles += (n + w) / 2;
-      // both sums against the references that O has in the end: the last tile's
-      if (n > 0) {
-        if (((n - 1) & 1) != w && !warp_wait(&sm.decided[w ^ 1][quad], other_tiles - 1)) return false;
-        m = any ? sm.ref[row] : 0.f;
-        l = l == 0.f ? 0.f : l * fast_exp2(ref - m);
-      }
-      sm.sum[w][row] = l;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.met);
-      if (!warp_wait(&sm.met, met_use++)) return false;
-      all = l + sm.sum[w ^ 1][row];
+    other_tiles += (n + w) / 2;
+    float m = ref;
+    if (n > 0) {  // both sums against the references that O has in the end: the last tile's
+      if (((n - 1) & 1) != w && !warp_wait(&sm.decided[w ^ 1][quad], other_tiles - 1)) return false;
+      m = any ? sm.ref[0][row] : 0.f;
+      l = l == 0.f ? 0.f : l * fast_exp2(ref - m);
     }
-    const bool none = all == 0.f;
-    float keep = 1.f;
-    if (a.sink && !split && flat >= 0) {
-      const float s = a.sink[flat % a.H] * kLog2e, high = fmaxf(none ? kNegBig : m, s);
-      keep = none ? 0.f : fast_exp2(m - high);
-      all = (none ? 0.f : all * keep) + (s == high ? 1.f : fast_exp2(s - high));
-      m = high;
-    }
-    const float scale = none ? 0.f : keep / all;
-    const int64_t rows = a.T * a.H, place = flat + (split ? range * rows : 0);
-    float* part_out = static_cast<float*>(a.workspace);
-    if (flat >= 0 && (two || w == 0) && half == 0) {
-      const float lse = all == 0.f ? -INFINITY : (m + log2f(all)) * kKvLn2;
-      if (split) part_out[p.splits * rows * D + place] = lse;
-      else if (a.lse) a.lse[flat] = lse;
-    }
+    sm.sum[w][row] = l;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.met);
+    if (!warp_wait(&sm.met, met_use++)) return false;
+    const float scale = finish_row(a, p, D, range, x.flat, l + sm.sum[w ^ 1][row], m, w == 0 && half == 0);
     if (n > 0) {
       if (!warp_wait(&sm.o_full[w], o_use++)) return false;
       tc_fence_after();
     }
     if (any) {
-      const int c0 = two ? 0 : w * (L::kDV / 2), c1 = two ? 128 : c0 + L::kDV / 2;
 #pragma unroll 1
-      for (int i = c0; i < c1; i += 32) {
+      for (int i = w * (L::kDV / 2); i < (w + 1) * (L::kDV / 2); i += 32) {
         float o[32];
-        if (n > 0) tmem_ld<32>(at_o + i, o);
-        if (n == 0 || none) {
+        if (n > 0) {
+          tmem_ld<32>(at_o + i, o);
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = 0.f;
+          for (int y = 0; y < 32; ++y) o[y] = scale == 0.f ? 0.f : o[y] * scale;
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = 0.f;
         }
-        if (flat >= 0) {
-          const int ch = half * L::kDV + i;
-          if (split) {
-            float4* to = reinterpret_cast<float4*>(part_out + place * D + ch);
-            if (!none) {  // else the join does not look at it
-#pragma unroll
-              for (int x = 0; x < 8; ++x) to[x] = make_float4(o[4 * x] * scale, o[4 * x + 1] * scale, o[4 * x + 2] * scale, o[4 * x + 3] * scale);
-            }
-          } else {
-            uint4* to = reinterpret_cast<uint4*>(a.out + place * D + ch);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              to[x] = make_uint4(pack_bf16x2_rn(o[8 * x] * scale, o[8 * x + 1] * scale), pack_bf16x2_rn(o[8 * x + 2] * scale, o[8 * x + 3] * scale),
-                                 pack_bf16x2_rn(o[8 * x + 4] * scale, o[8 * x + 5] * scale), pack_bf16x2_rn(o[8 * x + 6] * scale, o[8 * x + 7] * scale));
-          }
-        }
+        put_row(a, p, D, range, x.flat, half * L::kDV + i, o);
       }
     }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(&sm.job_empty[job_use & 1]);
-      if (!two) mbar_arrive(&sm.met);
+      mbar_arrive(&sm.met);
     }
-    if (!two && !warp_wait(&sm.met, met_use++)) return false;  // O and the sums are read
+    if (!warp_wait(&sm.met, met_use++)) return false;  // O and the sums are read
   }
 }
 
 // One thread: the products, in the order of their units.
 template <int D>
-__device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tmem) {
+__device__ __forceinline__ bool mma_jobs(KvSmall<D>& sm, uint32_t base, uint32_t tmem) {
   using L = KvLayout<D>;
   constexpr uint32_t kIdescS = idesc_bf16(128, false), kIdescO = idesc_bf16(128, true);
   uint32_t unit = 0, q_use = 0, p_use[2] = {0, 0};
@@ -367,7 +564,7 @@ __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tm
     if (two) {
       const uint32_t slot[2] = {q_use & 1, (q_use + 1) & 1};
       for (int w = 0; w < 2; ++w) {
-        if (!wait(&sm.q_full[slot[w]], (q_use + w) >> 1) || !unit_there(unit)) return false;  // (with the fence)
+        if (!wait(&sm.q_full[slot[w]], (q_use + w) >> 1) || !unit_there(unit)) return false;
         scores(w, slot[w], unit, 0);
         tc_commit(&sm.s_full[w]);
         if (n == 1) tc_commit(&sm.q_empty[slot[w]]);
@@ -376,12 +573,12 @@ __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tm
       for (int j = 0; j < n; ++j) {
         const uint32_t v = unit + 2 * j + 1, k = v + 1;  // values of this tile, keys of the next
         for (int w = 0; w < 2; ++w) {
-          if (!unit_there(v) || !wait(&sm.p_full[w], p_use[w]++)) return false;
+          if ((w == 0 && !unit_there(v)) || !wait(&sm.p_full[w], p_use[w]++)) return false;
           tc_fence_after();
           values(w, w * 128, v, j > 0);
           if (w == 1) tc_commit(&sm.empty[v % L::kRing]);
           if (j + 1 < n) {
-            if (!unit_there(k)) return false;
+            if (w == 0 && !unit_there(k)) return false;
             scores(w, slot[w], k, 0);
             tc_commit(&sm.s_full[w]);
             if (j + 2 == n) tc_commit(&sm.q_empty[slot[w]]);
@@ -412,7 +609,7 @@ __device__ __forceinline__ bool mma_jobs(KvSmall& sm, uint32_t base, uint32_t tm
         tc_fence_after();
         for (int u = 0; u < L::kVU; ++u, ++unit) {
           if (!unit_there(unit)) return false;
-          values(j & 1, u * 128, unit, j > 0);
+          values(j & 1, D == 128 ? (j & 1) * 128 : u * 128, unit, j > (D == 128 ? 1 : 0));
           tc_commit(&sm.empty[unit % L::kRing]);
         }
         tc_commit(&sm.pv_done[j & 1]);
@@ -431,7 +628,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   using L = KvLayout<D>;
   // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
   extern __shared__ __align__(1024) uint8_t smem[];
-  KvSmall& sm = *reinterpret_cast<KvSmall*>(smem + L::kSmall);
+  KvSmall<D>& sm = *reinterpret_cast<KvSmall<D>*>(smem + L::kSmall);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (smem_u32(smem) & 1023u) {
     pdl_wait();  // whoever follows in the stream counts on what came before having ended
@@ -475,7 +672,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   bool ok = true;
   if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    ok = soft_jobs<D>(a, p, sm, tmem);
+    if constexpr (D == 128) ok = soft_apart(a, p, sm, tmem);
+    else ok = soft_shared<D>(a, p, sm, tmem);
     tc_fence_before();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -489,7 +687,17 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       }
       __syncwarp();
     } else if (warp == kPlanWarp) {
-      ok = plan_jobs<L>(a, p, sm, jobs, [](const Job&, uint32_t) {});
+      ok = plan_jobs<L>(a, p, sm, jobs, [&](const Job& j, uint32_t i) {
+        if constexpr (D == 128) {
+          for (int r = lane; r < L::kRows; r += 32) {
+            Seen x{-1, 0, 0, 0};
+            if (r < j.tile.rows) x = seen_by(a, j.tile.tok0 + (j.tile.base + r) / a.G);
+            sm.rows[i].c[r] = x.c;
+            sm.rows[i].low[r] = x.low;
+            sm.rows[i].end[r] = x.end;
+          }
+        }
+      });
     } else if (warp >= kCopyWarp) {
       ok = copy_jobs<L>(a, sm, smem);
     }
