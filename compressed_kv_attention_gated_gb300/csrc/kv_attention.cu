@@ -69,6 +69,7 @@ struct SeenRows {
 template <int D>
 struct KvSmall : KvCommon {
   uint64_t decided[2][4];         // D > 128: warp q of group w knows the references under which its tile is taken
+  uint64_t half_s[2][2], half_p[2][2];  // D = 128: scores and weights of group w, by halves of a tile of keys (4 warps)
   uint64_t met;                   // both groups have got there: 8 warps, twice per job of shared rows
   float ref[D == 128 ? 2 : 1][128];  // references of shared rows (each group's own at D = 128)
   float sum[2][128];
@@ -144,18 +145,21 @@ __device__ __forceinline__ SoftRow soft_row(const KvAttentionArgs& a, const Job&
   return x;
 }
 
-// The keys of a tile (its places v .. v + 127 of the list) that the row sees, a bit each; true when that is not
-// every one of them for every row of the warp.
-__device__ __forceinline__ bool tile_bits(const KvAttentionArgs& a, const SoftRow& x, int32_t first, int32_t low, int32_t v, int32_t v1, uint4 gone,
-                                          uint32_t (&bits)[4]) {
-  const int32_t here = min(kKvKeys, v1 - v), head = first - v, k0 = low - head;  // places; those of first rows; the row of place 0, were it none
+// Which of n keys (places v .. v + n - 1 of the list) the row sees, a bit each; true when that is not every one
+// of them for every row of the warp.  gone: keys whose page is not there.
+template <int n>
+__device__ __forceinline__ bool tile_bits(const KvAttentionArgs& a, const SoftRow& x, int32_t first, int32_t low, int32_t v, int32_t v1,
+                                          const uint32_t* gone, uint32_t (&bits)[n / 32]) {
+  const int32_t here = min(n, v1 - v), head = first - v, k0 = low - head;  // places; those of first rows; the row of the first, were it none
   const Seen& see = x.see;
-  const bool whole = x.flat < 0 || (here == kKvKeys && k0 + kKvKeys <= see.c && (head <= 0 ? k0 : low) >= see.low);
-  if (!__any_sync(0xFFFFFFFFu, !whole) && !(gone.x | gone.y | gone.z | gone.w)) return false;
-  const uint32_t lost[4] = {gone.x, gone.y, gone.z, gone.w};
+  const bool whole = x.flat < 0 || (here == n && k0 + n <= see.c && (head <= 0 ? k0 : low) >= see.low);
+  uint32_t lost[n / 32], some = 0;
+#pragma unroll
+  for (int i = 0; i < n / 32; ++i) some |= lost[i] = gone[i];
+  if (!__any_sync(0xFFFFFFFFu, !whole) && some == 0) return false;
   uint32_t missed = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < n / 32; ++i) {
     const int32_t k = k0 + i * 32, y = i * 32;
     uint32_t m = bits_between(see.low - k, see.c - k) | bits_between(-k, see.first - k);
     if (a.words > 0 && k + 32 > see.c && k < see.end) {  // 32 bits of the drafts' mask, from bit k - c on
@@ -174,29 +178,32 @@ __device__ __forceinline__ bool tile_bits(const KvAttentionArgs& a, const SoftRo
   return true;
 }
 
-__device__ __forceinline__ float largest(const float (&z)[128]) {
+template <int n>
+__device__ __forceinline__ float largest(const float* z) {
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < 128; ++i) top[i % 4] = fmaxf(top[i % 4], z[i]);
+  for (int i = 0; i < n; ++i) top[i % 4] = fmaxf(top[i % 4], z[i]);
   return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 }
 
-// Scores of the warp's rows in log2 units over their references; -infinity for what a row does not see.
-__device__ __forceinline__ void over_reference(float (&z)[128], float c, float ref, bool masks, const uint32_t (&bits)[4]) {
+// n scores of the row in log2 units over its reference; -infinity for what it does not see.
+template <int n>
+__device__ __forceinline__ void over_reference(float* z, float c, float ref, bool masks, const uint32_t* bits) {
   const uint64_t scale = twice(c), shift = twice(-ref);
 #pragma unroll
-  for (int i = 0; i < 128; i += 2) fma2(z[i], z[i + 1], scale, shift);
+  for (int i = 0; i < n; i += 2) fma2(z[i], z[i + 1], scale, shift);
   if (masks) {
 #pragma unroll
-    for (int i = 0; i < 128; ++i) z[i] = (bits[i / 32] >> (i % 32)) & 1 ? z[i] : -INFINITY;
+    for (int i = 0; i < n; ++i) z[i] = (bits[i / 32] >> (i % 32)) & 1 ? z[i] : -INFINITY;
   }
 }
 
 // Their weights, rounded to bf16, to tensor memory as A of the second product; returns the sum.
-__device__ __forceinline__ float weights(const float (&z)[128], uint32_t at) {
+template <int n>
+__device__ __forceinline__ float weights(const float* z, uint32_t at) {
   float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < n / 32; ++i) {
     uint32_t x[16];
 #pragma unroll
     for (int y = 0; y < 32; y += 4) {
@@ -245,41 +252,28 @@ __device__ __forceinline__ float finish_row(const KvAttentionArgs& a, const KvPl
   return none ? 0.f : keep / all;
 }
 
-// 32 channels from `ch` on of the warp's rows.  Four neighbouring lanes trade pieces of 16 bytes, so that a row's
-// 64 bytes are written together.
+// 32 channels from `ch` on of a row, in whole sectors where its beginning allows that.
 __device__ __forceinline__ void put_row(const KvAttentionArgs& a, const KvPlan& p, int D, int32_t range, int32_t flat, int ch, const float (&o)[32]) {
-  const int lane = threadIdx.x & 31;
+  if (flat < 0) return;
   if (p.splits > 1) {
-    if (flat >= 0) {
-      float4* to = reinterpret_cast<float4*>(static_cast<float*>(a.workspace) + (a.T * a.H * static_cast<int64_t>(range) + flat) * D + ch);
+    float4* to = reinterpret_cast<float4*>(static_cast<float*>(a.workspace) + (a.T * a.H * static_cast<int64_t>(range) + flat) * D + ch);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) to[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-    }
+    for (int x = 0; x < 8; ++x) to[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
     return;
   }
-  uint4 x[4];
+  uint32_t x[16];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    x[i] = make_uint4(pack_bf16x2_rn(o[8 * i], o[8 * i + 1]), pack_bf16x2_rn(o[8 * i + 2], o[8 * i + 3]),
-                      pack_bf16x2_rn(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2_rn(o[8 * i + 6], o[8 * i + 7]));
-  auto trade = [&](uint4& lo, uint4& hi, int bit) {  // the lane with the bit keeps the upper piece
-    const bool up = lane & bit;
-    uint4 y = up ? lo : hi;
-    y.x = __shfl_xor_sync(0xFFFFFFFFu, y.x, bit);
-    y.y = __shfl_xor_sync(0xFFFFFFFFu, y.y, bit);
-    y.z = __shfl_xor_sync(0xFFFFFFFFu, y.z, bit);
-    y.w = __shfl_xor_sync(0xFFFFFFFFu, y.w, bit);
-    if (up) lo = y;
-    else hi = y;
-  };
-  trade(x[0], x[1], 1);
-  trade(x[2], x[3], 1);
-  trade(x[0], x[2], 2);
-  trade(x[1], x[3], 2);
+  for (int i = 0; i < 16; ++i) x[i] = pack_bf16x2_rn(o[2 * i], o[2 * i + 1]);
+  uint16_t* to = a.out + static_cast<int64_t>(flat) * D + ch;
+  if (reinterpret_cast<uintptr_t>(a.out) % 32 == 0) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int32_t f = __shfl_sync(0xFFFFFFFFu, flat, (lane & ~3) + i);
-    if (f >= 0) *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(f) * D + ch + (lane & 3) * 8) = x[i];
+    for (int i = 0; i < 2; ++i)
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + i * 16), "r"(x[8 * i]), "r"(x[8 * i + 1]), "r"(x[8 * i + 2]),
+                   "r"(x[8 * i + 3]), "r"(x[8 * i + 4]), "r"(x[8 * i + 5]), "r"(x[8 * i + 6]), "r"(x[8 * i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + i * 8) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
   }
 }
 
@@ -290,7 +284,7 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128, at_o = tmem + lanes + L::kTmemO + w * 128;
   const float c = a.softmax_scale * kLog2e;
-  uint32_t s_use = 0, o_use = 0, met_use = 0, keys_before = 0;
+  uint32_t use = 0, o_use = 0, met_use = 0, keys_before = 0;  // tiles of keys of the group, jobs with keys, ...
 #pragma unroll 1
   for (uint32_t job_use = 0;; ++job_use) {
     if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
@@ -308,49 +302,59 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
     const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
     float ref = x.flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
     const int j0 = two ? 0 : w, step = two ? 1 : 2;
+    // a tile of keys goes through in halves, each with a buffer of scores of its own, so that there are always
+    // scores to work on while the products of the other half run
 #pragma unroll 1
-    for (int j = j0; j < n; j += step) {
+    for (int j = j0; j < n; j += step, ++use) {
       const uint32_t jt = keys_before + j;
-      if (!warp_wait(&sm.s_full[w], s_use++) || !warp_wait(&sm.noted[jt % kKvNotes], jt / kKvNotes)) return false;
-      tc_fence_after();
-      if (any) {
-        float z[128];
+      if (!warp_wait(&sm.noted[jt % kKvNotes], jt / kKvNotes)) return false;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        uint32_t bits[2];
+        const bool masks = any && tile_bits<64>(a, x, first, low, v0 + j * kKvKeys + h * 64, v1, &sm.bad[jt % kKvNotes][h * 2], bits);
+        const uint32_t at = at_s + h * 64;
+        if (!warp_wait(&sm.half_s[w][h], use)) return false;
+        tc_fence_after();
+        if (any) {
+          float z[64];
+          tmem_ld32_async(at, z);
+          tmem_ld32_async(at + 32, z + 32);
+          tc_wait_ld();
+          settled32(z);
+          settled32(z + 32);
+          const bool unset = ref == kNegBig;
+          over_reference<64>(z, c, unset ? 0.f : ref, masks, bits);
+          if (__any_sync(0xFFFFFFFFu, unset)) {  // its output is 0: the reference is just set
+            const float top = largest<64>(z);
+            if (unset && top > -INFINITY) {
+              ref = top;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32_async(at_s + i * 32, z + i * 32);
-        uint32_t bits[4];
-        const bool masks = tile_bits(a, x, first, low, v0 + j * kKvKeys, v1, *reinterpret_cast<const uint4*>(sm.bad[jt % kKvNotes]), bits);
-        tc_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) settled32(z + i * 32);
-        const bool unset = ref == kNegBig;
-        over_reference(z, c, unset ? 0.f : ref, masks, bits);
-        if (__any_sync(0xFFFFFFFFu, unset)) {  // its output is 0: the reference is just set
-          const float top = largest(z);
-          if (unset && top > -INFINITY) {
-            ref = top;
-#pragma unroll
-            for (int i = 0; i < 128; ++i) z[i] -= top;
+              for (int i = 0; i < 64; ++i) z[i] -= top;
+            }
           }
-        }
-        // Weights under the reference as it is; when a row's sum shows that it has grown too old, once more.
-        float sum = weights(z, at_s);
-        while (__any_sync(0xFFFFFFFFu, sum > kKvMost)) {
-          const bool old = sum > kKvMost;
-          const float by = old ? largest(z) : 0.f, keep = fast_exp2(-by);
-          ref += by;
-          l *= keep;
+          // weights under the reference as it is; when a row's sum shows that it has grown too old, once more
+          float sum = weights<64>(z, at);
+          while (__any_sync(0xFFFFFFFFu, sum > kKvMost)) {
+            const float by = sum > kKvMost ? largest<64>(z) : 0.f, keep = fast_exp2(-by);
+            ref += by;
+            l *= keep;
 #pragma unroll
-          for (int i = 0; i < 128; ++i) z[i] -= by;
-          if (j > j0) rescale<128>(at_o, keep);  // the products before this tile's scores are done
+            for (int i = 0; i < 64; ++i) z[i] -= by;
+            if (j > j0 || h > 0) {  // the products of the half before
+              if (!warp_wait(&sm.pv_done[w], 2 * use + h - 1)) return false;
+              tc_fence_after();
+              rescale<128>(at_o, keep);
+            }
+            tc_wait_st();
+            sum = weights<64>(z, at);
+          }
+          l += sum;
           tc_wait_st();
-          sum = weights(z, at_s);
         }
-        l += sum;
-        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.half_p[w][h]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[w]);
     }
     keys_before += n;
     // ------------------------------------------------------------------ output
@@ -381,7 +385,7 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
         if (n > j0) {
           tmem_ld<32>(at_o + i, o);
 #pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] = mine == 0.f ? 0.f : o[y] * mine;
+          for (int y = 0; y < 32; ++y) o[y] *= mine;
         } else {
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = 0.f;
@@ -390,7 +394,7 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
           float o1[32];
           tmem_ld<32>(tmem + lanes + L::kTmemO + (w ^ 1) * 128 + i, o1);
 #pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] = other == 0.f ? o[y] : fmaf(o1[y], other, o[y]);
+          for (int y = 0; y < 32; ++y) o[y] = fmaf(o1[y], other, o[y]);
         }
         put_row(a, p, 128, range, x.flat, i, o);
       }
@@ -436,7 +440,7 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32_async(at_s + i * 32, z + i * 32);
         uint32_t bits[4];
-        const bool masks = tile_bits(a, x, first, low, v0 + j * kKvKeys, v1, *reinterpret_cast<const uint4*>(sm.bad[jt % kKvNotes]), bits);
+        const bool masks = tile_bits<128>(a, x, first, low, v0 + j * kKvKeys, v1, sm.bad[jt % kKvNotes], bits);
         tc_wait_ld();
 #pragma unroll
         for (int i = 0; i < 4; ++i) settled32(z + i * 32);
@@ -451,8 +455,8 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
         }
         const bool unset = ref == kNegBig;
         const float shift = unset ? 0.f : ref;
-        over_reference(z, c, shift, masks, bits);
-        const float over = largest(z);
+        over_reference<128>(z, c, shift, masks, bits);
+        const float over = largest<128>(z);
         if (__any_sync(0xFFFFFFFFu, over > kKvJump || (unset && over > -INFINITY))) {
           // the reference goes to the largest score so far
           const float by = unset ? (over > -INFINITY ? over : 0.f) : fmaxf(over, 0.f);
@@ -470,7 +474,7 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
         sm.ref[0][row] = ref;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.decided[w][quad]);
-        l += weights(z, at_s);
+        l += weights<128>(z, at_s);
         tc_wait_st();
       } else if (lane == 0) {
         mbar_arrive(&sm.decided[w][quad]);
@@ -504,7 +508,7 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
         if (n > 0) {
           tmem_ld<32>(at_o + i, o);
 #pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] = scale == 0.f ? 0.f : o[y] * scale;
+          for (int y = 0; y < 32; ++y) o[y] *= scale;
         } else {
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = 0.f;
@@ -526,7 +530,8 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
 template <int D>
 __device__ __forceinline__ bool mma_jobs(KvSmall<D>& sm, uint32_t base, uint32_t tmem) {
   using L = KvLayout<D>;
-  constexpr uint32_t kIdescS = idesc_bf16(128, false), kIdescO = idesc_bf16(128, true);
+  constexpr int kN = D == 128 ? 64 : 128;  // keys of a product of scores
+  constexpr uint32_t kIdescS = idesc_bf16(kN, false), kIdescO = idesc_bf16(128, true);
   uint32_t unit = 0, q_use = 0, p_use[2] = {0, 0};
   auto wait = [](uint64_t* bar, uint32_t n) { return mbar_wait_near(bar, n & 1u); };
   auto unit_there = [&](uint32_t c) {
@@ -535,21 +540,21 @@ __device__ __forceinline__ bool mma_jobs(KvSmall<D>& sm, uint32_t base, uint32_t
     tc_fence_after();
     return ok;
   };
-  // scores of group w: queries in slot q, with unit c for channels 128 u ...
-  auto scores = [&](int w, uint32_t q, uint32_t c, int u) {
+  // scores of group w with keys kN h ...: queries in slot q, with unit c for channels 128 u ...
+  auto scores = [&](int w, uint32_t q, uint32_t c, int u, int h) {
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
       const uint64_t da = smem_desc_sw128(base + q * L::kQSlot + (u * 2 + s / 4) * L::kQBlock + (s % 4) * 32, 16, 1024);
-      const uint64_t db = smem_desc_sw128(base + L::kUnits + (c % L::kRing) * kKvUnit + (s / 4) * 16384 + (s % 4) * 32, 16, 1024);
-      mma_f16_ss(tmem + L::kTmemS + w * 128, da, db, kIdescS, u > 0 || s > 0);
+      const uint64_t db = smem_desc_sw128(base + L::kUnits + (c % L::kRing) * kKvUnit + (s / 4) * 16384 + h * 8192 + (s % 4) * 32, 16, 1024);
+      mma_f16_ss(tmem + L::kTmemS + w * 128 + h * 64, da, db, kIdescS, u > 0 || s > 0);
     }
   };
-  // weights of group w with unit c, into 128 columns of the output
-  auto values = [&](int w, uint32_t column, uint32_t c, bool more) {
+  // weights of group w (of their half h) with unit c, into 128 columns of the output; 16 keys a step
+  auto values = [&](int w, uint32_t column, uint32_t c, bool more, int h) {
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const uint64_t db = smem_desc_sw128(base + L::kUnits + (c % L::kRing) * kKvUnit + s * 2048, 16384, 1024);
-      mma_f16_ts(tmem + L::kTmemO + column, tmem + L::kTmemS + w * 128 + s * 8, db, kIdescO, more || s > 0);
+    for (int s = 0; s < kN / 16; ++s) {
+      const uint64_t db = smem_desc_sw128(base + L::kUnits + (c % L::kRing) * kKvUnit + (h * 4 + s) * 2048, 16384, 1024);
+      mma_f16_ts(tmem + L::kTmemO + column, tmem + L::kTmemS + w * 128 + h * 64 + s * 8, db, kIdescO, more || s > 0);
     }
   };
 #pragma unroll 1
@@ -561,42 +566,79 @@ __device__ __forceinline__ bool mma_jobs(KvSmall<D>& sm, uint32_t base, uint32_t
     const bool two = L::kRows == 256 && job.two;
     mbar_arrive(&sm.job_empty[job_use & 1]);
     if (n == 0) continue;
-    if (two) {
-      const uint32_t slot[2] = {q_use & 1, (q_use + 1) & 1};
-      for (int w = 0; w < 2; ++w) {
-        if (!wait(&sm.q_full[slot[w]], (q_use + w) >> 1) || !unit_there(unit)) return false;
-        scores(w, slot[w], unit, 0);
-        tc_commit(&sm.s_full[w]);
-        if (n == 1) tc_commit(&sm.q_empty[slot[w]]);
-      }
-      tc_commit(&sm.empty[unit % L::kRing]);
-      for (int j = 0; j < n; ++j) {
-        const uint32_t v = unit + 2 * j + 1, k = v + 1;  // values of this tile, keys of the next
+    if constexpr (D == 128) {
+      const uint32_t slot[2] = {q_use & 1, (q_use + (two ? 1 : 0)) & 1};
+      // half of a tile's scores; the last to use the queries and the unit give them back
+      auto half_scores = [&](int w, int j, int h, uint32_t c) {
+        scores(w, slot[w], c, 0, h);
+        tc_commit(&sm.half_s[w][h]);
+        if (h == 0) return;
+        if (j == n - 1) tc_commit(&sm.q_empty[slot[w]]);
+        if (!two || w == 1) tc_commit(&sm.empty[c % L::kRing]);
+      };
+      auto half_values = [&](int w, int h, uint32_t c, bool more) {
+        if (!wait(&sm.half_p[w][h], p_use[w])) return false;
+        if (h == 1) ++p_use[w];
+        tc_fence_after();
+        values(w, w * 128, c, more, h);
+        tc_commit(&sm.pv_done[w]);
+        return true;
+      };
+      if (!wait(&sm.q_full[slot[0]], q_use >> 1) || !unit_there(unit)) return false;
+      if (two) {
         for (int w = 0; w < 2; ++w) {
-          if ((w == 0 && !unit_there(v)) || !wait(&sm.p_full[w], p_use[w]++)) return false;
-          tc_fence_after();
-          values(w, w * 128, v, j > 0);
-          if (w == 1) tc_commit(&sm.empty[v % L::kRing]);
-          if (j + 1 < n) {
-            if (w == 0 && !unit_there(k)) return false;
-            scores(w, slot[w], k, 0);
-            tc_commit(&sm.s_full[w]);
-            if (j + 2 == n) tc_commit(&sm.q_empty[slot[w]]);
-            if (w == 1) tc_commit(&sm.empty[k % L::kRing]);
-          } else {
-            tc_commit(&sm.o_full[w]);
-          }
+          if (w == 1 && !wait(&sm.q_full[slot[1]], (q_use + 1) >> 1)) return false;
+          fence_proxy_async_smem();
+          for (int h = 0; h < 2; ++h) half_scores(w, 0, h, unit);
         }
+        for (int j = 0; j < n; ++j) {
+          const uint32_t v = unit + 2 * j + 1, k = v + 1;  // values of this tile, keys of the next
+          if (!unit_there(v)) return false;
+          for (int h = 0; h < 2; ++h) {
+            for (int w = 0; w < 2; ++w) {
+              if (!half_values(w, h, v, j > 0 || h > 0)) return false;
+              if (j + 1 < n) {
+                if (h == 0 && w == 0 && !unit_there(k)) return false;
+                half_scores(w, j + 1, h, k);
+              } else if (h == 1) {
+                tc_commit(&sm.o_full[w]);
+              }
+            }
+          }
+          tc_commit(&sm.empty[v % L::kRing]);
+        }
+        q_use += 2;
+        unit += 2 * n;
+      } else {
+        // tiles by turns: keys 0, keys 1, values 0, keys 2, values 1, ...
+        for (int j = 0; j < 2 && j < n; ++j, ++unit) {
+          if (j > 0 && !unit_there(unit)) return false;
+          for (int h = 0; h < 2; ++h) half_scores(j, j, h, unit);
+        }
+        for (int j = 0; j < n; ++j) {
+          const uint32_t v = unit++;
+          if (!unit_there(v)) return false;
+          for (int h = 0; h < 2; ++h) {
+            if (!half_values(j & 1, h, v, j > 1 || h > 0)) return false;
+            if (h == 1) tc_commit(&sm.empty[v % L::kRing]);
+            if (j + 2 < n) {
+              if (h == 0 && !unit_there(unit)) return false;
+              half_scores(j & 1, j + 2, h, unit);
+            }
+          }
+          if (j + 2 < n) ++unit;
+        }
+        tc_commit(&sm.o_full[0]);
+        tc_commit(&sm.o_full[1]);
+        ++q_use;
       }
-      unit += 2 * n;
-      q_use += 2;
     } else {
       const uint32_t slot = q_use % L::kQSlots;
       if (!wait(&sm.q_full[slot], q_use / L::kQSlots)) return false;
       auto tile_scores = [&](int j) {
         for (int u = 0; u < L::kKU; ++u, ++unit) {
           if (!unit_there(unit)) return false;
-          scores(j & 1, slot, unit, u);
+          scores(j & 1, slot, unit, u, 0);
           tc_commit(&sm.empty[unit % L::kRing]);
         }
         tc_commit(&sm.s_full[j & 1]);
@@ -609,7 +651,7 @@ __device__ __forceinline__ bool mma_jobs(KvSmall<D>& sm, uint32_t base, uint32_t
         tc_fence_after();
         for (int u = 0; u < L::kVU; ++u, ++unit) {
           if (!unit_there(unit)) return false;
-          values(j & 1, D == 128 ? (j & 1) * 128 : u * 128, unit, j > (D == 128 ? 1 : 0));
+          values(j & 1, u * 128, unit, j > 0, 0);
           tc_commit(&sm.empty[unit % L::kRing]);
         }
         tc_commit(&sm.pv_done[j & 1]);
@@ -651,6 +693,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_init(&sm.q_empty[i], 1);
         mbar_init(&sm.s_full[i], 1);
         mbar_init(&sm.p_full[i], 4);
+        for (int h = 0; h < 2; ++h) {
+          mbar_init(&sm.half_s[i][h], 1);
+          mbar_init(&sm.half_p[i][h], 4);
+        }
         mbar_init(&sm.o_full[i], 1);
         mbar_init(&sm.pv_done[i], 1);
         mbar_init(&sm.job_full[i], 1);
