@@ -114,6 +114,20 @@ ckv_status check_kv_pointers(const ckv_kv_cache* c, bool values) {
   return CKV_OK;
 }
 
+// The places of a cache's rows in steps of the largest power of two that divides their strides; false when
+// they do not have 32 bits.
+bool kv_side(ckv::KvSide& s, const ckv_kv_cache& c, int64_t page, int64_t row, int64_t head) {
+  const int64_t all = page | row | head | 4096, unit = all & -all;  // elements; bits below 8 are zero
+  const __int128 last = static_cast<__int128>(c.num_pages > 0 ? c.num_pages - 1 : 0) * (page / unit) +
+                        static_cast<__int128>(c.page_size - 1) * (row / unit) + static_cast<__int128>(c.heads - 1) * (head / unit);
+  if (last > UINT32_MAX) return false;
+  s.unit = static_cast<uint32_t>(unit * sizeof(uint16_t));
+  s.page = static_cast<uint32_t>(page / unit);
+  s.row = static_cast<uint32_t>(row / unit);
+  s.head = static_cast<uint32_t>(head / unit);
+  return true;
+}
+
 // Sizes of ckv_kv_attention with work to do: (token, head) rows are counted in 32 bits.
 bool kv_attention_sizes_ok(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows, int32_t window, int32_t first_rows,
                            int32_t words) {
@@ -861,6 +875,9 @@ ckv_status ckv_kv_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_str
   a.q_st = q_stride_t;
   a.q_sh = q_stride_h;
   a.cache = *cache;
+  if (!kv_side(a.k_side, *cache, cache->k_stride_page, cache->k_stride_row, cache->k_stride_head) ||
+      !kv_side(a.v_side, *cache, cache->v_stride_page, cache->v_stride_row, cache->v_stride_head))
+    return CKV_ERR_SHAPE;
   a.table = block_table;
   a.table_stride = table_stride;
   a.row_start = row_start;

@@ -228,6 +228,11 @@ struct MergeArgs {
   int32_t n, H;
 };
 
+// Rows of keys or values of a cache: their places in steps of `unit` bytes.
+struct KvSide {
+  uint32_t unit, page, row, head;
+};
+
 struct KvAttentionArgs {
   const uint16_t* q;
   int64_t q_st, q_sh;
@@ -245,6 +250,7 @@ struct KvAttentionArgs {
   int64_t T;
   int32_t H, KH, G, B, max_rows, page_shift;
   int32_t window, first, words;
+  KvSide k_side, v_side;
   int32_t same;  // one row is key and value, and the form keeps its units for both products
   float softmax_scale;
 };

@@ -53,16 +53,10 @@ struct KvLayout {
   static constexpr int kQBlock = kQRows * 128;          // 64 channels of them
   static constexpr int kQSlot = kQBlock * (D / 64);
   static constexpr int kQSlots = D == 128 ? 2 : 1;
-  static constexpr int kRing = D == 256 ? 5 : D == 128 ? 4 : 3;
+  static constexpr int kRing = D == 512 ? 3 : 5;
   static constexpr int kUnits = kQSlots * kQSlot;  // where the ring begins, behind the queries
   static constexpr int kSmall = kUnits + kRing * kKvUnit;
   static constexpr int kTmemO = 0, kTmemS = 256;  // O: 256 columns; S: two buffers of 128, P over the first half of each
-};
-
-// What a job's rows see, by the planning warp.
-template <int R>
-struct SeenRows {
-  int32_t c[R], low[R], end[R];
 };
 
 // Beside the common ones (s_full[w], p_full[w], o_full[w] and pv_done[w] are group w's; p_full: 4 warps):
@@ -73,7 +67,6 @@ struct KvSmall : KvCommon {
   uint64_t met;                   // both groups have got there: 8 warps, twice per job of shared rows
   float ref[D == 128 ? 2 : 1][128];  // references of shared rows (each group's own at D = 128)
   float sum[2][128];
-  SeenRows<D == 128 ? KvLayout<D>::kRows : 1> rows[2];
 };
 
 template <int D>
@@ -294,10 +287,7 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
     const int32_t n = job.n, v0 = job.v0, v1 = job.v1, first = job.first, low = job.low, range = job.split;
     const int i0 = (two ? w * 128 : 0) + row;
     SoftRow x = soft_row(a, job, i0);
-    x.see.c = sm.rows[job_use & 1].c[i0];
-    x.see.low = sm.rows[job_use & 1].low[i0];
-    x.see.end = sm.rows[job_use & 1].end[i0];
-    x.see.first = min(a.first, x.see.low);
+    if (x.flat >= 0) x.see = seen_by(a, x.t);
     if (x.see.c < 0) x.flat = -1;
     const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
     float ref = x.flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
@@ -733,17 +723,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       }
       __syncwarp();
     } else if (warp == kPlanWarp) {
-      ok = plan_jobs<L>(a, p, sm, jobs, [&](const Job& j, uint32_t i) {
-        if constexpr (D == 128) {
-          for (int r = lane; r < L::kRows; r += 32) {
-            Seen x{-1, 0, 0, 0};
-            if (r < j.tile.rows) x = seen_by(a, j.tile.tok0 + (j.tile.base + r) / a.G);
-            sm.rows[i].c[r] = x.c;
-            sm.rows[i].low[r] = x.low;
-            sm.rows[i].end[r] = x.end;
-          }
-        }
-      });
+      ok = plan_jobs<L>(a, p, sm, jobs, [](const Job&, uint32_t) {});
     } else if (warp >= kCopyWarp) {
       ok = copy_jobs<L>(a, sm, smem);
     }

@@ -201,31 +201,47 @@ __device__ __forceinline__ bool plan_jobs(const KvAttentionArgs& a, const KvPlan
 }
 
 // Four warps: queries, keys and values of the jobs, unit by unit, as many ahead as the ring has places.
-// Every thread's copies arrive at the unit's barrier by themselves.
+// A unit is 128 rows x 256 bytes, 32 of the rows by each warp, 16 lanes to a row; every thread's copies
+// arrive at the unit's barrier by themselves.  A lane holds the place of one row, from which the others
+// get it by a shuffle; places are counted in KvSide::unit bytes, so that they have 32 bits.
 template <typename L>
 __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm, uint8_t* smem) {
-  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - kCopyWarp, x = lane & 15;
+  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - kCopyWarp, x = lane & 15, upper = lane >> 4;
+  constexpr bool kLate = L::kRows == 256;
   uint32_t unit = 0, q_use = 0, keys_before = 0;
   auto arrive = [](uint64_t* bar) { asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory"); };
-  // kRows / 4 rows x 256 bytes by this warp, 16 lanes to a row, into blocks of 64 channels: the row in lane i
-  // begins at from + off elements (off < 0: zeros)
-  auto copy = [&](auto rows, uint8_t* to, int block, const uint16_t* from, int64_t off) {
-    constexpr int kRows = decltype(rows)::value / 4;
+  auto copy16 = [](uint32_t to, const uint8_t* from, uint32_t bytes) {  // zeros behind `bytes`
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+  };
+  // where this lane's piece of row 2 i + upper of the warp goes, from the beginning of the unit
+  uint32_t piece[4];
 #pragma unroll
-    for (int i = 0; i < kRows / 2; ++i) {
-      const int from_lane = 2 * i + (lane >> 4), r = cw * kRows + from_lane;
-      const int64_t o = __shfl_sync(0xFFFFFFFFu, off, from_lane);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                       smem_u32(to + (x >> 3) * block + r * 128 + (((x & 7) ^ (r & 7)) * 16))),
-                   "l"(from + (o >= 0 ? o : 0) + x * 8), "r"(o >= 0 ? 16 : 0)
-                   : "memory");
+  for (int i = 0; i < 4; ++i) {
+    const int r = cw * 32 + 2 * i + upper;
+    piece[i] = (x >> 3) * 16384 + r * 128 + (((x & 7) ^ (r & 7)) * 16);
+  }
+  // the warp's rows of a unit, at `at` (one per lane; only those in `on` are there)
+  auto copy_rows = [&](uint32_t to, const uint8_t* from, uint32_t at, uint32_t step, uint32_t on) {
+    if (on == 0xFFFFFFFFu) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t r = __shfl_sync(0xFFFFFFFFu, at, 2 * i + upper);
+        copy16(to + piece[i % 4] + (i / 4) * 1024, from + static_cast<uint64_t>(r) * step, 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t r = __shfl_sync(0xFFFFFFFFu, at, 2 * i + upper);
+        copy16(to + piece[i % 4] + (i / 4) * 1024, from + static_cast<uint64_t>(r) * step, (on >> (2 * i + upper)) & 1 ? 16 : 0);
+      }
     }
   };
-  auto copy_unit = [&](const uint16_t* from, int64_t off) {
-    const uint32_t place = unit % L::kRing;
-    if (unit >= L::kRing && !warp_wait(&sm.empty[place], unit / L::kRing - 1)) return false;
-    copy(std::integral_constant<int, 128>(), smem + L::kUnits + place * kKvUnit, 16384, from, off);
-    arrive(&sm.full[place]);
+  const uint32_t ring = smem_u32(smem) + L::kUnits;
+  auto has_place = [&](uint32_t c) { return c < L::kRing || warp_wait(&sm.empty[c % L::kRing], c / L::kRing - 1); };
+  auto copy_unit = [&](const uint16_t* from, uint32_t at, uint32_t step, uint32_t on) {
+    if (!has_place(unit)) return false;
+    copy_rows(ring + unit % L::kRing * kKvUnit, reinterpret_cast<const uint8_t*>(from + x * 8), at, step, on);
+    arrive(&sm.full[unit % L::kRing]);
     ++unit;
     return true;
   };
@@ -248,56 +264,76 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm
     };
     auto page_of = [&](int32_t key) { return a.page_shift >= 0 ? key >> a.page_shift : key / a.cache.page_size; };
     int32_t key = key_of(0), page = key >= 0 ? table[page_of(key)] : 0;
-    for (int w = 0; w < (two ? 2 : 1) && ok; ++w, ++q_use) {
-      const uint32_t slot = q_use % L::kQSlots;
-      ok = q_use < L::kQSlots || warp_wait(&sm.q_empty[slot], q_use / L::kQSlots - 1);
-      if (!ok) break;
-      const int32_t i = w * 128 + cw * (L::kQRows / 4) + lane, r = job.tile.base + i;
-      int64_t off = -1;
-      if (lane < L::kQRows / 4 && i < job.tile.rows) {
-        const int32_t tok = r / a.G;
-        off = (job.tile.tok0 + tok) * a.q_st + (job.kh * a.G + r - tok * a.G) * a.q_sh;
-      }
-      for (int u = 0; u < L::kKU; ++u)
-        copy(std::integral_constant<int, L::kQRows>(), smem + slot * L::kQSlot + u * 2 * L::kQBlock, L::kQBlock, a.q + u * 128, off);
-      arrive(&sm.q_full[slot]);
-    }
-    int64_t v_off = -1, v_next = -1;
+    auto queries = [&]() {
+      for (int w = 0; w < (two ? 2 : 1); ++w, ++q_use) {
+        const uint32_t slot = q_use % L::kQSlots;
+        if (q_use >= L::kQSlots && !warp_wait(&sm.q_empty[slot], q_use / L::kQSlots - 1)) return false;
+        constexpr int kMine = L::kQRows / 4;  // rows of this warp
+        const int32_t i = w * 128 + cw * kMine + lane, r = job.tile.base + i;
+        int64_t off = -1;
+        if (lane < kMine && i < job.tile.rows) {
+          const int32_t tok = r / a.G;
+          off = (job.tile.tok0 + tok) * a.q_st + (job.kh * a.G + r - tok * a.G) * a.q_sh;
+        }
+        const uint32_t to = smem_u32(smem) + slot * L::kQSlot;
 #pragma unroll 1
-    for (int j = 0; j <= job.n && ok; ++j) {
-      if (j < job.n) {
-        const uint32_t jt = keys_before + j;
-        int64_t k_off = -1;
-        v_next = -1;
-        bool missing = false;
-        if (key >= 0) {
-          const int32_t at = key - page_of(key) * a.cache.page_size;
-          if (page >= 0 && page < a.cache.num_pages) {
-            k_off = page * a.cache.k_stride_page + at * a.cache.k_stride_row + job.kh * a.cache.k_stride_head;
-            v_next = page * a.cache.v_stride_page + at * a.cache.v_stride_row + job.kh * a.cache.v_stride_head + job.half * L::kDV;
-          } else {
-            missing = true;
+        for (int u = 0; u < L::kKU; ++u) {
+#pragma unroll
+          for (int k = 0; k < kMine / 2; ++k) {
+            const int rr = cw * kMine + 2 * k + upper;
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, 2 * k + upper);
+            copy16(to + (u * 2 + (x >> 3)) * L::kQBlock + rr * 128 + (((x & 7) ^ (rr & 7)) * 16),
+                   reinterpret_cast<const uint8_t*>(a.q + (o >= 0 ? o : 0) + u * 128 + x * 8), o >= 0 ? 16 : 0);
           }
         }
+        arrive(&sm.q_full[slot]);
+      }
+      return true;
+    };
+    uint32_t v_at = 0, v_on = 0;
+#pragma unroll 1
+    for (int j = 0; j <= job.n && ok; ++j) {
+      uint32_t next_at = 0, on = 0;
+      if (j < job.n) {
+        const uint32_t jt = keys_before + j;
+        uint32_t k_at = 0;
+        bool missing = false, there = false;
+        if (key >= 0) {
+          const uint32_t row = key - page_of(key) * a.cache.page_size;
+          there = page >= 0 && page < a.cache.num_pages;
+          missing = !there;
+          if (there) {
+            k_at = page * a.k_side.page + row * a.k_side.row + job.kh * a.k_side.head;
+            next_at = page * a.v_side.page + row * a.v_side.row + job.kh * a.v_side.head;
+          }
+        }
+        on = __ballot_sync(0xFFFFFFFFu, there);
         const uint32_t gone = __ballot_sync(0xFFFFFFFFu, missing);
         key = key_of(j + 1);
         page = key >= 0 ? table[page_of(key)] : 0;
         // The tile of keys whose notes lay in this place of `bad` is eight tiles back: with a place in the ring
         // for a unit of this tile its softmax is over.
-        ok = unit < L::kRing || warp_wait(&sm.empty[unit % L::kRing], unit / L::kRing - 1);
+        ok = has_place(unit);
         if (!ok) break;
         if (lane == 0) {
           sm.bad[jt % kKvNotes][cw] = gone;
           mbar_arrive(&sm.noted[jt % kKvNotes]);
         }
-        for (int u = 0; u < L::kKU && ok; ++u) ok = copy_unit(a.cache.k + u * 128, k_off);
+        for (int u = 0; u < L::kKU && ok; ++u) {
+          // Two tiles of queries come behind the first unit, whose place is free before theirs; otherwise their place is
+          // free first, and a unit behind could have to wait for what is made of them.
+          if (!kLate && j == 0 && u == 0) ok = queries();
+          ok = ok && copy_unit(a.cache.k + u * 128, k_at, a.k_side.unit, on);
+          if (kLate && j == 0 && u == 0) ok = ok && queries();
+        }
       }
       if (a.same) continue;  // the keys' units are the values'
       if (two ? j < job.n : j > 0) {
-        const int64_t off = two ? v_next : v_off;
-        for (int u = 0; u < L::kVU && ok; ++u) ok = copy_unit(a.cache.v + u * 128, off);
+        for (int u = 0; u < L::kVU && ok; ++u)
+          ok = copy_unit(a.cache.v + job.half * L::kDV + u * 128, two ? next_at : v_at, a.v_side.unit, two ? on : v_on);
       }
-      v_off = v_next;
+      v_at = next_at;
+      v_on = on;
     }
     if (!ok) break;
     keys_before += job.n;
