@@ -122,52 +122,61 @@ __device__ __forceinline__ uint64_t twice(float x) {
   return v;
 }
 
-// A softmax thread's row.
+// A softmax thread's row: what it sees, in places of the job's list of keys.
 struct SoftRow {
-  Seen see;
-  int32_t t, flat;  // token; (token, head) index, -1: none
+  int32_t flat, t;         // (token, head) index, -1: none; token
+  int32_t a1, b0, b1, b2;  // places 0 .. a1 - 1 and b0 .. b1 - 1, and of the drafts' from b1 to b2 - 1 those with a bit
 };
 
 __device__ __forceinline__ SoftRow soft_row(const KvAttentionArgs& a, const Job& job, int32_t i) {
-  SoftRow x{{-1, 0, 0, 0}, 0, -1};
+  SoftRow x{-1, 0, 0, 0, 0, 0};
   if (i < job.tile.rows) {
     const int32_t r = job.tile.base + i, tok = r / a.G;
     x.t = job.tile.tok0 + tok;
-    x.flat = x.t * a.H + job.kh * a.G + r - tok * a.G;
+    const Seen s = seen_by(a, x.t);
+    if (s.c >= 0) {
+      x.flat = x.t * a.H + job.kh * a.G + r - tok * a.G;
+      const int32_t at = job.first - job.low;  // a row's place over its number, behind the first rows
+      x.a1 = s.first > job.low ? s.first + at : min(job.first, s.c);
+      x.b0 = max(s.low + at, job.first);
+      x.b1 = s.c + at;
+      x.b2 = s.end + at;
+    }
   }
   return x;
 }
 
-// Which of n keys (places v .. v + n - 1 of the list) the row sees, a bit each; true when that is not every one
-// of them for every row of the warp.  gone: keys whose page is not there.
+// Which of n keys (places v .. v + n - 1, v1 the list's end) the row sees, a bit each; true when that is not every
+// one of them for every row of the warp.
 template <int n>
-__device__ __forceinline__ bool tile_bits(const KvAttentionArgs& a, const SoftRow& x, int32_t first, int32_t low, int32_t v, int32_t v1,
-                                          const uint32_t* gone, uint32_t (&bits)[n / 32]) {
-  const int32_t here = min(n, v1 - v), head = first - v, k0 = low - head;  // places; those of first rows; the row of the first, were it none
-  const Seen& see = x.see;
-  const bool whole = x.flat < 0 || (here == n && k0 + n <= see.c && (head <= 0 ? k0 : low) >= see.low);
-  uint32_t lost[n / 32], some = 0;
-#pragma unroll
-  for (int i = 0; i < n / 32; ++i) some |= lost[i] = gone[i];
-  if (!__any_sync(0xFFFFFFFFu, !whole) && some == 0) return false;
-  uint32_t missed = 0;
+__device__ __forceinline__ bool tile_bits(const KvAttentionArgs& a, const SoftRow& x, const Job& job, int32_t v, int32_t v1, bool missing,
+                                          uint32_t (&bits)[n / 32]) {
+  const bool whole = x.flat < 0 || ((x.a1 >= v + n || (x.b0 <= v && x.b1 >= v + n)) && v + n <= v1);
+  if (__all_sync(0xFFFFFFFFu, whole) && !missing) return false;
 #pragma unroll
   for (int i = 0; i < n / 32; ++i) {
-    const int32_t k = k0 + i * 32, y = i * 32;
-    uint32_t m = bits_between(see.low - k, see.c - k) | bits_between(-k, see.first - k);
-    if (a.words > 0 && k + 32 > see.c && k < see.end) {  // 32 bits of the drafts' mask, from bit k - c on
-      const int32_t d = k - see.c, at = d >> 5;          // rounded down
+    const int32_t y = v + i * 32;
+    uint32_t m = bits_between(0, x.a1 - y) | bits_between(x.b0 - y, x.b1 - y);
+    if (a.words > 0 && y + 32 > x.b1 && y < x.b2) {  // 32 bits of the drafts' mask, from bit y - b1 on
+      const int32_t d = y - x.b1, at = d >> 5;       // rounded down
       const uint32_t* words = reinterpret_cast<const uint32_t*>(a.mask + static_cast<int64_t>(x.t) * a.words);
       const uint32_t lo = at >= 0 && at < 2 * a.words ? words[at] : 0u, hi = at + 1 >= 0 && at + 1 < 2 * a.words ? words[at + 1] : 0u;
-      m |= __funnelshift_r(lo, hi, d & 31) & bits_between(0, see.end - k);
+      m |= __funnelshift_r(lo, hi, d & 31) & bits_between(0, x.b2 - y);
     }
-    const uint32_t heads = bits_between(0, head - y);
-    m = (m & ~heads) | (heads & bits_between(0, see.c - v - y));  // first rows: below low of everyone who sees any
-    m &= bits_between(0, here - y);
-    missed |= m & lost[i];
-    bits[i] = m & ~lost[i];
+    bits[i] = m & bits_between(0, v1 - y);
   }
-  if (missed && x.flat >= 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
+  if (missing) {  // keys whose page is not there, a lane each
+    const int32_t* table = a.table + static_cast<int64_t>(job.tile.b) * a.table_stride;
+    uint32_t missed = 0;
+#pragma unroll
+    for (int i = 0; i < n / 32; ++i) {
+      const int32_t y = v + i * 32 + (threadIdx.x & 31), key = y < job.first ? y : job.low + y - job.first;
+      const uint32_t gone = __ballot_sync(0xFFFFFFFFu, y < v1 && !kv_page_there(a, table[kv_page_of(a, key)]));
+      missed |= bits[i] & gone;
+      bits[i] &= ~gone;
+    }
+    if (missed && x.flat >= 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
+  }
   return true;
 }
 
@@ -277,18 +286,16 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128, at_o = tmem + lanes + L::kTmemO + w * 128;
   const float c = a.softmax_scale * kLog2e;
-  uint32_t use = 0, o_use = 0, met_use = 0, keys_before = 0;  // tiles of keys of the group, jobs with keys, ...
+  uint32_t use = 0, o_use = 0, met_use = 0;  // tiles of keys of the group, jobs with keys, ...
 #pragma unroll 1
   for (uint32_t job_use = 0;; ++job_use) {
     if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
     const Job& job = sm.job[job_use & 1];
     if (!job.live) return true;
     const bool two = job.two;  // a tile of rows of its own; otherwise the groups take tiles of keys of the same rows by turns
-    const int32_t n = job.n, v0 = job.v0, v1 = job.v1, first = job.first, low = job.low, range = job.split;
-    const int i0 = (two ? w * 128 : 0) + row;
-    SoftRow x = soft_row(a, job, i0);
-    if (x.flat >= 0) x.see = seen_by(a, x.t);
-    if (x.see.c < 0) x.flat = -1;
+    const int32_t n = job.n, v0 = job.v0, v1 = job.v1, range = job.split;
+    const bool missing = job.missing;
+    const SoftRow x = soft_row(a, job, (two ? w * 128 : 0) + row);
     const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
     float ref = x.flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
     const int j0 = two ? 0 : w, step = two ? 1 : 2;
@@ -296,12 +303,10 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
     // scores to work on while the products of the other half run
 #pragma unroll 1
     for (int j = j0; j < n; j += step, ++use) {
-      const uint32_t jt = keys_before + j;
-      if (!warp_wait(&sm.noted[jt % kKvNotes], jt / kKvNotes)) return false;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         uint32_t bits[2];
-        const bool masks = any && tile_bits<64>(a, x, first, low, v0 + j * kKvKeys + h * 64, v1, &sm.bad[jt % kKvNotes][h * 2], bits);
+        const bool masks = any && tile_bits<64>(a, x, job, v0 + j * kKvKeys + h * 64, v1, missing, bits);
         const uint32_t at = at_s + h * 64;
         if (!warp_wait(&sm.half_s[w][h], use)) return false;
         tc_fence_after();
@@ -346,7 +351,6 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
         if (lane == 0) mbar_arrive(&sm.half_p[w][h]);
       }
     }
-    keys_before += n;
     // ------------------------------------------------------------------ output
     float all = l, m = ref, mine = 1.f, other = 0.f;  // shares of the two outputs
     if (!two) {
@@ -407,30 +411,28 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128, at_o = tmem + lanes + L::kTmemO;
   const float c = a.softmax_scale * kLog2e;
-  uint32_t s_use = 0, o_use = 0, met_use = 0, keys_before = 0;
+  uint32_t s_use = 0, o_use = 0, met_use = 0;
   uint32_t other_tiles = 0;  // of the other group so far
 #pragma unroll 1
   for (uint32_t job_use = 0;; ++job_use) {
     if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
     const Job& job = sm.job[job_use & 1];
     if (!job.live) return true;
-    const int32_t n = job.n, v0 = job.v0, v1 = job.v1, first = job.first, low = job.low, range = job.split, half = job.half;
-    SoftRow x = soft_row(a, job, row);
-    if (x.flat >= 0) x.see = seen_by(a, x.t);
-    if (x.see.c < 0) x.flat = -1;
+    const int32_t n = job.n, v0 = job.v0, v1 = job.v1, range = job.split, half = job.half;
+    const bool missing = job.missing;
+    const SoftRow x = soft_row(a, job, row);
     const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
     float ref = x.flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
 #pragma unroll 1
     for (int j = w; j < n; j += 2) {
-      const uint32_t jt = keys_before + j;
-      if (!warp_wait(&sm.s_full[w], s_use++) || !warp_wait(&sm.noted[jt % kKvNotes], jt / kKvNotes)) return false;
+      uint32_t bits[4];
+      const bool masks = any && tile_bits<128>(a, x, job, v0 + j * kKvKeys, v1, missing, bits);
+      if (!warp_wait(&sm.s_full[w], s_use++)) return false;
       tc_fence_after();
       if (any) {
         float z[128];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32_async(at_s + i * 32, z + i * 32);
-        uint32_t bits[4];
-        const bool masks = tile_bits<128>(a, x, first, low, v0 + j * kKvKeys, v1, sm.bad[jt % kKvNotes], bits);
         tc_wait_ld();
 #pragma unroll
         for (int i = 0; i < 4; ++i) settled32(z + i * 32);
@@ -473,7 +475,6 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.p_full[w]);
     }
-    keys_before += n;
     // ------------------------------------------------------------------ output
     other_tiles += (n + w) / 2;
     float m = ref;
@@ -673,7 +674,6 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_init(&sm.full[i], 128);
         mbar_init(&sm.empty[i], 1);
       }
-      for (int i = 0; i < kKvNotes; ++i) mbar_init(&sm.noted[i], 4);
       for (int i = 0; i < 4; ++i) {
         mbar_init(&sm.decided[0][i], 1);
         mbar_init(&sm.decided[1][i], 1);

@@ -72,6 +72,11 @@ __host__ __device__ inline int kv_tile_pad(int G, int R) {
   return g < R ? R - g : 0;
 }
 
+__device__ __forceinline__ int32_t kv_page_of(const KvAttentionArgs& a, int32_t key) {
+  return a.page_shift >= 0 ? key >> a.page_shift : key / a.cache.page_size;
+}
+__device__ __forceinline__ bool kv_page_there(const KvAttentionArgs& a, int32_t page) { return page >= 0 && page < a.cache.num_pages; }
+
 // Which request and rows a tile has.
 struct KvTile {
   int32_t b, tok0, ntok;  // the request, and its ragged rows
@@ -103,7 +108,7 @@ __device__ __forceinline__ KvTile kv_find_tile(const KvAttentionArgs& a, int32_t
 }
 
 constexpr int kKvKeys = 128, kKvUnit = 32768;  // keys of a tile; bytes of a unit
-constexpr int kKvMaxRing = 6, kKvNotes = 8;    // places of the ring; tiles of keys whose missing keys are kept
+constexpr int kKvMaxRing = 6;                  // places of the ring
 constexpr float kKvJump = 16.f;                // log2 of the largest weight over its reference
 constexpr int kMmaWarp = 8, kPlanWarp = 9, kCopyWarp = 12, kKvThreads = 512;
 
@@ -114,6 +119,7 @@ struct Job {
   int32_t v0, v1;      // of the list
   int32_t n;           // tiles of keys
   int32_t two;         // each softmax group has a tile of rows of its own
+  int32_t missing;     // pages are not there: the softmax has to look
   int32_t live;        // 0: no more jobs
 };
 
@@ -127,11 +133,9 @@ struct KvCommon {
   uint64_t o_full[2];                            // every product of a job: once per job with keys
   uint64_t pv_done[2];                           // second products of a tile of keys
   uint64_t job_full[2], job_empty[2];
-  uint64_t noted[kKvNotes];  // missing keys of a tile of keys are noted: 4 copying warps
   uint64_t drain;
   uint32_t tmem;
   Job job[2];
-  alignas(16) uint32_t bad[kKvNotes][4];  // a bit per key of a tile whose page is not there
 };
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn_major) { return idesc_f16(n, false, b_mn_major) | (1u << 7) | (1u << 10); }
@@ -153,7 +157,7 @@ __device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& 
   j.tile = kv_find_tile(a, static_cast<int32_t>(id / p.splits), L::kRows);
   j.live = 1;
   j.two = L::kRows == 256 && j.tile.rows > 128;
-  j.first = j.low = j.v0 = j.v1 = j.n = 0;
+  j.first = j.low = j.v0 = j.v1 = j.n = j.missing = 0;
   if (j.tile.rows <= 0) return j;
   // what its tokens see together
   const int32_t t0 = j.tile.tok0 + j.tile.base / a.G, t1 = j.tile.tok0 + (j.tile.base + j.tile.rows - 1) / a.G;
@@ -174,6 +178,19 @@ __device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& 
   j.v0 = static_cast<int32_t>(min(static_cast<int64_t>(j.split) * p.chunk, static_cast<int64_t>(count)));
   j.v1 = j.split == p.splits - 1 ? count : min(count, j.v0 + p.chunk);
   j.n = (j.v1 - j.v0 + kKvKeys - 1) / kKvKeys;
+  if (j.n == 0) return j;
+  // the pages of its keys: rows v0 .. first - 1, then those from the list's second part
+  const int32_t* table = a.table + static_cast<int64_t>(j.tile.b) * a.table_stride;
+  bool lost = false;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int32_t k0 = part ? j.low + max(j.v0 - j.first, 0) : j.v0, k1 = part ? j.low + j.v1 - j.first : min(j.v1, j.first);
+    if (k0 >= k1) continue;
+    const int32_t p0 = kv_page_of(a, k0), p1 = kv_page_of(a, k1 - 1);
+#pragma unroll 4
+    for (int32_t p = p0 + lane; p <= p1; p += 32) lost |= !kv_page_there(a, table[p]);
+  }
+  j.missing = __any_sync(0xFFFFFFFFu, lost);
   return j;
 }
 
@@ -208,7 +225,7 @@ template <typename L>
 __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm, uint8_t* smem) {
   const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - kCopyWarp, x = lane & 15, upper = lane >> 4;
   constexpr bool kLate = L::kRows == 256;
-  uint32_t unit = 0, q_use = 0, keys_before = 0;
+  uint32_t unit = 0, q_use = 0;
   auto arrive = [](uint64_t* bar) { asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory"); };
   auto copy16 = [](uint32_t to, const uint8_t* from, uint32_t bytes) {  // zeros behind `bytes`
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
@@ -222,17 +239,19 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm
   }
   // the warp's rows of a unit, at `at` (one per lane; only those in `on` are there)
   auto copy_rows = [&](uint32_t to, const uint8_t* from, uint32_t at, uint32_t step, uint32_t on) {
-    if (on == 0xFFFFFFFFu) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t r = __shfl_sync(0xFFFFFFFFu, at, 2 * i + upper);
-        copy16(to + piece[i % 4] + (i / 4) * 1024, from + static_cast<uint64_t>(r) * step, 16);
-      }
-    } else {
+    for (int i0 = 0; i0 < 16; i0 += 8) {
+      // the shuffles first: the compiler keeps their order with the copies, each of which would wait for its own
+      uint32_t r[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t r = __shfl_sync(0xFFFFFFFFu, at, 2 * i + upper);
-        copy16(to + piece[i % 4] + (i / 4) * 1024, from + static_cast<uint64_t>(r) * step, (on >> (2 * i + upper)) & 1 ? 16 : 0);
+      for (int i = 0; i < 8; ++i) r[i] = __shfl_sync(0xFFFFFFFFu, at, 2 * (i0 + i) + upper);
+      if (on == 0xFFFFFFFFu) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) copy16(to + piece[i % 4] + ((i0 + i) / 4) * 1024, from + static_cast<uint64_t>(r[i]) * step, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          copy16(to + piece[i % 4] + ((i0 + i) / 4) * 1024, from + static_cast<uint64_t>(r[i]) * step, (on >> (2 * (i0 + i) + upper)) & 1 ? 16 : 0);
       }
     }
   };
@@ -262,8 +281,7 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm
       const int32_t v = job.v0 + j * kKvKeys + cw * 32 + lane;
       return j >= job.n || v >= job.v1 ? -1 : v < job.first ? v : job.low + v - job.first;
     };
-    auto page_of = [&](int32_t key) { return a.page_shift >= 0 ? key >> a.page_shift : key / a.cache.page_size; };
-    int32_t key = key_of(0), page = key >= 0 ? table[page_of(key)] : 0;
+    int32_t key = key_of(0), page = key >= 0 ? table[kv_page_of(a, key)] : 0;
     auto queries = [&]() {
       for (int w = 0; w < (two ? 2 : 1); ++w, ++q_use) {
         const uint32_t slot = q_use % L::kQSlots;
@@ -295,30 +313,16 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm
     for (int j = 0; j <= job.n && ok; ++j) {
       uint32_t next_at = 0, on = 0;
       if (j < job.n) {
-        const uint32_t jt = keys_before + j;
         uint32_t k_at = 0;
-        bool missing = false, there = false;
-        if (key >= 0) {
-          const uint32_t row = key - page_of(key) * a.cache.page_size;
-          there = page >= 0 && page < a.cache.num_pages;
-          missing = !there;
-          if (there) {
-            k_at = page * a.k_side.page + row * a.k_side.row + job.kh * a.k_side.head;
-            next_at = page * a.v_side.page + row * a.v_side.row + job.kh * a.v_side.head;
-          }
+        const bool there = key >= 0 && kv_page_there(a, page);
+        if (there) {
+          const uint32_t row = key - kv_page_of(a, key) * a.cache.page_size;
+          k_at = page * a.k_side.page + row * a.k_side.row + job.kh * a.k_side.head;
+          next_at = page * a.v_side.page + row * a.v_side.row + job.kh * a.v_side.head;
         }
         on = __ballot_sync(0xFFFFFFFFu, there);
-        const uint32_t gone = __ballot_sync(0xFFFFFFFFu, missing);
         key = key_of(j + 1);
-        page = key >= 0 ? table[page_of(key)] : 0;
-        // The tile of keys whose notes lay in this place of `bad` is eight tiles back: with a place in the ring
-        // for a unit of this tile its softmax is over.
-        ok = has_place(unit);
-        if (!ok) break;
-        if (lane == 0) {
-          sm.bad[jt % kKvNotes][cw] = gone;
-          mbar_arrive(&sm.noted[jt % kKvNotes]);
-        }
+        page = key >= 0 ? table[kv_page_of(a, key)] : 0;
         for (int u = 0; u < L::kKU && ok; ++u) {
           // Two tiles of queries come behind the first unit, whose place is free before theirs; otherwise their place is
           // free first, and a unit behind could have to wait for what is made of them.
@@ -336,7 +340,6 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm
       v_on = on;
     }
     if (!ok) break;
-    keys_before += job.n;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   return ok;

@@ -101,6 +101,8 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
     const FewRows<R>& rows = sm.rows[job_use & 1];
     if (!job.live) return true;
     const int32_t n = job.n, v0 = job.v0, v1 = job.v1, head0 = job.first, low0 = job.low;
+    const bool missing = job.missing;
+    const int32_t* table = a.table + static_cast<int64_t>(job.tile.b) * a.table_stride;
     float l[kCols];
 #pragma unroll
     for (int i = 0; i < kCols; ++i) l[i] = 0.f;
@@ -109,14 +111,14 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
 #pragma unroll 1
     for (int j = 0; j < n; ++j, ++tile) {
       const int buf = tile & 1;
-      ok = mbar_wait_near(&sm.s_full[buf], (tile >> 1) & 1) && mbar_wait_near(&sm.noted[tile % kKvNotes], (tile / kKvNotes) & 1);
+      ok = mbar_wait_near(&sm.s_full[buf], (tile >> 1) & 1);
       __syncwarp();
       tc_fence_after();
       const uint32_t at_s = tmem + lanes + L::kTmemS + buf * 64 + c0;
       // the key of the thread's place, which rows may see it
       const int32_t v = v0 + j * kKvKeys, k0 = low0 + v - head0;  // first place; its row, were it none of the first ones
       const int32_t key = v + place < head0 ? v + place : k0 + place;
-      const bool gone = (sm.bad[tile % kKvNotes][quad] >> lane) & 1, there = v + place < v1 && !gone;
+      const bool gone = missing && v + place < v1 && !kv_page_there(a, table[kv_page_of(a, key)]), there = v + place < v1 && !gone;
       const bool whole = v + kKvKeys <= v1 && k0 + kKvKeys <= rows.c_min && (v >= head0 ? k0 : low0) >= rows.low_max;
       const bool masks = __any_sync(0xFFFFFFFFu, gone) || !whole;
       // scores over the references in log2 units, -infinity for what a row does not see
@@ -385,7 +387,6 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_init(&sm.full[i], 128);
         mbar_init(&sm.empty[i], 1);
       }
-      for (int i = 0; i < kKvNotes; ++i) mbar_init(&sm.noted[i], 4);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.q_full[i], 128);
         mbar_init(&sm.q_empty[i], 1);
