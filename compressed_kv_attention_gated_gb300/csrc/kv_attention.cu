@@ -146,13 +146,24 @@ __device__ __forceinline__ SoftRow soft_row(const KvAttentionArgs& a, const Job&
   return x;
 }
 
-// Which of n keys (places v .. v + n - 1, v1 the list's end) the row sees, a bit each; true when that is not every
-// one of them for every row of the warp.
+// The spans of n keys from place v0 on that every row of the warp sees whole: the first a of them, and those from b0
+// to b1 - 1.  (Rows without a token do not count.)
+struct WholeSpans {
+  int32_t a, b0, b1;
+  __device__ __forceinline__ bool operator()(int32_t i) const { return i < a || (i >= b0 && i < b1); }
+};
 template <int n>
-__device__ __forceinline__ bool tile_bits(const KvAttentionArgs& a, const SoftRow& x, const Job& job, int32_t v, int32_t v1, bool missing,
+__device__ __forceinline__ WholeSpans whole_spans(const SoftRow& x, int32_t v0, int32_t v1, bool missing) {
+  const bool on = x.flat >= 0;
+  const int32_t a1 = min(__reduce_min_sync(0xFFFFFFFFu, on ? x.a1 : INT32_MAX), v1) - v0;
+  const int32_t b0 = __reduce_max_sync(0xFFFFFFFFu, on ? x.b0 : 0) - v0, b1 = min(__reduce_min_sync(0xFFFFFFFFu, on ? x.b1 : INT32_MAX), v1) - v0;
+  return missing ? WholeSpans{0, 0, 0} : WholeSpans{a1 / n, b0 > 0 ? (b0 + n - 1) / n : 0, b1 / n};
+}
+
+// Which of n keys (places v .. v + n - 1, v1 the list's end) the row sees, a bit each.
+template <int n>
+__device__ __forceinline__ void tile_bits(const KvAttentionArgs& a, const SoftRow& x, const Job& job, int32_t v, int32_t v1, bool missing,
                                           uint32_t (&bits)[n / 32]) {
-  const bool whole = x.flat < 0 || ((x.a1 >= v + n || (x.b0 <= v && x.b1 >= v + n)) && v + n <= v1);
-  if (__all_sync(0xFFFFFFFFu, whole) && !missing) return false;
 #pragma unroll
   for (int i = 0; i < n / 32; ++i) {
     const int32_t y = v + i * 32;
@@ -177,7 +188,6 @@ __device__ __forceinline__ bool tile_bits(const KvAttentionArgs& a, const SoftRo
     }
     if (missed && x.flat >= 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
   }
-  return true;
 }
 
 template <int n>
@@ -190,11 +200,10 @@ __device__ __forceinline__ float largest(const float* z) {
 
 // n scores of the row in log2 units over its reference; -infinity for what it does not see.
 template <int n>
-__device__ __forceinline__ void over_reference(float* z, float c, float ref, bool masks, const uint32_t* bits) {
-  const uint64_t scale = twice(c), shift = twice(-ref);
+__device__ __forceinline__ void over_reference(float* z, uint64_t scale, uint64_t shift, bool masks, const uint32_t* bits) {
 #pragma unroll
   for (int i = 0; i < n; i += 2) fma2(z[i], z[i + 1], scale, shift);
-  if (masks) {
+  if (__builtin_expect(masks, 0)) {
 #pragma unroll
     for (int i = 0; i < n; ++i) z[i] = (bits[i / 32] >> (i % 32)) & 1 ? z[i] : -INFINITY;
   }
@@ -285,8 +294,9 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, w = warp >> 2, row = threadIdx.x & 127;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128, at_o = tmem + lanes + L::kTmemO + w * 128;
-  const float c = a.softmax_scale * kLog2e;
+  const uint64_t scale = twice(a.softmax_scale * kLog2e);
   uint32_t use = 0, o_use = 0, met_use = 0;  // tiles of keys of the group, jobs with keys, ...
+  uint32_t last = 0;                         // jobs in which the group had a tile
 #pragma unroll 1
   for (uint32_t job_use = 0;; ++job_use) {
     if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
@@ -297,60 +307,74 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
     const bool missing = job.missing;
     const SoftRow x = soft_row(a, job, (two ? w * 128 : 0) + row);
     const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
+    const WholeSpans whole = whole_spans<64>(x, v0, v1, missing);
     float ref = x.flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
+    uint64_t shift = twice(0.f);                       // -ref, or 0 without one
+    bool unset = any;                                  // some row of the warp may have none
     const int j0 = two ? 0 : w, step = two ? 1 : 2;
     // a tile of keys goes through in halves, each with a buffer of scores of its own, so that there are always
     // scores to work on while the products of the other half run
+    auto half = [&](int j, int h) {
+      uint32_t bits[2];
+      const bool masks = any && !whole(2 * j + h);
+      if (__builtin_expect(masks, 0)) tile_bits<64>(a, x, job, v0 + j * kKvKeys + h * 64, v1, missing, bits);
+      const uint32_t at = at_s + h * 64;
+      if (!warp_wait(&sm.half_s[w][h], use)) return false;
+      tc_fence_after();
+      if (any) {
+        float z[64];
+        tmem_ld32_async(at, z);
+        tmem_ld32_async(at + 32, z + 32);
+        tc_wait_ld();
+        settled32(z);
+        settled32(z + 32);
+        over_reference<64>(z, scale, shift, masks, bits);
+        if (__builtin_expect(unset, 0)) {  // the output of a row without a reference is 0: the reference is just set
+          const float top = ref == kNegBig ? largest<64>(z) : -INFINITY;
+          if (top > -INFINITY) {
+            ref = top;
+            shift = twice(-top);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) z[i] -= top;
+          }
+          unset = __any_sync(0xFFFFFFFFu, ref == kNegBig);
+        }
+        // weights under the reference as it is; when a row's sum shows that it has grown too old, once more
+        float sum = weights<64>(z, at);
+        while (__builtin_expect(__any_sync(0xFFFFFFFFu, sum > kKvMost), 0)) {
+          const float by = sum > kKvMost ? largest<64>(z) : 0.f, keep = fast_exp2(-by);
+          if (sum > kKvMost) {
+            ref += by;
+            shift = twice(-ref);
+          }
+          l *= keep;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) z[i] -= by;
+          if (j > j0 || h > 0) {  // the products of the half before
+            if (h == 0 && !warp_wait(&sm.half_s[w][1], use)) return false;
+            // they came before the scores that were made next: this half's, the next tile's first, or none
+            if (h == 1 && !(j + step < n ? warp_wait(&sm.half_s[w][0], use + 1) : warp_wait(&sm.pv_done[w], last))) return false;
+            tc_fence_after();
+            rescale<128>(at_o, keep);
+          }
+          tc_wait_st();
+          sum = weights<64>(z, at);
+        }
+        l += sum;
+        tc_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.half_p[w][h]);
+      return true;
+    };
 #pragma unroll 1
     for (int j = j0; j < n; j += step, ++use) {
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        uint32_t bits[2];
-        const bool masks = any && tile_bits<64>(a, x, job, v0 + j * kKvKeys + h * 64, v1, missing, bits);
-        const uint32_t at = at_s + h * 64;
-        if (!warp_wait(&sm.half_s[w][h], use)) return false;
-        tc_fence_after();
-        if (any) {
-          float z[64];
-          tmem_ld32_async(at, z);
-          tmem_ld32_async(at + 32, z + 32);
-          tc_wait_ld();
-          settled32(z);
-          settled32(z + 32);
-          const bool unset = ref == kNegBig;
-          over_reference<64>(z, c, unset ? 0.f : ref, masks, bits);
-          if (__any_sync(0xFFFFFFFFu, unset)) {  // its output is 0: the reference is just set
-            const float top = largest<64>(z);
-            if (unset && top > -INFINITY) {
-              ref = top;
-#pragma unroll
-              for (int i = 0; i < 64; ++i) z[i] -= top;
-            }
-          }
-          // weights under the reference as it is; when a row's sum shows that it has grown too old, once more
-          float sum = weights<64>(z, at);
-          while (__any_sync(0xFFFFFFFFu, sum > kKvMost)) {
-            const float by = sum > kKvMost ? largest<64>(z) : 0.f, keep = fast_exp2(-by);
-            ref += by;
-            l *= keep;
-#pragma unroll
-            for (int i = 0; i < 64; ++i) z[i] -= by;
-            if (j > j0 || h > 0) {  // the products of the half before
-              if (!warp_wait(&sm.pv_done[w], 2 * use + h - 1)) return false;
-              tc_fence_after();
-              rescale<128>(at_o, keep);
-            }
-            tc_wait_st();
-            sum = weights<64>(z, at);
-          }
-          l += sum;
-          tc_wait_st();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.half_p[w][h]);
-      }
+      for (int h = 0; h < 2; ++h)
+        if (!half(j, h)) return false;
     }
+    if (n > j0) ++last;
     // ------------------------------------------------------------------ output
     float all = l, m = ref, mine = 1.f, other = 0.f;  // shares of the two outputs
     if (!two) {
@@ -365,11 +389,13 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
       other = l1 == 0.f ? 0.f : fast_exp2(m1 - m);
       all = l * mine + l1 * other;
     }
-    const float scale = finish_row(a, p, 128, range, x.flat, all, m, two || w == 0);
-    mine *= scale;
-    other *= scale;
+    const float share = finish_row(a, p, 128, range, x.flat, all, m, two || w == 0);
+    mine *= share;
+    other *= share;
     if (n > 0) {
-      if (!warp_wait(&sm.o_full[w], o_use++)) return false;
+      // (whoever is at the output has waited for its own products of all jobs before: no phase is mistaken)
+      if (!warp_wait(&sm.o_full[w], o_use) || (!two && !warp_wait(&sm.o_full[w ^ 1], o_use))) return false;
+      ++o_use;
       tc_fence_after();
     }
     if (any) {
@@ -410,7 +436,7 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, w = warp >> 2, row = threadIdx.x & 127;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128, at_o = tmem + lanes + L::kTmemO;
-  const float c = a.softmax_scale * kLog2e;
+  const uint64_t scale = twice(a.softmax_scale * kLog2e);
   uint32_t s_use = 0, o_use = 0, met_use = 0;
   uint32_t other_tiles = 0;  // of the other group so far
 #pragma unroll 1
@@ -422,11 +448,13 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
     const bool missing = job.missing;
     const SoftRow x = soft_row(a, job, row);
     const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
+    const WholeSpans whole = whole_spans<128>(x, v0, v1, missing);
     float ref = x.flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
 #pragma unroll 1
     for (int j = w; j < n; j += 2) {
       uint32_t bits[4];
-      const bool masks = any && tile_bits<128>(a, x, job, v0 + j * kKvKeys, v1, missing, bits);
+      const bool masks = any && !whole(j);
+      if (masks) tile_bits<128>(a, x, job, v0 + j * kKvKeys, v1, missing, bits);
       if (!warp_wait(&sm.s_full[w], s_use++)) return false;
       tc_fence_after();
       if (any) {
@@ -447,7 +475,7 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
         }
         const bool unset = ref == kNegBig;
         const float shift = unset ? 0.f : ref;
-        over_reference<128>(z, c, shift, masks, bits);
+        over_reference<128>(z, scale, twice(-shift), masks, bits);
         const float over = largest<128>(z);
         if (__any_sync(0xFFFFFFFFu, over > kKvJump || (unset && over > -INFINITY))) {
           // the reference goes to the largest score so far
@@ -487,7 +515,7 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.met);
     if (!warp_wait(&sm.met, met_use++)) return false;
-    const float scale = finish_row(a, p, D, range, x.flat, l + sm.sum[w ^ 1][row], m, w == 0 && half == 0);
+    const float share = finish_row(a, p, D, range, x.flat, l + sm.sum[w ^ 1][row], m, w == 0 && half == 0);
     if (n > 0) {
       if (!warp_wait(&sm.o_full[w], o_use++)) return false;
       tc_fence_after();
@@ -499,7 +527,7 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
         if (n > 0) {
           tmem_ld<32>(at_o + i, o);
 #pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] *= scale;
+          for (int y = 0; y < 32; ++y) o[y] *= share;
         } else {
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = 0.f;
@@ -517,141 +545,148 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
   }
 }
 
-// One thread: the products, in the order of their units.
-template <int D>
-__device__ __forceinline__ bool mma_jobs(KvSmall<D>& sm, uint32_t base, uint32_t tmem) {
+// Descriptors and products of a tile's keys: kN of them at a time in the scores.
+template <int D, int kN>
+struct Products {
   using L = KvLayout<D>;
-  constexpr int kN = D == 128 ? 64 : 128;  // keys of a product of scores
-  constexpr uint32_t kIdescS = idesc_bf16(kN, false), kIdescO = idesc_bf16(128, true);
-  uint32_t unit = 0, q_use = 0, p_use[2] = {0, 0};
-  auto wait = [](uint64_t* bar, uint32_t n) { return mbar_wait_near(bar, n & 1u); };
-  auto unit_there = [&](uint32_t c) {
+  static constexpr uint32_t kIdescS = idesc_bf16(kN, false), kIdescO = idesc_bf16(128, true);
+  KvCommon& sm;
+  uint64_t k_major, mn_major;  // descriptors of operands at the beginning of shared memory; places are added in 16 bytes
+  uint32_t tmem;
+  __device__ __forceinline__ Products(KvCommon& c, uint32_t base, uint32_t t)
+      : sm(c), k_major(smem_desc_sw128(base, 16, 1024)), mn_major(smem_desc_sw128(base, kKvUnit / 2, 1024)), tmem(t) {}
+  static __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t n) { return mbar_wait_near(bar, n & 1u); }
+  static __device__ __forceinline__ uint64_t place_of(uint32_t c) { return static_cast<uint64_t>((L::kUnits + c % L::kRing * kKvUnit) >> 4); }
+  __device__ __forceinline__ bool unit_there(uint32_t c) const {
     const bool ok = wait(&sm.full[c % L::kRing], c / L::kRing);
     fence_proxy_async_smem();  // the copies are ordinary writes of other threads, done when the barrier says so
     tc_fence_after();
     return ok;
-  };
-  // scores of group w with keys kN h ...: queries in slot q, with unit c for channels 128 u ...
-  auto scores = [&](int w, uint32_t q, uint32_t c, int u, int h) {
+  }
+  // scores of group w with keys kN h ... of unit c: queries in slot q, channels 128 u ...
+  __device__ __forceinline__ void scores(int w, uint32_t q, uint32_t c, int u, int h) const {
+    const uint64_t da = k_major + ((q * L::kQSlot + u * 2 * L::kQBlock) >> 4), db = k_major + place_of(c) + ((h * kN * 128) >> 4);
+    const uint32_t to = tmem + L::kTmemS + w * 128 + h * kN;
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const uint64_t da = smem_desc_sw128(base + q * L::kQSlot + (u * 2 + s / 4) * L::kQBlock + (s % 4) * 32, 16, 1024);
-      const uint64_t db = smem_desc_sw128(base + L::kUnits + (c % L::kRing) * kKvUnit + (s / 4) * 16384 + h * 8192 + (s % 4) * 32, 16, 1024);
-      mma_f16_ss(tmem + L::kTmemS + w * 128 + h * 64, da, db, kIdescS, u > 0 || s > 0);
-    }
-  };
+    for (int s = 0; s < 8; ++s)
+      mma_f16_ss(to, da + (((s / 4) * L::kQBlock + (s % 4) * 32) >> 4), db + (((s / 4) * (kKvUnit / 2) + (s % 4) * 32) >> 4), kIdescS, u > 0 || s > 0);
+  }
   // weights of group w (of their half h) with unit c, into 128 columns of the output; 16 keys a step
-  auto values = [&](int w, uint32_t column, uint32_t c, bool more, int h) {
+  __device__ __forceinline__ void values(int w, uint32_t column, uint32_t c, bool more, int h) const {
+    const uint64_t db = mn_major + place_of(c) + ((h * kN * 128) >> 4);
+    const uint32_t from = tmem + L::kTmemS + w * 128 + h * kN;
 #pragma unroll
-    for (int s = 0; s < kN / 16; ++s) {
-      const uint64_t db = smem_desc_sw128(base + L::kUnits + (c % L::kRing) * kKvUnit + (h * 4 + s) * 2048, 16384, 1024);
-      mma_f16_ts(tmem + L::kTmemO + column, tmem + L::kTmemS + w * 128 + h * 64 + s * 8, db, kIdescO, more || s > 0);
-    }
-  };
+    for (int s = 0; s < kN / 16; ++s) mma_f16_ts(tmem + L::kTmemO + column, from + s * 8, db + (s * 2048 >> 4), kIdescO, more || s > 0);
+  }
+};
+
+// D = 128: one thread for each softmax group issues that group's products, so that one's waits and fences lie under
+// the other's products.  Barriers that give back what both use (units, queries) count two.
+__device__ __forceinline__ bool mma_apart(KvSmall<128>& sm, uint32_t base, uint32_t tmem, int w) {
+  using L = KvLayout<128>;
+  const Products<128, 64> mma(sm, base, tmem);
+  uint32_t unit = 0, q_use = 0, p_use = 0;
 #pragma unroll 1
   for (uint32_t job_use = 0;; ++job_use) {
-    if (!wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
+    if (!mma.wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
     const Job& job = sm.job[job_use & 1];
     if (!job.live) return true;
     const int n = job.n;
-    const bool two = L::kRows == 256 && job.two;
+    const bool two = job.two;
     mbar_arrive(&sm.job_empty[job_use & 1]);
     if (n == 0) continue;
-    if constexpr (D == 128) {
-      const uint32_t slot[2] = {q_use & 1, (q_use + (two ? 1 : 0)) & 1};
-      // half of a tile's scores; the last to use the queries and the unit give them back
-      auto half_scores = [&](int w, int j, int h, uint32_t c) {
-        scores(w, slot[w], c, 0, h);
+    const int j0 = two ? 0 : w, step = two ? 1 : 2;
+    const uint32_t q = q_use + (two ? w : 0), slot = q & 1;
+    auto keys_of = [&](int j) { return unit + (two || j == 0 ? 2 * j : 2 * j - 1); };
+    auto values_of = [&](int j) { return unit + (two ? 2 * j + 1 : min(j + 2, n) + j); };
+    auto give_back = [&](uint64_t* bar) {  // this group's share; all of it where the other has none
+      tc_commit(bar);
+      if (!two) tc_commit(bar);
+    };
+    if (j0 < n) {
+      if (!mma.wait(&sm.q_full[slot], q >> 1) || !mma.unit_there(keys_of(j0))) return false;
+      for (int h = 0; h < 2; ++h) {
+        mma.scores(w, slot, keys_of(j0), 0, h);
         tc_commit(&sm.half_s[w][h]);
-        if (h == 0) return;
-        if (j == n - 1) tc_commit(&sm.q_empty[slot[w]]);
-        if (!two || w == 1) tc_commit(&sm.empty[c % L::kRing]);
-      };
-      auto half_values = [&](int w, int h, uint32_t c, bool more) {
-        if (!wait(&sm.half_p[w][h], p_use[w])) return false;
-        if (h == 1) ++p_use[w];
-        tc_fence_after();
-        values(w, w * 128, c, more, h);
-        tc_commit(&sm.pv_done[w]);
-        return true;
-      };
-      if (!wait(&sm.q_full[slot[0]], q_use >> 1) || !unit_there(unit)) return false;
-      if (two) {
-        for (int w = 0; w < 2; ++w) {
-          if (w == 1 && !wait(&sm.q_full[slot[1]], (q_use + 1) >> 1)) return false;
-          fence_proxy_async_smem();
-          for (int h = 0; h < 2; ++h) half_scores(w, 0, h, unit);
-        }
-        for (int j = 0; j < n; ++j) {
-          const uint32_t v = unit + 2 * j + 1, k = v + 1;  // values of this tile, keys of the next
-          if (!unit_there(v)) return false;
-          for (int h = 0; h < 2; ++h) {
-            for (int w = 0; w < 2; ++w) {
-              if (!half_values(w, h, v, j > 0 || h > 0)) return false;
-              if (j + 1 < n) {
-                if (h == 0 && w == 0 && !unit_there(k)) return false;
-                half_scores(w, j + 1, h, k);
-              } else if (h == 1) {
-                tc_commit(&sm.o_full[w]);
-              }
-            }
-          }
-          tc_commit(&sm.empty[v % L::kRing]);
-        }
-        q_use += 2;
-        unit += 2 * n;
-      } else {
-        // tiles by turns: keys 0, keys 1, values 0, keys 2, values 1, ...
-        for (int j = 0; j < 2 && j < n; ++j, ++unit) {
-          if (j > 0 && !unit_there(unit)) return false;
-          for (int h = 0; h < 2; ++h) half_scores(j, j, h, unit);
-        }
-        for (int j = 0; j < n; ++j) {
-          const uint32_t v = unit++;
-          if (!unit_there(v)) return false;
-          for (int h = 0; h < 2; ++h) {
-            if (!half_values(j & 1, h, v, j > 1 || h > 0)) return false;
-            if (h == 1) tc_commit(&sm.empty[v % L::kRing]);
-            if (j + 2 < n) {
-              if (h == 0 && !unit_there(unit)) return false;
-              half_scores(j & 1, j + 2, h, unit);
-            }
-          }
-          if (j + 2 < n) ++unit;
-        }
-        tc_commit(&sm.o_full[0]);
-        tc_commit(&sm.o_full[1]);
-        ++q_use;
       }
-    } else {
-      const uint32_t slot = q_use % L::kQSlots;
-      if (!wait(&sm.q_full[slot], q_use / L::kQSlots)) return false;
-      auto tile_scores = [&](int j) {
-        for (int u = 0; u < L::kKU; ++u, ++unit) {
-          if (!unit_there(unit)) return false;
-          scores(j & 1, slot, unit, u, 0);
-          tc_commit(&sm.empty[unit % L::kRing]);
-        }
-        tc_commit(&sm.s_full[j & 1]);
-        if (j == n - 1) tc_commit(&sm.q_empty[slot]);
-        return true;
-      };
-      if (!tile_scores(0) || (n > 1 && !tile_scores(1))) return false;
-      for (int j = 0; j < n; ++j) {
-        if (!wait(&sm.p_full[j & 1], p_use[j & 1]++)) return false;
-        tc_fence_after();
-        for (int u = 0; u < L::kVU; ++u, ++unit) {
-          if (!unit_there(unit)) return false;
-          values(j & 1, u * 128, unit, j > 0, 0);
-          tc_commit(&sm.empty[unit % L::kRing]);
-        }
-        tc_commit(&sm.pv_done[j & 1]);
-        if (j + 2 < n && !tile_scores(j + 2)) return false;
-      }
-      tc_commit(&sm.o_full[0]);
-      tc_commit(&sm.o_full[1]);
-      ++q_use;
+      give_back(&sm.empty[keys_of(j0) % L::kRing]);
     }
+    if (j0 + step >= n) {  // the queries were used for the last time, if at all
+      tc_commit(&sm.q_empty[slot]);
+      if (two) tc_commit(&sm.q_empty[slot]);
+    }
+    for (int j = j0; j < n; j += step, ++p_use) {
+      const bool more = j + step < n;
+      const uint32_t v = values_of(j), k = keys_of(j + step);
+      if (!mma.unit_there(v)) return false;
+      for (int h = 0; h < 2; ++h) {
+        if (!mma.wait(&sm.half_p[w][h], p_use)) return false;
+        tc_fence_after();
+        mma.values(w, w * 128, v, j > j0 || h > 0, h);
+        if (more) {
+          if (h == 0 && !mma.unit_there(k)) return false;
+          mma.scores(w, slot, k, 0, h);
+          tc_commit(&sm.half_s[w][h]);
+        } else if (h == 0) {
+          tc_commit(&sm.pv_done[w]);
+        }
+      }
+      give_back(&sm.empty[v % L::kRing]);
+      if (more) {
+        give_back(&sm.empty[k % L::kRing]);
+        if (j + 2 * step >= n) {
+          tc_commit(&sm.q_empty[slot]);
+          if (two) tc_commit(&sm.q_empty[slot]);
+        }
+      }
+    }
+    tc_commit(&sm.o_full[w]);
+    unit += 2 * n;
+    q_use += two ? 2 : 1;
+  }
+}
+
+// D = 256 and 512: one thread issues the products, in the order of their units.
+template <int D>
+__device__ __forceinline__ bool mma_shared(KvSmall<D>& sm, uint32_t base, uint32_t tmem) {
+  using L = KvLayout<D>;
+  const Products<D, 128> mma(sm, base, tmem);
+  uint32_t unit = 0, q_use = 0, p_use[2] = {0, 0};
+#pragma unroll 1
+  for (uint32_t job_use = 0;; ++job_use) {
+    if (!mma.wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
+    const Job& job = sm.job[job_use & 1];
+    if (!job.live) return true;
+    const int n = job.n;
+    mbar_arrive(&sm.job_empty[job_use & 1]);
+    if (n == 0) continue;
+    const uint32_t slot = q_use % L::kQSlots;
+    if (!mma.wait(&sm.q_full[slot], q_use / L::kQSlots)) return false;
+    auto tile_scores = [&](int j) {
+      for (int u = 0; u < L::kKU; ++u, ++unit) {
+        if (!mma.unit_there(unit)) return false;
+        mma.scores(j & 1, slot, unit, u, 0);
+        tc_commit(&sm.empty[unit % L::kRing]);
+      }
+      tc_commit(&sm.s_full[j & 1]);
+      if (j == n - 1) tc_commit(&sm.q_empty[slot]);
+      return true;
+    };
+    if (!tile_scores(0) || (n > 1 && !tile_scores(1))) return false;
+    for (int j = 0; j < n; ++j) {
+      if (!mma.wait(&sm.p_full[j & 1], p_use[j & 1]++)) return false;
+      tc_fence_after();
+      for (int u = 0; u < L::kVU; ++u, ++unit) {
+        if (!mma.unit_there(unit)) return false;
+        mma.values(j & 1, u * 128, unit, j > 0, 0);
+        tc_commit(&sm.empty[unit % L::kRing]);
+      }
+      tc_commit(&sm.pv_done[j & 1]);
+      if (j + 2 < n && !tile_scores(j + 2)) return false;
+    }
+    tc_commit(&sm.o_full[0]);
+    tc_commit(&sm.o_full[1]);
+    ++q_use;
   }
 }
 
@@ -661,6 +696,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   using L = KvLayout<D>;
   // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
   extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int kIssuers = D == 128 ? 2 : 1;  // threads that issue products
   KvSmall<D>& sm = *reinterpret_cast<KvSmall<D>*>(smem + L::kSmall);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (smem_u32(smem) & 1023u) {
@@ -672,7 +708,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     if (lane == 0) {
       for (int i = 0; i < L::kRing; ++i) {
         mbar_init(&sm.full[i], 128);
-        mbar_init(&sm.empty[i], 1);
+        mbar_init(&sm.empty[i], kIssuers);
       }
       for (int i = 0; i < 4; ++i) {
         mbar_init(&sm.decided[0][i], 1);
@@ -680,7 +716,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.q_full[i], 128);
-        mbar_init(&sm.q_empty[i], 1);
+        mbar_init(&sm.q_empty[i], kIssuers);
         mbar_init(&sm.s_full[i], 1);
         mbar_init(&sm.p_full[i], 4);
         for (int h = 0; h < 2; ++h) {
@@ -690,10 +726,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_init(&sm.o_full[i], 1);
         mbar_init(&sm.pv_done[i], 1);
         mbar_init(&sm.job_full[i], 1);
-        mbar_init(&sm.job_empty[i], 13);
+        mbar_init(&sm.job_empty[i], 12 + kIssuers);
       }
       mbar_init(&sm.met, 8);
-      mbar_init(&sm.drain, 1);
+      mbar_init(&sm.drain, kIssuers);
       fence_mbar_init();
     }
     __syncwarp();
@@ -713,9 +749,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     tc_fence_before();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp || (D == 128 && warp == kMmaWarp2)) {
       if (elect_one()) {
-        ok = mma_jobs<D>(sm, smem_u32(smem), tmem);
+        if constexpr (D == 128) ok = mma_apart(sm, smem_u32(smem), tmem, warp != kMmaWarp);
+        else ok = mma_shared<D>(sm, smem_u32(smem), tmem);
         // the end of every product: tensor memory may be given back
         tc_commit(&sm.drain);
         ok = mbar_wait_near(&sm.drain, 0) && ok;

@@ -110,7 +110,7 @@ __device__ __forceinline__ KvTile kv_find_tile(const KvAttentionArgs& a, int32_t
 constexpr int kKvKeys = 128, kKvUnit = 32768;  // keys of a tile; bytes of a unit
 constexpr int kKvMaxRing = 6;                  // places of the ring
 constexpr float kKvJump = 16.f;                // log2 of the largest weight over its reference
-constexpr int kMmaWarp = 8, kPlanWarp = 9, kCopyWarp = 12, kKvThreads = 512;
+constexpr int kMmaWarp = 8, kPlanWarp = 9, kMmaWarp2 = 10, kCopyWarp = 12, kKvThreads = 512;
 
 struct Job {
   KvTile tile;
