@@ -692,7 +692,7 @@ __device__ __forceinline__ bool mma_shared(KvSmall<D>& sm, uint32_t base, uint32
 
 template <int D>
 __global__ void __launch_bounds__(kKvThreads, 1)
-    kv_attention_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ KvPlan p, int64_t jobs) {
+    kv_attention_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ KvPlan p) {
   using L = KvLayout<D>;
   // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -729,6 +729,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_init(&sm.job_empty[i], 12 + kIssuers);
       }
       mbar_init(&sm.met, 8);
+      mbar_init(&sm.wanted, 1);
+      mbar_init(&sm.taken, 1);
       mbar_init(&sm.drain, kIssuers);
       fence_mbar_init();
     }
@@ -760,7 +762,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       }
       __syncwarp();
     } else if (warp == kPlanWarp) {
-      ok = plan_jobs<L>(a, p, sm, jobs, [](const Job&, uint32_t) {});
+      ok = plan_jobs<L>(a, p, sm, [](const Job&, uint32_t) {});
     } else if (warp >= kCopyWarp) {
       ok = copy_jobs<L>(a, sm, smem);
     }
@@ -874,14 +876,11 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
 
 template <int D>
 cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cudaStream_t s) {
-  int dev = 0, sms = 0;
   cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   if ((e = set_max_smem_once<kv_attention_kernel<D>>(kv_smem_bytes<D>())) != cudaSuccess) return e;
   const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * a.KH * KvLayout<D>::kHalves;
-  return launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(jobs < sms ? jobs : sms)), dim3(kKvThreads), kv_smem_bytes<D>(), use_pdl,
-                   s, a, p, jobs);
+  return launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(jobs)), dim3(kKvThreads), kv_smem_bytes<D>(), use_pdl,
+                   s, a, p);
 }
 
 template <int D>

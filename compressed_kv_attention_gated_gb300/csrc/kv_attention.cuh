@@ -133,7 +133,10 @@ struct KvCommon {
   uint64_t o_full[2];                            // every product of a job: once per job with keys
   uint64_t pv_done[2];                           // second products of a tile of keys
   uint64_t job_full[2], job_empty[2];
+  uint64_t wanted;                               // a job, by the first copying warp
+  uint64_t taken;                                // the answer to take_job()
   uint64_t drain;
+  alignas(16) uint64_t answer[2];
   uint32_t tmem;
   Job job[2];
 };
@@ -194,26 +197,53 @@ __device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& 
   return j;
 }
 
+// A job of a CTA that has not begun, which then never does: the launch has a CTA for each job, and CTAs that are
+// there take what is left, so that none waits for another's long jobs.  -1: there is none (and none may be asked for
+// again).  By one converged warp; false when the answer does not come.
+__device__ __forceinline__ bool take_job(KvCommon& sm, uint32_t use, int64_t& id) {
+  if ((threadIdx.x & 31) == 0) {
+    fence_proxy_async_smem();  // the last answer has been read
+    mbar_arrive_expect_tx(&sm.taken, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(sm.answer)),
+                 "r"(smem_u32(&sm.taken))
+                 : "memory");
+  }
+  __syncwarp();
+  if (!warp_wait(&sm.taken, use)) return false;
+  const uint64_t lo = sm.answer[0], hi = sm.answer[1];
+  uint32_t got, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n mov.b128 r, {%2, %3};\n clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+      " selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+      : "=r"(got), "=r"(x)
+      : "l"(lo), "l"(hi));
+  __syncwarp();
+  id = got ? static_cast<int64_t>(x) : -1;
+  return true;
+}
+
 // The planning warp: jobs that have something to do, one after the other; more(job, i) adds what a form wants to
 // know of the job in place i.
 template <typename L, typename F>
-__device__ __forceinline__ bool plan_jobs(const KvAttentionArgs& a, const KvPlan& p, KvCommon& sm, int64_t jobs, F&& more) {
+__device__ __forceinline__ bool plan_jobs(const KvAttentionArgs& a, const KvPlan& p, KvCommon& sm, F&& more) {
   const int lane = threadIdx.x & 31;
-  uint32_t use = 0;
-  for (int64_t id = blockIdx.x;; id += gridDim.x) {
+  uint32_t use = 0, asked = 0;
+  for (int64_t id = blockIdx.x;;) {
     Job j;
     j.live = 0;
-    if (id < jobs) {
-      j = make_job<L>(a, p, id);
-      if (j.tile.rows <= 0) continue;
+    if (id >= 0) j = make_job<L>(a, p, id);
+    if (!j.live || j.tile.rows > 0) {
+      if (use >= 2 && !warp_wait(&sm.job_empty[use & 1], (use >> 1) - 1)) return false;
+      if (j.live) more(j, use & 1);
+      if (lane == 0) sm.job[use & 1] = j;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.job_full[use & 1]);
+      // the next one is taken when the copies of this one come to their end
+      if (j.live && !warp_wait(&sm.wanted, use)) return false;
+      ++use;
+      if (!j.live) return true;
     }
-    if (use >= 2 && !warp_wait(&sm.job_empty[use & 1], (use >> 1) - 1)) return false;
-    if (j.live) more(j, use & 1);
-    if (lane == 0) sm.job[use & 1] = j;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.job_full[use & 1]);
-    ++use;
-    if (!j.live) return true;
+    if (!take_job(sm, asked++, id)) return false;
   }
 }
 
@@ -273,6 +303,7 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.job_empty[job_use & 1]);
     if (!job.live) break;
+    if (job.n <= 1 && cw == 0 && lane == 0) mbar_arrive(&sm.wanted);
     if (job.n == 0) continue;
     const bool two = L::kRows == 256 && job.two;
     const int32_t* table = a.table + static_cast<int64_t>(job.tile.b) * a.table_stride;
@@ -311,6 +342,7 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm
     uint32_t v_at = 0, v_on = 0;
 #pragma unroll 1
     for (int j = 0; j <= job.n && ok; ++j) {
+      if (job.n > 1 && j == job.n - 2 && cw == 0 && lane == 0) mbar_arrive(&sm.wanted);
       uint32_t next_at = 0, on = 0;
       if (j < job.n) {
         uint32_t k_at = 0;

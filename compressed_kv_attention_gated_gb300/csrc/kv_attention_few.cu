@@ -370,7 +370,7 @@ __device__ __forceinline__ bool few_mma(const KvAttentionArgs& a, FewSmall<R>& s
 
 template <int D, int R>
 __global__ void __launch_bounds__(kKvThreads, 1)
-    kv_attention_few_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ KvPlan p, int64_t jobs) {
+    kv_attention_few_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ KvPlan p) {
   using L = FewLayout<D, R>;
   // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -397,6 +397,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_init(&sm.job_full[i], 1);
         mbar_init(&sm.job_empty[i], 13);
       }
+      mbar_init(&sm.wanted, 1);
+      mbar_init(&sm.taken, 1);
       mbar_init(&sm.drain, 1);
       fence_mbar_init();
     }
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     }
     __syncwarp();
   } else if (warp == kPlanWarp) {
-    ok = plan_jobs<L>(a, p, sm, jobs, [&](const Job& j, uint32_t i) {
+    ok = plan_jobs<L>(a, p, sm, [&](const Job& j, uint32_t i) {
       FewRows<R>& rows = sm.rows[i];
       int32_t c_min = INT32_MAX, low_max = 0;
       for (int r = lane; r < R; r += 32) {
@@ -469,17 +471,14 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 template <int D, int R>
 cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cudaStream_t s) {
   static_assert(few_smem_bytes<D, R>() <= 227 * 1024, "shared memory");
-  int dev = 0, sms = 0;
   cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   if ((e = set_max_smem_once<kv_attention_few_kernel<D, R>>(few_smem_bytes<D, R>())) != cudaSuccess) return e;
   const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * a.KH;
   KvAttentionArgs b = a;
   const ckv_kv_cache& c = a.cache;
   b.same = c.k == c.v && c.k_stride_page == c.v_stride_page && c.k_stride_row == c.v_stride_row && c.k_stride_head == c.v_stride_head;
-  return launch_ex(kv_attention_few_kernel<D, R>, dim3(static_cast<unsigned>(jobs < sms ? jobs : sms)), dim3(kKvThreads), few_smem_bytes<D, R>(),
-                   use_pdl, s, b, p, jobs);
+  return launch_ex(kv_attention_few_kernel<D, R>, dim3(static_cast<unsigned>(jobs)), dim3(kKvThreads), few_smem_bytes<D, R>(),
+                   use_pdl, s, b, p);
 }
 
 template <int D>
