@@ -20,6 +20,7 @@ struct KvPlan {
   int tiles;   // bound of the number of tiles
   int splits;  // ranges of keys
   int chunk;   // keys of a range (a multiple of kKvKeys); the last range takes all that are left
+  int heads;   // key heads whose jobs a CTA takes together
 };
 cudaError_t launch_kv_attention_few(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cudaStream_t s);
 
@@ -147,15 +148,16 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn_major) { retu
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t n) { return __all_sync(0xFFFFFFFFu, mbar_wait_near(bar, n & 1u)); }
 
 // ---------------------------------------------------------------------- jobs
-// Job `id`, by one converged warp; rows <= 0 when there is nothing to do in it.
+// The first job of CTA `id`, by one converged warp; rows <= 0 when there is nothing to do in it.
 template <typename L>
 __device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& p, int64_t id) {
   const int lane = threadIdx.x & 31;
   Job j;
   j.half = static_cast<int32_t>(id % L::kHalves);
   id /= L::kHalves;
-  j.kh = static_cast<int32_t>(id % a.KH);
-  id /= a.KH;
+  const int32_t groups = (a.KH + p.heads - 1) / p.heads;
+  j.kh = static_cast<int32_t>(id % groups) * p.heads;
+  id /= groups;
   j.split = static_cast<int32_t>(id % p.splits);
   j.tile = kv_find_tile(a, static_cast<int32_t>(id / p.splits), L::kRows);
   j.live = 1;
@@ -232,16 +234,17 @@ __device__ __forceinline__ bool plan_jobs(const KvAttentionArgs& a, const KvPlan
     Job j;
     j.live = 0;
     if (id >= 0) j = make_job<L>(a, p, id);
-    if (!j.live || j.tile.rows > 0) {
+    if (j.live && j.tile.rows <= 0) j.kh = a.KH;
+    for (const int32_t last = j.live ? min(j.kh + p.heads, a.KH) : 1; j.live ? j.kh < last : true; ++j.kh) {
       if (use >= 2 && !warp_wait(&sm.job_empty[use & 1], (use >> 1) - 1)) return false;
       if (j.live) more(j, use & 1);
       if (lane == 0) sm.job[use & 1] = j;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.job_full[use & 1]);
-      // the next one is taken when the copies of this one come to their end
-      if (j.live && !warp_wait(&sm.wanted, use)) return false;
-      ++use;
       if (!j.live) return true;
+      // the next one follows when the copies of this one come to their end
+      if (!warp_wait(&sm.wanted, use)) return false;
+      ++use;
     }
     if (!take_job(sm, asked++, id)) return false;
   }

@@ -473,7 +473,7 @@ cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cuda
   static_assert(few_smem_bytes<D, R>() <= 227 * 1024, "shared memory");
   cudaError_t e;
   if ((e = set_max_smem_once<kv_attention_few_kernel<D, R>>(few_smem_bytes<D, R>())) != cudaSuccess) return e;
-  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * a.KH;
+  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * ((a.KH + p.heads - 1) / p.heads);
   KvAttentionArgs b = a;
   const ckv_kv_cache& c = a.cache;
   b.same = c.k == c.v && c.k_stride_page == c.v_stride_page && c.k_stride_row == c.v_stride_row && c.k_stride_head == c.v_stride_head;
