@@ -49,6 +49,7 @@ struct KvLayout {
   static constexpr int kHalves = D == 512 ? 2 : 1;
   static constexpr int kDV = D / kHalves;               // channels of the output that a CTA has
   static constexpr int kKU = D / 128, kVU = kDV / 128;  // units of a tile's keys and values
+  static constexpr bool kFindMissing = true;            // pages that are not there, by the planning warp
   static constexpr int kQRows = 128;                    // of a slot of queries
   static constexpr int kQBlock = kQRows * 128;          // 64 channels of them
   static constexpr int kQSlot = kQBlock * (D / 64);

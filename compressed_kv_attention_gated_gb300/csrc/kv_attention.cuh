@@ -110,6 +110,7 @@ __device__ __forceinline__ KvTile kv_find_tile(const KvAttentionArgs& a, int32_t
 
 constexpr int kKvKeys = 128, kKvUnit = 32768;  // keys of a tile; bytes of a unit
 constexpr int kKvMaxRing = 6;                  // places of the ring
+constexpr int kKvShort = 2;                    // tiles of keys of a job behind which the next one is taken at once
 constexpr float kKvJump = 16.f;                // log2 of the largest weight over its reference
 constexpr int kMmaWarp = 8, kPlanWarp = 9, kMmaWarp2 = 10, kCopyWarp = 12, kKvThreads = 512;
 
@@ -120,7 +121,7 @@ struct Job {
   int32_t v0, v1;      // of the list
   int32_t n;           // tiles of keys
   int32_t two;         // each softmax group has a tile of rows of its own
-  int32_t missing;     // pages are not there: the softmax has to look
+  int32_t missing;     // pages are not there: the softmax has to look (where L::kFindMissing; else it always does)
   int32_t live;        // 0: no more jobs
 };
 
@@ -134,7 +135,7 @@ struct KvCommon {
   uint64_t o_full[2];                            // every product of a job: once per job with keys
   uint64_t pv_done[2];                           // second products of a tile of keys
   uint64_t job_full[2], job_empty[2];
-  uint64_t wanted;                               // a job, by the first copying warp
+  uint64_t wanted;                               // a job behind a long one, by the first copying warp
   uint64_t taken;                                // the answer to take_job()
   uint64_t drain;
   alignas(16) uint64_t answer[2];
@@ -183,7 +184,7 @@ __device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& 
   j.v0 = static_cast<int32_t>(min(static_cast<int64_t>(j.split) * p.chunk, static_cast<int64_t>(count)));
   j.v1 = j.split == p.splits - 1 ? count : min(count, j.v0 + p.chunk);
   j.n = (j.v1 - j.v0 + kKvKeys - 1) / kKvKeys;
-  if (j.n == 0) return j;
+  if (j.n == 0 || !L::kFindMissing) return j;
   // the pages of its keys: rows v0 .. first - 1, then those from the list's second part
   const int32_t* table = a.table + static_cast<int64_t>(j.tile.b) * a.table_stride;
   bool lost = false;
@@ -229,7 +230,7 @@ __device__ __forceinline__ bool take_job(KvCommon& sm, uint32_t use, int64_t& id
 template <typename L, typename F>
 __device__ __forceinline__ bool plan_jobs(const KvAttentionArgs& a, const KvPlan& p, KvCommon& sm, F&& more) {
   const int lane = threadIdx.x & 31;
-  uint32_t use = 0, asked = 0;
+  uint32_t use = 0, asked = 0, wanted = 0;
   for (int64_t id = blockIdx.x;;) {
     Job j;
     j.live = 0;
@@ -242,9 +243,9 @@ __device__ __forceinline__ bool plan_jobs(const KvAttentionArgs& a, const KvPlan
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.job_full[use & 1]);
       if (!j.live) return true;
-      // the next one follows when the copies of this one come to their end
-      if (!warp_wait(&sm.wanted, use)) return false;
       ++use;
+      // the next one follows a long one when the copies of this one come to their end
+      if (j.n > kKvShort && !warp_wait(&sm.wanted, wanted++)) return false;
     }
     if (!take_job(sm, asked++, id)) return false;
   }
@@ -306,7 +307,6 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.job_empty[job_use & 1]);
     if (!job.live) break;
-    if (job.n <= 1 && cw == 0 && lane == 0) mbar_arrive(&sm.wanted);
     if (job.n == 0) continue;
     const bool two = L::kRows == 256 && job.two;
     const int32_t* table = a.table + static_cast<int64_t>(job.tile.b) * a.table_stride;
@@ -345,7 +345,7 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm
     uint32_t v_at = 0, v_on = 0;
 #pragma unroll 1
     for (int j = 0; j <= job.n && ok; ++j) {
-      if (job.n > 1 && j == job.n - 2 && cw == 0 && lane == 0) mbar_arrive(&sm.wanted);
+      if (job.n > kKvShort && j == job.n - 2 && cw == 0 && lane == 0) mbar_arrive(&sm.wanted);
       uint32_t next_at = 0, on = 0;
       if (j < job.n) {
         uint32_t k_at = 0;

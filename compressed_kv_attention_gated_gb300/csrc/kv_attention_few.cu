@@ -42,6 +42,7 @@ struct FewLayout {
   static constexpr int kRows = R, kHalves = 1, kDV = D;
   static constexpr int kKU = D / 128, kVU = D / 128;
   static constexpr int kQRows = R;
+  static constexpr bool kFindMissing = false;  // a softmax thread looks up the page of its key while it waits
   static constexpr int kQBlock = R * 128;
   static constexpr int kQSlot = kQBlock * (D / 64);
   static constexpr int kQSlots = kQSlot <= 16384 ? 2 : 1;
@@ -101,7 +102,6 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
     const FewRows<R>& rows = sm.rows[job_use & 1];
     if (!job.live) return true;
     const int32_t n = job.n, v0 = job.v0, v1 = job.v1, head0 = job.first, low0 = job.low;
-    const bool missing = job.missing;
     const int32_t* table = a.table + static_cast<int64_t>(job.tile.b) * a.table_stride;
     float l[kCols];
 #pragma unroll
@@ -111,14 +111,14 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
 #pragma unroll 1
     for (int j = 0; j < n; ++j, ++tile) {
       const int buf = tile & 1;
+      // the key of the thread's place, which rows may see it
+      const int32_t v = v0 + j * kKvKeys, k0 = low0 + v - head0;  // first place; its row, were it none of the first ones
+      const int32_t key = v + place < head0 ? v + place : k0 + place;
+      const bool gone = v + place < v1 && !kv_page_there(a, table[kv_page_of(a, key)]), there = v + place < v1 && !gone;
       ok = mbar_wait_near(&sm.s_full[buf], (tile >> 1) & 1);
       __syncwarp();
       tc_fence_after();
       const uint32_t at_s = tmem + lanes + L::kTmemS + buf * 64 + c0;
-      // the key of the thread's place, which rows may see it
-      const int32_t v = v0 + j * kKvKeys, k0 = low0 + v - head0;  // first place; its row, were it none of the first ones
-      const int32_t key = v + place < head0 ? v + place : k0 + place;
-      const bool gone = missing && v + place < v1 && !kv_page_there(a, table[kv_page_of(a, key)]), there = v + place < v1 && !gone;
       const bool whole = v + kKvKeys <= v1 && k0 + kKvKeys <= rows.c_min && (v >= head0 ? k0 : low0) >= rows.low_max;
       const bool masks = __any_sync(0xFFFFFFFFu, gone) || !whole;
       // scores over the references in log2 units, -infinity for what a row does not see
@@ -167,11 +167,11 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
       };
       float z[kCols];
       read_scores(z);
-      const float over = over_refs(z);
-      if (group_any(w, over > kKvJump || !ok)) {
+      // a job's first tile sets the references (nothing is lost where that was not to be known)
+      if (group_any(w, !ok || j == 0 || over_refs(z) > kKvJump)) {
         if (group_any(w, !ok)) return false;
         // new references: the largest score so far of each row
-        read_scores(z);
+        if (j > 0) read_scores(z);
         const float top = reduce_columns<kCols, true>(z, lane);
         constexpr int kShare = 32 / kCols;  // lanes that hold the same row's result
         if (lane % kShare == 0) sm.part[quad][c0 + lane / kShare] = top;
@@ -279,16 +279,26 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
           if (flat >= 0) part_out[(range + flat) * D + ch] = o[i] * l[i];
         }
       } else {
-        // neighbouring lanes (channels) trade halves: the even one has both channels of row i, the odd one of row i + 1
+        // Through the place of P, whose last product is done, so that rows leave in 16-byte pieces.  Neighbouring lanes
+        // (channels) trade halves: the even one has both channels of row i, the odd one of row i + 1.
         const bool odd = lane & 1;
+        uint8_t* stage = smem + L::kP + (c0 + (odd ? 1 : 0)) * 256 + (quad * 32 + (lane & ~1)) * 2;
 #pragma unroll
         for (int i = 0; i < kCols; i += 2) {
           const float o0 = o[i] * l[i], o1 = o[i + 1] * l[i + 1];
           const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? o0 : o1, 1);
-          const int32_t flat = rows.flat[c0 + i + (odd ? 1 : 0)];
-          if (flat >= 0)
-            *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(flat) * D + (ch & ~1)) = odd ? pack_bf16x2_rn(got, o1) : pack_bf16x2_rn(o0, got);
+          *reinterpret_cast<uint32_t*>(stage + i * 256) = odd ? pack_bf16x2_rn(got, o1) : pack_bf16x2_rn(o0, got);
         }
+        group_barrier(w);
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i) {
+          const int r = c0 + i * 8 + place / 16;
+          const int32_t flat = rows.flat[r];
+          if (flat >= 0)
+            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(flat) * D + u * 128 + place % 16 * 8) =
+                *reinterpret_cast<const uint4*>(smem + L::kP + r * 256 + place % 16 * 16);
+        }
+        group_barrier(w);
       }
     }
     tc_fence_before();
