@@ -296,8 +296,8 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128, at_o = tmem + lanes + L::kTmemO + w * 128;
   const uint64_t scale = twice(a.softmax_scale * kLog2e);
-  uint32_t use = 0, o_use = 0, met_use = 0;  // tiles of keys of the group, jobs with keys, ...
-  uint32_t last = 0;                         // jobs in which the group had a tile
+  uint32_t use = 0, met_use = 0;    // tiles of keys of the group, ...
+  uint32_t o_use[2] = {0, 0};       // jobs in which a group had a tile of keys
 #pragma unroll 1
   for (uint32_t job_use = 0;; ++job_use) {
     if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
@@ -354,7 +354,7 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
           if (j > j0 || h > 0) {  // the products of the half before
             if (h == 0 && !warp_wait(&sm.half_s[w][1], use)) return false;
             // they came before the scores that were made next: this half's, the next tile's first, or none
-            if (h == 1 && !(j + step < n ? warp_wait(&sm.half_s[w][0], use + 1) : warp_wait(&sm.pv_done[w], last))) return false;
+            if (h == 1 && !(j + step < n ? warp_wait(&sm.half_s[w][0], use + 1) : warp_wait(&sm.pv_done[w], o_use[w]))) return false;
             tc_fence_after();
             rescale<128>(at_o, keep);
           }
@@ -375,7 +375,6 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
       for (int h = 0; h < 2; ++h)
         if (!half(j, h)) return false;
     }
-    if (n > j0) ++last;
     // ------------------------------------------------------------------ output
     float all = l, m = ref, mine = 1.f, other = 0.f;  // shares of the two outputs
     if (!two) {
@@ -393,12 +392,11 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
     const float share = finish_row(a, p, 128, range, x.flat, all, m, two || w == 0);
     mine *= share;
     other *= share;
-    if (n > 0) {
-      // (whoever is at the output has waited for its own products of all jobs before: no phase is mistaken)
-      if (!warp_wait(&sm.o_full[w], o_use) || (!two && !warp_wait(&sm.o_full[w ^ 1], o_use))) return false;
-      ++o_use;
-      tc_fence_after();
-    }
+    // a group without a tile of keys has no products to wait for, and its thread for them could be a job ahead
+    if (n > j0 && !warp_wait(&sm.o_full[w], o_use[w])) return false;
+    if (!two && n > (w ^ 1) && !warp_wait(&sm.o_full[w ^ 1], o_use[w ^ 1])) return false;
+    for (int g = 0; g < 2; ++g) o_use[g] += n > (two ? 0 : g);
+    tc_fence_after();
     if (any) {
 #pragma unroll 1
       for (int i = two ? 0 : w * 64; i < (two ? 128 : w * 64 + 64); i += 32) {
@@ -582,11 +580,12 @@ struct Products {
 };
 
 // D = 128: one thread for each softmax group issues that group's products, so that one's waits and fences lie under
-// the other's products.  Barriers that give back what both use (units, queries) count two.
+// the other's products.  Both go through all units and queries, and a place is given back when both are through with
+// it: a thread that left out what the other uses could not tell the phases of the barriers apart.
 __device__ __forceinline__ bool mma_apart(KvSmall<128>& sm, uint32_t base, uint32_t tmem, int w) {
   using L = KvLayout<128>;
   const Products<128, 64> mma(sm, base, tmem);
-  uint32_t unit = 0, q_use = 0, p_use = 0;
+  uint32_t unit = 0, next = 0, q_use = 0, p_use = 0;  // next: the first unit that has not been waited for
 #pragma unroll 1
   for (uint32_t job_use = 0;; ++job_use) {
     if (!mma.wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
@@ -596,53 +595,66 @@ __device__ __forceinline__ bool mma_apart(KvSmall<128>& sm, uint32_t base, uint3
     const bool two = job.two;
     mbar_arrive(&sm.job_empty[job_use & 1]);
     if (n == 0) continue;
+    // tiles of keys of the group, and where its queries are
     const int j0 = two ? 0 : w, step = two ? 1 : 2;
     const uint32_t q = q_use + (two ? w : 0), slot = q & 1;
     auto keys_of = [&](int j) { return unit + (two || j == 0 ? 2 * j : 2 * j - 1); };
     auto values_of = [&](int j) { return unit + (two ? 2 * j + 1 : min(j + 2, n) + j); };
-    auto give_back = [&](uint64_t* bar) {  // this group's share; all of it where the other has none
-      tc_commit(bar);
-      if (!two) tc_commit(bar);
+    // units up to c - 1, which the other thread uses
+    auto pass_to = [&](uint32_t c) {
+      for (; next < c; ++next) {
+        if (!mma.wait(&sm.full[next % L::kRing], next / L::kRing)) return false;
+        mbar_arrive(&sm.empty[next % L::kRing]);
+      }
+      return true;
+    };
+    auto own_unit = [&](uint32_t c) {
+      const bool ok = pass_to(c) && mma.unit_there(c);
+      next = c + 1;
+      return ok;
+    };
+    auto pass_queries = [&](uint32_t i) {
+      if (!mma.wait(&sm.q_full[i & 1], i >> 1)) return false;
+      mbar_arrive(&sm.q_empty[i & 1]);
+      return true;
     };
     if (j0 < n) {
-      if (!mma.wait(&sm.q_full[slot], q >> 1) || !mma.unit_there(keys_of(j0))) return false;
+      if (!mma.wait(&sm.q_full[slot], q >> 1) || !own_unit(keys_of(j0))) return false;
       for (int h = 0; h < 2; ++h) {
         mma.scores(w, slot, keys_of(j0), 0, h);
         tc_commit(&sm.half_s[w][h]);
       }
-      give_back(&sm.empty[keys_of(j0) % L::kRing]);
-    }
-    if (j0 + step >= n) {  // the queries were used for the last time, if at all
-      tc_commit(&sm.q_empty[slot]);
-      if (two) tc_commit(&sm.q_empty[slot]);
+      tc_commit(&sm.empty[keys_of(j0) % L::kRing]);
+      if (j0 + step >= n) tc_commit(&sm.q_empty[slot]);  // used for the last time
+      if (two && !pass_queries(q_use + (w ^ 1))) return false;
+    } else if (!pass_queries(q)) {
+      return false;
     }
     for (int j = j0; j < n; j += step, ++p_use) {
       const bool more = j + step < n;
       const uint32_t v = values_of(j), k = keys_of(j + step);
-      if (!mma.unit_there(v)) return false;
+      if (!own_unit(v)) return false;
       for (int h = 0; h < 2; ++h) {
         if (!mma.wait(&sm.half_p[w][h], p_use)) return false;
         tc_fence_after();
         mma.values(w, w * 128, v, j > j0 || h > 0, h);
         if (more) {
-          if (h == 0 && !mma.unit_there(k)) return false;
+          if (h == 0 && !own_unit(k)) return false;
           mma.scores(w, slot, k, 0, h);
           tc_commit(&sm.half_s[w][h]);
         } else if (h == 0) {
           tc_commit(&sm.pv_done[w]);
         }
       }
-      give_back(&sm.empty[v % L::kRing]);
+      tc_commit(&sm.empty[v % L::kRing]);
       if (more) {
-        give_back(&sm.empty[k % L::kRing]);
-        if (j + 2 * step >= n) {
-          tc_commit(&sm.q_empty[slot]);
-          if (two) tc_commit(&sm.q_empty[slot]);
-        }
+        tc_commit(&sm.empty[k % L::kRing]);
+        if (j + 2 * step >= n) tc_commit(&sm.q_empty[slot]);
       }
     }
-    tc_commit(&sm.o_full[w]);
+    if (j0 < n) tc_commit(&sm.o_full[w]);
     unit += 2 * n;
+    if (!pass_to(unit)) return false;
     q_use += two ? 2 : 1;
   }
 }

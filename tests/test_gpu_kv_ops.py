@@ -275,6 +275,18 @@ def test_long_rows_of_few_tokens(ck, D, H, KH, before, window):
     s.check(out, lse)
 
 
+@pytest.mark.parametrize("D,H,KH,tokens,before,window", [
+    (128, 64, 8, 9, 40, 16), (128, 64, 8, 9, 300, 130), (128, 8, 1, 16, 20, 0), (128, 64, 8, 1, 60, 20), (256, 32, 2, 9, 100, 60),
+    (512, 130, 2, 1, 90, 40), (128, 40, 8, 60, 150, 100), (512, 64, 1, 1, 150, 0), (256, 64, 8, 1, 400, 0), (128, 64, 4, 2, 200, 129)])
+def test_many_short_jobs(ck, D, H, KH, tokens, before, window):
+    """Hundreds of tiles of rows with one tile of keys, two or three, one after the other on an SM."""
+    B = max(4, 500 // KH)
+    s = Step(D, H, KH, [tokens + (i % 3 == 0) for i in range(B)], [max(0, before - i % 50) for i in range(B)], 16, window, 2 if window else 0, seed=D + before)
+    out, lse, err = s.run(ck)
+    assert int(err) == 0
+    s.check(out, lse)
+
+
 def test_rows_left_alone(ck):
     s = Step(128, 8, 2, [3, 2, 2], [20, 140, 3], seed=3)
     T = s.q.shape[0]
