@@ -279,24 +279,29 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
           if (flat >= 0) part_out[(range + flat) * D + ch] = o[i] * l[i];
         }
       } else {
-        // Through the place of P, whose last product is done, so that rows leave in 16-byte pieces.  Neighbouring lanes
-        // (channels) trade halves: the even one has both channels of row i, the odd one of row i + 1.
+        // Through the group's own pieces of P, whose last product is done (the other group may be a job ahead and writing
+        // its own), so that rows leave in 16-byte pieces.  Neighbouring lanes (channels) trade halves: the even one has
+        // both channels of row i, the odd one of row i + 1.
+        auto piece_of = [&](int r, int y) {  // piece y of the group's row r
+          const int at = r % 8 * 16 + (y ^ (r % 2 * 4));
+          return smem + L::kP + at * 128 + ((c0 / 8 + r / 8) ^ (at & 7)) * 16;
+        };
         const bool odd = lane & 1;
-        uint8_t* stage = smem + L::kP + (c0 + (odd ? 1 : 0)) * 256 + (quad * 32 + (lane & ~1)) * 2;
 #pragma unroll
         for (int i = 0; i < kCols; i += 2) {
           const float o0 = o[i] * l[i], o1 = o[i + 1] * l[i + 1];
           const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? o0 : o1, 1);
-          *reinterpret_cast<uint32_t*>(stage + i * 256) = odd ? pack_bf16x2_rn(got, o1) : pack_bf16x2_rn(o0, got);
+          *reinterpret_cast<uint32_t*>(piece_of(i + (odd ? 1 : 0), quad * 4 + lane / 8) + lane % 8 / 2 * 4) =
+              odd ? pack_bf16x2_rn(got, o1) : pack_bf16x2_rn(o0, got);
         }
         group_barrier(w);
 #pragma unroll
         for (int i = 0; i < kCols / 8; ++i) {
-          const int r = c0 + i * 8 + place / 16;
-          const int32_t flat = rows.flat[r];
+          const int r = i * 8 + place / 16;
+          const int32_t flat = rows.flat[c0 + r];
           if (flat >= 0)
             *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(flat) * D + u * 128 + place % 16 * 8) =
-                *reinterpret_cast<const uint4*>(smem + L::kP + r * 256 + place % 16 * 16);
+                *reinterpret_cast<const uint4*>(piece_of(r, place % 16));
         }
         group_barrier(w);
       }

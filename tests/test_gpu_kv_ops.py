@@ -287,6 +287,29 @@ def test_many_short_jobs(ck, D, H, KH, tokens, before, window):
     s.check(out, lse)
 
 
+@pytest.mark.parametrize("D,H,KH,n,before,window", [
+    (128, 64, 8, 1, 1100, 1024), (128, 64, 8, 1, 140, 100), (128, 32, 2, 2, 300, 0), (256, 32, 2, 1, 300, 200), (512, 64, 1, 1, 200, 128),
+    (512, 48, 2, 2, 150, 0), (128, 64, 8, 16, 500, 400), (128, 32, 8, 40, 300, 0), (256, 32, 2, 40, 300, 0)])
+def test_the_same_call_gives_the_same_bits(ck, D, H, KH, n, before, window):
+    """Sums have a fixed order, and what the warps of a CTA leave one another in shared memory is not yet written over."""
+    g = torch.Generator(device="cuda").manual_seed(D + before)
+    B, ps = 200, 16
+    width = -(-(before + n) // ps)
+    table = torch.randperm(B * width, generator=g, device="cuda").int().view(B, width)
+    k, v = (torch.randn(B * width, ps, KH, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(B * n, H, D, generator=g, device="cuda").bfloat16()
+    ctx = _i32([before - b % 90 + i + 1 for b in range(B) for i in range(n)])
+    start = _i32(range(0, B * n + 1, n))
+
+    def call():
+        return ck.ckv_kv_attention(q, k, v, table, start, ctx, before + n, D ** -0.5, window=window)
+
+    out, lse = call()
+    for _ in range(30):
+        again = call()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
 def test_rows_left_alone(ck):
     s = Step(128, 8, 2, [3, 2, 2], [20, 140, 3], seed=3)
     T = s.q.shape[0]
