@@ -26,9 +26,6 @@
 // of the values that they multiply (by 2^-9 of their value on average); sums are of unrounded
 // ones, in fp32, as are scores and outputs.
 //
-// At D = 512 two CTAs have a tile, each forming the scores and half of the channels of the output,
-// which would fill tensor memory.
-//
 // Few tiles with many keys are split into ranges of keys; their results (fp32, and lse) go through
 // the workspace and are joined by a second kernel in a fixed order.
 #include <algorithm>
@@ -46,15 +43,13 @@ template <int D_>
 struct KvLayout {
   static constexpr int D = D_;
   static constexpr int kRows = D == 128 ? 256 : 128;    // of a job
-  static constexpr int kHalves = D == 512 ? 2 : 1;
-  static constexpr int kDV = D / kHalves;               // channels of the output that a CTA has
-  static constexpr int kKU = D / 128, kVU = kDV / 128;  // units of a tile's keys and values
+  static constexpr int kKU = D / 128;                   // units of a tile's keys, and of its values
   static constexpr bool kFindMissing = true;            // pages that are not there, by the planning warp
   static constexpr int kQRows = 128;                    // of a slot of queries
   static constexpr int kQBlock = kQRows * 128;          // 64 channels of them
   static constexpr int kQSlot = kQBlock * (D / 64);
   static constexpr int kQSlots = D == 128 ? 2 : 1;
-  static constexpr int kRing = D == 512 ? 3 : 5;
+  static constexpr int kRing = 5;
   static constexpr int kUnits = kQSlots * kQSlot;  // where the ring begins, behind the queries
   static constexpr int kSmall = kUnits + kRing * kKvUnit;
   static constexpr int kTmemO = 0, kTmemS = 256;  // O: 256 columns; S: two buffers of 128, P over the first half of each
@@ -74,7 +69,7 @@ template <int D>
 constexpr int kv_smem_bytes() {
   return KvLayout<D>::kSmall + static_cast<int>(sizeof(KvSmall<D>));
 }
-static_assert(kv_smem_bytes<128>() <= 227 * 1024 && kv_smem_bytes<256>() <= 227 * 1024 && kv_smem_bytes<512>() <= 227 * 1024, "shared memory");
+static_assert(kv_smem_bytes<128>() <= 227 * 1024 && kv_smem_bytes<256>() <= 227 * 1024, "shared memory");
 
 // 32 columns of the warp's lanes; the values are there after tc_wait_ld() and settled32().
 __device__ __forceinline__ void tmem_ld32_async(uint32_t addr, float* v) {
@@ -443,7 +438,7 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
     if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
     const Job& job = sm.job[job_use & 1];
     if (!job.live) return true;
-    const int32_t n = job.n, v0 = job.v0, v1 = job.v1, range = job.split, half = job.half;
+    const int32_t n = job.n, v0 = job.v0, v1 = job.v1, range = job.split;
     const bool missing = job.missing;
     const SoftRow x = soft_row(a, job, row);
     const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
@@ -487,7 +482,7 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
           if (j > 0 && __any_sync(0xFFFFFFFFu, keep != 1.f)) {
             if (!warp_wait(&sm.pv_done[w ^ 1], others - 1)) return false;  // the products of the tile before
             tc_fence_after();
-            rescale<L::kDV>(at_o, keep);
+            rescale<D>(at_o, keep);
           }
         }
         sm.ref[0][row] = ref;
@@ -514,14 +509,14 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.met);
     if (!warp_wait(&sm.met, met_use++)) return false;
-    const float share = finish_row(a, p, D, range, x.flat, l + sm.sum[w ^ 1][row], m, w == 0 && half == 0);
+    const float share = finish_row(a, p, D, range, x.flat, l + sm.sum[w ^ 1][row], m, w == 0);
     if (n > 0) {
       if (!warp_wait(&sm.o_full[w], o_use++)) return false;
       tc_fence_after();
     }
     if (any) {
 #pragma unroll 1
-      for (int i = w * (L::kDV / 2); i < (w + 1) * (L::kDV / 2); i += 32) {
+      for (int i = w * (D / 2); i < (w + 1) * (D / 2); i += 32) {
         float o[32];
         if (n > 0) {
           tmem_ld<32>(at_o + i, o);
@@ -531,7 +526,7 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = 0.f;
         }
-        put_row(a, p, D, range, x.flat, half * L::kDV + i, o);
+        put_row(a, p, D, range, x.flat, i, o);
       }
     }
     tc_fence_before();
@@ -689,7 +684,7 @@ __device__ __forceinline__ bool mma_shared(KvSmall<D>& sm, uint32_t base, uint32
     for (int j = 0; j < n; ++j) {
       if (!mma.wait(&sm.p_full[j & 1], p_use[j & 1]++)) return false;
       tc_fence_after();
-      for (int u = 0; u < L::kVU; ++u, ++unit) {
+      for (int u = 0; u < L::kKU; ++u, ++unit) {
         if (!mma.unit_there(unit)) return false;
         mma.values(j & 1, u * 128, unit, j > 0, 0);
         tc_commit(&sm.empty[unit % L::kRing]);
@@ -859,15 +854,19 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
   KvPlan p;
   const int G = H / KH;
   const int64_t rows = (T + B - 1) / B * G;  // of an average request and key head
-  const int R = p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : D == 128 ? 256 : 128;
+  // At D = 512 a tile of 128 rows has no place in tensor memory beside its scores, and two CTAs that form them both for half
+  // of the channels each take longer than tiles of 64 rows (8000 tokens x 64 heads, windows of 128 to 4096 rows: 698 against
+  // 315 us, 1659 against 1323, 3211 against 2965).  Below it, longer tiles win (D = 256, 32 heads, 4096: 631 against 942).
+  const int R = p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D == 512 ? 64 : D == 128 ? 256 : 128;
   const int64_t pad = kv_tile_pad(G, R);
   p.tiles = static_cast<int>((T * G + static_cast<int64_t>(B) * pad) / R);
   int64_t busy = (T * G + R - 1) / R;
   busy = busy < T && busy < B ? (T < B ? T : B) : busy;
-  busy *= static_cast<int64_t>(KH) * (D == 512 ? 2 : 1);
-  // keys that a tile's tokens see together when they follow each other
+  busy *= KH;
+  // keys that a tile's tokens, `tokens` at most, see together when they follow each other
   int64_t span = max_rows;
-  if (window > 0) span = std::min<int64_t>(max_rows, static_cast<int64_t>(window) + first + R / G + 64 * words);
+  const int g = G & -G, tokens = (G - std::min(g, R) + R + G - 1) / G;
+  if (window > 0) span = std::min<int64_t>(max_rows, static_cast<int64_t>(window) + first + tokens - 1 + 64 * words);
   const int64_t most = (span + kKvKeys - 1) / kKvKeys;
   const double around = 2.0, tile = D == 512 ? 2.0 : D == 256 ? 1.2 : 0.8;
   const int64_t least = (span + kKvMaxRange - 1) / kKvMaxRange;  // <= kKvMaxSplits: the callers' bound of max_rows
@@ -887,7 +886,7 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
   // What a job is about is looked up once for several key heads where jobs are short (a lookup takes 4 us, a tile of keys
   // 1.5) and leave each SM six CTAs all the same: 1024 requests x 64 heads over 128 rows 209 -> 158 us.
   p.heads = 1;
-  const int64_t ctas = static_cast<int64_t>(p.tiles) * p.splits * KH * (D == 512 && R == 128 ? 2 : 1);
+  const int64_t ctas = static_cast<int64_t>(p.tiles) * p.splits * KH;
   while (p.heads < KH && p.heads * ((p.chunk < span ? p.chunk : span) + kKvKeys - 1) / kKvKeys < 8 && ctas / (2 * p.heads) >= 152 * 6) p.heads *= 2;
   return p;
 }
@@ -896,7 +895,7 @@ template <int D>
 cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cudaStream_t s) {
   cudaError_t e;
   if ((e = set_max_smem_once<kv_attention_kernel<D>>(kv_smem_bytes<D>())) != cudaSuccess) return e;
-  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * ((a.KH + p.heads - 1) / p.heads) * KvLayout<D>::kHalves;
+  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * ((a.KH + p.heads - 1) / p.heads);
   return launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(jobs)), dim3(kKvThreads), kv_smem_bytes<D>(), use_pdl,
                    s, a, p);
 }
@@ -912,7 +911,9 @@ template <int D>
 cudaError_t launch_d(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s) {
   const KvPlan p = plan_kv(a.T, a.B, a.H, a.KH, D, a.max_rows, a.window, a.first, a.words);
   if (p.tiles == 0) return cudaSuccess;
-  const cudaError_t e = p.R <= 64 ? launch_kv_attention_few(a, p, use_pdl, s) : launch<D>(a, p, use_pdl, s);
+  cudaError_t e;
+  if constexpr (D == 512) e = launch_kv_attention_few(a, p, use_pdl, s);
+  else e = p.R <= 64 ? launch_kv_attention_few(a, p, use_pdl, s) : launch<D>(a, p, use_pdl, s);
   return e != cudaSuccess || p.splits == 1 ? e : launch_join<D>(a, p, s);
 }
 

@@ -116,7 +116,7 @@ constexpr int kMmaWarp = 8, kPlanWarp = 9, kMmaWarp2 = 10, kCopyWarp = 12, kKvTh
 
 struct Job {
   KvTile tile;
-  int32_t kh, half, split;
+  int32_t kh, split;
   int32_t first, low;  // the list of keys: rows 0 .. first - 1, then low, low + 1, ...
   int32_t v0, v1;      // of the list
   int32_t n;           // tiles of keys
@@ -154,8 +154,6 @@ template <typename L>
 __device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& p, int64_t id) {
   const int lane = threadIdx.x & 31;
   Job j;
-  j.half = static_cast<int32_t>(id % L::kHalves);
-  id /= L::kHalves;
   const int32_t groups = (a.KH + p.heads - 1) / p.heads;
   j.kh = static_cast<int32_t>(id % groups) * p.heads;
   id /= groups;
@@ -368,8 +366,8 @@ __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm
       }
       if (a.same) continue;  // the keys' units are the values'
       if (two ? j < job.n : j > 0) {
-        for (int u = 0; u < L::kVU && ok; ++u)
-          ok = copy_unit(a.cache.v + job.half * L::kDV + u * 128, two ? next_at : v_at, a.v_side.unit, two ? on : v_on);
+        for (int u = 0; u < L::kKU && ok; ++u)
+          ok = copy_unit(a.cache.v + u * 128, two ? next_at : v_at, a.v_side.unit, two ? on : v_on);
       }
       v_at = next_at;
       v_on = on;
