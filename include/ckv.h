@@ -753,9 +753,10 @@ ckv_status ckv_build_tree_masks(const int32_t* parents, const int32_t* row_start
  * ctx_rows[t] < 0, and rows from row_start[B] on, are left as they were.  Pages that no token of
  * the call sees need not be there: their table entries are not used.
  * q          device bf16, row (t, h) at t*q_stride_t + h*q_stride_h elements, 16-byte aligned.
- * cache      host struct.  A cache row that some token of the request sees has finite values: what
- *            is not finite in it may reach other tokens of that request.  Rows that none
- *            sees may hold anything.  From its first row to its last one a cache spans less than
+ * cache      host struct.  From the first row that a token of the request sees to the last one the
+ *            rows of pages that are there have finite values (rows between first_rows and the lowest
+ *            window need not): what is not finite in them may reach tokens that do not see them.  All
+ *            others may hold anything.  From its first row to its last one a cache spans less than
  *            2^32 times the largest power of two that divides its strides (at least 16 bytes, at
  *            most 8 KB; 1 TiB for rows of 128 channels side by side).
  * block_table  device int32, request b's row at b * table_stride (>= max_pages, or 0: one row that

@@ -388,6 +388,177 @@ def test_one_table_row_for_all_and_permuted_queries(ck):
     s.check(out, lse)
 
 
+@pytest.mark.parametrize("D,H,KH,n,before", [(128, 24, 3, 1, 60), (128, 40, 5, 1, 90), (128, 112, 7, 1, 30), (256, 24, 3, 2, 80), (512, 48, 3, 1, 70),
+                                             (128, 200, 5, 9, 60), (256, 240, 5, 4, 90)])
+def test_several_key_heads_are_looked_up_together(ck, D, H, KH, n, before):
+    """Short jobs and more than 152 x 6 CTAs of them; key heads that are no power of two."""
+    B = 1000 // KH
+    s = Step(D, H, KH, [n] * B, [before - i % 20 for i in range(B)], 16, 32, 2, seed=KH)
+    out, lse, err = s.run(ck)
+    assert int(err) == 0
+    s.check(out, lse)
+
+
+@pytest.mark.parametrize("D,H,KH,n,shared", [(256, 16, 2, [1, 3], True), (256, 32, 2, [30, 1], True), (512, 64, 2, [5, 70], False), (512, 16, 1, [1, 1], False),
+                                             (512, 24, 1, [1, 2], False), (128, 16, 1, [1, 5], True), (128, 32, 1, [30, 9], True)])
+def test_rows_that_are_key_and_value_or_not(ck, D, H, KH, n, shared):
+    s = Step(D, H, KH, n, [400, 130], 32, 300, 5, shared=shared, seed=D + H)
+    out, lse, err = s.run(ck)
+    assert int(err) == 0
+    s.check(out, lse)
+
+
+@pytest.mark.parametrize("D,H,KH,n", [(128, 8, 2, [1, 2]), (128, 32, 2, [20, 3]), (256, 32, 2, [20, 3]), (512, 64, 1, [2, 1])])
+def test_negative_and_zero_scale(ck, D, H, KH, n):
+    for scale in (-0.07, 0.0):
+        s = Step(D, H, KH, n, [200, 50], seed=11)
+        s.scale = scale
+        out, lse, err = s.run(ck)
+        assert int(err) == 0
+        s.check(out, lse)
+
+
+@pytest.mark.parametrize("D,H,KH,n,before,window", [(128, 16, 2, [1, 3], [300, 20], 100), (128, 32, 2, [40, 3], [300, 20], 0), (256, 32, 2, [40, 3], [300, 20], 0),
+                                                    (512, 64, 1, [2, 1], [700, 90], 0), (128, 8, 1, [1, 1], [9000, 10], 0)])
+def test_nothing_is_written_beside_the_outputs(ck, D, H, KH, n, before, window):
+    """Outputs and workspace lie between guards; the outputs begin on 16 bytes, not on 32."""
+    s = Step(D, H, KH, n, before, 16, window, seed=D)
+    T, pad = s.q.shape[0], 1024
+    need = ck.ckv_kv_attention_workspace(T, len(n), H, KH, D, s.max_rows, window)
+    o = torch.full((pad + 8 + T * H * D + pad,), 3.0, dtype=torch.bfloat16, device="cuda")
+    z = torch.full((pad + T * H + pad,), 3.0, device="cuda")
+    w = torch.full((pad + need + pad,), 77, dtype=torch.uint8, device="cuda")
+    out, lse, err = s.run(ck, out=o[pad + 8:pad + 8 + T * H * D].view(T, H, D), lse=z[pad:pad + T * H].view(T, H), workspace=w[pad:pad + need])
+    assert int(err) == 0
+    s.check(out, lse)
+    assert torch.all(o[:pad + 8] == 3) and torch.all(o[-pad:] == 3) and torch.all(z[:pad] == 3) and torch.all(z[-pad:] == 3)
+    assert torch.all(w[:pad] == 77) and torch.all(w[-pad:] == 77)
+    if need:
+        with pytest.raises(Exception):
+            s.run(ck, workspace=w[:need - 1])
+
+
+def test_calls_of_two_streams_at_once(ck):
+    """Each with its own tensors and workspace; results are those of calls one after the other."""
+    steps = [Step(128, 8, 1, [1, 2], [9000, 3000], 64, seed=1), Step(128, 32, 8, [300, 5], [700, 100], 64, 256, 4, seed=2),
+             Step(512, 64, 1, [40, 30], [500, 300], 64, seed=3)]
+    alone = [s.run(ck)[:2] for s in steps]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, stream in zip(steps, streams):
+            with torch.cuda.stream(stream):
+                got.append(s.run(ck)[:2])
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # named by the argument instead
+    got = [s.run(ck, stream=stream)[:2] for s, stream in zip(steps, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("use_pdl", [True, False])
+def test_a_captured_step_follows_its_inputs(ck, use_pdl):
+    """Masks, append, attention over drafts and a merge in one graph; replayed with other lengths, parents and rows."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    B, n, H, KH, D, ps, pages = 5, 7, 16, 2, 128, 16, 80
+    T, rows = B * n, 200
+    start = _i32(range(0, T + 1, n))
+    table = torch.randperm(pages, generator=g, device="cuda")[:B * 13].int().view(B, 13)
+    k0, v0 = (torch.randn(pages, ps, KH, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    kc, vc = k0.clone(), v0.clone()
+    cs = _angles(300, 128)
+    parents, ctx = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    loc = torch.zeros(T, dtype=torch.int64, device="cuda")
+    x = torch.zeros(T, H + 2 * KH, D, device="cuda")
+    far = torch.randn(T, H, D, generator=g, device="cuda").bfloat16(), torch.randn(T, H, generator=g, device="cuda")
+    err = _err()
+
+    def step():
+        more = dict(use_pdl=use_pdl, err_word=err)
+        mask, pos = ck.ckv_build_tree_masks(parents, start, ctx, **more)
+        q = ck.ckv_kv_append(x[:, H:H + KH], x[:, H + KH:], kc, vc, loc, positions=pos, cos_sin=cs, q=x[:, :H], **more)
+        near = ck.ckv_kv_attention(q, kc, vc, table, start, ctx, rows, D ** -0.5, window=60, first_rows=2, tree_mask=mask, **more)
+        out, lse = ck.ckv_merge_attention([near[0], far[0]], [near[1], far[1]], positions=pos, use_pdl=use_pdl)
+        return mask, pos, q, *near, out, lse
+
+    def inputs(seed):
+        rng = np.random.default_rng(seed)
+        parents.copy_(_i32([rng.integers(-1, i) if i else -1 for _ in range(B) for i in range(n)]))
+        c = np.repeat(rng.integers(0, rows - n, B), n)
+        ctx.copy_(_i32(c))
+        r = torch.as_tensor(c + np.tile(np.arange(n), B)).cuda()
+        loc.copy_(table.long()[torch.arange(B, device="cuda").repeat_interleave(n), r // ps] * ps + r % ps)
+        x.normal_(generator=g)
+        kc.copy_(k0)
+        vc.copy_(v0)
+
+    inputs(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed in (1, 2, 3):
+        inputs(seed)
+        graph.replay()
+        got = [t.clone() for t in held] + [kc.clone(), vc.clone()]
+        kc.copy_(k0)
+        vc.copy_(v0)
+        want = list(step()) + [kc, vc]
+        assert int(err) == 0
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_caches_and_queries_beyond_32_bits(ck):
+    """Pages whose first rows lie more than 2^31 elements apart, and tokens whose rows do."""
+    D, KH, ps = 128, 2, 16
+    stride = 150_000_000 // (ps * KH * D) * (ps * KH * D)
+    pages = 20  # 3 * 10^9 elements
+    flat = [torch.empty(stride * (pages - 1) + ps * KH * D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    k, v = (f.as_strided((pages, ps, KH, D), (stride, KH * D, D, 1)) for f in flat)
+    s = Step(D, 16, KH, [3, 40], [200, 30], ps, seed=12)
+    held = sorted(set(s.table.flatten().tolist()) - {-1})
+    to = torch.randperm(pages, device="cuda")[:len(held)]
+    assert int(to.max()) * stride > 2 ** 31
+    new = {p: int(t) for p, t in zip(held, to)}
+    for p, t in new.items():
+        k[t], v[t] = s.k[p], s.v[p]
+    table = torch.tensor([[new.get(p, -1) for p in r] for r in s.table.tolist()], dtype=torch.int32, device="cuda")
+    want = s.run(ck)
+    near = s.k, s.v, s.table
+    s.k, s.v, s.table = k, v, table
+    got = s.run(ck)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    # append: rows of the highest page
+    row = torch.randn(2, KH, D, device="cuda").bfloat16()
+    ck.ckv_kv_append(row, row * 2, k, v, torch.tensor([(pages - 1) * ps + 3, 5], device="cuda"))
+    assert torch.equal(k[pages - 1, 3], row[0]) and torch.equal(v[pages - 1, 3], row[0] * 2) and torch.equal(k[0, 5], row[1])
+    del k, v, flat, got
+    s.k, s.v, s.table = near
+    # more than 2^31 elements of queries and outputs: a request in front without tokens of its own
+    T, H, D = 33000, 130, 512
+    s = Step(D, H, 1, [2], [70], ps, seed=13)
+    q = torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda")
+    q[-2:] = s.q
+    ctx = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    ctx[-2:] = _i32(s.ctx)
+    out, lse = torch.zeros_like(q), torch.zeros(T, H, device="cuda")
+    want = s.run(ck)
+    ck.ckv_kv_attention(q, s.k, s.v, s.table.expand(2, -1), _i32([0, T - 2, T]), ctx, s.max_rows, s.scale, out=out, lse=lse)
+    s.check(out[-2:], lse[-2:])
+    assert int((out[:-2] != 0).any()) == 0 and int((lse[:-2] != 0).any()) == 0
+    merged, _ = ck.ckv_merge_attention([out, out], [lse, lse], out=out, lse=lse, positions=ctx)
+    s.check(out[-2:], lse[-2:] - float(np.log(2.0)))
+
+
 # ------------------------------------------------------------------ merge
 @pytest.mark.parametrize("D", [128, 256, 512])
 @pytest.mark.parametrize("parts", [1, 2, 3, 8])
