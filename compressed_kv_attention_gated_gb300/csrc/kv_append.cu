@@ -21,15 +21,23 @@ namespace ckv {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr uint32_t kAppendShare = 64;  // heads of a token that a warp takes at most
+constexpr uint32_t kAppendShare = 16;  // heads of a token that a warp takes at most
 enum Turn { kNone, kPairs, kHalves, kOddHalves };
+
+// CTAs of an SM, and of the grid: as many as registers allow without spilling much (64 of a thread with four).  A grid of more
+// goes in waves, the last of them hardly filled, and long units leave SMs waiting at the end: 8191 tokens x 48 heads 40.6 us
+// with 64 heads to a warp and eight CTAs per SM, 33.7 so; 4000 x 65 of 512 channels 158 and 102.
+template <int D, Turn kTurn, bool kF32>
+__host__ __device__ constexpr int append_ctas() {
+  return kTurn == kOddHalves ? (D == 512 ? 1 : 2) : D == 512 && !kF32 ? 3 : 4;
+}
 
 __device__ __forceinline__ float value_at(const void* x, int64_t i, bool f32) {
   return f32 ? static_cast<const float*>(x)[i] : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(x)[i]) << 16);
 }
 
 template <int D, Turn kTurn, bool kF32>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ KvAppendArgs a, uint32_t share) {
+__global__ void __launch_bounds__(kAppendThreads, (append_ctas<D, kTurn, kF32>())) kv_append_kernel(const __grid_constant__ KvAppendArgs a, uint32_t share) {
   constexpr int kLanes = D >= 256 ? 32 : D / 8;  // of a row
   constexpr int kRows = 32 / kLanes;             // rows of a warp
   constexpr int kGroups = D / (kLanes * 8);
@@ -56,10 +64,22 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
   pdl_wait();
   const uint32_t hq = a.set[0].heads, hk = hq + a.set[1].heads, heads = hk + a.set[2].heads;
   const uint32_t per = (heads + share - 1) / share, units = static_cast<uint32_t>(a.T) * per;
-  for (uint32_t u = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); u < units; u += gridDim.x * (kAppendThreads / 32)) {
+  const uint32_t stride = gridDim.x * (kAppendThreads / 32);
+  uint32_t u = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  int64_t next_loc = 0;  // of the next unit's token: known when it begins
+  int32_t next_pos = 0;
+  if (u < units) {
+    next_loc = a.loc[u / per];
+    next_pos = a.positions ? a.positions[u / per] : 0;
+  }
+  for (; u < units; u += stride) {
     const uint32_t t = u / per, h0 = (u - t * per) * share, h1 = min(h0 + share, heads);
-    const int64_t loc = a.loc[t];
-    const int32_t pos = a.positions ? a.positions[t] : 0;
+    const int64_t loc = next_loc;
+    const int32_t pos = next_pos;
+    if (u + stride < units) {
+      next_loc = a.loc[(u + stride) / per];
+      next_pos = a.positions ? a.positions[(u + stride) / per] : 0;
+    }
     if (pos < 0) continue;
     if (kTurn != kNone && pos >= a.num_positions) {
       if (lane == 0) flag_error(a.err, CKV_DEVERR_SEQ_LEN);
@@ -216,15 +236,16 @@ cudaError_t launch(const KvAppendArgs& a, bool use_pdl, cudaStream_t s) {
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  // as many heads of a token to a warp as leaves every resident warp (16 per SM) two units
+  // as many heads of a token to a warp as leaves every resident warp two units
   const int64_t heads = static_cast<int64_t>(a.set[0].heads) + a.set[1].heads + a.set[2].heads;
+  const int64_t most = static_cast<int64_t>(sms) * append_ctas<D, kTurn, kF32>();
   int64_t units = 0;
   uint32_t share = kAppendShare;
   for (;; share /= 2) {
     units = a.T * ((heads + share - 1) / share);
-    if (units >= 2 * 16 * static_cast<int64_t>(sms) || share == 1) break;
+    if (units >= 2 * (kAppendThreads / 32) * most || share == 1) break;
   }
-  const int64_t want = (units + kAppendThreads / 32 - 1) / (kAppendThreads / 32), most = static_cast<int64_t>(sms) * 8;
+  const int64_t want = (units + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
   return launch_ex(kv_append_kernel<D, kTurn, kF32>, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kAppendThreads), 0,
                    use_pdl, s, a, share);
 }
