@@ -3,13 +3,14 @@
 //
 //   pairs (a, b) of the rotated span become (a c - b s, b c + a s), fp32, one rounding.
 //
-// Bound by HBM: every row is read once and written once.  A lane owns eight channels
-// (two such groups at D = 512), a row takes 32 lanes (16 at D = 128, two rows to a
-// warp); a warp takes a token and some of its heads, queries, keys and values alike, so that
-// position, location and angles are loaded once for all of them.  Both channels of a
-// pair belong to one lane: eight neighbours when pairs are neighbours, four and their four
-// partners when they are halves of the span.  Halves that are not whole groups of four
-// channels read their partners one by one (from L1: the row has just been read).
+// Bound by HBM: every row is read once and written once.  A row takes 32 lanes (16 at D = 128, two
+// rows to a warp); a warp takes a token and some of its heads, queries, keys and values alike, so that
+// position, location and angles are loaded once for all of them.  Both channels of a pair belong to
+// one lane.  Where pairs are neighbours it has pieces of eight channels.  Where they are halves of the
+// span it has pieces of W channels and their W partners, lanes side by side, and those around the span
+// by twos; W = 4 where the span and its half begin on such a piece, 2 where the half does, otherwise 1
+// (8191 tokens x 48 heads of 128 channels: 34, 42 and 79 us; eight neighbours to a lane with their partners
+// read one by one took 112).
 #include <cstdint>
 
 #include "ckv_device.cuh"
@@ -22,43 +23,73 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr uint32_t kAppendShare = 16;  // heads of a token that a warp takes at most
-enum Turn { kNone, kPairs, kHalves, kOddHalves };
+enum Turn { kNone, kPairs, kHalves4, kHalves2, kHalves1 };
 
 // CTAs of an SM, and of the grid: as many as registers allow without spilling much (64 of a thread with four).  A grid of more
 // goes in waves, the last of them hardly filled, and long units leave SMs waiting at the end: 8191 tokens x 48 heads 40.6 us
 // with 64 heads to a warp and eight CTAs per SM, 33.7 so; 4000 x 65 of 512 channels 158 and 102.
 template <int D, Turn kTurn, bool kF32>
 __host__ __device__ constexpr int append_ctas() {
-  return kTurn == kOddHalves ? (D == 512 ? 1 : 2) : D == 512 && !kF32 ? 3 : 4;
+  return kTurn == kHalves1 ? 2 : D == 512 && !kF32 ? 3 : 4;
 }
 
-__device__ __forceinline__ float value_at(const void* x, int64_t i, bool f32) {
-  return f32 ? static_cast<const float*>(x)[i] : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(x)[i]) << 16);
+// kBytes bytes of one lane, as many words.
+template <int kBytes>
+__device__ __forceinline__ void load_piece(const uint8_t* p, uint32_t* x) {
+  if constexpr (kBytes >= 16) {
+#pragma unroll
+    for (int i = 0; i < kBytes / 16; ++i) {
+      const uint4 w = reinterpret_cast<const uint4*>(p)[i];
+      x[4 * i] = w.x, x[4 * i + 1] = w.y, x[4 * i + 2] = w.z, x[4 * i + 3] = w.w;
+    }
+  } else if constexpr (kBytes == 8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    x[0] = w.x, x[1] = w.y;
+  } else if constexpr (kBytes == 4) {
+    x[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    x[0] = *reinterpret_cast<const uint16_t*>(p);
+  }
+}
+
+// W values to bf16.
+template <int W>
+__device__ __forceinline__ void store_piece(uint16_t* p, const float* v) {
+  if constexpr (W == 8)
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
+  else if constexpr (W == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]));
+  else if constexpr (W == 2) *reinterpret_cast<uint32_t*>(p) = pack_bf16x2_rn(v[0], v[1]);
+  else *p = static_cast<uint16_t>(pack_bf16x2_rn(v[0], 0.f));
 }
 
 template <int D, Turn kTurn, bool kF32>
 __global__ void __launch_bounds__(kAppendThreads, (append_ctas<D, kTurn, kF32>())) kv_append_kernel(const __grid_constant__ KvAppendArgs a, uint32_t share) {
   constexpr int kLanes = D >= 256 ? 32 : D / 8;  // of a row
   constexpr int kRows = 32 / kLanes;             // rows of a warp
-  constexpr int kGroups = D / (kLanes * 8);
+  constexpr bool kHalves = kTurn >= kHalves4;
+  constexpr int W = kTurn == kHalves1 ? 1 : kTurn == kHalves2 ? 2 : kTurn == kHalves4 ? 4 : 8;
+  constexpr int N = D / kLanes / W;              // pieces of a lane; with halves, 2 n and 2 n + 1 belong together
+  constexpr int kES = kF32 ? 4 : 2, kWords = W * kES >= 4 ? W * kES / 4 : 1;
+  constexpr int kAngles = kHalves ? W : 4;       // of two pieces, or of one with pairs of neighbours
   constexpr int kBatch = (D == 512 ? 2 : 4) / (kF32 ? 2 : 1);  // rows of a lane in flight
   const int lane = threadIdx.x & 31, sl = lane % kLanes, sub = lane / kLanes;
   const int half = a.rope_dim >> 1;
-  int base[kGroups][2];
+  int base[N];
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const int q = g * 32 + sl;  // of D/8
-    base[g][0] = q * 8;
-    base[g][1] = q * 8 + 4;
-    if constexpr (kTurn == kHalves) {
-      if (q * 8 < a.rope_dim) {
-        base[g][0] = a.rope_offset + q * 4;
-        base[g][1] = a.rope_offset + half + q * 4;
-      } else {  // the channels around the span, four by four
-        const int c = q * 8 - a.rope_dim;
-        base[g][0] = c < a.rope_offset ? c : c + a.rope_dim;
-        base[g][1] = c + 4 < a.rope_offset ? c + 4 : c + 4 + a.rope_dim;
+  for (int n = 0; n < N; n += kHalves ? 2 : 1) {
+    if constexpr (kHalves) {
+      const int c = (n / 2 * kLanes + sl) * W;
+      if (c < half) {
+        base[n] = a.rope_offset + c;
+        base[n + 1] = a.rope_offset + half + c;
+      } else {  // the channels around the span, by twos
+        const int d = 2 * (c - half);
+        base[n] = d < a.rope_offset ? d : d + a.rope_dim;
+        base[n + 1] = d + W < a.rope_offset ? d + W : d + W + a.rope_dim;
       }
+    } else {
+      base[n] = (n * kLanes + sl) * 8;
     }
   }
   pdl_wait();
@@ -95,49 +126,32 @@ __global__ void __launch_bounds__(kAppendThreads, (append_ctas<D, kTurn, kF32>()
         if (lane == 0) flag_error(a.err, CKV_DEVERR_CACHE_LOC);
       }
     }
-    // angles of the lane's pairs, (1, 0) outside the span
-    float co[kGroups][kTurn == kOddHalves ? 8 : 4], si[kGroups][kTurn == kOddHalves ? 8 : 4];
-    int mate[kGroups][kTurn == kOddHalves ? 8 : 1];
-    bool turns[kGroups];
+    float co[N][kAngles], si[N][kAngles];
+    bool turns[N];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int n = 0; n < N; n += kHalves ? 2 : 1) {
       const float* cs = a.cos_sin + static_cast<int64_t>(pos) * a.rope_dim;
-      turns[g] = false;
+      turns[n] = false;
       if constexpr (kTurn == kPairs) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int k = base[g][0] + 2 * j - a.rope_offset;
+          const int k = base[n] + 2 * j - a.rope_offset;
           const bool in = k >= 0 && k < a.rope_dim;
-          turns[g] |= in;
-          co[g][j] = in ? cs[k >> 1] : 1.f;
-          si[g][j] = in ? cs[half + (k >> 1)] : 0.f;
+          turns[n] |= in;
+          co[n][j] = in ? cs[k >> 1] : 1.f;
+          si[n][j] = in ? cs[half + (k >> 1)] : 0.f;
         }
-      } else if constexpr (kTurn == kHalves) {
-        turns[g] = (g * 32 + sl) * 8 < a.rope_dim;
-        float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (turns[g]) {
-          const int p = base[g][0] - a.rope_offset;
-          c4 = *reinterpret_cast<const float4*>(cs + p);
-          s4 = *reinterpret_cast<const float4*>(cs + half + p);
-        }
-        co[g][0] = c4.x, co[g][1] = c4.y, co[g][2] = c4.z, co[g][3] = c4.w;
-        si[g][0] = s4.x, si[g][1] = s4.y, si[g][2] = s4.z, si[g][3] = s4.w;
-      } else if constexpr (kTurn == kOddHalves) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = base[g][0] + j, k = c - a.rope_offset;
-          const bool in = k >= 0 && k < a.rope_dim, second = k >= half;
-          const int p = second ? k - half : k;
-          turns[g] |= in;
-          mate[g][j] = !in ? -1 : second ? c - half : c + half;
-          co[g][j] = in ? cs[p] : 1.f;
-          si[g][j] = !in ? 0.f : second ? cs[half + p] : -cs[half + p];
+      } else if constexpr (kHalves) {
+        const int c = (n / 2 * kLanes + sl) * W;
+        turns[n] = c < half;
+        if (turns[n]) {
+          load_piece<4 * W>(reinterpret_cast<const uint8_t*>(cs + c), reinterpret_cast<uint32_t*>(co[n]));
+          load_piece<4 * W>(reinterpret_cast<const uint8_t*>(cs + half + c), reinterpret_cast<uint32_t*>(si[n]));
         }
       }
     }
     for (uint32_t h = h0; h < h1; h += kBatch * kRows) {
-      uint4 raw[kBatch][kGroups][kF32 ? 2 : 1];
-      float other[kBatch][kGroups][kTurn == kOddHalves ? 8 : 1];
+      uint32_t raw[kBatch][N][kWords];
       uint16_t* to[kBatch];
       bool turned[kBatch];
 #pragma unroll
@@ -154,76 +168,47 @@ __global__ void __launch_bounds__(kAppendThreads, (append_ctas<D, kTurn, kF32>()
           else to[b] = a.cache.v + page * a.cache.v_stride_page + row * a.cache.v_stride_row + i * a.cache.v_stride_head;
         }
         const ckv_kv_rows& m = a.set[set];
-        const int64_t in = static_cast<int64_t>(t) * m.stride_t + i * m.stride_h;
+        const uint8_t* in = static_cast<const uint8_t*>(m.x) + (static_cast<int64_t>(t) * m.stride_t + i * m.stride_h) * kES;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          raw[b][g][0] = raw[b][g][kF32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
-          if (to[b]) {
-            if constexpr (kF32) {
+        for (int n = 0; n < N; ++n) {
 #pragma unroll
-              for (int x = 0; x < 2; ++x) raw[b][g][x] = *reinterpret_cast<const uint4*>(static_cast<const float*>(m.x) + in + base[g][x]);
-            } else if constexpr (kTurn == kHalves) {
-              const uint2 lo = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(m.x) + in + base[g][0]);
-              const uint2 hi = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(m.x) + in + base[g][1]);
-              raw[b][g][0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-            } else {
-              raw[b][g][0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.x) + in + base[g][0]);
-            }
-          }
-          if constexpr (kTurn == kOddHalves) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) other[b][g][j] = to[b] && turned[b] && mate[g][j] >= 0 ? value_at(m.x, in + mate[g][j], kF32) : 0.f;
-          }
+          for (int x = 0; x < kWords; ++x) raw[b][n][x] = 0;
+          if (to[b]) load_piece<W * kES>(in + base[n] * kES, raw[b][n]);
         }
       }
-      // queries may be rotated in place: their partners' values are read by now
-      if constexpr (kTurn == kOddHalves) __syncwarp();
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
+        float v[N][W];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          float v[8];
-          const uint4 x = raw[b][g][0], y = raw[b][g][kF32 ? 1 : 0];
-          if constexpr (kF32) {
-            v[0] = __uint_as_float(x.x), v[1] = __uint_as_float(x.y), v[2] = __uint_as_float(x.z), v[3] = __uint_as_float(x.w);
-            v[4] = __uint_as_float(y.x), v[5] = __uint_as_float(y.y), v[6] = __uint_as_float(y.z), v[7] = __uint_as_float(y.w);
-          } else {
-            v[0] = bf16_lo(x.x), v[1] = bf16_hi(x.x), v[2] = bf16_lo(x.y), v[3] = bf16_hi(x.y);
-            v[4] = bf16_lo(x.z), v[5] = bf16_hi(x.z), v[6] = bf16_lo(x.w), v[7] = bf16_hi(x.w);
-          }
-          if (turned[b] && turns[g]) {
-            if constexpr (kTurn == kPairs) {
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float p = v[2 * j], q = v[2 * j + 1];
-                const int k = base[g][0] + 2 * j - a.rope_offset;
-                if (k >= 0 && k < a.rope_dim) {  // a pair outside stays what it is, infinite or not
-                  v[2 * j] = fmaf(p, co[g][j], -(q * si[g][j]));
-                  v[2 * j + 1] = fmaf(q, co[g][j], p * si[g][j]);
-                }
+          for (int j = 0; j < W; ++j)
+            v[n][j] = kF32 ? __uint_as_float(raw[b][n][j * kES / 4]) : j % 2 ? bf16_hi(raw[b][n][j / 2]) : bf16_lo(raw[b][n][j / 2]);
+#pragma unroll
+        for (int n = 0; n < N; n += kHalves ? 2 : 1) {
+          if (kTurn == kNone || !turned[b] || !turns[n]) continue;
+          if constexpr (kTurn == kPairs) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float p = v[n][2 * j], q = v[n][2 * j + 1];
+              const int k = base[n] + 2 * j - a.rope_offset;
+              if (k >= 0 && k < a.rope_dim) {  // a pair outside stays what it is, infinite or not
+                v[n][2 * j] = fmaf(p, co[n][j], -(q * si[n][j]));
+                v[n][2 * j + 1] = fmaf(q, co[n][j], p * si[n][j]);
               }
-            } else if constexpr (kTurn == kHalves) {
+            }
+          } else if constexpr (kHalves) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float p = v[j], q = v[4 + j];
-                v[j] = fmaf(p, co[g][j], -(q * si[g][j]));
-                v[4 + j] = fmaf(q, co[g][j], p * si[g][j]);
-              }
-            } else if constexpr (kTurn == kOddHalves) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (mate[g][j] >= 0) v[j] = fmaf(v[j], co[g][j], other[b][g][j] * si[g][j]);
+            for (int j = 0; j < W; ++j) {
+              const float p = v[n][j], q = v[n + 1][j];
+              v[n][j] = fmaf(p, co[n][j], -(q * si[n][j]));
+              v[n + 1][j] = fmaf(q, co[n][j], p * si[n][j]);
             }
           }
-          if (to[b]) {
-            const uint4 o = make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
-            if constexpr (kTurn == kHalves) {
-              *reinterpret_cast<uint2*>(to[b] + base[g][0]) = make_uint2(o.x, o.y);
-              *reinterpret_cast<uint2*>(to[b] + base[g][1]) = make_uint2(o.z, o.w);
-            } else {
-              *reinterpret_cast<uint4*>(to[b] + base[g][0]) = o;
-            }
-          }
+        }
+        if (to[b]) {
+#pragma unroll
+          for (int n = 0; n < N; ++n) store_piece<W>(to[b] + base[n], v[n]);
         }
       }
     }
@@ -254,9 +239,11 @@ template <int D, bool kF32>
 cudaError_t launch_d(const KvAppendArgs& a, bool use_pdl, cudaStream_t s) {
   if (a.rope_dim == 0) return launch<D, kNone, kF32>(a, use_pdl, s);
   if (a.interleaved) return launch<D, kPairs, kF32>(a, use_pdl, s);
-  // halves of whole groups of four channels, and cos | sin rows that 16-byte loads can start in
-  const bool whole = a.rope_offset % 4 == 0 && a.rope_dim % 8 == 0 && reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0;
-  return whole ? launch<D, kHalves, kF32>(a, use_pdl, s) : launch<D, kOddHalves, kF32>(a, use_pdl, s);
+  // Pieces as wide as the span's place, its half and the rows of angles allow; spans begin on even channels.
+  const uintptr_t angles = reinterpret_cast<uintptr_t>(a.cos_sin);
+  if (a.rope_offset % 4 == 0 && a.rope_dim % 8 == 0 && angles % 16 == 0) return launch<D, kHalves4, kF32>(a, use_pdl, s);
+  if (a.rope_dim % 4 == 0 && angles % 8 == 0) return launch<D, kHalves2, kF32>(a, use_pdl, s);
+  return launch<D, kHalves1, kF32>(a, use_pdl, s);
 }
 
 }  // namespace
