@@ -246,6 +246,7 @@ struct KvAttentionArgs {
   uint16_t* out;
   float* lse;
   void* workspace;
+  const int32_t* order;  // in the workspace or null: requests by falling length, then the first tile of each and the count of all
   int32_t* err;
   int64_t T;
   int32_t H, KH, G, B, max_rows, page_shift;

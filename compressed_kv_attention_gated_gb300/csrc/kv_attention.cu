@@ -784,6 +784,59 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   }
 }
 
+// Without a window jobs are as long as the contexts, and a long one that begins last leaves the other SMs waiting: requests
+// are put in the order of their last tokens' contexts, the longest first (and their tiles from the last one on).  That takes
+// a kernel of its own and longer lookups, which few or short jobs do not earn back.  With contexts of up to 4096 rows, not
+// sorted and sorted: 256 tokens x 64 heads of 512 channels (2 jobs to an SM) 180 and 142 us, x 32 heads of 256 (7) 330 and
+// 315, 128 drafts of 40 to 64 (7) 267 and 257; x 64 heads of 128 (14) 319 and 324, 1000 tokens x 32 heads (7) 185 and 196; up
+// to 1024 rows, 256 tokens x 32 heads of 256 109 and 113.
+constexpr int kOrderRequests = 256, kOrderTiles = 20, kOrderJobs = 152 * 8;
+
+__global__ void __launch_bounds__(kOrderRequests) kv_order_kernel(const __grid_constant__ KvAttentionArgs a, int R) {
+  __shared__ __align__(16) uint32_t key[kOrderRequests];
+  __shared__ int32_t count[kOrderRequests], total[32];
+  pdl_wait();
+  const int b = threadIdx.x, lane = b & 31, warp = b >> 5;
+  int32_t tiles = 0, len = 0;
+  if (b < a.B) {
+    const int32_t t0 = kv_start_of(a, b), n = kv_start_of(a, b + 1) - t0;
+    if (n > 0) {
+      tiles = static_cast<int32_t>((static_cast<int64_t>(n) * a.G + R - 1) / R);
+      len = min(max(a.ctx_rows[t0 + n - 1], 0), a.max_rows);
+    }
+  }
+  // contexts in steps of 16 rows (21 bits hold the largest), then the lower request: all keys are different
+  key[b] = b < a.B ? static_cast<uint32_t>(len) >> 4 << 10 | static_cast<uint32_t>(kOrderRequests - 1 - b) : 0u;
+  __syncthreads();
+  int rank = 0;
+  const uint32_t mine = key[b];
+  for (int i = 0; i < (a.B + 3) / 4; ++i) {
+    const uint4 k = reinterpret_cast<const uint4*>(key)[i];
+    rank += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+  }
+  int32_t* order = static_cast<int32_t*>(a.workspace);
+  if (b < a.B) {
+    order[rank] = b;
+    count[rank] = tiles;
+  }
+  __syncthreads();
+  const int32_t own = b < a.B ? count[b] : 0;
+  int32_t sum = own;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) total[warp] = sum;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) sum += total[i];
+  if (b < a.B) {
+    if (b == 0) order[a.B] = 0;
+    order[a.B + 1 + b] = sum;
+  }
+  pdl_trigger();
+}
+
 // Joins the ranges of a row, in their order: one warp per row and 128 channels.
 template <int D, bool kFew>
 __global__ void __launch_bounds__(128, kFew ? 12 : 4) kv_join_kernel(const __grid_constant__ KvAttentionArgs a, int splits) {
@@ -887,6 +940,7 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
   // 1.5) and leave each SM six CTAs all the same: 1024 requests x 64 heads over 128 rows 209 -> 158 us.
   p.heads = 1;
   const int64_t ctas = static_cast<int64_t>(p.tiles) * p.splits * KH;
+  p.sorted = window == 0 && p.splits == 1 && B > 1 && B <= kOrderRequests && most >= kOrderTiles && busy > 152 && busy <= kOrderJobs;
   while (p.heads < KH && p.heads * ((p.chunk < span ? p.chunk : span) + kKvKeys - 1) / kKvKeys < 8 && ctas / (2 * p.heads) >= 152 * 6) p.heads *= 2;
   return p;
 }
@@ -908,10 +962,16 @@ cudaError_t launch_join(const KvAttentionArgs& a, const KvPlan& p, cudaStream_t 
 }
 
 template <int D>
-cudaError_t launch_d(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s) {
-  const KvPlan p = plan_kv(a.T, a.B, a.H, a.KH, D, a.max_rows, a.window, a.first, a.words);
+cudaError_t launch_d(const KvAttentionArgs& args, bool use_pdl, cudaStream_t s) {
+  const KvPlan p = plan_kv(args.T, args.B, args.H, args.KH, D, args.max_rows, args.window, args.first, args.words);
   if (p.tiles == 0) return cudaSuccess;
   cudaError_t e;
+  KvAttentionArgs a = args;
+  if (p.sorted) {
+    a.order = static_cast<const int32_t*>(a.workspace);
+    if ((e = launch_ex(kv_order_kernel, dim3(1), dim3(kOrderRequests), 0, use_pdl, s, a, p.R)) != cudaSuccess) return e;
+    use_pdl = true;  // behind a kernel of this call
+  }
   if constexpr (D == 512) e = launch_kv_attention_few(a, p, use_pdl, s);
   else e = p.R <= 64 ? launch_kv_attention_few(a, p, use_pdl, s) : launch<D>(a, p, use_pdl, s);
   return e != cudaSuccess || p.splits == 1 ? e : launch_join<D>(a, p, s);
@@ -922,6 +982,7 @@ cudaError_t launch_d(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s) {
 int64_t kv_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows, int32_t window, int32_t first_rows,
                                int32_t words) {
   const KvPlan p = plan_kv(T, B, H, KH, D, max_rows, window, window > 0 ? first_rows : 0, words);
+  if (p.sorted) return (2 * static_cast<int64_t>(B) + 1) * static_cast<int64_t>(sizeof(int32_t));
   return p.splits == 1 ? 0 : static_cast<int64_t>(p.splits) * T * H * (D + 1) * static_cast<int64_t>(sizeof(float));
 }
 

@@ -21,6 +21,7 @@ struct KvPlan {
   int splits;  // ranges of keys
   int chunk;   // keys of a range (a multiple of kKvKeys); the last range takes all that are left
   int heads;   // key heads whose jobs a CTA takes together
+  bool sorted; // requests with the longest contexts first, by kv_order_kernel
 };
 cudaError_t launch_kv_attention_few(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cudaStream_t s);
 
@@ -88,21 +89,24 @@ struct KvTile {
 __device__ __forceinline__ KvTile kv_find_tile(const KvAttentionArgs& a, int32_t tile, int R) {
   const int lane = threadIdx.x & 31;
   const int64_t pad = kv_tile_pad(a.G, R);
+  const int32_t* first_tile = a.order + a.B;  // of request order[i], the i-th; where there is an order
   int lo = 0, n = a.B;  // the request is in [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int i = lo + lane * step;
-    const bool le = lane * step < n && (kv_start_of(a, i) * static_cast<int64_t>(a.G) + i * pad) / R <= tile;
+    const bool le = lane * step < n && (a.order ? first_tile[i] : (kv_start_of(a, i) * static_cast<int64_t>(a.G) + i * pad) / R) <= tile;
     const uint32_t m = __ballot_sync(0xFFFFFFFFu, le);
     const int last = m ? 31 - __clz(m) : 0;
     lo += last * step;
     n = min(step, n - last * step);
   }
   KvTile t;
-  t.b = lo;
-  t.tok0 = kv_start_of(a, lo);
-  t.ntok = kv_start_of(a, lo + 1) - t.tok0;
-  const int64_t base = (tile - (t.tok0 * static_cast<int64_t>(a.G) + lo * pad) / R) * R, left = static_cast<int64_t>(t.ntok) * a.G - base;
+  t.b = a.order ? a.order[lo] : lo;
+  t.tok0 = kv_start_of(a, t.b);
+  t.ntok = kv_start_of(a, t.b + 1) - t.tok0;
+  // with an order, a request's last tile, which sees most, comes first
+  const int64_t i = a.order ? first_tile[lo + 1] - 1 - tile : tile - (t.tok0 * static_cast<int64_t>(a.G) + lo * pad) / R;
+  const int64_t base = i * R, left = static_cast<int64_t>(t.ntok) * a.G - base;
   t.rows = base < 0 || left <= 0 ? 0 : static_cast<int32_t>(left < R ? left : R);  // base < 0: row_start does not begin with 0
   t.base = static_cast<int32_t>(base);
   return t;

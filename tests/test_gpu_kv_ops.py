@@ -310,6 +310,30 @@ def test_the_same_call_gives_the_same_bits(ck, D, H, KH, n, before, window):
         assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("D,H,KH,n,B", [(128, 16, 8, 1, 100), (512, 16, 1, 1, 250), (256, 32, 4, 2, 110), (128, 32, 8, 12, 130),
+                                         (128, 32, 8, 300, 9), (256, 16, 8, 70, 40)])
+def test_requests_in_the_order_of_their_lengths(ck, D, H, KH, n, B):
+    """Long contexts and few jobs to an SM; requests without tokens, without context and left alone among them."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 300, B)
+    lens[[0, B // 2]] = 2600 - n, 1500
+    tokens = [n] * B
+    tokens[1], tokens[B // 3] = 0, 2 * n
+    s = Step(D, H, KH, tokens, lens, 64, seed=B)
+    s.ctx = np.array(s.ctx)
+    s.ctx[s.start[5]:s.start[6]] = -1
+    s.ctx[s.start[7]] = 0
+    assert ck.ckv_kv_attention_workspace(B * n, B, H, KH, D, s.max_rows) == 4 * (2 * B + 1)
+    out, lse, err = s.run(ck)
+    assert int(err) == 0
+    s.check(out, lse)
+    s.window = s.max_rows  # which hides nothing: the same tiles as they come
+    assert ck.ckv_kv_attention_workspace(B * n, B, H, KH, D, s.max_rows, s.window) == 0
+    as_they_come = s.run(ck)
+    on = torch.as_tensor(s.ctx >= 0).cuda()
+    assert torch.equal(as_they_come[0][on], out[on]) and torch.equal(as_they_come[1][on], lse[on])
+
+
 def test_rows_left_alone(ck):
     s = Step(128, 8, 2, [3, 2, 2], [20, 140, 3], seed=3)
     T = s.q.shape[0]
