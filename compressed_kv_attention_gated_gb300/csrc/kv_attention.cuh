@@ -129,7 +129,6 @@ struct Job {
   int32_t live;        // 0: no more jobs
 };
 
-
 // Barriers of both forms.  Uses of a barrier are numbered from 0 over the whole kernel, so that everyone
 // counts alike.
 struct KvCommon {
@@ -153,7 +152,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn_major) { retu
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t n) { return __all_sync(0xFFFFFFFFu, mbar_wait_near(bar, n & 1u)); }
 
 // ---------------------------------------------------------------------- jobs
-// The first job of CTA `id`, by one converged warp; rows <= 0 when there is nothing to do in it.
+// The first job of CTA `id` (of p.heads), by one converged warp; rows <= 0 when there is nothing to do in it.
 template <typename L>
 __device__ __forceinline__ Job make_job(const KvAttentionArgs& a, const KvPlan& p, int64_t id) {
   const int lane = threadIdx.x & 31;
