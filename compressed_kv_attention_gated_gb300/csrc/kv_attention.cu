@@ -33,12 +33,13 @@
 // Few tiles with many keys are split into ranges of keys; their results (fp32, and lse) go through
 // the workspace and are joined by a second kernel in a fixed order.
 //
-// Measured: 9 prompts of 600 to 3000 tokens x 32 heads (8 key heads, D = 128, window 1024) 288 us, 960 TFLOP/s
-// without the masked parts; 128 drafts of 40 to 64 tokens over up to 4096 rows 250 us, 4.9 TB/s.  The tensor cores are
-// busy 49 and 53% of the time, instructions issue in 44 and 40% of the cycles, exponentials take 24%.  A job of 9 tiles of
-// keys takes 21 us: its output 2 (10% of the call, stores of rows that lie apart), the first scores and what ends before it
-// about as much, a tile of keys 1.9, of which the products 1.1.  Shared memory feeds the 64 columns of a half's scores at
-// two thirds of the rate that the tensor cores could take.
+// Measured: 9 prompts of 600 to 3000 tokens x 32 heads (8 key heads, D = 128, window 1024) 283 us, 976 TFLOP/s
+// without the masked parts; 128 drafts of 40 to 64 tokens over up to 4096 rows 248 us, 4.9 TB/s.  The tensor cores are
+// busy 49 and 53% of the time, instructions issue in 44 and 40% of the cycles, exponentials take 24%.  A softmax warp of the
+// prompts spends, of 39 k clocks on a job of 9 tiles of keys, 10 on exponentials and their rounding, 8 on scaling and
+// masks, 4.4 waiting for scores, 3 on the output, 4 on the next job's rows and on sums, and about 5 on getting its
+// instructions: loops are not unrolled for that.  Twice as many softmax warps (16 rows to a warp, four lanes to a row)
+// take as long (304 us when this took 290), with whole tiles of scores to a product longer (335).
 #include <algorithm>
 
 #include "kv_attention.cuh"
@@ -110,8 +111,10 @@ __device__ __forceinline__ void kv_tmem_st16(uint32_t addr, const uint32_t (&v)[
 
 // Bits x0 .. x1 - 1 of a 32-bit word (any of them outside it).
 __device__ __forceinline__ uint32_t bits_between(int32_t x0, int32_t x1) {
-  const int lo = min(max(x0, 0), 32), hi = min(max(x1, 0), 32);
-  return static_cast<uint32_t>(((1ull << hi) - 1ull) & ~((1ull << lo) - 1ull));
+  const int32_t lo = max(x0, 0);
+  uint32_t m;
+  asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(m) : "r"(lo), "r"(max(x1 - lo, 0)));
+  return m;
 }
 
 // Two fp32 values for the packed instructions (each half an ordinary IEEE operation).
@@ -174,14 +177,14 @@ __device__ __forceinline__ void tile_bits(const KvAttentionArgs& a, const SoftRo
 #pragma unroll
   for (int i = 0; i < n / 32; ++i) {
     const int32_t y = v + i * 32;
-    uint32_t m = bits_between(0, x.a1 - y) | bits_between(x.b0 - y, x.b1 - y);
+    uint32_t m = bits_between(0, min(x.a1, v1) - y) | bits_between(x.b0 - y, min(x.b1, v1) - y);
     if (a.words > 0 && y + 32 > x.b1 && y < x.b2) {  // 32 bits of the drafts' mask, from bit y - b1 on
       const int32_t d = y - x.b1, at = d >> 5;       // rounded down
       const uint32_t* words = reinterpret_cast<const uint32_t*>(a.mask + static_cast<int64_t>(x.t) * a.words);
       const uint32_t lo = at >= 0 && at < 2 * a.words ? words[at] : 0u, hi = at + 1 >= 0 && at + 1 < 2 * a.words ? words[at + 1] : 0u;
-      m |= __funnelshift_r(lo, hi, d & 31) & bits_between(0, x.b2 - y);
+      m |= __funnelshift_r(lo, hi, d & 31) & bits_between(0, min(x.b2, v1) - y);
     }
-    bits[i] = m & bits_between(0, v1 - y);
+    bits[i] = m;
   }
   if (missing) {  // keys whose page is not there, a lane each
     const int32_t* table = a.table + static_cast<int64_t>(job.tile.b) * a.table_stride;
@@ -324,11 +327,22 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
     auto half = [&](int j, int h) {
       uint32_t bits[2];
       const bool masks = any && !whole(2 * j + h);
-      if (__builtin_expect(masks, 0)) tile_bits<64>(a, x, job, v0 + j * kKvKeys + h * 64, v1, missing, bits);
+      bool some = any;  // of the warp's rows see some of the keys
+      if (__builtin_expect(masks, 0)) {
+        tile_bits<64>(a, x, job, v0 + j * kKvKeys + h * 64, v1, missing, bits);
+        some = __any_sync(0xFFFFFFFFu, bits[0] | bits[1]);
+      }
       const uint32_t at = at_s + h * 64;
       if (!warp_wait(&sm.half_s[w][h], use)) return false;
       tc_fence_after();
-      if (any) {
+      if (__builtin_expect(any && !some, 0)) {
+        uint32_t none[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) none[i] = 0;
+        kv_tmem_st16(at, none);
+        kv_tmem_st16(at + 16, none);
+        tc_wait_st();
+      } else if (any) {
         float z[64];
         tmem_ld32_async(at, z);
         tmem_ld32_async(at + 32, z + 32);
@@ -375,11 +389,11 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
       if (lane == 0) mbar_arrive(&sm.half_p[w][h]);
       return true;
     };
-#pragma unroll 1
-    for (int j = j0; j < n; j += step, ++use) {
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h)
-        if (!half(j, h)) return false;
+    for (int j = j0, h = 0; j < n;) {
+      if (!half(j, h)) return false;
+      j += h ? step : 0;
+      use += h;
+      h ^= 1;
     }
     // ------------------------------------------------------------------ output
     float all = l, m = ref, mine = 1.f, other = 0.f;  // shares of the two outputs
