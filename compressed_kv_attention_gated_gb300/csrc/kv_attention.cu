@@ -12,8 +12,8 @@
 // window of 128 is one tile of keys wherever it begins.  What single tokens do not see of it is masked.
 //
 // A job is a tile of rows with its keys (or a range of them); the launch has a CTA for each, and those
-// that are resident, one per SM, take over the others (take_job()).  Roles of a CTA: 8 softmax warps, a
-// thread per row of S; one thread that issues the products, two at D = 128; one warp that looks up the
+// that are resident, one per SM, take over the others (take_job()).  Roles of a CTA: softmax warps, 8 with a
+// thread per row of S at D = 128, 16 at D = 256; one thread that issues the products, two at D = 128; one warp that looks up the
 // jobs ahead of the others; 4 that copy queries, keys and values (cp.async, 16 bytes at a time: pages
 // begin anywhere in a tile and rows have any stride; TMA's gathered rows took 88 clocks per 512 bytes)
 // into a ring of units of 128 rows x 128 channels, across the jobs, so that memory is busy while a job
@@ -47,14 +47,17 @@
 namespace ckv {
 namespace {
 
-// Registers per thread: 512 x 128 at launch; then 256 x 192 + 256 x 64, the same.
-constexpr int kSoftRegs = 192, kOtherRegs = 64;
 constexpr float kKvMost = 65536.f;  // D = 128: sum of a tile's weights from which on the reference moves
 
 template <int D_>
 struct KvLayout {
   static constexpr int D = D_;
   static constexpr int kRows = D == 128 ? 256 : 128;    // of a job
+  static constexpr int kSoftWarps = D == 128 ? 8 : 16;
+  static constexpr int kMmaWarp = kSoftWarps, kPlanWarp = kSoftWarps + 1, kMmaWarp2 = kSoftWarps + 2, kCopyWarp = kSoftWarps + 4;
+  static constexpr int kThreads = (kSoftWarps + 8) * 32;
+  // registers per thread: 512 x 128 at launch, then 256 x 192 + 256 x 64; 768 x 80, then 512 x 88 + 256 x 64, the same
+  static constexpr int kSoftRegs = D == 128 ? 192 : 88, kOtherRegs = 64;
   static constexpr int kKU = D / 128;                   // units of a tile's keys, and of its values
   static constexpr bool kFindMissing = true;            // pages that are not there, by the planning warp
   static constexpr int kQRows = 128;                    // of a slot of queries
@@ -67,12 +70,12 @@ struct KvLayout {
   static constexpr int kTmemO = 0, kTmemS = 256;  // O: 256 columns; S: two buffers of 128, P over the first half of each
 };
 
-// Beside the common ones (s_full[w], p_full[w], o_full[w] and pv_done[w] are group w's; p_full: 4 warps):
+// Beside the common ones (s_full[w], p_full[w], o_full[w] and pv_done[w] are group w's; p_full: 8 warps):
 template <int D>
 struct KvSmall : KvCommon {
-  uint64_t decided[2][4];         // D > 128: warp q of group w knows the references under which its tile is taken
+  uint64_t decided[2][8];         // D = 256: warp i of group w knows the references under which its tile is taken
   uint64_t half_s[2][2], half_p[2][2];  // D = 128: scores and weights of group w, by halves of a tile of keys (4 warps)
-  uint64_t met;                   // both groups have got there: 8 warps, twice per job of shared rows
+  uint64_t met;                   // both groups have got there: all softmax warps, twice per job of shared rows
   float ref[D == 128 ? 2 : 1][128];  // references of shared rows (each group's own at D = 128)
   float sum[2][128];
 };
@@ -163,10 +166,10 @@ struct WholeSpans {
   __device__ __forceinline__ bool operator()(int32_t i) const { return i < a || (i >= b0 && i < b1); }
 };
 template <int n>
-__device__ __forceinline__ WholeSpans whole_spans(const SoftRow& x, int32_t v0, int32_t v1, bool missing) {
-  const bool on = x.flat >= 0;
-  const int32_t a1 = min(__reduce_min_sync(0xFFFFFFFFu, on ? x.a1 : INT32_MAX), v1) - v0;
-  const int32_t b0 = __reduce_max_sync(0xFFFFFFFFu, on ? x.b0 : 0) - v0, b1 = min(__reduce_min_sync(0xFFFFFFFFu, on ? x.b1 : INT32_MAX), v1) - v0;
+__device__ __forceinline__ WholeSpans whole_spans(const SoftRow& x, const SoftRow& y, int32_t v0, int32_t v1, bool missing) {  // two rows a thread
+  auto least = [&](int32_t p, int32_t q) { return __reduce_min_sync(0xFFFFFFFFu, min(x.flat >= 0 ? p : INT32_MAX, y.flat >= 0 ? q : INT32_MAX)); };
+  const int32_t a1 = min(least(x.a1, y.a1), v1) - v0, b1 = min(least(x.b1, y.b1), v1) - v0;
+  const int32_t b0 = __reduce_max_sync(0xFFFFFFFFu, max(x.flat >= 0 ? x.b0 : 0, y.flat >= 0 ? y.b0 : 0)) - v0;
   return missing ? WholeSpans{0, 0, 0} : WholeSpans{a1 / n, b0 > 0 ? (b0 + n - 1) / n : 0, b1 / n};
 }
 
@@ -317,7 +320,7 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
     const bool missing = job.missing;
     const SoftRow x = soft_row(a, job, (two ? w * 128 : 0) + row);
     const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
-    const WholeSpans whole = whole_spans<64>(x, v0, v1, missing);
+    const WholeSpans whole = whole_spans<64>(x, x, v0, v1, missing);
     float ref = x.flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
     uint64_t shift = twice(0.f);                       // -ref, or 0 without one
     bool unset = any;                                  // some row of the warp may have none
@@ -448,12 +451,127 @@ __device__ __forceinline__ bool soft_apart(const KvAttentionArgs& a, const KvPla
   }
 }
 
-// The part of the softmax warps at D = 256 and 512: the groups take tiles of keys by turns and share the output.
+// 16 lanes of tensor memory, in pieces of 8 columns: a thread has two neighbouring columns, 2 (lane % 4), of rows lane / 4
+// and lane / 4 + 8 in each piece (registers 4 i, 4 i + 1 and 4 i + 2, 4 i + 3).
+__device__ __forceinline__ void tmem_ld16x64(uint32_t addr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr));
+  tc_wait_ld();
+  settled32(v);
+}
+__device__ __forceinline__ void tmem_ld16x16(uint32_t addr, float (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(addr));
+  tc_wait_ld();
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
+}
+__device__ __forceinline__ void tmem_st16x16(uint32_t addr, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+// The same rows of 32 columns, in pieces of 4: column lane % 4 of both rows.
+__device__ __forceinline__ void tmem_st16x32(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Over the four lanes that have a row.
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+  return x + __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+}
+// Weights of both rows to tensor memory, rounded to bf16; their sums are added.
+__device__ __forceinline__ void weights16(const float* z, uint32_t at, float (&sum)[2]) {
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  uint32_t x[16];
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float p0 = fast_exp2(z[i]), p1 = fast_exp2(z[i + 1]), p2 = fast_exp2(z[i + 2]), p3 = fast_exp2(z[i + 3]);
+    add2(s0, s1, p0, p1);
+    add2(s2, s3, p2, p3);
+    x[i / 2] = pack_bf16x2_rn(p0, p1);
+    x[i / 2 + 1] = pack_bf16x2_rn(p2, p3);
+  }
+  tmem_st16x32(at, x);
+  sum[0] = s0 + s1;
+  sum[1] = s2 + s3;
+}
+
+// Four lanes trade the four words that each has: word i of lane j becomes word j of lane i.
+__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4], int lane) {
+#pragma unroll
+  for (int b = 1; b < 4; b *= 2) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & b) continue;
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, lane & b ? x[k] : x[k | b], b);
+      if (lane & b) x[k] = got;
+      else x[k | b] = got;
+    }
+  }
+}
+
+// 64 channels from `ch` on of a row, which four lanes have (o as of tmem_ld16x64, r: 0 or 1), times `share`.
+__device__ __forceinline__ void put_row16(const KvAttentionArgs& a, const KvPlan& p, int D, int32_t range, int32_t flat, int ch, const float (&o)[32], int r,
+                                          float share, int lane) {
+  if (p.splits > 1) {
+    float* to = static_cast<float*>(a.workspace) + (a.T * a.H * static_cast<int64_t>(range) + flat) * D + ch + lane % 4 * 2;
+    if (flat >= 0) {
+#pragma unroll
+      for (int y = 0; y < 8; ++y) *reinterpret_cast<float2*>(to + y * 8) = make_float2(o[4 * y + 2 * r] * share, o[4 * y + 2 * r + 1] * share);
+    }
+    return;
+  }
+#pragma unroll
+  for (int y = 0; y < 8; y += 4) {  // 32 channels: a lane gets eight that follow each other
+    uint32_t x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = pack_bf16x2_rn(o[4 * (y + k) + 2 * r] * share, o[4 * (y + k) + 2 * r + 1] * share);
+    quad_transpose(x, lane);
+    if (flat >= 0)
+      *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(flat) * D + ch + y * 8 + lane % 4 * 8) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+// Columns of O times what a move of the rows' references leaves.
+template <int kColumns>
+__device__ __forceinline__ void rescale16(uint32_t at, const float (&keep)[2]) {
+#pragma unroll 1
+  for (int i = 0; i < kColumns; i += 16) {
+    float o[8];
+    tmem_ld16x16(at + i, o);
+#pragma unroll
+    for (int y = 0; y < 8; ++y) o[y] *= keep[y / 2 % 2];
+    tmem_st16x16(at + i, o);
+  }
+  tc_wait_st();
+}
+
+// The part of the softmax warps at D = 256: the two groups of eight take tiles of keys by turns and share the output.  Products
+// of a group's next tile come behind those of its last one, so its time counts twice over, and it has eight warps: 16 rows to
+// a warp, four lanes to a row (8000 tokens x 64 heads over 128 rows 242 us, 32 heads over 1024 rows 310 us; with a row to a
+// thread 284 and 321).
 template <int D>
 __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPlan& p, KvSmall<D>& sm, uint32_t tmem) {
   using L = KvLayout<D>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, w = warp >> 2, row = threadIdx.x & 127;
-  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = (warp >> 2) & 1, part = (warp & 3) * 2 + (warp >> 3);
+  const int row = part * 16 + lane / 4;  // and row + 8
+  const uint32_t lanes = static_cast<uint32_t>(part * 16) << 16;
   const uint32_t at_s = tmem + lanes + L::kTmemS + w * 128, at_o = tmem + lanes + L::kTmemO;
   const uint64_t scale = twice(a.softmax_scale * kLog2e);
   uint32_t s_use = 0, o_use = 0, met_use = 0;
@@ -463,60 +581,114 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
     if (!warp_wait(&sm.job_full[job_use & 1], job_use >> 1)) return false;
     const Job& job = sm.job[job_use & 1];
     if (!job.live) return true;
-    const int32_t n = job.n, v0 = job.v0, v1 = job.v1, range = job.split;
+    const int32_t n = job.n, v0 = job.v0, v1 = job.v1;
     const bool missing = job.missing;
-    const SoftRow x = soft_row(a, job, row);
-    const bool any = __any_sync(0xFFFFFFFFu, x.flat >= 0);
-    const WholeSpans whole = whole_spans<128>(x, v0, v1, missing);
-    float ref = x.flat >= 0 ? kNegBig : 0.f, l = 0.f;  // a row that has seen no key yet has no reference
+    const SoftRow x[2] = {soft_row(a, job, row), soft_row(a, job, row + 8)};
+    const bool any = __any_sync(0xFFFFFFFFu, x[0].flat >= 0 || x[1].flat >= 0);
+    const WholeSpans whole = whole_spans<128>(x[0], x[1], v0, v1, missing);
+    float ref[2], l[2] = {0.f, 0.f};  // a row that has seen no key yet has no reference
+#pragma unroll
+    for (int r = 0; r < 2; ++r) ref[r] = x[r].flat >= 0 ? kNegBig : 0.f;
 #pragma unroll 1
     for (int j = w; j < n; j += 2) {
-      uint32_t bits[4];
+      uint32_t bits[2][4];
       const bool masks = any && !whole(j);
-      if (masks) tile_bits<128>(a, x, job, v0 + j * kKvKeys, v1, missing, bits);
+      if (masks) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          tile_bits<128>(a, x[r], job, v0 + j * kKvKeys, v1, missing, bits[r]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bits[r][i] >>= lane % 4 * 2;
+        }
+      }
       if (!warp_wait(&sm.s_full[w], s_use++)) return false;
       tc_fence_after();
       if (any) {
-        float z[128];
+        // scores of half of the tile in log2 units less `less`, -infinity for what a row does not see
+        auto scores = [&](int h, float (&z)[32], float less0, float less1) {
+          tmem_ld16x64(at_s + h * 64, z);
+          const uint64_t s0 = twice(-less0), s1 = twice(-less1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32_async(at_s + i * 32, z + i * 32);
-        tc_wait_ld();
+          for (int i = 0; i < 32; i += 4) {
+            fma2(z[i], z[i + 1], scale, s0);
+            fma2(z[i + 2], z[i + 3], scale, s1);
+          }
+          if (__builtin_expect(masks, 0)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) settled32(z + i * 32);
-        const uint32_t others = other_tiles + (j + 1) / 2;  // tiles of the other group before this one
-        if (j > 0) {                                        // the reference as it left it
-          if (!warp_wait(&sm.decided[w ^ 1][quad], others - 1)) return false;
-          const float now = sm.ref[0][row];
-          if (now != ref) {
-            l = l == 0.f ? 0.f : l * fast_exp2(ref - now);
-            ref = now;
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t b0 = h ? bits[r][2] : bits[r][0], b1 = h ? bits[r][3] : bits[r][1];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t two = (i < 4 ? b0 : b1) >> (i % 4 * 8);
+                if (!(two & 1)) z[4 * i + 2 * r] = -INFINITY;
+                if (!(two & 2)) z[4 * i + 2 * r + 1] = -INFINITY;
+              }
+            }
+          }
+        };
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float z[32];
+          scores(h, z, 0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            top[0] = fmaxf(top[0], fmaxf(z[i], z[i + 1]));
+            top[1] = fmaxf(top[1], fmaxf(z[i + 2], z[i + 3]));
           }
         }
-        const bool unset = ref == kNegBig;
-        const float shift = unset ? 0.f : ref;
-        over_reference<128>(z, scale, twice(-shift), masks, bits);
-        const float over = largest<128>(z);
-        if (__any_sync(0xFFFFFFFFu, over > kKvJump || (unset && over > -INFINITY))) {
-          // the reference goes to the largest score so far
-          const float by = unset ? (over > -INFINITY ? over : 0.f) : fmaxf(over, 0.f);
-          const float keep = unset ? 1.f : fast_exp2(-by);  // an unset row's output is 0
-          if (!unset || over > -INFINITY) ref = shift + by;
-          l *= keep;
+        const uint32_t others = other_tiles + (j + 1) / 2;                                // tiles of the other group before this one
+        if (j > 0 && !warp_wait(&sm.decided[w ^ 1][part], others - 1)) return false;  // the references as it left them
+        float keep[2];
+        bool moves = false;
 #pragma unroll
-          for (int i = 0; i < 128; ++i) z[i] -= by;
-          if (j > 0 && __any_sync(0xFFFFFFFFu, keep != 1.f)) {
+        for (int r = 0; r < 2; ++r) {
+          top[r] = quad_max(top[r]);
+          if (j > 0) {
+            const float now = sm.ref[0][row + 8 * r];
+            if (now != ref[r]) {
+              l[r] = l[r] == 0.f ? 0.f : l[r] * fast_exp2(ref[r] - now);
+              ref[r] = now;
+            }
+          }
+          const bool unset = ref[r] == kNegBig;
+          moves |= unset ? top[r] > -INFINITY : top[r] - ref[r] > kKvJump;
+        }
+        if (__any_sync(0xFFFFFFFFu, moves)) {  // references go to the largest scores so far
+          bool rescales = false;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const bool unset = ref[r] == kNegBig;
+            const float now = fmaxf(ref[r], top[r]);
+            keep[r] = unset ? 1.f : fast_exp2(ref[r] - now);  // an unset row's output is 0
+            l[r] *= keep[r];
+            ref[r] = now;
+            rescales |= keep[r] != 1.f;
+          }
+          if (j > 0 && __any_sync(0xFFFFFFFFu, rescales)) {
             if (!warp_wait(&sm.pv_done[w ^ 1], others - 1)) return false;  // the products of the tile before
             tc_fence_after();
-            rescale<D>(at_o, keep);
+            rescale16<D>(at_o, keep);
           }
         }
-        sm.ref[0][row] = ref;
+        if (lane % 4 == 0) {
+          sm.ref[0][row] = ref[0];
+          sm.ref[0][row + 8] = ref[1];
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.decided[w][quad]);
-        l += weights<128>(z, at_s);
+        if (lane == 0) mbar_arrive(&sm.decided[w][part]);
+        const float less[2] = {ref[0] == kNegBig ? 0.f : ref[0], ref[1] == kNegBig ? 0.f : ref[1]};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float z[32], sum[2];
+          scores(h, z, less[0], less[1]);
+          weights16(z, at_s + h * 32, sum);
+          l[0] += sum[0];
+          l[1] += sum[1];
+        }
         tc_wait_st();
       } else if (lane == 0) {
-        mbar_arrive(&sm.decided[w][quad]);
+        mbar_arrive(&sm.decided[w][part]);
       }
       tc_fence_before();
       __syncwarp();
@@ -524,34 +696,42 @@ __device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPl
     }
     // ------------------------------------------------------------------ output
     other_tiles += (n + w) / 2;
-    float m = ref;
+    float share[2] = {ref[0], ref[1]};
     if (n > 0) {  // both sums against the references that O has in the end: the last tile's
-      if (((n - 1) & 1) != w && !warp_wait(&sm.decided[w ^ 1][quad], other_tiles - 1)) return false;
-      m = any ? sm.ref[0][row] : 0.f;
-      l = l == 0.f ? 0.f : l * fast_exp2(ref - m);
+      if (((n - 1) & 1) != w && !warp_wait(&sm.decided[w ^ 1][part], other_tiles - 1)) return false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        share[r] = any ? sm.ref[0][row + 8 * r] : 0.f;
+        l[r] = l[r] == 0.f ? 0.f : l[r] * fast_exp2(ref[r] - share[r]);
+      }
     }
-    sm.sum[w][row] = l;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] = quad_sum(l[r]);
+      if (lane % 4 == 0) sm.sum[w][row + 8 * r] = l[r];
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.met);
     if (!warp_wait(&sm.met, met_use++)) return false;
-    const float share = finish_row(a, p, D, range, x.flat, l + sm.sum[w ^ 1][row], m, w == 0);
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      share[r] = finish_row(a, p, D, job.split, x[r].flat, l[r] + sm.sum[w ^ 1][row + 8 * r], share[r], w == 0 && lane % 4 == 0);
     if (n > 0) {
       if (!warp_wait(&sm.o_full[w], o_use++)) return false;
       tc_fence_after();
     }
     if (any) {
 #pragma unroll 1
-      for (int i = w * (D / 2); i < (w + 1) * (D / 2); i += 32) {
+      for (int i = w * (D / 2); i < (w + 1) * (D / 2); i += 64) {
         float o[32];
         if (n > 0) {
-          tmem_ld<32>(at_o + i, o);
-#pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] *= share;
+          tmem_ld16x64(at_o + i, o);
         } else {
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = 0.f;
         }
-        put_row(a, p, D, range, x.flat, i, o);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) put_row16(a, p, D, job.split, x[r].flat, i, o, r, n > 0 ? share[r] : 0.f, lane);
       }
     }
     tc_fence_before();
@@ -724,7 +904,7 @@ __device__ __forceinline__ bool mma_shared(KvSmall<D>& sm, uint32_t base, uint32
 }
 
 template <int D>
-__global__ void __launch_bounds__(kKvThreads, 1)
+__global__ void __launch_bounds__(KvLayout<D>::kThreads, 1)
     kv_attention_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ KvPlan p) {
   using L = KvLayout<D>;
   // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
@@ -737,13 +917,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     if (threadIdx.x == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
     return;
   }
-  if (warp == kMmaWarp) {
+  if (warp == L::kMmaWarp) {
     if (lane == 0) {
       for (int i = 0; i < L::kRing; ++i) {
         mbar_init(&sm.full[i], 128);
         mbar_init(&sm.empty[i], kIssuers);
       }
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         mbar_init(&sm.decided[0][i], 1);
         mbar_init(&sm.decided[1][i], 1);
       }
@@ -751,7 +931,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_init(&sm.q_full[i], 128);
         mbar_init(&sm.q_empty[i], kIssuers);
         mbar_init(&sm.s_full[i], 1);
-        mbar_init(&sm.p_full[i], 4);
+        mbar_init(&sm.p_full[i], 8);
         for (int h = 0; h < 2; ++h) {
           mbar_init(&sm.half_s[i][h], 1);
           mbar_init(&sm.half_p[i][h], 4);
@@ -759,9 +939,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_init(&sm.o_full[i], 1);
         mbar_init(&sm.pv_done[i], 1);
         mbar_init(&sm.job_full[i], 1);
-        mbar_init(&sm.job_empty[i], 12 + kIssuers);
+        mbar_init(&sm.job_empty[i], L::kSoftWarps + 4 + kIssuers);
       }
-      mbar_init(&sm.met, 8);
+      mbar_init(&sm.met, L::kSoftWarps);
       mbar_init(&sm.wanted, 1);
       mbar_init(&sm.taken, 1);
       mbar_init(&sm.drain, kIssuers);
@@ -777,16 +957,16 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   pdl_wait();
 
   bool ok = true;
-  if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+  if (warp < L::kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftRegs));
     if constexpr (D == 128) ok = soft_apart(a, p, sm, tmem);
     else ok = soft_shared<D>(a, p, sm, tmem);
     tc_fence_before();
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kMmaWarp || (D == 128 && warp == kMmaWarp2)) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
+    if (warp == L::kMmaWarp || (D == 128 && warp == L::kMmaWarp2)) {
       if (elect_one()) {
-        if constexpr (D == 128) ok = mma_apart(sm, smem_u32(smem), tmem, warp != kMmaWarp);
+        if constexpr (D == 128) ok = mma_apart(sm, smem_u32(smem), tmem, warp != L::kMmaWarp);
         else ok = mma_shared<D>(sm, smem_u32(smem), tmem);
         // the end of every product: tensor memory may be given back
         tc_commit(&sm.drain);
@@ -794,16 +974,16 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         if (!ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
       }
       __syncwarp();
-    } else if (warp == kPlanWarp) {
+    } else if (warp == L::kPlanWarp) {
       ok = plan_jobs<L>(a, p, sm, [](const Job&, uint32_t) {});
-    } else if (warp >= kCopyWarp) {
+    } else if (warp >= L::kCopyWarp) {
       ok = copy_jobs<L>(a, sm, smem);
     }
   }
   if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
   pdl_trigger();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == L::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
@@ -975,7 +1155,7 @@ cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cuda
   cudaError_t e;
   if ((e = set_max_smem_once<kv_attention_kernel<D>>(kv_smem_bytes<D>())) != cudaSuccess) return e;
   const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * ((a.KH + p.heads - 1) / p.heads);
-  return launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(jobs)), dim3(kKvThreads), kv_smem_bytes<D>(), use_pdl,
+  return launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(jobs)), dim3(KvLayout<D>::kThreads), kv_smem_bytes<D>(), use_pdl,
                    s, a, p);
 }
 

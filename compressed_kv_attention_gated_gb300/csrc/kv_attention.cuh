@@ -116,7 +116,6 @@ constexpr int kKvKeys = 128, kKvUnit = 32768;  // keys of a tile; bytes of a uni
 constexpr int kKvMaxRing = 6;                  // places of the ring
 constexpr int kKvShort = 2;                    // tiles of keys of a job behind which the next one is taken at once
 constexpr float kKvJump = 16.f;                // log2 of the largest weight over its reference
-constexpr int kMmaWarp = 8, kPlanWarp = 9, kMmaWarp2 = 10, kCopyWarp = 12, kKvThreads = 512;
 
 struct Job {
   KvTile tile;
@@ -258,7 +257,7 @@ __device__ __forceinline__ bool plan_jobs(const KvAttentionArgs& a, const KvPlan
 // get it by a shuffle; places are counted in KvSide::unit bytes, so that they have 32 bits.
 template <typename L>
 __device__ __forceinline__ bool copy_jobs(const KvAttentionArgs& a, KvCommon& sm, uint8_t* smem) {
-  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - kCopyWarp, x = lane & 15, upper = lane >> 4;
+  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - L::kCopyWarp, x = lane & 15, upper = lane >> 4;
   constexpr bool kLate = L::kRows == 256;
   uint32_t unit = 0, q_use = 0;
   auto arrive = [](uint64_t* bar) { asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory"); };

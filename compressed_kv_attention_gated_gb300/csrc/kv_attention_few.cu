@@ -44,6 +44,7 @@ template <int D_, int R>
 struct FewLayout {
   static constexpr int D = D_;
   static constexpr int kRows = R;
+  static constexpr int kMmaWarp = 8, kPlanWarp = 9, kCopyWarp = 12, kThreads = 512;  // behind the softmax's eight
   static constexpr int kKU = D / 128;  // units of a tile's keys, and of its values
   static constexpr int kQRows = R;
   static constexpr bool kFindMissing = false;  // a softmax thread looks up the page of its key while it waits
@@ -388,7 +389,7 @@ __device__ __forceinline__ bool few_mma(const KvAttentionArgs& a, FewSmall<R>& s
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kKvThreads, 1)
+__global__ void __launch_bounds__((FewLayout<D, R>::kThreads), 1)
     kv_attention_few_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ KvPlan p) {
   using L = FewLayout<D, R>;
   // no static shared memory: the dynamic one begins on the swizzle's 1024 bytes (checked below)
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     if (threadIdx.x == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
     return;
   }
-  if (warp == kMmaWarp) {
+  if (warp == L::kMmaWarp) {
     if (lane == 0) {
       for (int i = 0; i < L::kRing; ++i) {
         mbar_init(&sm.full[i], 128);
@@ -431,10 +432,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   pdl_wait();
 
   bool ok = true;
-  if (warp < kMmaWarp) {
+  if (warp < L::kMmaWarp) {
     ok = few_soft<D, R>(a, p, sm, smem, tmem);
     tc_fence_before();
-  } else if (warp == kMmaWarp) {
+  } else if (warp == L::kMmaWarp) {
     if (elect_one()) {
       ok = few_mma<D, R>(a, sm, smem_u32(smem), tmem);
       // the end of every product: tensor memory may be given back
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       if (!ok) flag_error(a.err, CKV_DEVERR_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp == kPlanWarp) {
+  } else if (warp == L::kPlanWarp) {
     ok = plan_jobs<L>(a, p, sm, [&](const Job& j, uint32_t i) {
       FewRows<R>& rows = sm.rows[i];
       int32_t c_min = INT32_MAX, low_max = 0;
@@ -475,13 +476,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         rows.low_max = low_max;
       }
     });
-  } else if (warp >= kCopyWarp) {
+  } else if (warp >= L::kCopyWarp) {
     ok = copy_jobs<L>(a, sm, smem);
   }
   if (!ok && lane == 0) flag_error(a.err, CKV_DEVERR_TIMEOUT);
   pdl_trigger();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == L::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
@@ -499,7 +500,7 @@ cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cuda
   // there only jobs of one tile keep them (1024 tokens x 64 heads: 128 keys 65 us against 72, 1024 keys 256 against 242).
   b.same = c.k == c.v && c.k_stride_page == c.v_stride_page && c.k_stride_row == c.v_stride_row && c.k_stride_head == c.v_stride_head &&
            (FewLayout<D, R>::kRing > FewLayout<D, R>::kKU || p.chunk <= kKvKeys);
-  return launch_ex(kv_attention_few_kernel<D, R>, dim3(static_cast<unsigned>(jobs)), dim3(kKvThreads), few_smem_bytes<D, R>(),
+  return launch_ex(kv_attention_few_kernel<D, R>, dim3(static_cast<unsigned>(jobs)), dim3(FewLayout<D, R>::kThreads), few_smem_bytes<D, R>(),
                    use_pdl, s, b, p);
 }
 
