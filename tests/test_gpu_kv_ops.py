@@ -462,6 +462,59 @@ def test_nothing_is_written_beside_the_outputs(ck, D, H, KH, n, before, window):
             s.run(ck, workspace=w[:need - 1])
 
 
+@pytest.mark.parametrize("D,H,KH,n", [(128, 1024, 1, [2, 1]), (128, 1024, 1024, [1, 3]), (512, 1024, 2, [1, 1]), (256, 1000, 8, [3, 2])])
+def test_a_thousand_heads(ck, D, H, KH, n):
+    s = Step(D, H, KH, n, [60, 9], 16, 40, 3, sink=True, seed=H)
+    out, lse, err = s.run(ck)
+    assert int(err) == 0
+    s.check(out, lse)
+
+
+@pytest.mark.parametrize("window", [0, 20])
+def test_65536_requests(ck, window):
+    """Requests that repeat: the first ones against the reference, the others against those."""
+    B, kinds, D, H, ps = 65536, 64, 128, 4, 16
+    s = Step(D, H, 2, [1] * kinds, [i for i in range(kinds)], ps, window, seed=14)
+    want = s.run(ck)
+    s.check(*want[:2])
+    of = torch.arange(B, device="cuda") % kinds
+    got = ck.ckv_kv_attention(s.q[of], s.k, s.v, s.table[of], _i32(range(B + 1)), _i32(s.ctx)[of], s.max_rows, s.scale, window=window)
+    assert torch.equal(got[0], want[0][of]) and torch.equal(got[1], want[1][of])
+    # most of them without tokens
+    start = _i32(np.minimum(np.arange(B + 1), kinds))
+    got = ck.ckv_kv_attention(s.q, s.k, s.v, s.table[of], start, _i32(s.ctx), s.max_rows, s.scale, window=window)
+    s.check(*got)
+    with pytest.raises(Exception):
+        ck.ckv_kv_attention(s.q, s.k, s.v, s.table[of[:1]].expand(B + 1, -1), torch.zeros(B + 2, dtype=torch.int32, device="cuda"), _i32(s.ctx), s.max_rows, s.scale)
+
+
+def test_no_tokens_and_no_requests(ck):
+    s = Step(128, 8, 2, [1], [20], seed=15)
+    out, lse = ck.ckv_kv_attention(s.q[:0], s.k, s.v, s.table, _i32([0, 0]), _i32([]), s.max_rows, s.scale)
+    assert out.shape == (0, 8, 128) and lse.shape == (0, 8)
+    kept = torch.full_like(s.q, 2.0)
+    ck.ckv_kv_attention(s.q, s.k, s.v, s.table[:0], _i32([0]), _i32(s.ctx), s.max_rows, s.scale, out=kept)
+    assert torch.all(kept == 2)
+    m, p = ck.ckv_build_tree_masks(_i32([]), _i32([0]), None, 1)
+    assert m.shape == (0, 1) and p.shape == (0,)
+    assert ck.ckv_kv_append(s.k[:0, 0], s.v[:0, 0], s.k, s.v, torch.zeros(0, dtype=torch.int64, device="cuda"), q=s.q[:0]).shape == (0, 8, 128)
+    assert ck.ckv_merge_attention([out], [lse])[0].shape == (0, 8, 128)
+
+
+@pytest.mark.parametrize("D,H,KH,n", [(128, 8, 1, [1]), (128, 32, 1, [9]), (256, 32, 1, [9]), (512, 64, 1, [1])])
+def test_constant_values_over_a_long_context(ck, D, H, KH, n):
+    """150,000 rows whose scores are all the same: the tensor cores cut a range's sum off towards 0 by less than 2^-23 of it
+    per 16 keys, 2^17 / 16 times at most, which is 2^-10 of it; then the rounding."""
+    L, ps = 150_000, 1000
+    k, v = torch.zeros(L // ps, ps, KH, D, device="cuda").bfloat16(), torch.full((L // ps, ps, KH, D), 1.75, device="cuda").bfloat16()
+    q = torch.ones(n[0], H, D, device="cuda").bfloat16()
+    table = torch.arange(L // ps, dtype=torch.int32, device="cuda")[None]
+    out, lse = ck.ckv_kv_attention(q, k, v, table, _i32([0, n[0]]), _i32([L - n[0] + i + 1 for i in range(n[0])]), L, 1.0)
+    assert torch.all((out.double() - 1.75).abs() <= 1.75 * (2.0 ** -8 + 2.0 ** -10))
+    want = torch.tensor([float(np.log(L - n[0] + i + 1)) for i in range(n[0])], device="cuda").double()
+    assert torch.all((lse.double() - want[:, None]).abs() <= 2.0 ** -16)
+
+
 def test_calls_of_two_streams_at_once(ck):
     """Each with its own tensors and workspace; results are those of calls one after the other."""
     steps = [Step(128, 8, 1, [1, 2], [9000, 3000], 64, seed=1), Step(128, 32, 8, [300, 5], [700, 100], 64, 256, 4, seed=2),
