@@ -1114,7 +1114,7 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
   const int64_t rows = (T + B - 1) / B * G;  // of an average request and key head
   // At D = 512 a tile of 128 rows has no place in tensor memory beside its scores, and two CTAs that form them both for half
   // of the channels each take longer than tiles of 64 rows (8000 tokens x 64 heads, windows of 128 to 4096 rows: 698 against
-  // 315 us, 1659 against 1323, 3211 against 2965).  Below it, longer tiles win (D = 256, 32 heads, 4096: 631 against 942).
+  // 336 us, 1659 against 1323, 3211 against 2965).  Below it, longer tiles win (D = 256, 32 heads, 4096: 631 against 942).
   const int R = p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D == 512 ? 64 : D == 128 ? 256 : 128;
   const int64_t pad = kv_tile_pad(G, R);
   p.tiles = static_cast<int>((T * G + static_cast<int64_t>(B) * pad) / R);

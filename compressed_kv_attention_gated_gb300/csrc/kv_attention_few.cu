@@ -16,7 +16,7 @@
 // Bound by HBM with grouped heads (every row of the window is read once for its heads): 256 tokens x 64 heads over
 // 1024 rows of 8 key heads, D = 128, 163 us, 99% of the copy rate.  At D = 512 with 64 rows queries (64 KB), P and one
 // tile of keys fill shared memory, and the next tile's keys wait for the second product of this one: 1024 tokens x
-// 64 heads over 128 rows 58 us (4.6 TB/s), 8000 over 128 rows 315 us.  With more keys M = 128 and N = 64 leave the
+// 64 heads over 128 rows 60 us (4.5 TB/s), 8000 over 128 rows 336 us.  With more keys M = 128 and N = 64 leave the
 // products bound by shared memory at two thirds of the tensor cores' rate (8000 tokens over 4096 rows 2965 us, 1.24 PFLOP/s).
 #include "kv_attention.cuh"
 
@@ -111,8 +111,7 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
     float l[kCols];
 #pragma unroll
     for (int i = 0; i < kCols; ++i) l[i] = 0.f;
-    if (place < kCols) sm.ref[c0 + place] = kNegBig;
-    group_barrier(w);
+    if (n == 0 && place < kCols) sm.ref[c0 + place] = kNegBig;
 #pragma unroll 1
     for (int j = 0; j < n; ++j, ++tile) {
       const int buf = tile & 1;
@@ -173,17 +172,16 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
       float z[kCols];
       read_scores(z);
       // a job's first tile sets the references (nothing is lost where that was not to be known)
-      if (group_any(w, !ok || j == 0 || over_refs(z) > kKvJump)) {
-        if (group_any(w, !ok)) return false;
+      if (j == 0 || group_any(w, !ok || over_refs(z) > kKvJump)) {
         // new references: the largest score so far of each row
         if (j > 0) read_scores(z);
         const float top = reduce_columns<kCols, true>(z, lane);
         constexpr int kShare = 32 / kCols;  // lanes that hold the same row's result
         if (lane % kShare == 0) sm.part[quad][c0 + lane / kShare] = top;
-        group_barrier(w);
+        if (group_any(w, !ok)) return false;
         if (place < kCols) {
           const int r = c0 + place;
-          const float old = sm.ref[r];
+          const float old = j == 0 ? kNegBig : sm.ref[r];
           const float now = fmaxf(fmaxf(fmaxf(sm.part[0][r], sm.part[1][r]), fmaxf(sm.part[2][r], sm.part[3][r])), old);
           sm.keep[r] = fast_exp2(old - now);
           sm.ref[r] = now;
@@ -287,26 +285,23 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
         // Through the group's own pieces of P, whose last product is done (the other group may be a job ahead and writing
         // its own), so that rows leave in 16-byte pieces.  Neighbouring lanes (channels) trade halves: the even one has
         // both channels of row i, the odd one of row i + 1.
-        auto piece_of = [&](int r, int y) {  // piece y of the group's row r
-          const int at = r % 8 * 16 + (y ^ (r % 2 * 4));
-          return smem + L::kP + at * 128 + ((c0 / 8 + r / 8) ^ (at & 7)) * 16;
-        };
-        const bool odd = lane & 1;
+        // Piece y of the group's row r is piece r / 8 of its own in row at = r % 8 * 16 + (y, by 4 further on in odd rows) of P.
+        const int odd = lane & 1, to = odd * 16 + ((quad * 4 + lane / 8) ^ (odd * 4));
 #pragma unroll
         for (int i = 0; i < kCols; i += 2) {
           const float o0 = o[i] * l[i], o1 = o[i + 1] * l[i + 1];
           const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? o0 : o1, 1);
-          *reinterpret_cast<uint32_t*>(piece_of(i + (odd ? 1 : 0), quad * 4 + lane / 8) + lane % 8 / 2 * 4) =
+          *reinterpret_cast<uint32_t*>(smem + L::kP + (i % 8 * 16 + to) * 128 + ((c0 / 8 + i / 8) ^ (to & 7)) * 16 + lane % 8 / 2 * 4) =
               odd ? pack_bf16x2_rn(got, o1) : pack_bf16x2_rn(o0, got);
         }
         group_barrier(w);
 #pragma unroll
         for (int i = 0; i < kCols / 8; ++i) {
-          const int r = i * 8 + place / 16;
-          const int32_t flat = rows.flat[c0 + r];
+          const int at = place ^ (place / 16 % 2 * 4);
+          const int32_t flat = rows.flat[c0 + i * 8 + place / 16];
           if (flat >= 0)
             *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(flat) * D + u * 128 + place % 16 * 8) =
-                *reinterpret_cast<const uint4*>(piece_of(r, place % 16));
+                *reinterpret_cast<const uint4*>(smem + L::kP + at * 128 + ((c0 / 8 + i) ^ (at & 7)) * 16);
         }
         group_barrier(w);
       }
