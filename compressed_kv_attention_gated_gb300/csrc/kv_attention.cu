@@ -1150,9 +1150,24 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
   return p;
 }
 
+// Warps that ask for more registers than the CTA has would wait for ever: the registers of its launch have to be as counted.
+template <int D>
+cudaError_t check_registers_once() {
+  static const cudaError_t result = [] {
+    using L = KvLayout<D>;
+    cudaFuncAttributes attr;
+    const cudaError_t e = cudaFuncGetAttributes(&attr, kv_attention_kernel<D>);
+    if (e != cudaSuccess) return e;
+    const int need = L::kSoftWarps * 32 * L::kSoftRegs + (L::kThreads - L::kSoftWarps * 32) * L::kOtherRegs;
+    return attr.numRegs * L::kThreads >= need ? cudaSuccess : cudaErrorInvalidConfiguration;
+  }();
+  return result;
+}
+
 template <int D>
 cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cudaStream_t s) {
   cudaError_t e;
+  if ((e = check_registers_once<D>()) != cudaSuccess) return e;
   if ((e = set_max_smem_once<kv_attention_kernel<D>>(kv_smem_bytes<D>())) != cudaSuccess) return e;
   const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * ((a.KH + p.heads - 1) / p.heads);
   return launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(jobs)), dim3(KvLayout<D>::kThreads), kv_smem_bytes<D>(), use_pdl,
