@@ -432,6 +432,17 @@ def test_rows_that_are_key_and_value_or_not(ck, D, H, KH, n, shared):
     s.check(out, lse)
 
 
+@pytest.mark.parametrize("D,H,KH,n", [(128, 8, 1, [1, 2]), (128, 32, 1, [20, 3]), (256, 32, 2, [20, 3]), (512, 64, 1, [2, 1])])
+@pytest.mark.parametrize("tree", [False, True])
+def test_a_bound_far_above_the_contexts(ck, D, H, KH, n, tree):
+    """Most ranges of keys are empty, and those of one request where the other's are not."""
+    s = Step(D, H, KH, n, [300, 9], 16, tree=tree, sink=True, seed=D, width_more=1000)
+    assert ck.ckv_kv_attention_workspace(sum(n), 2, H, KH, D, 16000, mask_words=1 if tree else 0) > 0
+    out, lse, err = s.run(ck, max_rows=16000)
+    assert int(err) == 0
+    s.check(out, lse)
+
+
 @pytest.mark.parametrize("D,H,KH,n", [(128, 8, 2, [1, 2]), (128, 32, 2, [20, 3]), (256, 32, 2, [20, 3]), (512, 64, 1, [2, 1])])
 def test_negative_and_zero_scale(ck, D, H, KH, n):
     for scale in (-0.07, 0.0):
