@@ -1075,7 +1075,7 @@ __global__ void __launch_bounds__(128, kFew ? 12 : 4) kv_join_kernel(const __gri
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-  if (a.sink) all += sink == m ? 1.f : fast_exp2((sink - safe) * kLog2e);
+  if (a.sink) all += sink == safe ? 1.f : fast_exp2((sink - safe) * kLog2e);  // safe: one of -infinity counts for nothing
   const float4* o = reinterpret_cast<const float4*>(ws + flat * D + part * 128) + lane;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

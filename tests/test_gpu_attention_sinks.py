@@ -1,0 +1,37 @@
+"""Sinks at the ends of their type, in the attention over the uncompressed cache: one of -infinity leaves all as it is
+without one, and where nothing is seen lse is the sink itself."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_kv_ops import Step, ck  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# D, H, KH, tokens of two requests: keys on the M side, rows on the M side
+FORMS = [(128, 8, 1, [1, 2]), (128, 32, 1, [20, 3]), (256, 8, 1, [1, 2]), (256, 32, 1, [20, 3]), (512, 64, 1, [2, 1])]
+
+
+def _step(D, H, KH, n, before):
+    """The first and the last token see nothing."""
+    s = Step(D, H, KH, n, before, 16, sink=True, seed=D, width_more=1000)
+    s.ctx = np.array(s.ctx)
+    s.ctx[[0, -1]] = 0
+    return s
+
+
+@pytest.mark.parametrize("D,H,KH,n", FORMS)
+def test_minus_infinity_over_ranges_of_keys(ck, D, H, KH, n):  # noqa: F811
+    """A bound far above the contexts splits the keys; what is merged behind it counts alone where nothing was seen."""
+    s = _step(D, H, KH, n, [300, 9])
+    s.sink[::2] = -torch.inf
+    assert ck.ckv_kv_attention_workspace(sum(n), 2, H, KH, D, 16000) > 0
+    out, lse, err = s.run(ck, max_rows=16000)
+    assert int(err) == 0
+    s.check(out, lse)
+    assert torch.equal(lse[0], s.sink) and torch.equal(lse[-1], s.sink)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    far, far_lse = torch.randn(out.shape, generator=g, device="cuda").bfloat16(), torch.randn(lse.shape, generator=g, device="cuda")
+    both, total = ck.ckv_merge_attention([out, far], [lse, far_lse])
+    off = torch.isneginf(lse)
+    assert int(off.sum()) == H and torch.equal(both[off], far[off]) and torch.equal(total[off], far_lse[off])
