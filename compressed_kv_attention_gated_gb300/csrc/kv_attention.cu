@@ -269,7 +269,8 @@ __device__ __forceinline__ float finish_row(const KvAttentionArgs& a, const KvPl
     m = high;
   }
   if (flat >= 0 && tell) {
-    const float lse = all == 0.f ? -INFINITY : (m + log2f(all)) * kKvLn2;
+    // nothing at all: no sink, or one that is -infinity in log2 units
+    const float lse = all == 0.f ? a.sink && !split ? a.sink[flat % a.H] : -INFINITY : (m + log2f(all)) * kKvLn2;
     if (split) static_cast<float*>(a.workspace)[a.T * a.H * (p.splits * D + static_cast<int64_t>(range)) + flat] = lse;
     else if (a.lse) a.lse[flat] = lse;
   }

@@ -252,7 +252,8 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
       }
       sm.scale[r] = none ? 0.f : keep / all;
       if (flat >= 0) {
-        const float lse = all == 0.f ? -INFINITY : (m + log2f(all)) * kKvLn2;
+        // nothing at all: no sink, or one that is -infinity in log2 units
+        const float lse = all == 0.f ? a.sink && !split ? a.sink[flat % a.H] : -INFINITY : (m + log2f(all)) * kKvLn2;
         if (split) part_out[p.splits * all_rows * D + range + flat] = lse;
         else if (a.lse) a.lse[flat] = lse;
       }

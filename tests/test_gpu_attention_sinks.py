@@ -1,5 +1,8 @@
-"""Sinks at the ends of their type, in the attention over the uncompressed cache: one of -infinity leaves all as it is
-without one, and where nothing is seen lse is the sink itself."""
+"""Sinks at the ends of their type, in the attention over the uncompressed cache.
+
+A sink takes part in the sum alone: one of -infinity, or so low that its weight is 0 against every score, leaves
+all as it is without one, bit for bit.  Where nothing is seen lse is the sink itself (tolerance 2^-22 of it: it goes
+through units of log2 and back, four roundings of 2^-24)."""
 import numpy as np
 import pytest
 import torch
@@ -10,6 +13,7 @@ pytestmark = pytest.mark.gpu
 
 # D, H, KH, tokens of two requests: keys on the M side, rows on the M side
 FORMS = [(128, 8, 1, [1, 2]), (128, 32, 1, [20, 3]), (256, 8, 1, [1, 2]), (256, 32, 1, [20, 3]), (512, 64, 1, [2, 1])]
+LOWEST = torch.finfo(torch.float32).min
 
 
 def _step(D, H, KH, n, before):
@@ -35,3 +39,21 @@ def test_minus_infinity_over_ranges_of_keys(ck, D, H, KH, n):  # noqa: F811
     both, total = ck.ckv_merge_attention([out, far], [lse, far_lse])
     off = torch.isneginf(lse)
     assert int(off.sum()) == H and torch.equal(both[off], far[off]) and torch.equal(total[off], far_lse[off])
+
+
+@pytest.mark.parametrize("D,H,KH,n", FORMS)
+@pytest.mark.parametrize("before,rows", [([40, 9], None), ([300, 9], 16000)])
+def test_the_lowest_values(ck, D, H, KH, n, before, rows):  # noqa: F811
+    """In one range of keys and in several."""
+    s = _step(D, H, KH, n, before)
+    assert (ck.ckv_kv_attention_workspace(sum(n), 2, H, KH, D, rows or s.max_rows) > 0) == (rows is not None)
+    s.sink[:] = torch.tensor([LOWEST, -torch.inf, -3e38, LOWEST, -1e30, 4.0, LOWEST, -2e38], device="cuda").repeat(H // 8)
+    out, lse, err = s.run(ck, max_rows=rows)
+    assert int(err) == 0
+    s.check(out, lse)
+    ends = s.sink <= -3e38
+    assert torch.equal(lse[0][ends], s.sink[ends]) and torch.equal(lse[-1][ends], s.sink[ends])
+    low = s.sink < 0
+    s.sink = None
+    plain = s.run(ck, max_rows=rows)
+    assert torch.equal(plain[0][:, low], out[:, low]) and torch.equal(plain[1][1:-1, low], lse[1:-1, low])
