@@ -351,7 +351,8 @@ __global__ void __launch_bounds__((Layout<D, R>::kThreads), 1) fp4_attention_ker
           } else {
             sm.c[r] = all == 0.f ? 0.f : a.g / all;
           }
-          if (a.lse && flat >= 0) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+          // nothing at all: no sink, or one that is -infinity in log2 units
+          if (a.lse && flat >= 0) a.lse[flat] = all == 0.f ? a.sink ? a.sink[flat % a.H] : -INFINITY : (m + log2f(all)) * kLn2;
         }
       }
       soft_barrier();

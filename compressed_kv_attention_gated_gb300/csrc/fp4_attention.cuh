@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(128, kFew ? 12 : 4) fp4_join_kernel(const __gr
   const float inv = all == 0.f ? 0.f : a.g / all;
   *reinterpret_cast<uint2*>(a.out + flat * D + part * 128 + lane * 4) =
       make_uint2(pack_bf16x2_rn(acc[0] * inv, acc[1] * inv), pack_bf16x2_rn(acc[2] * inv, acc[3] * inv));
-  if (part == 0 && lane == 0 && a.lse) a.lse[flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+  // nothing at all: no sink, or one that is -infinity in log2 units
+  if (part == 0 && lane == 0 && a.lse) a.lse[flat] = all == 0.f ? a.sink ? a.sink[flat % a.H] : -INFINITY : (m + log2f(all)) * kLn2;
 }
 
 template <int D, int R, int kHalves>

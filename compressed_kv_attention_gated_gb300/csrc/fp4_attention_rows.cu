@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(RowLayout<D>::kThreads, 1)
           m = high;
         }
         scale = all == 0.f ? 0.f : keep * a.g / all;
-        if (a.lse && my_flat >= 0 && half == 0 && half_v == 0) a.lse[my_flat] = all == 0.f ? -INFINITY : (m + log2f(all)) * kLn2;
+        // nothing at all: no sink, or one that is -infinity in log2 units
+        if (a.lse && my_flat >= 0 && half == 0 && half_v == 0)
+          a.lse[my_flat] = all == 0.f ? a.sink ? a.sink[my_flat % a.H] : -INFINITY : (m + log2f(all)) * kLn2;
       }
       if (n > 0 && ok) {
         // not o_done: a warp that has not waited for tile n - 2 could take its phase for the last one's

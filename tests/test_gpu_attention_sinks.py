@@ -1,4 +1,4 @@
-"""Sinks at the ends of their type, in the attention over the uncompressed cache.
+"""Sinks at the ends of their type, in the attention over the uncompressed cache and in the one over 4-bit rows.
 
 A sink takes part in the sum alone: one of -infinity, or so low that its weight is 0 against every score, leaves
 all as it is without one, bit for bit.  Where nothing is seen lse is the sink itself (tolerance 2^-22 of it: it goes
@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from test_gpu_kv_ops import Step, ck  # noqa: F401
+from test_gpu_serving_ops import _attn_inputs, _err, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +58,18 @@ def test_the_lowest_values(ck, D, H, KH, n, before, rows):  # noqa: F811
     s.sink = None
     plain = s.run(ck, max_rows=rows)
     assert torch.equal(plain[0][:, low], out[:, low]) and torch.equal(plain[1][1:-1, low], lse[1:-1, low])
+
+
+@pytest.mark.parametrize("D,H,n,ctx", [(256, 6, [1, 3], [50, 0, 200, 200]), (128, 8, [1, 2], [3, 0, 9000]), (512, 64, [1, 2], [0, 3, 40]),
+                                       (128, 32, [60, 20], [0, 100] * 40), (256, 32, [60], [2000] * 59 + [0])])
+def test_the_lowest_value_over_4_bit_rows(ck, D, H, n, ctx):  # noqa: F811
+    rng = np.random.default_rng(D + H)
+    ctx = np.array(ctx)
+    start, T, table, cache, q, width = _attn_inputs(rng, np.array(n), ctx, H, D, 16)
+    args = (q.cuda(), torch.from_numpy(cache).cuda(), _i32(table), _i32(start), _i32(ctx), int(ctx.max()), 0.06)
+    err = _err()
+    o, l = ck.ckv_fp4_attention(*args, err_word=err)
+    blind = torch.from_numpy(ctx == 0).cuda()
+    for low in (LOWEST, -torch.inf):
+        o1, l1 = ck.ckv_fp4_attention(*args, sink=torch.full((H,), low, device="cuda"), err_word=err)
+        assert int(err) == 0 and torch.equal(o, o1) and torch.equal(l[~blind], l1[~blind]) and bool((l1[blind] == low).all())
