@@ -838,7 +838,7 @@ ckv_status ckv_build_tree_masks(const int32_t* parents, const int32_t* row_start
 int64_t ckv_kv_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows,
                                    int32_t window, int32_t first_rows, int32_t mask_words) {
   if (T <= 0 || B <= 0 || !kv_attention_sizes_ok(T, B, H, KH, D, max_rows, window, first_rows, mask_words)) return 0;
-  return ckv::kv_attention_workspace(T, B, H, KH, D, max_rows, window, first_rows, mask_words);
+  return std::max<int64_t>(ckv::kv_attention_workspace(T, B, H, KH, D, max_rows, window, first_rows, mask_words), 0);
 }
 
 ckv_status ckv_kv_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int64_t T, int32_t H,
@@ -857,13 +857,14 @@ ckv_status ckv_kv_attention(const uint16_t* q, int64_t q_stride_t, int64_t q_str
   if (!kv_attention_sizes_ok(T, B, H, KH, D, max_rows, window, first_rows, mask_words) ||
       max_rows > static_cast<int64_t>(max_pages) * cache->page_size || q_stride_t < 0 || q_stride_h < 0)
     return CKV_ERR_SHAPE;
+  const int64_t need = ckv::kv_attention_workspace(T, B, H, KH, D, max_rows, window, first_rows, mask_words);
+  if (need < 0) return CKV_ERR_SHAPE;
   if (!q || !block_table || !row_start || !ctx_rows || !out || (mask_words > 0 && !tree_mask)) return CKV_ERR_NULL;
   if (ckv_status c = check_kv_pointers(cache, true)) return c;
   if (!aligned(q, 16) || q_stride_t % 8 || q_stride_h % 8 || !aligned(block_table, 4) || !aligned(row_start, 4) || !aligned(ctx_rows, 4) ||
       !aligned(tree_mask, 8) || !aligned(sink, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
       !aligned(err_word, 4))
     return CKV_ERR_ALIGN;
-  const int64_t need = ckv::kv_attention_workspace(T, B, H, KH, D, max_rows, window, first_rows, mask_words);
   if (need > 0 && !workspace) return CKV_ERR_NULL;
   if (workspace_bytes < need) return CKV_ERR_SHAPE;
   // several CTAs read a query row, and one may have written its output before another has read

@@ -261,6 +261,7 @@ static_assert(kKvMaxSplits * kKvMaxRange == CKV_KV_ATTENTION_MAX_ROWS, "header")
 cudaError_t launch_kv_append(const KvAppendArgs& a, int D, int dtype, bool use_pdl, cudaStream_t s);
 cudaError_t launch_tree_masks(const TreeMasksArgs& a, bool use_pdl, cudaStream_t s);
 cudaError_t launch_merge_attention(const MergeArgs& a, int D, int dtype, int out_dtype, bool use_pdl, cudaStream_t s);
+// -1: sizes that do not fit a launch.
 int64_t kv_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows, int32_t window,
                                int32_t first_rows, int32_t words);
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, bool use_pdl, cudaStream_t s);

@@ -1132,6 +1132,7 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
   int64_t best_s = least;
   double best = 0;
   for (int64_t s = least; s <= most && s <= kKvMaxSplits; ++s) {
+    if (s > least && p.tiles * s * KH > INT32_MAX) break;  // CTAs of a grid
     const int64_t waves = (busy * s + 151) / 152;
     double us = static_cast<double>(waves) * (around + tile * static_cast<double>((most + s - 1) / s));
     if (s > 1) us += 2.5 + 0.02 * static_cast<double>(s) + 2.0 * static_cast<double>(T * H * s) * D * 4 / 4e6;
@@ -1170,8 +1171,7 @@ cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cuda
   cudaError_t e;
   if ((e = check_registers_once<D>()) != cudaSuccess) return e;
   if ((e = set_max_smem_once<kv_attention_kernel<D>>(kv_smem_bytes<D>())) != cudaSuccess) return e;
-  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * ((a.KH + p.heads - 1) / p.heads);
-  return launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(jobs)), dim3(KvLayout<D>::kThreads), kv_smem_bytes<D>(), use_pdl,
+  return launch_ex(kv_attention_kernel<D>, dim3(static_cast<unsigned>(kv_jobs(p, a.KH))), dim3(KvLayout<D>::kThreads), kv_smem_bytes<D>(), use_pdl,
                    s, a, p);
 }
 
@@ -1203,6 +1203,7 @@ cudaError_t launch_d(const KvAttentionArgs& args, bool use_pdl, cudaStream_t s) 
 int64_t kv_attention_workspace(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows, int32_t window, int32_t first_rows,
                                int32_t words) {
   const KvPlan p = plan_kv(T, B, H, KH, D, max_rows, window, window > 0 ? first_rows : 0, words);
+  if (kv_jobs(p, KH) > INT32_MAX) return -1;  // more CTAs than a grid has
   if (p.sorted) return (2 * static_cast<int64_t>(B) + 1) * static_cast<int64_t>(sizeof(int32_t));
   return p.splits == 1 ? 0 : static_cast<int64_t>(p.splits) * T * H * (D + 1) * static_cast<int64_t>(sizeof(float));
 }

@@ -23,6 +23,8 @@ struct KvPlan {
   int heads;   // key heads whose jobs a CTA takes together
   bool sorted; // requests with the longest contexts first, by kv_order_kernel
 };
+// CTAs of the launch: a tile, a range of keys and p.heads key heads each.
+inline int64_t kv_jobs(const KvPlan& p, int32_t KH) { return static_cast<int64_t>(p.tiles) * p.splits * ((KH + p.heads - 1) / p.heads); }
 cudaError_t launch_kv_attention_few(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cudaStream_t s);
 
 namespace {

@@ -489,14 +489,13 @@ cudaError_t launch(const KvAttentionArgs& a, const KvPlan& p, bool use_pdl, cuda
   static_assert(few_smem_bytes<D, R>() <= 227 * 1024, "shared memory");
   cudaError_t e;
   if ((e = set_max_smem_once<kv_attention_few_kernel<D, R>>(few_smem_bytes<D, R>())) != cudaSuccess) return e;
-  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.splits * ((a.KH + p.heads - 1) / p.heads);
   KvAttentionArgs b = a;
   const ckv_kv_cache& c = a.cache;
   // Units that stay keep the next tile's out of a ring that has no more places than one tile has units (D = 512, 64 rows):
   // there only jobs of one tile keep them (1024 tokens x 64 heads: 128 keys 65 us against 72, 1024 keys 256 against 242).
   b.same = c.k == c.v && c.k_stride_page == c.v_stride_page && c.k_stride_row == c.v_stride_row && c.k_stride_head == c.v_stride_head &&
            (FewLayout<D, R>::kRing > FewLayout<D, R>::kKU || p.chunk <= kKvKeys);
-  return launch_ex(kv_attention_few_kernel<D, R>, dim3(static_cast<unsigned>(jobs)), dim3(FewLayout<D, R>::kThreads), few_smem_bytes<D, R>(),
+  return launch_ex(kv_attention_few_kernel<D, R>, dim3(static_cast<unsigned>(kv_jobs(p, a.KH))), dim3(FewLayout<D, R>::kThreads), few_smem_bytes<D, R>(),
                    use_pdl, s, b, p);
 }
 
