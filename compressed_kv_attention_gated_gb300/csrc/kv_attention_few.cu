@@ -119,7 +119,7 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
       const int32_t v = v0 + j * kKvKeys, k0 = low0 + v - head0;  // first place; its row, were it none of the first ones
       const int32_t key = v + place < head0 ? v + place : k0 + place;
       const bool gone = v + place < v1 && !kv_page_there(a, table[kv_page_of(a, key)]), there = v + place < v1 && !gone;
-      ok = mbar_wait_near(&sm.s_full[buf], (tile >> 1) & 1);
+      ok = mbar_wait_near(&sm.s_full[buf], (tile >> 1) & 1) && ok;  // a wait that ran out before is not forgotten
       __syncwarp();
       tc_fence_after();
       const uint32_t at_s = tmem + lanes + L::kTmemS + buf * 64 + c0;
@@ -191,7 +191,7 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
           load_row<kCols>(&sm.keep[c0], z);
 #pragma unroll
           for (int i = 0; i < kCols; ++i) l[i] *= z[i];
-          ok = mbar_wait_near(&sm.pv_done[0], (tile - 1) & 1);
+          ok = mbar_wait_near(&sm.pv_done[0], (tile - 1) & 1) && ok;
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1

@@ -1,5 +1,8 @@
 """The ends of what the operators around the uncompressed cache accept, on the CPU: every call here returns during
 argument validation."""
+import os
+import re
+
 import pytest
 
 from test_kv_ops_host import ATTN, P, _cache, _call, lib  # noqa: F401
@@ -24,3 +27,14 @@ def test_grids_beyond_31_bits(lib, B, KH, rows, takes):  # noqa: F811
     # the same rows behind a window, and in one request
     assert _call(lib.ckv_kv_attention, call, **sizes, window=4096, q=None) == 1
     assert _call(lib.ckv_kv_attention, call, **{**sizes, "B": 1}, q=None) == 1
+
+
+@pytest.mark.parametrize("name", ["kv_attention.cu", "kv_attention_few.cu"])
+def test_no_answer_of_a_wait_is_written_over(name):
+    """A wait that runs out ends the kernel with an error, which no later wait may take back: an answer goes into `ok`
+    together with those before it.  (From the source: on a GPU it would take a wait that does not end.)"""
+    import compressed_kv_attention_gated_gb300 as ck
+
+    text = open(os.path.join(os.path.dirname(ck.__file__), "csrc", name)).read()
+    waits = re.findall(r"\bok = [^;]*mbar_wait_near\([^;]*;", text)
+    assert waits and all(re.search(r"&& ok;$|= ok &&", w) for w in waits), waits
