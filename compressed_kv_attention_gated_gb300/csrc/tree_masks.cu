@@ -39,9 +39,10 @@ __global__ void __launch_bounds__(kTreeThreads) tree_masks_kernel(const __grid_c
   const int32_t n = t1 - t0, most = a.words * 64, used = min(n, most);
   for (int32_t i = threadIdx.x; i < used; i += kTreeThreads) {
     int32_t p = a.parents[t0 + i];
-    s_ctx[i] = a.ctx_rows ? a.ctx_rows[t0 + i] : 0;
+    const int32_t ctx = a.ctx_rows ? a.ctx_rows[t0 + i] : 0;
+    s_ctx[i] = ctx;
     if (p < -1 || p >= i) {
-      flag_error(a.err, CKV_DEVERR_PLAN);
+      if (ctx >= 0) flag_error(a.err, CKV_DEVERR_PLAN);  // padding has no parent
       p = -1;
     }
     s_parent[i] = static_cast<int16_t>(p);
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_masks_kernel(const __grid_c
   for (int32_t i = threadIdx.x; i < n; i += kTreeThreads) {
     const int32_t t = t0 + i, ctx = i < most ? s_ctx[i] : -1;
     if (ctx < 0) {
-      if (i >= most) flag_error(a.err, CKV_DEVERR_PLAN);
+      if (i >= most && !(a.ctx_rows && a.ctx_rows[t] < 0)) flag_error(a.err, CKV_DEVERR_PLAN);
       none(t);
       continue;
     }

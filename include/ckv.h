@@ -729,8 +729,9 @@ ckv_status ckv_kv_append(const ckv_kv_rows* k, const ckv_kv_rows* v, const ckv_k
  *              position of its rotation.
  * ctx_rows   device int32 [T], nullable (= 0): committed tokens before the draft; < 0: padding.
  * words      1..16; a request has 64 * words drafts at most.
- * Rows with ctx_rows < 0 and rows from row_start[B] to T - 1 get an empty mask and position -1.
- * A parent that is not -1 and not below its draft sets CKV_DEVERR_PLAN and counts as -1; drafts from
+ * Rows with ctx_rows < 0 and rows from row_start[B] to T - 1 get an empty mask and position -1,
+ * whatever parents they hold: they are no drafts, though the indices of drafts behind them count them.
+ * A draft's parent that is not -1 and not below it sets CKV_DEVERR_PLAN and counts as -1; drafts from
  * 64 * words on set it too and get an empty mask and position -1.
  */
 ckv_status ckv_build_tree_masks(const int32_t* parents, const int32_t* row_start, int32_t B, const int32_t* ctx_rows,
