@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   float all = 0.f;
 #pragma unroll
   for (int i = 0; i < kParts; ++i) {
-    s[i] = fast_exp2((s[i] - safe) * kLog2e);
+    s[i] = s[i] == safe ? 1.f : fast_exp2((s[i] - safe) * kLog2e);  // infinity less infinity is no number
     all += s[i];
   }
   const float inv = all == 0.f ? 0.f : 1.f / all;

@@ -804,7 +804,8 @@ typedef struct ckv_attention_part {
  *     lse = log(sum_i e^lse_i),   out = sum_i e^(lse_i - lse) out_i
  * for every token and head (a sink belongs in one of the parts only).  A part with lse_i =
  * -infinity counts for nothing, whatever its out_i holds; where every part has it, out is zero and
- * lse -infinity.  fp32 arithmetic, one rounding.
+ * lse -infinity.  Where a part has lse_i = +infinity (a sink of +infinity), lse is +infinity and out the mean of
+ * the parts that have it.  fp32 arithmetic, one rounding.
  * parts      host array of num_parts (1..8).    dtype  of all out_i: CKV_F32 or CKV_BF16.
  * positions  device int32 [T], nullable; < 0: the token's rows are left as they were.
  * out        device [T][H][D] of out_dtype, 16-byte aligned; may be one of the out_i when the

@@ -73,3 +73,18 @@ def test_the_lowest_value_over_4_bit_rows(ck, D, H, n, ctx):  # noqa: F811
     for low in (LOWEST, -torch.inf):
         o1, l1 = ck.ckv_fp4_attention(*args, sink=torch.full((H,), low, device="cuda"), err_word=err)
         assert int(err) == 0 and torch.equal(o, o1) and torch.equal(l[~blind], l1[~blind]) and bool((l1[blind] == low).all())
+
+
+@pytest.mark.parametrize("D,H,KH,n", FORMS)
+@pytest.mark.parametrize("before,rows", [([40, 9], None), ([300, 9], 16000)])
+def test_infinity_takes_all(ck, D, H, KH, n, before, rows):  # noqa: F811
+    s = _step(D, H, KH, n, before)
+    s.sink[::2] = torch.inf
+    out, lse, err = s.run(ck, max_rows=rows)
+    assert int(err) == 0 and torch.all(out[:, ::2] == 0) and torch.all(lse[:, ::2] == torch.inf)
+    far, far_lse = torch.ones_like(out), torch.zeros_like(lse)
+    both, total = ck.ckv_merge_attention([far, out], [far_lse, lse])
+    assert torch.all(both[:, ::2] == 0) and torch.all(total[:, ::2] == torch.inf)
+    near, alone = out[:, 1::2].contiguous(), lse[:, 1::2].contiguous()
+    want = ck.ckv_merge_attention([far[:, 1::2].contiguous(), near], [far_lse[:, 1::2].contiguous(), alone])
+    assert torch.equal(both[:, 1::2], want[0]) and torch.equal(total[:, 1::2], want[1])

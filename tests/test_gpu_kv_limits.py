@@ -25,3 +25,20 @@ def test_padding_among_drafts_is_not_looked_at(ck):  # noqa: F811
     ctx[7] = 40  # a draft, with a parent that is none
     mask, pos = ck.ckv_build_tree_masks(_i32(parents), _i32(start), _i32(ctx), 2, err_word=err)
     assert int(err) == 8 and pos.tolist()[7] == 40
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_merge_of_infinite_parts(ck, dtype):  # noqa: F811
+    """A part whose lse is infinite (a sink of infinity) counts alone; two of them count alike; and the lowest value is a
+    number like others."""
+    inf, low = torch.inf, torch.finfo(torch.float32).min
+    rows = [([inf, 3.0], [1.0, 0.0], inf), ([-inf, inf], [0.0, 1.0], inf), ([inf, inf], [0.5, 0.5], inf), ([low, 3.0], [0.0, 1.0], 3.0),
+            ([low, -inf], [1.0, 0.0], low), ([-inf, -inf], [0.0, 0.0], -inf)]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for D in (128, 256, 512):
+        a, b = (torch.randn(len(rows), 3, D, generator=g, device="cuda").to(dtype) for _ in range(2))
+        la, lb = (torch.tensor([r[0][i] for r in rows], device="cuda")[:, None].expand(-1, 3).contiguous() for i in range(2))
+        out, lse = ck.ckv_merge_attention([a, b], [la, lb], out=torch.empty_like(a))
+        wa, wb = (torch.tensor([r[1][i] for r in rows], device="cuda")[:, None, None] for i in range(2))
+        assert torch.equal(out, (a.float() * wa + b.float() * wb).to(dtype))
+        assert torch.equal(lse, torch.tensor([r[2] for r in rows], device="cuda")[:, None].expand(-1, 3))
