@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import kv_reference as ref
-from test_gpu_kv_ops import _err, _i32, ck  # noqa: F401
+from test_gpu_kv_ops import Step, _err, _i32, ck  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,22 @@ def test_merge_of_infinite_parts(ck, dtype):  # noqa: F811
         wa, wb = (torch.tensor([r[1][i] for r in rows], device="cuda")[:, None, None] for i in range(2))
         assert torch.equal(out, (a.float() * wa + b.float() * wb).to(dtype))
         assert torch.equal(lse, torch.tensor([r[2] for r in rows], device="cuda")[:, None].expand(-1, 3))
+
+
+@pytest.mark.parametrize("D,H,KH,n,before,B", [(128, 24, 3, 1, 60, 700), (128, 40, 5, 1, 90, 800), (128, 56, 7, 4, 30, 300), (256, 56, 7, 1, 60, 300),
+                                               (256, 24, 3, 2, 80, 1300), (512, 48, 3, 1, 70, 1300), (512, 80, 5, 1, 40, 400)])
+@pytest.mark.parametrize("window,first", [(32, 2), (0, 0)])
+def test_few_rows_of_several_key_heads(ck, D, H, KH, n, before, B, window, first):  # noqa: F811
+    """Keys on the M side, and enough CTAs (2 x 6 x 152 for two, twice that for four) that each takes the jobs of two or four
+    key heads from one lookup; the count of key heads is no multiple of them, so a last lookup has fewer."""
+    tokens = [n + (i % 50 == 7) - (i % 50 == 9) for i in range(B)]
+    s = Step(D, H, KH, tokens, [before - i % 20 for i in range(B)], 16, window, first, sink=True, seed=KH)
+    s.ctx = np.array(s.ctx)
+    s.ctx[[3, 11]] = -1, 0
+    G = H // KH
+    R = 16 if n * G <= 16 else 32
+    tiles = (n * B * G + B * max(0, R - (G & -G))) // R
+    assert sum(tokens) == n * B and n * G <= R and tiles * KH >= 2 * 6 * 152
+    out, lse, err = s.run(ck)
+    assert int(err) == 0
+    s.check(out, lse)
