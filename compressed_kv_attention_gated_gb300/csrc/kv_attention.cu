@@ -261,16 +261,17 @@ __device__ __forceinline__ void rescale(uint32_t at, float keep) {
 // Sum and reference of a row -> the scale of its output; stores lse (of the range when the row is split).
 __device__ __forceinline__ float finish_row(const KvAttentionArgs& a, const KvPlan& p, int D, int32_t range, int32_t flat, float all, float m, bool tell) {
   const bool none = all == 0.f, split = p.splits > 1;
-  float keep = 1.f;
+  float keep = 1.f, sink = -INFINITY;
   if (a.sink && !split && flat >= 0) {
-    const float s = a.sink[flat % a.H] * kLog2e, high = fmaxf(none ? kNegBig : m, s);
+    sink = a.sink[flat % a.H];
+    const float s = sink * kLog2e, high = fmaxf(none ? kNegBig : m, s);
     keep = none ? 0.f : fast_exp2(m - high);
     all = (none ? 0.f : all * keep) + (s == high ? 1.f : fast_exp2(s - high));
     m = high;
   }
   if (flat >= 0 && tell) {
     // nothing at all: no sink, or one that is -infinity in log2 units
-    const float lse = all == 0.f ? a.sink && !split ? a.sink[flat % a.H] : -INFINITY : (m + log2f(all)) * kKvLn2;
+    const float lse = all == 0.f ? sink : (m + log2f(all)) * kKvLn2;
     if (split) static_cast<float*>(a.workspace)[a.T * a.H * (p.splits * D + static_cast<int64_t>(range)) + flat] = lse;
     else if (a.lse) a.lse[flat] = lse;
   }

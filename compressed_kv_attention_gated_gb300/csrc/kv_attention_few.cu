@@ -242,10 +242,11 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
     if (place < kCols) {
       const int r = c0 + place;
       const int32_t flat = rows.flat[r];
-      float all = (sm.part[0][r] + sm.part[1][r]) + (sm.part[2][r] + sm.part[3][r]), m = sm.ref[r], keep = 1.f;
+      float all = (sm.part[0][r] + sm.part[1][r]) + (sm.part[2][r] + sm.part[3][r]), m = sm.ref[r], keep = 1.f, sink = -INFINITY;
       const bool none = all == 0.f;
       if (a.sink && !split && flat >= 0) {
-        const float s = a.sink[flat % a.H] * kLog2e, high = fmaxf(none ? kNegBig : m, s);
+        sink = a.sink[flat % a.H];
+        const float s = sink * kLog2e, high = fmaxf(none ? kNegBig : m, s);
         keep = none ? 0.f : fast_exp2(m - high);
         all = (none ? 0.f : all * keep) + (s == high ? 1.f : fast_exp2(s - high));
         m = high;
@@ -253,7 +254,7 @@ __device__ __forceinline__ bool few_soft(const KvAttentionArgs& a, const KvPlan&
       sm.scale[r] = none ? 0.f : keep / all;
       if (flat >= 0) {
         // nothing at all: no sink, or one that is -infinity in log2 units
-        const float lse = all == 0.f ? a.sink && !split ? a.sink[flat % a.H] : -INFINITY : (m + log2f(all)) * kKvLn2;
+        const float lse = all == 0.f ? sink : (m + log2f(all)) * kKvLn2;
         if (split) part_out[p.splits * all_rows * D + range + flat] = lse;
         else if (a.lse) a.lse[flat] = lse;
       }
