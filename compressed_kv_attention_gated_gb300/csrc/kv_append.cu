@@ -9,7 +9,7 @@
 // one lane.  Where pairs are neighbours it has pieces of eight channels.  Where they are halves of the
 // span it has pieces of W channels and their W partners, lanes side by side, and those around the span
 // by twos; W = 4 where the span and its half begin on such a piece, 2 where the half does, otherwise 1
-// (8191 tokens x 48 heads of 128 channels: 34, 42 and 79 us; eight neighbours to a lane with their partners
+// (8191 tokens x 48 heads of 128 channels: 34, 40 and 78 us; eight neighbours to a lane with their partners
 // read one by one took 112).
 #include <cstdint>
 

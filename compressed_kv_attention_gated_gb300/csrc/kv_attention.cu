@@ -33,8 +33,8 @@
 // Few tiles with many keys are split into ranges of keys; their results (fp32, and lse) go through
 // the workspace and are joined by a second kernel in a fixed order.
 //
-// Measured: 9 prompts of 600 to 3000 tokens x 32 heads (8 key heads, D = 128, window 1024) 283 us, 976 TFLOP/s
-// without the masked parts; 128 drafts of 40 to 64 tokens over up to 4096 rows 248 us, 4.9 TB/s.  The tensor cores are
+// Measured: 9 prompts of 600 to 3000 tokens x 32 heads (8 key heads, D = 128, window 1024) 286 us, 965 TFLOP/s
+// without the masked parts; 128 drafts of 40 to 64 tokens over up to 4096 rows 255 us (247 to 261 from run to run), 4.75 TB/s.  The tensor cores are
 // busy 49 and 53% of the time, instructions issue in 44 and 40% of the cycles, exponentials take 24%.  A softmax warp of the
 // prompts spends, of 39 k clocks on a job of 9 tiles of keys, 10 on exponentials and their rounding, 8 on scaling and
 // masks, 4.4 waiting for scores, 3 on the output, 4 on the next job's rows and on sums, and about 5 on getting its
@@ -70,7 +70,7 @@ struct KvLayout {
   static constexpr int kTmemO = 0, kTmemS = 256;  // O: 256 columns; S: two buffers of 128, P over the first half of each
 };
 
-// Beside the common ones (s_full[w], p_full[w], o_full[w] and pv_done[w] are group w's; p_full: 8 warps):
+// Beside the common ones (o_full[w] and pv_done[w] are group w's; at D = 256 s_full[w] and p_full[w] too, p_full of 8 warps):
 template <int D>
 struct KvSmall : KvCommon {
   uint64_t decided[2][8];         // D = 256: warp i of group w knows the references under which its tile is taken
@@ -568,8 +568,8 @@ __device__ __forceinline__ void rescale16(uint32_t at, const float (&keep)[2]) {
 // of a group's next tile come behind those of its last one, so its time counts twice over, and it has eight warps: 16 rows to
 // a warp, four lanes to a row (8000 tokens x 64 heads over 128 rows 242 us, 32 heads over 1024 rows 310 us; with a row to a
 // thread 284 and 321).
-template <int D>
-__device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPlan& p, KvSmall<D>& sm, uint32_t tmem) {
+__device__ __forceinline__ bool soft_shared(const KvAttentionArgs& a, const KvPlan& p, KvSmall<256>& sm, uint32_t tmem) {
+  constexpr int D = 256;
   using L = KvLayout<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = (warp >> 2) & 1, part = (warp & 3) * 2 + (warp >> 3);
   const int row = part * 16 + lane / 4;  // and row + 8
@@ -861,9 +861,9 @@ __device__ __forceinline__ bool mma_apart(KvSmall<128>& sm, uint32_t base, uint3
   }
 }
 
-// D = 256 and 512: one thread issues the products, in the order of their units.
-template <int D>
-__device__ __forceinline__ bool mma_shared(KvSmall<D>& sm, uint32_t base, uint32_t tmem) {
+// D = 256: one thread issues the products, in the order of their units.
+__device__ __forceinline__ bool mma_shared(KvSmall<256>& sm, uint32_t base, uint32_t tmem) {
+  constexpr int D = 256;
   using L = KvLayout<D>;
   const Products<D, 128> mma(sm, base, tmem);
   uint32_t unit = 0, q_use = 0, p_use[2] = {0, 0};
@@ -925,18 +925,18 @@ __global__ void __launch_bounds__(KvLayout<D>::kThreads, 1)
         mbar_init(&sm.full[i], 128);
         mbar_init(&sm.empty[i], kIssuers);
       }
-      for (int i = 0; i < 8; ++i) {
-        mbar_init(&sm.decided[0][i], 1);
-        mbar_init(&sm.decided[1][i], 1);
-      }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.q_full[i], 128);
         mbar_init(&sm.q_empty[i], kIssuers);
-        mbar_init(&sm.s_full[i], 1);
-        mbar_init(&sm.p_full[i], 8);
-        for (int h = 0; h < 2; ++h) {
-          mbar_init(&sm.half_s[i][h], 1);
-          mbar_init(&sm.half_p[i][h], 4);
+        if constexpr (D == 128) {
+          for (int h = 0; h < 2; ++h) {
+            mbar_init(&sm.half_s[i][h], 1);
+            mbar_init(&sm.half_p[i][h], 4);
+          }
+        } else {
+          mbar_init(&sm.s_full[i], 1);
+          mbar_init(&sm.p_full[i], 8);
+          for (int x = 0; x < 8; ++x) mbar_init(&sm.decided[i][x], 1);
         }
         mbar_init(&sm.o_full[i], 1);
         mbar_init(&sm.pv_done[i], 1);
@@ -962,14 +962,14 @@ __global__ void __launch_bounds__(KvLayout<D>::kThreads, 1)
   if (warp < L::kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftRegs));
     if constexpr (D == 128) ok = soft_apart(a, p, sm, tmem);
-    else ok = soft_shared<D>(a, p, sm, tmem);
+    else ok = soft_shared(a, p, sm, tmem);
     tc_fence_before();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
     if (warp == L::kMmaWarp || (D == 128 && warp == L::kMmaWarp2)) {
       if (elect_one()) {
         if constexpr (D == 128) ok = mma_apart(sm, smem_u32(smem), tmem, warp != L::kMmaWarp);
-        else ok = mma_shared<D>(sm, smem_u32(smem), tmem);
+        else ok = mma_shared(sm, smem_u32(smem), tmem);
         // the end of every product: tensor memory may be given back
         tc_commit(&sm.drain);
         ok = mbar_wait_near(&sm.drain, 0) && ok;
@@ -996,7 +996,8 @@ __global__ void __launch_bounds__(KvLayout<D>::kThreads, 1)
 // a kernel of its own and longer lookups, which few or short jobs do not earn back.  With contexts of up to 4096 rows, not
 // sorted and sorted: 256 tokens x 64 heads of 512 channels (2 jobs to an SM) 180 and 142 us, x 32 heads of 256 (7) 330 and
 // 315, 128 drafts of 40 to 64 (7) 267 and 257; x 64 heads of 128 (14) 319 and 324, 1000 tokens x 32 heads (7) 185 and 196; up
-// to 1024 rows, 256 tokens x 32 heads of 256 109 and 113.
+// to 1024 rows, 256 tokens x 32 heads of 256 109 and 113.  One CTA ranks the requests, a thread each: more than its 256
+// are taken as they come, however few their jobs.
 constexpr int kOrderRequests = 256, kOrderTiles = 20, kOrderJobs = 152 * 8;
 
 __global__ void __launch_bounds__(kOrderRequests) kv_order_kernel(const __grid_constant__ KvAttentionArgs a, int R) {
@@ -1109,7 +1110,9 @@ __global__ void __launch_bounds__(128, kFew ? 12 : 4) kv_join_kernel(const __gri
 // Rows of tiles, and into how many ranges of keys a tile is split: the count that a model of the time
 // finds best.  CTAs take their jobs one after the other.  Lengths are known on the host by their
 // bound only, so ranges are of equal size, and of 2^17 keys at most (the tensor cores cut each sum
-// off towards 0: fp4_attention.cu has the figures).
+// off towards 0: fp4_attention.cu has the figures).  With a window that holds where a tile's tokens have
+// contexts next to one another, as tokens of a request do; where they are apart the last range has all
+// that the span leaves out, of which a token sees its window at most.
 KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t max_rows, int32_t window, int32_t first, int32_t words) {
   KvPlan p;
   const int G = H / KH;

@@ -19,7 +19,7 @@ struct KvPlan {
   int R;       // rows of a tile: 16, 32 or 64 (keys on the M side), 128 or 256 (rows on the M side)
   int tiles;   // bound of the number of tiles
   int splits;  // ranges of keys
-  int chunk;   // keys of a range (a multiple of kKvKeys); the last range takes all that are left
+  int chunk;   // keys of a range (a multiple of kKvKeys); the last range takes all that are left: more, if a tile's contexts lie apart
   int heads;   // key heads whose jobs a CTA takes together
   bool sorted; // requests with the longest contexts first, by kv_order_kernel
 };

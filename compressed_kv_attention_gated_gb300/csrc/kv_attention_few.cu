@@ -14,10 +14,11 @@
 // value, its units stay for the second product.
 //
 // Bound by HBM with grouped heads (every row of the window is read once for its heads): 256 tokens x 64 heads over
-// 1024 rows of 8 key heads, D = 128, 163 us, 99% of the copy rate.  At D = 512 with 64 rows queries (64 KB), P and one
+// 1024 rows of 8 key heads, D = 128, 165 us, 98% of the copy rate.  At D = 512 with 64 rows queries (64 KB), P and one
 // tile of keys fill shared memory, and the next tile's keys wait for the second product of this one: 1024 tokens x
-// 64 heads over 128 rows 60 us (4.5 TB/s), 8000 over 128 rows 336 us.  With more keys M = 128 and N = 64 leave the
-// products bound by shared memory at two thirds of the tensor cores' rate (8000 tokens over 4096 rows 2965 us, 1.24 PFLOP/s).
+// 64 heads over 128 rows 59 us (4.5 TB/s), 8000 over 128 rows 327 us.  With more keys the copies of a tile (256 KB, keys and
+// values) and its products still take turns: 8000 tokens over 4096 rows 5175 us, 830 TFLOP/s, the tensor cores busy 34%
+// of the time and 10 TB/s from L2, half of what the copies reach alone.
 #include "kv_attention.cuh"
 
 namespace ckv {

@@ -753,6 +753,9 @@ ckv_status ckv_build_tree_masks(const int32_t* parents, const int32_t* row_start
  * A token that sees nothing gets zeros and lse = sink[h], or -infinity without sink.  Rows with
  * ctx_rows[t] < 0, and rows from row_start[B] on, are left as they were.  Pages that no token of
  * the call sees need not be there: their table entries are not used.
+ * fp32 scores, sums and outputs, one rounding of out; the weights e^(z_j - m), m near the largest z, are
+ * rounded to bf16, the type of the values, before they multiply them (the sums take them unrounded): up
+ * to 2^-8 of sum_j e^(z_j - lse) |v_j| beside the rounding of out.  lse is not affected.
  * q          device bf16, row (t, h) at t*q_stride_t + h*q_stride_h elements, 16-byte aligned.
  * cache      host struct.  From the first row that a token of the request sees to the last one the
  *            rows of pages that are there have finite values (rows between first_rows and the lowest
@@ -767,7 +770,10 @@ ckv_status ckv_build_tree_masks(const int32_t* parents, const int32_t* row_start
  * max_rows   host bound of the rows of a request, drafts included (1 <= max_rows <= max_pages *
  *            page_size and CKV_KV_ATTENTION_MAX_ROWS): larger ctx_rows set CKV_DEVERR_SEQ_LEN and are
  *            clamped, drafts beyond set it too and are unseen.  It chooses how far the rows are
- *            split over CTAs, so a tight bound is faster.
+ *            split over CTAs, so a tight bound is faster.  An fp32 sum of the tensor cores, which they cut
+ *            off towards 0 (7.4e-4 of it over 2^17 rows), runs over 2^17 seen rows at most; where contexts
+ *            of neighbouring tokens of a request lie further apart than their places do, over
+ *            `window` more.
  * window, first_rows  >= 0; first_rows means nothing without a window.
  * tree_mask  device uint64 [T][mask_words], nullable (mask_words == 0); mask_words 1..16.
  * sink       device fp32 [H], nullable.
