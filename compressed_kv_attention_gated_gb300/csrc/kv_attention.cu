@@ -1122,7 +1122,7 @@ KvPlan plan_kv(int64_t T, int32_t B, int32_t H, int32_t KH, int32_t D, int64_t m
   // 336 us, 1659 against 1323, 3211 against 2965).  Below it, longer tiles win (D = 256, 32 heads, 4096: 631 against 942).
   const int R = p.R = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || D == 512 ? 64 : D == 128 ? 256 : 128;
   const int64_t pad = kv_tile_pad(G, R);
-  p.tiles = static_cast<int>((T * G + static_cast<int64_t>(B) * pad) / R);
+  p.tiles = static_cast<int>((T * G + std::min<int64_t>(T, B) * pad) / R);
   int64_t busy = (T * G + R - 1) / R;
   busy = busy < T && busy < B ? (T < B ? T : B) : busy;
   busy *= KH;

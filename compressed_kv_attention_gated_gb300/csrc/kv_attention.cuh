@@ -68,9 +68,12 @@ __device__ __forceinline__ int32_t kv_start_of(const KvAttentionArgs& a, int32_t
 }
 
 // The (token, head of a group) rows of a request are cut into tiles of R.  Tiles begin anew with every
-// request: request b's first tile is (r_b + b (R - g)) / R with r_b the rows before it and g =
-// gcd(G, R), which all r_b and R are multiples of.  That leaves it ceil(rows / R) tiles at least,
-// and none over where tokens are whole tiles.
+// request: request b's first tile is (r_b + m (R - g)) / R with r_b the rows before it, g =
+// gcd(G, R), which all r_b and R are multiples of, and m the lesser of b and the tokens before it, which
+// grows by one at least with every request that has tokens.  That leaves it ceil(rows / R) tiles at
+// least, and none over where tokens are whole tiles; and there are no more tiles than the tokens can
+// fill, however many requests have none (a CTA that passes over an empty one takes some 3 us for it, and
+// its other warps wait for two seconds at most).
 __host__ __device__ inline int kv_tile_pad(int G, int R) {
   const int g = G & -G;  // R is a power of two
   return g < R ? R - g : 0;
@@ -80,6 +83,10 @@ __device__ __forceinline__ int32_t kv_page_of(const KvAttentionArgs& a, int32_t 
   return a.page_shift >= 0 ? key >> a.page_shift : key / a.cache.page_size;
 }
 __device__ __forceinline__ bool kv_page_there(const KvAttentionArgs& a, int32_t page) { return page >= 0 && page < a.cache.num_pages; }
+
+__device__ __forceinline__ int32_t kv_first_tile(const KvAttentionArgs& a, int32_t b, int32_t tok0, int64_t pad, int R) {
+  return static_cast<int32_t>((tok0 * static_cast<int64_t>(a.G) + min(b, tok0) * pad) / R);
+}
 
 // Which request and rows a tile has.
 struct KvTile {
@@ -96,7 +103,7 @@ __device__ __forceinline__ KvTile kv_find_tile(const KvAttentionArgs& a, int32_t
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int i = lo + lane * step;
-    const bool le = lane * step < n && (a.order ? first_tile[i] : (kv_start_of(a, i) * static_cast<int64_t>(a.G) + i * pad) / R) <= tile;
+    const bool le = lane * step < n && (a.order ? first_tile[i] : kv_first_tile(a, i, kv_start_of(a, i), pad, R)) <= tile;
     const uint32_t m = __ballot_sync(0xFFFFFFFFu, le);
     const int last = m ? 31 - __clz(m) : 0;
     lo += last * step;
@@ -107,7 +114,7 @@ __device__ __forceinline__ KvTile kv_find_tile(const KvAttentionArgs& a, int32_t
   t.tok0 = kv_start_of(a, t.b);
   t.ntok = kv_start_of(a, t.b + 1) - t.tok0;
   // with an order, a request's last tile, which sees most, comes first
-  const int64_t i = a.order ? first_tile[lo + 1] - 1 - tile : tile - (t.tok0 * static_cast<int64_t>(a.G) + lo * pad) / R;
+  const int64_t i = a.order ? first_tile[lo + 1] - 1 - tile : tile - kv_first_tile(a, lo, t.tok0, pad, R);
   const int64_t base = i * R, left = static_cast<int64_t>(t.ntok) * a.G - base;
   t.rows = base < 0 || left <= 0 ? 0 : static_cast<int32_t>(left < R ? left : R);  // base < 0: row_start does not begin with 0
   t.base = static_cast<int32_t>(base);

@@ -780,9 +780,9 @@ ckv_status ckv_build_tree_masks(const int32_t* parents, const int32_t* row_start
  * out        device bf16 [T][H][D] contiguous, apart from q (the spans of memory from first to
  *            last element may not overlap).    lse  device fp32 [T][H], nullable.
  * H          1..1024, a multiple of KH.   B <= 65536.   T * H < 2^31.  A launch has a CTA for each tile
- *            of rows (16 at least; each request may add one), range of keys (2^17 rows at most,
- *            where the rows seen together go beyond that) and key head: sizes that come to 2^31
- *            CTAs or more, such as 65,536 requests x 1024 key heads x 20,971,520 rows, are refused.
+ *            of rows (16 at least; each request with tokens may add one), range of keys (2^17 rows at
+ *            most, where the rows seen together go beyond that) and key head: sizes that come to 2^31
+ *            CTAs or more, such as 16,384 requests x 1024 key heads x 20,971,520 rows, are refused.
  * workspace  device, 16-byte aligned, ckv_kv_attention_workspace() bytes (may be NULL when that
  *            is 0); its contents need no initial value and do not outlive the call.  Calls that
  *            overlap on the GPU need one each.  The bytes follow how the rows are split and do not

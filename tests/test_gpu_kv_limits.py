@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import kv_reference as ref
-from test_gpu_kv_ops import Step, _err, _i32, ck  # noqa: F401
+from test_gpu_kv_ops import Step, _err, _i32, ck, close  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,29 @@ def test_few_rows_of_several_key_heads(ck, D, H, KH, n, before, B, window, first
     out, lse, err = s.run(ck)
     assert int(err) == 0
     s.check(out, lse)
+
+
+@pytest.mark.parametrize("D,H,KH,n", [(128, 1024, 1024, 1), (128, 256, 2, 10), (256, 96, 1, 10), (512, 64, 1, 2), (128, 24, 3, 5)])
+def test_a_few_tokens_among_65536_requests(ck, D, H, KH, n):  # noqa: F811
+    """Requests without tokens have no tiles of rows; a bound of 160 * 2^17 rows would split every one of those into 160
+    ranges of keys, one after the other on the same CTAs.  All rows of a page are its first one: a token's output is that
+    value row, its lse the score and the log of the rows that it sees."""
+    B, ps = 65536, 2 ** 21
+    g = torch.Generator(device="cuda").manual_seed(D)
+    k1, v1 = (torch.randn(4, 1, KH, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(n + 1, H, D, generator=g, device="cuda").bfloat16()
+    table = torch.full((B, 10), -1, dtype=torch.int32, device="cuda")
+    table[777, 0], table[65535, 0] = 1, 3
+    start = np.zeros(B + 1, dtype=int)
+    start[778:], start[65536:] = 1, n + 1
+    ctx = [70] + [300 + i for i in range(n)]
+    assert ck.ckv_kv_attention_workspace(n + 1, B, H, KH, D, 10 * ps) >= 160 * (n + 1) * H * (D + 1) * 4
+    err = _err()
+    out, lse = ck.ckv_kv_attention(q, k1.expand(-1, ps, -1, -1), v1.expand(-1, ps, -1, -1), table, _i32(start), _i32(ctx), 10 * ps, D ** -0.5,
+                                   err_word=err)
+    assert int(err) == 0
+    page = torch.tensor([1] + [3] * n, device="cuda")
+    k, v = (x[page, 0].double().repeat_interleave(H // KH, 1) for x in (k1, v1))
+    z = (q.double() * k).sum(-1) * D ** -0.5
+    seen = torch.tensor(ctx, device="cuda", dtype=torch.float64).log()[:, None]
+    close(out, lse, v, z + seen, v.abs(), (q.double() * k).abs().sum(-1) * D ** -0.5, D)

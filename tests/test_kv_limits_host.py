@@ -10,19 +10,19 @@ from test_kv_ops_host import ATTN, P, _cache, _call, lib  # noqa: F401
 MAX_ROWS = 160 * 2 ** 17
 
 
-@pytest.mark.parametrize("B,KH,rows,takes", [
-    (65536, 1024, MAX_ROWS, False),          # 61,440 tiles of rows x 160 ranges of keys x 1024 key heads
-    (65536, 1024, 35 * 2 ** 17, False),      # 2.2 * 10^9
-    (65536, 256, MAX_ROWS, False),           # 61,440 x 160 x 256 = 2.5 * 10^9
-    (65536, 128, MAX_ROWS, True),            # 1.3 * 10^9
-    (65536, 1024, 34 * 2 ** 17, True),       # 2.1 * 10^9, in 34 ranges; in 35 it is too many
-    (65536, 1024, 2 ** 17, True), (1024, 1024, MAX_ROWS, True)])
-def test_grids_beyond_31_bits(lib, B, KH, rows, takes):  # noqa: F811
-    """One token, and B requests that may have it.  What fits is refused for the missing queries that come next."""
-    sizes = dict(T=1, B=B, H=KH, rows=rows, mp=-(-rows // 16), tstride=-(-rows // 16))
+@pytest.mark.parametrize("T,B,KH,rows,takes", [
+    (16384, 16384, 1024, MAX_ROWS, False),         # a tile of rows to a request x 160 ranges of keys x 1024 key heads
+    (65536, 65536, 1024, 32 * 2 ** 17, False),     # 2^31 CTAs
+    (65536, 65536, 1024, 31 * 2 ** 17, True),
+    (65536, 65536, 256, MAX_ROWS, False), (65536, 65536, 128, MAX_ROWS, True),
+    # requests without tokens need none
+    (1, 65536, 1024, MAX_ROWS, True), (8192, 65536, 1024, MAX_ROWS, True), (16384, 65536, 1024, MAX_ROWS, False)])
+def test_grids_beyond_31_bits(lib, T, B, KH, rows, takes):  # noqa: F811
+    """What fits is refused for the missing queries that come next."""
+    sizes = dict(T=T, B=B, H=KH, rows=rows, mp=-(-rows // 16), tstride=-(-rows // 16))
     call = {**ATTN, "cache": _cache(heads=KH, k_stride_row=128 * KH, v_stride_row=128 * KH)}
     assert _call(lib.ckv_kv_attention, call, **sizes, q=None) == (1 if takes else 2)
-    need = lib.ckv_kv_attention_workspace(1, B, KH, KH, 128, rows, 0, 0, 0)
+    need = lib.ckv_kv_attention_workspace(T, B, KH, KH, 128, rows, 0, 0, 0)
     assert need > 0 if takes else need == 0
     # the same rows behind a window, and in one request
     assert _call(lib.ckv_kv_attention, call, **sizes, window=4096, q=None) == 1
