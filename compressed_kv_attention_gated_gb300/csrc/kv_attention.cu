@@ -34,7 +34,7 @@
 // the workspace and are joined by a second kernel in a fixed order.
 //
 // Measured: 9 prompts of 600 to 3000 tokens x 32 heads (8 key heads, D = 128, window 1024) 286 us, 965 TFLOP/s
-// without the masked parts; 128 drafts of 40 to 64 tokens over up to 4096 rows 255 us (247 to 261 from run to run), 4.75 TB/s.  The tensor cores are
+// without the masked parts; 128 drafts of 40 to 64 tokens over up to 4096 rows 255 us (247 to 272 from run to run), 4.75 TB/s.  The tensor cores are
 // busy 49 and 53% of the time, instructions issue in 44 and 40% of the cycles, exponentials take 24%.  A softmax warp of the
 // prompts spends, of 39 k clocks on a job of 9 tiles of keys, 10 on exponentials and their rounding, 8 on scaling and
 // masks, 4.4 waiting for scores, 3 on the output, 4 on the next job's rows and on sums, and about 5 on getting its

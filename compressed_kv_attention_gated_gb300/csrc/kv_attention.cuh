@@ -72,7 +72,7 @@ __device__ __forceinline__ int32_t kv_start_of(const KvAttentionArgs& a, int32_t
 // gcd(G, R), which all r_b and R are multiples of, and m the lesser of b and the tokens before it, which
 // grows by one at least with every request that has tokens.  That leaves it ceil(rows / R) tiles at
 // least, and none over where tokens are whole tiles; and there are no more tiles than the tokens can
-// fill, however many requests have none (a CTA that passes over an empty one takes some 3 us for it, and
+// fill, however many requests have none (a CTA that passes over an empty one takes 1.6 us for it, and
 // its other warps wait for two seconds at most).
 __host__ __device__ inline int kv_tile_pad(int G, int R) {
   const int g = G & -G;  // R is a power of two
